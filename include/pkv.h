@@ -108,7 +108,9 @@ typedef enum pkv_status {
                                 not valid */
 } pkv_status;
 
-typedef enum pkv_dtype { PKV_F32 = 0, PKV_BF16 = 1 } pkv_dtype;
+/* PKV_E4M3: pools of the 8-bit cache (the *_fp8 calls and the calls that take
+ * k_scale and v_scale); rows, q and out are never of this type. */
+typedef enum pkv_dtype { PKV_F32 = 0, PKV_BF16 = 1, PKV_E4M3 = 2 } pkv_dtype;
 
 /* Layout of each pool.  NHD: [num_blocks, block_size, num_kv_heads, head_dim]
  * (a token's row of all kv heads is contiguous).  HND: [num_blocks,
@@ -130,7 +132,7 @@ typedef struct pkv_cache_desc {
     int32_t block_size;   /* tokens per page: 16 or 32 */
     int32_t num_kv_heads; /* Hkv */
     int32_t head_dim;     /* D: 64, 80, 96, 112, 128 or 256 (see each call) */
-    int32_t dtype;        /* pkv_dtype of the pools, q and out */
+    int32_t dtype;        /* pkv_dtype of the pools, and of q and out (PKV_E4M3: bf16 q and out) */
     int32_t layout;       /* pkv_layout of the pools */
 } pkv_cache_desc;
 
@@ -433,6 +435,101 @@ PKV_API pkv_status pkv_paged_decode_noalloc(void *out, const void *q, const void
                                             int window_left, float sm_scale,
                                             int partition_size, float *lse_out,
                                             int32_t *dev_error, void *stream);
+
+/*
+ * The 8-bit cache.  The pools hold e4m3 codes (dtype PKV_E4M3, one byte per
+ * element, NHD or HND as the other pools) and, for every token and kv head, one
+ * E8M0 byte in k_scale / v_scale, [num_blocks, num_kv_heads, block_size] for
+ * both layouts.  Element i of a head row stands for code_i * 2^(byte - 127);
+ * byte 255 marks a row of NaN.  The scale is a power of two, so the value is
+ * exact in bf16 (down to its subnormals) and writing rounds once.  Codes 0x7f
+ * and 0xff (e4m3's NaN) are never written and are not valid in a pool.
+ *
+ * reshape_and_cache_fp8: as pkv_reshape_and_cache, with quantisation: for a
+ * head row x of D values and a = max_i |x_i|,
+ *   e = ceil(log2(a / 448)) clamped to [-126, 119], byte = e + 127,
+ *   code_i = the e4m3 value nearest x_i * 2^-e (ties to even), at most 448.
+ * A row with a NaN or an infinity gets byte 255 and codes 0.
+ *   key, value    rows of `dtype` (PKV_BF16 or PKV_F32): token t, kv head h at
+ *                 element t * key_stride + h * D (value_stride alike); strides
+ *                 are in elements, at least Hkv * D and multiples of 16 bytes,
+ *                 so a slice of a fused projection can be passed
+ * Slots, dev_error and alignment as in pkv_reshape_and_cache.  Supported:
+ * head sizes 64/80/96/112/128/256, block_size 16 or 32.
+ */
+PKV_API pkv_status pkv_reshape_and_cache_fp8(const void *key, const void *value,
+                                             int64_t key_stride, int64_t value_stride, int dtype,
+                                             void *k_cache, void *v_cache, uint8_t *k_scale,
+                                             uint8_t *v_scale, const int64_t *slot_mapping,
+                                             int64_t num_tokens, pkv_cache_desc cache,
+                                             int32_t *dev_error, void *stream);
+
+/*
+ * gather_cache_fp8: read the first cu_seq_lens_k[r+1] - cu_seq_lens_k[r]
+ * positions of every request r back through its pages, as bf16 rows
+ * cu_seq_lens_k[r] .. of key and value ([total_k, Hkv, D], contiguous): the
+ * arrays pkv_varlen_prefill_contiguous takes.  block_table is [batch,
+ * max_blocks_per_seq].  Rows that belong to no request, and rows whose page
+ * is out of range (PKV_DEVERR_BLOCK_ID; beyond the table PKV_DEVERR_SEQLEN),
+ * are left as they were.  Offsets that decrease or leave [0, total_k] set
+ * PKV_DEVERR_SEQLEN.  total_k at most 2^30.
+ */
+PKV_API pkv_status pkv_gather_cache_fp8(void *key, void *value, const void *k_cache,
+                                        const void *v_cache, const uint8_t *k_scale,
+                                        const uint8_t *v_scale, pkv_cache_desc cache,
+                                        const int32_t *block_table, int max_blocks_per_seq,
+                                        const int32_t *cu_seq_lens_k, int batch, int64_t total_k,
+                                        int32_t *dev_error, void *stream);
+
+/*
+ * paged_decode_fp8: pkv_paged_decode over the 8-bit cache: q and out are bf16,
+ * everything else (masks, sink, ALiBi, partitions, lse, workspace of
+ * pkv_paged_decode_workspace_size bytes) as there.  k_scale and v_scale are
+ * 16-byte aligned.  Head sizes 64/80/96/112/128/256, at most 16 query heads per
+ * kv head.
+ */
+PKV_API pkv_status pkv_paged_decode_fp8(void *out, const void *q, const void *k_cache,
+                                        const void *v_cache, const uint8_t *k_scale,
+                                        const uint8_t *v_scale, pkv_cache_desc cache,
+                                        const int32_t *block_table, int max_blocks_per_seq,
+                                        const int32_t *cache_seqlens, int max_seqlen,
+                                        const float *sink, const float *alibi_slopes, int batch,
+                                        int num_qo_heads, int window_left, float sm_scale,
+                                        int partition_size, float *lse_out, void *workspace,
+                                        size_t workspace_bytes, int32_t *dev_error,
+                                        void *stream);
+
+/*
+ * qk_norm_rope_reshape_and_cache: for every token, an RMS norm of each q and k
+ * head, the rotary embedding of pkv_rope_reshape_and_cache, and the cache
+ * write, in one pass:
+ *   y_i = x_i / sqrt(mean_j x_j^2 + eps) * weight_i   (over the head's D values)
+ *   rotate y's first rotary_dim dimensions by positions[t]; round once to dtype
+ *   query_out / key_out <- the rotated rows; the rotated key (as rounded) and
+ *   the value to flat slot slot_mapping[t] of the pools: copied when cache.dtype
+ *   is dtype, quantised as in pkv_reshape_and_cache_fp8 when it is PKV_E4M3
+ *   (then k_scale and v_scale are needed; else they are ignored).
+ *   dtype         PKV_BF16 or PKV_F32, of query, key, value and the outputs
+ *   *_stride      elements between tokens (heads are contiguous), as in
+ *                 pkv_reshape_and_cache_fp8; query_out / key_out may be query /
+ *                 key themselves (in place) and otherwise must not overlap an
+ *                 input
+ *   q_weight, k_weight  [D], fp32 when weight_f32 != 0, else dtype
+ * Sums and products are fp32.  positions, slots and their errors, and
+ * query == NULL with num_qo_heads == 0, as in pkv_rope_reshape_and_cache: a
+ * token whose position is out of range is skipped (nothing of it is written).
+ * Requirements: rotary_dim a multiple of 16, at most D; head sizes
+ * 64/80/96/112/128/256; block_size 16 or 32; every pointer 16-byte aligned
+ * (positions and slot_mapping 8-byte, the scales any).
+ */
+PKV_API pkv_status pkv_qk_norm_rope_reshape_and_cache(
+    const void *query, const void *key, const void *value, int64_t query_stride,
+    int64_t key_stride, int64_t value_stride, int dtype, void *query_out, void *key_out,
+    int64_t query_out_stride, int64_t key_out_stride, void *k_cache, void *v_cache,
+    uint8_t *k_scale, uint8_t *v_scale, const int64_t *positions, const int64_t *slot_mapping,
+    int64_t num_tokens, int num_qo_heads, pkv_cache_desc cache, const void *q_weight,
+    const void *k_weight, int weight_f32, float eps, const float *cos_sin, int max_position,
+    int rotary_dim, int is_neox_style, int32_t *dev_error, void *stream);
 
 #ifdef __cplusplus
 }

@@ -45,12 +45,15 @@ __all__ = [
     "rope_cos_sin_table", "rope_reshape_and_cache", "get_device_error",
     "selftest_bounded_wait",
     "minference_sizes", "minference_prefill",
+    "reshape_and_cache_fp8", "gather_cache_fp8", "paged_decode_fp8",
+    "qk_norm_rope_reshape_and_cache",
     "DEVERR_BLOCK_ID", "DEVERR_SLOT", "DEVERR_SEQLEN", "DEVERR_TIMEOUT", "DEVERR_POSITION",
     "EXPORTED_SYMBOLS",
 ]
 
 PKV_F32 = 0
 PKV_BF16 = 1
+PKV_E4M3 = 2
 DEVERR_BLOCK_ID = 1
 DEVERR_SLOT = 2
 DEVERR_SEQLEN = 4
@@ -64,6 +67,8 @@ EXPORTED_SYMBOLS = (
     "pkv_varlen_prefill_contiguous", "pkv_rope_cos_sin_table", "pkv_rope_reshape_and_cache",
     "pkv_minference_sizes", "pkv_minference_workspace_size", "pkv_minference_prefill",
     "pkv_paged_decode_noalloc", "pkv_get_device_error", "pkv_selftest_bounded_wait",
+    "pkv_reshape_and_cache_fp8", "pkv_gather_cache_fp8", "pkv_paged_decode_fp8",
+    "pkv_qk_norm_rope_reshape_and_cache",
 )
 
 
@@ -146,6 +151,19 @@ def load_library(path: Optional[str] = None):
         lib.pkv_get_device_error.restype = i32
         lib.pkv_selftest_bounded_wait.argtypes = [P, P]
         lib.pkv_selftest_bounded_wait.restype = i32
+        lib.pkv_reshape_and_cache_fp8.argtypes = [P, P, i64, i64, i32, P, P, P, P, P, i64,
+                                                  CacheDesc, P, P]
+        lib.pkv_reshape_and_cache_fp8.restype = i32
+        lib.pkv_gather_cache_fp8.argtypes = [P, P, P, P, P, P, CacheDesc, P, i32, P, i32, i64, P,
+                                             P]
+        lib.pkv_gather_cache_fp8.restype = i32
+        lib.pkv_paged_decode_fp8.argtypes = [P, P, P, P, P, P, CacheDesc, P, i32, P, i32, P, P,
+                                             i32, i32, i32, f32, i32, P, P, sz, P, P]
+        lib.pkv_paged_decode_fp8.restype = i32
+        lib.pkv_qk_norm_rope_reshape_and_cache.argtypes = [
+            P, P, P, i64, i64, i64, i32, P, P, i64, i64, P, P, P, P, P, P, i64, i32, CacheDesc, P,
+            P, i32, f32, P, i32, i32, i32, P, P]
+        lib.pkv_qk_norm_rope_reshape_and_cache.restype = i32
         _lib = lib
         return lib
 
@@ -586,3 +604,247 @@ def paged_decode_noalloc(q, k_cache, v_cache, block_table, cache_seqlens, max_se
         _stream_handle(stream))
     _check("pkv_paged_decode_noalloc", st)
     return out
+
+
+# ---------------------------------------------------------------------------
+# the 8-bit cache
+# ---------------------------------------------------------------------------
+
+def _cache_desc_fp8(k_cache, v_cache, k_scale, v_scale, layout: str) -> CacheDesc:
+    torch = _torch()
+    _cuda_contig("k_cache", k_cache, torch.float8_e4m3fn, 4)
+    _cuda_contig("v_cache", v_cache, torch.float8_e4m3fn, 4)
+    _require(k_cache.shape == v_cache.shape, "k_cache and v_cache must have the same shape")
+    nb, bs, hkv, d = _pool_dims(k_cache, layout)
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _require(t is not None, f"{name} is needed for an 8-bit cache")
+        _cuda_contig(name, t, torch.uint8, 3)
+        _require(tuple(t.shape) == (nb, hkv, bs),
+                 f"{name} must be [num_blocks, num_kv_heads, block_size]")
+    return CacheDesc(nb, bs, hkv, d, PKV_E4M3, LAYOUTS[layout])
+
+
+def _token_rows(name, t, dtype, heads: int, head_dim: int) -> int:
+    """Checks [T, heads, head_dim] rows whose heads are contiguous; returns the
+    elements between tokens (a slice of a fused projection keeps its own)."""
+    _require(t.dim() == 3 and t.shape[1] == heads and t.shape[2] == head_dim,
+             f"{name} must be [T, {heads}, {head_dim}], got {list(t.shape)}")
+    if t.is_contiguous():
+        _cuda_contig(name, t, dtype)
+        return heads * head_dim
+    _cuda_contig(name, t[:1], dtype)
+    return t.stride(0)
+
+
+def _same_device(first, *others):
+    for t in others:
+        _require(t is None or t.device == first.device,
+                 f"all tensors must be on one device: {t.device if t is not None else None} "
+                 f"and {first.device}")
+
+
+def _check_error_word(dev_error):
+    if dev_error is not None:
+        _cuda_contig("dev_error", dev_error, _torch().int32, 1)
+        _require(dev_error.numel() >= 1, "dev_error must have one element")
+
+
+class _launch_on:
+    """The device of ``t`` made current, and with a ``stream`` that stream, so
+    that what the call allocates belongs to the stream its kernels run on."""
+
+    def __init__(self, t, stream):
+        self.t, self.stream, self.ctx = t, stream, None
+
+    def __enter__(self):
+        if not self.t.is_cuda:
+            return
+        torch = _torch()
+        if self.stream is not None:
+            self.ctx = torch.cuda.stream(self.stream)
+        elif self.t.device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(self.t.device)
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def reshape_and_cache_fp8(key, value, k_cache, v_cache, k_scale, v_scale, slot_mapping,
+                          dev_error=None, stream=None, layout: str = "NHD") -> None:
+    """reshape_and_cache into the 8-bit cache (in place): each head row of
+    key/value [T, Hkv, D] (bf16 or float32; a token's heads contiguous, tokens
+    any stride) becomes e4m3 codes in k_cache/v_cache (torch.float8_e4m3fn, the
+    pool shapes of ``layout``) and one E8M0 byte in k_scale/v_scale ([num_blocks,
+    Hkv, block_size] uint8): value = code * 2^(byte - 127), the exponent the
+    smallest that keeps max|x| within 448.  A row with a NaN or an infinity is
+    stored as byte 255 and reads as NaN.  slot_mapping: [T] int64, negative =
+    skip; dev_error receives PKV_DEVERR_SLOT for slots outside the pool."""
+    torch = _torch()
+    desc = _cache_desc_fp8(k_cache, v_cache, k_scale, v_scale, layout)
+    dt = _dtype_code(key.dtype)
+    ks = _token_rows("key", key, key.dtype, desc.num_kv_heads, desc.head_dim)
+    vs = _token_rows("value", value, key.dtype, desc.num_kv_heads, desc.head_dim)
+    _cuda_contig("slot_mapping", slot_mapping, torch.int64, 1)
+    _require(key.shape[0] == value.shape[0] == slot_mapping.shape[0],
+             "key, value and slot_mapping must have T entries")
+    _check_error_word(dev_error)
+    _same_device(key, value, k_cache, v_cache, k_scale, v_scale, slot_mapping, dev_error)
+    with _launch_on(key, stream):
+        st = load_library().pkv_reshape_and_cache_fp8(
+            _ptr(key), _ptr(value), ks, vs, dt, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+            _ptr(v_scale), _ptr(slot_mapping), key.shape[0], desc, _ptr(dev_error),
+            _stream_handle(stream))
+    _check("pkv_reshape_and_cache_fp8", st)
+
+
+def gather_cache_fp8(k_cache, v_cache, k_scale, v_scale, block_table, cu_seq_lens_k,
+                     total_k: int, key=None, value=None, dev_error=None, stream=None,
+                     layout: str = "NHD"):
+    """The cached rows of every request as bf16: returns (key, value), each
+    [total_k, Hkv, D], request r's positions 0.. at rows cu_seq_lens_k[r] ..
+    (the arrays varlen_prefill_contiguous takes).  block_table: [B, max_blocks]
+    int32; cu_seq_lens_k: [B+1] int32; total_k: host int, the rows of the
+    outputs.  Rows of no request are left as they were (uninitialised in
+    outputs allocated here)."""
+    torch = _torch()
+    desc = _cache_desc_fp8(k_cache, v_cache, k_scale, v_scale, layout)
+    _cuda_contig("block_table", block_table, torch.int32, 2)
+    _cuda_contig("cu_seq_lens_k", cu_seq_lens_k, torch.int32, 1)
+    B = cu_seq_lens_k.shape[0] - 1
+    _require(B >= 0 and block_table.shape[0] == B, "block_table must have one row per request")
+    _require(total_k >= 0, "total_k must not be negative")
+    shape = (int(total_k), desc.num_kv_heads, desc.head_dim)
+    for name, t in (("key", key), ("value", value)):
+        if t is not None:
+            _cuda_contig(name, t, torch.bfloat16, 3)
+            _require(tuple(t.shape) == shape, f"{name} must be [total_k, Hkv, D]")
+    _check_error_word(dev_error)
+    _same_device(k_cache, v_cache, k_scale, v_scale, block_table, cu_seq_lens_k, key, value,
+                 dev_error)
+    with _launch_on(k_cache, stream):
+        if key is None:
+            key = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
+        if value is None:
+            value = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
+        st = load_library().pkv_gather_cache_fp8(
+            _ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+            desc, _ptr(block_table), block_table.shape[1], _ptr(cu_seq_lens_k), B, int(total_k),
+            _ptr(dev_error), _stream_handle(stream))
+    _check("pkv_gather_cache_fp8", st)
+    return key, value
+
+
+def paged_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_seqlens,
+                     max_seqlen: int, sink=None, window_left: int = -1,
+                     sm_scale: Optional[float] = None, partition_size: int = 512, out=None,
+                     lse=None, workspace=None, dev_error=None, stream=None, alibi_slopes=None,
+                     layout: str = "NHD"):
+    """paged_decode over the 8-bit cache of reshape_and_cache_fp8: q and out are
+    bf16 [B, Hq, D]; everything else as paged_decode (workspace of
+    paged_decode_workspace_size bytes)."""
+    torch = _torch()
+    desc = _cache_desc_fp8(k_cache, v_cache, k_scale, v_scale, layout)
+    _cuda_contig("q", q, torch.bfloat16, 3)
+    _cuda_contig("block_table", block_table, torch.int32, 2)
+    _cuda_contig("cache_seqlens", cache_seqlens, torch.int32, 1)
+    B, Hq, D = q.shape
+    _require(D == desc.head_dim, "head_dim of q and cache differ")
+    _require(block_table.shape[0] == B and cache_seqlens.shape[0] == B,
+             "block_table / cache_seqlens batch mismatch")
+    _head_vector("sink", sink, Hq)
+    _head_vector("alibi_slopes", alibi_slopes, Hq)
+    if out is not None:
+        _cuda_contig("out", out, q.dtype, 3)
+        _require(out.shape == q.shape, "out must be shaped like q")
+    if lse is not None:
+        _cuda_contig("lse", lse, torch.float32, 2)
+        _require(tuple(lse.shape) == (B, Hq), "lse must be [B, Hq]")
+    _check_error_word(dev_error)
+    _same_device(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_seqlens, sink,
+                 alibi_slopes, out, lse, workspace, dev_error)
+    scale = float(sm_scale) if sm_scale is not None else D ** -0.5
+    need = paged_decode_workspace_size(B, Hq, D, max_seqlen, partition_size, window_left)
+    with _launch_on(q, stream):
+        if out is None:
+            out = torch.empty_like(q)
+        ws = _workspace(need, q.device, workspace)
+        st = load_library().pkv_paged_decode_fp8(
+            _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), desc,
+            _ptr(block_table), block_table.shape[1], _ptr(cache_seqlens), int(max_seqlen),
+            _ptr(sink), _ptr(alibi_slopes), B, Hq, int(window_left), scale, int(partition_size),
+            _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _ptr(dev_error),
+            _stream_handle(stream))
+    _check("pkv_paged_decode_fp8", st)
+    return out
+
+
+def qk_norm_rope_reshape_and_cache(query, key, value, k_cache, v_cache, positions, slot_mapping,
+                                   cos_sin, q_weight, k_weight, eps: float = 1e-6,
+                                   rotary_dim: Optional[int] = None, is_neox_style: bool = True,
+                                   query_out=None, key_out=None, k_scale=None, v_scale=None,
+                                   dev_error=None, stream=None, layout: str = "NHD") -> None:
+    """RMS norm of every head of query [T, Hq, D] and key [T, Hkv, D] (weights
+    q_weight and k_weight [D], float32 or the rows' dtype), rotary embedding by
+    positions [T] with the table cos_sin, and the cache write of the rotated key
+    and the value at slot_mapping [T], in one pass.
+
+    Rows are bf16 or float32; a token's heads are contiguous and tokens may
+    have any stride (slices of a fused projection).  The rotated rows go to
+    query_out / key_out, or back in place when these are None.  With k_scale and
+    v_scale the pools are the 8-bit cache of reshape_and_cache_fp8, else pools of
+    the rows' dtype.  query (with query_out and q_weight) may be None."""
+    torch = _torch()
+    dt = _dtype_code(key.dtype)
+    if k_scale is not None or v_scale is not None:
+        desc = _cache_desc_fp8(k_cache, v_cache, k_scale, v_scale, layout)
+    else:
+        desc = _cache_desc(k_cache, v_cache, layout)
+        _require(k_cache.dtype == key.dtype, "the pools must have the dtype of key")
+    D = desc.head_dim
+    ks = _token_rows("key", key, key.dtype, desc.num_kv_heads, D)
+    vs = _token_rows("value", value, key.dtype, desc.num_kv_heads, D)
+    T, Hq, qs, qos = key.shape[0], 0, 0, 0
+    _require(value.shape[0] == T, "key and value must have the same tokens")
+    if key_out is None:
+        key_out = key
+    kos = _token_rows("key_out", key_out, key.dtype, desc.num_kv_heads, D)
+    _require(key_out.shape[0] == T, "key_out must be shaped like key")
+    if query is not None:
+        if query_out is None:
+            query_out = query
+        Hq = query.shape[1] if query.dim() == 3 else 0
+        qs = _token_rows("query", query, key.dtype, Hq, D)
+        qos = _token_rows("query_out", query_out, key.dtype, Hq, D)
+        _require(query.shape[0] == T and query_out.shape[0] == T,
+                 "query must be [T, num_qo_heads, head_dim]")
+    else:
+        query_out = q_weight = None
+    _cuda_contig("positions", positions, torch.int64, 1)
+    _cuda_contig("slot_mapping", slot_mapping, torch.int64, 1)
+    _cuda_contig("cos_sin", cos_sin, torch.float32, 3)
+    _require(positions.shape[0] == T and slot_mapping.shape[0] == T,
+             "positions and slot_mapping must have T entries")
+    rd = int(rotary_dim) if rotary_dim is not None else 2 * cos_sin.shape[1]
+    _require(cos_sin.shape[1] * 2 == rd and cos_sin.shape[2] == 2,
+             "cos_sin must be [max_position, rotary_dim // 2, 2]")
+    w32 = k_weight.dtype == torch.float32
+    for name, w in (("k_weight", k_weight), ("q_weight", q_weight)):
+        if w is None:
+            _require(name == "q_weight" and query is None, f"{name} is needed")
+            continue
+        _cuda_contig(name, w, torch.float32 if w32 else key.dtype, 1)
+        _require(w.shape[0] == D, f"{name} must have head_dim entries")
+    _check_error_word(dev_error)
+    _same_device(key, value, k_cache, v_cache, positions, slot_mapping, cos_sin, k_weight,
+                 q_weight, query, query_out, key_out, k_scale, v_scale, dev_error)
+    with _launch_on(key, stream):
+        st = load_library().pkv_qk_norm_rope_reshape_and_cache(
+            _ptr(query), _ptr(key), _ptr(value), qs, ks, vs, dt, _ptr(query_out), _ptr(key_out),
+            qos, kos, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+            _ptr(positions), _ptr(slot_mapping), T, Hq, desc, _ptr(q_weight), _ptr(k_weight),
+            int(w32), float(eps), _ptr(cos_sin), cos_sin.shape[0], rd, int(bool(is_neox_style)),
+            _ptr(dev_error), _stream_handle(stream))
+    _check("pkv_qk_norm_rope_reshape_and_cache", st)

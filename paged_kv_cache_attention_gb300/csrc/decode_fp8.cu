@@ -1,0 +1,581 @@
+// decode_fp8.cu -- split-KV decode over the 8-bit cache.
+//
+// The attention of decode.cu (same masks, sink, ALiBi and partitions; see
+// there) with key j of a kv head stored as e4m3 codes kc_j and a byte:
+//   s_j = sm_scale * 2^ek_j * <q, kc_j> + bias,   o = sum_j p_j 2^ev_j vc_j / l.
+//
+// HBM bound: 2*(D + 1) bytes per key and kv head, half of the bf16 cache.
+// At 6.8 TB/s an SM receives 23 codes per clock, so turning codes into tensor-
+// core operands must cost little: each 32-bit word of four codes becomes two
+// f16 pairs of code * 2^-8 in seven integer instructions, and neither scale
+// touches the codes:
+//   * K: the byte multiplies the fp32 score of its key;
+//   * V: the byte multiplies p_j before p rounds to f16.  Weights are kept
+//     relative to the largest byte E seen so far by the warp, p_j *
+//     2^(ev_j - E + 14) <= 2^14: f16 keeps 11 bits of every weight down to
+//     2^-28 of the largest; the accumulators move by 2^(E_old - E_new) together
+//     with the softmax's own rescale.
+// q is scaled per head by a power of two to at most 2^15 and held in f16,
+// which is exact for every bf16 value within 2^-28 of the row's largest (and
+// off by less than 2^-39 of the largest below that).
+//
+// The mma fragments follow the bytes: a 32-bit word of an ldmatrix row holds
+// four consecutive dims of a key, split into (0, 2) and (1, 3), so a k-step of
+// Q K^T takes 16 dims in that order (q's fragment is loaded to match); a
+// transposed ldmatrix word holds two consecutive dims of two consecutive keys,
+// whose split is one even-dim and one odd-dim fragment of O^T += V^T P^T.
+//
+// CTAs of two warps, each streaming every other 32-token stage of the
+// partition through its own ring of NST stages: K and V by TMA (one box per
+// page), the scale bytes by 16-byte cp.async on the same barrier.
+#include "pkv_fp8.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kWarps = 2;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTok = 32;  // tokens per stage
+constexpr int kMaxGroup = 16;
+constexpr float kNegInf = -INFINITY;
+
+__device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
+    const uintptr_t a = (reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023);
+    return reinterpret_cast<uint8_t *>(a);
+}
+
+__device__ __forceinline__ int clipped_len(const DecodeParams &p, int b, int block_size,
+                                           bool report) {
+    const long long cap_blocks = (long long)p.max_blocks_per_seq * block_size;
+    const int cap = cap_blocks < p.max_seqlen ? (int)cap_blocks : p.max_seqlen;
+    const int L = p.seqlens[b];
+    if ((L < 0 || L > cap) && report) flag_error(p.dev_error, PKV_DEVERR_SEQLEN);
+    return min(max(L, 0), cap);
+}
+
+__device__ __forceinline__ int first_kept(int L, int window_left) {
+    return window_left < 0 ? 0 : max(L - 1 - window_left, 0);
+}
+
+// Byte offset of 16-byte chunk c of row r in a tile of W-byte rows (W = 64 or
+// 128) that TMA wrote with W-byte swizzling.
+template <int W>
+__device__ __forceinline__ uint32_t swz(uint32_t r, uint32_t c) {
+    return W == 128 ? sw128(r, c) : r * 64u + ((c ^ ((r >> 1) & 3u)) << 4);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+template <int D, int NST>
+struct Shape {
+    static constexpr int ROWB = D < 128 ? D : 128;           // bytes of a box row
+    static constexpr int PARTS = D / ROWB;                   // boxes across the head size
+    static constexpr int PART_BYTES = kTok * ROWB;
+    static constexpr int KV_BYTES = PARTS * PART_BYTES;      // K (or V) of one stage
+    static constexpr int RING = kWarps * NST * 2 * KV_BYTES;
+    static constexpr int SCALE_OFF = RING;                   // [warp][stage][K, V][32] bytes
+    static constexpr int BAR_OFF = SCALE_OFF + kWarps * NST * 2 * kTok;
+    static constexpr int M_OFF = BAR_OFF + kWarps * NST * 8;
+    static constexpr int L_OFF = M_OFF + kWarps * kMaxGroup * 4;
+    static constexpr int BLK_OFF = L_OFF + kWarps * kMaxGroup * 4;
+    static constexpr int SMEM_FIXED = 1024 + BLK_OFF;        // + the partition's block ids
+    static_assert(kWarps * 8 * D * 4 <= RING, "merge scratch must fit in the ring");
+};
+
+template <int D, int BS, int NHT, int NST, bool HND>
+__global__ void __launch_bounds__(kThreads)
+decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap tmk,
+                  const __grid_constant__ CUtensorMap tmv) {
+    using C = Shape<D, NST>;
+    constexpr int PPS = kTok / BS;  // pages per stage
+    constexpr int NC = D / 16;      // 16-dim chunks
+    const DecodeParams &p = pp.d;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align1024(smem_raw);
+    int *s_blk = reinterpret_cast<int *>(smem + C::BLK_OFF);
+    float *s_m = reinterpret_cast<float *>(smem + C::M_OFF);
+    float *s_l = reinterpret_cast<float *>(smem + C::L_OFF);
+
+    pdl_trigger();
+    pdl_wait();
+    const int g = blockIdx.x, b = blockIdx.z;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int L = clipped_len(p, b, BS, blockIdx.y == 0 && g == 0 && threadIdx.x == 0);
+    const int start = first_kept(L, p.window_left);
+    const int part = start / p.partition_size + blockIdx.y;
+    const int tok_lo = max(part * p.partition_size, start);
+    const int tok_hi = min((part + 1) * p.partition_size, L);
+    if (tok_lo >= tok_hi) return;  // this slot holds no attended key
+
+    // stages are 32 tokens at multiples of 32; pages of the range
+    const int st_lo = tok_lo / kTok, nst = (tok_hi - 1) / kTok - st_lo + 1;
+    const int pg_lo = st_lo * PPS, pg_first = tok_lo / BS, pg_last = (tok_hi - 1) / BS;
+
+    const uint32_t ring = smem_u32(smem);
+    const uint32_t bars = ring + C::BAR_OFF;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kWarps * NST; ++i) mbar_init(bars + 8 * i, 1 + 4);
+        fence_barrier_init();
+        tma_prefetch_desc(&tmk);
+        tma_prefetch_desc(&tmv);
+    }
+    const int32_t *bt = p.block_table + (int64_t)b * p.max_blocks_per_seq;
+    for (int i = threadIdx.x; i < nst * PPS; i += kThreads) {
+        const int page = pg_lo + i;
+        int id = -1;
+        if (page >= pg_first && page <= pg_last) {  // else: no attended key, not read
+            id = bt[page];
+            if (id < 0 || id >= p.num_blocks) {
+                flag_error(p.dev_error, PKV_DEVERR_BLOCK_ID);
+                id = -1;
+            }
+        }
+        s_blk[i] = id;
+    }
+    __syncthreads();
+
+    const int nmine = nst > warp ? (nst - warp + kWarps - 1) / kWarps : 0;
+    const uint32_t wring = ring + warp * NST * 2 * C::KV_BYTES;
+    const uint32_t wbars = bars + warp * NST * 8;
+    const uint32_t wscale = ring + C::SCALE_OFF + warp * NST * 2 * kTok;
+    const uint64_t policy = l2_policy_evict_first();
+
+    // Stage j of this warp: lane 0 asks TMA for the boxes, lanes 0..3 copy the
+    // scale bytes (16 K and 16 V bytes for each half of the stage).
+    auto issue = [&](int j) {
+        const int s = j % NST;
+        const uint32_t bar = wbars + 8 * s;
+        const int *blk = s_blk + (warp + j * kWarps) * PPS;
+        if (lane == 0) {
+            uint32_t bytes = 0;
+#pragma unroll
+            for (int q = 0; q < PPS; ++q)
+                if (blk[q] >= 0) bytes += 2 * C::PARTS * BS * C::ROWB;
+            mbar_arrive_expect_tx(bar, bytes);
+            const uint32_t dst = wring + s * 2 * C::KV_BYTES;
+#pragma unroll
+            for (int q = 0; q < PPS; ++q) {
+                if (blk[q] < 0) continue;
+                const int cy = HND ? 0 : g;
+                const int cz = HND ? blk[q] * p.num_kv_heads + g : blk[q] * BS;
+#pragma unroll
+                for (int h = 0; h < C::PARTS; ++h) {
+                    const uint32_t o = dst + h * C::PART_BYTES + q * BS * C::ROWB;
+                    tma_load_3d_hint(o, &tmk, bar, h * 128, cy, cz, policy);
+                    tma_load_3d_hint(o + C::KV_BYTES, &tmv, bar, h * 128, cy, cz, policy);
+                }
+            }
+        }
+        if (lane < 4) {
+            const int half = lane & 1, q = BS == 16 ? half : 0;
+            if (blk[q] >= 0) {
+                const uint8_t *src = lane < 2 ? pp.k_scale : pp.v_scale;
+                const int64_t at = ((int64_t)blk[q] * p.num_kv_heads + g) * BS +
+                                   (BS == 32 ? half * 16 : 0);
+                cp_async16(wscale + s * 2 * kTok + (lane < 2 ? 0 : kTok) + half * 16, src + at);
+            }
+            cp_async_arrive(bar);
+        }
+    };
+    for (int j = 0; j < NST && j < nmine; ++j) issue(j);
+
+    // q as the A operand: row = head, 16 dims per k-step in the byte order
+    const int gq = lane >> 2, tq = lane & 3;
+    const int G = p.group, Dh = p.head_dim;
+    const __nv_bfloat16 *qb =
+        static_cast<const __nv_bfloat16 *>(p.q) + ((int64_t)b * p.num_qo_heads + g * G) * Dh;
+    uint32_t qa[NHT][NC][2];
+    float rowf[NHT];
+#pragma unroll
+    for (int ht = 0; ht < NHT; ++ht) {
+        const int h = ht * 8 + gq;
+        uint2 w[NC];
+        uint32_t amax = 0;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            w[c] = make_uint2(0u, 0u);
+            if (h < G && c * 16 < Dh)
+                w[c] = *reinterpret_cast<const uint2 *>(qb + h * Dh + c * 16 + 4 * tq);
+            const uint32_t v[2] = {w[c].x, w[c].y};
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                amax = max(amax, max(v[i] & 0x7fffu, (v[i] >> 16) & 0x7fffu));
+        }
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // largest magnitude 2^E..2^(E+1): times 2^(14 - E)
+        const int E = max((int)(amax >> 7) - 127, -100);
+        const float f = __uint_as_float((uint32_t)(127 + 14 - E) << 23);
+        // score = <q f, code 2^-8> * 2^8 / f * sm_scale
+        rowf[ht] = p.scale_log2 * __uint_as_float((uint32_t)(min(127 + E - 6, 254)) << 23);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const float x0 = __uint_as_float(w[c].x << 16) * f;
+            const float x1 = __uint_as_float(w[c].x & 0xffff0000u) * f;
+            const float x2 = __uint_as_float(w[c].y << 16) * f;
+            const float x3 = __uint_as_float(w[c].y & 0xffff0000u) * f;
+            qa[ht][c][0] = pack_f16(x0, x2);
+            qa[ht][c][1] = pack_f16(x1, x3);
+        }
+    }
+
+    float oacc[NHT][NC][4];
+    float m_run[NHT], l_run[NHT], al2[NHT];
+    bool head_ok[NHT];
+#pragma unroll
+    for (int ht = 0; ht < NHT; ++ht) {
+        m_run[ht] = kNegInf;
+        l_run[ht] = 0.f;
+        head_ok[ht] = ht * 8 + gq < G;
+        al2[ht] = (p.alibi && head_ok[ht]) ? p.alibi[g * G + ht * 8 + gq] * kLog2e : 0.f;
+#pragma unroll
+        for (int mt = 0; mt < NC; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) oacc[ht][mt][e] = 0.f;
+    }
+    int gauge = 0;  // the largest V scale byte so far
+    const int qpos = L - 1;
+
+    int consumed = 0;
+    for (int j = 0; j < nmine; ++j) {
+        const int i = warp + j * kWarps;
+        const int s = j % NST;
+        if (!warp_wait_bounded(wbars + 8 * s, (j / NST) & 1, p.dev_error)) break;
+        consumed = j + 1;
+        const uint32_t kb = wring + s * 2 * C::KV_BYTES, vb = kb + C::KV_BYTES;
+        const uint8_t *sc = smem + C::SCALE_OFF + (warp * NST + s) * 2 * kTok;
+        const int tok0 = (st_lo + i) * kTok;
+        // lane = token of the stage: is it attended, and its V scale
+        const int tok_l = tok0 + lane;
+        const bool ok_l = tok_l >= tok_lo && tok_l < tok_hi && s_blk[i * PPS + lane / BS] >= 0;
+        const uint32_t okm = __ballot_sync(0xffffffffu, ok_l);
+        const int vmax = __reduce_max_sync(0xffffffffu, ok_l ? (int)sc[kTok + lane] : 0);
+        const int gnew = max(gauge, vmax);
+        // 2^(gauge - gnew), zero past the float range
+        const float gcorr = gauge == gnew || gauge - gnew < -126
+                                ? (gauge == gnew ? 1.f : 0.f)
+                                : __uint_as_float((uint32_t)(127 + gauge - gnew) << 23);
+        gauge = gnew;
+
+        float sacc[4][4];
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sacc[nt][e] = 0.f;
+#pragma unroll
+            for (int c4 = 0; c4 < NC / 4; ++c4) {
+                const int c = c4 * 4 + (lane >> 3);
+                const int r = nt * 8 + (lane & 7);
+                uint32_t w[4];
+                ldsm_x4(kb + (c >> 3) * C::PART_BYTES + swz<C::ROWB>(r, c & 7), w[0], w[1], w[2],
+                        w[3]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_f16_16816(sacc[nt], qa[0][c4 * 4 + k][0],
+                                  NHT > 1 ? qa[NHT - 1][c4 * 4 + k][0] : 0u,
+                                  qa[0][c4 * 4 + k][1],
+                                  NHT > 1 ? qa[NHT - 1][c4 * 4 + k][1] : 0u,
+                                  e4m3_even_f16(w[k]), e4m3_odd_f16(w[k]));
+            }
+        }
+        float kf[4][2], vf[4][2];
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+            const int t = nt * 8 + 2 * tq;
+            const uint32_t k2 = *reinterpret_cast<const uint16_t *>(sc + t);
+            const uint32_t v2 = *reinterpret_cast<const uint16_t *>(sc + kTok + t);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t kbyte = (k2 >> (8 * e)) & 255u;
+                const int vbyte = (int)((v2 >> (8 * e)) & 255u);
+                kf[nt][e] = scale_value(kbyte);
+                const int x = vbyte - gauge + 14 + 127;
+                vf[nt][e] = vbyte == (int)kScaleNaN ? __uint_as_float(0x7fffffffu)
+                            : x > 0                 ? __uint_as_float((uint32_t)x << 23)
+                                                    : 0.f;
+            }
+        }
+        // online softmax (log2 units), one head row per lane quad
+#pragma unroll
+        for (int ht = 0; ht < NHT; ++ht) {
+            float mx = kNegInf;
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int t = nt * 8 + 2 * tq + e;
+                    const bool ok = head_ok[ht] && ((okm >> t) & 1u);
+                    const float sv = ok ? fmaf(sacc[nt][2 * ht + e] * kf[nt][e], rowf[ht],
+                                               al2[ht] * (float)(tok0 + t - qpos))
+                                        : kNegInf;
+                    sacc[nt][2 * ht + e] = sv;
+                    mx = fmaxf(mx, sv);
+                }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float m_new = fmaxf(m_run[ht], mx);
+            const float msub = m_new == kNegInf ? 0.f : m_new;
+            const float alpha = fast_exp2(m_run[ht] - msub);
+            float psum = 0.f;
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int t = nt * 8 + 2 * tq + e;
+                    const float pv = fast_exp2(sacc[nt][2 * ht + e] - msub);
+                    psum += pv;
+                    // an unattended row's byte may be anything: its weight is 0
+                    sacc[nt][2 * ht + e] = ((okm >> t) & 1u) ? pv * vf[nt][e] : 0.f;
+                }
+            l_run[ht] = l_run[ht] * alpha + psum;
+            m_run[ht] = m_new;
+            const float ao = alpha * gcorr;
+            const float a0 = __shfl_sync(0xffffffffu, ao, 8 * tq);
+            const float a1 = __shfl_sync(0xffffffffu, ao, 8 * tq + 4);
+#pragma unroll
+            for (int mt = 0; mt < NC; ++mt) {
+                oacc[ht][mt][0] *= a0;
+                oacc[ht][mt][1] *= a1;
+                oacc[ht][mt][2] *= a0;
+                oacc[ht][mt][3] *= a1;
+            }
+        }
+        // O^T += V^T P^T.  Codes of rows that are not attended are finite
+        // whatever bits they hold, and their weights are zero.
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            uint32_t pb0[NHT], pb1[NHT];
+#pragma unroll
+            for (int ht = 0; ht < NHT; ++ht) {
+                pb0[ht] = pack_f16(sacc[2 * ks][2 * ht], sacc[2 * ks][2 * ht + 1]);
+                pb1[ht] = pack_f16(sacc[2 * ks + 1][2 * ht], sacc[2 * ks + 1][2 * ht + 1]);
+            }
+            const int jm = lane >> 3;
+            const int r = ks * 16 + ((jm & 1) << 3) + (lane & 7);
+#pragma unroll
+            for (int c2 = 0; c2 < NC / 2; ++c2) {
+                const int c = c2 * 2 + (jm >> 1);
+                uint32_t w[4];  // (keys 0-7, 8-15) of chunk 2*c2, then of 2*c2 + 1
+                ldsm_x4_t(vb + (c >> 3) * C::PART_BYTES + swz<C::ROWB>(r, c & 7), w[0], w[1],
+                          w[2], w[3]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t a0 = e4m3_even_f16(w[2 * k]), a1 = e4m3_odd_f16(w[2 * k]);
+                    const uint32_t a2 = e4m3_even_f16(w[2 * k + 1]);
+                    const uint32_t a3 = e4m3_odd_f16(w[2 * k + 1]);
+#pragma unroll
+                    for (int ht = 0; ht < NHT; ++ht)
+                        mma_f16_16816(oacc[ht][c2 * 2 + k], a0, a1, a2, a3, pb0[ht], pb1[ht]);
+                }
+            }
+        }
+        __syncwarp();
+        if (j + NST < nmine) {
+            fence_proxy_async_smem();
+            issue(j + NST);
+        }
+    }
+    if (consumed < nmine) {  // a wait gave up: let the copies in flight land
+        const int last = min(nmine, consumed + NST);
+        for (int j = consumed + 1; j < last; ++j)
+            mbar_wait_bounded(wbars + 8 * (j % NST), (j / NST) & 1, p.dev_error);
+    }
+
+#pragma unroll
+    for (int ht = 0; ht < NHT; ++ht) {
+        l_run[ht] += __shfl_xor_sync(0xffffffffu, l_run[ht], 1);
+        l_run[ht] += __shfl_xor_sync(0xffffffffu, l_run[ht], 2);
+        if (tq == 0) {
+            s_m[warp * kMaxGroup + ht * 8 + gq] = m_run[ht];
+            s_l[warp * kMaxGroup + ht * 8 + gq] = l_run[ht];
+        }
+    }
+    // O in its own units: code * 2^-8, weights * 2^(14 - gauge)
+    const float unit = gauge > 0 ? __uint_as_float((uint32_t)gauge << 23) * 0x1p-6f : 0.f;
+    float *s_o = reinterpret_cast<float *>(smem);  // [warp][8 heads][D]
+#pragma unroll
+    for (int ht = 0; ht < NHT; ++ht) {
+        __syncthreads();  // the ring is free (ht 0); the last heads are written (ht 1)
+#pragma unroll
+        for (int mt = 0; mt < NC; ++mt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                *reinterpret_cast<float2 *>(s_o + (warp * 8 + 2 * tq + c) * D + mt * 16 +
+                                            2 * gq) =
+                    make_float2(oacc[ht][mt][c] * unit, oacc[ht][mt][2 + c] * unit);
+        __syncthreads();
+        const int heads = min(8, G - ht * 8);
+        for (int i = threadIdx.x; i < heads * (Dh / 4); i += kThreads) {
+            const int h = i / (Dh / 4), d = (i - h * (Dh / 4)) * 4, hh = ht * 8 + h;
+            const float m0 = s_m[hh], m1 = s_m[kMaxGroup + hh];
+            const float M = fmaxf(m0, m1);
+            const float f0 = M == kNegInf ? 0.f : exp2f(m0 - M);
+            const float f1 = M == kNegInf ? 0.f : exp2f(m1 - M);
+            const float l = f0 * s_l[hh] + f1 * s_l[kMaxGroup + hh];
+            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays
+            const float4 a = *reinterpret_cast<const float4 *>(s_o + h * D + d);
+            const float4 c = *reinterpret_cast<const float4 *>(s_o + (8 + h) * D + d);
+            // a warp without weight (f = 0) has only zeros: no 0 * NaN
+            const int64_t idx =
+                ((int64_t)b * p.num_qo_heads + g * G + hh) * p.num_parts + blockIdx.y;
+            float4 o;
+            o.x = (a.x * f0 + c.x * f1) * inv;
+            o.y = (a.y * f0 + c.y * f1) * inv;
+            o.z = (a.z * f0 + c.z * f1) * inv;
+            o.w = (a.w * f0 + c.w * f1) * inv;
+            *reinterpret_cast<float4 *>(p.part_o + idx * Dh + d) = o;
+            if (d == 0) p.part_lse[idx] = l == 0.f ? kNegInf : M + log2f(l);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// merge of the partitions, sink, cast: one warp per (sequence, query head)
+// ---------------------------------------------------------------------------
+constexpr int kMergeThreads = 128;
+
+// out = sum_i 2^(lse_i - M) o_i / (sum_i 2^(lse_i - M) + 2^(sink - M)).
+// SPLIT warps share a row's partitions (long sequences of few heads).
+template <int SPLIT>
+__global__ void __launch_bounds__(kMergeThreads)
+merge_fp8_kernel(const DecodeParams p, int D, int block_size) {
+    constexpr int kUnits = kMergeThreads / 32 / SPLIT;
+    __shared__ float s_acc[SPLIT > 1 ? kMergeThreads / 32 : 1][256];
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t unit = (int64_t)blockIdx.x * kUnits + warp / SPLIT;
+    const bool live = unit < (int64_t)p.batch * p.num_qo_heads;
+    if (SPLIT == 1 && !live) return;
+    const int b = live ? (int)(unit / p.num_qo_heads) : 0;
+    const int h = live ? (int)(unit % p.num_qo_heads) : 0;
+    const int L = clipped_len(p, b, block_size, false);
+    const int P = p.partition_size, start = first_kept(L, p.window_left);
+    const int n = live && L > 0 ? (L - 1) / P - start / P + 1 : 0;
+    const int64_t base = ((int64_t)b * p.num_qo_heads + h) * p.num_parts;
+    const float *lp = p.part_lse + base;
+    const float sink = p.sink ? p.sink[h] * kLog2e : kNegInf;
+    float M = sink;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, lp[i]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    const float Ms = M == kNegInf ? 0.f : M;
+    float sum = 0.f;
+    for (int i = lane; i < n; i += 32) sum += exp2f(lp[i] - Ms);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    const float lam = sum + exp2f(sink - Ms);
+    // lane l sums columns 4l .. 4l+3 (and 128 + 4l .. for D = 256)
+    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    const int c0 = 4 * lane;
+    const float *po = p.part_o + base * D;
+#pragma unroll 4
+    for (int i = warp % SPLIT; i < n; i += SPLIT) {
+        const float w = exp2f(lp[i] - Ms);
+        const float *row = po + (int64_t)i * D;
+        if (c0 < D) {
+            const float4 v = *reinterpret_cast<const float4 *>(row + c0);
+            acc[0].x = fmaf(w, v.x, acc[0].x);
+            acc[0].y = fmaf(w, v.y, acc[0].y);
+            acc[0].z = fmaf(w, v.z, acc[0].z);
+            acc[0].w = fmaf(w, v.w, acc[0].w);
+        }
+        if (c0 + 128 < D) {
+            const float4 v = *reinterpret_cast<const float4 *>(row + 128 + c0);
+            acc[1].x = fmaf(w, v.x, acc[1].x);
+            acc[1].y = fmaf(w, v.y, acc[1].y);
+            acc[1].z = fmaf(w, v.z, acc[1].z);
+            acc[1].w = fmaf(w, v.w, acc[1].w);
+        }
+    }
+    if (SPLIT > 1) {
+        *reinterpret_cast<float4 *>(&s_acc[warp][c0]) = acc[0];
+        *reinterpret_cast<float4 *>(&s_acc[warp][128 + c0]) = acc[1];
+        __syncthreads();
+        if (warp % SPLIT != 0 || !live) return;
+#pragma unroll
+        for (int w = 1; w < SPLIT; ++w)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float4 v =
+                    *reinterpret_cast<const float4 *>(&s_acc[warp + w][k * 128 + c0]);
+                acc[k].x += v.x;
+                acc[k].y += v.y;
+                acc[k].z += v.z;
+                acc[k].w += v.w;
+            }
+    }
+    const float inv = lam > 0.f ? 1.f / lam : (lam == 0.f ? 0.f : lam);
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + unit * D;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (c0 + k * 128 < D)
+            *reinterpret_cast<uint2 *>(out + k * 128 + c0) =
+                make_uint2(pack_bf16(acc[k].x * inv, acc[k].y * inv),
+                           pack_bf16(acc[k].z * inv, acc[k].w * inv));
+    if (p.lse_out && lane == 0)
+        p.lse_out[unit] = lam == 0.f ? kNegInf : (Ms + log2f(lam)) * kLn2;
+}
+
+cudaError_t launch_merge_fp8(const DecodeParams &p, int D, int BS, cudaStream_t stream) {
+    const int64_t units = (int64_t)p.batch * p.num_qo_heads;
+    if (p.num_parts > 16) {
+        return launch_pdl(merge_fp8_kernel<4>, dim3((unsigned)units), dim3(kMergeThreads), 0,
+                          stream, p, D, BS);
+    }
+    constexpr int kUnits = kMergeThreads / 32;
+    return launch_pdl(merge_fp8_kernel<1>, dim3((unsigned)((units + kUnits - 1) / kUnits)),
+                      dim3(kMergeThreads), 0, stream, p, D, BS);
+}
+
+template <int D, int BS, int NHT>
+cudaError_t launch_one(const DecodeFp8Params &p, const CUtensorMap *tk, const CUtensorMap *tv,
+                       cudaStream_t stream) {
+    constexpr int NST = D == 64 ? 4 : 2;
+    using C = Shape<D, NST>;
+    auto kern = p.d.hnd ? decode_fp8_kernel<D, BS, NHT, NST, true>
+                        : decode_fp8_kernel<D, BS, NHT, NST, false>;
+    // a partition meets at most partition_size / 32 + 1 stages
+    const int smem = C::SMEM_FIXED + (p.d.partition_size / kTok + 1) * (kTok / BS) * 4;
+    cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(p.d.num_kv_heads, p.d.num_parts, p.d.batch), dim3(kThreads),
+                      (size_t)smem, stream, p, *tk, *tv);
+}
+
+template <int D>
+cudaError_t launch_d(const DecodeFp8Params &p, int BS, const CUtensorMap *tk,
+                     const CUtensorMap *tv, cudaStream_t stream) {
+    if (BS == 16)
+        return p.d.group <= 8 ? launch_one<D, 16, 1>(p, tk, tv, stream)
+                              : launch_one<D, 16, 2>(p, tk, tv, stream);
+    return p.d.group <= 8 ? launch_one<D, 32, 1>(p, tk, tv, stream)
+                          : launch_one<D, 32, 2>(p, tk, tv, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_fp8(const DecodeFp8Params &p, const pkv_cache_desc &cache,
+                              const CUtensorMap *tmap_k, const CUtensorMap *tmap_v,
+                              cudaStream_t stream) {
+    const int D = cache.head_dim, BS = cache.block_size;
+    cudaError_t e;
+    if (D <= 64)
+        e = launch_d<64>(p, BS, tmap_k, tmap_v, stream);
+    else if (D <= 128)
+        e = launch_d<128>(p, BS, tmap_k, tmap_v, stream);
+    else
+        e = launch_d<256>(p, BS, tmap_k, tmap_v, stream);
+    if (e != cudaSuccess) return e;
+    return launch_merge_fp8(p.d, D, BS, stream);
+}
+
+}  // namespace pkv

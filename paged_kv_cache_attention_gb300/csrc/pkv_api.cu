@@ -10,6 +10,7 @@
 #include <mutex>
 #include <vector>
 
+#include "pkv_fp8.h"
 #include "pkv_internal.h"
 
 namespace pkv {
@@ -143,6 +144,18 @@ pkv_status from_cuda(cudaError_t e) {
 
 }  // namespace
 
+pkv_status encode_map_3d(CUtensorMap *map, CUtensorMapDataType type, const void *base,
+                         const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
+                         const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle) {
+    auto enc = encoder();
+    if (!enc) return PKV_ERR_CUDA;
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(map, type, 3, const_cast<void *>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_CUDA;
+}
+
 int device_sm_count() {
     static std::atomic<int> cache[kMaxDevices];
     int dev = 0;
@@ -197,7 +210,7 @@ const char *pkv_status_string(int status) {
     }
 }
 
-int pkv_version(void) { return 501; }
+int pkv_version(void) { return 600; }
 
 pkv_status pkv_get_device_error(const int32_t *dev_error, int32_t *bits, int clear,
                                 void *stream) {

@@ -1,0 +1,133 @@
+// pkv_fp8.cuh -- device helpers of the 8-bit cache.
+//
+// A cached row (one token, one kv head) is D e4m3 codes and one E8M0 byte b:
+// value_i = code_i * 2^(b - 127).  The scale is a power of two, so
+//   * the value has e4m3's 4 significant bits and is exact in bf16,
+//   * writing rounds once (x * 2^-e is exact in fp32), and
+//   * the attention kernels can move the scale into exponents.
+// e4m3's relative step does not depend on the scale: rounding max|x| / 448 up
+// to a power of two costs nothing but up to one binade of the smallest
+// (subnormal) codes.
+#pragma once
+
+#include "pkv_device.cuh"
+#include "pkv_fp8.h"
+
+namespace pkv {
+
+constexpr uint32_t kScaleNaN = 255u;  // a row that holds a NaN or an infinity
+
+// E8M0 byte of a row whose largest magnitude has the fp32 bits `amax` (sign
+// cleared): e = ceil(log2(amax / 448)), clamped to [-126, 119].  amax =
+// m * 2^x with 1 <= m < 2 and 448 = 1.75 * 2^8, so e = x - 8 when m <= 1.75
+// and x - 7 above: the carry of adding 2^21 - 1 to the bits decides.  119:
+// 448 * 2^119 is the largest code value that a float holds.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
+    if (amax >= 0x7f800000u) return kScaleNaN;
+    const int e = (int)((amax + 0x1fffffu) >> 23) - 135;
+    return (uint32_t)(min(max(e, -126), 119) + 127);
+}
+
+// 2^-(byte - 127) as a float, for bytes written by scale_byte.
+__device__ __forceinline__ float scale_inverse(uint32_t byte) {
+    return byte == kScaleNaN ? 0.f : __uint_as_float((254u - byte) << 23);
+}
+
+// 2^(byte - 127); 255 is NaN.  (2^-127, byte 0, is a subnormal float.)
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+    if (byte == kScaleNaN) return __uint_as_float(0x7fffffffu);
+    return byte == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
+}
+
+// Two floats -> two e4m3 codes, nearest even, saturating at 448; lo in the low byte.
+__device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Four codes from four floats times `inv`; a row of scale byte 255 stores 0.
+__device__ __forceinline__ uint32_t quant4(const float *x, float inv, bool bad) {
+    if (bad) return 0u;
+    return cvt_e4m3x2(x[0] * inv, x[1] * inv) | (cvt_e4m3x2(x[2] * inv, x[3] * inv) << 16);
+}
+
+// The codes of bytes 0 and 2 (lo) / 1 and 3 (hi) of w as f16 pairs of
+// code * 2^-8: an e4m3 code's exponent and mantissa fields, moved to the top
+// of f16's, are the same number with exponent bias 15 instead of 7,
+// subnormals included.  The NaN codes 0x7f and 0xff, which the library never
+// writes, read as +-480.  Seven integer instructions for four codes.
+__device__ __forceinline__ uint32_t e4m3_even_f16(uint32_t w) {
+    return ((w << 7) & 0x3f803f80u) | ((w << 8) & 0x80008000u);
+}
+__device__ __forceinline__ uint32_t e4m3_odd_f16(uint32_t w) {
+    return ((w >> 1) & 0x3f803f80u) | (w & 0x80008000u);
+}
+
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1,
+                                              uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+        "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two fp32 -> packed f16x2 (nearest even); lo in the low half.
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// 16 e4m3 codes (one 16-byte vector) times 2^(byte-127) as 16 bf16: exact.
+// A code's fields moved to the top of bf16's low exponent bits are
+// code * 2^-120; the two factors bring 2^120 and the scale.  One product with
+// 2^(120 + e) would leave bf16's range for e > 7, so the exponent is split.
+__device__ __forceinline__ void dequant16_bf16(const uint4 &c, uint32_t byte, uint32_t (&r)[8]) {
+    const int e = (int)byte - 127;
+    // 2^(120 + e1) * 2^e2, e1 + e2 = e, both factors normal
+    const int e1 = min(e, 0) > -120 ? min(e, 0) : -120, e2 = e - e1;
+    const uint32_t f1 = (uint32_t)(e1 + 120 + 127) << 7;
+    const uint32_t f2 = byte == kScaleNaN ? 0x7fffu : (uint32_t)(e2 + 127) << 7;
+    __nv_bfloat162 m1, m2;
+    *reinterpret_cast<uint32_t *>(&m1) = f1 | (f1 << 16);
+    *reinterpret_cast<uint32_t *>(&m2) = f2 | (f2 << 16);
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // bytes (0, 1) and (2, 3) side by side, each in the top byte of a half
+        const uint32_t p0 = __byte_perm(w[i], 0u, 0x1404), p1 = __byte_perm(w[i], 0u, 0x3424);
+        const uint32_t h0 = (p0 & 0x80008000u) | ((p0 >> 4) & 0x07f007f0u);
+        const uint32_t h1 = (p1 & 0x80008000u) | ((p1 >> 4) & 0x07f007f0u);
+        __nv_bfloat162 a0, a1;
+        *reinterpret_cast<uint32_t *>(&a0) = h0;
+        *reinterpret_cast<uint32_t *>(&a1) = h1;
+        a0 = __hmul2(a0, m1);
+        a1 = __hmul2(a1, m1);
+        if (e2 != 0) {  // rare: values above 448, or below 2^-120
+            a0 = __hmul2(a0, m2);
+            a1 = __hmul2(a1, m2);
+        }
+        r[2 * i] = *reinterpret_cast<uint32_t *>(&a0);
+        r[2 * i + 1] = *reinterpret_cast<uint32_t *>(&a1);
+    }
+}
+
+// Element offset of (slot, kv head g) in a pool, and of its scale byte.
+struct PoolSlot {
+    int64_t row;    // first element of the head row
+    int64_t scale;  // index of the row's E8M0 byte
+};
+
+__device__ __forceinline__ PoolSlot pool_slot(const PoolArgs &p, int64_t slot, int g) {
+    const int64_t blk = slot / p.block_size, off = slot - blk * p.block_size;
+    const int64_t hnd = (blk * p.num_kv_heads + g) * p.block_size + off;
+    PoolSlot s;
+    s.scale = hnd;
+    s.row = (p.hnd ? hnd : slot * p.num_kv_heads + g) * p.head_dim;
+    return s;
+}
+
+}  // namespace pkv

@@ -1,0 +1,256 @@
+// qk_norm_rope.cu -- RMS norm of every q and k head, the rotary embedding and
+// the cache write in one pass over a step's new tokens.
+//
+// Per token t and q or k head row x (D values):
+//   y_i = x_i / sqrt(mean_j x_j^2 + eps) * w_i
+//   the pairs of the first rotary_dim dimensions turn by the table's angle at
+//   positions[t], as in rope_reshape_and_cache; the result rounds once.
+// The rotated key (as rounded) and the value go to the pools at the token's
+// slot: copied, or quantised as in reshape_and_cache_fp8.
+//
+// HBM bound: q, k, v are read once, q_out, k_out and the pools written once.
+// A head row is held by LPR = D/8 lanes (rounded up to a power of two) of a
+// warp, eight values each, so the sum of squares and a neox pair's other half
+// are shuffles and nothing is read twice.  A group of LPR lanes takes several
+// heads of one token, with the token's cos/sin and the weights in registers.
+#include <type_traits>
+
+#include "pkv_fp8.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kThreads = 128;
+
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, float (&x)[8]) {
+    if constexpr (sizeof(T) == 2) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    } else {
+        const float4 a = *reinterpret_cast<const float4 *>(p);
+        const float4 b = *(reinterpret_cast<const float4 *>(p) + 1);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T *p, const float (&x)[8]) {
+    if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                                                   pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+    } else {
+        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+        *(reinterpret_cast<float4 *>(p) + 1) = make_float4(x[4], x[5], x[6], x[7]);
+    }
+}
+
+// The value a store of T keeps.
+template <typename T>
+__device__ __forceinline__ float rounded(float x) {
+    if constexpr (sizeof(T) == 2) return __bfloat162float(__float2bfloat16_rn(x));
+    return x;
+}
+
+// Store one row to the pool at `slot` (in range): a copy, or codes and scale.
+// Every lane of the warp calls it (shuffles); `store` says whether this
+// lane's group writes.
+template <typename T, int LPR, bool FP8>
+__device__ __forceinline__ void pool_store(const NormRopeParams &p, bool store, int64_t slot,
+                                           int g, bool is_v, int sub, bool active,
+                                           const float (&x)[8]) {
+    if constexpr (FP8) {
+        uint32_t amax = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7fffffffu);
+#pragma unroll
+        for (int off = LPR / 2; off > 0; off >>= 1)
+            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+        if (!store) return;
+        const uint32_t byte = scale_byte(amax);
+        const float inv = scale_inverse(byte);
+        const bool bad = byte == kScaleNaN;
+        const PoolSlot s = pool_slot(p.pool, slot, g);
+        if (active)
+            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(is_v ? p.pool.v : p.pool.k) +
+                                       s.row + sub * 8) =
+                make_uint2(quant4(x, inv, bad), quant4(x + 4, inv, bad));
+        if (sub == 0) (is_v ? p.pool.v_scale : p.pool.k_scale)[s.scale] = (uint8_t)byte;
+    } else {
+        if (!store || !active) return;
+        const PoolSlot s = pool_slot(p.pool, slot, g);
+        store8<T>(static_cast<T *>(is_v ? p.pool.v : p.pool.k) + s.row + sub * 8, x);
+    }
+}
+
+// gpt groups of LPR lanes share a token (gpt a power of two dividing the
+// CTA's groups); group i takes the head rows i, i + gpt, ... of the
+// Hq + 2 Hkv rows of q, k and v.
+template <typename T, int LPR, bool FP8>
+__global__ void __launch_bounds__(kThreads)
+norm_rope_kernel(const NormRopeParams p, int gpt) {
+    pdl_trigger();
+    pdl_wait();
+    constexpr int kGroups = kThreads / LPR;
+    const int sub = threadIdx.x % LPR, grp = threadIdx.x / LPR;
+    const int D = p.pool.head_dim, Hq = p.num_qo_heads, Hkv = p.pool.num_kv_heads;
+    const bool active = sub * 8 < D;
+    const int64_t t = (int64_t)blockIdx.x * (kGroups / gpt) + grp / gpt;
+    const int r0 = grp % gpt;
+    const bool live = t < p.num_tokens;
+
+    int64_t pos = -1, slot = -1;
+    if (live) {
+        pos = __ldg(p.positions + t);
+        slot = __ldg(p.slot_mapping + t);
+        if (pos < 0 || pos >= p.max_position) {
+            if (sub == 0 && r0 == 0) flag_error(p.dev_error, PKV_DEVERR_POSITION);
+            pos = -1;  // the token is left as it is
+        } else if (slot >= p.pool.capacity) {
+            if (sub == 0 && r0 == 0) flag_error(p.dev_error, PKV_DEVERR_SLOT);
+            slot = -1;
+        }
+    }
+    const bool on = live && pos >= 0;
+
+    // this lane's dimensions are 8*sub .. 8*sub+7; neox: lane sub < half_l
+    // holds the first member of its pairs and lane sub + half_l the second
+    const int rd = p.rotary_dim, half_l = rd / 16;
+    const bool rot = active && sub * 8 < rd;
+    float cs[8], sn[8];  // neox: eight frequencies; GPT-J: four
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        cs[i] = 1.f;
+        sn[i] = 0.f;
+    }
+    if (on && rot) {
+        const float2 *row = p.cos_sin + pos * (rd / 2);
+        const int f0 = p.neox ? 8 * (sub < half_l ? sub : sub - half_l) : 4 * sub;
+        const int nf = p.neox ? 8 : 4;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            if (i >= nf) break;
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(row + f0 + i));
+            cs[i] = v.x;
+            sn[i] = v.y;
+            cs[i + 1] = v.z;
+            sn[i + 1] = v.w;
+        }
+        if (p.neox && sub < half_l)  // x_a' = x_a c - x_b s
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sn[i] = -sn[i];
+    }
+    const int partner = p.neox && rot ? (sub < half_l ? sub + half_l : sub - half_l) : sub;
+    const int src_lane = (threadIdx.x & 31) - sub + partner;
+
+    const int rows = Hq + 2 * Hkv;
+    const int rounds = (rows + gpt - 1) / gpt;  // the same for every lane of the CTA
+    constexpr int UNR = 3;
+    for (int k0 = 0; k0 < rounds; k0 += UNR) {
+        float x[UNR][8];
+#pragma unroll
+        for (int u = 0; u < UNR; ++u) {
+            const int r = r0 + (k0 + u) * gpt;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
+            if (!on || !active || r >= rows) continue;
+            const T *src = r < Hq ? static_cast<const T *>(p.query) + t * p.q_stride + r * D
+                           : r < Hq + Hkv
+                               ? static_cast<const T *>(p.key) + t * p.k_stride + (r - Hq) * D
+                               : static_cast<const T *>(p.value) + t * p.v_stride +
+                                     (r - Hq - Hkv) * D;
+            load8<T>(src + sub * 8, x[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < UNR; ++u) {
+            const int r = r0 + (k0 + u) * gpt;
+            const bool here = on && r < rows;
+            const bool is_v = r >= Hq + Hkv;
+            // the norm and the rotation of a v row are computed and dropped:
+            // the shuffles need every lane of the warp
+            float ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(x[u][i], x[u][i], ss);
+#pragma unroll
+            for (int off = LPR / 2; off > 0; off >>= 1)
+                ss += __shfl_xor_sync(0xffffffffu, ss, off);
+            const float inv = 1.f / sqrtf(ss / (float)D + p.eps);
+            float y[8], w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = 0.f;
+            if (here && !is_v && active) {
+                const void *wp = r < Hq ? p.q_weight : p.k_weight;
+                if (p.weight_f32)
+                    load8<float>(static_cast<const float *>(wp) + sub * 8, w);
+                else
+                    load8<T>(static_cast<const T *>(wp) + sub * 8, w);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = x[u][i] * inv * w[i];
+            if (p.neox) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float o = __shfl_sync(0xffffffffu, y[i], src_lane);
+                    if (rot) y[i] = fmaf(o, sn[i], y[i] * cs[i]);
+                }
+            } else if (rot) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float a = y[2 * i], b = y[2 * i + 1];
+                    y[2 * i] = fmaf(-b, sn[i], a * cs[i]);
+                    y[2 * i + 1] = fmaf(a, sn[i], b * cs[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = is_v ? x[u][i] : rounded<T>(y[i]);
+            if (here && active && r < Hq)
+                store8<T>(static_cast<T *>(p.query_out) + t * p.qo_stride + r * D + sub * 8, y);
+            else if (here && active && !is_v)
+                store8<T>(static_cast<T *>(p.key_out) + t * p.ko_stride + (r - Hq) * D + sub * 8,
+                          y);
+            pool_store<T, LPR, FP8>(p, here && r >= Hq && slot >= 0, slot,
+                                    is_v ? r - Hq - Hkv : r - Hq, is_v, sub, active, y);
+        }
+    }
+}
+
+template <typename T, int LPR, bool FP8>
+cudaError_t launch_lpr(const NormRopeParams &p, cudaStream_t stream) {
+    constexpr int kGroups = kThreads / LPR;
+    const int rows = p.num_qo_heads + 2 * p.pool.num_kv_heads;
+    int gpt = 1;
+    while (gpt * 2 <= kGroups && gpt * 2 <= rows) gpt *= 2;
+    const int64_t per_cta = kGroups / gpt;
+    const int64_t blocks = (p.num_tokens + per_cta - 1) / per_cta;
+    if (blocks > 0x7fffffffLL) return cudaErrorNotSupported;
+    return launch_pdl(norm_rope_kernel<T, LPR, FP8>, dim3((unsigned)blocks), dim3(kThreads), 0,
+                      stream, p, gpt);
+}
+
+template <typename T, bool FP8>
+cudaError_t launch_t(const NormRopeParams &p, cudaStream_t stream) {
+    const int D = p.pool.head_dim;
+    if (D <= 64) return launch_lpr<T, 8, FP8>(p, stream);
+    if (D <= 128) return launch_lpr<T, 16, FP8>(p, stream);
+    return launch_lpr<T, 32, FP8>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_rope(const NormRopeParams &p, int dtype, cudaStream_t stream) {
+    if (p.num_tokens == 0) return cudaSuccess;
+    if (p.pool.k_scale)
+        return dtype == PKV_F32 ? launch_t<float, true>(p, stream)
+                                : launch_t<__nv_bfloat16, true>(p, stream);
+    return dtype == PKV_F32 ? launch_t<float, false>(p, stream)
+                            : launch_t<__nv_bfloat16, false>(p, stream);
+}
+
+}  // namespace pkv
