@@ -531,6 +531,58 @@ PKV_API pkv_status pkv_qk_norm_rope_reshape_and_cache(
     const void *k_weight, int weight_f32, float eps, const float *cos_sin, int max_position,
     int rotary_dim, int is_neox_style, int32_t *dev_error, void *stream);
 
+/* Workspace bytes pkv_paged_tree_attention needs (its split-KV partials). */
+PKV_API size_t pkv_paged_tree_attention_workspace_size(int batch, int num_qo_heads,
+                                                       int num_kv_heads, int head_dim,
+                                                       int64_t total_q, int max_seqlen_q,
+                                                       int max_seqlen, int partition_size,
+                                                       int window_left);
+
+/*
+ * paged_tree_attention: attention of a tree (or any set) of drafted tokens of
+ * every request over its pages, in which each drafted token sees the cached
+ * context and those drafts its mask names.  Request r has q_len =
+ * cu_seq_lens_q[r+1] - cu_seq_lens_q[r] drafts, whose K/V are already in the
+ * pages as the last q_len of its cache_seqlens[r] positions (write them first
+ * with one of the cache writes); ctx = cache_seqlens[r] - q_len.  Draft i:
+ *   sees key j < ctx, and key ctx + n (draft n) iff bit n of its mask is set;
+ *   pos(j) = j for j < ctx, ctx + tree_depth[n] for draft n, qpos = ctx +
+ *   tree_depth[i]; keep key j iff seen and (window_left < 0 or pos(j) >= qpos -
+ *   window_left); the ALiBi bias is alibi_slopes[h] * (pos(j) - qpos); sink, lse
+ *   and a draft that keeps no key as in pkv_paged_decode.
+ *   out, q         [total_q, num_qo_heads, head_dim] bf16, contiguous; rows of
+ *                  no request are not touched
+ *   cache.dtype    PKV_BF16 (k_scale, v_scale ignored) or PKV_E4M3 (the 8-bit
+ *                  cache, scales 16-byte aligned)
+ *   block_table    [batch, max_blocks_per_seq]; cu_seq_lens_q [batch + 1];
+ *                  cache_seqlens [batch] (all int32, device)
+ *   max_seqlen_q   host int >= every q_len, at most 256
+ *   max_seqlen     host int >= every cache_seqlens[r], at most 2^30
+ *   tree_mask      [total_q, mask_words] int64: bit n % 64 of word n / 64 is
+ *                  draft n of the same request; bits at or past q_len are
+ *                  ignored; mask_words * 64 >= max_seqlen_q
+ *   tree_depth     [total_q] int32, the draft's distance from the first draft
+ *                  position (0 for the root; below 0 reads as 0).  May be NULL
+ *                  without a window and without ALiBi, where it has no effect
+ *   partition_size split-KV partition in tokens, a multiple of 128; 0: chosen
+ *                  from the shapes
+ * A NaN or an infinity in a V row reaches only drafts that keep that key (where
+ * some drafts do not, the whole output row of one that does is NaN).  Requests
+ * whose drafts do not fit their length (q_len > cache_seqlens[r]) attend
+ * nothing and set PKV_DEVERR_SEQLEN, as do lengths beyond their maximum and
+ * offsets outside the rows of q (clipped).
+ * Supported: head sizes 64/80/96/112/128/256, block_size 16 or 32, at most 16
+ * query heads per kv head, total_q at most 2^24.
+ */
+PKV_API pkv_status pkv_paged_tree_attention(
+    void *out, const void *q, const void *k_cache, const void *v_cache, const uint8_t *k_scale,
+    const uint8_t *v_scale, pkv_cache_desc cache, const int32_t *block_table,
+    int max_blocks_per_seq, const int32_t *cu_seq_lens_q, const int32_t *cache_seqlens,
+    int max_seqlen_q, int max_seqlen, int total_q, const int64_t *tree_mask, int mask_words,
+    const int32_t *tree_depth, const float *sink, const float *alibi_slopes, int batch,
+    int num_qo_heads, int window_left, float sm_scale, int partition_size, float *lse_out,
+    void *workspace, size_t workspace_bytes, int32_t *dev_error, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

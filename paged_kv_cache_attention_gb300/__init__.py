@@ -46,7 +46,8 @@ __all__ = [
     "selftest_bounded_wait",
     "minference_sizes", "minference_prefill",
     "reshape_and_cache_fp8", "gather_cache_fp8", "paged_decode_fp8",
-    "qk_norm_rope_reshape_and_cache",
+    "qk_norm_rope_reshape_and_cache", "paged_tree_attention",
+    "paged_tree_attention_workspace_size",
     "DEVERR_BLOCK_ID", "DEVERR_SLOT", "DEVERR_SEQLEN", "DEVERR_TIMEOUT", "DEVERR_POSITION",
     "EXPORTED_SYMBOLS",
 ]
@@ -68,7 +69,8 @@ EXPORTED_SYMBOLS = (
     "pkv_minference_sizes", "pkv_minference_workspace_size", "pkv_minference_prefill",
     "pkv_paged_decode_noalloc", "pkv_get_device_error", "pkv_selftest_bounded_wait",
     "pkv_reshape_and_cache_fp8", "pkv_gather_cache_fp8", "pkv_paged_decode_fp8",
-    "pkv_qk_norm_rope_reshape_and_cache",
+    "pkv_qk_norm_rope_reshape_and_cache", "pkv_paged_tree_attention_workspace_size",
+    "pkv_paged_tree_attention",
 )
 
 
@@ -164,6 +166,13 @@ def load_library(path: Optional[str] = None):
             P, P, P, i64, i64, i64, i32, P, P, i64, i64, P, P, P, P, P, P, i64, i32, CacheDesc, P,
             P, i32, f32, P, i32, i32, i32, P, P]
         lib.pkv_qk_norm_rope_reshape_and_cache.restype = i32
+        lib.pkv_paged_tree_attention_workspace_size.argtypes = [i32, i32, i32, i32, i64, i32, i32,
+                                                                i32, i32]
+        lib.pkv_paged_tree_attention_workspace_size.restype = sz
+        lib.pkv_paged_tree_attention.argtypes = [
+            P, P, P, P, P, P, CacheDesc, P, i32, P, P, i32, i32, i32, P, i32, P, P, P, i32, i32,
+            i32, f32, i32, P, P, sz, P, P]
+        lib.pkv_paged_tree_attention.restype = i32
         _lib = lib
         return lib
 
@@ -848,3 +857,89 @@ def qk_norm_rope_reshape_and_cache(query, key, value, k_cache, v_cache, position
             int(w32), float(eps), _ptr(cos_sin), cos_sin.shape[0], rd, int(bool(is_neox_style)),
             _ptr(dev_error), _stream_handle(stream))
     _check("pkv_qk_norm_rope_reshape_and_cache", st)
+
+
+# ---------------------------------------------------------------------------
+# attention of drafted tokens
+# ---------------------------------------------------------------------------
+
+def paged_tree_attention_workspace_size(batch: int, num_qo_heads: int, num_kv_heads: int,
+                                        head_dim: int, total_q: int, max_seqlen_q: int,
+                                        max_seqlen: int, partition_size: int = 0,
+                                        window_left: int = -1) -> int:
+    return int(load_library().pkv_paged_tree_attention_workspace_size(
+        batch, num_qo_heads, num_kv_heads, head_dim, total_q, max_seqlen_q, max_seqlen,
+        partition_size, window_left))
+
+
+def paged_tree_attention(q, k_cache, v_cache, block_table, cu_seq_lens_q, cache_seqlens,
+                         max_seqlen_q: int, max_seqlen: int, tree_mask, tree_depth=None,
+                         k_scale=None, v_scale=None, sink=None, window_left: int = -1,
+                         sm_scale: Optional[float] = None, partition_size: int = 0, out=None,
+                         lse=None, workspace=None, dev_error=None, stream=None,
+                         alibi_slopes=None, layout: str = "NHD"):
+    """Attention of up to 256 drafted tokens per request over its pages; returns
+    out [total_q, Hq, D].
+
+    q: [total_q, Hq, D] bf16, the drafts of request r at rows cu_seq_lens_q[r] ..
+    ([B+1] int32); their K/V are the last q_len of the cache_seqlens[r] ([B]
+    int32) positions in the pages.  Every draft sees the context before them,
+    and draft n of its request iff bit n % 64 of tree_mask[row, n // 64] is set
+    (tree_mask [total_q, words] int64, words * 64 >= max_seqlen_q): set a
+    draft's own bit and its ancestors'.  tree_depth: [total_q] int32, a draft's
+    depth below the first draft position, needed with window_left or
+    alibi_slopes (positions are context length + depth).  Pools are bf16, or the
+    8-bit cache when k_scale and v_scale are given.  max_seqlen_q / max_seqlen:
+    host ints; partition_size: split-KV partition (a multiple of 128; 0: chosen).
+    sink, lse ([total_q, Hq] float32), window, layout as paged_decode."""
+    torch = _torch()
+    if k_scale is not None or v_scale is not None:
+        desc = _cache_desc_fp8(k_cache, v_cache, k_scale, v_scale, layout)
+    else:
+        desc = _cache_desc(k_cache, v_cache, layout)
+    _cuda_contig("q", q, torch.bfloat16, 3)
+    _cuda_contig("block_table", block_table, torch.int32, 2)
+    _cuda_contig("cu_seq_lens_q", cu_seq_lens_q, torch.int32, 1)
+    _cuda_contig("cache_seqlens", cache_seqlens, torch.int32, 1)
+    _cuda_contig("tree_mask", tree_mask, torch.int64, 2)
+    total_q, Hq, D = q.shape
+    B = cache_seqlens.shape[0]
+    _require(D == desc.head_dim, "head_dim of q and cache differ")
+    _require(cu_seq_lens_q.shape[0] == B + 1, "cu_seq_lens_q must have B + 1 entries")
+    _require(block_table.shape[0] == B, "block_table must have one row per request")
+    _require(tree_mask.shape[0] == total_q and 64 * tree_mask.shape[1] >= max_seqlen_q,
+             "tree_mask must be [total_q, words] with words * 64 >= max_seqlen_q")
+    if tree_depth is not None:
+        _cuda_contig("tree_depth", tree_depth, torch.int32, 1)
+        _require(tree_depth.shape[0] == total_q, "tree_depth must have total_q entries")
+    _require(tree_depth is not None or (window_left < 0 and alibi_slopes is None),
+             "tree_depth is needed with a window or ALiBi slopes")
+    _head_vector("sink", sink, Hq)
+    _head_vector("alibi_slopes", alibi_slopes, Hq)
+    if out is not None:
+        _cuda_contig("out", out, q.dtype, 3)
+        _require(out.shape == q.shape, "out must be shaped like q")
+    if lse is not None:
+        _cuda_contig("lse", lse, torch.float32, 2)
+        _require(tuple(lse.shape) == (total_q, Hq), "lse must be [total_q, Hq]")
+    _check_error_word(dev_error)
+    _same_device(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_seq_lens_q,
+                 cache_seqlens, tree_mask, tree_depth, sink, alibi_slopes, out, lse, workspace,
+                 dev_error)
+    scale = float(sm_scale) if sm_scale is not None else D ** -0.5
+    need = paged_tree_attention_workspace_size(B, Hq, desc.num_kv_heads, D, total_q,
+                                               max_seqlen_q, max_seqlen, partition_size,
+                                               window_left)
+    with _launch_on(q, stream):
+        if out is None:
+            out = torch.empty_like(q)
+        ws = _workspace(need, q.device, workspace)
+        st = load_library().pkv_paged_tree_attention(
+            _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), desc,
+            _ptr(block_table), block_table.shape[1], _ptr(cu_seq_lens_q), _ptr(cache_seqlens),
+            int(max_seqlen_q), int(max_seqlen), total_q, _ptr(tree_mask), tree_mask.shape[1],
+            _ptr(tree_depth), _ptr(sink), _ptr(alibi_slopes), B, Hq, int(window_left), scale,
+            int(partition_size), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(),
+            _ptr(dev_error), _stream_handle(stream))
+    _check("pkv_paged_tree_attention", st)
+    return out

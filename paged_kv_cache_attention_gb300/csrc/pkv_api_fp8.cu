@@ -77,6 +77,46 @@ pkv_status pool_map(CUtensorMap *map, const void *base, const pkv_cache_desc &c)
                          w * e == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Partitions of the tree attention: `partition_size` keys each when given,
+// else as many as keep the SMs busy -- about two CTAs' worth of work per slot
+// for kTreeSlots resident CTAs -- and not below kMinTreePart keys.  A fixed
+// slot count, so that the workspace of a problem does not depend on the device.
+constexpr int kTreeTile = 128, kMaxDraft = 256, kTreeSlots = 304, kMinTreePart = 256;
+
+struct TreeSplit {
+    int part, row_tiles;
+    int64_t num_parts;
+    size_t lse_bytes, total;
+};
+
+TreeSplit tree_split(int batch, int Hq, int Hkv, int D, int max_q, int64_t total_q, int max_len,
+                     int partition_size, int window_left) {
+    TreeSplit s;
+    const int64_t rows = (int64_t)max_q * (Hq / Hkv);
+    s.row_tiles = (int)((rows + kTreeTile - 1) / kTreeTile);
+    if (s.row_tiles < 1) s.row_tiles = 1;
+    int64_t span = max_len;
+    if (window_left >= 0 && (int64_t)window_left + max_q < span) span = window_left + max_q;
+    s.part = partition_size;
+    if (s.part == 0) {
+        const int64_t units = (int64_t)batch * Hkv * s.row_tiles;
+        const int64_t want = (2 * kTreeSlots + units - 1) / units;
+        int64_t part = (span + want - 1) / want;
+        part = (part + kTreeTile - 1) / kTreeTile * kTreeTile;
+        s.part = (int)(part < kMinTreePart ? kMinTreePart : part);
+    }
+    s.num_parts = ((int64_t)max_len + s.part - 1) / s.part;
+    if (window_left >= 0) {
+        const int64_t w = (span + s.part - 1) / s.part + 1;
+        if (w < s.num_parts) s.num_parts = w;
+    }
+    if (s.num_parts < 1) s.num_parts = 1;
+    const size_t units = (size_t)total_q * Hq * (size_t)s.num_parts;
+    s.lse_bytes = s.num_parts > 1 ? (units * sizeof(float) + 255) / 256 * 256 : 0;
+    s.total = s.num_parts > 1 ? s.lse_bytes + units * D * sizeof(float) + 256 : 256;
+    return s;
+}
+
 }  // namespace
 
 }  // namespace pkv
@@ -291,6 +331,98 @@ pkv_status pkv_qk_norm_rope_reshape_and_cache(
     p.pool = pool_args(cache, k_cache, v_cache, fp8 ? k_scale : nullptr,
                        fp8 ? v_scale : nullptr);
     return from_cuda(launch_norm_rope(p, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+size_t pkv_paged_tree_attention_workspace_size(int batch, int num_qo_heads, int num_kv_heads,
+                                               int head_dim, int64_t total_q, int max_seqlen_q,
+                                               int max_seqlen, int partition_size,
+                                               int window_left) {
+    if (batch <= 0 || num_kv_heads <= 0 || num_qo_heads < num_kv_heads || head_dim <= 0 ||
+        total_q < 0 || max_seqlen_q < 0 || max_seqlen < 0 || partition_size < 0)
+        return 256;
+    return tree_split(batch, num_qo_heads, num_kv_heads, head_dim, max_seqlen_q, total_q,
+                      max_seqlen, partition_size, window_left)
+        .total;
+}
+
+pkv_status pkv_paged_tree_attention(
+    void *out, const void *q, const void *k_cache, const void *v_cache, const uint8_t *k_scale,
+    const uint8_t *v_scale, pkv_cache_desc cache, const int32_t *block_table,
+    int max_blocks_per_seq, const int32_t *cu_seq_lens_q, const int32_t *cache_seqlens,
+    int max_seqlen_q, int max_seqlen, int total_q, const int64_t *tree_mask, int mask_words,
+    const int32_t *tree_depth, const float *sink, const float *alibi_slopes, int batch,
+    int num_qo_heads, int window_left, float sm_scale, int partition_size, float *lse_out,
+    void *workspace, size_t workspace_bytes, int32_t *dev_error, void *stream) {
+    pkv_status st = check_pool(cache, true, true);
+    if (st != PKV_OK) return st;
+    if (cache.dtype == PKV_F32) return PKV_ERR_UNSUPPORTED;
+    const bool fp8 = cache.dtype == PKV_E4M3;
+    if (batch < 0 || batch > 65535 || num_qo_heads <= 0 || max_seqlen < 0 || max_seqlen_q < 0 ||
+        total_q < 0 || max_blocks_per_seq <= 0 || window_left < -1 || !std::isfinite(sm_scale) ||
+        partition_size < 0 || partition_size % kTreeTile != 0)
+        return PKV_ERR_INVALID_ARG;
+    if (num_qo_heads % cache.num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
+    const int G = num_qo_heads / cache.num_kv_heads;
+    if (G > 16 || max_seqlen_q > kMaxDraft || max_seqlen > (1 << 30) || total_q > (1 << 24))
+        return PKV_ERR_UNSUPPORTED;
+    if (mask_words * (int64_t)64 < max_seqlen_q) return PKV_ERR_INVALID_ARG;
+    // positions of drafts come from their depths
+    if ((window_left >= 0 || alibi_slopes) && !tree_depth) return PKV_ERR_INVALID_ARG;
+    if (batch == 0 || total_q == 0 || max_seqlen_q == 0) return PKV_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_table || !cu_seq_lens_q || !cache_seqlens ||
+        !tree_mask || (fp8 && (!k_scale || !v_scale)))
+        return PKV_ERR_INVALID_ARG;
+    if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(block_table, 4) || !aligned(cu_seq_lens_q, 4) || !aligned(cache_seqlens, 4) ||
+        !aligned(tree_mask, 8) || (fp8 && (!aligned(k_scale, 16) || !aligned(v_scale, 16))))
+        return PKV_ERR_INVALID_ARG;
+    const TreeSplit s =
+        tree_split(batch, num_qo_heads, cache.num_kv_heads, cache.head_dim, max_seqlen_q,
+                   total_q, max_seqlen, partition_size, window_left);
+    if (s.num_parts > 65535) return PKV_ERR_UNSUPPORTED;  // grid.y limit
+    if (s.num_parts > 1 && (!workspace || !aligned(workspace, 256) || workspace_bytes < s.total))
+        return PKV_ERR_WORKSPACE;
+
+    TreeParams p;
+    std::memset(&p, 0, sizeof p);
+    p.q = q;
+    p.out = out;
+    p.block_table = block_table;
+    p.cu_q = cu_seq_lens_q;
+    p.seqlens = cache_seqlens;
+    p.mask = tree_mask;
+    p.depth = tree_depth;
+    p.sink = sink;
+    p.alibi = alibi_slopes;
+    p.lse_out = lse_out;
+    p.part_lse = static_cast<float *>(workspace);
+    p.part_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + s.lse_bytes);
+    p.dev_error = dev_error;
+    p.k_scale = fp8 ? k_scale : nullptr;
+    p.v_scale = fp8 ? v_scale : nullptr;
+    p.num_blocks = cache.num_blocks;
+    p.batch = batch;
+    p.num_qo_heads = num_qo_heads;
+    p.num_kv_heads = cache.num_kv_heads;
+    p.group = G;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.max_seqlen = max_seqlen;
+    p.max_seqlen_q = max_seqlen_q;
+    p.total_q = total_q;
+    p.mask_words = mask_words;
+    p.window_left = window_left;
+    p.head_dim = cache.head_dim;
+    p.hnd = cache.layout == PKV_HND ? 1 : 0;
+    p.block_size = cache.block_size;
+    p.partition_size = s.part;
+    p.num_parts = (int)s.num_parts;
+    p.row_tiles = s.row_tiles;
+    p.scale_log2 = sm_scale * 1.4426950408889634f;
+
+    alignas(64) CUtensorMap tk, tv;
+    if ((st = pool_map(&tk, k_cache, cache)) != PKV_OK) return st;
+    if ((st = pool_map(&tv, v_cache, cache)) != PKV_OK) return st;
+    return from_cuda(launch_tree(p, &tk, &tv, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

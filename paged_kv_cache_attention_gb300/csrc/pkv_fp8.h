@@ -70,7 +70,6 @@ struct TreeParams {
     float *lse_out;                // [total_q, Hq] or nullptr
     float *part_lse;               // [total_q, Hq, num_parts] (log2 units)
     float *part_o;                 // [total_q, Hq, num_parts, D]
-    int32_t *abort;                // launch-wide abort word (zeroed by the launcher)
     int32_t *dev_error;
     const uint8_t *k_scale, *v_scale;
     int64_t num_blocks;

@@ -110,7 +110,7 @@ def paged(lens, bs, num_blocks, gen):
 
 def attend(q, k, v, keep, scale, sink=None, bias=None):
     """q [T, Hq, D], k/v [n, Hkv, D] (float64), keep [T, n] -> out, lse and the
-    bound's ingredients: sum_j p_j |v_j| and scale * max_j sum |q k_j|."""
+    bound's ingredients: sum_j p_j |v_j| and |scale| * max_j sum |q k_j|."""
     t, hq, d = q.shape
     n, hkv = k.shape[0], k.shape[1]
     grp = hq // hkv
@@ -127,7 +127,7 @@ def attend(q, k, v, keep, scale, sink=None, bias=None):
             if bias is not None:
                 lg = lg + bias[h, i][sel]
             if lg.numel():
-                smax[i, h] = scale * (kk[sel].abs() @ q[i, h].abs()).max()
+                smax[i, h] = abs(scale) * (kk[sel].abs() @ q[i, h].abs()).max()
             if sink is not None:
                 lg = torch.cat([lg, sink[h:h + 1].to(torch.float64)])
             if not lg.numel():
