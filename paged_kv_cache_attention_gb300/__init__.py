@@ -32,6 +32,7 @@ of FlashInfer's sink_attention_reference.py, ALiBi slopes, head sizes 64, 80,
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -616,69 +617,147 @@ def paged_decode_noalloc(q, k_cache, v_cache, block_table, cache_seqlens, max_se
 
 
 # ---------------------------------------------------------------------------
-# the 8-bit cache
+# the 8-bit cache, the q/k norm and the attention of drafted tokens.  These
+# calls are short on the GPU in a decode step, so their checks are written to
+# cost little: one test per tensor, the reason worked out only on failure.
 # ---------------------------------------------------------------------------
 
-def _cache_desc_fp8(k_cache, v_cache, k_scale, v_scale, layout: str) -> CacheDesc:
+def _cuda_index(name, t) -> int:
+    """The index of the CUDA device ``t`` lives on."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _arg(name, t, dtype, ndim: int, dev: int):
+    """A contiguous tensor of ``dtype`` with ``ndim`` dims on device ``dev``."""
+    if (t.dtype is dtype and t.dim() == ndim and t.get_device() == dev and t.is_contiguous()):
+        return
+    if t.get_device() < 0 <= dev:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    _require(t.get_device() == dev, f"{name} must be on the same device as the other tensors")
+    _require(t.dtype is dtype, f"{name} must be {dtype}, got {t.dtype}")
+    _require(t.dim() == ndim, f"{name} must have {ndim} dims, got {t.dim()}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _arg_shape(name, t, dtype, shape, dev: int):
+    _arg(name, t, dtype, len(shape), dev)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _error_word(dev_error, dev: int):
+    """The address of the caller's error word, or None."""
+    if dev_error is None:
+        return None
+    _arg("dev_error", dev_error, _torch().int32, 1, dev)
+    _require(dev_error.shape[0] >= 1, "dev_error must have one element")
+    return dev_error.data_ptr()
+
+
+_descs = {}
+
+
+def _desc(*fields) -> CacheDesc:
+    """The CacheDesc of a shape (kept: building one costs as much as a check)."""
+    d = _descs.get(fields)
+    if d is None:
+        if len(_descs) > 4096:
+            _descs.clear()
+        d = _descs[fields] = CacheDesc(*fields)
+    return d
+
+
+def _pools(k_cache, v_cache, k_scale, v_scale, dtype, layout: str, dev: int) -> CacheDesc:
+    """Checks two pools: of ``dtype`` without scales, else of the 8-bit cache."""
     torch = _torch()
-    _cuda_contig("k_cache", k_cache, torch.float8_e4m3fn, 4)
-    _cuda_contig("v_cache", v_cache, torch.float8_e4m3fn, 4)
-    _require(k_cache.shape == v_cache.shape, "k_cache and v_cache must have the same shape")
-    nb, bs, hkv, d = _pool_dims(k_cache, layout)
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _require(t is not None, f"{name} is needed for an 8-bit cache")
-        _cuda_contig(name, t, torch.uint8, 3)
-        _require(tuple(t.shape) == (nb, hkv, bs),
-                 f"{name} must be [num_blocks, num_kv_heads, block_size]")
-    return CacheDesc(nb, bs, hkv, d, PKV_E4M3, LAYOUTS[layout])
+    fp8 = k_scale is not None or v_scale is not None
+    dt = torch.float8_e4m3fn if fp8 else dtype
+    _arg("k_cache", k_cache, dt, 4, dev)
+    _arg("v_cache", v_cache, dt, 4, dev)
+    shape = k_cache.shape
+    if v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    if layout not in LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(LAYOUTS)}")
+    nb, bs, hkv, d = shape
+    if layout == "HND":
+        bs, hkv = hkv, bs
+    if not fp8:
+        return _desc(nb, bs, hkv, d, _dtype_code(dt), LAYOUTS[layout])
+    want = (nb, hkv, bs)
+    for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if s is None:
+            raise ValueError(f"{name} is needed for an 8-bit cache")
+        _arg(name, s, torch.uint8, 3, dev)
+        if s.shape != want:
+            raise ValueError(f"{name} must be [num_blocks, num_kv_heads, block_size]")
+    return _desc(nb, bs, hkv, d, PKV_E4M3, LAYOUTS[layout])
 
 
-def _token_rows(name, t, dtype, heads: int, head_dim: int) -> int:
-    """Checks [T, heads, head_dim] rows whose heads are contiguous; returns the
-    elements between tokens (a slice of a fused projection keeps its own)."""
-    _require(t.dim() == 3 and t.shape[1] == heads and t.shape[2] == head_dim,
-             f"{name} must be [T, {heads}, {head_dim}], got {list(t.shape)}")
-    if t.is_contiguous():
-        _cuda_contig(name, t, dtype)
+def _token_rows(name, t, dtype, tokens: int, heads: int, head_dim: int, dev: int) -> int:
+    """Checks [tokens, heads, head_dim] rows whose heads are contiguous; returns
+    the elements between tokens (a slice of a fused projection keeps its own)."""
+    if t.dtype is not dtype or t.get_device() != dev or tuple(t.shape) != (tokens, heads,
+                                                                            head_dim):
+        _arg(name, t.new_empty(t.shape), dtype, 3, dev)
+        raise ValueError(f"{name} must be [{tokens}, {heads}, {head_dim}], got {list(t.shape)}")
+    if tokens <= 1 or t.is_contiguous():
+        _require(t.is_contiguous(), f"{name}: the heads of a token must be contiguous")
         return heads * head_dim
-    _cuda_contig(name, t[:1], dtype)
+    _require(t[0].is_contiguous(), f"{name}: the heads of a token must be contiguous")
     return t.stride(0)
 
 
-def _same_device(first, *others):
-    for t in others:
-        _require(t is None or t.device == first.device,
-                 f"all tensors must be on one device: {t.device if t is not None else None} "
-                 f"and {first.device}")
-
-
-def _check_error_word(dev_error):
-    if dev_error is not None:
-        _cuda_contig("dev_error", dev_error, _torch().int32, 1)
-        _require(dev_error.numel() >= 1, "dev_error must have one element")
-
-
 class _launch_on:
-    """The device of ``t`` made current, and with a ``stream`` that stream, so
-    that what the call allocates belongs to the stream its kernels run on."""
+    """The device ``dev`` made current, and with a ``stream`` that stream, so
+    that what a call allocates belongs to the stream its kernels run on.  The
+    value of the context is the stream's handle."""
 
-    def __init__(self, t, stream):
-        self.t, self.stream, self.ctx = t, stream, None
+    def __init__(self, dev: int, stream):
+        self.dev, self.stream, self.ctx = dev, stream, None
 
-    def __enter__(self):
-        if not self.t.is_cuda:
-            return
+    def __enter__(self) -> int:
         torch = _torch()
+        if self.dev < 0:
+            return _stream_handle(self.stream)
         if self.stream is not None:
             self.ctx = torch.cuda.stream(self.stream)
-        elif self.t.device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(self.t.device)
-        if self.ctx is not None:
-            self.ctx.__enter__()
+        elif self.dev != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(self.dev)
+        else:
+            return torch.cuda.current_stream(self.dev).cuda_stream
+        self.ctx.__enter__()
+        return torch.cuda.current_stream(self.dev).cuda_stream
 
     def __exit__(self, *exc):
         if self.ctx is not None:
             self.ctx.__exit__(*exc)
+
+
+def _scratch(nbytes: int, dev: int, device, workspace):
+    """(address, bytes) of the workspace, and the tensor that holds it."""
+    torch = _torch()
+    if workspace is None:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return ws.data_ptr(), nbytes, ws
+    size = workspace.numel() * workspace.element_size()
+    if workspace.get_device() != dev or not workspace.is_contiguous() or size < nbytes:
+        raise ValueError(f"workspace must be {nbytes} contiguous bytes on the tensors' device")
+    return workspace.data_ptr(), size, workspace
+
+
+@functools.lru_cache(maxsize=1024)
+def _decode_ws(batch, Hq, D, max_seqlen, partition, window) -> int:
+    return paged_decode_workspace_size(batch, Hq, D, max_seqlen, partition, window)
+
+
+@functools.lru_cache(maxsize=1024)
+def _tree_ws(batch, Hq, Hkv, D, total_q, max_q, max_seqlen, partition, window) -> int:
+    return paged_tree_attention_workspace_size(batch, Hq, Hkv, D, total_q, max_q, max_seqlen,
+                                               partition, window)
 
 
 def reshape_and_cache_fp8(key, value, k_cache, v_cache, k_scale, v_scale, slot_mapping,
@@ -692,20 +771,20 @@ def reshape_and_cache_fp8(key, value, k_cache, v_cache, k_scale, v_scale, slot_m
     stored as byte 255 and reads as NaN.  slot_mapping: [T] int64, negative =
     skip; dev_error receives PKV_DEVERR_SLOT for slots outside the pool."""
     torch = _torch()
-    desc = _cache_desc_fp8(k_cache, v_cache, k_scale, v_scale, layout)
+    dev = _cuda_index("key", key)
+    _require(k_scale is not None, "k_scale is needed for an 8-bit cache")
+    desc = _pools(k_cache, v_cache, k_scale, v_scale, None, layout, dev)
     dt = _dtype_code(key.dtype)
-    ks = _token_rows("key", key, key.dtype, desc.num_kv_heads, desc.head_dim)
-    vs = _token_rows("value", value, key.dtype, desc.num_kv_heads, desc.head_dim)
-    _cuda_contig("slot_mapping", slot_mapping, torch.int64, 1)
-    _require(key.shape[0] == value.shape[0] == slot_mapping.shape[0],
-             "key, value and slot_mapping must have T entries")
-    _check_error_word(dev_error)
-    _same_device(key, value, k_cache, v_cache, k_scale, v_scale, slot_mapping, dev_error)
-    with _launch_on(key, stream):
-        st = load_library().pkv_reshape_and_cache_fp8(
-            _ptr(key), _ptr(value), ks, vs, dt, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-            _ptr(v_scale), _ptr(slot_mapping), key.shape[0], desc, _ptr(dev_error),
-            _stream_handle(stream))
+    T = key.shape[0]
+    ks = _token_rows("key", key, key.dtype, T, desc.num_kv_heads, desc.head_dim, dev)
+    vs = _token_rows("value", value, key.dtype, T, desc.num_kv_heads, desc.head_dim, dev)
+    _arg_shape("slot_mapping", slot_mapping, torch.int64, (T,), dev)
+    err = _error_word(dev_error, dev)
+    lib = load_library()
+    with _launch_on(dev, stream) as handle:
+        st = lib.pkv_reshape_and_cache_fp8(
+            key.data_ptr(), value.data_ptr(), ks, vs, dt, k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), slot_mapping.data_ptr(), T, desc, err, handle)
     _check("pkv_reshape_and_cache_fp8", st)
 
 
@@ -719,73 +798,84 @@ def gather_cache_fp8(k_cache, v_cache, k_scale, v_scale, block_table, cu_seq_len
     outputs.  Rows of no request are left as they were (uninitialised in
     outputs allocated here)."""
     torch = _torch()
-    desc = _cache_desc_fp8(k_cache, v_cache, k_scale, v_scale, layout)
-    _cuda_contig("block_table", block_table, torch.int32, 2)
-    _cuda_contig("cu_seq_lens_k", cu_seq_lens_k, torch.int32, 1)
+    dev = _cuda_index("k_cache", k_cache)
+    _require(k_scale is not None, "k_scale is needed for an 8-bit cache")
+    desc = _pools(k_cache, v_cache, k_scale, v_scale, None, layout, dev)
+    _arg("cu_seq_lens_k", cu_seq_lens_k, torch.int32, 1, dev)
+    _arg("block_table", block_table, torch.int32, 2, dev)
     B = cu_seq_lens_k.shape[0] - 1
     _require(B >= 0 and block_table.shape[0] == B, "block_table must have one row per request")
+    total_k = int(total_k)
     _require(total_k >= 0, "total_k must not be negative")
-    shape = (int(total_k), desc.num_kv_heads, desc.head_dim)
+    shape = (total_k, desc.num_kv_heads, desc.head_dim)
     for name, t in (("key", key), ("value", value)):
         if t is not None:
-            _cuda_contig(name, t, torch.bfloat16, 3)
-            _require(tuple(t.shape) == shape, f"{name} must be [total_k, Hkv, D]")
-    _check_error_word(dev_error)
-    _same_device(k_cache, v_cache, k_scale, v_scale, block_table, cu_seq_lens_k, key, value,
-                 dev_error)
-    with _launch_on(k_cache, stream):
+            _arg_shape(name, t, torch.bfloat16, shape, dev)
+    err = _error_word(dev_error, dev)
+    lib = load_library()
+    with _launch_on(dev, stream) as handle:
         if key is None:
             key = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
         if value is None:
             value = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
-        st = load_library().pkv_gather_cache_fp8(
-            _ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-            desc, _ptr(block_table), block_table.shape[1], _ptr(cu_seq_lens_k), B, int(total_k),
-            _ptr(dev_error), _stream_handle(stream))
+        st = lib.pkv_gather_cache_fp8(
+            key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), desc, block_table.data_ptr(),
+            block_table.shape[1], cu_seq_lens_k.data_ptr(), B, total_k, err, handle)
     _check("pkv_gather_cache_fp8", st)
     return key, value
 
 
+def _attention_extras(sink, alibi_slopes, out, lse, q, dev: int):
+    """Checks what both attention calls take beside q and the pools."""
+    f32 = _torch().float32
+    rows, Hq = q.shape[0], q.shape[1]
+    if sink is not None:
+        _arg_shape("sink", sink, f32, (Hq,), dev)
+    if alibi_slopes is not None:
+        _arg_shape("alibi_slopes", alibi_slopes, f32, (Hq,), dev)
+    if out is not None:
+        _arg_shape("out", out, q.dtype, tuple(q.shape), dev)
+    if lse is not None:
+        _arg_shape("lse", lse, f32, (rows, Hq), dev)
+
+
 def paged_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_seqlens,
                      max_seqlen: int, sink=None, window_left: int = -1,
-                     sm_scale: Optional[float] = None, partition_size: int = 512, out=None,
+                     sm_scale: Optional[float] = None, partition_size: int = 0, out=None,
                      lse=None, workspace=None, dev_error=None, stream=None, alibi_slopes=None,
                      layout: str = "NHD"):
     """paged_decode over the 8-bit cache of reshape_and_cache_fp8: q and out are
     bf16 [B, Hq, D]; everything else as paged_decode (workspace of
-    paged_decode_workspace_size bytes)."""
+    paged_decode_workspace_size bytes for the same arguments), but for
+    partition_size 0, which lets the library choose (512 or more)."""
     torch = _torch()
-    desc = _cache_desc_fp8(k_cache, v_cache, k_scale, v_scale, layout)
-    _cuda_contig("q", q, torch.bfloat16, 3)
-    _cuda_contig("block_table", block_table, torch.int32, 2)
-    _cuda_contig("cache_seqlens", cache_seqlens, torch.int32, 1)
+    dev = _cuda_index("q", q)
+    _require(k_scale is not None, "k_scale is needed for an 8-bit cache")
+    desc = _pools(k_cache, v_cache, k_scale, v_scale, None, layout, dev)
+    _arg("q", q, torch.bfloat16, 3, dev)
     B, Hq, D = q.shape
     _require(D == desc.head_dim, "head_dim of q and cache differ")
+    _arg("block_table", block_table, torch.int32, 2, dev)
+    _arg("cache_seqlens", cache_seqlens, torch.int32, 1, dev)
     _require(block_table.shape[0] == B and cache_seqlens.shape[0] == B,
              "block_table / cache_seqlens batch mismatch")
-    _head_vector("sink", sink, Hq)
-    _head_vector("alibi_slopes", alibi_slopes, Hq)
-    if out is not None:
-        _cuda_contig("out", out, q.dtype, 3)
-        _require(out.shape == q.shape, "out must be shaped like q")
-    if lse is not None:
-        _cuda_contig("lse", lse, torch.float32, 2)
-        _require(tuple(lse.shape) == (B, Hq), "lse must be [B, Hq]")
-    _check_error_word(dev_error)
-    _same_device(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_seqlens, sink,
-                 alibi_slopes, out, lse, workspace, dev_error)
+    _attention_extras(sink, alibi_slopes, out, lse, q, dev)
+    err = _error_word(dev_error, dev)
     scale = float(sm_scale) if sm_scale is not None else D ** -0.5
-    need = paged_decode_workspace_size(B, Hq, D, max_seqlen, partition_size, window_left)
-    with _launch_on(q, stream):
+    max_seqlen, window_left, partition_size = int(max_seqlen), int(window_left), int(partition_size)
+    need = _decode_ws(B, Hq, D, max_seqlen, partition_size, window_left)
+    lib = load_library()
+    with _launch_on(dev, stream) as handle:
         if out is None:
             out = torch.empty_like(q)
-        ws = _workspace(need, q.device, workspace)
-        st = load_library().pkv_paged_decode_fp8(
-            _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), desc,
-            _ptr(block_table), block_table.shape[1], _ptr(cache_seqlens), int(max_seqlen),
-            _ptr(sink), _ptr(alibi_slopes), B, Hq, int(window_left), scale, int(partition_size),
-            _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _ptr(dev_error),
-            _stream_handle(stream))
+        ws, ws_bytes, held = _scratch(need, dev, q.device, workspace)
+        st = lib.pkv_paged_decode_fp8(
+            out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), desc, block_table.data_ptr(),
+            block_table.shape[1], cache_seqlens.data_ptr(), max_seqlen, _ptr(sink),
+            _ptr(alibi_slopes), B, Hq, window_left, scale, partition_size, _ptr(lse), ws,
+            ws_bytes, err, handle)
     _check("pkv_paged_decode_fp8", st)
     return out
 
@@ -806,62 +896,53 @@ def qk_norm_rope_reshape_and_cache(query, key, value, k_cache, v_cache, position
     v_scale the pools are the 8-bit cache of reshape_and_cache_fp8, else pools of
     the rows' dtype.  query (with query_out and q_weight) may be None."""
     torch = _torch()
-    dt = _dtype_code(key.dtype)
-    if k_scale is not None or v_scale is not None:
-        desc = _cache_desc_fp8(k_cache, v_cache, k_scale, v_scale, layout)
-    else:
-        desc = _cache_desc(k_cache, v_cache, layout)
-        _require(k_cache.dtype == key.dtype, "the pools must have the dtype of key")
-    D = desc.head_dim
-    ks = _token_rows("key", key, key.dtype, desc.num_kv_heads, D)
-    vs = _token_rows("value", value, key.dtype, desc.num_kv_heads, D)
-    T, Hq, qs, qos = key.shape[0], 0, 0, 0
-    _require(value.shape[0] == T, "key and value must have the same tokens")
+    dev = _cuda_index("key", key)
+    dtype = key.dtype
+    dt = _dtype_code(dtype)
+    desc = _pools(k_cache, v_cache, k_scale, v_scale, dtype, layout, dev)
+    D, Hkv, T = desc.head_dim, desc.num_kv_heads, key.shape[0]
+    ks = _token_rows("key", key, dtype, T, Hkv, D, dev)
+    vs = _token_rows("value", value, dtype, T, Hkv, D, dev)
+    kos = ks
     if key_out is None:
         key_out = key
-    kos = _token_rows("key_out", key_out, key.dtype, desc.num_kv_heads, D)
-    _require(key_out.shape[0] == T, "key_out must be shaped like key")
-    if query is not None:
+    else:
+        kos = _token_rows("key_out", key_out, dtype, T, Hkv, D, dev)
+    Hq, qs, qos = 0, 0, 0
+    if query is None:
+        query_out = q_weight = None
+    else:
+        _require(query.dim() == 3, "query must be [T, num_qo_heads, head_dim]")
+        Hq = query.shape[1]
+        qs = qos = _token_rows("query", query, dtype, T, Hq, D, dev)
         if query_out is None:
             query_out = query
-        Hq = query.shape[1] if query.dim() == 3 else 0
-        qs = _token_rows("query", query, key.dtype, Hq, D)
-        qos = _token_rows("query_out", query_out, key.dtype, Hq, D)
-        _require(query.shape[0] == T and query_out.shape[0] == T,
-                 "query must be [T, num_qo_heads, head_dim]")
-    else:
-        query_out = q_weight = None
-    _cuda_contig("positions", positions, torch.int64, 1)
-    _cuda_contig("slot_mapping", slot_mapping, torch.int64, 1)
-    _cuda_contig("cos_sin", cos_sin, torch.float32, 3)
-    _require(positions.shape[0] == T and slot_mapping.shape[0] == T,
-             "positions and slot_mapping must have T entries")
+        else:
+            qos = _token_rows("query_out", query_out, dtype, T, Hq, D, dev)
+    _arg_shape("positions", positions, torch.int64, (T,), dev)
+    _arg_shape("slot_mapping", slot_mapping, torch.int64, (T,), dev)
+    _arg("cos_sin", cos_sin, torch.float32, 3, dev)
     rd = int(rotary_dim) if rotary_dim is not None else 2 * cos_sin.shape[1]
     _require(cos_sin.shape[1] * 2 == rd and cos_sin.shape[2] == 2,
              "cos_sin must be [max_position, rotary_dim // 2, 2]")
-    w32 = k_weight.dtype == torch.float32
-    for name, w in (("k_weight", k_weight), ("q_weight", q_weight)):
-        if w is None:
-            _require(name == "q_weight" and query is None, f"{name} is needed")
-            continue
-        _cuda_contig(name, w, torch.float32 if w32 else key.dtype, 1)
-        _require(w.shape[0] == D, f"{name} must have head_dim entries")
-    _check_error_word(dev_error)
-    _same_device(key, value, k_cache, v_cache, positions, slot_mapping, cos_sin, k_weight,
-                 q_weight, query, query_out, key_out, k_scale, v_scale, dev_error)
-    with _launch_on(key, stream):
-        st = load_library().pkv_qk_norm_rope_reshape_and_cache(
-            _ptr(query), _ptr(key), _ptr(value), qs, ks, vs, dt, _ptr(query_out), _ptr(key_out),
-            qos, kos, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-            _ptr(positions), _ptr(slot_mapping), T, Hq, desc, _ptr(q_weight), _ptr(k_weight),
-            int(w32), float(eps), _ptr(cos_sin), cos_sin.shape[0], rd, int(bool(is_neox_style)),
-            _ptr(dev_error), _stream_handle(stream))
+    _require(k_weight is not None and (q_weight is not None or query is None),
+             "q_weight and k_weight are needed")
+    w32 = k_weight.dtype is torch.float32
+    wd = torch.float32 if w32 else dtype
+    _arg_shape("k_weight", k_weight, wd, (D,), dev)
+    if q_weight is not None:
+        _arg_shape("q_weight", q_weight, wd, (D,), dev)
+    err = _error_word(dev_error, dev)
+    lib = load_library()
+    with _launch_on(dev, stream) as handle:
+        st = lib.pkv_qk_norm_rope_reshape_and_cache(
+            _ptr(query), key.data_ptr(), value.data_ptr(), qs, ks, vs, dt, _ptr(query_out),
+            key_out.data_ptr(), qos, kos, k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale),
+            _ptr(v_scale), positions.data_ptr(), slot_mapping.data_ptr(), T, Hq, desc,
+            _ptr(q_weight), k_weight.data_ptr(), w32, float(eps), cos_sin.data_ptr(),
+            cos_sin.shape[0], rd, bool(is_neox_style), err, handle)
     _check("pkv_qk_norm_rope_reshape_and_cache", st)
 
-
-# ---------------------------------------------------------------------------
-# attention of drafted tokens
-# ---------------------------------------------------------------------------
 
 def paged_tree_attention_workspace_size(batch: int, num_qo_heads: int, num_kv_heads: int,
                                         head_dim: int, total_q: int, max_seqlen_q: int,
@@ -893,53 +974,42 @@ def paged_tree_attention(q, k_cache, v_cache, block_table, cu_seq_lens_q, cache_
     host ints; partition_size: split-KV partition (a multiple of 128; 0: chosen).
     sink, lse ([total_q, Hq] float32), window, layout as paged_decode."""
     torch = _torch()
-    if k_scale is not None or v_scale is not None:
-        desc = _cache_desc_fp8(k_cache, v_cache, k_scale, v_scale, layout)
-    else:
-        desc = _cache_desc(k_cache, v_cache, layout)
-    _cuda_contig("q", q, torch.bfloat16, 3)
-    _cuda_contig("block_table", block_table, torch.int32, 2)
-    _cuda_contig("cu_seq_lens_q", cu_seq_lens_q, torch.int32, 1)
-    _cuda_contig("cache_seqlens", cache_seqlens, torch.int32, 1)
-    _cuda_contig("tree_mask", tree_mask, torch.int64, 2)
+    dev = _cuda_index("q", q)
+    desc = _pools(k_cache, v_cache, k_scale, v_scale, torch.bfloat16, layout, dev)
+    _arg("q", q, torch.bfloat16, 3, dev)
     total_q, Hq, D = q.shape
-    B = cache_seqlens.shape[0]
     _require(D == desc.head_dim, "head_dim of q and cache differ")
-    _require(cu_seq_lens_q.shape[0] == B + 1, "cu_seq_lens_q must have B + 1 entries")
+    _arg("block_table", block_table, torch.int32, 2, dev)
+    _arg("cache_seqlens", cache_seqlens, torch.int32, 1, dev)
+    B = cache_seqlens.shape[0]
+    _arg_shape("cu_seq_lens_q", cu_seq_lens_q, torch.int32, (B + 1,), dev)
     _require(block_table.shape[0] == B, "block_table must have one row per request")
-    _require(tree_mask.shape[0] == total_q and 64 * tree_mask.shape[1] >= max_seqlen_q,
+    _arg("tree_mask", tree_mask, torch.int64, 2, dev)
+    words = tree_mask.shape[1]
+    max_seqlen_q, max_seqlen = int(max_seqlen_q), int(max_seqlen)
+    window_left, partition_size = int(window_left), int(partition_size)
+    _require(tree_mask.shape[0] == total_q and 64 * words >= max_seqlen_q,
              "tree_mask must be [total_q, words] with words * 64 >= max_seqlen_q")
     if tree_depth is not None:
-        _cuda_contig("tree_depth", tree_depth, torch.int32, 1)
-        _require(tree_depth.shape[0] == total_q, "tree_depth must have total_q entries")
-    _require(tree_depth is not None or (window_left < 0 and alibi_slopes is None),
-             "tree_depth is needed with a window or ALiBi slopes")
-    _head_vector("sink", sink, Hq)
-    _head_vector("alibi_slopes", alibi_slopes, Hq)
-    if out is not None:
-        _cuda_contig("out", out, q.dtype, 3)
-        _require(out.shape == q.shape, "out must be shaped like q")
-    if lse is not None:
-        _cuda_contig("lse", lse, torch.float32, 2)
-        _require(tuple(lse.shape) == (total_q, Hq), "lse must be [total_q, Hq]")
-    _check_error_word(dev_error)
-    _same_device(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_seq_lens_q,
-                 cache_seqlens, tree_mask, tree_depth, sink, alibi_slopes, out, lse, workspace,
-                 dev_error)
+        _arg_shape("tree_depth", tree_depth, torch.int32, (total_q,), dev)
+    elif window_left >= 0 or alibi_slopes is not None:
+        raise ValueError("tree_depth is needed with a window or ALiBi slopes")
+    _attention_extras(sink, alibi_slopes, out, lse, q, dev)
+    err = _error_word(dev_error, dev)
     scale = float(sm_scale) if sm_scale is not None else D ** -0.5
-    need = paged_tree_attention_workspace_size(B, Hq, desc.num_kv_heads, D, total_q,
-                                               max_seqlen_q, max_seqlen, partition_size,
-                                               window_left)
-    with _launch_on(q, stream):
+    need = _tree_ws(B, Hq, desc.num_kv_heads, D, total_q, max_seqlen_q, max_seqlen,
+                    partition_size, window_left)
+    lib = load_library()
+    with _launch_on(dev, stream) as handle:
         if out is None:
             out = torch.empty_like(q)
-        ws = _workspace(need, q.device, workspace)
-        st = load_library().pkv_paged_tree_attention(
-            _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), desc,
-            _ptr(block_table), block_table.shape[1], _ptr(cu_seq_lens_q), _ptr(cache_seqlens),
-            int(max_seqlen_q), int(max_seqlen), total_q, _ptr(tree_mask), tree_mask.shape[1],
-            _ptr(tree_depth), _ptr(sink), _ptr(alibi_slopes), B, Hq, int(window_left), scale,
-            int(partition_size), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(),
-            _ptr(dev_error), _stream_handle(stream))
+        ws, ws_bytes, held = _scratch(need, dev, q.device, workspace)
+        st = lib.pkv_paged_tree_attention(
+            out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale),
+            _ptr(v_scale), desc, block_table.data_ptr(), block_table.shape[1],
+            cu_seq_lens_q.data_ptr(), cache_seqlens.data_ptr(), max_seqlen_q, max_seqlen,
+            total_q, tree_mask.data_ptr(), words, _ptr(tree_depth), _ptr(sink),
+            _ptr(alibi_slopes), B, Hq, window_left, scale, partition_size, _ptr(lse), ws,
+            ws_bytes, err, handle)
     _check("pkv_paged_tree_attention", st)
     return out

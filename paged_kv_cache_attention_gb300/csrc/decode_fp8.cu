@@ -5,29 +5,32 @@
 //   s_j = sm_scale * 2^ek_j * <q, kc_j> + bias,   o = sum_j p_j 2^ev_j vc_j / l.
 //
 // HBM bound: 2*(D + 1) bytes per key and kv head, half of the bf16 cache.
-// At 6.8 TB/s an SM receives 23 codes per clock, so turning codes into tensor-
-// core operands must cost little: each 32-bit word of four codes becomes two
-// f16 pairs of code * 2^-8 in seven integer instructions, and neither scale
-// touches the codes:
-//   * K: the byte multiplies the fp32 score of its key;
+// At 6.8 TB/s an SM receives 23 codes per clock, so the instructions spent on a
+// code decide whether the kernel keeps up.  A 32-bit word of four codes becomes
+// two f16 pairs in two conversions (three with V's byte shuffle), both scales
+// stay out of the codes, and the softmax's bookkeeping is skipped while no
+// row's maximum grows:
+//   * K: the byte, as 2^ek, multiplies the fp32 score of its key;
 //   * V: the byte multiplies p_j before p rounds to f16.  Weights are kept
 //     relative to the largest byte E seen so far by the warp, p_j *
-//     2^(ev_j - E + 14) <= 2^14: f16 keeps 11 bits of every weight down to
-//     2^-28 of the largest; the accumulators move by 2^(E_old - E_new) together
-//     with the softmax's own rescale.
+//     2^(ev_j - E + 10); with p <= 2^4 (below) that is at most 2^14, and f16
+//     keeps 11 bits of every weight down to 2^-24 of 2^ev_max.  The
+//     accumulators move by 2^(E_old - E_new) with the softmax's own rescale;
+//   * a row's maximum reference moves only when a score exceeds it by 2^4.
 // q is scaled per head by a power of two to at most 2^15 and held in f16,
 // which is exact for every bf16 value within 2^-28 of the row's largest (and
 // off by less than 2^-39 of the largest below that).
 //
 // The mma fragments follow the bytes: a 32-bit word of an ldmatrix row holds
-// four consecutive dims of a key, split into (0, 2) and (1, 3), so a k-step of
-// Q K^T takes 16 dims in that order (q's fragment is loaded to match); a
-// transposed ldmatrix word holds two consecutive dims of two consecutive keys,
-// whose split is one even-dim and one odd-dim fragment of O^T += V^T P^T.
+// four consecutive dims of a key, two pairs, so a k-step of Q K^T takes 16 dims
+// in that order (q's fragment is loaded to match); a transposed ldmatrix word
+// holds two consecutive dims of two consecutive keys: one byte shuffle and it is
+// one even-dim and one odd-dim fragment of O^T += V^T P^T.
 //
-// CTAs of two warps, each streaming every other 32-token stage of the
-// partition through its own ring of NST stages: K and V by TMA (one box per
-// page), the scale bytes by 16-byte cp.async on the same barrier.
+// CTAs of two warps, each streaming every other stage of the partition (32
+// tokens, 64 of a 64-dim head) through its own ring of two stages: K and V by
+// TMA (one box per page and 128 dims), the scale bytes by 16-byte cp.async on
+// the same barrier.
 #include "pkv_fp8.cuh"
 
 namespace pkv {
@@ -36,8 +39,9 @@ namespace {
 
 constexpr int kWarps = 2;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTok = 32;  // tokens per stage
 constexpr int kMaxGroup = 16;
+constexpr int kWeightExp = 10;   // weights are at most 2^kWeightExp * 2^kLazy
+constexpr float kLazy = 4.f;     // log2 units a score may exceed its row's reference
 constexpr float kNegInf = -INFINITY;
 
 __device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
@@ -65,23 +69,41 @@ __device__ __forceinline__ uint32_t swz(uint32_t r, uint32_t c) {
     return W == 128 ? sw128(r, c) : r * 64u + ((c ^ ((r >> 1) & 3u)) << 4);
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Normalise and store one row slice: the output itself when there is one
+// partition, else the partition's partial.
+__device__ __forceinline__ void store_row4(const DecodeParams &p, int64_t unit, int hq, int d,
+                                           float4 o, float M, float l, bool first) {
+    if (p.num_parts > 1) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays
+        const int64_t idx = unit * p.num_parts + blockIdx.y;
+        *reinterpret_cast<float4 *>(p.part_o + idx * p.head_dim + d) =
+            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (first) p.part_lse[idx] = l == 0.f ? kNegInf : M + log2f(l);
+        return;
+    }
+    const float sink = p.sink ? p.sink[hq] * kLog2e : kNegInf;
+    const float T = fmaxf(M, sink), Ts = T == kNegInf ? 0.f : T;
+    const float f = exp2f(M - Ts);
+    const float lam = (l != l ? l : l * f) + exp2f(sink - Ts);
+    const float inv = lam == 0.f ? 0.f : f / lam;
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + unit * p.head_dim + d) =
+        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    if (first && p.lse_out)
+        p.lse_out[unit] = lam == 0.f ? kNegInf : (Ts + log2f(lam)) * kLn2;
 }
 
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-template <int D, int NST>
+template <int D>
 struct Shape {
+    static constexpr int TOK = D == 64 ? 64 : 32;            // tokens per stage
+    static constexpr int NST = 2;                            // stages per warp
     static constexpr int ROWB = D < 128 ? D : 128;           // bytes of a box row
     static constexpr int PARTS = D / ROWB;                   // boxes across the head size
-    static constexpr int PART_BYTES = kTok * ROWB;
+    static constexpr int PART_BYTES = TOK * ROWB;
     static constexpr int KV_BYTES = PARTS * PART_BYTES;      // K (or V) of one stage
     static constexpr int RING = kWarps * NST * 2 * KV_BYTES;
-    static constexpr int SCALE_OFF = RING;                   // [warp][stage][K, V][32] bytes
-    static constexpr int BAR_OFF = SCALE_OFF + kWarps * NST * 2 * kTok;
+    static constexpr int SCALE_OFF = RING;                   // [warp][stage][K, V][TOK] bytes
+    static constexpr int FACT_OFF = SCALE_OFF + kWarps * NST * 2 * TOK;  // [warp][K, V][TOK] f32
+    static constexpr int BAR_OFF = FACT_OFF + kWarps * 2 * TOK * 4;
     static constexpr int M_OFF = BAR_OFF + kWarps * NST * 8;
     static constexpr int L_OFF = M_OFF + kWarps * kMaxGroup * 4;
     static constexpr int BLK_OFF = L_OFF + kWarps * kMaxGroup * 4;
@@ -89,13 +111,16 @@ struct Shape {
     static_assert(kWarps * 8 * D * 4 <= RING, "merge scratch must fit in the ring");
 };
 
-template <int D, int BS, int NHT, int NST, bool HND>
+template <int D, int BS, int NHT, bool HND>
 __global__ void __launch_bounds__(kThreads)
 decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmv) {
-    using C = Shape<D, NST>;
-    constexpr int PPS = kTok / BS;  // pages per stage
+    using C = Shape<D>;
+    constexpr int NST = C::NST, TOK = C::TOK;
+    constexpr int PPS = TOK / BS;   // pages per stage
     constexpr int NC = D / 16;      // 16-dim chunks
+    constexpr int NT = TOK / 8;     // 8-token tiles
+    constexpr int NCP = TOK / 16;   // 16-byte pieces of a stage's K (or V) scale bytes
     const DecodeParams &p = pp.d;
 
     extern __shared__ uint8_t smem_raw[];
@@ -108,21 +133,31 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
     pdl_wait();
     const int g = blockIdx.x, b = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = p.group, Dh = p.head_dim;
+    const int64_t unit0 = (int64_t)b * p.num_qo_heads + g * G;
     const int L = clipped_len(p, b, BS, blockIdx.y == 0 && g == 0 && threadIdx.x == 0);
     const int start = first_kept(L, p.window_left);
     const int part = start / p.partition_size + blockIdx.y;
     const int tok_lo = max(part * p.partition_size, start);
     const int tok_hi = min((part + 1) * p.partition_size, L);
-    if (tok_lo >= tok_hi) return;  // this slot holds no attended key
+    if (tok_lo >= tok_hi) {  // this slot holds no attended key
+        if (p.num_parts == 1)
+            for (int i = threadIdx.x; i < G * (Dh / 4); i += kThreads) {
+                const int h = i / (Dh / 4), d = (i - h * (Dh / 4)) * 4;
+                store_row4(p, unit0 + h, g * G + h, d, make_float4(0.f, 0.f, 0.f, 0.f), kNegInf,
+                           0.f, d == 0);
+            }
+        return;
+    }
 
-    // stages are 32 tokens at multiples of 32; pages of the range
-    const int st_lo = tok_lo / kTok, nst = (tok_hi - 1) / kTok - st_lo + 1;
+    // stages start at multiples of TOK; pages of the range
+    const int st_lo = tok_lo / TOK, nst = (tok_hi - 1) / TOK - st_lo + 1;
     const int pg_lo = st_lo * PPS, pg_first = tok_lo / BS, pg_last = (tok_hi - 1) / BS;
 
     const uint32_t ring = smem_u32(smem);
     const uint32_t bars = ring + C::BAR_OFF;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kWarps * NST; ++i) mbar_init(bars + 8 * i, 1 + 4);
+        for (int i = 0; i < kWarps * NST; ++i) mbar_init(bars + 8 * i, 1 + 2 * NCP);
         fence_barrier_init();
         tma_prefetch_desc(&tmk);
         tma_prefetch_desc(&tmv);
@@ -145,11 +180,12 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
     const int nmine = nst > warp ? (nst - warp + kWarps - 1) / kWarps : 0;
     const uint32_t wring = ring + warp * NST * 2 * C::KV_BYTES;
     const uint32_t wbars = bars + warp * NST * 8;
-    const uint32_t wscale = ring + C::SCALE_OFF + warp * NST * 2 * kTok;
+    const uint32_t wscale = ring + C::SCALE_OFF + warp * NST * 2 * TOK;
+    float *wfact = reinterpret_cast<float *>(smem + C::FACT_OFF) + warp * 2 * TOK;
     const uint64_t policy = l2_policy_evict_first();
 
-    // Stage j of this warp: lane 0 asks TMA for the boxes, lanes 0..3 copy the
-    // scale bytes (16 K and 16 V bytes for each half of the stage).
+    // Stage j of this warp: lane 0 asks TMA for the boxes, the first lanes copy
+    // the scale bytes, 16 K or V bytes each.
     auto issue = [&](int j) {
         const int s = j % NST;
         const uint32_t bar = wbars + 8 * s;
@@ -174,24 +210,21 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
                 }
             }
         }
-        if (lane < 4) {
-            const int half = lane & 1, q = BS == 16 ? half : 0;
-            if (blk[q] >= 0) {
-                const uint8_t *src = lane < 2 ? pp.k_scale : pp.v_scale;
-                const int64_t at = ((int64_t)blk[q] * p.num_kv_heads + g) * BS +
-                                   (BS == 32 ? half * 16 : 0);
-                cp_async16(wscale + s * 2 * kTok + (lane < 2 ? 0 : kTok) + half * 16, src + at);
-            }
+        if (lane < 2 * NCP) {
+            const int isv = lane / NCP, t = (lane % NCP) * 16, id = blk[t / BS];
+            if (id >= 0)
+                cp_async16(wscale + s * 2 * TOK + isv * TOK + t,
+                           (isv ? pp.v_scale : pp.k_scale) +
+                               ((int64_t)id * p.num_kv_heads + g) * BS + t % BS);
             cp_async_arrive(bar);
         }
     };
     for (int j = 0; j < NST && j < nmine; ++j) issue(j);
 
-    // q as the A operand: row = head, 16 dims per k-step in the byte order
+    // q as the A operand: row = head, 16 dims per k-step in the byte order.  A
+    // negative sm_scale goes into q, so that scores grow with the products.
     const int gq = lane >> 2, tq = lane & 3;
-    const int G = p.group, Dh = p.head_dim;
-    const __nv_bfloat16 *qb =
-        static_cast<const __nv_bfloat16 *>(p.q) + ((int64_t)b * p.num_qo_heads + g * G) * Dh;
+    const __nv_bfloat16 *qb = static_cast<const __nv_bfloat16 *>(p.q) + unit0 * Dh;
     uint32_t qa[NHT][NC][2];
     float rowf[NHT];
 #pragma unroll
@@ -213,26 +246,24 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
         amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         // largest magnitude 2^E..2^(E+1): times 2^(14 - E)
         const int E = max((int)(amax >> 7) - 127, -100);
-        const float f = __uint_as_float((uint32_t)(127 + 14 - E) << 23);
-        // score = <q f, code 2^-8> * 2^8 / f * sm_scale
-        rowf[ht] = p.scale_log2 * __uint_as_float((uint32_t)(min(127 + E - 6, 254)) << 23);
+        const uint32_t neg = p.scale_log2 < 0.f ? 0x80000000u : 0u;
+        const float f = __uint_as_float(((uint32_t)(127 + 14 - E) << 23) | neg);
+        rowf[ht] = fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + E - 14) << 23);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const float x0 = __uint_as_float(w[c].x << 16) * f;
-            const float x1 = __uint_as_float(w[c].x & 0xffff0000u) * f;
-            const float x2 = __uint_as_float(w[c].y << 16) * f;
-            const float x3 = __uint_as_float(w[c].y & 0xffff0000u) * f;
-            qa[ht][c][0] = pack_f16(x0, x2);
-            qa[ht][c][1] = pack_f16(x1, x3);
+            qa[ht][c][0] = pack_f16(__uint_as_float(w[c].x << 16) * f,
+                                    __uint_as_float(w[c].x & 0xffff0000u) * f);
+            qa[ht][c][1] = pack_f16(__uint_as_float(w[c].y << 16) * f,
+                                    __uint_as_float(w[c].y & 0xffff0000u) * f);
         }
     }
 
     float oacc[NHT][NC][4];
-    float m_run[NHT], l_run[NHT], al2[NHT];
+    float m_ref[NHT], l_run[NHT], al2[NHT];
     bool head_ok[NHT];
 #pragma unroll
     for (int ht = 0; ht < NHT; ++ht) {
-        m_run[ht] = kNegInf;
+        m_ref[ht] = kNegInf;
         l_run[ht] = 0.f;
         head_ok[ht] = ht * 8 + gq < G;
         al2[ht] = (p.alibi && head_ok[ht]) ? p.alibi[g * G + ht * 8 + gq] * kLog2e : 0.f;
@@ -251,23 +282,55 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
         if (!warp_wait_bounded(wbars + 8 * s, (j / NST) & 1, p.dev_error)) break;
         consumed = j + 1;
         const uint32_t kb = wring + s * 2 * C::KV_BYTES, vb = kb + C::KV_BYTES;
-        const uint8_t *sc = smem + C::SCALE_OFF + (warp * NST + s) * 2 * kTok;
-        const int tok0 = (st_lo + i) * kTok;
-        // lane = token of the stage: is it attended, and its V scale
-        const int tok_l = tok0 + lane;
-        const bool ok_l = tok_l >= tok_lo && tok_l < tok_hi && s_blk[i * PPS + lane / BS] >= 0;
-        const uint32_t okm = __ballot_sync(0xffffffffu, ok_l);
-        const int vmax = __reduce_max_sync(0xffffffffu, ok_l ? (int)sc[kTok + lane] : 0);
-        const int gnew = max(gauge, vmax);
-        // 2^(gauge - gnew), zero past the float range
-        const float gcorr = gauge == gnew || gauge - gnew < -126
-                                ? (gauge == gnew ? 1.f : 0.f)
-                                : __uint_as_float((uint32_t)(127 + gauge - gnew) << 23);
-        gauge = gnew;
-
-        float sacc[4][4];
+        const uint8_t *sc = smem + C::SCALE_OFF + (warp * NST + s) * 2 * TOK;
+        const int tok0 = (st_lo + i) * TOK;
+        // lane = token (and token + 32): is it attended, its factors
+        uint32_t okm[TOK / 32];
+        bool full = true;
+        int vmax = 0;
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
+        for (int h = 0; h < TOK / 32; ++h) {
+            const int t = tok0 + h * 32 + lane;
+            const bool ok = t >= tok_lo && t < tok_hi && s_blk[i * PPS + (h * 32 + lane) / BS] >= 0;
+            okm[h] = __ballot_sync(0xffffffffu, ok);
+            full = full && okm[h] == 0xffffffffu;
+            if (ok) vmax = max(vmax, (int)sc[TOK + h * 32 + lane]);
+        }
+        vmax = __reduce_max_sync(0xffffffffu, vmax);
+        const bool regauge = vmax > gauge;
+        float gcorr = 1.f;
+        if (regauge) {
+            gcorr = gauge - vmax < -126 ? 0.f
+                                        : __uint_as_float((uint32_t)(127 + gauge - vmax) << 23);
+            gauge = vmax;
+        }
+#pragma unroll
+        for (int h = 0; h < TOK / 32; ++h) {
+            const int t = h * 32 + lane;
+            const uint32_t kbyte = sc[t], vbyte = sc[TOK + t];
+            const int x = (int)vbyte - gauge + kWeightExp + 127;
+            wfact[t] = scale_value(kbyte);
+            // an unattended row's byte may be anything: its factor is 0
+            wfact[TOK + t] = !((okm[h] >> lane) & 1u) ? 0.f
+                             : vbyte == kScaleNaN     ? __uint_as_float(0x7fffffffu)
+                             : x > 0                  ? __uint_as_float((uint32_t)x << 23)
+                                                      : 0.f;
+        }
+        if (!full) {
+            // unattended V rows may hold any bits: zero them, so that a zero
+            // weight never meets a NaN code
+            for (int e = lane; e < C::PARTS * TOK * (C::ROWB / 16); e += 32) {
+                const int h = e / (TOK * (C::ROWB / 16)), r = (e / (C::ROWB / 16)) % TOK;
+                const int c = e % (C::ROWB / 16);
+                if (!((okm[r / 32] >> (r % 32)) & 1u))
+                    st_shared_zero16(vb + h * C::PART_BYTES + swz<C::ROWB>(r, c));
+            }
+        }
+        __syncwarp();
+
+        float sacc[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) sacc[nt][e] = 0.f;
 #pragma unroll
@@ -278,80 +341,88 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
                 ldsm_x4(kb + (c >> 3) * C::PART_BYTES + swz<C::ROWB>(r, c & 7), w[0], w[1], w[2],
                         w[3]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t b0, b1;
+                    e4m3_to_f16(w[k], b0, b1);
                     mma_f16_16816(sacc[nt], qa[0][c4 * 4 + k][0],
                                   NHT > 1 ? qa[NHT - 1][c4 * 4 + k][0] : 0u,
                                   qa[0][c4 * 4 + k][1],
-                                  NHT > 1 ? qa[NHT - 1][c4 * 4 + k][1] : 0u,
-                                  e4m3_even_f16(w[k]), e4m3_odd_f16(w[k]));
-            }
-        }
-        float kf[4][2], vf[4][2];
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-            const int t = nt * 8 + 2 * tq;
-            const uint32_t k2 = *reinterpret_cast<const uint16_t *>(sc + t);
-            const uint32_t v2 = *reinterpret_cast<const uint16_t *>(sc + kTok + t);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint32_t kbyte = (k2 >> (8 * e)) & 255u;
-                const int vbyte = (int)((v2 >> (8 * e)) & 255u);
-                kf[nt][e] = scale_value(kbyte);
-                const int x = vbyte - gauge + 14 + 127;
-                vf[nt][e] = vbyte == (int)kScaleNaN ? __uint_as_float(0x7fffffffu)
-                            : x > 0                 ? __uint_as_float((uint32_t)x << 23)
-                                                    : 0.f;
+                                  NHT > 1 ? qa[NHT - 1][c4 * 4 + k][1] : 0u, b0, b1);
+                }
             }
         }
         // online softmax (log2 units), one head row per lane quad
+        float ao[NHT];
+        bool moved = regauge;
 #pragma unroll
         for (int ht = 0; ht < NHT; ++ht) {
-            float mx = kNegInf;
+            float mx = kNegInf, rf = rowf[ht];
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+                const float2 kf = *reinterpret_cast<const float2 *>(wfact + nt * 8 + 2 * tq);
+                sacc[nt][2 * ht] *= kf.x;
+                sacc[nt][2 * ht + 1] *= kf.y;
+            }
+            if (!full || p.alibi) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int t = nt * 8 + 2 * tq + e;
-                    const bool ok = head_ok[ht] && ((okm >> t) & 1u);
-                    const float sv = ok ? fmaf(sacc[nt][2 * ht + e] * kf[nt][e], rowf[ht],
-                                               al2[ht] * (float)(tok0 + t - qpos))
-                                        : kNegInf;
-                    sacc[nt][2 * ht + e] = sv;
-                    mx = fmaxf(mx, sv);
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int t = nt * 8 + 2 * tq + e;
+                        const bool ok = (okm[t / 32] >> (t % 32)) & 1u;
+                        sacc[nt][2 * ht + e] =
+                            ok ? fmaf(sacc[nt][2 * ht + e], rf,
+                                      al2[ht] * (float)(tok0 + t - qpos))
+                               : kNegInf;
+                    }
+                rf = 1.f;  // the scores are complete
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                mx = fmax3(mx, sacc[nt][2 * ht], sacc[nt][2 * ht + 1]);
+            mx *= rf;
+            if (!head_ok[ht]) mx = kNegInf;
+            ao[ht] = 1.f;
+            if (__any_sync(0xffffffffu, mx > m_ref[ht] + kLazy)) {
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const float m_new = fmaxf(m_ref[ht], mx);
+                ao[ht] = m_new == kNegInf ? 1.f : fast_exp2(m_ref[ht] - m_new);
+                l_run[ht] *= ao[ht];
+                m_ref[ht] = m_new;
+                moved = true;
+            }
+            const float msub = m_ref[ht] == kNegInf ? 0.f : m_ref[ht];
+            float p0 = 0.f, p1 = 0.f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float2 vf = *reinterpret_cast<const float2 *>(wfact + TOK + nt * 8 + 2 * tq);
+                const float x = fast_exp2(fmaf(sacc[nt][2 * ht], rf, -msub));
+                const float y = fast_exp2(fmaf(sacc[nt][2 * ht + 1], rf, -msub));
+                p0 += x;
+                p1 += y;
+                sacc[nt][2 * ht] = x * vf.x;
+                sacc[nt][2 * ht + 1] = y * vf.y;
+            }
+            l_run[ht] += p0 + p1;
+        }
+        if (moved) {  // O^T columns of this lane are heads ht*8 + 2tq and +1
+#pragma unroll
+            for (int ht = 0; ht < NHT; ++ht) {
+                const float a0 = __shfl_sync(0xffffffffu, ao[ht], 8 * tq) * gcorr;
+                const float a1 = __shfl_sync(0xffffffffu, ao[ht], 8 * tq + 4) * gcorr;
+#pragma unroll
+                for (int mt = 0; mt < NC; ++mt) {
+                    oacc[ht][mt][0] *= a0;
+                    oacc[ht][mt][1] *= a1;
+                    oacc[ht][mt][2] *= a0;
+                    oacc[ht][mt][3] *= a1;
                 }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float m_new = fmaxf(m_run[ht], mx);
-            const float msub = m_new == kNegInf ? 0.f : m_new;
-            const float alpha = fast_exp2(m_run[ht] - msub);
-            float psum = 0.f;
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int t = nt * 8 + 2 * tq + e;
-                    const float pv = fast_exp2(sacc[nt][2 * ht + e] - msub);
-                    psum += pv;
-                    // an unattended row's byte may be anything: its weight is 0
-                    sacc[nt][2 * ht + e] = ((okm >> t) & 1u) ? pv * vf[nt][e] : 0.f;
-                }
-            l_run[ht] = l_run[ht] * alpha + psum;
-            m_run[ht] = m_new;
-            const float ao = alpha * gcorr;
-            const float a0 = __shfl_sync(0xffffffffu, ao, 8 * tq);
-            const float a1 = __shfl_sync(0xffffffffu, ao, 8 * tq + 4);
-#pragma unroll
-            for (int mt = 0; mt < NC; ++mt) {
-                oacc[ht][mt][0] *= a0;
-                oacc[ht][mt][1] *= a1;
-                oacc[ht][mt][2] *= a0;
-                oacc[ht][mt][3] *= a1;
             }
         }
-        // O^T += V^T P^T.  Codes of rows that are not attended are finite
-        // whatever bits they hold, and their weights are zero.
+        // O^T += V^T P^T
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
+        for (int ks = 0; ks < NT / 2; ++ks) {
             uint32_t pb0[NHT], pb1[NHT];
 #pragma unroll
             for (int ht = 0; ht < NHT; ++ht) {
@@ -368,9 +439,9 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
                           w[2], w[3]);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const uint32_t a0 = e4m3_even_f16(w[2 * k]), a1 = e4m3_odd_f16(w[2 * k]);
-                    const uint32_t a2 = e4m3_even_f16(w[2 * k + 1]);
-                    const uint32_t a3 = e4m3_odd_f16(w[2 * k + 1]);
+                    uint32_t a0, a1, a2, a3;  // even dims, odd dims of keys 0-7 and 8-15
+                    e4m3_to_f16(__byte_perm(w[2 * k], 0u, 0x3120), a0, a1);
+                    e4m3_to_f16(__byte_perm(w[2 * k + 1], 0u, 0x3120), a2, a3);
 #pragma unroll
                     for (int ht = 0; ht < NHT; ++ht)
                         mma_f16_16816(oacc[ht][c2 * 2 + k], a0, a1, a2, a3, pb0[ht], pb1[ht]);
@@ -394,12 +465,13 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
         l_run[ht] += __shfl_xor_sync(0xffffffffu, l_run[ht], 1);
         l_run[ht] += __shfl_xor_sync(0xffffffffu, l_run[ht], 2);
         if (tq == 0) {
-            s_m[warp * kMaxGroup + ht * 8 + gq] = m_run[ht];
+            s_m[warp * kMaxGroup + ht * 8 + gq] = m_ref[ht];
             s_l[warp * kMaxGroup + ht * 8 + gq] = l_run[ht];
         }
     }
-    // O in its own units: code * 2^-8, weights * 2^(14 - gauge)
-    const float unit = gauge > 0 ? __uint_as_float((uint32_t)gauge << 23) * 0x1p-6f : 0.f;
+    // O in its own units: the weights carry 2^(kWeightExp - gauge)
+    const float unit =
+        gauge > 0 ? __uint_as_float((uint32_t)gauge << 23) * (1.f / (1 << kWeightExp)) : 0.f;
     float *s_o = reinterpret_cast<float *>(smem);  // [warp][8 heads][D]
 #pragma unroll
     for (int ht = 0; ht < NHT; ++ht) {
@@ -416,23 +488,17 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
         for (int i = threadIdx.x; i < heads * (Dh / 4); i += kThreads) {
             const int h = i / (Dh / 4), d = (i - h * (Dh / 4)) * 4, hh = ht * 8 + h;
             const float m0 = s_m[hh], m1 = s_m[kMaxGroup + hh];
-            const float M = fmaxf(m0, m1);
-            const float f0 = M == kNegInf ? 0.f : exp2f(m0 - M);
-            const float f1 = M == kNegInf ? 0.f : exp2f(m1 - M);
-            const float l = f0 * s_l[hh] + f1 * s_l[kMaxGroup + hh];
-            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays
+            const float M = fmaxf(m0, m1), Ms = M == kNegInf ? 0.f : M;
+            const float f0 = exp2f(m0 - Ms), f1 = exp2f(m1 - Ms);
+            const float l0 = s_l[hh], l1 = s_l[kMaxGroup + hh];
+            // a NaN sum keeps its reference at -inf: do not lose it to f = 0
+            const float l = (l0 != l0 ? l0 : f0 * l0) + (l1 != l1 ? l1 : f1 * l1);
             const float4 a = *reinterpret_cast<const float4 *>(s_o + h * D + d);
             const float4 c = *reinterpret_cast<const float4 *>(s_o + (8 + h) * D + d);
-            // a warp without weight (f = 0) has only zeros: no 0 * NaN
-            const int64_t idx =
-                ((int64_t)b * p.num_qo_heads + g * G + hh) * p.num_parts + blockIdx.y;
-            float4 o;
-            o.x = (a.x * f0 + c.x * f1) * inv;
-            o.y = (a.y * f0 + c.y * f1) * inv;
-            o.z = (a.z * f0 + c.z * f1) * inv;
-            o.w = (a.w * f0 + c.w * f1) * inv;
-            *reinterpret_cast<float4 *>(p.part_o + idx * Dh + d) = o;
-            if (d == 0) p.part_lse[idx] = l == 0.f ? kNegInf : M + log2f(l);
+            store_row4(p, unit0 + hh, g * G + hh, d,
+                       make_float4(a.x * f0 + c.x * f1, a.y * f0 + c.y * f1, a.z * f0 + c.z * f1,
+                                   a.w * f0 + c.w * f1),
+                       M, l, d == 0);
         }
     }
 }
@@ -539,12 +605,11 @@ cudaError_t launch_merge_fp8(const DecodeParams &p, int D, int BS, cudaStream_t 
 template <int D, int BS, int NHT>
 cudaError_t launch_one(const DecodeFp8Params &p, const CUtensorMap *tk, const CUtensorMap *tv,
                        cudaStream_t stream) {
-    constexpr int NST = D == 64 ? 4 : 2;
-    using C = Shape<D, NST>;
-    auto kern = p.d.hnd ? decode_fp8_kernel<D, BS, NHT, NST, true>
-                        : decode_fp8_kernel<D, BS, NHT, NST, false>;
-    // a partition meets at most partition_size / 32 + 1 stages
-    const int smem = C::SMEM_FIXED + (p.d.partition_size / kTok + 1) * (kTok / BS) * 4;
+    using C = Shape<D>;
+    auto kern = p.d.hnd ? decode_fp8_kernel<D, BS, NHT, true>
+                        : decode_fp8_kernel<D, BS, NHT, false>;
+    // a partition meets at most partition_size / TOK + 2 stages
+    const int smem = C::SMEM_FIXED + (p.d.partition_size / C::TOK + 2) * (C::TOK / BS) * 4;
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(p.d.num_kv_heads, p.d.num_parts, p.d.batch), dim3(kThreads),
@@ -574,7 +639,7 @@ cudaError_t launch_decode_fp8(const DecodeFp8Params &p, const pkv_cache_desc &ca
         e = launch_d<128>(p, BS, tmap_k, tmap_v, stream);
     else
         e = launch_d<256>(p, BS, tmap_k, tmap_v, stream);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || p.d.num_parts == 1) return e;
     return launch_merge_fp8(p.d, D, BS, stream);
 }
 

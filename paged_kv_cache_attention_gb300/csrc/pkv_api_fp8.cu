@@ -13,6 +13,8 @@ namespace {
 
 constexpr int kDefaultPartition = 512;
 constexpr int kMaxPartition = 16384;
+constexpr int kMaxAutoPartition = 2048;
+constexpr int kDecodeSlots = 912;  // CTAs of the 8-bit decode that run at once: 6 per SM
 
 bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -53,6 +55,7 @@ PoolArgs pool_args(const pkv_cache_desc &c, const void *k, const void *v, const 
     a.num_kv_heads = c.num_kv_heads;
     a.head_dim = c.head_dim;
     a.block_size = c.block_size;
+    a.bs_shift = c.block_size == 16 ? 4 : 5;
     a.hnd = c.layout == PKV_HND ? 1 : 0;
     return a;
 }
@@ -203,9 +206,15 @@ pkv_status pkv_paged_decode_fp8(void *out, const void *q, const void *k_cache,
     if (num_qo_heads % cache.num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
     const int G = num_qo_heads / cache.num_kv_heads;
     if (G > 16) return PKV_ERR_UNSUPPORTED;
-    const int P = partition_size > 0 ? partition_size : kDefaultPartition;
-    if (partition_size < 0 || P % cache.block_size != 0 || P > kMaxPartition)
-        return PKV_ERR_INVALID_ARG;
+    int P = partition_size;
+    if (P == 0) {
+        // twice the default while that leaves the SMs eight full rounds of CTAs
+        P = kDefaultPartition;
+        while (P < kMaxAutoPartition &&
+               (int64_t)batch * cache.num_kv_heads * (max_seqlen / P) > 8 * kDecodeSlots)
+            P *= 2;
+    }
+    if (P < 0 || P % cache.block_size != 0 || P > kMaxPartition) return PKV_ERR_INVALID_ARG;
     if (batch == 0) return PKV_OK;
     if (!out || !q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table ||
         !cache_seqlens)

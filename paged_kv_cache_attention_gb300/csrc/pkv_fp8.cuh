@@ -52,16 +52,26 @@ __device__ __forceinline__ uint32_t quant4(const float *x, float inv, bool bad) 
     return cvt_e4m3x2(x[0] * inv, x[1] * inv) | (cvt_e4m3x2(x[2] * inv, x[3] * inv) << 16);
 }
 
-// The codes of bytes 0 and 2 (lo) / 1 and 3 (hi) of w as f16 pairs of
-// code * 2^-8: an e4m3 code's exponent and mantissa fields, moved to the top
-// of f16's, are the same number with exponent bias 15 instead of 7,
-// subnormals included.  The NaN codes 0x7f and 0xff, which the library never
-// writes, read as +-480.  Seven integer instructions for four codes.
-__device__ __forceinline__ uint32_t e4m3_even_f16(uint32_t w) {
-    return ((w << 7) & 0x3f803f80u) | ((w << 8) & 0x80008000u);
+// Four e4m3 codes of a word as f16 pairs: bytes 0 and 1 in lo, 2 and 3 in hi
+// (exact; the NaN codes give NaN).
+__device__ __forceinline__ void e4m3_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
 }
-__device__ __forceinline__ uint32_t e4m3_odd_f16(uint32_t w) {
-    return ((w >> 1) & 0x3f803f80u) | (w & 0x80008000u);
+
+// 16-byte asynchronous copies, completing on an mbarrier.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
 }
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1,
@@ -115,18 +125,20 @@ __device__ __forceinline__ void dequant16_bf16(const uint4 &c, uint32_t byte, ui
     }
 }
 
-// Element offset of (slot, kv head g) in a pool, and of its scale byte.
+// Where a slot's rows are in a pool: kv head g's row starts at element row +
+// g * row_step, its E8M0 byte is scale + g * block_size.  slot is in [0,
+// capacity), which is below 2^31.
 struct PoolSlot {
-    int64_t row;    // first element of the head row
-    int64_t scale;  // index of the row's E8M0 byte
+    int64_t row, scale;
+    int row_step;
 };
 
-__device__ __forceinline__ PoolSlot pool_slot(const PoolArgs &p, int64_t slot, int g) {
-    const int64_t blk = slot / p.block_size, off = slot - blk * p.block_size;
-    const int64_t hnd = (blk * p.num_kv_heads + g) * p.block_size + off;
+__device__ __forceinline__ PoolSlot pool_slot(const PoolArgs &p, uint32_t slot) {
+    const uint32_t blk = slot >> p.bs_shift, off = slot & (p.block_size - 1);
     PoolSlot s;
-    s.scale = hnd;
-    s.row = (p.hnd ? hnd : slot * p.num_kv_heads + g) * p.head_dim;
+    s.scale = (int64_t)blk * (p.num_kv_heads * p.block_size) + off;
+    s.row = (p.hnd ? s.scale : (int64_t)slot * p.num_kv_heads) * p.head_dim;
+    s.row_step = p.hnd ? p.block_size * p.head_dim : p.head_dim;
     return s;
 }
 

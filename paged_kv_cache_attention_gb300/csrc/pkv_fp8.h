@@ -14,6 +14,7 @@ struct PoolArgs {
     uint8_t *k_scale, *v_scale;
     int64_t capacity;    // num_blocks * block_size
     int num_kv_heads, head_dim, block_size;
+    int bs_shift;        // log2(block_size)
     int hnd;
 };
 

@@ -59,11 +59,11 @@ __device__ __forceinline__ float rounded(float x) {
     return x;
 }
 
-// Store one row to the pool at `slot` (in range): a copy, or codes and scale.
+// Store one row of a k or v head to the pools: a copy, or codes and scale.
 // Every lane of the warp calls it (shuffles); `store` says whether this
 // lane's group writes.
 template <typename T, int LPR, bool FP8>
-__device__ __forceinline__ void pool_store(const NormRopeParams &p, bool store, int64_t slot,
+__device__ __forceinline__ void pool_store(const PoolArgs &p, const PoolSlot &s, bool store,
                                            int g, bool is_v, int sub, bool active,
                                            const float (&x)[8]) {
     if constexpr (FP8) {
@@ -77,33 +77,35 @@ __device__ __forceinline__ void pool_store(const NormRopeParams &p, bool store, 
         const uint32_t byte = scale_byte(amax);
         const float inv = scale_inverse(byte);
         const bool bad = byte == kScaleNaN;
-        const PoolSlot s = pool_slot(p.pool, slot, g);
         if (active)
-            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(is_v ? p.pool.v : p.pool.k) +
-                                       s.row + sub * 8) =
+            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(is_v ? p.v : p.k) + s.row +
+                                       (int64_t)g * s.row_step + sub * 8) =
                 make_uint2(quant4(x, inv, bad), quant4(x + 4, inv, bad));
-        if (sub == 0) (is_v ? p.pool.v_scale : p.pool.k_scale)[s.scale] = (uint8_t)byte;
+        if (sub == 0)
+            (is_v ? p.v_scale : p.k_scale)[s.scale + g * p.block_size] = (uint8_t)byte;
     } else {
-        if (!store || !active) return;
-        const PoolSlot s = pool_slot(p.pool, slot, g);
-        store8<T>(static_cast<T *>(is_v ? p.pool.v : p.pool.k) + s.row + sub * 8, x);
+        if (store && active)
+            store8<T>(static_cast<T *>(is_v ? p.v : p.k) + s.row + (int64_t)g * s.row_step +
+                          sub * 8,
+                      x);
     }
 }
 
 // gpt groups of LPR lanes share a token (gpt a power of two dividing the
-// CTA's groups); group i takes the head rows i, i + gpt, ... of the
-// Hq + 2 Hkv rows of q, k and v.
-template <typename T, int LPR, bool FP8>
+// CTA's groups); group r0 takes the head rows r0, r0 + gpt, ... of the Hq +
+// Hkv rows of q and k, then of the Hkv rows of v.
+template <typename T, int LPR, bool FP8, bool NEOX>
 __global__ void __launch_bounds__(kThreads)
 norm_rope_kernel(const NormRopeParams p, int gpt) {
     pdl_trigger();
     pdl_wait();
     constexpr int kGroups = kThreads / LPR;
+    constexpr int UNR = 3;  // rows in flight per thread
     const int sub = threadIdx.x % LPR, grp = threadIdx.x / LPR;
     const int D = p.pool.head_dim, Hq = p.num_qo_heads, Hkv = p.pool.num_kv_heads;
     const bool active = sub * 8 < D;
     const int64_t t = (int64_t)blockIdx.x * (kGroups / gpt) + grp / gpt;
-    const int r0 = grp % gpt;
+    const int r0 = grp & (gpt - 1);
     const bool live = t < p.num_tokens;
 
     int64_t pos = -1, slot = -1;
@@ -118,89 +120,91 @@ norm_rope_kernel(const NormRopeParams p, int gpt) {
             slot = -1;
         }
     }
-    const bool on = live && pos >= 0;
+    const bool on = live && pos >= 0, cached = on && slot >= 0;
+    const PoolSlot ps = pool_slot(p.pool, cached ? (uint32_t)slot : 0u);
+    const int d0 = sub * 8;  // this lane's dimensions are d0 .. d0 + 7
 
-    // this lane's dimensions are 8*sub .. 8*sub+7; neox: lane sub < half_l
-    // holds the first member of its pairs and lane sub + half_l the second
+    // neox: lane sub < half_l holds the first member of its pairs and lane
+    // sub + half_l the second
     const int rd = p.rotary_dim, half_l = rd / 16;
-    const bool rot = active && sub * 8 < rd;
-    float cs[8], sn[8];  // neox: eight frequencies; GPT-J: four
+    const bool rot = active && d0 < rd;
+    constexpr int NF = NEOX ? 8 : 4;  // frequencies per lane
+    float cs[NF], sn[NF];
+    float wq[8], wk[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < NF; ++i) {
         cs[i] = 1.f;
         sn[i] = 0.f;
     }
-    if (on && rot) {
-        const float2 *row = p.cos_sin + pos * (rd / 2);
-        const int f0 = p.neox ? 8 * (sub < half_l ? sub : sub - half_l) : 4 * sub;
-        const int nf = p.neox ? 8 : 4;
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            if (i >= nf) break;
-            const float4 v = __ldg(reinterpret_cast<const float4 *>(row + f0 + i));
+    for (int i = 0; i < 8; ++i) wq[i] = wk[i] = 0.f;
+    if (active) {
+        if (p.weight_f32) {
+            if (Hq) load8<float>(static_cast<const float *>(p.q_weight) + d0, wq);
+            load8<float>(static_cast<const float *>(p.k_weight) + d0, wk);
+        } else {
+            if (Hq) load8<T>(static_cast<const T *>(p.q_weight) + d0, wq);
+            load8<T>(static_cast<const T *>(p.k_weight) + d0, wk);
+        }
+    }
+    if (on && rot) {
+        const int f0 = NEOX ? 8 * (sub < half_l ? sub : sub - half_l) : 4 * sub;
+        const float4 *row = reinterpret_cast<const float4 *>(p.cos_sin + pos * (rd / 2) + f0);
+#pragma unroll
+        for (int i = 0; i < NF; i += 2) {
+            const float4 v = __ldg(row + i / 2);
             cs[i] = v.x;
             sn[i] = v.y;
             cs[i + 1] = v.z;
             sn[i + 1] = v.w;
         }
-        if (p.neox && sub < half_l)  // x_a' = x_a c - x_b s
+        if (NEOX && sub < half_l)  // x_a' = x_a c - x_b s
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sn[i] = -sn[i];
+            for (int i = 0; i < NF; ++i) sn[i] = -sn[i];
     }
-    const int partner = p.neox && rot ? (sub < half_l ? sub + half_l : sub - half_l) : sub;
+    const int partner = NEOX && rot ? (sub < half_l ? sub + half_l : sub - half_l) : sub;
     const int src_lane = (threadIdx.x & 31) - sub + partner;
+    const float inv_d = 1.f / (float)D;
 
-    const int rows = Hq + 2 * Hkv;
-    const int rounds = (rows + gpt - 1) / gpt;  // the same for every lane of the CTA
-    constexpr int UNR = 3;
-    for (int k0 = 0; k0 < rounds; k0 += UNR) {
+    const T *q_in = static_cast<const T *>(p.query) + t * p.q_stride + d0;
+    const T *k_in = static_cast<const T *>(p.key) + t * p.k_stride + d0;
+    const T *v_in = static_cast<const T *>(p.value) + t * p.v_stride + d0;
+    T *q_out = static_cast<T *>(p.query_out) + t * p.qo_stride + d0;
+    T *k_out = static_cast<T *>(p.key_out) + t * p.ko_stride + d0;
+
+    const int rows = Hq + Hkv;  // every lane of the CTA makes the same rounds
+    for (int base = 0; base < rows; base += gpt * UNR) {
         float x[UNR][8];
 #pragma unroll
         for (int u = 0; u < UNR; ++u) {
-            const int r = r0 + (k0 + u) * gpt;
+            const int r = base + u * gpt + r0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
-            if (!on || !active || r >= rows) continue;
-            const T *src = r < Hq ? static_cast<const T *>(p.query) + t * p.q_stride + r * D
-                           : r < Hq + Hkv
-                               ? static_cast<const T *>(p.key) + t * p.k_stride + (r - Hq) * D
-                               : static_cast<const T *>(p.value) + t * p.v_stride +
-                                     (r - Hq - Hkv) * D;
-            load8<T>(src + sub * 8, x[u]);
+            if (on && active && r < rows)
+                load8<T>(r < Hq ? q_in + r * D : k_in + (r - Hq) * D, x[u]);
         }
 #pragma unroll
         for (int u = 0; u < UNR; ++u) {
-            const int r = r0 + (k0 + u) * gpt;
-            const bool here = on && r < rows;
-            const bool is_v = r >= Hq + Hkv;
-            // the norm and the rotation of a v row are computed and dropped:
-            // the shuffles need every lane of the warp
+            if (base + u * gpt >= rows) break;  // the same for the whole CTA
+            const int r = base + u * gpt + r0;
+            const bool is_q = r < Hq, here = on && r < rows;
             float ss = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss = fmaf(x[u][i], x[u][i], ss);
 #pragma unroll
             for (int off = LPR / 2; off > 0; off >>= 1)
                 ss += __shfl_xor_sync(0xffffffffu, ss, off);
-            const float inv = 1.f / sqrtf(ss / (float)D + p.eps);
-            float y[8], w[8];
+            const float inv = rsqrtf(fmaf(ss, inv_d, p.eps));
+            float y[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = 0.f;
-            if (here && !is_v && active) {
-                const void *wp = r < Hq ? p.q_weight : p.k_weight;
-                if (p.weight_f32)
-                    load8<float>(static_cast<const float *>(wp) + sub * 8, w);
-                else
-                    load8<T>(static_cast<const T *>(wp) + sub * 8, w);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = x[u][i] * inv * w[i];
-            if (p.neox) {
+            for (int i = 0; i < 8; ++i) y[i] = x[u][i] * inv * (is_q ? wq[i] : wk[i]);
+            if constexpr (NEOX) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float o = __shfl_sync(0xffffffffu, y[i], src_lane);
-                    if (rot) y[i] = fmaf(o, sn[i], y[i] * cs[i]);
+                    y[i] = fmaf(o, sn[i], y[i] * cs[i]);  // not rotated: y * 1 + y * 0
                 }
-            } else if (rot) {
+            } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float a = y[2 * i], b = y[2 * i + 1];
@@ -208,15 +212,30 @@ norm_rope_kernel(const NormRopeParams p, int gpt) {
                     y[2 * i + 1] = fmaf(a, sn[i], b * cs[i]);
                 }
             }
+            if (here && active && is_q) store8<T>(q_out + r * D, y);
+            if (here && active && !is_q) store8<T>(k_out + (r - Hq) * D, y);
+            if (base + u * gpt + gpt > Hq) {  // some group of the CTA holds a k row
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = is_v ? x[u][i] : rounded<T>(y[i]);
-            if (here && active && r < Hq)
-                store8<T>(static_cast<T *>(p.query_out) + t * p.qo_stride + r * D + sub * 8, y);
-            else if (here && active && !is_v)
-                store8<T>(static_cast<T *>(p.key_out) + t * p.ko_stride + (r - Hq) * D + sub * 8,
-                          y);
-            pool_store<T, LPR, FP8>(p, here && r >= Hq && slot >= 0, slot,
-                                    is_v ? r - Hq - Hkv : r - Hq, is_v, sub, active, y);
+                for (int i = 0; i < 8; ++i) y[i] = rounded<T>(y[i]);
+                pool_store<T, LPR, FP8>(p.pool, ps, cached && r < rows && !is_q, r - Hq, false,
+                                        sub, active, y);
+            }
+        }
+    }
+    for (int base = 0; base < Hkv; base += gpt * UNR) {
+        float x[UNR][8];
+#pragma unroll
+        for (int u = 0; u < UNR; ++u) {
+            const int g = base + u * gpt + r0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
+            if (cached && active && g < Hkv) load8<T>(v_in + g * D, x[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < UNR; ++u) {
+            if (base + u * gpt >= Hkv) break;
+            const int g = base + u * gpt + r0;
+            pool_store<T, LPR, FP8>(p.pool, ps, cached && g < Hkv, g, true, sub, active, x[u]);
         }
     }
 }
@@ -224,14 +243,14 @@ norm_rope_kernel(const NormRopeParams p, int gpt) {
 template <typename T, int LPR, bool FP8>
 cudaError_t launch_lpr(const NormRopeParams &p, cudaStream_t stream) {
     constexpr int kGroups = kThreads / LPR;
-    const int rows = p.num_qo_heads + 2 * p.pool.num_kv_heads;
+    const int rows = p.num_qo_heads + p.pool.num_kv_heads;
     int gpt = 1;
     while (gpt * 2 <= kGroups && gpt * 2 <= rows) gpt *= 2;
     const int64_t per_cta = kGroups / gpt;
     const int64_t blocks = (p.num_tokens + per_cta - 1) / per_cta;
     if (blocks > 0x7fffffffLL) return cudaErrorNotSupported;
-    return launch_pdl(norm_rope_kernel<T, LPR, FP8>, dim3((unsigned)blocks), dim3(kThreads), 0,
-                      stream, p, gpt);
+    auto kern = p.neox ? norm_rope_kernel<T, LPR, FP8, true> : norm_rope_kernel<T, LPR, FP8, false>;
+    return launch_pdl(kern, dim3((unsigned)blocks), dim3(kThreads), 0, stream, p, gpt);
 }
 
 template <typename T, bool FP8>

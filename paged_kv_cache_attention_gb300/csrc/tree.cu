@@ -79,10 +79,6 @@ __device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
     return reinterpret_cast<uint8_t *>(a);
 }
 
-__device__ __forceinline__ void st_zero16(uint32_t addr) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
-}
-
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
                                             uint32_t d) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
@@ -97,14 +93,6 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
                  : "r"(addr)
                  : "memory");
     return v;
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // What a request attends.  Lengths and offsets live on the device and are
@@ -346,7 +334,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                         }
                         if (!in || bad)
                             for (int c = 0; c < T / 8; ++c)
-                                st_zero16(vb + (c >> 3) * C::HALF + sw128(r, c & 7));
+                                st_shared_zero16(vb + (c >> 3) * C::HALF + sw128(r, c & 7));
                         const uint32_t m = __ballot_sync(0xffffffffu, in && bad);
                         if (lane == 0) pois[w] = m;
                     }
