@@ -39,6 +39,19 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
     return byte == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
 }
 
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// The larger of two bf16 pairs, NaN if either is (as 0x7fff).
+__device__ __forceinline__ uint32_t bf16x2_max_nan(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // Two floats -> two e4m3 codes, nearest even, saturating at 448; lo in the low byte.
 __device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
     uint16_t r;
@@ -46,10 +59,14 @@ __device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
     return r;
 }
 
-// Four codes from four floats times `inv`; a row of scale byte 255 stores 0.
+// Four codes from four floats times `inv` (a row of scale byte 255 stores 0).
 __device__ __forceinline__ uint32_t quant4(const float *x, float inv, bool bad) {
-    if (bad) return 0u;
-    return cvt_e4m3x2(x[0] * inv, x[1] * inv) | (cvt_e4m3x2(x[2] * inv, x[3] * inv) << 16);
+    const uint64_t f = f2_pack(inv, inv);
+    float a, b, c, d;
+    f2_unpack(f2_mul(f2_pack(x[0], x[1]), f), a, b);
+    f2_unpack(f2_mul(f2_pack(x[2], x[3]), f), c, d);
+    const uint32_t r = cvt_e4m3x2(a, b) | (cvt_e4m3x2(c, d) << 16);
+    return bad ? 0u : r;
 }
 
 // Four e4m3 codes of a word as f16 pairs: bytes 0 and 1 in lo, 2 and 3 in hi

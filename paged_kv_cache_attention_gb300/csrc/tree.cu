@@ -16,13 +16,17 @@
 // the tensor core about half the time its 64 KB of bf16 K and V take from HBM,
 // the padding of small trees is free.
 //
+// Over 8-bit pools the codes become f16 tiles as they are; K's scale multiplies
+// its column of S and V's scale its column of P, both in fp32, and q is scaled
+// per row by a power of two into f16 (decode_fp8.cu gives the error bounds).
+//
 // One CTA per (kv head, row tile, partition, request): split-KV over
 // partitions of a multiple of 128 keys and a merge kernel, or one partition and
 // a direct store.  Warps 0-3: softmax, one row per thread; warp 4: TMA; warp 5:
-// MMA issue; with 8-bit pools eight more warps turn codes into bf16 tiles.
-//   S = Q K^T -> TMEM; the softmax reads S twice (maximum, then weights), writes
-//   P (bf16) over S; O += P V with P from TMEM.  O is rescaled only when a
-//   row's maximum grows by more than 2^8.  bf16 pools up to D = 128 run two CTAs
+// MMA issue; with 8-bit pools four more warps turn codes into f16 tiles.
+//   S = Q K^T -> TMEM; the softmax takes its row into registers, writes P (16
+//   bits) over S; O += P V with P from TMEM.  O is rescaled only when a row's
+//   maximum grows by more than 2^4.  bf16 pools up to D = 128 run two CTAs
 //   per SM (256 TMEM columns, 97 KB each) that cover each other's softmax;
 //   the others run one CTA with two S buffers.
 // Tiles that hold anything a row does not see (the drafts, the window's edge,
@@ -39,7 +43,8 @@ namespace {
 constexpr int kTile = 128;      // rows and keys per tile
 constexpr int kMaxDraft = 256;
 constexpr float kNegInf = -INFINITY;
-constexpr float kLazy = 8.f;    // log2 units a maximum may grow before O is rescaled
+constexpr float kLazy = 4.f;    // log2 units a maximum may grow before O is rescaled
+constexpr int kWeightExp = 10;  // f16 weights stay below 2^(kWeightExp + kLazy)
 
 template <int T, bool KV8>
 struct Cfg {
@@ -49,29 +54,27 @@ struct Cfg {
     static constexpr int CTAS = (!KV8 && T <= 128) ? 2 : 1;
     static constexpr int NS = CTAS == 2 ? 1 : 2;     // S buffers
     static constexpr int KB = (T == 64 || (KV8 && T == 128)) ? 2 : 1;  // K and V buffers
-    static constexpr int RU = !KV8 ? 0 : T == 256 ? 1 : T == 128 ? 4 : 8;  // raw tiles
-    // Barriers of the raw ring: an even count, so that the K warps meet every
-    // phase of theirs and the V warps of theirs (tiles alternate K, V).
-    static constexpr int RB = RU == 1 ? 2 : RU;
+    static constexpr int RU = !KV8 ? 0 : T == 256 ? 1 : T == 128 ? 3 : 8;  // raw tiles
     static constexpr int RAW = T * kTile;
     static constexpr int ROWB = T < 128 ? T : 128;   // bytes of a raw box row (8-bit pools)
-    static constexpr int THREADS = KV8 ? 448 : 192;
+    static constexpr int THREADS = KV8 ? 320 : 192;
     static constexpr int TMEM = NS * 128 + T <= 256 ? 256 : 512;
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_K = TILE;
     static constexpr int OFF_V = OFF_K + KB * TILE;
     static constexpr int OFF_RAW = OFF_V + KB * TILE;
     static constexpr int OFF_SCALE = OFF_RAW + RU * RAW;
-    static constexpr int OFF_DEPTH = OFF_SCALE + RU * kTile;
-    static constexpr int OFF_BAR = OFF_DEPTH + kMaxDraft * 4;
+    static constexpr int OFF_FACT = OFF_SCALE + RU * kTile;  // [KB][K, V][128] float
+    static constexpr int OFF_DEPTH = OFF_FACT + (KV8 ? KB * 2 * kTile * 4 : 0);
+    static constexpr int OFF_BAR = OFF_DEPTH + kMaxDraft * 2;
     // barriers
     static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + KB, B_VFULL = B_KEMPTY + KB,
                          B_VEMPTY = B_VFULL + KB, B_SFULL = B_VEMPTY + KB,
                          B_PFULL = B_SFULL + NS, B_O = B_PFULL + NS, B_LAND = B_O + 1,
-                         B_POISON = B_LAND + 1, B_RFULL = B_POISON + 2, B_REMPTY = B_RFULL + RB,
-                         NBAR = B_REMPTY + RB;
+                         B_POISON = B_LAND + 1, B_FACT = B_POISON + 2, B_RFULL = B_FACT + KB,
+                         B_REMPTY = B_RFULL + RU, NBAR = B_REMPTY + RU;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // tmem, abort, maxdepth, poison[2][4]
-    static constexpr int SMEM = 1024 + OFF_MISC + 64;
+    static constexpr int SMEM = 1024 + OFF_MISC + 48;
 };
 
 __device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
@@ -152,7 +155,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align1024(smem_raw);
     const uint32_t base = smem_u32(smem);
-    int *s_depth = reinterpret_cast<int *>(smem + C::OFF_DEPTH);
+    uint16_t *s_depth = reinterpret_cast<uint16_t *>(smem + C::OFF_DEPTH);
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     int32_t *s_abort = reinterpret_cast<int32_t *>(misc + 1);
     int *s_maxdepth = reinterpret_cast<int *>(misc + 2);
@@ -207,8 +210,9 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         }
         mbar_init(bar(C::B_O), 1);
         mbar_init(bar(C::B_LAND), 1);
-        for (int i = 0; i < 2; ++i) mbar_init(bar(C::B_POISON + i), KV8 ? 4 : 1);
-        for (int i = 0; i < C::RB; ++i) {
+        for (int i = 0; i < 2; ++i) mbar_init(bar(C::B_POISON + i), 1);
+        for (int i = 0; i < C::KB; ++i) mbar_init(bar(C::B_FACT + i), 4);
+        for (int i = 0; i < C::RU; ++i) {
             mbar_init(bar(C::B_RFULL + i), 1 + 8);
             mbar_init(bar(C::B_REMPTY + i), 4);
         }
@@ -222,19 +226,61 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         tc::tmem_alloc(base + C::OFF_MISC, C::TMEM);
         tc::tmem_relinquish();
     }
-    for (int i = threadIdx.x; i < kTile * (T / 8); i += C::THREADS) {
-        const int r = i / (T / 8), c = i - r * (T / 8);
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (r < nrows && c * 8 < Dh)
-            v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) +
-                                                      row_unit(r) * Dh + c * 8));
-        st_shared16(base + C::OFF_Q + (c >> 3) * C::HALF + sw128(r, c & 7), v.x, v.y, v.z, v.w);
+    float rowf = fabsf(p.scale_log2);  // score = S * rowf
+    if constexpr (!KV8) {
+        for (int i = threadIdx.x; i < kTile * (T / 8); i += C::THREADS) {
+            const int r = i / (T / 8), c = i - r * (T / 8);
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (r < nrows && c * 8 < Dh)
+                v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) +
+                                                          row_unit(r) * Dh + c * 8));
+            if (p.scale_log2 < 0.f) {  // the scale's sign goes into q
+                v.x ^= 0x80008000u;
+                v.y ^= 0x80008000u;
+                v.z ^= 0x80008000u;
+                v.w ^= 0x80008000u;
+            }
+            st_shared16(base + C::OFF_Q + (c >> 3) * C::HALF + sw128(r, c & 7), v.x, v.y, v.z,
+                        v.w);
+        }
+    } else if (threadIdx.x < kTile) {
+        // row r of thread r, in f16: times a power of two that brings its largest
+        // value to 2^14..2^15 (exact down to 2^-28 of it)
+        const int r = threadIdx.x;
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            static_cast<const __nv_bfloat16 *>(p.q) + (r < nrows ? row_unit(r) : 0) * Dh);
+        const int nc = r < nrows ? Dh / 8 : 0;
+        uint32_t amax = 0;
+        for (int c = 0; c < nc; ++c) {
+            const uint4 v = __ldg(src + c);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                amax = max(amax, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+        }
+        const int E = max((int)(amax >> 7) - 127, -100);
+        const uint32_t neg = p.scale_log2 < 0.f ? 0x80000000u : 0u;
+        const float f = __uint_as_float(((uint32_t)(127 + 14 - E) << 23) | neg);
+        rowf *= __uint_as_float((uint32_t)(127 + E - 14) << 23);
+        for (int c = 0; c < T / 8; ++c) {
+            uint32_t x[4] = {0u, 0u, 0u, 0u};
+            if (c < nc) {
+                const uint4 v = __ldg(src + c);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[e] = pack_f16(__uint_as_float(w[e] << 16) * f,
+                                    __uint_as_float(w[e] & 0xffff0000u) * f);
+            }
+            st_shared16(base + C::OFF_Q + (c >> 3) * C::HALF + sw128(r, c & 7), x[0], x[1], x[2],
+                        x[3]);
+        }
     }
     fence_proxy_async_smem();
     __syncthreads();  // s_maxdepth is zero
     for (int i = threadIdx.x; i < rq.q_len; i += C::THREADS) {
-        const int d = p.depth ? max(p.depth[rq.q_start + i], 0) : 0;
-        s_depth[i] = d;
+        const int d = p.depth ? min(max(p.depth[rq.q_start + i], 0), 65535) : 0;
+        s_depth[i] = (uint16_t)d;
         atomicMax(s_maxdepth, d);
     }
     tc::fence_before_sync();
@@ -352,12 +398,11 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                 // scale bytes: lane l < 8 copies bytes 16 l .. of the tile
                 const int sid = __shfl_sync(0xffffffffu, id_now, (lane * 16 / BS) & 31);
                 for (int v = 0; v < 2 && alive; ++v) {
-                    const int u = 2 * i + v, s = u % C::RU, last = u - C::RU;
-                    const uint32_t full = bar(C::B_RFULL + u % C::RB);
-                    if (last >= 0)  // the buffer's last tile has been converted
-                        alive = warp_wait_bounded(bar(C::B_REMPTY + last % C::RB),
-                                                  (uint32_t)(last / C::RB) & 1u, p.dev_error,
-                                                  s_abort);
+                    const int u = 2 * i + v, s = u % C::RU;
+                    const uint32_t full = bar(C::B_RFULL + s);
+                    alive = warp_wait_bounded(bar(C::B_REMPTY + s),
+                                              ((uint32_t)(u / C::RU) & 1u) ^ 1u, p.dev_error,
+                                              s_abort);
                     if (!alive) break;
                     if (lane == 0) mbar_arrive_expect_tx(full, C::RAW);
                     __syncwarp();
@@ -390,14 +435,17 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     warp_wait_bounded(bar(C::B_LAND), (uint32_t)(nfix - 1) & 1u, p.dev_error);
             } else {
                 for (int u = max(0, nk - C::RU); u < nk; ++u)
-                    warp_wait_bounded(bar(C::B_RFULL + u % C::RB), (uint32_t)(u / C::RB) & 1u,
+                    warp_wait_bounded(bar(C::B_RFULL + u % C::RU), (uint32_t)(u / C::RU) & 1u,
                                       p.dev_error);
             }
         }
     } else if (warp == 5) {
         // ------------------------------------------------------------ MMA issuer
-        constexpr uint32_t idS = tc::idesc_bf16_f32(128, 128, 0, 0);
-        constexpr uint32_t idO = tc::idesc_bf16_f32(128, T, 0, 1);
+        // f16 operands over 8-bit pools, bf16 otherwise (A and B alike; the
+        // format fields are bits 7 and 10)
+        constexpr uint32_t fmt = KV8 ? (1u << 7 | 1u << 10) : 0u;
+        constexpr uint32_t idS = tc::idesc_bf16_f32(128, 128, 0, 0) & ~fmt;
+        constexpr uint32_t idO = tc::idesc_bf16_f32(128, T, 0, 1) & ~fmt;
         const uint64_t dq = tc::smem_desc_sw128(base + C::OFF_Q, 16, 1024);
         const uint64_t dk0 = tc::smem_desc_sw128(base + C::OFF_K, 16, 1024);
         const uint64_t dv0 = tc::smem_desc_sw128(base + C::OFF_V, C::HALF, 1024);
@@ -456,14 +504,10 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         const int64_t unit = row_on ? row_unit(r) : 0;
         const int node = row_on ? (rt * kTile + r) / G : 0;
         const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-        const int depth = s_depth[node];
-        const int qpos = rq.ctx + depth;
-        const int wlo = p.window_left < 0 ? 0 : max(qpos - p.window_left, 0);
         const int head = row_on ? g * G + (rt * kTile + r) % G : 0;
-        const float slope = p.alibi && row_on ? p.alibi[head] * kLog2e : 0.f;
-        const float scale = p.scale_log2;
-        const bool general_all = p.alibi != nullptr || !(scale >= 0.f);
-        const int64_t *mrow = p.mask + (int64_t)(rq.q_start + node) * p.mask_words;
+        // weights are 2^(s - m_ref), and over 8-bit pools times the key's V scale:
+        // m_ref follows the row's largest score, plus there the tile's largest
+        // scale over 2^10, so that f16 holds the product; both sums share it
         float m_ref = kNegInf, l = 0.f;
         bool alive = true;
         int nfix = 0;
@@ -473,21 +517,54 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         };
         int id = warp_on ? page_id(0) : 0;
         for (int i = 0; i < ntiles; ++i) {
-            const int k0 = (kt0 + i) * kTile;
             const uint32_t t_s = tmem + (i % C::NS) * 128 + lane_base;
             const bool fix = partial(i);
             const uint32_t badpg =
                 __ballot_sync(0xffffffffu, id < 0 || (int64_t)id >= p.num_blocks);
             if (warp_on && i + 1 < ntiles) id = page_id(i + 1);
-            const bool general = fix || general_all || badpg != 0;
-            uint32_t vis[4], pois[4] = {0u, 0u, 0u, 0u};
-            if (general && warp_on) {
+            const bool general = fix || badpg != 0 || p.alibi != nullptr;
+            alive = warp_wait_bounded(bar(C::B_SFULL + i % C::NS), (uint32_t)(i / C::NS) & 1u,
+                                      p.dev_error, s_abort);
+            if (KV8 && alive)
+                alive = warp_wait_bounded(bar(C::B_FACT + i % C::KB),
+                                          (uint32_t)(i / C::KB) & 1u, p.dev_error, s_abort);
+            if (!KV8 && fix && alive) {
+                alive = warp_wait_bounded(bar(C::B_POISON + (nfix & 1)),
+                                          (uint32_t)(nfix >> 1) & 1u, p.dev_error, s_abort);
+                ++nfix;
+            }
+            if (!alive) break;
+            if (warp_on) {
+                const float4 *kf =
+                    reinterpret_cast<const float4 *>(smem + C::OFF_FACT) + (i % C::KB) * 64;
+                const float4 *vf = kf + 32;
+                tc::fence_after_sync();
+                const int k0 = (kt0 + i) * kTile;
+                const float rf = general ? 1.f : rowf;
+                // Chunk c (32 keys) of S as loaded -> scores: over 8-bit pools times
+                // the K scales; in a general tile complete, with bias, -inf for what
+                // the row does not see, NaN for a key whose V row is not finite.
+                auto to_scores = [&](int c, uint32_t (&v)[32], uint32_t &hide) {
+                    if constexpr (KV8) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 f = kf[c * 8 + e / 4];
+                            v[e] = __float_as_uint(__uint_as_float(v[e]) * f.x);
+                            v[e + 1] = __float_as_uint(__uint_as_float(v[e + 1]) * f.y);
+                            v[e + 2] = __float_as_uint(__uint_as_float(v[e + 2]) * f.z);
+                            v[e + 3] = __float_as_uint(__uint_as_float(v[e + 3]) * f.w);
+                        }
+                    }
+                    hide = 0u;
+                    if (!general) return;
+                    const int depth = s_depth[node], qpos = rq.ctx + depth;
+                    const int wlo = p.window_left < 0 ? 0 : max(qpos - p.window_left, 0);
                     const int kc = k0 + 32 * c;
-                    vis[c] = range_bits(max(wlo, tok_lo) - kc, min(rq.ctx, tok_hi) - kc);
-                    const int n0 = kc - rq.ctx;  // draft node of the word's first key
+                    uint32_t vis = range_bits(max(wlo, tok_lo) - kc, min(rq.ctx, tok_hi) - kc);
+                    const int n0 = kc - rq.ctx;  // draft node of the chunk's first key
                     if (n0 > -32 && n0 < rq.q_len && row_on) {
+                        const int64_t *mrow =
+                            p.mask + (int64_t)(rq.q_start + node) * p.mask_words;
                         uint32_t d = mask_bits(mrow, p.mask_words, n0) &
                                      range_bits(max(tok_lo, rq.ctx) - kc, tok_hi - kc);
                         if (p.window_left >= 0) {
@@ -496,134 +573,151 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                                 if (s_depth[n0 + e] < depth - p.window_left) d &= ~(1u << e);
                             }
                         }
-                        vis[c] |= d;
+                        vis |= d;
                     }
                     for (int q = 0; q < 32 / BS; ++q)
                         if ((badpg >> (c * 32 / BS + q)) & 1u)
-                            vis[c] &= ~range_bits(q * BS, q * BS + BS);
-                }
-            }
-            if (!warp_wait_bounded(bar(C::B_SFULL + i % C::NS), (uint32_t)(i / C::NS) & 1u,
-                                   p.dev_error, s_abort)) {
-                alive = false;
-                break;
-            }
-            if (fix) {
-                if (!warp_wait_bounded(bar(C::B_POISON + (nfix & 1)), (uint32_t)(nfix >> 1) & 1u,
-                                       p.dev_error, s_abort)) {
-                    alive = false;
-                    break;
-                }
+                            vis &= ~range_bits(q * BS, q * BS + BS);
+                    const uint32_t pois =
+                        !KV8 && fix ? *reinterpret_cast<volatile uint32_t *>(
+                                          s_poison + ((nfix - 1) & 1) * 4 + c)
+                                    : 0u;
+                    hide = ~vis;
+                    const float slope = p.alibi && row_on ? p.alibi[head] * kLog2e : 0.f;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    pois[c] = *reinterpret_cast<volatile uint32_t *>(s_poison + (nfix & 1) * 4 + c);
-                ++nfix;
-            }
-            if (warp_on) {
-                tc::fence_after_sync();
-                float mt = kNegInf;
-                if (!general) {
-                    float a0 = kNegInf, a1 = kNegInf;
+                    for (int e = 0; e < 32; ++e) {
+                        float x = __uint_as_float(v[e]) * rowf;
+                        if (p.alibi) {
+                            const int k = kc + e;
+                            const int n = min(max(k - rq.ctx, 0), rq.q_len - 1);
+                            const int kpos = k < rq.ctx ? k : rq.ctx + s_depth[n];
+                            x = fmaf(slope, (float)(kpos - qpos), x);
+                        }
+                        if ((pois >> e) & 1u) x = __uint_as_float(0x7fffffffu);
+                        v[e] = __float_as_uint((vis >> e) & 1u ? x : kNegInf);
+                    }
+                };
+                float a0 = kNegInf, a1 = kNegInf;
+                auto maximum = [&](const uint32_t (&v)[32]) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        a0 = fmax3(a0, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                        a1 = fmax3(a1, __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+                    }
+                };
+                // bf16 pools hold the whole row in registers; over 8-bit pools,
+                // whose scales need them too, S is read from TMEM a second time
+                uint32_t v[KV8 ? 2 : 4][32], hide[KV8 ? 2 : 4];
+                float shift = 0.f;
+                if constexpr (!KV8) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tc::ld_32x32b_x32(t_s + 32 * c, v[c]);
+                    tc::wait_ld();
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32];
-                        tc::ld_32x32b_x32(t_s + 32 * c, v);
-                        tc::wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            a0 = fmax3(a0, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-                            a1 = fmax3(a1, __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
-                        }
+                        to_scores(c, v[c], hide[c]);
+                        maximum(v[c]);
                     }
-                    mt = fmaxf(a0, a1) * scale;
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32];
-                        tc::ld_32x32b_x32(t_s + 32 * c, v);
+                    for (int h = 0; h < 2; ++h) {
+                        tc::ld_32x32b_x32(t_s + 64 * h, v[0]);
+                        tc::ld_32x32b_x32(t_s + 64 * h + 32, v[1]);
                         tc::wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            float x = __uint_as_float(v[e]) * scale;
-                            if (p.alibi) {
-                                const int k = k0 + 32 * c + e;
-                                const int n = min(k - rq.ctx, rq.q_len - 1);
-                                const int kpos = k < rq.ctx ? k : rq.ctx + s_depth[n];
-                                x = fmaf(slope, (float)(kpos - qpos), x);
-                            }
-                            mt = fmaxf(mt, (vis[c] >> e) & 1u ? x : kNegInf);
-                        }
+                        to_scores(2 * h, v[0], hide[0]);
+                        maximum(v[0]);
+                        to_scores(2 * h + 1, v[1], hide[1]);
+                        maximum(v[1]);
                     }
+                    // the tile's largest V scale (NaN rows aside), not below 2^-90:
+                    // weights without the scale stay finite
+                    const uint4 w = reinterpret_cast<const uint4 *>(vf)[lane];
+                    uint32_t mxb = 0;
+                    mxb = w.x < 0x7f800000u ? max(mxb, w.x) : mxb;
+                    mxb = w.y < 0x7f800000u ? max(mxb, w.y) : mxb;
+                    mxb = w.z < 0x7f800000u ? max(mxb, w.z) : mxb;
+                    mxb = w.w < 0x7f800000u ? max(mxb, w.w) : mxb;
+                    mxb = __reduce_max_sync(0xffffffffu, mxb);
+                    shift = (float)(max((int)(mxb >> 23), 37) - 127 - kWeightExp);
                 }
+                const float mt = fmaxf(a0, a1) * rf + shift;
                 if (i == 0) {
                     m_ref = mt;
                 } else {
                     const bool grow = mt > m_ref + kLazy || (m_ref == kNegInf && mt > kNegInf);
                     if (__any_sync(0xffffffffu, grow)) {
                         if (C::NS == 2) {  // O must be at rest: the last PV is done
-                            if (!warp_wait_bounded(bar(C::B_VEMPTY + (i - 1) % C::KB),
-                                                   (uint32_t)((i - 1) / C::KB) & 1u,
-                                                   p.dev_error, s_abort)) {
-                                alive = false;
-                                break;
-                            }
+                            alive = warp_wait_bounded(bar(C::B_VEMPTY + (i - 1) % C::KB),
+                                                      (uint32_t)((i - 1) / C::KB) & 1u,
+                                                      p.dev_error, s_abort);
+                            if (!alive) break;
                             tc::fence_after_sync();
                         }
                         const float f = grow ? fast_exp2(m_ref - mt) : 1.f;
                         if (grow) m_ref = mt;
                         l *= f;
 #pragma unroll 1
-                        for (int c = 0; c < T / 32; ++c) {
-                            uint32_t v[32];
-                            tc::ld_32x32b_x32(t_o + lane_base + 32 * c, v);
+                        for (int c = 0; c < T / 16; ++c) {
+                            uint32_t o[16];
+                            tc::ld_32x32b_x16(t_o + lane_base + 16 * c, o);
                             tc::wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-                            tc::st_32x32b_x32(t_o + lane_base + 32 * c, v);
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tc::st_32x32b_x16(t_o + lane_base + 16 * c, o);
                         }
                     }
                 }
                 const float msub = m_ref == kNegInf ? 0.f : m_ref;
                 float s0 = 0.f, s1 = 0.f;
+                // weights of chunk c: their sum, and 16 columns of P over S columns
+                // that have been read
+                auto to_weights = [&](int c, const uint32_t (&v)[32], uint32_t hide) {
+                    uint32_t w[16];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t v[32], w[16];
-                    tc::ld_32x32b_x32(t_s + 32 * c, v);
-                    tc::wait_ld();
-                    if (!general) {
+                    for (int e = 0; e < 32; e += 4) {
+                        float x[4];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float a =
-                                fast_exp2(fmaf(__uint_as_float(v[e]), scale, -msub));
-                            const float bb =
-                                fast_exp2(fmaf(__uint_as_float(v[e + 1]), scale, -msub));
-                            s0 += a;
-                            s1 += bb;
-                            w[e / 2] = pack_bf16(a, bb);
-                        }
-                    } else {
+                        for (int k = 0; k < 4; ++k)
+                            x[k] = fast_exp2(fmaf(__uint_as_float(v[e + k]), rf, -msub));
+                        s0 += x[0];
+                        s1 += x[1];
+                        s0 += x[2];
+                        s1 += x[3];
+                        if constexpr (KV8) {
+                            const float4 f = vf[c * 8 + e / 4];
+                            x[0] *= f.x;
+                            x[1] *= f.y;
+                            x[2] *= f.z;
+                            x[3] *= f.w;
+                            if (general) {  // a hidden key's scale may be NaN
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            float x = __uint_as_float(v[e]) * scale;
-                            if (p.alibi) {
-                                const int k = k0 + 32 * c + e;
-                                const int n = min(k - rq.ctx, rq.q_len - 1);
-                                const int kpos = k < rq.ctx ? k : rq.ctx + s_depth[n];
-                                x = fmaf(slope, (float)(kpos - qpos), x);
+                                for (int k = 0; k < 4; ++k)
+                                    if ((hide >> (e + k)) & 1u) x[k] = 0.f;
                             }
-                            float a = (vis[c] >> e) & 1u ? fast_exp2(x - msub) : 0.f;
-                            if ((vis[c] & pois[c]) >> e & 1u) a = __uint_as_float(0x7fffffffu);
-                            s0 += a;
-                            v[e] = __float_as_uint(a);
+                            w[e / 2] = pack_f16(x[0], x[1]);
+                            w[e / 2 + 1] = pack_f16(x[2], x[3]);
+                        } else {
+                            w[e / 2] = pack_bf16(x[0], x[1]);
+                            w[e / 2 + 1] = pack_bf16(x[2], x[3]);
                         }
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2)
-                            w[e / 2] =
-                                pack_bf16(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
                     }
-                    // 16 columns of P over S columns that have been read
                     tc::st_32x32b_x16(t_s + 16 * c, w);
+                };
+                if constexpr (!KV8) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) to_weights(c, v[c], hide[c]);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        tc::ld_32x32b_x32(t_s + 64 * h, v[0]);
+                        tc::ld_32x32b_x32(t_s + 64 * h + 32, v[1]);
+                        tc::wait_ld();
+                        to_scores(2 * h, v[0], hide[0]);
+                        to_weights(2 * h, v[0], hide[0]);
+                        to_scores(2 * h + 1, v[1], hide[1]);
+                        to_weights(2 * h + 1, v[1], hide[1]);
+                    }
                 }
                 l += s0 + s1;
                 tc::wait_st();
@@ -690,66 +784,76 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             }
         }
     } else if constexpr (KV8) {
-        // ------------------------------------------------------------ codes -> bf16 tiles
-        // warps 6-9 take K tiles, 10-13 V tiles, 32 rows each; a lane takes
-        // 16 codes of a row at a time
+        // ------------------------------------------------------------ codes -> f16 tiles
+        // warps 6-9, 32 rows of every K and V tile each; a lane takes 16 codes
+        // of a row at a time, and holds the row's scale bytes
         constexpr int CH = T / 16, RPI = 32 / CH;  // chunks per row, rows per round
-        const int w = (warp - 6) & 3, isv = warp >= 10 ? 1 : 0;
-        const uint32_t buf0 = base + (isv ? C::OFF_V : C::OFF_K);
-        const int bfull = isv ? C::B_VFULL : C::B_KFULL, bempty = isv ? C::B_VEMPTY : C::B_KEMPTY;
+        const int w = warp - 6;
         bool alive = true;
-        int nfix = 0;
         auto row_id = [&](int i) {  // lane = row: its page if the row is in the range
             const int key = (kt0 + i) * kTile + w * 32 + lane;
             return key >= tok_lo && key < tok_hi ? bt[key / BS] : -1;
         };
         int id = row_id(0);
-        for (int i = 0; i < ntiles; ++i) {
+        for (int i = 0; i < ntiles && alive; ++i) {
             const uint32_t ok =
                 __ballot_sync(0xffffffffu, id >= 0 && (int64_t)id < p.num_blocks);
             if (i + 1 < ntiles) id = row_id(i + 1);
-            const int u = 2 * i + isv, rs = u % C::RU, s = i % C::KB;
-            alive = warp_wait_bounded(bar(C::B_RFULL + u % C::RB), (uint32_t)(u / C::RB) & 1u,
-                                      p.dev_error, s_abort) &&
-                    warp_wait_bounded(bar(bempty + s), ((uint32_t)(i / C::KB) & 1u) ^ 1u,
-                                      p.dev_error, s_abort);
-            if (!alive) break;
-            const uint32_t raw = base + C::OFF_RAW + rs * C::RAW;
-            const uint8_t *sc = smem + C::OFF_SCALE + rs * kTile + w * 32;
-            const bool fix = partial(i);
-            const uint32_t nan_rows = __ballot_sync(0xffffffffu, sc[lane] == kScaleNaN) & ok;
-            // V rows that must be zero: not attended, or NaN where some row does
-            // not see them
-            const uint32_t zero = isv ? ~ok | (fix ? nan_rows : 0u) : 0u;
-#pragma unroll 2
-            for (int it = 0; it < 32 / RPI; ++it) {
-                const int rr = it * RPI + lane / CH, c = lane % CH, r = w * 32 + rr;
-                const int part_c = (c * 16) / C::ROWB, cc = c - part_c * (C::ROWB / 16);
-                const uint32_t ra = raw + part_c * (kTile * C::ROWB) +
-                                    (C::ROWB == 128 ? sw128(r, cc)
-                                                    : r * 64u + ((cc ^ ((r >> 1) & 3)) << 4));
-                const uint4 code = ld_shared16(ra);
-                uint32_t x[8];
-                dequant16_bf16(code, sc[rr], x);
-                if ((zero >> rr) & 1u)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = 0u;
-                const uint32_t dst = buf0 + s * C::TILE + (c >> 2) * C::HALF;
-                const int ch = (2 * c) & 7;
-                st_shared16(dst + sw128(r, ch), x[0], x[1], x[2], x[3]);
-                st_shared16(dst + sw128(r, ch + 1), x[4], x[5], x[6], x[7]);
+            const int s = i % C::KB;
+            const uint32_t free_ph = ((uint32_t)(i / C::KB) & 1u) ^ 1u;
+            float *fact = reinterpret_cast<float *>(smem + C::OFF_FACT) + s * 256 + w * 32 + lane;
+            float kscale = 0.f;
+#pragma unroll 1
+            for (int isv = 0; isv < 2; ++isv) {
+                const int u = 2 * i + isv, rs = u % C::RU;
+                alive = warp_wait_bounded(bar(C::B_RFULL + rs), (uint32_t)(u / C::RU) & 1u,
+                                          p.dev_error, s_abort) &&
+                        warp_wait_bounded(bar((isv ? C::B_VEMPTY : C::B_KEMPTY) + s), free_ph,
+                                          p.dev_error, s_abort);
+                if (!alive) break;
+                const uint32_t raw = base + C::OFF_RAW + rs * C::RAW;
+                const uint32_t byte = smem[C::OFF_SCALE + rs * kTile + w * 32 + lane];
+                if (!isv) {
+                    kscale = scale_value(byte);
+                } else {
+                    // both factors of this row: V's buffer is free, so the softmax of
+                    // the tile that last used this slot is done
+                    fact[0] = kscale;
+                    fact[128] = (ok >> lane) & 1u ? scale_value(byte) : 0.f;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::B_FACT + s));
+                }
+                // V rows that are not attended may hold any codes, and a row of NaN
+                // reaches who sees it through its factor: zero both
+                const uint32_t nan_rows = __ballot_sync(0xffffffffu, byte == kScaleNaN);
+                const uint32_t zero = isv ? ~ok | nan_rows : 0u;
+                const uint32_t buf = base + (isv ? C::OFF_V : C::OFF_K) + s * C::TILE;
+#pragma unroll 4
+                for (int it = 0; it < 32 / RPI; ++it) {
+                    const int rr = it * RPI + lane / CH, c = lane % CH, r = w * 32 + rr;
+                    const int part_c = (c * 16) / C::ROWB, cc = c - part_c * (C::ROWB / 16);
+                    const uint32_t ra = raw + part_c * (kTile * C::ROWB) +
+                                        (C::ROWB == 128 ? sw128(r, cc)
+                                                        : r * 64u + ((cc ^ ((r >> 1) & 3)) << 4));
+                    uint4 code = ld_shared16(ra);
+                    if ((zero >> rr) & 1u) code = make_uint4(0u, 0u, 0u, 0u);
+                    uint32_t x[8];
+                    e4m3_to_f16(code.x, x[0], x[1]);
+                    e4m3_to_f16(code.y, x[2], x[3]);
+                    e4m3_to_f16(code.z, x[4], x[5]);
+                    e4m3_to_f16(code.w, x[6], x[7]);
+                    const uint32_t dst = buf + (c >> 2) * C::HALF;
+                    const int ch = (2 * c) & 7;
+                    st_shared16(dst + sw128(r, ch), x[0], x[1], x[2], x[3]);
+                    st_shared16(dst + sw128(r, ch + 1), x[4], x[5], x[6], x[7]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar((isv ? C::B_VFULL : C::B_KFULL) + s));
+                    mbar_arrive(bar(C::B_REMPTY + rs));
+                }
             }
-            if (fix && isv) {
-                if (lane == 0) s_poison[(nfix & 1) * 4 + w] = nan_rows;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                if (fix && isv) mbar_arrive(bar(C::B_POISON + (nfix & 1)));
-                mbar_arrive(bar(bfull + s));
-                mbar_arrive(bar(C::B_REMPTY + u % C::RB));
-            }
-            if (fix) ++nfix;
         }
     }
     tc::fence_before_sync();
