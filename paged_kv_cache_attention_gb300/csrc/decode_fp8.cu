@@ -44,11 +44,6 @@ constexpr int kWeightExp = 10;   // weights are at most 2^kWeightExp * 2^kLazy
 constexpr float kLazy = 4.f;     // log2 units a score may exceed its row's reference
 constexpr float kNegInf = -INFINITY;
 
-__device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
-    const uintptr_t a = (reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023);
-    return reinterpret_cast<uint8_t *>(a);
-}
-
 __device__ __forceinline__ int clipped_len(const DecodeParams &p, int b, int block_size,
                                            bool report) {
     const long long cap_blocks = (long long)p.max_blocks_per_seq * block_size;
@@ -124,7 +119,7 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
     const DecodeParams &p = pp.d;
 
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = align1024(smem_raw);
+    uint8_t *smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // 1024-aligned
     int *s_blk = reinterpret_cast<int *>(smem + C::BLK_OFF);
     float *s_m = reinterpret_cast<float *>(smem + C::M_OFF);
     float *s_l = reinterpret_cast<float *>(smem + C::L_OFF);

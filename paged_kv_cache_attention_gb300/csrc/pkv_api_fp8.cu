@@ -81,10 +81,9 @@ pkv_status pool_map(CUtensorMap *map, const void *base, const pkv_cache_desc &c)
 }
 
 // Partitions of the tree attention: `partition_size` keys each when given,
-// else as many as keep the SMs busy -- about two CTAs' worth of work per slot
-// for kTreeSlots resident CTAs -- and not below kMinTreePart keys.  A fixed
-// slot count, so that the workspace of a problem does not depend on the device.
-constexpr int kTreeTile = 128, kMaxDraft = 256, kTreeSlots = 304, kMinTreePart = 256;
+// else as many as give about kTreeCtas CTAs, but not below kMinTreePart keys.  A
+// fixed count, so that the workspace of a problem does not depend on the device.
+constexpr int kTreeTile = 128, kMaxDraft = 256, kTreeCtas = 608, kMinTreePart = 256;
 
 struct TreeSplit {
     int part, row_tiles;
@@ -102,8 +101,9 @@ TreeSplit tree_split(int batch, int Hq, int Hkv, int D, int max_q, int64_t total
     if (window_left >= 0 && (int64_t)window_left + max_q < span) span = window_left + max_q;
     s.part = partition_size;
     if (s.part == 0) {
-        const int64_t units = (int64_t)batch * Hkv * s.row_tiles;
-        const int64_t want = (2 * kTreeSlots + units - 1) / units;
+        // row tiles go two to a CTA (one at head size 256)
+        const int64_t units = (int64_t)batch * Hkv * (D > 128 ? s.row_tiles : (s.row_tiles + 1) / 2);
+        const int64_t want = (kTreeCtas + units - 1) / units;
         int64_t part = (span + want - 1) / want;
         part = (part + kTreeTile - 1) / kTreeTile * kTreeTile;
         s.part = (int)(part < kMinTreePart ? kMinTreePart : part);

@@ -16,23 +16,29 @@
 // the tensor core about half the time its 64 KB of bf16 K and V take from HBM,
 // the padding of small trees is free.
 //
-// Over 8-bit pools the codes become f16 tiles as they are; K's scale multiplies
-// its column of S and V's scale its column of P, both in fp32, and q is scaled
-// per row by a power of two into f16 (decode_fp8.cu gives the error bounds).
+// Over 8-bit pools the codes become f16 tiles, each row times 2^(its scale's
+// exponent - the tile's largest), exact unless a row is more than 2^15 smaller
+// than another of its tile (then off by 2^-25 of the largest scale).  The
+// tile's two largest scales are scalars of the softmax: K's multiplies the
+// scores, V's moves the exponent of the weights.  q is scaled per row by a power
+// of two into f16 (decode_fp8.cu gives the error bound).
 //
-// One CTA per (kv head, row tile, partition, request): split-KV over
+// One CTA per (kv head, one or two row tiles, partition, request): split-KV over
 // partitions of a multiple of 128 keys and a merge kernel, or one partition and
-// a direct store.  Warps 0-3: softmax, one row per thread; warp 4: TMA; warp 5:
-// MMA issue; with 8-bit pools four more warps turn codes into f16 tiles.
+// a direct store.  Four softmax warps per row tile, one row per thread; a TMA
+// warp; an MMA warp; over 8-bit pools the warps that convert codes.
 //   S = Q K^T -> TMEM; the softmax takes its row into registers, writes P (16
 //   bits) over S; O += P V with P from TMEM.  O is rescaled only when a row's
-//   maximum grows by more than 2^4.  bf16 pools up to D = 128 run two CTAs
-//   per SM (256 TMEM columns, 97 KB each) that cover each other's softmax;
-//   the others run one CTA with two S buffers.
+//   maximum grows by more than 2^4.
+// The products run in units n = (key tile, row tile), row tiles fastest, with two S
+// buffers in turn: S(n + 2) is issued right behind O(n), so a unit's softmax
+// always has the other buffer's products beside it -- those of the other row
+// tile, or of the next key tile when there is one.  Two row tiles share every
+// K and V tile.  K and V tiles are double-buffered where shared memory allows.
 // Tiles that hold anything a row does not see (the drafts, the window's edge,
-// the ends of the partition) take a general path with 128 visibility bits per
-// row; V rows behind the end are zeroed, and a V row with a non-finite value
-// is zeroed too and reaches, as NaN, only the rows that see it.
+// the ends of the partition) take a general path with visibility bits; V rows
+// behind the end are zeroed, and a V row with a non-finite value is zeroed too
+// and reaches, as NaN, only the rows that see it.
 #include "pkv_fp8.cuh"
 #include "pkv_tcgen05.cuh"
 
@@ -46,41 +52,44 @@ constexpr float kNegInf = -INFINITY;
 constexpr float kLazy = 4.f;    // log2 units a maximum may grow before O is rescaled
 constexpr int kWeightExp = 10;  // f16 weights stay below 2^(kWeightExp + kLazy)
 
-template <int T, bool KV8>
+// T: tile width (head size padded to 64, 128 or 256); X: row tiles per CTA.
+template <int T, bool KV8, int X>
 struct Cfg {
     static constexpr int HALVES = T / 64;
     static constexpr int HALF = kTile * 128;         // 128 rows of 64 dims
     static constexpr int TILE = HALVES * HALF;
-    static constexpr int CTAS = (!KV8 && T <= 128) ? 2 : 1;
-    static constexpr int NS = CTAS == 2 ? 1 : 2;     // S buffers
-    static constexpr int KB = (T == 64 || (KV8 && T == 128)) ? 2 : 1;  // K and V buffers
-    static constexpr int RU = !KV8 ? 0 : T == 256 ? 1 : T == 128 ? 3 : 8;  // raw tiles
+    // K and V tiles: as many as fit, for the bytes in flight (over 8-bit pools the
+    // raw tiles are what is in flight)
+    static constexpr int KB = KV8 ? (T == 64 ? 2 : 1) : T == 64 ? 4 : T == 128 ? 3 : 1;
+    static constexpr int VB = KV8 ? (T == 64 || (T == 128 && X == 1) ? 2 : 1)
+                                  : T == 64 ? 4 : T == 128 ? 4 - X : 1;
+    // raw tiles of codes, K and V in turn
+    static constexpr int RU = !KV8 ? 0 : T == 256 ? 1 : 4;
     static constexpr int RAW = T * kTile;
-    static constexpr int ROWB = T < 128 ? T : 128;   // bytes of a raw box row (8-bit pools)
-    static constexpr int THREADS = KV8 ? 320 : 192;
-    static constexpr int TMEM = NS * 128 + T <= 256 ? 256 : 512;
+    static constexpr int ROWB = T < 128 ? T : 128;   // bytes of a raw box row
+    static constexpr int DW = !KV8 ? 0 : X == 2 ? 2 : 4;  // converting warps
+    static constexpr int W_TMA = 4 * X, W_MMA = 4 * X + 1, W_CVT = 4 * X + 2;
+    static constexpr int THREADS = 32 * (4 * X + 2 + DW);
+    static constexpr int TMEM = 512;                 // two S of 128 columns, X O of T
     static constexpr int OFF_Q = 0;
-    static constexpr int OFF_K = TILE;
+    static constexpr int OFF_K = X * TILE;
     static constexpr int OFF_V = OFF_K + KB * TILE;
-    static constexpr int OFF_RAW = OFF_V + KB * TILE;
+    static constexpr int OFF_RAW = OFF_V + VB * TILE;
     static constexpr int OFF_SCALE = OFF_RAW + RU * RAW;
-    static constexpr int OFF_FACT = OFF_SCALE + RU * kTile;  // [KB][K, V][128] float
-    static constexpr int OFF_DEPTH = OFF_FACT + (KV8 ? KB * 2 * kTile * 4 : 0);
+    static constexpr int OFF_DEPTH = OFF_SCALE + RU * kTile;
     static constexpr int OFF_BAR = OFF_DEPTH + kMaxDraft * 2;
     // barriers
     static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + KB, B_VFULL = B_KEMPTY + KB,
-                         B_VEMPTY = B_VFULL + KB, B_SFULL = B_VEMPTY + KB,
-                         B_PFULL = B_SFULL + NS, B_O = B_PFULL + NS, B_LAND = B_O + 1,
-                         B_POISON = B_LAND + 1, B_FACT = B_POISON + 2, B_RFULL = B_FACT + KB,
-                         B_REMPTY = B_RFULL + RU, NBAR = B_REMPTY + RU;
-    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // tmem, abort, maxdepth, poison[2][4]
-    static constexpr int SMEM = 1024 + OFF_MISC + 48;
+                         B_VEMPTY = B_VFULL + VB, B_SFULL = B_VEMPTY + VB,
+                         B_PFULL = B_SFULL + 2, B_O = B_PFULL + 2, B_LAND = B_O + 2,
+                         B_POISON = B_LAND + 1, B_FACT = B_POISON + 2, B_RFULL = B_FACT + 2,
+                         B_REMPTY = B_RFULL + RU, B_Q = B_REMPTY + RU, NBAR = B_Q + 1;
+    // tmem, abort, maxdepth, -, poison[2][4], scale bytes[2][K, V]
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+    static constexpr int SMEM = 1024 + OFF_MISC + 64;
+    static_assert(256 + X * T <= 512, "tensor memory");
+    static_assert(SMEM <= 232448, "shared memory");
 };
-
-__device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
-    const uintptr_t a = (reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023);
-    return reinterpret_cast<uint8_t *>(a);
-}
 
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
                                             uint32_t d) {
@@ -147,30 +156,33 @@ __device__ __forceinline__ uint32_t range_bits(int lo, int hi) {
     return top & ~((1u << lo) - 1u);
 }
 
-template <int T, bool KV8>
-__global__ void __launch_bounds__(Cfg<T, KV8>::THREADS, Cfg<T, KV8>::CTAS)
+template <int T, bool KV8, int X>
+__global__ void __launch_bounds__(Cfg<T, KV8, X>::THREADS, 1)
 tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             const __grid_constant__ CUtensorMap tmv) {
-    using C = Cfg<T, KV8>;
+    using C = Cfg<T, KV8, X>;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = align1024(smem_raw);
+    uint8_t *smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // 1024-aligned
     const uint32_t base = smem_u32(smem);
     uint16_t *s_depth = reinterpret_cast<uint16_t *>(smem + C::OFF_DEPTH);
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     int32_t *s_abort = reinterpret_cast<int32_t *>(misc + 1);
     int *s_maxdepth = reinterpret_cast<int *>(misc + 2);
-    uint32_t *s_poison = misc + 4;  // [2][4]
+    uint32_t *s_poison = misc + 4;   // [2][4]
+    uint32_t *s_byte = misc + 12;    // [2][K, V]: a tile's largest scale bytes
     auto bar = [&](int i) { return base + C::OFF_BAR + 8 * i; };
 
     pdl_trigger();
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.z;
-    const int g = blockIdx.x / p.row_tiles, rt = blockIdx.x - g * p.row_tiles;
+    const int rgroups = (p.row_tiles + X - 1) / X;
+    const int g = blockIdx.x / rgroups, rt = (blockIdx.x - g * rgroups) * X;
     const Req rq = request(p, b, blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0);
     const int G = p.group, Dh = p.head_dim;
-    const int nrows = min(rq.q_len * G - rt * kTile, kTile);  // rows of this tile
+    const int nrows = min(rq.q_len * G - rt * kTile, X * kTile);  // rows of this CTA
     if (nrows <= 0) return;
+    const int nx = nrows > kTile ? 2 : 1;  // its row tiles
     const int P = p.partition_size;
     const int part = rq.start / P + blockIdx.y;
     const int tok_lo = max(part * P, rq.start);
@@ -198,23 +210,27 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
 
     // ---- set-up: barriers, TMEM, Q tile, depths
     if (threadIdx.x == 0) {
+        constexpr int kFill = KV8 ? C::DW : 1;  // arrivals that fill a tile
         for (int i = 0; i < C::KB; ++i) {
-            mbar_init(bar(C::B_KFULL + i), KV8 ? 4 : 1);
+            mbar_init(bar(C::B_KFULL + i), kFill);
             mbar_init(bar(C::B_KEMPTY + i), 1);
-            mbar_init(bar(C::B_VFULL + i), KV8 ? 4 : 1);
+        }
+        for (int i = 0; i < C::VB; ++i) {
+            mbar_init(bar(C::B_VFULL + i), kFill);
             mbar_init(bar(C::B_VEMPTY + i), 1);
         }
-        for (int i = 0; i < C::NS; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(bar(C::B_SFULL + i), 1);
             mbar_init(bar(C::B_PFULL + i), 4);
+            mbar_init(bar(C::B_O + i), 1);
+            mbar_init(bar(C::B_POISON + i), kFill);
+            mbar_init(bar(C::B_FACT + i), 1);
         }
-        mbar_init(bar(C::B_O), 1);
         mbar_init(bar(C::B_LAND), 1);
-        for (int i = 0; i < 2; ++i) mbar_init(bar(C::B_POISON + i), 1);
-        for (int i = 0; i < C::KB; ++i) mbar_init(bar(C::B_FACT + i), 4);
+        mbar_init(bar(C::B_Q), 4 * X);
         for (int i = 0; i < C::RU; ++i) {
             mbar_init(bar(C::B_RFULL + i), 1 + 8);
-            mbar_init(bar(C::B_REMPTY + i), 4);
+            mbar_init(bar(C::B_REMPTY + i), C::DW);
         }
         fence_barrier_init();
         *s_abort = 0;
@@ -222,72 +238,22 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         tma_prefetch_desc(&tmk);
         tma_prefetch_desc(&tmv);
     }
-    if (warp == 5) {
+    if (warp == C::W_MMA) {
         tc::tmem_alloc(base + C::OFF_MISC, C::TMEM);
         tc::tmem_relinquish();
     }
-    float rowf = fabsf(p.scale_log2);  // score = S * rowf
-    if constexpr (!KV8) {
-        for (int i = threadIdx.x; i < kTile * (T / 8); i += C::THREADS) {
-            const int r = i / (T / 8), c = i - r * (T / 8);
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (r < nrows && c * 8 < Dh)
-                v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) +
-                                                          row_unit(r) * Dh + c * 8));
-            if (p.scale_log2 < 0.f) {  // the scale's sign goes into q
-                v.x ^= 0x80008000u;
-                v.y ^= 0x80008000u;
-                v.z ^= 0x80008000u;
-                v.w ^= 0x80008000u;
-            }
-            st_shared16(base + C::OFF_Q + (c >> 3) * C::HALF + sw128(r, c & 7), v.x, v.y, v.z,
-                        v.w);
+    if (p.depth && (p.window_left >= 0 || p.alibi)) {
+        __syncthreads();  // s_maxdepth is zero
+        for (int i = threadIdx.x; i < rq.q_len; i += C::THREADS) {
+            const int d = min(max(p.depth[rq.q_start + i], 0), 65535);
+            s_depth[i] = (uint16_t)d;
+            atomicMax(s_maxdepth, d);
         }
-    } else if (threadIdx.x < kTile) {
-        // row r of thread r, in f16: times a power of two that brings its largest
-        // value to 2^14..2^15 (exact down to 2^-28 of it)
-        const int r = threadIdx.x;
-        const uint4 *src = reinterpret_cast<const uint4 *>(
-            static_cast<const __nv_bfloat16 *>(p.q) + (r < nrows ? row_unit(r) : 0) * Dh);
-        const int nc = r < nrows ? Dh / 8 : 0;
-        uint32_t amax = 0;
-        for (int c = 0; c < nc; ++c) {
-            const uint4 v = __ldg(src + c);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                amax = max(amax, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-        }
-        const int E = max((int)(amax >> 7) - 127, -100);
-        const uint32_t neg = p.scale_log2 < 0.f ? 0x80000000u : 0u;
-        const float f = __uint_as_float(((uint32_t)(127 + 14 - E) << 23) | neg);
-        rowf *= __uint_as_float((uint32_t)(127 + E - 14) << 23);
-        for (int c = 0; c < T / 8; ++c) {
-            uint32_t x[4] = {0u, 0u, 0u, 0u};
-            if (c < nc) {
-                const uint4 v = __ldg(src + c);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    x[e] = pack_f16(__uint_as_float(w[e] << 16) * f,
-                                    __uint_as_float(w[e] & 0xffff0000u) * f);
-            }
-            st_shared16(base + C::OFF_Q + (c >> 3) * C::HALF + sw128(r, c & 7), x[0], x[1], x[2],
-                        x[3]);
-        }
-    }
-    fence_proxy_async_smem();
-    __syncthreads();  // s_maxdepth is zero
-    for (int i = threadIdx.x; i < rq.q_len; i += C::THREADS) {
-        const int d = p.depth ? min(max(p.depth[rq.q_start + i], 0), 65535) : 0;
-        s_depth[i] = (uint16_t)d;
-        atomicMax(s_maxdepth, d);
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = misc[0];
-    const uint32_t t_o = tmem + C::NS * 128;
 
     const int BS = p.block_size, npg = kTile / BS;
     const int32_t *bt = p.block_table + (int64_t)b * p.max_blocks_per_seq;
@@ -301,7 +267,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         return k0 < tok_lo || k0 < wfull || k0 + kTile > tok_hi || k0 + kTile > rq.ctx;
     };
 
-    if (warp == 4) {
+    if (warp == C::W_TMA) {
         // ------------------------------------------------------------ producer
         // box coordinates of (page, kv head); one past the pool reads zeros
         const int oob = p.hnd ? (int)(p.num_blocks * p.num_kv_heads)
@@ -328,24 +294,27 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             const int id_now = id;
             if (i + 1 < ntiles) id = page_id(i + 1);
             if constexpr (!KV8) {
-                const int s = i % C::KB;
-                const uint32_t ph = (uint32_t)(i / C::KB) & 1u;
+                const int ks = i % C::KB, vs = i % C::VB;
                 // lane -> (page, 64-dim half)
                 const int lp = lane / C::HALVES, lh = lane % C::HALVES;
                 const int brow = __shfl_sync(0xffffffffu, row, lp);
-                alive = warp_wait_bounded(bar(C::B_KEMPTY + s), ph ^ 1u, p.dev_error, s_abort);
+                alive = warp_wait_bounded(bar(C::B_KEMPTY + ks),
+                                          ((uint32_t)(i / C::KB) & 1u) ^ 1u, p.dev_error,
+                                          s_abort);
                 if (!alive) break;
-                if (lane == 0) mbar_arrive_expect_tx(bar(C::B_KFULL + s), C::TILE);
+                if (lane == 0) mbar_arrive_expect_tx(bar(C::B_KFULL + ks), C::TILE);
                 __syncwarp();
                 if (lp < npg)
-                    tma_load_3d(base + C::OFF_K + s * C::TILE + lh * C::HALF + lp * BS * 128,
-                                &tmk, bar(C::B_KFULL + s), lh * 64, cy, brow);
+                    tma_load_3d(base + C::OFF_K + ks * C::TILE + lh * C::HALF + lp * BS * 128,
+                                &tmk, bar(C::B_KFULL + ks), lh * 64, cy, brow);
                 ++nk;
-                alive = warp_wait_bounded(bar(C::B_VEMPTY + s), ph ^ 1u, p.dev_error, s_abort);
+                alive = warp_wait_bounded(bar(C::B_VEMPTY + vs),
+                                          ((uint32_t)(i / C::VB) & 1u) ^ 1u, p.dev_error,
+                                          s_abort);
                 if (!alive) break;
                 const bool fix = partial(i);
-                const uint32_t vbar = fix ? bar(C::B_LAND) : bar(C::B_VFULL + s);
-                const uint32_t vb = base + C::OFF_V + s * C::TILE;
+                const uint32_t vbar = fix ? bar(C::B_LAND) : bar(C::B_VFULL + vs);
+                const uint32_t vb = base + C::OFF_V + vs * C::TILE;
                 if (lane == 0) mbar_arrive_expect_tx(vbar, C::TILE);
                 __syncwarp();
                 if (lp < npg)
@@ -388,7 +357,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(bar(C::B_POISON + ((nfix - 1) & 1)));
-                        mbar_arrive(bar(C::B_VFULL + s));
+                        mbar_arrive(bar(C::B_VFULL + vs));
                     }
                 }
             } else {
@@ -427,10 +396,10 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                 for (int i = max(0, nk - C::KB); i < nk; ++i)
                     warp_wait_bounded(bar(C::B_KFULL + i % C::KB), (uint32_t)(i / C::KB) & 1u,
                                       p.dev_error);
-                for (int i = max(0, nv - C::KB); i < nv; ++i)
+                for (int i = max(0, nv - C::VB); i < nv; ++i)
                     if (!partial(i))
-                        warp_wait_bounded(bar(C::B_VFULL + i % C::KB),
-                                          (uint32_t)(i / C::KB) & 1u, p.dev_error);
+                        warp_wait_bounded(bar(C::B_VFULL + i % C::VB),
+                                          (uint32_t)(i / C::VB) & 1u, p.dev_error);
                 if (nv > 0 && partial(nv - 1) && nfix > 0)
                     warp_wait_bounded(bar(C::B_LAND), (uint32_t)(nfix - 1) & 1u, p.dev_error);
             } else {
@@ -439,127 +408,195 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                                       p.dev_error);
             }
         }
-    } else if (warp == 5) {
+    } else if (warp == C::W_MMA) {
         // ------------------------------------------------------------ MMA issuer
         // f16 operands over 8-bit pools, bf16 otherwise (A and B alike; the
         // format fields are bits 7 and 10)
         constexpr uint32_t fmt = KV8 ? (1u << 7 | 1u << 10) : 0u;
         constexpr uint32_t idS = tc::idesc_bf16_f32(128, 128, 0, 0) & ~fmt;
         constexpr uint32_t idO = tc::idesc_bf16_f32(128, T, 0, 1) & ~fmt;
-        const uint64_t dq = tc::smem_desc_sw128(base + C::OFF_Q, 16, 1024);
+        const uint64_t dq0 = tc::smem_desc_sw128(base + C::OFF_Q, 16, 1024);
         const uint64_t dk0 = tc::smem_desc_sw128(base + C::OFF_K, 16, 1024);
         const uint64_t dv0 = tc::smem_desc_sw128(base + C::OFF_V, C::HALF, 1024);
         bool alive = true;
-        auto issue_s = [&](int i) {
-            const int s = i % C::KB;
-            alive = warp_wait_bounded(bar(C::B_KFULL + s), (uint32_t)(i / C::KB) & 1u,
-                                      p.dev_error, s_abort);
+        int sj = 0, sx = 0;  // key tile and row tile of the next S
+        auto issue_s = [&](int n) {
+            const int s = sj % C::KB;
+            if (sx == 0)
+                alive = warp_wait_bounded(bar(C::B_KFULL + s), (uint32_t)(sj / C::KB) & 1u,
+                                          p.dev_error, s_abort);
             if (!alive) return;
             tc::fence_after_sync();
             if (lane == 0) {
+                const uint64_t dq = dq0 + (uint64_t)((sx * C::TILE) >> 4);
                 const uint64_t dk = dk0 + (uint64_t)((s * C::TILE) >> 4);
-                const uint32_t d = tmem + (i % C::NS) * 128;
+                const uint32_t d = tmem + (n & 1) * 128;
+                if constexpr (T == 128) {
+                    tc::mma_ss8<C::HALF>(d, dq, dk, idS, 0u);
+                } else {
 #pragma unroll
-                for (int h = 0; h < C::HALVES; ++h)
+                    for (int h = 0; h < C::HALVES; ++h)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t off = (h * C::HALF + k * 32) >> 4;
-                        tc::mma_ss(d, dq + off, dk + off, idS, h + k > 0 ? 1u : 0u);
-                    }
-                tc::commit(bar(C::B_SFULL + i % C::NS));
-                tc::commit(bar(C::B_KEMPTY + s));
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t off = (h * C::HALF + k * 32) >> 4;
+                            tc::mma_ss(d, dq + off, dk + off, idS, h + k > 0 ? 1u : 0u);
+                        }
+                }
+                tc::commit(bar(C::B_SFULL + (n & 1)));
+                if (sx + 1 == nx) tc::commit(bar(C::B_KEMPTY + s));
             }
             __syncwarp();
+            if (++sx == nx) {
+                sx = 0;
+                ++sj;
+            }
         };
-        issue_s(0);
-        for (int i = 0; i < ntiles && alive; ++i) {
-            if (C::NS == 2 && i + 1 < ntiles) issue_s(i + 1);
-            if (!alive) break;
-            const int s = i % C::KB;
-            alive = warp_wait_bounded(bar(C::B_PFULL + i % C::NS), (uint32_t)(i / C::NS) & 1u,
-                                      p.dev_error, s_abort) &&
-                    warp_wait_bounded(bar(C::B_VFULL + s), (uint32_t)(i / C::KB) & 1u,
+        const int total = ntiles * nx;
+        alive = warp_wait_bounded(bar(C::B_Q), 0, p.dev_error, s_abort);
+        if (alive) issue_s(0);
+        if (total > 1 && alive) issue_s(1);
+        int j = 0, x = 0;
+        for (int n = 0; n < total && alive; ++n) {
+            const int s = j % C::VB;
+            alive = warp_wait_bounded(bar(C::B_PFULL + (n & 1)), (uint32_t)(n >> 1) & 1u,
                                       p.dev_error, s_abort);
+            if (alive && x == 0)
+                alive = warp_wait_bounded(bar(C::B_VFULL + s), (uint32_t)(j / C::VB) & 1u,
+                                          p.dev_error, s_abort);
             if (!alive) break;
             tc::fence_after_sync();
             if (lane == 0) {
                 const uint64_t dv = dv0 + (uint64_t)((s * C::TILE) >> 4);
-                tc::mma_ts8(t_o, tmem + (i % C::NS) * 128, dv, idO, i > 0 ? 1u : 0u);
-                tc::commit(bar(C::B_VEMPTY + s));
-                if (i + 1 == ntiles) tc::commit(bar(C::B_O));
+                tc::mma_ts8(tmem + 256 + x * T, tmem + (n & 1) * 128, dv, idO, j > 0 ? 1u : 0u);
+                if (x + 1 == nx) tc::commit(bar(C::B_VEMPTY + s));
+                if (j + 1 == ntiles) tc::commit(bar(C::B_O + x));
             }
             __syncwarp();
-            if (C::NS == 1 && i + 1 < ntiles) issue_s(i + 1);
+            if (n + 2 < total) issue_s(n + 2);
+            if (++x == nx) {
+                x = 0;
+                ++j;
+            }
         }
         if (!alive) {  // let the products in flight finish (bounded) before TMEM goes
             if (lane == 0) tc::commit(bar(C::B_O));
             __syncwarp();
             warp_wait_bounded(bar(C::B_O), 0, p.dev_error);
         }
-    } else if (warp < 4) {
+    } else if (warp < 4 * X) {
         // ------------------------------------------------------------ softmax
-        const int r = threadIdx.x;           // row = TMEM lane
+        const int x = warp >> 2;             // row tile
+        const int r = threadIdx.x;           // row of the CTA; TMEM lane r % 128
         const bool warp_on = warp * 32 < nrows;
         const bool row_on = r < nrows;
         const int64_t unit = row_on ? row_unit(r) : 0;
         const int node = row_on ? (rt * kTile + r) / G : 0;
-        const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
         const int head = row_on ? g * G + (rt * kTile + r) % G : 0;
-        // weights are 2^(s - m_ref), and over 8-bit pools times the key's V scale:
-        // m_ref follows the row's largest score, plus there the tile's largest
-        // scale over 2^10, so that f16 holds the product; both sums share it
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t t_o = tmem + 256 + x * T + lane_base;
+        // ---- this warp's 32 rows of Q into shared memory (rows past the last:
+        // zeros), 16 lanes per 128 dims of a row; the loads of eight steps are in
+        // flight at once
+        float rowf = fabsf(p.scale_log2);  // score = S * rowf
+        {
+            const uint32_t sq = base + C::OFF_Q + x * C::TILE;
+            const uint32_t neg = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // its sign goes into q
+            constexpr int LPR = T / 8 < 32 ? T / 8 : 32, RPS = 32 / LPR;  // lanes per row
+            constexpr int STEPS = 32 / RPS, BATCH = 8;
+            const int c = lane % LPR, rsub = lane / LPR;
+#pragma unroll 1
+            for (int s0 = 0; s0 < STEPS; s0 += BATCH) {
+                uint4 v[BATCH];
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const int rr = warp * 32 + (s0 + k) * RPS + rsub;
+                    v[k] = make_uint4(0u, 0u, 0u, 0u);
+                    if (rr < nrows && c * 8 < Dh)
+                        v[k] = __ldg(reinterpret_cast<const uint4 *>(
+                                         static_cast<const __nv_bfloat16 *>(p.q) +
+                                         row_unit(rr) * Dh) +
+                                     c);
+                }
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                    if constexpr (KV8) {
+                        // in f16, times a power of two that brings the row's largest value
+                        // to 2^14..2^15 (exact down to 2^-28 of it)
+                        uint32_t amax = 0;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            amax = max(amax, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+#pragma unroll
+                        for (int off = LPR / 2; off > 0; off >>= 1)
+                            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+                        const int E = max((int)(amax >> 7) - 127, -100);
+                        const float f = __uint_as_float((uint32_t)(127 + 14 - E) << 23);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = pack_f16(__uint_as_float(w[e] << 16) * f,
+                                            __uint_as_float(w[e] & 0xffff0000u) * f);
+                        // lane r of the warp keeps the factor of row r
+                        const int Er = __shfl_sync(0xffffffffu, E, (lane % RPS) * LPR);
+                        if (lane / RPS == s0 + k)
+                            rowf *= __uint_as_float((uint32_t)(127 + Er - 14) << 23);
+                    }
+                    const int rr = (warp & 3) * 32 + (s0 + k) * RPS + rsub;
+                    st_shared16(sq + (c >> 3) * C::HALF + sw128(rr, c & 7), w[0] ^ neg,
+                                w[1] ^ neg, w[2] ^ neg, w[3] ^ neg);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::B_Q));
+        }
+        // Weights are 2^(s - m_ref), over 8-bit pools times the tile's largest V
+        // scale.  m_ref follows the row's largest score (there plus that scale
+        // over 2^10, so that f16 holds the product); O and l share it.
         float m_ref = kNegInf, l = 0.f;
+        const bool positions = p.window_left >= 0 || p.alibi;  // depths are loaded
         bool alive = true;
         int nfix = 0;
-        auto page_id = [&](int i) {
-            const int pg = (kt0 + i) * npg + lane;
+        auto page_id = [&](int j) {
+            const int pg = (kt0 + j) * npg + lane;
             return lane < npg && pg >= pg_first && pg <= pg_last ? bt[pg] : 0;
         };
         int id = warp_on ? page_id(0) : 0;
-        for (int i = 0; i < ntiles; ++i) {
-            const uint32_t t_s = tmem + (i % C::NS) * 128 + lane_base;
-            const bool fix = partial(i);
+        for (int j = 0; j < ntiles && x < nx; ++j) {
+            const int n = j * nx + x;
+            const uint32_t t_s = tmem + (n & 1) * 128 + lane_base;
+            const bool fix = partial(j);
             const uint32_t badpg =
                 __ballot_sync(0xffffffffu, id < 0 || (int64_t)id >= p.num_blocks);
-            if (warp_on && i + 1 < ntiles) id = page_id(i + 1);
+            if (warp_on && j + 1 < ntiles) id = page_id(j + 1);
             const bool general = fix || badpg != 0 || p.alibi != nullptr;
-            alive = warp_wait_bounded(bar(C::B_SFULL + i % C::NS), (uint32_t)(i / C::NS) & 1u,
+            alive = warp_wait_bounded(bar(C::B_SFULL + (n & 1)), (uint32_t)(n >> 1) & 1u,
                                       p.dev_error, s_abort);
             if (KV8 && alive)
-                alive = warp_wait_bounded(bar(C::B_FACT + i % C::KB),
-                                          (uint32_t)(i / C::KB) & 1u, p.dev_error, s_abort);
-            if (!KV8 && fix && alive) {
+                alive = warp_wait_bounded(bar(C::B_FACT + (j & 1)), (uint32_t)(j >> 1) & 1u,
+                                          p.dev_error, s_abort);
+            if (fix && alive) {
                 alive = warp_wait_bounded(bar(C::B_POISON + (nfix & 1)),
                                           (uint32_t)(nfix >> 1) & 1u, p.dev_error, s_abort);
                 ++nfix;
             }
             if (!alive) break;
             if (warp_on) {
-                const float4 *kf =
-                    reinterpret_cast<const float4 *>(smem + C::OFF_FACT) + (i % C::KB) * 64;
-                const float4 *vf = kf + 32;
                 tc::fence_after_sync();
-                const int k0 = (kt0 + i) * kTile;
-                const float rf = general ? 1.f : rowf;
-                // Chunk c (32 keys) of S as loaded -> scores: over 8-bit pools times
-                // the K scales; in a general tile complete, with bias, -inf for what
-                // the row does not see, NaN for a key whose V row is not finite.
-                auto to_scores = [&](int c, uint32_t (&v)[32], uint32_t &hide) {
-                    if constexpr (KV8) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 f = kf[c * 8 + e / 4];
-                            v[e] = __float_as_uint(__uint_as_float(v[e]) * f.x);
-                            v[e + 1] = __float_as_uint(__uint_as_float(v[e + 1]) * f.y);
-                            v[e + 2] = __float_as_uint(__uint_as_float(v[e + 2]) * f.z);
-                            v[e + 3] = __float_as_uint(__uint_as_float(v[e + 3]) * f.w);
-                        }
-                    }
-                    hide = 0u;
-                    if (!general) return;
-                    const int depth = s_depth[node], qpos = rq.ctx + depth;
+                float rf = rowf, vexp = 0.f, shift = 0.f;
+                if constexpr (KV8) {
+                    const volatile uint32_t *by = s_byte + (j & 1) * 2;
+                    rf *= scale_value(by[0]);
+                    vexp = (float)((int)by[1] - 127);
+                    shift = vexp - kWeightExp;
+                }
+                // Chunk c (32 keys) of S as complete scores in log2 units: with bias,
+                // -inf for what the row does not see, NaN for a key whose V row is
+                // not finite.
+                auto complete = [&](int c, uint32_t (&v)[32]) {
+                    const int depth = positions ? s_depth[node] : 0, qpos = rq.ctx + depth;
                     const int wlo = p.window_left < 0 ? 0 : max(qpos - p.window_left, 0);
-                    const int kc = k0 + 32 * c;
+                    const int kc = (kt0 + j) * kTile + 32 * c;
                     uint32_t vis = range_bits(max(wlo, tok_lo) - kc, min(rq.ctx, tok_hi) - kc);
                     const int n0 = kc - rq.ctx;  // draft node of the chunk's first key
                     if (n0 > -32 && n0 < rq.q_len && row_on) {
@@ -579,155 +616,133 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                         if ((badpg >> (c * 32 / BS + q)) & 1u)
                             vis &= ~range_bits(q * BS, q * BS + BS);
                     const uint32_t pois =
-                        !KV8 && fix ? *reinterpret_cast<volatile uint32_t *>(
-                                          s_poison + ((nfix - 1) & 1) * 4 + c)
-                                    : 0u;
-                    hide = ~vis;
-                    const float slope = p.alibi && row_on ? p.alibi[head] * kLog2e : 0.f;
+                        fix ? *reinterpret_cast<volatile uint32_t *>(
+                                  s_poison + ((nfix - 1) & 1) * 4 + c)
+                            : 0u;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        v[e] = __float_as_uint(__uint_as_float(v[e]) * rf);
+                    if (p.alibi) {
+                        const float slope = row_on ? p.alibi[head] * kLog2e : 0.f;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const int k = kc + e;
+                            const int m = min(max(k - rq.ctx, 0), rq.q_len - 1);
+                            const int kpos = k < rq.ctx ? k : rq.ctx + s_depth[m];
+                            v[e] = __float_as_uint(
+                                fmaf(slope, (float)(kpos - qpos), __uint_as_float(v[e])));
+                        }
+                    }
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        float x = __uint_as_float(v[e]) * rowf;
-                        if (p.alibi) {
-                            const int k = kc + e;
-                            const int n = min(max(k - rq.ctx, 0), rq.q_len - 1);
-                            const int kpos = k < rq.ctx ? k : rq.ctx + s_depth[n];
-                            x = fmaf(slope, (float)(kpos - qpos), x);
-                        }
-                        if ((pois >> e) & 1u) x = __uint_as_float(0x7fffffffu);
-                        v[e] = __float_as_uint((vis >> e) & 1u ? x : kNegInf);
+                        if ((pois >> e) & 1u) v[e] = 0x7fffffffu;
+                        if (!((vis >> e) & 1u)) v[e] = __float_as_uint(kNegInf);
                     }
                 };
-                float a0 = kNegInf, a1 = kNegInf;
-                auto maximum = [&](const uint32_t (&v)[32]) {
+                auto maximum = [&](float m, const uint32_t (&v)[32]) {
+                    float a0 = m, a1 = kNegInf;
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
                         a0 = fmax3(a0, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
                         a1 = fmax3(a1, __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
                     }
+                    return fmaxf(a0, a1);
                 };
-                // bf16 pools hold the whole row in registers; over 8-bit pools,
-                // whose scales need them too, S is read from TMEM a second time
-                uint32_t v[KV8 ? 2 : 4][32], hide[KV8 ? 2 : 4];
-                float shift = 0.f;
-                if constexpr (!KV8) {
+                // Weights of chunk c, 2^(v * f - m): their sum, and 16 columns of P
+                // over S columns that have been read.
+                auto weights = [&](int c, const uint32_t (&v)[32], float f, float m) {
+                    float s0 = 0.f, s1 = 0.f;
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float a = fast_exp2(fmaf(__uint_as_float(v[e]), f, -m));
+                        const float b = fast_exp2(fmaf(__uint_as_float(v[e + 1]), f, -m));
+                        s0 += a;
+                        s1 += b;
+                        w[e / 2] = KV8 ? pack_f16(a, b) : pack_bf16(a, b);
+                    }
+                    tc::st_32x32b_x16(t_s + 16 * c, w);
+                    return s0 + s1;
+                };
+                // The row's reference follows mt; returns false if a wait gave up.
+                auto refer = [&](float mt) {
+                    if (j == 0) {
+                        m_ref = mt;
+                        return true;
+                    }
+                    const bool grow = mt > m_ref + kLazy || (m_ref == kNegInf && mt > kNegInf);
+                    if (!__any_sync(0xffffffffu, grow)) return true;
+                    if (nx == 1) {  // O must be at rest: the last PV is done
+                        // (with two row tiles, S(n) came behind this O's last PV)
+                        if (!warp_wait_bounded(bar(C::B_VEMPTY + (j - 1) % C::VB),
+                                               (uint32_t)((j - 1) / C::VB) & 1u, p.dev_error,
+                                               s_abort))
+                            return false;
+                        tc::fence_after_sync();
+                    }
+                    const float f = grow ? fast_exp2(m_ref - mt) : 1.f;
+                    if (grow) m_ref = mt;
+                    l *= f;
+#pragma unroll 1
+                    for (int c = 0; c < T / 16; ++c) {
+                        uint32_t o[16];
+                        tc::ld_32x32b_x16(t_o + 16 * c, o);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tc::st_32x32b_x16(t_o + 16 * c, o);
+                    }
+                    return true;
+                };
+                float sum = 0.f;
+                if (!general) {
+                    uint32_t v[4][32];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tc::ld_32x32b_x32(t_s + 32 * c, v[c]);
                     tc::wait_ld();
+                    float mt = kNegInf;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        to_scores(c, v[c], hide[c]);
-                        maximum(v[c]);
-                    }
-                } else {
+                    for (int c = 0; c < 4; ++c) mt = maximum(mt, v[c]);
+                    alive = refer(mt * rf + shift);
+                    if (!alive) break;
+                    const float m = (m_ref == kNegInf ? 0.f : m_ref) - vexp;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        tc::ld_32x32b_x32(t_s + 64 * h, v[0]);
-                        tc::ld_32x32b_x32(t_s + 64 * h + 32, v[1]);
-                        tc::wait_ld();
-                        to_scores(2 * h, v[0], hide[0]);
-                        maximum(v[0]);
-                        to_scores(2 * h + 1, v[1], hide[1]);
-                        maximum(v[1]);
-                    }
-                    // the tile's largest V scale (NaN rows aside), not below 2^-90:
-                    // weights without the scale stay finite
-                    const uint4 w = reinterpret_cast<const uint4 *>(vf)[lane];
-                    uint32_t mxb = 0;
-                    mxb = w.x < 0x7f800000u ? max(mxb, w.x) : mxb;
-                    mxb = w.y < 0x7f800000u ? max(mxb, w.y) : mxb;
-                    mxb = w.z < 0x7f800000u ? max(mxb, w.z) : mxb;
-                    mxb = w.w < 0x7f800000u ? max(mxb, w.w) : mxb;
-                    mxb = __reduce_max_sync(0xffffffffu, mxb);
-                    shift = (float)(max((int)(mxb >> 23), 37) - 127 - kWeightExp);
-                }
-                const float mt = fmaxf(a0, a1) * rf + shift;
-                if (i == 0) {
-                    m_ref = mt;
+                    for (int c = 0; c < 4; ++c) sum += weights(c, v[c], rf, m);
                 } else {
-                    const bool grow = mt > m_ref + kLazy || (m_ref == kNegInf && mt > kNegInf);
-                    if (__any_sync(0xffffffffu, grow)) {
-                        if (C::NS == 2) {  // O must be at rest: the last PV is done
-                            alive = warp_wait_bounded(bar(C::B_VEMPTY + (i - 1) % C::KB),
-                                                      (uint32_t)((i - 1) / C::KB) & 1u,
-                                                      p.dev_error, s_abort);
-                            if (!alive) break;
-                            tc::fence_after_sync();
-                        }
-                        const float f = grow ? fast_exp2(m_ref - mt) : 1.f;
-                        if (grow) m_ref = mt;
-                        l *= f;
+                    float mt = kNegInf;
 #pragma unroll 1
-                        for (int c = 0; c < T / 16; ++c) {
-                            uint32_t o[16];
-                            tc::ld_32x32b_x16(t_o + lane_base + 16 * c, o);
-                            tc::wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tc::st_32x32b_x16(t_o + lane_base + 16 * c, o);
-                        }
-                    }
-                }
-                const float msub = m_ref == kNegInf ? 0.f : m_ref;
-                float s0 = 0.f, s1 = 0.f;
-                // weights of chunk c: their sum, and 16 columns of P over S columns
-                // that have been read
-                auto to_weights = [&](int c, const uint32_t (&v)[32], uint32_t hide) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        float x[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            x[k] = fast_exp2(fmaf(__uint_as_float(v[e + k]), rf, -msub));
-                        s0 += x[0];
-                        s1 += x[1];
-                        s0 += x[2];
-                        s1 += x[3];
-                        if constexpr (KV8) {
-                            const float4 f = vf[c * 8 + e / 4];
-                            x[0] *= f.x;
-                            x[1] *= f.y;
-                            x[2] *= f.z;
-                            x[3] *= f.w;
-                            if (general) {  // a hidden key's scale may be NaN
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    if ((hide >> (e + k)) & 1u) x[k] = 0.f;
-                            }
-                            w[e / 2] = pack_f16(x[0], x[1]);
-                            w[e / 2 + 1] = pack_f16(x[2], x[3]);
-                        } else {
-                            w[e / 2] = pack_bf16(x[0], x[1]);
-                            w[e / 2 + 1] = pack_bf16(x[2], x[3]);
-                        }
-                    }
-                    tc::st_32x32b_x16(t_s + 16 * c, w);
-                };
-                if constexpr (!KV8) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) to_weights(c, v[c], hide[c]);
-                } else {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        tc::ld_32x32b_x32(t_s + 64 * h, v[0]);
-                        tc::ld_32x32b_x32(t_s + 64 * h + 32, v[1]);
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        tc::ld_32x32b_x32(t_s + 32 * c, v);
                         tc::wait_ld();
-                        to_scores(2 * h, v[0], hide[0]);
-                        to_weights(2 * h, v[0], hide[0]);
-                        to_scores(2 * h + 1, v[1], hide[1]);
-                        to_weights(2 * h + 1, v[1], hide[1]);
+                        complete(c, v);
+                        __syncwarp();
+                        mt = maximum(mt, v);
+                    }
+                    alive = refer(mt + shift);
+                    if (!alive) break;
+                    const float m = (m_ref == kNegInf ? 0.f : m_ref) - vexp;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        tc::ld_32x32b_x32(t_s + 32 * c, v);
+                        tc::wait_ld();
+                        complete(c, v);
+                        __syncwarp();
+                        sum += weights(c, v, 1.f, m);
                     }
                 }
-                l += s0 + s1;
+                l += KV8 ? sum * exp2f(-vexp) : sum;
                 tc::wait_st();
                 tc::fence_before_sync();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::B_PFULL + i % C::NS));
+            if (lane == 0) mbar_arrive(bar(C::B_PFULL + (n & 1)));
         }
         // ---- epilogue
-        if (alive) alive = warp_wait_bounded(bar(C::B_O), 0, p.dev_error, s_abort);
+        if (alive && x < nx)  // the last product of all: K and V tiles are free too
+            alive = warp_wait_bounded(bar(C::B_O + nx - 1), 0, p.dev_error, s_abort);
         if (alive && warp_on) {
             tc::fence_after_sync();
             float mul, lse;
@@ -745,120 +760,199 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                 // a NaN weight leaves m_ref as it was: keep the NaN
                 if (l != l) mul = lse = l;
             }
-            const int64_t pidx = unit * p.num_parts + blockIdx.y;
+            if (row_on) {
+                if (p.num_parts > 1)
+                    p.part_lse[unit * p.num_parts + blockIdx.y] = lse;
+                else if (p.lse_out)
+                    p.lse_out[unit] = lse;
+            }
+            // O goes through shared memory (the K and V tiles are done with), so that
+            // whole rows are stored: row r's 16-byte chunk c lies at chunk c ^ r of
+            // its row, where neither side meets a bank twice
+            constexpr int CPR = T / 4;  // chunks per row
+            uint8_t *stage = smem + C::OFF_K + warp * 32 * T * 4;
+            static_assert(4 * X * 32 * T * 4 <= C::OFF_SCALE - C::OFF_K, "staging");
 #pragma unroll 1
             for (int c = 0; c < T / 32; ++c) {
                 uint32_t v[32];
-                tc::ld_32x32b_x32(t_o + lane_base + 32 * c, v);
+                tc::ld_32x32b_x32(t_o + 32 * c, v);
                 tc::wait_ld();
-                if (row_on && p.num_parts > 1) {
-                    float *dst = p.part_o + pidx * Dh + 32 * c;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        if (32 * c + e < Dh)
-                            *reinterpret_cast<float4 *>(dst + e) = make_float4(
-                                __uint_as_float(v[e]) * mul, __uint_as_float(v[e + 1]) * mul,
-                                __uint_as_float(v[e + 2]) * mul,
-                                __uint_as_float(v[e + 3]) * mul);
-                } else if (row_on) {
-                    __nv_bfloat16 *dst =
-                        static_cast<__nv_bfloat16 *>(p.out) + unit * Dh + 32 * c;
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        if (32 * c + e >= Dh) continue;
-                        uint32_t w[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            w[k] = pack_bf16(__uint_as_float(v[e + 2 * k]) * mul,
-                                             __uint_as_float(v[e + 2 * k + 1]) * mul);
-                        *reinterpret_cast<uint4 *>(dst + e) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                }
-                __syncwarp();  // the next load is warp-wide
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<float4 *>(
+                        stage + lane * T * 4 + (((8 * c + e / 4) ^ lane) % CPR) * 16) =
+                        make_float4(__uint_as_float(v[e]) * mul, __uint_as_float(v[e + 1]) * mul,
+                                    __uint_as_float(v[e + 2]) * mul,
+                                    __uint_as_float(v[e + 3]) * mul);
             }
-            if (row_on) {
-                if (p.num_parts > 1)
-                    p.part_lse[pidx] = lse;
-                else if (p.lse_out)
-                    p.lse_out[unit] = lse;
+            __syncwarp();
+            const int rows = min(nrows - warp * 32, 32);
+            constexpr int RPS = CPR < 32 ? 32 / CPR : 1;       // rows per step
+            constexpr int CPL = CPR > 32 ? CPR / 32 : 1;       // chunks per lane
+#pragma unroll 4
+            for (int r0 = 0; r0 < rows; r0 += RPS) {
+                const int rr = r0 + lane / CPR;
+                const int64_t u = row_unit(min(warp * 32 + rr, nrows - 1));
+#pragma unroll
+                for (int k = 0; k < CPL; ++k) {
+                    const int c = lane % CPR + 32 * k;
+                    const float4 o = *reinterpret_cast<const float4 *>(
+                        stage + (rr & 31) * T * 4 + ((c ^ rr) % CPR) * 16);
+                    if (rr >= rows || c * 4 >= Dh) continue;
+                    if (p.num_parts > 1)
+                        *reinterpret_cast<float4 *>(
+                            p.part_o + (u * p.num_parts + blockIdx.y) * Dh + c * 4) = o;
+                    else
+                        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + u * Dh +
+                                                   c * 4) =
+                            make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+                }
             }
         }
     } else if constexpr (KV8) {
         // ------------------------------------------------------------ codes -> f16 tiles
-        // warps 6-9, 32 rows of every K and V tile each; a lane takes 16 codes
-        // of a row at a time, and holds the row's scale bytes
-        constexpr int CH = T / 16, RPI = 32 / CH;  // chunks per row, rows per round
-        const int w = warp - 6;
+        // 128 / DW rows of every K and V tile per warp; a lane converts 16 codes at
+        // a time.  Rows r and r ^ 5 go side by side: their 16-byte chunks, four of
+        // each, meet no bank twice, neither where they are read nor written.
+        constexpr int ROWS = kTile / C::DW;
+        const int w = warp - C::W_CVT;
         bool alive = true;
-        auto row_id = [&](int i) {  // lane = row: its page if the row is in the range
-            const int key = (kt0 + i) * kTile + w * 32 + lane;
-            return key >= tok_lo && key < tok_hi ? bt[key / BS] : -1;
+        int nfix = 0;
+        auto page_id = [&](int j) {  // lane l < npg: page l of tile j, -1: not attended
+            const int pg = (kt0 + j) * npg + lane;
+            return lane < npg && pg >= pg_first && pg <= pg_last ? bt[pg] : -1;
         };
-        int id = row_id(0);
-        for (int i = 0; i < ntiles && alive; ++i) {
-            const uint32_t ok =
-                __ballot_sync(0xffffffffu, id >= 0 && (int64_t)id < p.num_blocks);
-            if (i + 1 < ntiles) id = row_id(i + 1);
-            const int s = i % C::KB;
-            const uint32_t free_ph = ((uint32_t)(i / C::KB) & 1u) ^ 1u;
-            float *fact = reinterpret_cast<float *>(smem + C::OFF_FACT) + s * 256 + w * 32 + lane;
-            float kscale = 0.f;
+        int id = page_id(0);
+        for (int j = 0; j < ntiles && alive; ++j) {
+            const int k0 = (kt0 + j) * kTile;
+            // lane: rows 4 lane .. 4 lane + 3 of the tile, all in one page
+            const int myid = __shfl_sync(0xffffffffu, id, lane * 4 / BS);
+            const bool idok = myid >= 0 && (int64_t)myid < p.num_blocks;
+            const uint32_t in4 = idok ? range_bits(tok_lo - k0 - 4 * lane, tok_hi - k0 - 4 * lane) &
+                                            15u
+                                      : 0u;
+            if (j + 1 < ntiles) id = page_id(j + 1);
+            const bool fix = partial(j);
+            uint32_t kmax = 1;
 #pragma unroll 1
             for (int isv = 0; isv < 2; ++isv) {
-                const int u = 2 * i + isv, rs = u % C::RU;
+                const int u = 2 * j + isv, rs = u % C::RU;
+                const int nb = isv ? C::VB : C::KB, s = j % nb;
                 alive = warp_wait_bounded(bar(C::B_RFULL + rs), (uint32_t)(u / C::RU) & 1u,
                                           p.dev_error, s_abort) &&
-                        warp_wait_bounded(bar((isv ? C::B_VEMPTY : C::B_KEMPTY) + s), free_ph,
-                                          p.dev_error, s_abort);
+                        warp_wait_bounded(bar((isv ? C::B_VEMPTY : C::B_KEMPTY) + s),
+                                          ((uint32_t)(j / nb) & 1u) ^ 1u, p.dev_error, s_abort);
                 if (!alive) break;
-                const uint32_t raw = base + C::OFF_RAW + rs * C::RAW;
-                const uint32_t byte = smem[C::OFF_SCALE + rs * kTile + w * 32 + lane];
-                if (!isv) {
-                    kscale = scale_value(byte);
-                } else {
-                    // both factors of this row: V's buffer is free, so the softmax of
-                    // the tile that last used this slot is done
-                    fact[0] = kscale;
-                    fact[128] = (ok >> lane) & 1u ? scale_value(byte) : 0.f;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(C::B_FACT + s));
+                const uint8_t *sc = smem + C::OFF_SCALE + rs * kTile;
+                // the largest scale byte of the attended rows, NaN rows aside; not
+                // below 2^-90, so that 1 / scale stays finite
+                const uint32_t b4 = *reinterpret_cast<const uint32_t *>(sc + 4 * lane);
+                uint32_t top = 37;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t by = (b4 >> (8 * e)) & 255u;
+                    if (((in4 >> e) & 1u) && by != kScaleNaN) top = max(top, by);
                 }
-                // V rows that are not attended may hold any codes, and a row of NaN
-                // reaches who sees it through its factor: zero both
-                const uint32_t nan_rows = __ballot_sync(0xffffffffu, byte == kScaleNaN);
-                const uint32_t zero = isv ? ~ok | nan_rows : 0u;
-                const uint32_t buf = base + (isv ? C::OFF_V : C::OFF_K) + s * C::TILE;
-#pragma unroll 4
-                for (int it = 0; it < 32 / RPI; ++it) {
-                    const int rr = it * RPI + lane / CH, c = lane % CH, r = w * 32 + rr;
-                    const int part_c = (c * 16) / C::ROWB, cc = c - part_c * (C::ROWB / 16);
-                    const uint32_t ra = raw + part_c * (kTile * C::ROWB) +
-                                        (C::ROWB == 128 ? sw128(r, cc)
-                                                        : r * 64u + ((cc ^ ((r >> 1) & 3)) << 4));
-                    uint4 code = ld_shared16(ra);
-                    if ((zero >> rr) & 1u) code = make_uint4(0u, 0u, 0u, 0u);
-                    uint32_t x[8];
-                    e4m3_to_f16(code.x, x[0], x[1]);
-                    e4m3_to_f16(code.y, x[2], x[3]);
-                    e4m3_to_f16(code.z, x[4], x[5]);
-                    e4m3_to_f16(code.w, x[6], x[7]);
-                    const uint32_t dst = buf + (c >> 2) * C::HALF;
-                    const int ch = (2 * c) & 7;
-                    st_shared16(dst + sw128(r, ch), x[0], x[1], x[2], x[3]);
-                    st_shared16(dst + sw128(r, ch + 1), x[4], x[5], x[6], x[7]);
+                top = __reduce_max_sync(0xffffffffu, top);
+                if (!isv) {
+                    kmax = top;
+                } else if (w == 0 && lane == 0) {
+                    // V's buffer is free, so the softmax that last used this slot is done
+                    s_byte[(j & 1) * 2] = kmax;
+                    s_byte[(j & 1) * 2 + 1] = top;
+                    mbar_arrive(bar(C::B_FACT + (j & 1)));
+                }
+                // NaN rows of a V tile that some row does not see are zeroed and noted
+                uint32_t bad4 = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (((b4 >> (8 * e)) & 255u) == kScaleNaN) bad4 |= 1u << e;
+                bad4 &= in4;
+                if (isv && fix) {
+                    // lane l holds rows 4l..: word q of the tile is lanes 8q .. 8q + 7
+                    uint32_t word = bad4 << (4 * (lane & 7));
+                    word |= __shfl_xor_sync(0xffffffffu, word, 1);
+                    word |= __shfl_xor_sync(0xffffffffu, word, 2);
+                    word |= __shfl_xor_sync(0xffffffffu, word, 4);
+                    if (w == 0 && (lane & 7) == 0) s_poison[(nfix & 1) * 4 + (lane >> 3)] = word;
+                }
+                const uint32_t zero4 = isv ? (~in4 & 15u) | (fix ? bad4 : 0u) : 0u;
+                const bool zeros = __any_sync(0xffffffffu, zero4 != 0u);
+                // Row r = 8 * group + rq: its chunks' places in the raw tile and in the
+                // f16 tile depend on the group only through 8 rows' distance.
+                const int q = lane >> 3, c4 = lane & 3, rq = (lane & 4) ? q ^ 5 : q;
+                const uint8_t *src = smem + C::OFF_RAW + rs * C::RAW + w * ROWS * C::ROWB;
+                uint8_t *dst = smem + (isv ? C::OFF_V : C::OFF_K) + s * C::TILE + w * ROWS * 128;
+                uint32_t so[C::HALVES];
+#pragma unroll
+                for (int h = 0; h < C::HALVES; ++h) {
+                    const int c = h * 4 + c4, part_c = (c * 16) / C::ROWB;
+                    const int cc = c - part_c * (C::ROWB / 16);
+                    so[h] = part_c * (kTile * C::ROWB) +
+                            (C::ROWB == 128 ? sw128(rq, cc)
+                                            : rq * 64u + ((cc ^ ((rq >> 1) & 3)) << 4));
+                }
+                const uint32_t do0 = sw128(rq, 2 * c4), do1 = sw128(rq, 2 * c4 + 1);
+                constexpr int BATCH = T == 256 ? 2 : 4;  // groups whose loads are in flight
+#pragma unroll 1
+                for (int g0 = 0; g0 < ROWS / 8; g0 += BATCH) {
+                    uint4 code[BATCH][C::HALVES];
+                    uint32_t by[BATCH];
+#pragma unroll
+                    for (int gi = 0; gi < BATCH; ++gi) {
+                        by[gi] = sc[w * ROWS + (g0 + gi) * 8 + rq];
+#pragma unroll
+                        for (int h = 0; h < C::HALVES; ++h)
+                            code[gi][h] = *reinterpret_cast<const uint4 *>(
+                                src + (g0 + gi) * 8 * C::ROWB + so[h]);
+                    }
+#pragma unroll
+                    for (int gi = 0; gi < BATCH; ++gi) {
+                        // 2^(byte - top) in f16, a NaN for a NaN row
+                        const int d = (int)by[gi] - (int)top;
+                        uint32_t f = d >= -14 ? (uint32_t)(15 + min(d, 0)) << 10
+                                     : d >= -24 ? 1u << (24 + d)
+                                                : 0u;
+                        if (by[gi] == kScaleNaN) f = 0x7fffu;
+                        f |= f << 16;
+                        bool zero = false;
+                        if (zeros) {
+                            const int r = w * ROWS + (g0 + gi) * 8 + rq;
+                            zero = (__shfl_sync(0xffffffffu, zero4, r >> 2) >> (r & 3)) & 1u;
+                        }
+#pragma unroll
+                        for (int h = 0; h < C::HALVES; ++h) {
+                            const uint4 cw = code[gi][h];
+                            uint32_t y[8];
+                            e4m3_to_f16(cw.x, y[0], y[1]);
+                            e4m3_to_f16(cw.y, y[2], y[3]);
+                            e4m3_to_f16(cw.z, y[4], y[5]);
+                            e4m3_to_f16(cw.w, y[6], y[7]);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) y[e] = f16x2_mul(y[e], f);
+                            if (zero)
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) y[e] = 0u;
+                            uint8_t *o = dst + h * C::HALF + (g0 + gi) * 1024;
+                            *reinterpret_cast<uint4 *>(o + do0) = make_uint4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<uint4 *>(o + do1) = make_uint4(y[4], y[5], y[6], y[7]);
+                        }
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
+                    if (isv && fix) mbar_arrive(bar(C::B_POISON + (nfix & 1)));
                     mbar_arrive(bar((isv ? C::B_VFULL : C::B_KFULL) + s));
                     mbar_arrive(bar(C::B_REMPTY + rs));
                 }
             }
+            if (fix) ++nfix;
         }
     }
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == 5) {
+    if (warp == C::W_MMA) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, C::TMEM);
     }
@@ -913,33 +1007,35 @@ tree_merge_kernel(const TreeParams p) {
     if (p.lse_out && lane == 0) p.lse_out[unit] = lam == 0.f ? kNegInf : (Ms + log2f(lam)) * kLn2;
 }
 
-template <int T, bool KV8>
+template <int T, bool KV8, int X>
 cudaError_t launch_one(const TreeParams &p, const CUtensorMap *tk, const CUtensorMap *tv,
                        cudaStream_t stream) {
-    using C = Cfg<T, KV8>;
-    static_assert(C::SMEM * C::CTAS + (C::CTAS - 1) * 1024 <= 232448, "shared memory");
-    auto kern = tree_kernel<T, KV8>;
+    using C = Cfg<T, KV8, X>;
+    auto kern = tree_kernel<T, KV8, X>;
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), C::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(p.num_kv_heads * p.row_tiles, p.num_parts, p.batch),
+    const int rgroups = (p.row_tiles + X - 1) / X;
+    return launch_pdl(kern, dim3(p.num_kv_heads * rgroups, p.num_parts, p.batch),
                       dim3(C::THREADS), (size_t)C::SMEM, stream, p, *tk, *tv);
+}
+
+template <bool KV8>
+cudaError_t launch_kv(const TreeParams &p, const CUtensorMap *tk, const CUtensorMap *tv,
+                      cudaStream_t stream) {
+    if (p.head_dim > 128) return launch_one<256, KV8, 1>(p, tk, tv, stream);
+    if (p.row_tiles > 1)
+        return p.head_dim <= 64 ? launch_one<64, KV8, 2>(p, tk, tv, stream)
+                                : launch_one<128, KV8, 2>(p, tk, tv, stream);
+    return p.head_dim <= 64 ? launch_one<64, KV8, 1>(p, tk, tv, stream)
+                            : launch_one<128, KV8, 1>(p, tk, tv, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_tree(const TreeParams &p, const CUtensorMap *tmap_k,
                         const CUtensorMap *tmap_v, cudaStream_t stream) {
-    const bool kv8 = p.k_scale != nullptr;
-    cudaError_t e;
-    if (p.head_dim <= 64)
-        e = kv8 ? launch_one<64, true>(p, tmap_k, tmap_v, stream)
-                : launch_one<64, false>(p, tmap_k, tmap_v, stream);
-    else if (p.head_dim <= 128)
-        e = kv8 ? launch_one<128, true>(p, tmap_k, tmap_v, stream)
-                : launch_one<128, false>(p, tmap_k, tmap_v, stream);
-    else
-        e = kv8 ? launch_one<256, true>(p, tmap_k, tmap_v, stream)
-                : launch_one<256, false>(p, tmap_k, tmap_v, stream);
+    cudaError_t e = p.k_scale ? launch_kv<true>(p, tmap_k, tmap_v, stream)
+                              : launch_kv<false>(p, tmap_k, tmap_v, stream);
     if (e != cudaSuccess || p.num_parts == 1) return e;
     constexpr int kHeads = kMergeThreads / 32;
     return launch_pdl(tree_merge_kernel,
