@@ -80,10 +80,13 @@ pkv_status pool_map(CUtensorMap *map, const void *base, const pkv_cache_desc &c)
                          w * e == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Partitions of the tree attention: `partition_size` keys each when given,
-// else as many as give about kTreeCtas CTAs, but not below kMinTreePart keys.  A
-// fixed count, so that the workspace of a problem does not depend on the device.
-constexpr int kTreeTile = 128, kMaxDraft = 256, kTreeCtas = 608, kMinTreePart = 256;
+// Partitions of the tree attention: `partition_size` keys each when given, else
+// chosen: with u CTAs per partition on kTreeSms SMs and n partitions of t
+// 128-key tiles, (u n / SMs + 1) rounds of t + kTreeFixed tiles' time are
+// about what the launch takes (a CTA's start and end cost some tiles' time, and
+// the last round is half empty); the n with the least is taken.  Fixed
+// counts, so that the workspace of a problem does not depend on the device.
+constexpr int kTreeTile = 128, kMaxDraft = 256, kTreeSms = 152, kTreeFixed = 6;
 
 struct TreeSplit {
     int part, row_tiles;
@@ -102,11 +105,20 @@ TreeSplit tree_split(int batch, int Hq, int Hkv, int D, int max_q, int64_t total
     s.part = partition_size;
     if (s.part == 0) {
         // row tiles go two to a CTA (one at head size 256)
-        const int64_t units = (int64_t)batch * Hkv * (D > 128 ? s.row_tiles : (s.row_tiles + 1) / 2);
-        const int64_t want = (kTreeCtas + units - 1) / units;
-        int64_t part = (span + want - 1) / want;
-        part = (part + kTreeTile - 1) / kTreeTile * kTreeTile;
-        s.part = (int)(part < kMinTreePart ? kMinTreePart : part);
+        const int64_t units =
+            (int64_t)batch * Hkv * (D > 128 ? s.row_tiles : (s.row_tiles + 1) / 2);
+        const int64_t tiles = (span + kTreeTile - 1) / kTreeTile;
+        int64_t best = tiles < 1 ? 1 : tiles;
+        double best_cost = 1e300;
+        for (int64_t n = 1; n <= 64 && n <= tiles; ++n) {
+            const int64_t t = (tiles + n - 1) / n;
+            const double cost = ((double)(units * n) / kTreeSms + 1.0) * (double)(t + kTreeFixed);
+            if (cost < best_cost) {
+                best_cost = cost;
+                best = t;
+            }
+        }
+        s.part = (int)(best * kTreeTile);
     }
     s.num_parts = ((int64_t)max_len + s.part - 1) / s.part;
     if (window_left >= 0) {

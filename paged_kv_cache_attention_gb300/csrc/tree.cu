@@ -208,8 +208,35 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         return;
     }
 
-    // ---- set-up: barriers, TMEM, Q tile, depths
-    if (threadIdx.x == 0) {
+    // ---- set-up: barriers, TMEM, depths; the first loads of the Q rows (softmax
+    // warps, 32 rows each, LPR lanes per row) and of the page ids are in flight
+    // meanwhile: beside 150 streaming SMs a load takes microseconds
+    const int BS = p.block_size, npg = kTile / BS;
+    const int32_t *bt = p.block_table + (int64_t)b * p.max_blocks_per_seq;
+    const int pg_first = tok_lo / BS, pg_last = (tok_hi - 1) / BS;
+    // lane l < npg: the id of page l of tile j, `none` where no key is attended
+    auto page_id = [&](int j, int none) {
+        const int pg = (kt0 + j) * npg + lane;
+        return lane < npg && pg >= pg_first && pg <= pg_last ? bt[pg] : none;
+    };
+    int id = page_id(0, warp < 4 * X ? 0 : -1);
+    constexpr int LPR = T / 8 < 32 ? T / 8 : 32, RPS = 32 / LPR;  // lanes per row, rows per step
+    constexpr int STEPS = 32 / RPS < 16 ? 32 / RPS : 16;          // steps in flight
+    const int64_t unit = warp < 4 * X && (int)threadIdx.x < nrows ? row_unit(threadIdx.x) : 0;
+    const __nv_bfloat16 *qc = static_cast<const __nv_bfloat16 *>(p.q) + (lane % LPR) * 8;
+    uint4 qv[STEPS];
+    auto load_q = [&](int s0) {
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) {
+            const int rr = (s0 + k) * RPS + lane / LPR;
+            const int64_t u = __shfl_sync(0xffffffffu, unit, rr);
+            qv[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (warp * 32 + rr < nrows && (lane % LPR) * 8 < Dh)
+                qv[k] = __ldg(reinterpret_cast<const uint4 *>(qc + u * Dh));
+        }
+    };
+    if (warp < 4 * X) load_q(0);
+    if (threadIdx.x == 32 * C::W_TMA) {
         constexpr int kFill = KV8 ? C::DW : 1;  // arrivals that fill a tile
         for (int i = 0; i < C::KB; ++i) {
             mbar_init(bar(C::B_KFULL + i), kFill);
@@ -242,7 +269,8 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         tc::tmem_alloc(base + C::OFF_MISC, C::TMEM);
         tc::tmem_relinquish();
     }
-    if (p.depth && (p.window_left >= 0 || p.alibi)) {
+    const bool positions = p.depth && (p.window_left >= 0 || p.alibi);
+    if (positions) {
         __syncthreads();  // s_maxdepth is zero
         for (int i = threadIdx.x; i < rq.q_len; i += C::THREADS) {
             const int d = min(max(p.depth[rq.q_start + i], 0), 65535);
@@ -251,15 +279,21 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         }
     }
     tc::fence_before_sync();
-    __syncthreads();
+    if (warp == C::W_TMA && !positions) {
+        // the barriers are this warp's own work: it starts loading, and only
+        // announces that they are there
+        __syncwarp();
+        asm volatile("barrier.cta.arrive 1, %0;" ::"n"(C::THREADS) : "memory");
+    } else if (!positions) {
+        asm volatile("barrier.cta.sync 1, %0;" ::"n"(C::THREADS) : "memory");
+    } else {
+        __syncthreads();
+    }
     tc::fence_after_sync();
-    const uint32_t tmem = misc[0];
+    const uint32_t tmem = warp == C::W_TMA ? 0u : misc[0];
 
-    const int BS = p.block_size, npg = kTile / BS;
-    const int32_t *bt = p.block_table + (int64_t)b * p.max_blocks_per_seq;
-    const int pg_first = tok_lo / BS, pg_last = (tok_hi - 1) / BS;
     // every row sees keys [wfull, ctx)
-    const int wfull = p.window_left < 0
+    const int wfull = p.window_left < 0 || !positions
                           ? 0
                           : (int)max((long long)rq.ctx + *s_maxdepth - p.window_left, 0LL);
     auto partial = [&](int i) {  // some row does not see some key of tile i
@@ -273,11 +307,6 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         const int oob = p.hnd ? (int)(p.num_blocks * p.num_kv_heads)
                               : (int)(p.num_blocks * BS);
         const int cy = p.hnd ? 0 : g;
-        auto page_id = [&](int i) {  // lane l < npg: page l of tile i, -1: not attended
-            const int pg = (kt0 + i) * npg + lane;
-            return lane < npg && pg >= pg_first && pg <= pg_last ? bt[pg] : -1;
-        };
-        int id = page_id(0);
         bool alive = true;
         int nk = 0, nv = 0, nfix = 0;
         for (int i = 0; i < ntiles && alive; ++i) {
@@ -292,7 +321,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                 }
             }
             const int id_now = id;
-            if (i + 1 < ntiles) id = page_id(i + 1);
+            if (i + 1 < ntiles) id = page_id(i + 1, -1);
             if constexpr (!KV8) {
                 const int ks = i % C::KB, vs = i % C::VB;
                 // lane -> (page, 64-dim half)
@@ -418,18 +447,22 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         const uint64_t dq0 = tc::smem_desc_sw128(base + C::OFF_Q, 16, 1024);
         const uint64_t dk0 = tc::smem_desc_sw128(base + C::OFF_K, 16, 1024);
         const uint64_t dv0 = tc::smem_desc_sw128(base + C::OFF_V, C::HALF, 1024);
-        bool alive = true;
-        int sj = 0, sx = 0;  // key tile and row tile of the next S
-        auto issue_s = [&](int n) {
-            const int s = sj % C::KB;
-            if (sx == 0)
-                alive = warp_wait_bounded(bar(C::B_KFULL + s), (uint32_t)(sj / C::KB) & 1u,
-                                          p.dev_error, s_abort);
-            if (!alive) return;
-            tc::fence_after_sync();
-            if (lane == 0) {
+        // One thread issues, and spends as little as it can between two products:
+        // the tensor pipe runs dry meanwhile (buffer indexes and phases are
+        // counted, not divided out; K's barrier is looked at ahead of need).
+        if (lane == 0) {
+            auto wait = [&](int i, uint32_t phase) {
+                return mbar_wait_bounded(bar(i), phase, p.dev_error, s_abort);
+            };
+            int sx = 0, ks = 0;      // row tile and K buffer of the next S
+            uint32_t kph = 0;        // and that buffer's phase
+            bool k_ready = false;
+            auto issue_s = [&](int n) {
+                if (!k_ready && !wait(C::B_KFULL + ks, kph)) return false;
+                k_ready = true;
+                tc::fence_after_sync();
                 const uint64_t dq = dq0 + (uint64_t)((sx * C::TILE) >> 4);
-                const uint64_t dk = dk0 + (uint64_t)((s * C::TILE) >> 4);
+                const uint64_t dk = dk0 + (uint64_t)((ks * C::TILE) >> 4);
                 const uint32_t d = tmem + (n & 1) * 128;
                 if constexpr (T == 128) {
                     tc::mma_ss8<C::HALF>(d, dq, dk, idS, 0u);
@@ -443,83 +476,70 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                         }
                 }
                 tc::commit(bar(C::B_SFULL + (n & 1)));
-                if (sx + 1 == nx) tc::commit(bar(C::B_KEMPTY + s));
-            }
-            __syncwarp();
-            if (++sx == nx) {
-                sx = 0;
-                ++sj;
-            }
-        };
-        const int total = ntiles * nx;
-        alive = warp_wait_bounded(bar(C::B_Q), 0, p.dev_error, s_abort);
-        if (alive) issue_s(0);
-        if (total > 1 && alive) issue_s(1);
-        int j = 0, x = 0;
-        for (int n = 0; n < total && alive; ++n) {
-            const int s = j % C::VB;
-            alive = warp_wait_bounded(bar(C::B_PFULL + (n & 1)), (uint32_t)(n >> 1) & 1u,
-                                      p.dev_error, s_abort);
-            if (alive && x == 0)
-                alive = warp_wait_bounded(bar(C::B_VFULL + s), (uint32_t)(j / C::VB) & 1u,
-                                          p.dev_error, s_abort);
-            if (!alive) break;
-            tc::fence_after_sync();
-            if (lane == 0) {
-                const uint64_t dv = dv0 + (uint64_t)((s * C::TILE) >> 4);
+                if (++sx == nx) {
+                    tc::commit(bar(C::B_KEMPTY + ks));
+                    sx = 0;
+                    k_ready = false;
+                    if (++ks == C::KB) {
+                        ks = 0;
+                        kph ^= 1u;
+                    }
+                }
+                return true;
+            };
+            const int total = ntiles * nx;
+            bool alive = wait(C::B_Q, 0) && issue_s(0) && (total == 1 || issue_s(1));
+            int j = 0, x = 0, vs = 0;
+            uint32_t vph = 0;
+            for (int n = 0; n < total && alive; ++n) {
+                alive = wait(C::B_PFULL + (n & 1), (uint32_t)(n >> 1) & 1u) &&
+                        (x > 0 || wait(C::B_VFULL + vs, vph));
+                if (!alive) break;
+                tc::fence_after_sync();
+                const uint64_t dv = dv0 + (uint64_t)((vs * C::TILE) >> 4);
                 tc::mma_ts8(tmem + 256 + x * T, tmem + (n & 1) * 128, dv, idO, j > 0 ? 1u : 0u);
-                if (x + 1 == nx) tc::commit(bar(C::B_VEMPTY + s));
-                if (j + 1 == ntiles) tc::commit(bar(C::B_O + x));
+                const bool last = j + 1 == ntiles;
+                const int ox = x;
+                if (++x == nx) {
+                    tc::commit(bar(C::B_VEMPTY + vs));
+                    x = 0;
+                    ++j;
+                    if (++vs == C::VB) {
+                        vs = 0;
+                        vph ^= 1u;
+                    }
+                }
+                if (last) tc::commit(bar(C::B_O + ox));
+                if (n + 2 < total) alive = issue_s(n + 2);
             }
-            __syncwarp();
-            if (n + 2 < total) issue_s(n + 2);
-            if (++x == nx) {
-                x = 0;
-                ++j;
+            if (!alive) {  // let the products in flight finish (bounded) before TMEM goes
+                tc::commit(bar(C::B_O));
+                mbar_wait_bounded(bar(C::B_O), 0, p.dev_error);
             }
         }
-        if (!alive) {  // let the products in flight finish (bounded) before TMEM goes
-            if (lane == 0) tc::commit(bar(C::B_O));
-            __syncwarp();
-            warp_wait_bounded(bar(C::B_O), 0, p.dev_error);
-        }
+        __syncwarp();
     } else if (warp < 4 * X) {
         // ------------------------------------------------------------ softmax
         const int x = warp >> 2;             // row tile
         const int r = threadIdx.x;           // row of the CTA; TMEM lane r % 128
         const bool warp_on = warp * 32 < nrows;
         const bool row_on = r < nrows;
-        const int64_t unit = row_on ? row_unit(r) : 0;
         const int node = row_on ? (rt * kTile + r) / G : 0;
         const int head = row_on ? g * G + (rt * kTile + r) % G : 0;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_o = tmem + 256 + x * T + lane_base;
-        // ---- this warp's 32 rows of Q into shared memory (rows past the last:
-        // zeros), 16 lanes per 128 dims of a row; the loads of eight steps are in
-        // flight at once
+        // ---- this warp's rows of Q into shared memory (rows past the last: zeros)
         float rowf = fabsf(p.scale_log2);  // score = S * rowf
         {
             const uint32_t sq = base + C::OFF_Q + x * C::TILE;
             const uint32_t neg = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // its sign goes into q
-            constexpr int LPR = T / 8 < 32 ? T / 8 : 32, RPS = 32 / LPR;  // lanes per row
-            constexpr int STEPS = 32 / RPS, BATCH = 8;
-            const int c = lane % LPR, rsub = lane / LPR;
+            const int c = lane % LPR;
 #pragma unroll 1
-            for (int s0 = 0; s0 < STEPS; s0 += BATCH) {
-                uint4 v[BATCH];
+            for (int s0 = 0; s0 < 32 / RPS; s0 += STEPS) {
+                if (s0 > 0) load_q(s0);
 #pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
-                    const int rr = warp * 32 + (s0 + k) * RPS + rsub;
-                    v[k] = make_uint4(0u, 0u, 0u, 0u);
-                    if (rr < nrows && c * 8 < Dh)
-                        v[k] = __ldg(reinterpret_cast<const uint4 *>(
-                                         static_cast<const __nv_bfloat16 *>(p.q) +
-                                         row_unit(rr) * Dh) +
-                                     c);
-                }
-#pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
-                    uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                for (int k = 0; k < STEPS; ++k) {
+                    uint32_t w[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
                     if constexpr (KV8) {
                         // in f16, times a power of two that brings the row's largest value
                         // to 2^14..2^15 (exact down to 2^-28 of it)
@@ -541,7 +561,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                         if (lane / RPS == s0 + k)
                             rowf *= __uint_as_float((uint32_t)(127 + Er - 14) << 23);
                     }
-                    const int rr = (warp & 3) * 32 + (s0 + k) * RPS + rsub;
+                    const int rr = (warp & 3) * 32 + (s0 + k) * RPS + lane / LPR;
                     st_shared16(sq + (c >> 3) * C::HALF + sw128(rr, c & 7), w[0] ^ neg,
                                 w[1] ^ neg, w[2] ^ neg, w[3] ^ neg);
                 }
@@ -554,21 +574,15 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         // scale.  m_ref follows the row's largest score (there plus that scale
         // over 2^10, so that f16 holds the product); O and l share it.
         float m_ref = kNegInf, l = 0.f;
-        const bool positions = p.window_left >= 0 || p.alibi;  // depths are loaded
         bool alive = true;
         int nfix = 0;
-        auto page_id = [&](int j) {
-            const int pg = (kt0 + j) * npg + lane;
-            return lane < npg && pg >= pg_first && pg <= pg_last ? bt[pg] : 0;
-        };
-        int id = warp_on ? page_id(0) : 0;
         for (int j = 0; j < ntiles && x < nx; ++j) {
             const int n = j * nx + x;
             const uint32_t t_s = tmem + (n & 1) * 128 + lane_base;
             const bool fix = partial(j);
             const uint32_t badpg =
                 __ballot_sync(0xffffffffu, id < 0 || (int64_t)id >= p.num_blocks);
-            if (warp_on && j + 1 < ntiles) id = page_id(j + 1);
+            if (warp_on && j + 1 < ntiles) id = page_id(j + 1, 0);
             const bool general = fix || badpg != 0 || p.alibi != nullptr;
             alive = warp_wait_bounded(bar(C::B_SFULL + (n & 1)), (uint32_t)(n >> 1) & 1u,
                                       p.dev_error, s_abort);
@@ -787,17 +801,18 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             }
             __syncwarp();
             const int rows = min(nrows - warp * 32, 32);
-            constexpr int RPS = CPR < 32 ? 32 / CPR : 1;       // rows per step
+            constexpr int RPI = CPR < 32 ? 32 / CPR : 1;       // rows per step
             constexpr int CPL = CPR > 32 ? CPR / 32 : 1;       // chunks per lane
 #pragma unroll 4
-            for (int r0 = 0; r0 < rows; r0 += RPS) {
+            for (int r0 = 0; r0 < 32; r0 += RPI) {
+                if (r0 >= rows) break;
                 const int rr = r0 + lane / CPR;
-                const int64_t u = row_unit(min(warp * 32 + rr, nrows - 1));
+                const int64_t u = __shfl_sync(0xffffffffu, unit, rr);
 #pragma unroll
                 for (int k = 0; k < CPL; ++k) {
                     const int c = lane % CPR + 32 * k;
                     const float4 o = *reinterpret_cast<const float4 *>(
-                        stage + (rr & 31) * T * 4 + ((c ^ rr) % CPR) * 16);
+                        stage + rr * T * 4 + ((c ^ rr) % CPR) * 16);
                     if (rr >= rows || c * 4 >= Dh) continue;
                     if (p.num_parts > 1)
                         *reinterpret_cast<float4 *>(
@@ -818,11 +833,6 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         const int w = warp - C::W_CVT;
         bool alive = true;
         int nfix = 0;
-        auto page_id = [&](int j) {  // lane l < npg: page l of tile j, -1: not attended
-            const int pg = (kt0 + j) * npg + lane;
-            return lane < npg && pg >= pg_first && pg <= pg_last ? bt[pg] : -1;
-        };
-        int id = page_id(0);
         for (int j = 0; j < ntiles && alive; ++j) {
             const int k0 = (kt0 + j) * kTile;
             // lane: rows 4 lane .. 4 lane + 3 of the tile, all in one page
@@ -831,7 +841,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             const uint32_t in4 = idok ? range_bits(tok_lo - k0 - 4 * lane, tok_hi - k0 - 4 * lane) &
                                             15u
                                       : 0u;
-            if (j + 1 < ntiles) id = page_id(j + 1);
+            if (j + 1 < ntiles) id = page_id(j + 1, -1);
             const bool fix = partial(j);
             uint32_t kmax = 1;
 #pragma unroll 1
