@@ -486,8 +486,9 @@ PKV_API pkv_status pkv_gather_cache_fp8(void *key, void *value, const void *k_ca
  * everything else (masks, sink, ALiBi, partitions, lse, workspace of
  * pkv_paged_decode_workspace_size bytes for the same arguments) as there, but
  * for partition_size 0: the partition is chosen from the shapes (512 to 2048
- * tokens).  k_scale and v_scale are 16-byte aligned.  Head sizes 64/80/96/112/128/256, at most 16 query heads per
- * kv head.
+ * tokens).  With max_seqlen within one partition the workspace may be NULL.
+ * k_scale and v_scale are 16-byte aligned.  Head sizes 64/80/96/112/128/256, at
+ * most 16 query heads per kv head.
  */
 PKV_API pkv_status pkv_paged_decode_fp8(void *out, const void *q, const void *k_cache,
                                         const void *v_cache, const uint8_t *k_scale,
@@ -532,7 +533,8 @@ PKV_API pkv_status pkv_qk_norm_rope_reshape_and_cache(
     const void *k_weight, int weight_f32, float eps, const float *cos_sin, int max_position,
     int rotary_dim, int is_neox_style, int32_t *dev_error, void *stream);
 
-/* Workspace bytes pkv_paged_tree_attention needs (its split-KV partials). */
+/* Workspace bytes pkv_paged_tree_attention needs (its split-KV partials); 256
+ * when it runs as one partition, which uses none (the workspace may be NULL). */
 PKV_API size_t pkv_paged_tree_attention_workspace_size(int batch, int num_qo_heads,
                                                        int num_kv_heads, int head_dim,
                                                        int64_t total_q, int max_seqlen_q,

@@ -105,6 +105,8 @@ def build(force: bool = False) -> str:
 def load_library(path: Optional[str] = None):
     """Load libpkv.so (building it first if it is absent) and declare the ABI."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -618,8 +620,9 @@ def paged_decode_noalloc(q, k_cache, v_cache, block_table, cache_seqlens, max_se
 
 # ---------------------------------------------------------------------------
 # the 8-bit cache, the q/k norm and the attention of drafted tokens.  These
-# calls are short on the GPU in a decode step, so their checks are written to
-# cost little: one test per tensor, the reason worked out only on failure.
+# calls are short on the GPU in a decode step, so a call first asks whether
+# its arguments are of the usual kind in one expression; only if not are they
+# checked one by one, which finds the reason or lets them pass.
 # ---------------------------------------------------------------------------
 
 def _cuda_index(name, t) -> int:
@@ -648,6 +651,14 @@ def _arg_shape(name, t, dtype, shape, dev: int):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
+def _arg_vector(name, t, dtype, n: int, dev: int):
+    """A contiguous vector of n entries."""
+    if (t.dtype is dtype and t.get_device() == dev and t.dim() == 1 and t.size(0) == n
+            and t.is_contiguous()):
+        return
+    _arg_shape(name, t, dtype, (n,), dev)
+
+
 def _error_word(dev_error, dev: int):
     """The address of the caller's error word, or None."""
     if dev_error is None:
@@ -657,16 +668,44 @@ def _error_word(dev_error, dev: int):
     return dev_error.data_ptr()
 
 
-_descs = {}
+_descs = {}         # what a pool's shape says (building a CacheDesc costs as much as a check)
+_scale_shapes = {}  # and the shape of the scales that go with it
 
 
 def _desc(*fields) -> CacheDesc:
-    """The CacheDesc of a shape (kept: building one costs as much as a check)."""
+    """The CacheDesc of a shape."""
     d = _descs.get(fields)
     if d is None:
         if len(_descs) > 4096:
             _descs.clear()
         d = _descs[fields] = CacheDesc(*fields)
+    return d
+
+
+def _fp8_pools(k_cache, v_cache, k_scale, v_scale, layout: str, dev: int) -> CacheDesc:
+    """Checks the pools and scales of the 8-bit cache."""
+    ty = _types()
+    if (k_scale is not None and v_scale is not None
+            and k_cache.dtype is ty.e4m3 and v_cache.dtype is ty.e4m3
+            and k_scale.dtype is ty.u8 and v_scale.dtype is ty.u8
+            and k_cache.get_device() == v_cache.get_device() == k_scale.get_device()
+            == v_scale.get_device() == dev
+            and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and k_scale.is_contiguous() and v_scale.is_contiguous()):
+        shape = k_cache.shape
+        key = (shape, layout)
+        d = _descs.get(key)
+        if d is not None and v_cache.shape == shape and \
+                k_scale.shape == v_scale.shape == _scale_shapes[key]:
+            return d
+    _require(k_scale is not None, "k_scale is needed for an 8-bit cache")
+    _require(v_scale is not None, "v_scale is needed for an 8-bit cache")
+    d = _pools(k_cache, v_cache, k_scale, v_scale, None, layout, dev)
+    if len(_scale_shapes) > 4096:
+        _descs.clear()
+        _scale_shapes.clear()
+    _scale_shapes[(k_cache.shape, layout)] = k_scale.shape
+    _descs[(k_cache.shape, layout)] = d
     return d
 
 
@@ -700,48 +739,59 @@ def _pools(k_cache, v_cache, k_scale, v_scale, dtype, layout: str, dev: int) -> 
 def _token_rows(name, t, dtype, tokens: int, heads: int, head_dim: int, dev: int) -> int:
     """Checks [tokens, heads, head_dim] rows whose heads are contiguous; returns
     the elements between tokens (a slice of a fused projection keeps its own)."""
-    if t.dtype is not dtype or t.get_device() != dev or tuple(t.shape) != (tokens, heads,
-                                                                            head_dim):
-        _arg(name, t.new_empty(t.shape), dtype, 3, dev)
-        raise ValueError(f"{name} must be [{tokens}, {heads}, {head_dim}], got {list(t.shape)}")
-    if tokens <= 1 or t.is_contiguous():
-        _require(t.is_contiguous(), f"{name}: the heads of a token must be contiguous")
-        return heads * head_dim
-    _require(t[0].is_contiguous(), f"{name}: the heads of a token must be contiguous")
-    return t.stride(0)
+    if (t.dtype is dtype and t.get_device() == dev and t.dim() == 3 and t.size(0) == tokens
+            and t.size(1) == heads and t.size(2) == head_dim):
+        if t.is_contiguous():
+            return heads * head_dim
+        if t.stride(2) == 1 and (heads == 1 or t.stride(1) == head_dim):
+            return t.stride(0) if tokens > 1 else heads * head_dim
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    _require(t.get_device() == dev, f"{name} must be on the same device as the other tensors")
+    _require(t.dtype is dtype, f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be [{tokens}, {heads}, {head_dim}], got {list(t.shape)}")
 
 
-class _launch_on:
-    """The device ``dev`` made current, and with a ``stream`` that stream, so
-    that what a call allocates belongs to the stream its kernels run on.  The
-    value of the context is the stream's handle."""
+class _Types:
+    """torch and the dtypes the checks compare with, looked up once."""
+    torch = bf16 = f32 = i32 = i64 = u8 = e4m3 = None
+    device = raw_stream = None  # the current device, and a device's current stream handle
 
-    def __init__(self, dev: int, stream):
-        self.dev, self.stream, self.ctx = dev, stream, None
 
-    def __enter__(self) -> int:
-        torch = _torch()
-        if self.dev < 0:
-            return _stream_handle(self.stream)
-        if self.stream is not None:
-            self.ctx = torch.cuda.stream(self.stream)
-        elif self.dev != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(self.dev)
-        else:
-            return torch.cuda.current_stream(self.dev).cuda_stream
-        self.ctx.__enter__()
-        return torch.cuda.current_stream(self.dev).cuda_stream
+def _types():
+    if _Types.torch is None:
+        import torch
+        _Types.bf16, _Types.f32, _Types.i32 = torch.bfloat16, torch.float32, torch.int32
+        _Types.i64, _Types.u8, _Types.e4m3 = torch.int64, torch.uint8, torch.float8_e4m3fn
+        _Types.device = torch.cuda.current_device
+        _Types.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        _Types.torch = torch
+    return _Types
 
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+
+def _on_stream(dev: int, stream, call):
+    """call(stream handle), with the device of the tensors current, and with a
+    ``stream`` that stream, so that what the call allocates belongs to the
+    stream its kernels run on."""
+    if dev < 0:
+        return call(_stream_handle(stream))
+    t = _types()
+    if stream is not None:
+        with t.torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+    if t.device() != dev:
+        with t.torch.cuda.device(dev):
+            return call(t.raw_stream(dev))
+    return call(t.raw_stream(dev))
 
 
 def _scratch(nbytes: int, dev: int, device, workspace):
     """(address, bytes) of the workspace, and the tensor that holds it."""
-    torch = _torch()
     if workspace is None:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        if nbytes == 0:
+            return None, 0, None
+        ty = _types()
+        ws = ty.torch.empty(nbytes, dtype=ty.u8, device=device)
         return ws.data_ptr(), nbytes, ws
     size = workspace.numel() * workspace.element_size()
     if workspace.get_device() != dev or not workspace.is_contiguous() or size < nbytes:
@@ -770,22 +820,23 @@ def reshape_and_cache_fp8(key, value, k_cache, v_cache, k_scale, v_scale, slot_m
     smallest that keeps max|x| within 448.  A row with a NaN or an infinity is
     stored as byte 255 and reads as NaN.  slot_mapping: [T] int64, negative =
     skip; dev_error receives PKV_DEVERR_SLOT for slots outside the pool."""
-    torch = _torch()
     dev = _cuda_index("key", key)
-    _require(k_scale is not None, "k_scale is needed for an 8-bit cache")
-    desc = _pools(k_cache, v_cache, k_scale, v_scale, None, layout, dev)
-    dt = _dtype_code(key.dtype)
-    T = key.shape[0]
-    ks = _token_rows("key", key, key.dtype, T, desc.num_kv_heads, desc.head_dim, dev)
-    vs = _token_rows("value", value, key.dtype, T, desc.num_kv_heads, desc.head_dim, dev)
-    _arg_shape("slot_mapping", slot_mapping, torch.int64, (T,), dev)
+    desc = _fp8_pools(k_cache, v_cache, k_scale, v_scale, layout, dev)
+    dtype, T = key.dtype, key.size(0)
+    dt = _dtype_code(dtype)
+    ks = _token_rows("key", key, dtype, T, desc.num_kv_heads, desc.head_dim, dev)
+    vs = _token_rows("value", value, dtype, T, desc.num_kv_heads, desc.head_dim, dev)
+    _arg_vector("slot_mapping", slot_mapping, _types().i64, T, dev)
     err = _error_word(dev_error, dev)
     lib = load_library()
-    with _launch_on(dev, stream) as handle:
-        st = lib.pkv_reshape_and_cache_fp8(
+
+    def call(handle):
+        return lib.pkv_reshape_and_cache_fp8(
             key.data_ptr(), value.data_ptr(), ks, vs, dt, k_cache.data_ptr(), v_cache.data_ptr(),
             k_scale.data_ptr(), v_scale.data_ptr(), slot_mapping.data_ptr(), T, desc, err, handle)
-    _check("pkv_reshape_and_cache_fp8", st)
+    st = _on_stream(dev, stream, call)
+    if st:
+        _check("pkv_reshape_and_cache_fp8", st)
 
 
 def gather_cache_fp8(k_cache, v_cache, k_scale, v_scale, block_table, cu_seq_lens_k,
@@ -797,47 +848,47 @@ def gather_cache_fp8(k_cache, v_cache, k_scale, v_scale, block_table, cu_seq_len
     int32; cu_seq_lens_k: [B+1] int32; total_k: host int, the rows of the
     outputs.  Rows of no request are left as they were (uninitialised in
     outputs allocated here)."""
-    torch = _torch()
+    ty = _types()
     dev = _cuda_index("k_cache", k_cache)
-    _require(k_scale is not None, "k_scale is needed for an 8-bit cache")
-    desc = _pools(k_cache, v_cache, k_scale, v_scale, None, layout, dev)
-    _arg("cu_seq_lens_k", cu_seq_lens_k, torch.int32, 1, dev)
-    _arg("block_table", block_table, torch.int32, 2, dev)
-    B = cu_seq_lens_k.shape[0] - 1
-    _require(B >= 0 and block_table.shape[0] == B, "block_table must have one row per request")
+    desc = _fp8_pools(k_cache, v_cache, k_scale, v_scale, layout, dev)
+    _arg("cu_seq_lens_k", cu_seq_lens_k, ty.i32, 1, dev)
+    _arg("block_table", block_table, ty.i32, 2, dev)
+    B = cu_seq_lens_k.size(0) - 1
+    _require(B >= 0 and block_table.size(0) == B, "block_table must have one row per request")
     total_k = int(total_k)
     _require(total_k >= 0, "total_k must not be negative")
     shape = (total_k, desc.num_kv_heads, desc.head_dim)
-    for name, t in (("key", key), ("value", value)):
-        if t is not None:
-            _arg_shape(name, t, torch.bfloat16, shape, dev)
+    if key is not None:
+        _arg_shape("key", key, ty.bf16, shape, dev)
+    if value is not None:
+        _arg_shape("value", value, ty.bf16, shape, dev)
     err = _error_word(dev_error, dev)
     lib = load_library()
-    with _launch_on(dev, stream) as handle:
-        if key is None:
-            key = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
-        if value is None:
-            value = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
-        st = lib.pkv_gather_cache_fp8(
-            key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+
+    def call(handle):
+        k = ty.torch.empty(shape, dtype=ty.bf16, device=k_cache.device) if key is None else key
+        v = ty.torch.empty(shape, dtype=ty.bf16, device=k_cache.device) if value is None else value
+        return k, v, lib.pkv_gather_cache_fp8(
+            k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             k_scale.data_ptr(), v_scale.data_ptr(), desc, block_table.data_ptr(),
-            block_table.shape[1], cu_seq_lens_k.data_ptr(), B, total_k, err, handle)
-    _check("pkv_gather_cache_fp8", st)
+            block_table.size(1), cu_seq_lens_k.data_ptr(), B, total_k, err, handle)
+    key, value, st = _on_stream(dev, stream, call)
+    if st:
+        _check("pkv_gather_cache_fp8", st)
     return key, value
 
 
-def _attention_extras(sink, alibi_slopes, out, lse, q, dev: int):
+def _attention_extras(sink, alibi_slopes, out, lse, q, rows: int, Hq: int, dev: int):
     """Checks what both attention calls take beside q and the pools."""
-    f32 = _torch().float32
-    rows, Hq = q.shape[0], q.shape[1]
+    ty = _types()
     if sink is not None:
-        _arg_shape("sink", sink, f32, (Hq,), dev)
+        _arg_vector("sink", sink, ty.f32, Hq, dev)
     if alibi_slopes is not None:
-        _arg_shape("alibi_slopes", alibi_slopes, f32, (Hq,), dev)
+        _arg_vector("alibi_slopes", alibi_slopes, ty.f32, Hq, dev)
     if out is not None:
-        _arg_shape("out", out, q.dtype, tuple(q.shape), dev)
+        _arg_shape("out", out, ty.bf16, tuple(q.shape), dev)
     if lse is not None:
-        _arg_shape("lse", lse, f32, (rows, Hq), dev)
+        _arg_shape("lse", lse, ty.f32, (rows, Hq), dev)
 
 
 def paged_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_seqlens,
@@ -849,34 +900,36 @@ def paged_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_s
     bf16 [B, Hq, D]; everything else as paged_decode (workspace of
     paged_decode_workspace_size bytes for the same arguments), but for
     partition_size 0, which lets the library choose (512 or more)."""
-    torch = _torch()
+    ty = _types()
     dev = _cuda_index("q", q)
-    _require(k_scale is not None, "k_scale is needed for an 8-bit cache")
-    desc = _pools(k_cache, v_cache, k_scale, v_scale, None, layout, dev)
-    _arg("q", q, torch.bfloat16, 3, dev)
+    desc = _fp8_pools(k_cache, v_cache, k_scale, v_scale, layout, dev)
+    _arg("q", q, ty.bf16, 3, dev)
     B, Hq, D = q.shape
     _require(D == desc.head_dim, "head_dim of q and cache differ")
-    _arg("block_table", block_table, torch.int32, 2, dev)
-    _arg("cache_seqlens", cache_seqlens, torch.int32, 1, dev)
-    _require(block_table.shape[0] == B and cache_seqlens.shape[0] == B,
-             "block_table / cache_seqlens batch mismatch")
-    _attention_extras(sink, alibi_slopes, out, lse, q, dev)
+    _arg("block_table", block_table, ty.i32, 2, dev)
+    _arg_vector("cache_seqlens", cache_seqlens, ty.i32, B, dev)
+    _require(block_table.size(0) == B, "block_table / cache_seqlens batch mismatch")
+    _attention_extras(sink, alibi_slopes, out, lse, q, B, Hq, dev)
     err = _error_word(dev_error, dev)
     scale = float(sm_scale) if sm_scale is not None else D ** -0.5
     max_seqlen, window_left, partition_size = int(max_seqlen), int(window_left), int(partition_size)
-    need = _decode_ws(B, Hq, D, max_seqlen, partition_size, window_left)
+    # one partition needs no workspace
+    need = 0 if max_seqlen <= (partition_size or 512) else \
+        _decode_ws(B, Hq, D, max_seqlen, partition_size, window_left)
     lib = load_library()
-    with _launch_on(dev, stream) as handle:
-        if out is None:
-            out = torch.empty_like(q)
+
+    def call(handle):
+        o = ty.torch.empty_like(q) if out is None else out
         ws, ws_bytes, held = _scratch(need, dev, q.device, workspace)
-        st = lib.pkv_paged_decode_fp8(
-            out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        return o, lib.pkv_paged_decode_fp8(
+            o.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             k_scale.data_ptr(), v_scale.data_ptr(), desc, block_table.data_ptr(),
-            block_table.shape[1], cache_seqlens.data_ptr(), max_seqlen, _ptr(sink),
+            block_table.size(1), cache_seqlens.data_ptr(), max_seqlen, _ptr(sink),
             _ptr(alibi_slopes), B, Hq, window_left, scale, partition_size, _ptr(lse), ws,
             ws_bytes, err, handle)
-    _check("pkv_paged_decode_fp8", st)
+    out, st = _on_stream(dev, stream, call)
+    if st:
+        _check("pkv_paged_decode_fp8", st)
     return out
 
 
@@ -895,12 +948,15 @@ def qk_norm_rope_reshape_and_cache(query, key, value, k_cache, v_cache, position
     query_out / key_out, or back in place when these are None.  With k_scale and
     v_scale the pools are the 8-bit cache of reshape_and_cache_fp8, else pools of
     the rows' dtype.  query (with query_out and q_weight) may be None."""
-    torch = _torch()
+    ty = _types()
     dev = _cuda_index("key", key)
     dtype = key.dtype
     dt = _dtype_code(dtype)
-    desc = _pools(k_cache, v_cache, k_scale, v_scale, dtype, layout, dev)
-    D, Hkv, T = desc.head_dim, desc.num_kv_heads, key.shape[0]
+    if k_scale is None and v_scale is None:
+        desc = _pools(k_cache, v_cache, None, None, dtype, layout, dev)
+    else:
+        desc = _fp8_pools(k_cache, v_cache, k_scale, v_scale, layout, dev)
+    D, Hkv, T = desc.head_dim, desc.num_kv_heads, key.size(0)
     ks = _token_rows("key", key, dtype, T, Hkv, D, dev)
     vs = _token_rows("value", value, dtype, T, Hkv, D, dev)
     kos = ks
@@ -913,35 +969,38 @@ def qk_norm_rope_reshape_and_cache(query, key, value, k_cache, v_cache, position
         query_out = q_weight = None
     else:
         _require(query.dim() == 3, "query must be [T, num_qo_heads, head_dim]")
-        Hq = query.shape[1]
+        Hq = query.size(1)
         qs = qos = _token_rows("query", query, dtype, T, Hq, D, dev)
         if query_out is None:
             query_out = query
         else:
             qos = _token_rows("query_out", query_out, dtype, T, Hq, D, dev)
-    _arg_shape("positions", positions, torch.int64, (T,), dev)
-    _arg_shape("slot_mapping", slot_mapping, torch.int64, (T,), dev)
-    _arg("cos_sin", cos_sin, torch.float32, 3, dev)
-    rd = int(rotary_dim) if rotary_dim is not None else 2 * cos_sin.shape[1]
-    _require(cos_sin.shape[1] * 2 == rd and cos_sin.shape[2] == 2,
-             "cos_sin must be [max_position, rotary_dim // 2, 2]")
+    _arg_vector("positions", positions, ty.i64, T, dev)
+    _arg_vector("slot_mapping", slot_mapping, ty.i64, T, dev)
+    _arg("cos_sin", cos_sin, ty.f32, 3, dev)
+    maxpos, half, two = cos_sin.shape
+    rd = int(rotary_dim) if rotary_dim is not None else 2 * half
+    _require(2 * half == rd and two == 2, "cos_sin must be [max_position, rotary_dim // 2, 2]")
     _require(k_weight is not None and (q_weight is not None or query is None),
              "q_weight and k_weight are needed")
-    w32 = k_weight.dtype is torch.float32
-    wd = torch.float32 if w32 else dtype
-    _arg_shape("k_weight", k_weight, wd, (D,), dev)
+    w32 = k_weight.dtype is ty.f32
+    wd = ty.f32 if w32 else dtype
+    _arg_vector("k_weight", k_weight, wd, D, dev)
     if q_weight is not None:
-        _arg_shape("q_weight", q_weight, wd, (D,), dev)
+        _arg_vector("q_weight", q_weight, wd, D, dev)
     err = _error_word(dev_error, dev)
     lib = load_library()
-    with _launch_on(dev, stream) as handle:
-        st = lib.pkv_qk_norm_rope_reshape_and_cache(
+
+    def call(handle):
+        return lib.pkv_qk_norm_rope_reshape_and_cache(
             _ptr(query), key.data_ptr(), value.data_ptr(), qs, ks, vs, dt, _ptr(query_out),
             key_out.data_ptr(), qos, kos, k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale),
             _ptr(v_scale), positions.data_ptr(), slot_mapping.data_ptr(), T, Hq, desc,
-            _ptr(q_weight), k_weight.data_ptr(), w32, float(eps), cos_sin.data_ptr(),
-            cos_sin.shape[0], rd, bool(is_neox_style), err, handle)
-    _check("pkv_qk_norm_rope_reshape_and_cache", st)
+            _ptr(q_weight), k_weight.data_ptr(), w32, float(eps), cos_sin.data_ptr(), maxpos, rd,
+            bool(is_neox_style), err, handle)
+    st = _on_stream(dev, stream, call)
+    if st:
+        _check("pkv_qk_norm_rope_reshape_and_cache", st)
 
 
 def paged_tree_attention_workspace_size(batch: int, num_qo_heads: int, num_kv_heads: int,
@@ -973,43 +1032,50 @@ def paged_tree_attention(q, k_cache, v_cache, block_table, cu_seq_lens_q, cache_
     8-bit cache when k_scale and v_scale are given.  max_seqlen_q / max_seqlen:
     host ints; partition_size: split-KV partition (a multiple of 128; 0: chosen).
     sink, lse ([total_q, Hq] float32), window, layout as paged_decode."""
-    torch = _torch()
+    ty = _types()
     dev = _cuda_index("q", q)
-    desc = _pools(k_cache, v_cache, k_scale, v_scale, torch.bfloat16, layout, dev)
-    _arg("q", q, torch.bfloat16, 3, dev)
+    if k_scale is None and v_scale is None:
+        desc = _pools(k_cache, v_cache, None, None, ty.bf16, layout, dev)
+    else:
+        desc = _fp8_pools(k_cache, v_cache, k_scale, v_scale, layout, dev)
+    _arg("q", q, ty.bf16, 3, dev)
     total_q, Hq, D = q.shape
     _require(D == desc.head_dim, "head_dim of q and cache differ")
-    _arg("block_table", block_table, torch.int32, 2, dev)
-    _arg("cache_seqlens", cache_seqlens, torch.int32, 1, dev)
-    B = cache_seqlens.shape[0]
-    _arg_shape("cu_seq_lens_q", cu_seq_lens_q, torch.int32, (B + 1,), dev)
-    _require(block_table.shape[0] == B, "block_table must have one row per request")
-    _arg("tree_mask", tree_mask, torch.int64, 2, dev)
-    words = tree_mask.shape[1]
+    _arg("block_table", block_table, ty.i32, 2, dev)
+    _arg("cache_seqlens", cache_seqlens, ty.i32, 1, dev)
+    B = cache_seqlens.size(0)
+    _arg_vector("cu_seq_lens_q", cu_seq_lens_q, ty.i32, B + 1, dev)
+    _require(block_table.size(0) == B, "block_table must have one row per request")
+    _arg("tree_mask", tree_mask, ty.i64, 2, dev)
+    words = tree_mask.size(1)
     max_seqlen_q, max_seqlen = int(max_seqlen_q), int(max_seqlen)
     window_left, partition_size = int(window_left), int(partition_size)
-    _require(tree_mask.shape[0] == total_q and 64 * words >= max_seqlen_q,
+    _require(tree_mask.size(0) == total_q and 64 * words >= max_seqlen_q,
              "tree_mask must be [total_q, words] with words * 64 >= max_seqlen_q")
     if tree_depth is not None:
-        _arg_shape("tree_depth", tree_depth, torch.int32, (total_q,), dev)
+        _arg_vector("tree_depth", tree_depth, ty.i32, total_q, dev)
     elif window_left >= 0 or alibi_slopes is not None:
         raise ValueError("tree_depth is needed with a window or ALiBi slopes")
-    _attention_extras(sink, alibi_slopes, out, lse, q, dev)
+    _attention_extras(sink, alibi_slopes, out, lse, q, total_q, Hq, dev)
     err = _error_word(dev_error, dev)
     scale = float(sm_scale) if sm_scale is not None else D ** -0.5
     need = _tree_ws(B, Hq, desc.num_kv_heads, D, total_q, max_seqlen_q, max_seqlen,
                     partition_size, window_left)
+    if need <= 256:
+        need = 0  # one partition needs no workspace
     lib = load_library()
-    with _launch_on(dev, stream) as handle:
-        if out is None:
-            out = torch.empty_like(q)
+
+    def call(handle):
+        o = ty.torch.empty_like(q) if out is None else out
         ws, ws_bytes, held = _scratch(need, dev, q.device, workspace)
-        st = lib.pkv_paged_tree_attention(
-            out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale),
-            _ptr(v_scale), desc, block_table.data_ptr(), block_table.shape[1],
+        return o, lib.pkv_paged_tree_attention(
+            o.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale),
+            _ptr(v_scale), desc, block_table.data_ptr(), block_table.size(1),
             cu_seq_lens_q.data_ptr(), cache_seqlens.data_ptr(), max_seqlen_q, max_seqlen,
             total_q, tree_mask.data_ptr(), words, _ptr(tree_depth), _ptr(sink),
             _ptr(alibi_slopes), B, Hq, window_left, scale, partition_size, _ptr(lse), ws,
             ws_bytes, err, handle)
-    _check("pkv_paged_tree_attention", st)
+    out, st = _on_stream(dev, stream, call)
+    if st:
+        _check("pkv_paged_tree_attention", st)
     return out

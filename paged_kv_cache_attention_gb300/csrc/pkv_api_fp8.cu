@@ -235,11 +235,6 @@ pkv_status pkv_paged_decode_fp8(void *out, const void *q, const void *k_cache,
         !aligned(k_scale, 16) || !aligned(v_scale, 16) || !aligned(block_table, 4) ||
         !aligned(cache_seqlens, 4))
         return PKV_ERR_INVALID_ARG;
-    // the layout of the workspace is paged_decode's: lse, then outputs
-    const size_t need = pkv_paged_decode_workspace_size(batch, num_qo_heads, cache.head_dim,
-                                                        max_seqlen, P, window_left);
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < need)
-        return PKV_ERR_WORKSPACE;
     int64_t np = ((int64_t)max_seqlen + P - 1) / P;
     if (window_left >= 0) {
         const int64_t w = ((int64_t)window_left + 1 + P - 1) / P + 1;
@@ -248,6 +243,12 @@ pkv_status pkv_paged_decode_fp8(void *out, const void *q, const void *k_cache,
     if (np < 1) np = 1;
     if (np > 65535) return PKV_ERR_UNSUPPORTED;  // grid.y limit
     const size_t units = (size_t)batch * num_qo_heads * (size_t)np;
+    // the layout of the workspace is paged_decode's: lse, then outputs; one
+    // partition writes the output itself
+    const size_t need = pkv_paged_decode_workspace_size(batch, num_qo_heads, cache.head_dim,
+                                                        max_seqlen, P, window_left);
+    if (np > 1 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
+        return PKV_ERR_WORKSPACE;
 
     DecodeFp8Params pp;
     std::memset(&pp, 0, sizeof pp);
