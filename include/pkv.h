@@ -533,13 +533,11 @@ PKV_API pkv_status pkv_qk_norm_rope_reshape_and_cache(
     const void *k_weight, int weight_f32, float eps, const float *cos_sin, int max_position,
     int rotary_dim, int is_neox_style, int32_t *dev_error, void *stream);
 
-/* Workspace bytes pkv_paged_tree_attention needs (its split-KV partials); 256
- * when it runs as one partition, which uses none (the workspace may be NULL). */
+/* Workspace bytes pkv_paged_tree_attention needs (at most two partial results
+ * per CTA, and 8 bytes per request). */
 PKV_API size_t pkv_paged_tree_attention_workspace_size(int batch, int num_qo_heads,
                                                        int num_kv_heads, int head_dim,
-                                                       int64_t total_q, int max_seqlen_q,
-                                                       int max_seqlen, int partition_size,
-                                                       int window_left);
+                                                       int max_seqlen_q);
 
 /*
  * paged_tree_attention: attention of a tree (or any set) of drafted tokens of
@@ -565,10 +563,13 @@ PKV_API size_t pkv_paged_tree_attention_workspace_size(int batch, int num_qo_hea
  *                  draft n of the same request; bits at or past q_len are
  *                  ignored; mask_words * 64 >= max_seqlen_q
  *   tree_depth     [total_q] int32, the draft's distance from the first draft
- *                  position (0 for the root; below 0 reads as 0).  May be NULL
+ *                  position (0 for the root; read as clamped to [0, 65535]).  May be NULL
  *                  without a window and without ALiBi, where it has no effect
- *   partition_size split-KV partition in tokens, a multiple of 128; 0: chosen
- *                  from the shapes
+ *   partition_size the least number of keys that one CTA takes of a kv head in
+ *                  one go, a multiple of 128 (0: 128).  All keys are shared out
+ *                  evenly over the SMs; a larger value keeps short contexts whole
+ *   workspace      device scratch of pkv_paged_tree_attention_workspace_size
+ *                  bytes, 256-byte aligned; needs no initialisation
  * A NaN or an infinity in a V row reaches only drafts that keep that key (where
  * some drafts do not, the whole output row of one that does is NaN).  Requests
  * whose drafts do not fit their length (q_len > cache_seqlens[r]) attend

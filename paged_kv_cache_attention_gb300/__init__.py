@@ -169,8 +169,7 @@ def load_library(path: Optional[str] = None):
             P, P, P, i64, i64, i64, i32, P, P, i64, i64, P, P, P, P, P, P, i64, i32, CacheDesc, P,
             P, i32, f32, P, i32, i32, i32, P, P]
         lib.pkv_qk_norm_rope_reshape_and_cache.restype = i32
-        lib.pkv_paged_tree_attention_workspace_size.argtypes = [i32, i32, i32, i32, i64, i32, i32,
-                                                                i32, i32]
+        lib.pkv_paged_tree_attention_workspace_size.argtypes = [i32, i32, i32, i32, i32]
         lib.pkv_paged_tree_attention_workspace_size.restype = sz
         lib.pkv_paged_tree_attention.argtypes = [
             P, P, P, P, P, P, CacheDesc, P, i32, P, P, i32, i32, i32, P, i32, P, P, P, i32, i32,
@@ -805,9 +804,8 @@ def _decode_ws(batch, Hq, D, max_seqlen, partition, window) -> int:
 
 
 @functools.lru_cache(maxsize=1024)
-def _tree_ws(batch, Hq, Hkv, D, total_q, max_q, max_seqlen, partition, window) -> int:
-    return paged_tree_attention_workspace_size(batch, Hq, Hkv, D, total_q, max_q, max_seqlen,
-                                               partition, window)
+def _tree_ws(batch, Hq, Hkv, D, max_q) -> int:
+    return paged_tree_attention_workspace_size(batch, Hq, Hkv, D, max_q)
 
 
 def reshape_and_cache_fp8(key, value, k_cache, v_cache, k_scale, v_scale, slot_mapping,
@@ -1004,12 +1002,9 @@ def qk_norm_rope_reshape_and_cache(query, key, value, k_cache, v_cache, position
 
 
 def paged_tree_attention_workspace_size(batch: int, num_qo_heads: int, num_kv_heads: int,
-                                        head_dim: int, total_q: int, max_seqlen_q: int,
-                                        max_seqlen: int, partition_size: int = 0,
-                                        window_left: int = -1) -> int:
+                                        head_dim: int, max_seqlen_q: int) -> int:
     return int(load_library().pkv_paged_tree_attention_workspace_size(
-        batch, num_qo_heads, num_kv_heads, head_dim, total_q, max_seqlen_q, max_seqlen,
-        partition_size, window_left))
+        batch, num_qo_heads, num_kv_heads, head_dim, max_seqlen_q))
 
 
 def paged_tree_attention(q, k_cache, v_cache, block_table, cu_seq_lens_q, cache_seqlens,
@@ -1030,7 +1025,8 @@ def paged_tree_attention(q, k_cache, v_cache, block_table, cu_seq_lens_q, cache_
     depth below the first draft position, needed with window_left or
     alibi_slopes (positions are context length + depth).  Pools are bf16, or the
     8-bit cache when k_scale and v_scale are given.  max_seqlen_q / max_seqlen:
-    host ints; partition_size: split-KV partition (a multiple of 128; 0: chosen).
+    host ints; partition_size: least keys a CTA takes in one go (a multiple of 128;
+    0: 128).
     sink, lse ([total_q, Hq] float32), window, layout as paged_decode."""
     ty = _types()
     dev = _cuda_index("q", q)
@@ -1059,10 +1055,7 @@ def paged_tree_attention(q, k_cache, v_cache, block_table, cu_seq_lens_q, cache_
     _attention_extras(sink, alibi_slopes, out, lse, q, total_q, Hq, dev)
     err = _error_word(dev_error, dev)
     scale = float(sm_scale) if sm_scale is not None else D ** -0.5
-    need = _tree_ws(B, Hq, desc.num_kv_heads, D, total_q, max_seqlen_q, max_seqlen,
-                    partition_size, window_left)
-    if need <= 256:
-        need = 0  # one partition needs no workspace
+    need = _tree_ws(B, Hq, desc.num_kv_heads, D, max_seqlen_q)
     lib = load_library()
 
     def call(handle):

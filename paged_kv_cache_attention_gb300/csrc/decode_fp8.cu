@@ -13,10 +13,11 @@
 //   * K: the byte, as 2^ek, multiplies the fp32 score of its key;
 //   * V: the byte multiplies p_j before p rounds to f16.  Weights are kept
 //     relative to the largest byte E seen so far by the warp, p_j *
-//     2^(ev_j - E + 10); with p <= 2^4 (below) that is at most 2^14, and f16
-//     keeps 11 bits of every weight down to 2^-24 of 2^ev_max.  The
-//     accumulators move by 2^(E_old - E_new) with the softmax's own rescale;
-//   * a row's maximum reference moves only when a score exceeds it by 2^4.
+//     2^(ev_j - E + 6); with p <= 2^9 (below) that is at most 2^15, and f16
+//     keeps 11 bits of every weight down to 2^-20 of the reference's (an error
+//     of 2^-31 of it below that).  The accumulators move by 2^(E_old - E_new)
+//     with the softmax's own rescale;
+//   * a row's reference moves only when a score exceeds it by 9 log2 units.
 // q is scaled per head by a power of two to at most 2^15 and held in f16,
 // which is exact for every bf16 value within 2^-28 of the row's largest (and
 // off by less than 2^-39 of the largest below that).
@@ -31,6 +32,14 @@
 // tokens, 64 of a 64-dim head) through its own ring of two stages: K and V by
 // TMA (one box per page and 128 dims), the scale bytes by 16-byte cp.async on
 // the same barrier.
+//
+// Measured (GB300): 64 sequences of 512..4096 tokens, 32/8 heads of 128: 60 us,
+// 5.0 TB/s, 74 % of a copy's rate (the bf16 cache takes 108 us); 8 of
+// 32K..128K, 64/8 heads of 64: 118 us, 83 %.  Half as long stages (twice the
+// warps) take 69 and 138 us, three or four of them in the ring 71 and 143, twice
+// as long ones 72 and 152; partitions of 1024 tokens 65 and 120.  What is
+// left is latency between dependent instructions at 2.5 warps per scheduler
+// (issue slots 39 % used, tensor pipe 22 %).
 #include "pkv_fp8.cuh"
 
 namespace pkv {
@@ -40,8 +49,8 @@ namespace {
 constexpr int kWarps = 2;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxGroup = 16;
-constexpr int kWeightExp = 10;   // weights are at most 2^kWeightExp * 2^kLazy
-constexpr float kLazy = 4.f;     // log2 units a score may exceed its row's reference
+constexpr int kWeightExp = 6;    // weights are at most 2^kWeightExp * 2^kLazy
+constexpr float kLazy = 9.f;     // log2 units a score may exceed its row's reference
 constexpr float kNegInf = -INFINITY;
 
 __device__ __forceinline__ int clipped_len(const DecodeParams &p, int b, int block_size,
@@ -112,7 +121,7 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
                   const __grid_constant__ CUtensorMap tmv) {
     using C = Shape<D>;
     constexpr int NST = C::NST, TOK = C::TOK;
-    constexpr int PPS = TOK / BS;   // pages per stage
+    constexpr int BR = BS < TOK ? BS : TOK;  // tokens per box: a page, or a stage's part of one
     constexpr int NC = D / 16;      // 16-dim chunks
     constexpr int NT = TOK / 8;     // 8-token tiles
     constexpr int NCP = TOK / 16;   // 16-byte pieces of a stage's K (or V) scale bytes
@@ -124,7 +133,8 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
     float *s_m = reinterpret_cast<float *>(smem + C::M_OFF);
     float *s_l = reinterpret_cast<float *>(smem + C::L_OFF);
 
-    pdl_trigger();
+    // no early trigger: merge CTAs that wait on the SMs cost more (2 %) than
+    // their launch latency
     pdl_wait();
     const int g = blockIdx.x, b = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -147,7 +157,7 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
 
     // stages start at multiples of TOK; pages of the range
     const int st_lo = tok_lo / TOK, nst = (tok_hi - 1) / TOK - st_lo + 1;
-    const int pg_lo = st_lo * PPS, pg_first = tok_lo / BS, pg_last = (tok_hi - 1) / BS;
+    const int pg_lo = st_lo * TOK / BS, pg_first = tok_lo / BS, pg_last = (tok_hi - 1) / BS;
 
     const uint32_t ring = smem_u32(smem);
     const uint32_t bars = ring + C::BAR_OFF;
@@ -158,8 +168,8 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
         tma_prefetch_desc(&tmv);
     }
     const int32_t *bt = p.block_table + (int64_t)b * p.max_blocks_per_seq;
-    for (int i = threadIdx.x; i < nst * PPS; i += kThreads) {
-        const int page = pg_lo + i;
+    const int pg_end = ((st_lo + nst) * TOK - 1) / BS;  // the last stage's last page
+    for (int page = pg_lo + threadIdx.x; page <= pg_end; page += kThreads) {
         int id = -1;
         if (page >= pg_first && page <= pg_last) {  // else: no attended key, not read
             id = bt[page];
@@ -168,7 +178,7 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
                 id = -1;
             }
         }
-        s_blk[i] = id;
+        s_blk[page - pg_lo] = id;
     }
     __syncthreads();
 
@@ -184,31 +194,36 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
     auto issue = [&](int j) {
         const int s = j % NST;
         const uint32_t bar = wbars + 8 * s;
-        const int *blk = s_blk + (warp + j * kWarps) * PPS;
+        const int first = (st_lo + warp + j * kWarps) * TOK;  // the stage's first token
         if (lane == 0) {
+            int id[TOK / BR];
             uint32_t bytes = 0;
 #pragma unroll
-            for (int q = 0; q < PPS; ++q)
-                if (blk[q] >= 0) bytes += 2 * C::PARTS * BS * C::ROWB;
+            for (int q = 0; q < TOK / BR; ++q) {
+                id[q] = s_blk[(first + q * BR) / BS - pg_lo];
+                if (id[q] >= 0) bytes += 2 * C::PARTS * BR * C::ROWB;
+            }
             mbar_arrive_expect_tx(bar, bytes);
             const uint32_t dst = wring + s * 2 * C::KV_BYTES;
 #pragma unroll
-            for (int q = 0; q < PPS; ++q) {
-                if (blk[q] < 0) continue;
-                const int cy = HND ? 0 : g;
-                const int cz = HND ? blk[q] * p.num_kv_heads + g : blk[q] * BS;
+            for (int q = 0; q < TOK / BR; ++q) {
+                if (id[q] < 0) continue;
+                const int off = (first + q * BR) % BS;
+                const int cy = HND ? off : g;
+                const int cz = HND ? id[q] * p.num_kv_heads + g : id[q] * BS + off;
 #pragma unroll
                 for (int h = 0; h < C::PARTS; ++h) {
-                    const uint32_t o = dst + h * C::PART_BYTES + q * BS * C::ROWB;
+                    const uint32_t o = dst + h * C::PART_BYTES + q * BR * C::ROWB;
                     tma_load_3d_hint(o, &tmk, bar, h * 128, cy, cz, policy);
                     tma_load_3d_hint(o + C::KV_BYTES, &tmv, bar, h * 128, cy, cz, policy);
                 }
             }
         }
         if (lane < 2 * NCP) {
-            const int isv = lane / NCP, t = (lane % NCP) * 16, id = blk[t / BS];
+            const int isv = lane / NCP, t = first + (lane % NCP) * 16;
+            const int id = s_blk[t / BS - pg_lo];
             if (id >= 0)
-                cp_async16(wscale + s * 2 * TOK + isv * TOK + t,
+                cp_async16(wscale + s * 2 * TOK + isv * TOK + (lane % NCP) * 16,
                            (isv ? pp.v_scale : pp.k_scale) +
                                ((int64_t)id * p.num_kv_heads + g) * BS + t % BS);
             cp_async_arrive(bar);
@@ -280,15 +295,17 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
         const uint8_t *sc = smem + C::SCALE_OFF + (warp * NST + s) * 2 * TOK;
         const int tok0 = (st_lo + i) * TOK;
         // lane = token (and token + 32): is it attended, its factors
-        uint32_t okm[TOK / 32];
+        constexpr int NW = (TOK + 31) / 32;
+        uint32_t okm[NW];
         bool full = true;
         int vmax = 0;
 #pragma unroll
-        for (int h = 0; h < TOK / 32; ++h) {
+        for (int h = 0; h < NW; ++h) {
             const int t = tok0 + h * 32 + lane;
-            const bool ok = t >= tok_lo && t < tok_hi && s_blk[i * PPS + (h * 32 + lane) / BS] >= 0;
+            const bool ok = h * 32 + lane < TOK && t >= tok_lo && t < tok_hi &&
+                            s_blk[t / BS - pg_lo] >= 0;
             okm[h] = __ballot_sync(0xffffffffu, ok);
-            full = full && okm[h] == 0xffffffffu;
+            full = full && okm[h] == (TOK < 32 ? (1u << (TOK % 32)) - 1u : 0xffffffffu);
             if (ok) vmax = max(vmax, (int)sc[TOK + h * 32 + lane]);
         }
         vmax = __reduce_max_sync(0xffffffffu, vmax);
@@ -300,8 +317,9 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
             gauge = vmax;
         }
 #pragma unroll
-        for (int h = 0; h < TOK / 32; ++h) {
+        for (int h = 0; h < NW; ++h) {
             const int t = h * 32 + lane;
+            if (TOK < 32 && t >= TOK) break;
             const uint32_t kbyte = sc[t], vbyte = sc[TOK + t];
             const int x = (int)vbyte - gauge + kWeightExp + 127;
             wfact[t] = scale_value(kbyte);
@@ -603,8 +621,8 @@ cudaError_t launch_one(const DecodeFp8Params &p, const CUtensorMap *tk, const CU
     using C = Shape<D>;
     auto kern = p.d.hnd ? decode_fp8_kernel<D, BS, NHT, true>
                         : decode_fp8_kernel<D, BS, NHT, false>;
-    // a partition meets at most partition_size / TOK + 2 stages
-    const int smem = C::SMEM_FIXED + (p.d.partition_size / C::TOK + 2) * (C::TOK / BS) * 4;
+    // the pages of a partition, and those beside it in its first and last stage
+    const int smem = C::SMEM_FIXED + (p.d.partition_size / BS + 6) * 4;
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(p.d.num_kv_heads, p.d.num_parts, p.d.batch), dim3(kThreads),
@@ -622,6 +640,13 @@ cudaError_t launch_d(const DecodeFp8Params &p, int BS, const CUtensorMap *tk,
 }
 
 }  // namespace
+
+// Tokens per TMA box: see Shape.
+int decode_fp8_box_rows(int head_dim, int block_size) {
+    const int tok = head_dim <= 64 ? Shape<64>::TOK : Shape<128>::TOK;
+    static_assert(Shape<128>::TOK == Shape<256>::TOK, "one rule for both");
+    return block_size < tok ? block_size : tok;
+}
 
 cudaError_t launch_decode_fp8(const DecodeFp8Params &p, const pkv_cache_desc &cache,
                               const CUtensorMap *tmap_k, const CUtensorMap *tmap_v,

@@ -60,18 +60,18 @@ PoolArgs pool_args(const pkv_cache_desc &c, const void *k, const void *v, const 
     return a;
 }
 
-// TMA view of one pool whose box is box_elems dims of one (page, kv head):
-// NHD {D, Hkv, num_blocks * bs}, HND {D, bs, num_blocks * Hkv}.
-pkv_status pool_map(CUtensorMap *map, const void *base, const pkv_cache_desc &c) {
+// TMA view of one pool whose box is 128 bytes (64 for the codes of a 64-dim
+// head) of box_rows tokens of one (page, kv head): NHD {D, Hkv, num_blocks *
+// bs}, HND {D, bs, num_blocks * Hkv}.
+pkv_status pool_map(CUtensorMap *map, const void *base, const pkv_cache_desc &c, int box_rows) {
     const bool fp8 = c.dtype == PKV_E4M3;
     const cuuint64_t e = fp8 ? 1 : 2, D = (cuuint64_t)c.head_dim;
-    const cuuint32_t bs = (cuuint32_t)c.block_size;
+    const cuuint32_t bs = (cuuint32_t)box_rows;
     const bool nhd = c.layout == PKV_NHD;
     const cuuint64_t mid = nhd ? c.num_kv_heads : c.block_size;
     const cuuint64_t rows = (cuuint64_t)c.num_blocks * (nhd ? c.block_size : c.num_kv_heads);
     const cuuint64_t dims[3] = {D, mid, rows};
     const cuuint64_t strides[2] = {D * e, D * e * mid};
-    // 128-byte rows in shared memory; 64 for the codes of a 64-dim head
     const cuuint32_t w = fp8 ? (D == 64 ? 64 : 128) : 64;
     const cuuint32_t box[3] = {w, nhd ? 1u : bs, nhd ? bs : 1u};
     return encode_map_3d(map,
@@ -80,55 +80,28 @@ pkv_status pool_map(CUtensorMap *map, const void *base, const pkv_cache_desc &c)
                          w * e == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Partitions of the tree attention: `partition_size` keys each when given, else
-// chosen: with u CTAs per partition on kTreeSms SMs and n partitions of t
-// 128-key tiles, (u n / SMs + 1) rounds of t + kTreeFixed tiles' time are
-// about what the launch takes (a CTA's start and end cost some tiles' time, and
-// the last round is half empty); the n with the least is taken.  Fixed
-// counts, so that the workspace of a problem does not depend on the device.
-constexpr int kTreeTile = 128, kMaxDraft = 256, kTreeSms = 152, kTreeFixed = 6;
+// Workspace of the tree attention: the line of work, and two partials per CTA.
+// CTAs: groups of one per kv head on kTreeSms SMs.  A fixed count, so that the
+// workspace of a problem does not depend on the device.
+constexpr int kTreeTile = 128, kMaxDraft = 256, kTreeSms = 152;
 
 struct TreeSplit {
-    int part, row_tiles;
-    int64_t num_parts;
-    size_t lse_bytes, total;
+    int groups, row_tiles;
+    size_t line_bytes, lse_bytes, total;
 };
 
-TreeSplit tree_split(int batch, int Hq, int Hkv, int D, int max_q, int64_t total_q, int max_len,
-                     int partition_size, int window_left) {
+TreeSplit tree_split(int batch, int Hq, int Hkv, int D, int max_q) {
     TreeSplit s;
     const int64_t rows = (int64_t)max_q * (Hq / Hkv);
     s.row_tiles = (int)((rows + kTreeTile - 1) / kTreeTile);
     if (s.row_tiles < 1) s.row_tiles = 1;
-    int64_t span = max_len;
-    if (window_left >= 0 && (int64_t)window_left + max_q < span) span = window_left + max_q;
-    s.part = partition_size;
-    if (s.part == 0) {
-        // row tiles go two to a CTA (one at head size 256)
-        const int64_t units =
-            (int64_t)batch * Hkv * (D > 128 ? s.row_tiles : (s.row_tiles + 1) / 2);
-        const int64_t tiles = (span + kTreeTile - 1) / kTreeTile;
-        int64_t best = tiles < 1 ? 1 : tiles;
-        double best_cost = 1e300;
-        for (int64_t n = 1; n <= 64 && n <= tiles; ++n) {
-            const int64_t t = (tiles + n - 1) / n;
-            const double cost = ((double)(units * n) / kTreeSms + 1.0) * (double)(t + kTreeFixed);
-            if (cost < best_cost) {
-                best_cost = cost;
-                best = t;
-            }
-        }
-        s.part = (int)(best * kTreeTile);
-    }
-    s.num_parts = ((int64_t)max_len + s.part - 1) / s.part;
-    if (window_left >= 0) {
-        const int64_t w = (span + s.part - 1) / s.part + 1;
-        if (w < s.num_parts) s.num_parts = w;
-    }
-    if (s.num_parts < 1) s.num_parts = 1;
-    const size_t units = (size_t)total_q * Hq * (size_t)s.num_parts;
-    s.lse_bytes = s.num_parts > 1 ? (units * sizeof(float) + 255) / 256 * 256 : 0;
-    s.total = s.num_parts > 1 ? s.lse_bytes + units * D * sizeof(float) + 256 : 256;
+    s.groups = kTreeSms / Hkv > 0 ? kTreeSms / Hkv : 1;
+    // rows of a row group: two tiles where the CTA takes two
+    const size_t grow = kTreeTile * (D <= 128 && s.row_tiles > 1 ? 2 : 1);
+    const size_t units = (size_t)2 * s.groups * Hkv * grow;
+    s.line_bytes = (((size_t)batch + 2) * 8 + 255) / 256 * 256;
+    s.lse_bytes = (units * sizeof(float) + 255) / 256 * 256;
+    s.total = s.line_bytes + s.lse_bytes + units * D * sizeof(float);
     return s;
 }
 
@@ -281,8 +254,9 @@ pkv_status pkv_paged_decode_fp8(void *out, const void *q, const void *k_cache,
     pp.v_scale = v_scale;
 
     alignas(64) CUtensorMap tk, tv;
-    if ((st = pool_map(&tk, k_cache, cache)) != PKV_OK) return st;
-    if ((st = pool_map(&tv, v_cache, cache)) != PKV_OK) return st;
+    const int rows = decode_fp8_box_rows(cache.head_dim, cache.block_size);
+    if ((st = pool_map(&tk, k_cache, cache, rows)) != PKV_OK) return st;
+    if ((st = pool_map(&tv, v_cache, cache, rows)) != PKV_OK) return st;
     return from_cuda(launch_decode_fp8(pp, cache, &tk, &tv, static_cast<cudaStream_t>(stream)));
 }
 
@@ -356,15 +330,11 @@ pkv_status pkv_qk_norm_rope_reshape_and_cache(
 }
 
 size_t pkv_paged_tree_attention_workspace_size(int batch, int num_qo_heads, int num_kv_heads,
-                                               int head_dim, int64_t total_q, int max_seqlen_q,
-                                               int max_seqlen, int partition_size,
-                                               int window_left) {
+                                               int head_dim, int max_seqlen_q) {
     if (batch <= 0 || num_kv_heads <= 0 || num_qo_heads < num_kv_heads || head_dim <= 0 ||
-        total_q < 0 || max_seqlen_q < 0 || max_seqlen < 0 || partition_size < 0)
+        max_seqlen_q < 0)
         return 256;
-    return tree_split(batch, num_qo_heads, num_kv_heads, head_dim, max_seqlen_q, total_q,
-                      max_seqlen, partition_size, window_left)
-        .total;
+    return tree_split(batch, num_qo_heads, num_kv_heads, head_dim, max_seqlen_q).total;
 }
 
 pkv_status pkv_paged_tree_attention(
@@ -399,10 +369,8 @@ pkv_status pkv_paged_tree_attention(
         !aligned(tree_mask, 8) || (fp8 && (!aligned(k_scale, 16) || !aligned(v_scale, 16))))
         return PKV_ERR_INVALID_ARG;
     const TreeSplit s =
-        tree_split(batch, num_qo_heads, cache.num_kv_heads, cache.head_dim, max_seqlen_q,
-                   total_q, max_seqlen, partition_size, window_left);
-    if (s.num_parts > 65535) return PKV_ERR_UNSUPPORTED;  // grid.y limit
-    if (s.num_parts > 1 && (!workspace || !aligned(workspace, 256) || workspace_bytes < s.total))
+        tree_split(batch, num_qo_heads, cache.num_kv_heads, cache.head_dim, max_seqlen_q);
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < s.total)
         return PKV_ERR_WORKSPACE;
 
     TreeParams p;
@@ -417,8 +385,10 @@ pkv_status pkv_paged_tree_attention(
     p.sink = sink;
     p.alibi = alibi_slopes;
     p.lse_out = lse_out;
-    p.part_lse = static_cast<float *>(workspace);
-    p.part_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + s.lse_bytes);
+    char *ws = static_cast<char *>(workspace);
+    p.line = reinterpret_cast<long long *>(ws);
+    p.part_lse = reinterpret_cast<float *>(ws + s.line_bytes);
+    p.part_o = reinterpret_cast<float *>(ws + s.line_bytes + s.lse_bytes);
     p.dev_error = dev_error;
     p.k_scale = fp8 ? k_scale : nullptr;
     p.v_scale = fp8 ? v_scale : nullptr;
@@ -436,14 +406,14 @@ pkv_status pkv_paged_tree_attention(
     p.head_dim = cache.head_dim;
     p.hnd = cache.layout == PKV_HND ? 1 : 0;
     p.block_size = cache.block_size;
-    p.partition_size = s.part;
-    p.num_parts = (int)s.num_parts;
+    p.groups = s.groups;
+    p.min_tiles = partition_size > 0 ? partition_size / kTreeTile : 1;
     p.row_tiles = s.row_tiles;
     p.scale_log2 = sm_scale * 1.4426950408889634f;
 
     alignas(64) CUtensorMap tk, tv;
-    if ((st = pool_map(&tk, k_cache, cache)) != PKV_OK) return st;
-    if ((st = pool_map(&tv, v_cache, cache)) != PKV_OK) return st;
+    if ((st = pool_map(&tk, k_cache, cache, cache.block_size)) != PKV_OK) return st;
+    if ((st = pool_map(&tv, v_cache, cache, cache.block_size)) != PKV_OK) return st;
     return from_cuda(launch_tree(p, &tk, &tv, static_cast<cudaStream_t>(stream)));
 }
 

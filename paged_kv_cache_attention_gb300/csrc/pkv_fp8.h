@@ -69,15 +69,19 @@ struct TreeParams {
     const int32_t *depth;          // [total_q] or nullptr
     const float *sink, *alibi;
     float *lse_out;                // [total_q, Hq] or nullptr
-    float *part_lse;               // [total_q, Hq, num_parts] (log2 units)
-    float *part_o;                 // [total_q, Hq, num_parts, D]
+    long long *line;               // [B + 2] the requests' places on the line of work,
+                                   // its length and a CTA group's share (tree.cu)
+    float *part_lse;               // [2 * groups, Hkv, rows of a row group] (log2 units)
+    float *part_o;                 // the same with [D]
     int32_t *dev_error;
     const uint8_t *k_scale, *v_scale;
     int64_t num_blocks;
     int batch, num_qo_heads, num_kv_heads, group;
     int max_blocks_per_seq, max_seqlen, max_seqlen_q, total_q;
     int mask_words, window_left, head_dim, hnd, block_size;
-    int partition_size, num_parts, row_tiles;
+    int groups;                    // CTA groups of num_kv_heads CTAs
+    int min_tiles;                 // least key tiles of a group's share
+    int row_tiles;                 // 128-row tiles of the largest request
     float scale_log2;
 };
 
@@ -89,6 +93,8 @@ pkv_status encode_map_3d(CUtensorMap *map, CUtensorMapDataType type, const void 
 cudaError_t launch_quant_write(const QuantWriteParams &p, int dtype, cudaStream_t stream);
 cudaError_t launch_gather(const GatherParams &p, cudaStream_t stream);
 cudaError_t launch_norm_rope(const NormRopeParams &p, int dtype, cudaStream_t stream);
+// Tokens of a page that one box of the decode's tensor maps holds.
+int decode_fp8_box_rows(int head_dim, int block_size);
 cudaError_t launch_decode_fp8(const DecodeFp8Params &p, const pkv_cache_desc &cache,
                               const CUtensorMap *tmap_k, const CUtensorMap *tmap_v,
                               cudaStream_t stream);

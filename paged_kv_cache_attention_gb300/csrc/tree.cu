@@ -23,13 +23,22 @@
 // scores, V's moves the exponent of the weights.  q is scaled per row by a power
 // of two into f16 (decode_fp8.cu gives the error bound).
 //
-// One CTA per (kv head, one or two row tiles, partition, request): split-KV over
-// partitions of a multiple of 128 keys and a merge kernel, or one partition and
-// a direct store.  Four softmax warps per row tile, one row per thread; a TMA
-// warp; an MMA warp; over 8-bit pools the warps that convert codes.
+// Persistent CTAs, one per SM, in groups of one CTA per kv head.  The work of a kv
+// head is one line of key tiles: request after request, and in a request row
+// group after row group (X row tiles of one request; its key tiles).  Group i
+// takes the i-th equal part of the line, so every SM is busy to the end
+// whatever the lengths are, and a CTA's fixed costs (Q, the pipeline's fill, the
+// last rows out) come once per row group it meets, with the next K and V tiles
+// already on their way.  A row group that lies in one group's part is stored by
+// it; one that is cut leaves partials, at most two per CTA, for a merge kernel.
+// The heads of one group read the same tokens at the same time.
+//
+// Warps: four softmax warps per row tile, one row per thread; a TMA warp, which
+// also works out the CTA's segments and hands them to the others through a
+// ring; an MMA warp; over 8-bit pools the warps that convert codes.
 //   S = Q K^T -> TMEM; the softmax takes its row into registers, writes P (16
 //   bits) over S; O += P V with P from TMEM.  O is rescaled only when a row's
-//   maximum grows by more than 2^4.
+//   maximum has grown a lot.
 // The products run in units n = (key tile, row tile), row tiles fastest, with two S
 // buffers in turn: S(n + 2) is issued right behind O(n), so a unit's softmax
 // always has the other buffer's products beside it -- those of the other row
@@ -47,10 +56,17 @@ namespace pkv {
 namespace {
 
 constexpr int kTile = 128;      // rows and keys per tile
-constexpr int kMaxDraft = 256;
+constexpr int kRing = 4;        // segments handed over ahead
 constexpr float kNegInf = -INFINITY;
-constexpr float kLazy = 4.f;    // log2 units a maximum may grow before O is rescaled
-constexpr int kWeightExp = 10;  // f16 weights stay below 2^(kWeightExp + kLazy)
+// A row's reference moves (and O is rescaled, which costs about a tile's time)
+// only when a score exceeds it by kLazy log2 units.  bf16 weights have fp32's
+// range and lose nothing by it; f16 weights start at 2^kWeightExp and stay
+// below 2^15, with 11 bits kept down to 2^-20 of the reference and an error of
+// 2^-31 of it below that.  With 4 for both, rows of real spread rescaled in half
+// of the tiles: 402 us instead of 230 on 8 x 64 drafts over 16K..32K tokens.
+template <bool KV8>
+constexpr float kLazy = KV8 ? 9.f : 24.f;
+constexpr int kWeightExp = 6;
 
 // T: tile width (head size padded to 64, 128 or 256); X: row tiles per CTA.
 template <int T, bool KV8, int X>
@@ -76,15 +92,16 @@ struct Cfg {
     static constexpr int OFF_V = OFF_K + KB * TILE;
     static constexpr int OFF_RAW = OFF_V + VB * TILE;
     static constexpr int OFF_SCALE = OFF_RAW + RU * RAW;
-    static constexpr int OFF_DEPTH = OFF_SCALE + RU * kTile;
-    static constexpr int OFF_BAR = OFF_DEPTH + kMaxDraft * 2;
+    static constexpr int OFF_RING = OFF_SCALE + RU * kTile;  // [kRing] Seg
+    static constexpr int OFF_BAR = OFF_RING + kRing * 48;
     // barriers
     static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + KB, B_VFULL = B_KEMPTY + KB,
                          B_VEMPTY = B_VFULL + VB, B_SFULL = B_VEMPTY + VB,
-                         B_PFULL = B_SFULL + 2, B_O = B_PFULL + 2, B_LAND = B_O + 2,
+                         B_PFULL = B_SFULL + 2, B_O = B_PFULL + 2, B_LAND = B_O + 1,
                          B_POISON = B_LAND + 1, B_FACT = B_POISON + 2, B_RFULL = B_FACT + 2,
-                         B_REMPTY = B_RFULL + RU, B_Q = B_REMPTY + RU, NBAR = B_Q + 1;
-    // tmem, abort, maxdepth, -, poison[2][4], scale bytes[2][K, V]
+                         B_REMPTY = B_RFULL + RU, B_Q = B_REMPTY + RU, B_IFULL = B_Q + 1,
+                         B_IEMPTY = B_IFULL + kRing, NBAR = B_IEMPTY + kRing;
+    // tmem, abort, -, -, poison[2][4], scale bytes[2][K, V]
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = 1024 + OFF_MISC + 64;
     static_assert(256 + X * T <= 512, "tensor memory");
@@ -110,12 +127,17 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
 // What a request attends.  Lengths and offsets live on the device and are
 // checked here: nothing outside [0, total_q) rows or the block table is used.
 struct Req {
-    int q_start, q_len, L, ctx, start;  // start: the first key any draft may see
+    int q_start, q_len, L;
+    __device__ __forceinline__ int ctx() const { return max(L - q_len, 0); }
+    // the first key any draft may see
+    __device__ __forceinline__ int start(int window_left) const {
+        return window_left < 0 ? 0 : max(ctx() - window_left, 0);
+    }
 };
 
 __device__ __forceinline__ Req request(const TreeParams &p, int b, bool report) {
     Req r;
-    const int a = p.cu_q[b], e = p.cu_q[b + 1];
+    const int a = p.cu_q[b], e = p.cu_q[b + 1], L = p.seqlens[b];
     bool bad = a < 0 || a > p.total_q;
     r.q_start = min(max(a, 0), p.total_q);
     long long n = (long long)e - a;
@@ -124,7 +146,6 @@ __device__ __forceinline__ Req request(const TreeParams &p, int b, bool report) 
     r.q_len = (int)min(n, (long long)min(p.max_seqlen_q, p.total_q - r.q_start));
     const long long cap_blocks = (long long)p.max_blocks_per_seq * p.block_size;
     const int cap = cap_blocks < p.max_seqlen ? (int)cap_blocks : p.max_seqlen;
-    const int L = p.seqlens[b];
     if (L < 0 || L > cap) bad = true;
     r.L = min(max(L, 0), cap);
     if (r.L < r.q_len) {  // the drafts are not all in the cache: nothing is attended
@@ -132,10 +153,39 @@ __device__ __forceinline__ Req request(const TreeParams &p, int b, bool report) 
         r.L = 0;
     }
     if (bad && report) flag_error(p.dev_error, PKV_DEVERR_SEQLEN);
-    r.ctx = max(r.L - r.q_len, 0);
-    r.start = p.window_left < 0 ? 0 : max(r.ctx - p.window_left, 0);
     return r;
 }
+
+// A request on the line of work: its key tiles (one without keys, for the
+// zeros), its row groups of `rows` rows, and their product.
+struct Cost {
+    int tiles, groups;
+    __device__ __forceinline__ long long total() const { return (long long)tiles * groups; }
+};
+
+__device__ __forceinline__ Cost cost_of(const TreeParams &p, const Req &r, int rows) {
+    Cost c;
+    const int start = r.start(p.window_left);
+    c.tiles = r.L > start ? (r.L - 1) / kTile - start / kTile + 1 : 1;
+    c.groups = (r.q_len * p.group + rows - 1) / rows;
+    return c;
+}
+
+// A segment: key tiles [tile0, tile0 + ntiles) of one row group of a request.
+struct Seg {
+    int q_start, q_len, ctx;
+    int row0, nrows;               // the group's (draft, head) rows
+    int tile0, ntiles;             // absolute key tiles; ntiles 0: no key at all
+    int tok_lo, tok_hi;            // the keys of these tiles that are attended
+    int full_lo, full_hi;          // tiles [full_lo, full_hi): every row sees every key
+    int slot_b;                    // 4 * request + cut; -1: no more segments.  cut: 0 the
+                                   // whole row group, 1 its begin is another CTA's (or both
+                                   // ends are), 2 only its end is
+    __device__ __forceinline__ int b() const { return slot_b >> 2; }
+    __device__ __forceinline__ int cut() const { return slot_b & 3; }
+    __device__ __forceinline__ bool partial(int j) const { return j < full_lo || j >= full_hi; }
+};
+static_assert(sizeof(Seg) == 48, "ring layout");
 
 // Bits n0 .. n0+31 of a draft's mask of nw 64-bit words (n0 may be negative).
 __device__ __forceinline__ uint32_t mask_bits(const int64_t *m, int nw, int n0) {
@@ -164,78 +214,20 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // 1024-aligned
     const uint32_t base = smem_u32(smem);
-    uint16_t *s_depth = reinterpret_cast<uint16_t *>(smem + C::OFF_DEPTH);
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     int32_t *s_abort = reinterpret_cast<int32_t *>(misc + 1);
-    int *s_maxdepth = reinterpret_cast<int *>(misc + 2);
     uint32_t *s_poison = misc + 4;   // [2][4]
     uint32_t *s_byte = misc + 12;    // [2][K, V]: a tile's largest scale bytes
+    Seg *ring = reinterpret_cast<Seg *>(smem + C::OFF_RING);
     auto bar = [&](int i) { return base + C::OFF_BAR + 8 * i; };
 
-    pdl_trigger();
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = blockIdx.z;
-    const int rgroups = (p.row_tiles + X - 1) / X;
-    const int g = blockIdx.x / rgroups, rt = (blockIdx.x - g * rgroups) * X;
-    const Req rq = request(p, b, blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0);
-    const int G = p.group, Dh = p.head_dim;
-    const int nrows = min(rq.q_len * G - rt * kTile, X * kTile);  // rows of this CTA
-    if (nrows <= 0) return;
-    const int nx = nrows > kTile ? 2 : 1;  // its row tiles
-    const int P = p.partition_size;
-    const int part = rq.start / P + blockIdx.y;
-    const int tok_lo = max(part * P, rq.start);
-    const int tok_hi = (int)min((long long)(part + 1) * P, (long long)rq.L);
-    const int kt0 = tok_lo / kTile;
-    const int ntiles = tok_hi > tok_lo ? (tok_hi - 1) / kTile - kt0 + 1 : 0;
-    if (ntiles == 0 && p.num_parts > 1) return;
-    // (draft, head) of a row, and its index in q, out and lse
-    auto row_unit = [&](int r) {
-        const int i = rt * kTile + r, t = i / G;
-        return (int64_t)(rq.q_start + t) * p.num_qo_heads + g * G + (i - t * G);
-    };
-    if (ntiles == 0) {  // no key at all: zeros, and the sink alone
-        for (int i = threadIdx.x; i < nrows * (Dh / 8); i += C::THREADS) {
-            const int r = i / (Dh / 8), c = i - r * (Dh / 8);
-            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + row_unit(r) * Dh +
-                                       c * 8) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        if (p.lse_out)
-            for (int r = threadIdx.x; r < nrows; r += C::THREADS)
-                p.lse_out[row_unit(r)] =
-                    p.sink ? p.sink[g * G + (rt * kTile + r) % G] : kNegInf;
-        return;
-    }
+    const int Hkv = p.num_kv_heads, G = p.group, Dh = p.head_dim;
+    const int g = blockIdx.x % Hkv, group = blockIdx.x / Hkv;
+    const int BS = p.block_size, bs_shift = BS == 32 ? 5 : 4, npg = kTile >> bs_shift;
 
-    // ---- set-up: barriers, TMEM, depths; the first loads of the Q rows (softmax
-    // warps, 32 rows each, LPR lanes per row) and of the page ids are in flight
-    // meanwhile: beside 150 streaming SMs a load takes microseconds
-    const int BS = p.block_size, npg = kTile / BS;
-    const int32_t *bt = p.block_table + (int64_t)b * p.max_blocks_per_seq;
-    const int pg_first = tok_lo / BS, pg_last = (tok_hi - 1) / BS;
-    // lane l < npg: the id of page l of tile j, `none` where no key is attended
-    auto page_id = [&](int j, int none) {
-        const int pg = (kt0 + j) * npg + lane;
-        return lane < npg && pg >= pg_first && pg <= pg_last ? bt[pg] : none;
-    };
-    int id = page_id(0, warp < 4 * X ? 0 : -1);
-    constexpr int LPR = T / 8 < 32 ? T / 8 : 32, RPS = 32 / LPR;  // lanes per row, rows per step
-    constexpr int STEPS = 32 / RPS < 16 ? 32 / RPS : 16;          // steps in flight
-    const int64_t unit = warp < 4 * X && (int)threadIdx.x < nrows ? row_unit(threadIdx.x) : 0;
-    const __nv_bfloat16 *qc = static_cast<const __nv_bfloat16 *>(p.q) + (lane % LPR) * 8;
-    uint4 qv[STEPS];
-    auto load_q = [&](int s0) {
-#pragma unroll
-        for (int k = 0; k < STEPS; ++k) {
-            const int rr = (s0 + k) * RPS + lane / LPR;
-            const int64_t u = __shfl_sync(0xffffffffu, unit, rr);
-            qv[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (warp * 32 + rr < nrows && (lane % LPR) * 8 < Dh)
-                qv[k] = __ldg(reinterpret_cast<const uint4 *>(qc + u * Dh));
-        }
-    };
-    if (warp < 4 * X) load_q(0);
+    // ---- set-up: barriers and TMEM
     if (threadIdx.x == 32 * C::W_TMA) {
         constexpr int kFill = KV8 ? C::DW : 1;  // arrivals that fill a tile
         for (int i = 0; i < C::KB; ++i) {
@@ -249,19 +241,22 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(C::B_SFULL + i), 1);
             mbar_init(bar(C::B_PFULL + i), 4);
-            mbar_init(bar(C::B_O + i), 1);
             mbar_init(bar(C::B_POISON + i), kFill);
             mbar_init(bar(C::B_FACT + i), 1);
         }
+        mbar_init(bar(C::B_O), 1);
         mbar_init(bar(C::B_LAND), 1);
         mbar_init(bar(C::B_Q), 4 * X);
         for (int i = 0; i < C::RU; ++i) {
             mbar_init(bar(C::B_RFULL + i), 1 + 8);
             mbar_init(bar(C::B_REMPTY + i), C::DW);
         }
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(bar(C::B_IFULL + i), 1);
+            mbar_init(bar(C::B_IEMPTY + i), 4 * X + 1 + C::DW);
+        }
         fence_barrier_init();
         *s_abort = 0;
-        *s_maxdepth = 0;
         tma_prefetch_desc(&tmk);
         tma_prefetch_desc(&tmv);
     }
@@ -269,155 +264,265 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         tc::tmem_alloc(base + C::OFF_MISC, C::TMEM);
         tc::tmem_relinquish();
     }
-    const bool positions = p.depth && (p.window_left >= 0 || p.alibi);
-    if (positions) {
-        __syncthreads();  // s_maxdepth is zero
-        for (int i = threadIdx.x; i < rq.q_len; i += C::THREADS) {
-            const int d = min(max(p.depth[rq.q_start + i], 0), 65535);
-            s_depth[i] = (uint16_t)d;
-            atomicMax(s_maxdepth, d);
-        }
-    }
     tc::fence_before_sync();
-    if (warp == C::W_TMA && !positions) {
-        // the barriers are this warp's own work: it starts loading, and only
-        // announces that they are there
+    if (warp == C::W_TMA) {
+        // the barriers are this warp's own work: it goes on, and only announces
+        // that they are there
         __syncwarp();
         asm volatile("barrier.cta.arrive 1, %0;" ::"n"(C::THREADS) : "memory");
-    } else if (!positions) {
-        asm volatile("barrier.cta.sync 1, %0;" ::"n"(C::THREADS) : "memory");
     } else {
-        __syncthreads();
+        asm volatile("barrier.cta.sync 1, %0;" ::"n"(C::THREADS) : "memory");
     }
     tc::fence_after_sync();
     const uint32_t tmem = warp == C::W_TMA ? 0u : misc[0];
 
-    // every row sees keys [wfull, ctx)
-    const int wfull = p.window_left < 0 || !positions
-                          ? 0
-                          : (int)max((long long)rq.ctx + *s_maxdepth - p.window_left, 0LL);
-    auto partial = [&](int i) {  // some row does not see some key of tile i
-        const int k0 = (kt0 + i) * kTile;
-        return k0 < tok_lo || k0 < wfull || k0 + kTile > tok_hi || k0 + kTile > rq.ctx;
+    // Segment n of this CTA lies in slot n % kRing of the ring, where the warps
+    // read it until they release it; null: none left, or a wait gave up.
+    auto segment = [&](int n) -> const Seg * {
+        const int s = n % kRing;
+        if (!warp_wait_bounded(bar(C::B_IFULL + s), (uint32_t)(n / kRing) & 1u, p.dev_error,
+                               s_abort) ||
+            ring[s].slot_b < 0)
+            return nullptr;
+        return ring + s;
     };
-
+    auto release = [&](int n) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::B_IEMPTY + n % kRing));
+    };
+    // lane l < npg: the id of page l of tile j, `none` where no key is attended
+    auto page_id = [&](const Seg &sg, int j, int none) {
+        const int pg = (sg.tile0 + j) * npg + lane;
+        return lane < npg && pg >= sg.tok_lo >> bs_shift && pg <= (sg.tok_hi - 1) >> bs_shift
+                   ? p.block_table[(int64_t)sg.b() * p.max_blocks_per_seq + pg]
+                   : none;
+    };
     if (warp == C::W_TMA) {
-        // ------------------------------------------------------------ producer
+        // ------------------------------------------------------------ segments, loads
+        constexpr int kRows = X * kTile;
+        const int groups = gridDim.x / Hkv;
+        // the line's length; the requests' places on it go to the merge kernel
+        long long total = 0;
+        for (int b0 = 0; b0 < p.batch; b0 += 32) {
+            long long c = 0;
+            if (b0 + lane < p.batch)
+                c = cost_of(p, request(p, b0 + lane, blockIdx.x == 0), kRows).total();
+            long long incl = c;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const long long o = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += o;
+            }
+            if (blockIdx.x == 0 && b0 + lane < p.batch)
+                p.line[b0 + lane] = total + incl - c;
+            total += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        const long long share =
+            max((total + groups - 1) / groups, (long long)p.min_tiles);
+        if (blockIdx.x == 0 && lane == 0) {
+            p.line[p.batch] = total;
+            p.line[p.batch + 1] = share;
+        }
+        const long long lo = min(share * group, total), hi = min(lo + share, total);
+
         // box coordinates of (page, kv head); one past the pool reads zeros
-        const int oob = p.hnd ? (int)(p.num_blocks * p.num_kv_heads)
-                              : (int)(p.num_blocks * BS);
+        const int oob = p.hnd ? (int)(p.num_blocks * Hkv) : (int)(p.num_blocks * BS);
         const int cy = p.hnd ? 0 : g;
         bool alive = true;
-        int nk = 0, nv = 0, nfix = 0;
-        for (int i = 0; i < ntiles && alive; ++i) {
-            const int pg = (kt0 + i) * npg + lane;
-            int row = oob;
-            if (lane < npg && pg >= pg_first && pg <= pg_last) {
-                if (id < 0 || id >= p.num_blocks) {
-                    flag_error(p.dev_error, PKV_DEVERR_BLOCK_ID);
-                    id = -1;
-                } else {
-                    row = p.hnd ? id * p.num_kv_heads + g : id * BS;
-                }
-            }
-            const int id_now = id;
-            if (i + 1 < ntiles) id = page_id(i + 1, -1);
-            if constexpr (!KV8) {
-                const int ks = i % C::KB, vs = i % C::VB;
-                // lane -> (page, 64-dim half)
-                const int lp = lane / C::HALVES, lh = lane % C::HALVES;
-                const int brow = __shfl_sync(0xffffffffu, row, lp);
-                alive = warp_wait_bounded(bar(C::B_KEMPTY + ks),
-                                          ((uint32_t)(i / C::KB) & 1u) ^ 1u, p.dev_error,
-                                          s_abort);
-                if (!alive) break;
-                if (lane == 0) mbar_arrive_expect_tx(bar(C::B_KFULL + ks), C::TILE);
-                __syncwarp();
-                if (lp < npg)
-                    tma_load_3d(base + C::OFF_K + ks * C::TILE + lh * C::HALF + lp * BS * 128,
-                                &tmk, bar(C::B_KFULL + ks), lh * 64, cy, brow);
-                ++nk;
-                alive = warp_wait_bounded(bar(C::B_VEMPTY + vs),
-                                          ((uint32_t)(i / C::VB) & 1u) ^ 1u, p.dev_error,
-                                          s_abort);
-                if (!alive) break;
-                const bool fix = partial(i);
-                const uint32_t vbar = fix ? bar(C::B_LAND) : bar(C::B_VFULL + vs);
-                const uint32_t vb = base + C::OFF_V + vs * C::TILE;
-                if (lane == 0) mbar_arrive_expect_tx(vbar, C::TILE);
-                __syncwarp();
-                if (lp < npg)
-                    tma_load_3d(vb + lh * C::HALF + lp * BS * 128, &tmv, vbar, lh * 64, cy,
-                                brow);
-                ++nv;
-                if (fix) {
-                    alive = warp_wait_bounded(bar(C::B_LAND), (uint32_t)nfix & 1u, p.dev_error,
-                                              s_abort);
-                    ++nfix;
-                    if (!alive) break;
-                    // lane owns rows lane, lane + 32, ..: rows outside the range
-                    // are zeroed, and rows with an infinity or a NaN, noted
-                    uint32_t *pois = s_poison + ((nfix - 1) & 1) * 4;
-                    const int k0 = (kt0 + i) * kTile;
-#pragma unroll 1
-                    for (int w = 0; w < 4; ++w) {
-                        const int r = w * 32 + lane, key = k0 + r;
-                        const bool in = key >= tok_lo && key < tok_hi;
-                        bool bad = false;
-                        if (in) {
-#pragma unroll 4
-                            for (int c = 0; c < T / 8; ++c) {
-                                const uint4 v =
-                                    ld_shared16(vb + (c >> 3) * C::HALF + sw128(r, c & 7));
-                                const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    bad |= (x[e] & 0x7f80u) == 0x7f80u ||
-                                           (x[e] & 0x7f800000u) == 0x7f800000u;
-                            }
-                        }
-                        if (!in || bad)
-                            for (int c = 0; c < T / 8; ++c)
-                                st_shared_zero16(vb + (c >> 3) * C::HALF + sw128(r, c & 7));
-                        const uint32_t m = __ballot_sync(0xffffffffu, in && bad);
-                        if (lane == 0) pois[w] = m;
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar(C::B_POISON + ((nfix - 1) & 1)));
-                        mbar_arrive(bar(C::B_VFULL + vs));
+        int nk = 0, nv = 0, nfix = 0;  // tiles (8-bit: raw tiles) and repaired tiles so far
+        uint32_t landed = 0;           // bit i: the last use of V buffer i was a repaired tile
+        auto load_segment = [&](const Seg &sg) {
+            const int tok_lo = sg.tok_lo, tok_hi = sg.tok_hi;
+            int id = page_id(sg, 0, -1);
+            for (int i = 0; i < sg.ntiles && alive; ++i) {
+                const int pg = (sg.tile0 + i) * npg + lane;
+                int row = oob;
+                if (lane < npg && pg >= tok_lo >> bs_shift && pg <= (tok_hi - 1) >> bs_shift) {
+                    if (id < 0 || id >= p.num_blocks) {
+                        flag_error(p.dev_error, PKV_DEVERR_BLOCK_ID);
+                        id = -1;
+                    } else {
+                        row = p.hnd ? id * Hkv + g : id * BS;
                     }
                 }
-            } else {
-                constexpr int PARTS = T / C::ROWB;  // boxes across the head size
-                const int lp = lane / PARTS, lh = lane % PARTS;
-                const int brow = __shfl_sync(0xffffffffu, row, lp);
-                // scale bytes: lane l < 8 copies bytes 16 l .. of the tile
-                const int sid = __shfl_sync(0xffffffffu, id_now, (lane * 16 / BS) & 31);
-                for (int v = 0; v < 2 && alive; ++v) {
-                    const int u = 2 * i + v, s = u % C::RU;
-                    const uint32_t full = bar(C::B_RFULL + s);
-                    alive = warp_wait_bounded(bar(C::B_REMPTY + s),
-                                              ((uint32_t)(u / C::RU) & 1u) ^ 1u, p.dev_error,
+                const int id_now = id;
+                if (i + 1 < sg.ntiles) id = page_id(sg, i + 1, -1);
+                if constexpr (!KV8) {
+                    const int ks = nk % C::KB, vs = nv % C::VB;
+                    // lane -> (page, 64-dim half)
+                    const int lp = lane / C::HALVES, lh = lane % C::HALVES;
+                    const int brow = __shfl_sync(0xffffffffu, row, lp);
+                    alive = warp_wait_bounded(bar(C::B_KEMPTY + ks),
+                                              ((uint32_t)(nk / C::KB) & 1u) ^ 1u, p.dev_error,
                                               s_abort);
                     if (!alive) break;
-                    if (lane == 0) mbar_arrive_expect_tx(full, C::RAW);
+                    if (lane == 0) mbar_arrive_expect_tx(bar(C::B_KFULL + ks), C::TILE);
                     __syncwarp();
                     if (lp < npg)
-                        tma_load_3d(base + C::OFF_RAW + s * C::RAW +
-                                        lh * (kTile * C::ROWB) + lp * BS * C::ROWB,
-                                    v ? &tmv : &tmk, full, lh * 128, cy, brow);
-                    if (lane < 8) {
-                        if (sid >= 0)
-                            cp_async16(base + C::OFF_SCALE + s * kTile + lane * 16,
-                                       (v ? p.v_scale : p.k_scale) +
-                                           ((int64_t)sid * p.num_kv_heads + g) * BS +
-                                           (lane * 16) % BS);
-                        cp_async_arrive(full);
-                    }
+                        tma_load_3d(base + C::OFF_K + ks * C::TILE + lh * C::HALF + lp * BS * 128,
+                                    &tmk, bar(C::B_KFULL + ks), lh * 64, cy, brow);
                     ++nk;
+                    alive = warp_wait_bounded(bar(C::B_VEMPTY + vs),
+                                              ((uint32_t)(nv / C::VB) & 1u) ^ 1u, p.dev_error,
+                                              s_abort);
+                    if (!alive) break;
+                    const bool fix = sg.partial(i);
+                    landed = fix ? landed | 1u << vs : landed & ~(1u << vs);
+                    const uint32_t vbar = fix ? bar(C::B_LAND) : bar(C::B_VFULL + vs);
+                    const uint32_t vb = base + C::OFF_V + vs * C::TILE;
+                    if (lane == 0) mbar_arrive_expect_tx(vbar, C::TILE);
+                    __syncwarp();
+                    if (lp < npg)
+                        tma_load_3d(vb + lh * C::HALF + lp * BS * 128, &tmv, vbar, lh * 64, cy,
+                                    brow);
+                    ++nv;
+                    if (fix) {
+                        alive = warp_wait_bounded(bar(C::B_LAND), (uint32_t)nfix & 1u, p.dev_error,
+                                                  s_abort);
+                        ++nfix;
+                        if (!alive) break;
+                        // lane owns rows lane, lane + 32, ..: rows outside the range
+                        // are zeroed, and rows with an infinity or a NaN, noted
+                        uint32_t *pois = s_poison + ((nfix - 1) & 1) * 4;
+                        const int k0 = (sg.tile0 + i) * kTile;
+#pragma unroll 1
+                        for (int w = 0; w < 4; ++w) {
+                            const int r = w * 32 + lane, key = k0 + r;
+                            const bool in = key >= tok_lo && key < tok_hi;
+                            bool bad = false;
+                            if (in) {
+#pragma unroll 4
+                                for (int c = 0; c < T / 8; ++c) {
+                                    const uint4 v =
+                                        ld_shared16(vb + (c >> 3) * C::HALF + sw128(r, c & 7));
+                                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        bad |= (x[e] & 0x7f80u) == 0x7f80u ||
+                                               (x[e] & 0x7f800000u) == 0x7f800000u;
+                                }
+                            }
+                            if (!in || bad)
+                                for (int c = 0; c < T / 8; ++c)
+                                    st_shared_zero16(vb + (c >> 3) * C::HALF + sw128(r, c & 7));
+                            const uint32_t m = __ballot_sync(0xffffffffu, in && bad);
+                            if (lane == 0) pois[w] = m;
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(bar(C::B_POISON + ((nfix - 1) & 1)));
+                            mbar_arrive(bar(C::B_VFULL + vs));
+                        }
+                    }
+                } else {
+                    constexpr int PARTS = T / C::ROWB;  // boxes across the head size
+                    const int lp = lane / PARTS, lh = lane % PARTS;
+                    const int brow = __shfl_sync(0xffffffffu, row, lp);
+                    // scale bytes: lane l < 8 copies bytes 16 l .. of the tile
+                    const int sid = __shfl_sync(0xffffffffu, id_now, (lane * 16 >> bs_shift) & 31);
+                    for (int v = 0; v < 2 && alive; ++v) {
+                        const int s = nk % C::RU;
+                        const uint32_t full = bar(C::B_RFULL + s);
+                        alive = warp_wait_bounded(bar(C::B_REMPTY + s),
+                                                  ((uint32_t)(nk / C::RU) & 1u) ^ 1u, p.dev_error,
+                                                  s_abort);
+                        if (!alive) break;
+                        if (lane == 0) mbar_arrive_expect_tx(full, C::RAW);
+                        __syncwarp();
+                        if (lp < npg)
+                            tma_load_3d(base + C::OFF_RAW + s * C::RAW +
+                                            lh * (kTile * C::ROWB) + lp * BS * C::ROWB,
+                                        v ? &tmv : &tmk, full, lh * 128, cy, brow);
+                        if (lane < 8) {
+                            if (sid >= 0)
+                                cp_async16(base + C::OFF_SCALE + s * kTile + lane * 16,
+                                           (v ? p.v_scale : p.k_scale) +
+                                               ((int64_t)sid * Hkv + g) * BS +
+                                               (lane * 16) % BS);
+                            cp_async_arrive(full);
+                        }
+                        ++nk;
+                    }
                 }
+            }
+            return alive;
+        };
+        int nseg = 0;
+        long long place = 0;           // where the chunk's first request begins
+        for (int b0 = 0; b0 < p.batch && place < hi && alive; b0 += 32) {
+            Req mine = {0, 0, 0};
+            long long c = 0;
+            if (b0 + lane < p.batch) {
+                mine = request(p, b0 + lane, false);
+                c = cost_of(p, mine, kRows).total();
+            }
+            long long incl = c;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const long long o = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += o;
+            }
+            const long long first = place + incl - c;
+            place += __shfl_sync(0xffffffffu, incl, 31);
+            // the requests of this chunk that meet [lo, hi)
+            uint32_t meet = __ballot_sync(0xffffffffu, c > 0 && first < hi && first + c > lo);
+            for (; meet && alive; meet &= meet - 1) {
+                const int src = __ffs(meet) - 1;
+                Req rq;
+                rq.q_start = __shfl_sync(0xffffffffu, mine.q_start, src);
+                rq.q_len = __shfl_sync(0xffffffffu, mine.q_len, src);
+                rq.L = __shfl_sync(0xffffffffu, mine.L, src);
+                const long long at = __shfl_sync(0xffffffffu, first, src);
+                const Cost co = cost_of(p, rq, kRows);
+                const int start = rq.start(p.window_left);
+                int wfull = 0;
+                if (p.window_left >= 0) {  // the deepest draft bounds what all rows see
+                    int d = 0;
+                    for (int i = lane; i < rq.q_len; i += 32) d = max(d, p.depth[rq.q_start + i]);
+                    d = __reduce_max_sync(0xffffffffu, d);
+                    wfull = (int)min(max((long long)rq.ctx() + d - p.window_left, 0LL),
+                                     (long long)rq.L);
+                }
+                for (int rg = 0; rg < co.groups && alive; ++rg) {
+                    const long long s = at + (long long)rg * co.tiles, e = s + co.tiles;
+                    if (e <= lo || s >= hi) continue;
+                    const int t0 = (int)(max(s, lo) - s), t1 = (int)(min(e, hi) - s);
+                    Seg sg;
+                    sg.q_start = rq.q_start;
+                    sg.q_len = rq.q_len;
+                    sg.ctx = rq.ctx();
+                    sg.row0 = rg * kRows;
+                    sg.nrows = min(rq.q_len * G - sg.row0, kRows);
+                    sg.tile0 = start / kTile + t0;
+                    sg.ntiles = rq.L > start ? t1 - t0 : 0;
+                    sg.tok_lo = max(sg.tile0 * kTile, start);
+                    sg.tok_hi =
+                        (int)min((long long)(sg.tile0 + sg.ntiles) * kTile, (long long)rq.L);
+                    sg.full_lo = (max(sg.tok_lo, wfull) + kTile - 1) / kTile - sg.tile0;
+                    sg.full_hi = min(sg.tok_hi, sg.ctx) / kTile - sg.tile0;
+                    sg.slot_b = 4 * (b0 + src) + (lo > s ? 1 : hi < e ? 2 : 0);
+                    const int rs = nseg % kRing;
+                    alive = warp_wait_bounded(bar(C::B_IEMPTY + rs),
+                                              ((uint32_t)(nseg / kRing) & 1u) ^ 1u, p.dev_error,
+                                              s_abort);
+                    if (!alive) break;
+                    if (lane == 0) {
+                        ring[rs] = sg;
+                        mbar_arrive(bar(C::B_IFULL + rs));
+                    }
+                    ++nseg;
+                    if (sg.ntiles > 0) alive = load_segment(sg);
+                }
+            }
+        }
+        if (alive) {  // no more
+            const int rs = nseg % kRing;
+            alive = warp_wait_bounded(bar(C::B_IEMPTY + rs),
+                                      ((uint32_t)(nseg / kRing) & 1u) ^ 1u, p.dev_error, s_abort);
+            if (alive && lane == 0) {
+                ring[rs].slot_b = -1;
+                mbar_arrive(bar(C::B_IFULL + rs));
             }
         }
         if (!alive) {  // a wait gave up: let the copies in flight land (bounded)
@@ -426,10 +531,10 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     warp_wait_bounded(bar(C::B_KFULL + i % C::KB), (uint32_t)(i / C::KB) & 1u,
                                       p.dev_error);
                 for (int i = max(0, nv - C::VB); i < nv; ++i)
-                    if (!partial(i))
+                    if (!((landed >> (i % C::VB)) & 1u))
                         warp_wait_bounded(bar(C::B_VFULL + i % C::VB),
                                           (uint32_t)(i / C::VB) & 1u, p.dev_error);
-                if (nv > 0 && partial(nv - 1) && nfix > 0)
+                if (nfix > 0)
                     warp_wait_bounded(bar(C::B_LAND), (uint32_t)(nfix - 1) & 1u, p.dev_error);
             } else {
                 for (int u = max(0, nk - C::RU); u < nk; ++u)
@@ -449,94 +554,133 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         const uint64_t dv0 = tc::smem_desc_sw128(base + C::OFF_V, C::HALF, 1024);
         // One thread issues, and spends as little as it can between two products:
         // the tensor pipe runs dry meanwhile (buffer indexes and phases are
-        // counted, not divided out; K's barrier is looked at ahead of need).
-        if (lane == 0) {
-            auto wait = [&](int i, uint32_t phase) {
-                return mbar_wait_bounded(bar(i), phase, p.dev_error, s_abort);
-            };
-            int sx = 0, ks = 0;      // row tile and K buffer of the next S
-            uint32_t kph = 0;        // and that buffer's phase
-            bool k_ready = false;
-            auto issue_s = [&](int n) {
-                if (!k_ready && !wait(C::B_KFULL + ks, kph)) return false;
-                k_ready = true;
-                tc::fence_after_sync();
-                const uint64_t dq = dq0 + (uint64_t)((sx * C::TILE) >> 4);
-                const uint64_t dk = dk0 + (uint64_t)((ks * C::TILE) >> 4);
-                const uint32_t d = tmem + (n & 1) * 128;
-                if constexpr (T == 128) {
-                    tc::mma_ss8<C::HALF>(d, dq, dk, idS, 0u);
-                } else {
+        // counted, not divided out).
+        auto wait = [&](int i, uint32_t phase) {
+            return mbar_wait_bounded(bar(i), phase, p.dev_error, s_abort);
+        };
+        int ks = 0, vs = 0;             // K buffer of the next S, V buffer of the next O
+        uint32_t kph = 0, vph = 0;      // and their phases
+        int un = 0;                     // units so far
+        bool alive = true;
+        for (int ns = 0; alive; ++ns) {
+            const Seg *sg = segment(ns);
+            if (!sg) break;
+            const int nx = sg->nrows > kTile ? 2 : 1, total = sg->ntiles * nx;
+            release(ns);
+            if (lane == 0) {
+                int sx = 0;             // row tile of the next S
+                bool k_ready = false;
+                auto issue_s = [&](int n) {
+                    if (!k_ready && !wait(C::B_KFULL + ks, kph)) return false;
+                    k_ready = true;
+                    tc::fence_after_sync();
+                    const uint64_t dq = dq0 + (uint64_t)((sx * C::TILE) >> 4);
+                    const uint64_t dk = dk0 + (uint64_t)((ks * C::TILE) >> 4);
+                    const uint32_t d = tmem + (n & 1) * 128;
+                    if constexpr (T == 128) {
+                        tc::mma_ss8<C::HALF>(d, dq, dk, idS, 0u);
+                    } else {
 #pragma unroll
-                    for (int h = 0; h < C::HALVES; ++h)
+                        for (int h = 0; h < C::HALVES; ++h)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t off = (h * C::HALF + k * 32) >> 4;
-                            tc::mma_ss(d, dq + off, dk + off, idS, h + k > 0 ? 1u : 0u);
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t off = (h * C::HALF + k * 32) >> 4;
+                                tc::mma_ss(d, dq + off, dk + off, idS, h + k > 0 ? 1u : 0u);
+                            }
+                    }
+                    tc::commit(bar(C::B_SFULL + (n & 1)));
+                    if (++sx == nx) {
+                        tc::commit(bar(C::B_KEMPTY + ks));
+                        sx = 0;
+                        k_ready = false;
+                        if (++ks == C::KB) {
+                            ks = 0;
+                            kph ^= 1u;
                         }
-                }
-                tc::commit(bar(C::B_SFULL + (n & 1)));
-                if (++sx == nx) {
-                    tc::commit(bar(C::B_KEMPTY + ks));
-                    sx = 0;
-                    k_ready = false;
-                    if (++ks == C::KB) {
-                        ks = 0;
-                        kph ^= 1u;
                     }
-                }
-                return true;
-            };
-            const int total = ntiles * nx;
-            bool alive = wait(C::B_Q, 0) && issue_s(0) && (total == 1 || issue_s(1));
-            int j = 0, x = 0, vs = 0;
-            uint32_t vph = 0;
-            for (int n = 0; n < total && alive; ++n) {
-                alive = wait(C::B_PFULL + (n & 1), (uint32_t)(n >> 1) & 1u) &&
-                        (x > 0 || wait(C::B_VFULL + vs, vph));
-                if (!alive) break;
-                tc::fence_after_sync();
-                const uint64_t dv = dv0 + (uint64_t)((vs * C::TILE) >> 4);
-                tc::mma_ts8(tmem + 256 + x * T, tmem + (n & 1) * 128, dv, idO, j > 0 ? 1u : 0u);
-                const bool last = j + 1 == ntiles;
-                const int ox = x;
-                if (++x == nx) {
-                    tc::commit(bar(C::B_VEMPTY + vs));
-                    x = 0;
-                    ++j;
-                    if (++vs == C::VB) {
-                        vs = 0;
-                        vph ^= 1u;
+                    return true;
+                };
+                alive = wait(C::B_Q, (uint32_t)ns & 1u);
+                if (alive && total > 0) alive = issue_s(un);
+                if (alive && total > 1) alive = issue_s(un + 1);
+                int x = 0;
+                for (int i = 0; i < total && alive; ++i) {
+                    const int n = un + i;
+                    alive = wait(C::B_PFULL + (n & 1), (uint32_t)(n >> 1) & 1u) &&
+                            (x > 0 || wait(C::B_VFULL + vs, vph));
+                    if (!alive) break;
+                    tc::fence_after_sync();
+                    const uint64_t dv = dv0 + (uint64_t)((vs * C::TILE) >> 4);
+                    tc::mma_ts8(tmem + 256 + x * T, tmem + (n & 1) * 128, dv, idO,
+                                i >= nx ? 1u : 0u);
+                    if (++x == nx) {
+                        tc::commit(bar(C::B_VEMPTY + vs));
+                        x = 0;
+                        if (++vs == C::VB) {
+                            vs = 0;
+                            vph ^= 1u;
+                        }
                     }
+                    if (i + 2 < total) alive = issue_s(n + 2);
                 }
-                if (last) tc::commit(bar(C::B_O + ox));
-                if (n + 2 < total) alive = issue_s(n + 2);
+                tc::commit(bar(C::B_O));  // (with nothing in flight it arrives at once)
+                un += total;
+                // a wait gave up: let the products in flight finish (bounded)
+                if (!alive) mbar_wait_bounded(bar(C::B_O), (uint32_t)ns & 1u, p.dev_error);
             }
-            if (!alive) {  // let the products in flight finish (bounded) before TMEM goes
-                tc::commit(bar(C::B_O));
-                mbar_wait_bounded(bar(C::B_O), 0, p.dev_error);
-            }
+            alive = __shfl_sync(0xffffffffu, alive ? 1 : 0, 0) != 0;
         }
         __syncwarp();
     } else if (warp < 4 * X) {
         // ------------------------------------------------------------ softmax
         const int x = warp >> 2;             // row tile
         const int r = threadIdx.x;           // row of the CTA; TMEM lane r % 128
-        const bool warp_on = warp * 32 < nrows;
-        const bool row_on = r < nrows;
-        const int node = row_on ? (rt * kTile + r) / G : 0;
-        const int head = row_on ? g * G + (rt * kTile + r) % G : 0;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_o = tmem + 256 + x * T + lane_base;
+        const uint32_t sq = base + C::OFF_Q + x * C::TILE;
+        // Q: this warp's 32 rows, LPR lanes per row, STEPS steps in flight.  Beside
+        // 150 streaming SMs a load takes microseconds, so the next segment's rows
+        // are asked for before the last one's are stored.
+        constexpr int LPR = T / 8 < 32 ? T / 8 : 32, RPS = 32 / LPR;
+        constexpr int STEPS = 32 / RPS < 16 ? 32 / RPS : 16;
+        uint4 qv[STEPS];
+        // (draft, head) of this thread's row, as its index in q, out and lse
+        auto unit_of = [&](const Seg &sg) {
+            const int i = sg.row0 + min(r, sg.nrows - 1), tok = i / G;
+            return (int64_t)(sg.q_start + tok) * p.num_qo_heads + g * G + (i - tok * G);
+        };
+        auto load_q = [&](const Seg &sg, int s0) {
+            const int64_t unit = unit_of(sg);
+            const __nv_bfloat16 *qc =
+                static_cast<const __nv_bfloat16 *>(p.q) + (lane % LPR) * 8;
+            const int nrows = sg.nrows;
+#pragma unroll
+            for (int k = 0; k < STEPS; ++k) {
+                const int rr = (s0 + k) * RPS + lane / LPR;
+                const int64_t u = __shfl_sync(0xffffffffu, unit, rr);
+                qv[k] = make_uint4(0u, 0u, 0u, 0u);
+                if (warp * 32 + rr < nrows && (lane % LPR) * 8 < Dh)
+                    qv[k] = __ldg(reinterpret_cast<const uint4 *>(qc + u * Dh));
+            }
+        };
+        const bool positions = p.window_left >= 0 || p.alibi;
+        int un = 0, jt = 0, nfix = 0;        // units, key tiles and repaired tiles so far
+        bool alive = true;
+        const Seg *sp = segment(0);
+        if (sp) load_q(*sp, 0);
+        for (int ns = 0; sp && alive; ++ns) {
+        const Seg &sg = *sp;                 // stays in the ring until it is released
+        const int ntiles = sg.ntiles, nx = sg.nrows > kTile ? 2 : 1;
+        const int full_lo = sg.full_lo, full_hi = sg.full_hi;
+        const bool warp_on = warp * 32 < sg.nrows, row_on = r < sg.nrows;
         // ---- this warp's rows of Q into shared memory (rows past the last: zeros)
         float rowf = fabsf(p.scale_log2);  // score = S * rowf
         {
-            const uint32_t sq = base + C::OFF_Q + x * C::TILE;
             const uint32_t neg = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // its sign goes into q
             const int c = lane % LPR;
 #pragma unroll 1
             for (int s0 = 0; s0 < 32 / RPS; s0 += STEPS) {
-                if (s0 > 0) load_q(s0);
+                if (s0 > 0) load_q(sg, s0);
 #pragma unroll
                 for (int k = 0; k < STEPS; ++k) {
                     uint32_t w[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
@@ -574,20 +718,19 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         // scale.  m_ref follows the row's largest score (there plus that scale
         // over 2^10, so that f16 holds the product); O and l share it.
         float m_ref = kNegInf, l = 0.f;
-        bool alive = true;
-        int nfix = 0;
+        int id = warp_on && ntiles > 0 ? page_id(sg, 0, 0) : 0;
         for (int j = 0; j < ntiles && x < nx; ++j) {
-            const int n = j * nx + x;
+            const int n = un + j * nx + x, jn = jt + j;
             const uint32_t t_s = tmem + (n & 1) * 128 + lane_base;
-            const bool fix = partial(j);
+            const bool fix = j < full_lo || j >= full_hi;
             const uint32_t badpg =
                 __ballot_sync(0xffffffffu, id < 0 || (int64_t)id >= p.num_blocks);
-            if (warp_on && j + 1 < ntiles) id = page_id(j + 1, 0);
+            if (warp_on && j + 1 < ntiles) id = page_id(sg, j + 1, 0);
             const bool general = fix || badpg != 0 || p.alibi != nullptr;
             alive = warp_wait_bounded(bar(C::B_SFULL + (n & 1)), (uint32_t)(n >> 1) & 1u,
                                       p.dev_error, s_abort);
             if (KV8 && alive)
-                alive = warp_wait_bounded(bar(C::B_FACT + (j & 1)), (uint32_t)(j >> 1) & 1u,
+                alive = warp_wait_bounded(bar(C::B_FACT + (jn & 1)), (uint32_t)(jn >> 1) & 1u,
                                           p.dev_error, s_abort);
             if (fix && alive) {
                 alive = warp_wait_bounded(bar(C::B_POISON + (nfix & 1)),
@@ -599,7 +742,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                 tc::fence_after_sync();
                 float rf = rowf, vexp = 0.f, shift = 0.f;
                 if constexpr (KV8) {
-                    const volatile uint32_t *by = s_byte + (j & 1) * 2;
+                    const volatile uint32_t *by = s_byte + (jn & 1) * 2;
                     rf *= scale_value(by[0]);
                     vexp = (float)((int)by[1] - 127);
                     shift = vexp - kWeightExp;
@@ -608,20 +751,25 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                 // -inf for what the row does not see, NaN for a key whose V row is
                 // not finite.
                 auto complete = [&](int c, uint32_t (&v)[32]) {
-                    const int depth = positions ? s_depth[node] : 0, qpos = rq.ctx + depth;
+                    const int i = sg.row0 + min(r, sg.nrows - 1), node = i / G;
+                    const int ctx = sg.ctx, tok_lo = sg.tok_lo, tok_hi = sg.tok_hi;
+                    auto depth_of = [&](int k) {  // a draft's depth
+                        return positions ? min(max(p.depth[sg.q_start + k], 0), 65535) : 0;
+                    };
+                    const int depth = depth_of(node), qpos = ctx + depth;
                     const int wlo = p.window_left < 0 ? 0 : max(qpos - p.window_left, 0);
-                    const int kc = (kt0 + j) * kTile + 32 * c;
-                    uint32_t vis = range_bits(max(wlo, tok_lo) - kc, min(rq.ctx, tok_hi) - kc);
-                    const int n0 = kc - rq.ctx;  // draft node of the chunk's first key
-                    if (n0 > -32 && n0 < rq.q_len && row_on) {
-                        const int64_t *mrow =
-                            p.mask + (int64_t)(rq.q_start + node) * p.mask_words;
-                        uint32_t d = mask_bits(mrow, p.mask_words, n0) &
-                                     range_bits(max(tok_lo, rq.ctx) - kc, tok_hi - kc);
+                    const int kc = (sg.tile0 + j) * kTile + 32 * c;
+                    uint32_t vis = range_bits(max(wlo, tok_lo) - kc, min(ctx, tok_hi) - kc);
+                    const int n0 = kc - ctx;  // draft node of the chunk's first key
+                    if (n0 > -32 && n0 < sg.q_len && row_on) {
+                        uint32_t d =
+                            mask_bits(p.mask + (int64_t)(sg.q_start + node) * p.mask_words,
+                                      p.mask_words, n0);
+                        d &= range_bits(max(tok_lo, ctx) - kc, tok_hi - kc);
                         if (p.window_left >= 0) {
                             for (uint32_t m = d; m; m &= m - 1) {
                                 const int e = __ffs(m) - 1;
-                                if (s_depth[n0 + e] < depth - p.window_left) d &= ~(1u << e);
+                                if (depth_of(n0 + e) < depth - p.window_left) d &= ~(1u << e);
                             }
                         }
                         vis |= d;
@@ -637,12 +785,12 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     for (int e = 0; e < 32; ++e)
                         v[e] = __float_as_uint(__uint_as_float(v[e]) * rf);
                     if (p.alibi) {
-                        const float slope = row_on ? p.alibi[head] * kLog2e : 0.f;
+                        const float slope = p.alibi[g * G + i % G] * kLog2e;
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
                             const int k = kc + e;
-                            const int m = min(max(k - rq.ctx, 0), rq.q_len - 1);
-                            const int kpos = k < rq.ctx ? k : rq.ctx + s_depth[m];
+                            const int m = min(max(k - ctx, 0), sg.q_len - 1);
+                            const int kpos = k < ctx ? k : ctx + depth_of(m);
                             v[e] = __float_as_uint(
                                 fmaf(slope, (float)(kpos - qpos), __uint_as_float(v[e])));
                         }
@@ -684,12 +832,12 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                         m_ref = mt;
                         return true;
                     }
-                    const bool grow = mt > m_ref + kLazy || (m_ref == kNegInf && mt > kNegInf);
+                    const bool grow = mt > m_ref + kLazy<KV8> || (m_ref == kNegInf && mt > kNegInf);
                     if (!__any_sync(0xffffffffu, grow)) return true;
                     if (nx == 1) {  // O must be at rest: the last PV is done
                         // (with two row tiles, S(n) came behind this O's last PV)
-                        if (!warp_wait_bounded(bar(C::B_VEMPTY + (j - 1) % C::VB),
-                                               (uint32_t)((j - 1) / C::VB) & 1u, p.dev_error,
+                        if (!warp_wait_bounded(bar(C::B_VEMPTY + (jn - 1) % C::VB),
+                                               (uint32_t)((jn - 1) / C::VB) & 1u, p.dev_error,
                                                s_abort))
                             return false;
                         tc::fence_after_sync();
@@ -733,7 +881,9 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                         complete(c, v);
                         __syncwarp();
                         mt = maximum(mt, v);
+                        tc::st_32x32b_x32(t_s + 32 * c, v);
                     }
+                    tc::wait_st();
                     alive = refer(mt + shift);
                     if (!alive) break;
                     const float m = (m_ref == kNegInf ? 0.f : m_ref) - vexp;
@@ -742,8 +892,6 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                         uint32_t v[32];
                         tc::ld_32x32b_x32(t_s + 32 * c, v);
                         tc::wait_ld();
-                        complete(c, v);
-                        __syncwarp();
                         sum += weights(c, v, 1.f, m);
                     }
                 }
@@ -754,15 +902,33 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::B_PFULL + (n & 1)));
         }
-        // ---- epilogue
-        if (alive && x < nx)  // the last product of all: K and V tiles are free too
-            alive = warp_wait_bounded(bar(C::B_O + nx - 1), 0, p.dev_error, s_abort);
-        if (alive && warp_on) {
+        un += ntiles * nx;
+        jt += ntiles;
+        if (x >= nx)  // this row tile is empty: its repaired tiles count all the same
+            nfix += ntiles - max(min(full_hi, ntiles) - max(full_lo, 0), 0);
+        // every product of the segment is done: O is at rest and Q's tile free
+        if (alive)
+            alive = warp_wait_bounded(bar(C::B_O), (uint32_t)ns & 1u, p.dev_error, s_abort);
+        if (!alive) break;
+        const Seg *next = segment(ns + 1);
+        // (assigned either way, so that the registers are free in the main loop)
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) qv[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (next) load_q(*next, 0);
+        // ---- the rows' results
+        if (warp_on) {
             tc::fence_after_sync();
+            // partials: [CTA group][its first or last row group][kv head][row]
+            const bool part = sg.cut() != 0;
+            const int64_t prow =
+                ((int64_t)(2 * group + sg.cut() / 2) * Hkv + g) * (X * kTile) + warp * 32;
+            const int64_t unit = unit_of(sg);
+            const int head = g * G + (sg.row0 + min(r, sg.nrows - 1)) % G;
             float mul, lse;
-            if (p.num_parts > 1) {
+            if (part) {
                 mul = l == 0.f ? 0.f : 1.f / l;
                 lse = l == 0.f ? kNegInf : m_ref + log2f(l);
+                if (row_on) p.part_lse[prow + lane] = lse;
             } else {
                 const float sink = p.sink ? p.sink[head] * kLog2e : kNegInf;
                 const float M = fmaxf(m_ref, sink);
@@ -773,56 +939,53 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                 lse = lam == 0.f ? kNegInf : (Ms + log2f(lam)) * kLn2;
                 // a NaN weight leaves m_ref as it was: keep the NaN
                 if (l != l) mul = lse = l;
+                if (row_on && p.lse_out) p.lse_out[unit] = lse;
             }
-            if (row_on) {
-                if (p.num_parts > 1)
-                    p.part_lse[unit * p.num_parts + blockIdx.y] = lse;
-                else if (p.lse_out)
-                    p.lse_out[unit] = lse;
-            }
-            // O goes through shared memory (the K and V tiles are done with), so that
-            // whole rows are stored: row r's 16-byte chunk c lies at chunk c ^ r of
-            // its row, where neither side meets a bank twice
-            constexpr int CPR = T / 4;  // chunks per row
-            uint8_t *stage = smem + C::OFF_K + warp * 32 * T * 4;
-            static_assert(4 * X * 32 * T * 4 <= C::OFF_SCALE - C::OFF_K, "staging");
+            // O goes through this warp's part of the Q tile, 32 columns at a time, so
+            // that whole 128-byte pieces of rows are stored: 16-byte chunk c of row r
+            // lies at chunk c ^ (r % 8), where neither side meets a bank twice
+            const int rows = min(sg.nrows - warp * 32, 32);
 #pragma unroll 1
             for (int c = 0; c < T / 32; ++c) {
+                uint8_t *stage = smem + C::OFF_Q + x * C::TILE + (c % C::HALVES) * C::HALF +
+                                 (warp & 3) * 4096;
                 uint32_t v[32];
-                tc::ld_32x32b_x32(t_o + 32 * c, v);
-                tc::wait_ld();
+                if (ntiles > 0) {
+                    tc::ld_32x32b_x32(t_o + 32 * c, v);
+                    tc::wait_ld();
+                }
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                    *reinterpret_cast<float4 *>(
-                        stage + lane * T * 4 + (((8 * c + e / 4) ^ lane) % CPR) * 16) =
-                        make_float4(__uint_as_float(v[e]) * mul, __uint_as_float(v[e + 1]) * mul,
-                                    __uint_as_float(v[e + 2]) * mul,
-                                    __uint_as_float(v[e + 3]) * mul);
-            }
-            __syncwarp();
-            const int rows = min(nrows - warp * 32, 32);
-            constexpr int RPI = CPR < 32 ? 32 / CPR : 1;       // rows per step
-            constexpr int CPL = CPR > 32 ? CPR / 32 : 1;       // chunks per lane
-#pragma unroll 4
-            for (int r0 = 0; r0 < 32; r0 += RPI) {
-                if (r0 >= rows) break;
-                const int rr = r0 + lane / CPR;
-                const int64_t u = __shfl_sync(0xffffffffu, unit, rr);
+                for (int e = 0; e < 32; e += 4) {
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (ntiles > 0)
+                        o = make_float4(
+                            __uint_as_float(v[e]) * mul, __uint_as_float(v[e + 1]) * mul,
+                            __uint_as_float(v[e + 2]) * mul, __uint_as_float(v[e + 3]) * mul);
+                    *reinterpret_cast<float4 *>(stage + lane * 128 +
+                                                (((e / 4) ^ (lane & 7)) << 4)) = o;
+                }
+                __syncwarp();
+                const int cc = lane & 7, col = 32 * c + 4 * cc;
 #pragma unroll
-                for (int k = 0; k < CPL; ++k) {
-                    const int c = lane % CPR + 32 * k;
+                for (int k = 0; k < 8; ++k) {
+                    const int rr = k * 4 + (lane >> 3);
+                    const int64_t u = __shfl_sync(0xffffffffu, unit, rr);
                     const float4 o = *reinterpret_cast<const float4 *>(
-                        stage + rr * T * 4 + ((c ^ rr) % CPR) * 16);
-                    if (rr >= rows || c * 4 >= Dh) continue;
-                    if (p.num_parts > 1)
-                        *reinterpret_cast<float4 *>(
-                            p.part_o + (u * p.num_parts + blockIdx.y) * Dh + c * 4) = o;
+                        stage + rr * 128 + ((cc ^ (rr & 7)) << 4));
+                    if (rr >= rows || col >= Dh) continue;
+                    if (part)
+                        *reinterpret_cast<float4 *>(p.part_o + (prow + rr) * Dh + col) = o;
                     else
                         *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + u * Dh +
-                                                   c * 4) =
+                                                   col) =
                             make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
                 }
+                __syncwarp();
             }
+            tc::fence_before_sync();
+        }
+        release(ns);
+        sp = next;
         }
     } else if constexpr (KV8) {
         // ------------------------------------------------------------ codes -> f16 tiles
@@ -832,26 +995,32 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         constexpr int ROWS = kTile / C::DW;
         const int w = warp - C::W_CVT;
         bool alive = true;
-        int nfix = 0;
-        for (int j = 0; j < ntiles && alive; ++j) {
-            const int k0 = (kt0 + j) * kTile;
+        int jt = 0, nfix = 0;                // key tiles and repaired tiles so far
+        for (int ns = 0; alive; ++ns) {
+        const Seg *sp = segment(ns);
+        if (!sp) break;
+        const Seg &sg = *sp;                 // stays in the ring until it is released
+        const int tok_lo = sg.tok_lo, tok_hi = sg.tok_hi;
+        int id = sg.ntiles > 0 ? page_id(sg, 0, -1) : -1;
+        for (int i = 0; i < sg.ntiles && alive; ++i, ++jt) {
+            const int k0 = (sg.tile0 + i) * kTile;
             // lane: rows 4 lane .. 4 lane + 3 of the tile, all in one page
-            const int myid = __shfl_sync(0xffffffffu, id, lane * 4 / BS);
+            const int myid = __shfl_sync(0xffffffffu, id, lane * 4 >> bs_shift);
             const bool idok = myid >= 0 && (int64_t)myid < p.num_blocks;
             const uint32_t in4 = idok ? range_bits(tok_lo - k0 - 4 * lane, tok_hi - k0 - 4 * lane) &
                                             15u
                                       : 0u;
-            if (j + 1 < ntiles) id = page_id(j + 1, -1);
-            const bool fix = partial(j);
+            if (i + 1 < sg.ntiles) id = page_id(sg, i + 1, -1);
+            const bool fix = sg.partial(i);
             uint32_t kmax = 1;
 #pragma unroll 1
             for (int isv = 0; isv < 2; ++isv) {
-                const int u = 2 * j + isv, rs = u % C::RU;
-                const int nb = isv ? C::VB : C::KB, s = j % nb;
+                const int u = 2 * jt + isv, rs = u % C::RU;
+                const int nb = isv ? C::VB : C::KB, s = jt % nb;
                 alive = warp_wait_bounded(bar(C::B_RFULL + rs), (uint32_t)(u / C::RU) & 1u,
                                           p.dev_error, s_abort) &&
                         warp_wait_bounded(bar((isv ? C::B_VEMPTY : C::B_KEMPTY) + s),
-                                          ((uint32_t)(j / nb) & 1u) ^ 1u, p.dev_error, s_abort);
+                                          ((uint32_t)(jt / nb) & 1u) ^ 1u, p.dev_error, s_abort);
                 if (!alive) break;
                 const uint8_t *sc = smem + C::OFF_SCALE + rs * kTile;
                 // the largest scale byte of the attended rows, NaN rows aside; not
@@ -868,9 +1037,9 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     kmax = top;
                 } else if (w == 0 && lane == 0) {
                     // V's buffer is free, so the softmax that last used this slot is done
-                    s_byte[(j & 1) * 2] = kmax;
-                    s_byte[(j & 1) * 2 + 1] = top;
-                    mbar_arrive(bar(C::B_FACT + (j & 1)));
+                    s_byte[(jt & 1) * 2] = kmax;
+                    s_byte[(jt & 1) * 2 + 1] = top;
+                    mbar_arrive(bar(C::B_FACT + (jt & 1)));
                 }
                 // NaN rows of a V tile that some row does not see are zeroed and noted
                 uint32_t bad4 = 0;
@@ -959,6 +1128,8 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             }
             if (fix) ++nfix;
         }
+        release(ns);
+        }
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -974,7 +1145,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
 constexpr int kMergeThreads = 128;
 
 __global__ void __launch_bounds__(kMergeThreads)
-tree_merge_kernel(const TreeParams p) {
+tree_merge_kernel(const TreeParams p, int rows) {
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31;
@@ -982,30 +1153,40 @@ tree_merge_kernel(const TreeParams p) {
     const int h = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
     const Req rq = request(p, b, false);
     if (t >= rq.q_len || h >= p.num_qo_heads) return;
-    const int P = p.partition_size, D = p.head_dim;
-    const int n = rq.L > rq.start ? (rq.L - 1) / P - rq.start / P + 1 : 0;
-    const int64_t unit = (int64_t)(rq.q_start + t) * p.num_qo_heads + h;
-    const float *lp = p.part_lse + unit * p.num_parts;
-    const float *po = p.part_o + unit * p.num_parts * D;
+    // the row group's place on the line, and the CTA groups it meets: the first
+    // left the second slot of its two, the others their first
+    const int D = p.head_dim, G = p.group, g = h / G;
+    const int row = t * G + (h - g * G), rg = row / rows;
+    const int tiles = cost_of(p, rq, rows).tiles;
+    const long long s = p.line[b] + (long long)rg * tiles, share = p.line[p.batch + 1];
+    const int first = (int)(s / share), last = (int)((s + tiles - 1) / share);
+    if (first == last) return;  // one CTA had all of it
+    const int n = last - first + 1;
+    auto at = [&](int i) {
+        const int slot = i == 0 ? 2 * first + 1 : 2 * (first + i);
+        return ((int64_t)slot * p.num_kv_heads + g) * rows + (row - rg * rows);
+    };
     const float sink = p.sink ? p.sink[h] * kLog2e : kNegInf;
     float M = sink;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, lp[i]);
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, p.part_lse[at(i)]);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     const float Ms = M == kNegInf ? 0.f : M;
     float sum = 0.f;
-    for (int i = lane; i < n; i += 32) sum += exp2f(lp[i] - Ms);
+    for (int i = lane; i < n; i += 32) sum += exp2f(p.part_lse[at(i)] - Ms);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     const float lam = sum + exp2f(sink - Ms);
     const float inv = lam == 0.f ? 0.f : 1.f / lam;
+    const int64_t unit = (int64_t)(rq.q_start + t) * p.num_qo_heads + h;
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + unit * D;
     for (int c = 4 * lane; c < D; c += 128) {
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int i = 0; i < n; ++i) {
-            const float w = exp2f(lp[i] - Ms);
-            const float4 v = *reinterpret_cast<const float4 *>(po + (int64_t)i * D + c);
+            const int64_t k = at(i);
+            const float w = exp2f(p.part_lse[k] - Ms);
+            const float4 v = *reinterpret_cast<const float4 *>(p.part_o + k * D + c);
             acc.x = fmaf(w, v.x, acc.x);
             acc.y = fmaf(w, v.y, acc.y);
             acc.z = fmaf(w, v.z, acc.z);
@@ -1024,9 +1205,8 @@ cudaError_t launch_one(const TreeParams &p, const CUtensorMap *tk, const CUtenso
     auto kern = tree_kernel<T, KV8, X>;
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), C::SMEM);
     if (e != cudaSuccess) return e;
-    const int rgroups = (p.row_tiles + X - 1) / X;
-    return launch_pdl(kern, dim3(p.num_kv_heads * rgroups, p.num_parts, p.batch),
-                      dim3(C::THREADS), (size_t)C::SMEM, stream, p, *tk, *tv);
+    return launch_pdl(kern, dim3(p.num_kv_heads * p.groups), dim3(C::THREADS), (size_t)C::SMEM,
+                      stream, p, *tk, *tv);
 }
 
 template <bool KV8>
@@ -1046,11 +1226,12 @@ cudaError_t launch_tree(const TreeParams &p, const CUtensorMap *tmap_k,
                         const CUtensorMap *tmap_v, cudaStream_t stream) {
     cudaError_t e = p.k_scale ? launch_kv<true>(p, tmap_k, tmap_v, stream)
                               : launch_kv<false>(p, tmap_k, tmap_v, stream);
-    if (e != cudaSuccess || p.num_parts == 1) return e;
+    if (e != cudaSuccess) return e;
     constexpr int kHeads = kMergeThreads / 32;
     return launch_pdl(tree_merge_kernel,
                       dim3((p.num_qo_heads + kHeads - 1) / kHeads, p.max_seqlen_q, p.batch),
-                      dim3(kMergeThreads), 0, stream, p);
+                      dim3(kMergeThreads), 0, stream, p,
+                      p.head_dim <= 128 && p.row_tiles > 1 ? 2 * kTile : kTile);
 }
 
 }  // namespace pkv

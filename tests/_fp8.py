@@ -139,12 +139,23 @@ def attend(q, k, v, keep, scale, sink=None, bias=None):
     return out, lse, absv, smax
 
 
-def out_bound(ref, absv, smax, d, p_eps):
+def out_bound(ref, absv, smax, d, p_eps, f16_floor=0.0):
     """Half a bf16 step of the output, plus the weights' error: each p rounds to
     p_eps relative; its score is an fp32 sum of d products (d + 8 roundings of
-    2^-24 of sum |q k|), which moves p and the normaliser."""
+    2^-24 of sum |q k|), which moves p and the normaliser.  f16_floor: see there."""
     p_err = p_eps + 2 * (d + 8) * 2.0 ** -24 * smax[..., None] + 2.0 ** -19
-    return 2.0 ** -8 * ref.abs() + p_err * absv * (1 + 2.0 ** -8) + 2.0 ** -100
+    return 2.0 ** -8 * ref.abs() + p_err * absv * (1 + 2.0 ** -8) + f16_floor + 2.0 ** -100
+
+
+def f16_floor(v):
+    """What f16 weights may add over 8-bit pools: weights are held times 2^6 at the
+    softmax's reference (p <= 1) and the largest V scale 2^E, and f16's smallest
+    step is 2^-24, so a small weight is off by at most 2^-25 * 2^-6 of p * 2^E = 1 *
+    2^E; a code is at most 448 and the row with the scale 2^E has a value of at
+    least 224 * 2^E, so n keys add at most n * 2^-31 * 2 max|v|."""
+    n = v.shape[0]
+    v = v[torch.isfinite(v)].abs()
+    return float(v.max()) * 2.0 ** -30 * n if v.numel() else 0.0
 
 
 def lse_bound(lse, smax, d):
