@@ -36,7 +36,7 @@
 // Warps: four softmax warps per row tile, one row per thread; a TMA warp, which
 // also works out the CTA's segments and hands them to the others through a
 // ring; an MMA warp; over 8-bit pools the warps that convert codes.
-//   S = Q K^T -> TMEM; the softmax takes its row into registers, writes P (16
+//   S = Q K^T -> TMEM; the softmax reads S twice (maximum, weights), writes P (16
 //   bits) over S; O += P V with P from TMEM.  O is rescaled only when a row's
 //   maximum has grown a lot.
 // The products run in units n = (key tile, row tile), row tiles fastest, with two S
@@ -57,6 +57,7 @@ namespace {
 
 constexpr int kTile = 128;      // rows and keys per tile
 constexpr int kRing = 4;        // segments handed over ahead
+constexpr int kInfo = 8;        // key tiles whose bad pages are: more than are ever under way
 constexpr float kNegInf = -INFINITY;
 // A row's reference moves (and O is rescaled, which costs about a tile's time)
 // only when a score exceeds it by kLazy log2 units.  bf16 weights have fp32's
@@ -76,7 +77,7 @@ struct Cfg {
     static constexpr int TILE = HALVES * HALF;
     // K and V tiles: as many as fit, for the bytes in flight (over 8-bit pools the
     // raw tiles are what is in flight)
-    static constexpr int KB = KV8 ? (T == 64 ? 2 : 1) : T == 64 ? 4 : T == 128 ? 3 : 1;
+    static constexpr int KB = KV8 ? (T <= 128 ? 2 : 1) : T == 64 ? 4 : T == 128 ? 3 : 1;
     static constexpr int VB = KV8 ? (T == 64 || (T == 128 && X == 1) ? 2 : 1)
                                   : T == 64 ? 4 : T == 128 ? 4 - X : 1;
     // raw tiles of codes, K and V in turn
@@ -100,8 +101,9 @@ struct Cfg {
                          B_PFULL = B_SFULL + 2, B_O = B_PFULL + 2, B_LAND = B_O + 1,
                          B_POISON = B_LAND + 1, B_FACT = B_POISON + 2, B_RFULL = B_FACT + 2,
                          B_REMPTY = B_RFULL + RU, B_Q = B_REMPTY + RU, B_IFULL = B_Q + 1,
-                         B_IEMPTY = B_IFULL + kRing, NBAR = B_IEMPTY + kRing;
-    // tmem, abort, -, -, poison[2][4], scale bytes[2][K, V]
+                         B_IEMPTY = B_IFULL + kRing, B_INFO = B_IEMPTY + kRing,
+                         NBAR = B_INFO + kInfo;
+    // tmem, abort, bad pages[kInfo] (8 bits each), poison[2][4], scale bytes[2][K, V]
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = 1024 + OFF_MISC + 64;
     static_assert(256 + X * T <= 512, "tensor memory");
@@ -187,6 +189,19 @@ struct Seg {
 };
 static_assert(sizeof(Seg) == 48, "ring layout");
 
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Bits n0 .. n0+31 of a draft's mask of nw 64-bit words (n0 may be negative).
 __device__ __forceinline__ uint32_t mask_bits(const int64_t *m, int nw, int n0) {
     if (n0 <= -32 || n0 >= nw * 64) return 0u;
@@ -216,6 +231,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
     const uint32_t base = smem_u32(smem);
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     int32_t *s_abort = reinterpret_cast<int32_t *>(misc + 1);
+    volatile uint8_t *s_bad = reinterpret_cast<uint8_t *>(misc + 2);  // [kInfo]
     uint32_t *s_poison = misc + 4;   // [2][4]
     uint32_t *s_byte = misc + 12;    // [2][K, V]: a tile's largest scale bytes
     Seg *ring = reinterpret_cast<Seg *>(smem + C::OFF_RING);
@@ -251,6 +267,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             mbar_init(bar(C::B_RFULL + i), 1 + 8);
             mbar_init(bar(C::B_REMPTY + i), C::DW);
         }
+        for (int i = 0; i < kInfo; ++i) mbar_init(bar(C::B_INFO + i), 1);
         for (int i = 0; i < kRing; ++i) {
             mbar_init(bar(C::B_IFULL + i), 1);
             mbar_init(bar(C::B_IEMPTY + i), 4 * X + 1 + C::DW);
@@ -290,13 +307,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::B_IEMPTY + n % kRing));
     };
-    // lane l < npg: the id of page l of tile j, `none` where no key is attended
-    auto page_id = [&](const Seg &sg, int j, int none) {
-        const int pg = (sg.tile0 + j) * npg + lane;
-        return lane < npg && pg >= sg.tok_lo >> bs_shift && pg <= (sg.tok_hi - 1) >> bs_shift
-                   ? p.block_table[(int64_t)sg.b() * p.max_blocks_per_seq + pg]
-                   : none;
-    };
+
     if (warp == C::W_TMA) {
         // ------------------------------------------------------------ segments, loads
         constexpr int kRows = X * kTile;
@@ -333,20 +344,34 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         uint32_t landed = 0;           // bit i: the last use of V buffer i was a repaired tile
         auto load_segment = [&](const Seg &sg) {
             const int tok_lo = sg.tok_lo, tok_hi = sg.tok_hi;
-            int id = page_id(sg, 0, -1);
-            for (int i = 0; i < sg.ntiles && alive; ++i) {
+            // 32 page ids per warp-wide load, a load ahead: beside 150 streaming SMs
+            // it takes longer than a tile
+            const int32_t *bt = p.block_table + (int64_t)sg.b() * p.max_blocks_per_seq;
+            const int first = tok_lo >> bs_shift, last = (tok_hi - 1) >> bs_shift;
+            const int tpb = 32 / npg;
+            auto page_ids = [&](int i) {  // tiles i .. i + tpb - 1
                 const int pg = (sg.tile0 + i) * npg + lane;
-                int row = oob;
-                if (lane < npg && pg >= tok_lo >> bs_shift && pg <= (tok_hi - 1) >> bs_shift) {
-                    if (id < 0 || id >= p.num_blocks) {
-                        flag_error(p.dev_error, PKV_DEVERR_BLOCK_ID);
-                        id = -1;
-                    } else {
-                        row = p.hnd ? id * Hkv + g : id * BS;
-                    }
+                return pg >= first && pg <= last ? bt[pg] : -1;
+            };
+            int ids = -1, ids_next = page_ids(0);
+            for (int i = 0; i < sg.ntiles && alive; ++i) {
+                if (i % tpb == 0) {
+                    ids = ids_next;
+                    ids_next = page_ids(i + tpb);
                 }
-                const int id_now = id;
-                if (i + 1 < sg.ntiles) id = page_id(sg, i + 1, -1);
+                int id = __shfl_sync(0xffffffffu, ids, ((i % tpb) * npg + lane) & 31);
+                const int pg = (sg.tile0 + i) * npg + lane;
+                const bool attended = lane < npg && pg >= first && pg <= last;
+                const bool bad = attended && (id < 0 || id >= p.num_blocks);
+                if (bad) flag_error(p.dev_error, PKV_DEVERR_BLOCK_ID);
+                if (!attended || bad) id = -1;
+                const int row = id < 0 ? oob : p.hnd ? id * Hkv + g : id * BS;
+                const int id_now = id, jn = KV8 ? nk / 2 : nk;
+                const uint32_t badpg = __ballot_sync(0xffffffffu, bad);
+                if (lane == 0) {
+                    s_bad[jn % kInfo] = (uint8_t)badpg;
+                    mbar_arrive(bar(C::B_INFO + jn % kInfo));
+                }
                 if constexpr (!KV8) {
                     const int ks = nk % C::KB, vs = nv % C::VB;
                     // lane -> (page, 64-dim half)
@@ -570,8 +595,16 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             if (lane == 0) {
                 int sx = 0;             // row tile of the next S
                 bool k_ready = false;
-                auto issue_s = [&](int n) {
-                    if (!k_ready && !wait(C::B_KFULL + ks, kph)) return false;
+                // S of unit n; `must`: waits for its K tile, else gives up if that is
+                // not there.  Returns 1 when issued, 0 when not, -1 when a wait gave up.
+                auto issue_s = [&](int n, bool must) {
+                    if (!k_ready) {
+                        if (must) {
+                            if (!wait(C::B_KFULL + ks, kph)) return -1;
+                        } else if (!mbar_test(bar(C::B_KFULL + ks), kph)) {
+                            return 0;
+                        }
+                    }
                     k_ready = true;
                     tc::fence_after_sync();
                     const uint64_t dq = dq0 + (uint64_t)((sx * C::TILE) >> 4);
@@ -598,13 +631,20 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                             kph ^= 1u;
                         }
                     }
-                    return true;
+                    return 1;
                 };
                 alive = wait(C::B_Q, (uint32_t)ns & 1u);
-                if (alive && total > 0) alive = issue_s(un);
-                if (alive && total > 1) alive = issue_s(un + 1);
-                int x = 0;
+                int x = 0, issued = 0;  // row tile of the next O; S so far
                 for (int i = 0; i < total && alive; ++i) {
+                    // S runs up to two units ahead of O, but does not hold O up when
+                    // its K tile is late
+                    while (issued < total && issued < i + 2) {
+                        const int did = issue_s(un + issued, issued == i);
+                        alive = did >= 0;
+                        if (did <= 0) break;
+                        ++issued;
+                    }
+                    if (!alive) break;
                     const int n = un + i;
                     alive = wait(C::B_PFULL + (n & 1), (uint32_t)(n >> 1) & 1u) &&
                             (x > 0 || wait(C::B_VFULL + vs, vph));
@@ -621,7 +661,6 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                             vph ^= 1u;
                         }
                     }
-                    if (i + 2 < total) alive = issue_s(n + 2);
                 }
                 tc::commit(bar(C::B_O));  // (with nothing in flight it arrives at once)
                 un += total;
@@ -718,14 +757,14 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         // scale.  m_ref follows the row's largest score (there plus that scale
         // over 2^10, so that f16 holds the product); O and l share it.
         float m_ref = kNegInf, l = 0.f;
-        int id = warp_on && ntiles > 0 ? page_id(sg, 0, 0) : 0;
         for (int j = 0; j < ntiles && x < nx; ++j) {
             const int n = un + j * nx + x, jn = jt + j;
             const uint32_t t_s = tmem + (n & 1) * 128 + lane_base;
             const bool fix = j < full_lo || j >= full_hi;
-            const uint32_t badpg =
-                __ballot_sync(0xffffffffu, id < 0 || (int64_t)id >= p.num_blocks);
-            if (warp_on && j + 1 < ntiles) id = page_id(sg, j + 1, 0);
+            alive = warp_wait_bounded(bar(C::B_INFO + jn % kInfo), (uint32_t)(jn / kInfo) & 1u,
+                                      p.dev_error, s_abort);
+            if (!alive) break;
+            const uint32_t badpg = s_bad[jn % kInfo];
             const bool general = fix || badpg != 0 || p.alibi != nullptr;
             alive = warp_wait_bounded(bar(C::B_SFULL + (n & 1)), (uint32_t)(n >> 1) & 1u,
                                       p.dev_error, s_abort);
@@ -859,18 +898,29 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                 };
                 float sum = 0.f;
                 if (!general) {
-                    uint32_t v[4][32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tc::ld_32x32b_x32(t_s + 32 * c, v[c]);
-                    tc::wait_ld();
+                    // twice over S, 64 columns at a time, in loops: unrolled over the
+                    // row, the code alone outgrows the schedulers' instruction caches
                     float mt = kNegInf;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) mt = maximum(mt, v[c]);
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t v[2][32];
+                        tc::ld_32x32b_x32(t_s + 64 * h, v[0]);
+                        tc::ld_32x32b_x32(t_s + 64 * h + 32, v[1]);
+                        tc::wait_ld();
+                        mt = maximum(maximum(mt, v[0]), v[1]);
+                    }
                     alive = refer(mt * rf + shift);
                     if (!alive) break;
                     const float m = (m_ref == kNegInf ? 0.f : m_ref) - vexp;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) sum += weights(c, v[c], rf, m);
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t v[2][32];
+                        tc::ld_32x32b_x32(t_s + 64 * h, v[0]);
+                        tc::ld_32x32b_x32(t_s + 64 * h + 32, v[1]);
+                        tc::wait_ld();
+                        sum += weights(2 * h, v[0], rf, m);
+                        sum += weights(2 * h + 1, v[1], rf, m);
+                    }
                 } else {
                     float mt = kNegInf;
 #pragma unroll 1
@@ -1001,16 +1051,9 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         if (!sp) break;
         const Seg &sg = *sp;                 // stays in the ring until it is released
         const int tok_lo = sg.tok_lo, tok_hi = sg.tok_hi;
-        int id = sg.ntiles > 0 ? page_id(sg, 0, -1) : -1;
         for (int i = 0; i < sg.ntiles && alive; ++i, ++jt) {
             const int k0 = (sg.tile0 + i) * kTile;
-            // lane: rows 4 lane .. 4 lane + 3 of the tile, all in one page
-            const int myid = __shfl_sync(0xffffffffu, id, lane * 4 >> bs_shift);
-            const bool idok = myid >= 0 && (int64_t)myid < p.num_blocks;
-            const uint32_t in4 = idok ? range_bits(tok_lo - k0 - 4 * lane, tok_hi - k0 - 4 * lane) &
-                                            15u
-                                      : 0u;
-            if (i + 1 < sg.ntiles) id = page_id(sg, i + 1, -1);
+            uint32_t in4 = 0;  // lane: which of rows 4 lane .. 4 lane + 3 are attended
             const bool fix = sg.partial(i);
             uint32_t kmax = 1;
 #pragma unroll 1
@@ -1022,6 +1065,8 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                         warp_wait_bounded(bar((isv ? C::B_VEMPTY : C::B_KEMPTY) + s),
                                           ((uint32_t)(jt / nb) & 1u) ^ 1u, p.dev_error, s_abort);
                 if (!alive) break;
+                if (!isv && !((s_bad[jt % kInfo] >> (lane * 4 >> bs_shift)) & 1u))
+                    in4 = range_bits(tok_lo - k0 - 4 * lane, tok_hi - k0 - 4 * lane) & 15u;
                 const uint8_t *sc = smem + C::OFF_SCALE + rs * kTile;
                 // the largest scale byte of the attended rows, NaN rows aside; not
                 // below 2^-90, so that 1 / scale stays finite
