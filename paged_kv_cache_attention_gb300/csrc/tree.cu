@@ -189,6 +189,36 @@ struct Seg {
 };
 static_assert(sizeof(Seg) == 48, "ring layout");
 
+// The bounded wait of a whole warp (mbar_wait_bounded), written to be short: it
+// stands at thirty places, and code that has to be fetched beside 150 streaming
+// SMs takes microseconds.
+__device__ __noinline__ void gave_up(int32_t *dev_error, int32_t *abort) {
+    flag_error(dev_error, PKV_DEVERR_TIMEOUT);
+    if (abort) *reinterpret_cast<volatile int32_t *>(abort) = 1;
+}
+
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, int32_t *dev_error,
+                                         int32_t *abort = nullptr) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+        const long long t0 = clock64();
+#pragma unroll 1
+        while (!(ok = mbar_try_wait(bar, parity))) {
+            if (abort && *reinterpret_cast<volatile int32_t *>(abort) != 0) break;
+            if (clock64() - t0 > kWaitLimitCycles) {
+                gave_up(dev_error, abort);
+                break;
+            }
+        }
+    }
+    return ok;
+}
+
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int32_t *dev_error,
+                                          int32_t *abort = nullptr) {
+    return __all_sync(0xffffffffu, wait_one(bar, parity, dev_error, abort));
+}
+
 // Whether the phase has completed, without waiting.
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     uint32_t ok;
@@ -297,7 +327,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
     // read it until they release it; null: none left, or a wait gave up.
     auto segment = [&](int n) -> const Seg * {
         const int s = n % kRing;
-        if (!warp_wait_bounded(bar(C::B_IFULL + s), (uint32_t)(n / kRing) & 1u, p.dev_error,
+        if (!wait_warp(bar(C::B_IFULL + s), (uint32_t)(n / kRing) & 1u, p.dev_error,
                                s_abort) ||
             ring[s].slot_b < 0)
             return nullptr;
@@ -377,7 +407,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     // lane -> (page, 64-dim half)
                     const int lp = lane / C::HALVES, lh = lane % C::HALVES;
                     const int brow = __shfl_sync(0xffffffffu, row, lp);
-                    alive = warp_wait_bounded(bar(C::B_KEMPTY + ks),
+                    alive = wait_warp(bar(C::B_KEMPTY + ks),
                                               ((uint32_t)(nk / C::KB) & 1u) ^ 1u, p.dev_error,
                                               s_abort);
                     if (!alive) break;
@@ -387,7 +417,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                         tma_load_3d(base + C::OFF_K + ks * C::TILE + lh * C::HALF + lp * BS * 128,
                                     &tmk, bar(C::B_KFULL + ks), lh * 64, cy, brow);
                     ++nk;
-                    alive = warp_wait_bounded(bar(C::B_VEMPTY + vs),
+                    alive = wait_warp(bar(C::B_VEMPTY + vs),
                                               ((uint32_t)(nv / C::VB) & 1u) ^ 1u, p.dev_error,
                                               s_abort);
                     if (!alive) break;
@@ -402,7 +432,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                                     brow);
                     ++nv;
                     if (fix) {
-                        alive = warp_wait_bounded(bar(C::B_LAND), (uint32_t)nfix & 1u, p.dev_error,
+                        alive = wait_warp(bar(C::B_LAND), (uint32_t)nfix & 1u, p.dev_error,
                                                   s_abort);
                         ++nfix;
                         if (!alive) break;
@@ -449,7 +479,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     for (int v = 0; v < 2 && alive; ++v) {
                         const int s = nk % C::RU;
                         const uint32_t full = bar(C::B_RFULL + s);
-                        alive = warp_wait_bounded(bar(C::B_REMPTY + s),
+                        alive = wait_warp(bar(C::B_REMPTY + s),
                                                   ((uint32_t)(nk / C::RU) & 1u) ^ 1u, p.dev_error,
                                                   s_abort);
                         if (!alive) break;
@@ -528,7 +558,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     sg.full_hi = min(sg.tok_hi, sg.ctx) / kTile - sg.tile0;
                     sg.slot_b = 4 * (b0 + src) + (lo > s ? 1 : hi < e ? 2 : 0);
                     const int rs = nseg % kRing;
-                    alive = warp_wait_bounded(bar(C::B_IEMPTY + rs),
+                    alive = wait_warp(bar(C::B_IEMPTY + rs),
                                               ((uint32_t)(nseg / kRing) & 1u) ^ 1u, p.dev_error,
                                               s_abort);
                     if (!alive) break;
@@ -543,7 +573,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         }
         if (alive) {  // no more
             const int rs = nseg % kRing;
-            alive = warp_wait_bounded(bar(C::B_IEMPTY + rs),
+            alive = wait_warp(bar(C::B_IEMPTY + rs),
                                       ((uint32_t)(nseg / kRing) & 1u) ^ 1u, p.dev_error, s_abort);
             if (alive && lane == 0) {
                 ring[rs].slot_b = -1;
@@ -553,17 +583,17 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         if (!alive) {  // a wait gave up: let the copies in flight land (bounded)
             if constexpr (!KV8) {
                 for (int i = max(0, nk - C::KB); i < nk; ++i)
-                    warp_wait_bounded(bar(C::B_KFULL + i % C::KB), (uint32_t)(i / C::KB) & 1u,
+                    wait_warp(bar(C::B_KFULL + i % C::KB), (uint32_t)(i / C::KB) & 1u,
                                       p.dev_error);
                 for (int i = max(0, nv - C::VB); i < nv; ++i)
                     if (!((landed >> (i % C::VB)) & 1u))
-                        warp_wait_bounded(bar(C::B_VFULL + i % C::VB),
+                        wait_warp(bar(C::B_VFULL + i % C::VB),
                                           (uint32_t)(i / C::VB) & 1u, p.dev_error);
                 if (nfix > 0)
-                    warp_wait_bounded(bar(C::B_LAND), (uint32_t)(nfix - 1) & 1u, p.dev_error);
+                    wait_warp(bar(C::B_LAND), (uint32_t)(nfix - 1) & 1u, p.dev_error);
             } else {
                 for (int u = max(0, nk - C::RU); u < nk; ++u)
-                    warp_wait_bounded(bar(C::B_RFULL + u % C::RU), (uint32_t)(u / C::RU) & 1u,
+                    wait_warp(bar(C::B_RFULL + u % C::RU), (uint32_t)(u / C::RU) & 1u,
                                       p.dev_error);
             }
         }
@@ -581,7 +611,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         // the tensor pipe runs dry meanwhile (buffer indexes and phases are
         // counted, not divided out).
         auto wait = [&](int i, uint32_t phase) {
-            return mbar_wait_bounded(bar(i), phase, p.dev_error, s_abort);
+            return wait_one(bar(i), phase, p.dev_error, s_abort);
         };
         int ks = 0, vs = 0;             // K buffer of the next S, V buffer of the next O
         uint32_t kph = 0, vph = 0;      // and their phases
@@ -665,7 +695,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                 tc::commit(bar(C::B_O));  // (with nothing in flight it arrives at once)
                 un += total;
                 // a wait gave up: let the products in flight finish (bounded)
-                if (!alive) mbar_wait_bounded(bar(C::B_O), (uint32_t)ns & 1u, p.dev_error);
+                if (!alive) wait_one(bar(C::B_O), (uint32_t)ns & 1u, p.dev_error);
             }
             alive = __shfl_sync(0xffffffffu, alive ? 1 : 0, 0) != 0;
         }
@@ -677,76 +707,71 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_o = tmem + 256 + x * T + lane_base;
         const uint32_t sq = base + C::OFF_Q + x * C::TILE;
-        // Q: this warp's 32 rows, LPR lanes per row, STEPS steps in flight.  Beside
-        // 150 streaming SMs a load takes microseconds, so the next segment's rows
-        // are asked for before the last one's are stored.
-        constexpr int LPR = T / 8 < 32 ? T / 8 : 32, RPS = 32 / LPR;
-        constexpr int STEPS = 32 / RPS < 16 ? 32 / RPS : 16;
-        uint4 qv[STEPS];
         // (draft, head) of this thread's row, as its index in q, out and lse
         auto unit_of = [&](const Seg &sg) {
             const int i = sg.row0 + min(r, sg.nrows - 1), tok = i / G;
             return (int64_t)(sg.q_start + tok) * p.num_qo_heads + g * G + (i - tok * G);
         };
-        auto load_q = [&](const Seg &sg, int s0) {
-            const int64_t unit = unit_of(sg);
-            const __nv_bfloat16 *qc =
-                static_cast<const __nv_bfloat16 *>(p.q) + (lane % LPR) * 8;
-            const int nrows = sg.nrows;
-#pragma unroll
-            for (int k = 0; k < STEPS; ++k) {
-                const int rr = (s0 + k) * RPS + lane / LPR;
-                const int64_t u = __shfl_sync(0xffffffffu, unit, rr);
-                qv[k] = make_uint4(0u, 0u, 0u, 0u);
-                if (warp * 32 + rr < nrows && (lane % LPR) * 8 < Dh)
-                    qv[k] = __ldg(reinterpret_cast<const uint4 *>(qc + u * Dh));
-            }
-        };
         const bool positions = p.window_left >= 0 || p.alibi;
         int un = 0, jt = 0, nfix = 0;        // units, key tiles and repaired tiles so far
         bool alive = true;
         const Seg *sp = segment(0);
-        if (sp) load_q(*sp, 0);
         for (int ns = 0; sp && alive; ++ns) {
         const Seg &sg = *sp;                 // stays in the ring until it is released
         const int ntiles = sg.ntiles, nx = sg.nrows > kTile ? 2 : 1;
         const int full_lo = sg.full_lo, full_hi = sg.full_hi;
         const bool warp_on = warp * 32 < sg.nrows, row_on = r < sg.nrows;
-        // ---- this warp's rows of Q into shared memory (rows past the last: zeros)
+        // ---- this warp's rows of Q into shared memory (rows past the last: zeros),
+        // LPR lanes per row
+        const int64_t unit = unit_of(sg);
         float rowf = fabsf(p.scale_log2);  // score = S * rowf
         {
+            constexpr int LPR = T / 8 < 32 ? T / 8 : 32, RPS = 32 / LPR;
+            const int c = lane % LPR, r0 = lane / LPR;
+            const __nv_bfloat16 *qc = static_cast<const __nv_bfloat16 *>(p.q) + c * 8;
+            const bool col_on = c * 8 < Dh;
+#pragma unroll 4
+            for (int k = 0; k < 32 / RPS; ++k) {
+                const int rr = k * RPS + r0;
+                const int64_t u = __shfl_sync(0xffffffffu, unit, rr);
+                const int row = (warp & 3) * 32 + rr;
+                cp_async16_or_zero(sq + (c >> 3) * C::HALF + sw128(row, c & 7),
+                                   col_on ? qc + u * Dh : qc,
+                                   col_on && warp * 32 + rr < sg.nrows);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
             const uint32_t neg = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // its sign goes into q
-            const int c = lane % LPR;
-#pragma unroll 1
-            for (int s0 = 0; s0 < 32 / RPS; s0 += STEPS) {
-                if (s0 > 0) load_q(sg, s0);
+            if (KV8 || neg) {
+                // this thread's row in place: to f16, times a power of two that brings
+                // its largest value to 2^14..2^15 (exact down to 2^-28 of it)
+                const uint32_t row = (uint32_t)r % kTile;
+                uint32_t m = 0;
+                float f = 1.f;
+                if constexpr (KV8) {
+#pragma unroll 4
+                    for (int k = 0; k < T / 8; ++k) {
+                        const uint4 v = ld_shared16(sq + (k >> 3) * C::HALF + sw128(row, k & 7));
+                        m = bf16x2_max_nan(m, bf16x2_max_nan(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu));
+                        m = bf16x2_max_nan(m, bf16x2_max_nan(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+                    }
+                    const int E = max((int)(max(m & 0xffffu, m >> 16) >> 7) - 127, -100);
+                    f = __uint_as_float((uint32_t)(127 + 14 - E) << 23);
+                    rowf *= __uint_as_float((uint32_t)(127 + E - 14) << 23);
+                }
+#pragma unroll 2
+                for (int k = 0; k < T / 8; ++k) {
+                    const uint32_t at = sq + (k >> 3) * C::HALF + sw128(row, k & 7);
+                    const uint4 v = ld_shared16(at);
+                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int k = 0; k < STEPS; ++k) {
-                    uint32_t w[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
-                    if constexpr (KV8) {
-                        // in f16, times a power of two that brings the row's largest value
-                        // to 2^14..2^15 (exact down to 2^-28 of it)
-                        uint32_t amax = 0;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            amax = max(amax, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-#pragma unroll
-                        for (int off = LPR / 2; off > 0; off >>= 1)
-                            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-                        const int E = max((int)(amax >> 7) - 127, -100);
-                        const float f = __uint_as_float((uint32_t)(127 + 14 - E) << 23);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (KV8)
                             w[e] = pack_f16(__uint_as_float(w[e] << 16) * f,
                                             __uint_as_float(w[e] & 0xffff0000u) * f);
-                        // lane r of the warp keeps the factor of row r
-                        const int Er = __shfl_sync(0xffffffffu, E, (lane % RPS) * LPR);
-                        if (lane / RPS == s0 + k)
-                            rowf *= __uint_as_float((uint32_t)(127 + Er - 14) << 23);
+                        w[e] ^= neg;
                     }
-                    const int rr = (warp & 3) * 32 + (s0 + k) * RPS + lane / LPR;
-                    st_shared16(sq + (c >> 3) * C::HALF + sw128(rr, c & 7), w[0] ^ neg,
-                                w[1] ^ neg, w[2] ^ neg, w[3] ^ neg);
+                    st_shared16(at, w[0], w[1], w[2], w[3]);
                 }
             }
             fence_proxy_async_smem();
@@ -761,18 +786,18 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             const int n = un + j * nx + x, jn = jt + j;
             const uint32_t t_s = tmem + (n & 1) * 128 + lane_base;
             const bool fix = j < full_lo || j >= full_hi;
-            alive = warp_wait_bounded(bar(C::B_INFO + jn % kInfo), (uint32_t)(jn / kInfo) & 1u,
+            alive = wait_warp(bar(C::B_INFO + jn % kInfo), (uint32_t)(jn / kInfo) & 1u,
                                       p.dev_error, s_abort);
             if (!alive) break;
             const uint32_t badpg = s_bad[jn % kInfo];
             const bool general = fix || badpg != 0 || p.alibi != nullptr;
-            alive = warp_wait_bounded(bar(C::B_SFULL + (n & 1)), (uint32_t)(n >> 1) & 1u,
+            alive = wait_warp(bar(C::B_SFULL + (n & 1)), (uint32_t)(n >> 1) & 1u,
                                       p.dev_error, s_abort);
             if (KV8 && alive)
-                alive = warp_wait_bounded(bar(C::B_FACT + (jn & 1)), (uint32_t)(jn >> 1) & 1u,
+                alive = wait_warp(bar(C::B_FACT + (jn & 1)), (uint32_t)(jn >> 1) & 1u,
                                           p.dev_error, s_abort);
             if (fix && alive) {
-                alive = warp_wait_bounded(bar(C::B_POISON + (nfix & 1)),
+                alive = wait_warp(bar(C::B_POISON + (nfix & 1)),
                                           (uint32_t)(nfix >> 1) & 1u, p.dev_error, s_abort);
                 ++nfix;
             }
@@ -824,15 +849,16 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     for (int e = 0; e < 32; ++e)
                         v[e] = __float_as_uint(__uint_as_float(v[e]) * rf);
                     if (p.alibi) {
+                        // lane e holds the position of the chunk's key e
                         const float slope = p.alibi[g * G + i % G] * kLog2e;
+                        const int k = kc + lane;
+                        const int kpos =
+                            k < ctx ? k : ctx + depth_of(min(k - ctx, sg.q_len - 1));
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const int k = kc + e;
-                            const int m = min(max(k - ctx, 0), sg.q_len - 1);
-                            const int kpos = k < ctx ? k : ctx + depth_of(m);
+                        for (int e = 0; e < 32; ++e)
                             v[e] = __float_as_uint(
-                                fmaf(slope, (float)(kpos - qpos), __uint_as_float(v[e])));
-                        }
+                                fmaf(slope, (float)(__shfl_sync(0xffffffffu, kpos, e) - qpos),
+                                     __uint_as_float(v[e])));
                     }
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
@@ -875,7 +901,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     if (!__any_sync(0xffffffffu, grow)) return true;
                     if (nx == 1) {  // O must be at rest: the last PV is done
                         // (with two row tiles, S(n) came behind this O's last PV)
-                        if (!warp_wait_bounded(bar(C::B_VEMPTY + (jn - 1) % C::VB),
+                        if (!wait_warp(bar(C::B_VEMPTY + (jn - 1) % C::VB),
                                                (uint32_t)((jn - 1) / C::VB) & 1u, p.dev_error,
                                                s_abort))
                             return false;
@@ -896,11 +922,11 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     }
                     return true;
                 };
-                float sum = 0.f;
+                // Twice over S, in loops: unrolled over the row, the code alone outgrows
+                // the schedulers' instruction caches.  The first pass takes the
+                // maximum, and in a general tile leaves the completed scores behind.
+                float mt = kNegInf;
                 if (!general) {
-                    // twice over S, 64 columns at a time, in loops: unrolled over the
-                    // row, the code alone outgrows the schedulers' instruction caches
-                    float mt = kNegInf;
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
                         uint32_t v[2][32];
@@ -909,20 +935,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                         tc::wait_ld();
                         mt = maximum(maximum(mt, v[0]), v[1]);
                     }
-                    alive = refer(mt * rf + shift);
-                    if (!alive) break;
-                    const float m = (m_ref == kNegInf ? 0.f : m_ref) - vexp;
-#pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t v[2][32];
-                        tc::ld_32x32b_x32(t_s + 64 * h, v[0]);
-                        tc::ld_32x32b_x32(t_s + 64 * h + 32, v[1]);
-                        tc::wait_ld();
-                        sum += weights(2 * h, v[0], rf, m);
-                        sum += weights(2 * h + 1, v[1], rf, m);
-                    }
                 } else {
-                    float mt = kNegInf;
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         uint32_t v[32];
@@ -934,16 +947,20 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                         tc::st_32x32b_x32(t_s + 32 * c, v);
                     }
                     tc::wait_st();
-                    alive = refer(mt + shift);
-                    if (!alive) break;
-                    const float m = (m_ref == kNegInf ? 0.f : m_ref) - vexp;
+                    rf = 1.f;
+                }
+                alive = refer(mt * rf + shift);
+                if (!alive) break;
+                const float m = (m_ref == kNegInf ? 0.f : m_ref) - vexp;
+                float sum = 0.f;
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32];
-                        tc::ld_32x32b_x32(t_s + 32 * c, v);
-                        tc::wait_ld();
-                        sum += weights(c, v, 1.f, m);
-                    }
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t v[2][32];
+                    tc::ld_32x32b_x32(t_s + 64 * h, v[0]);
+                    tc::ld_32x32b_x32(t_s + 64 * h + 32, v[1]);
+                    tc::wait_ld();
+                    sum += weights(2 * h, v[0], rf, m);
+                    sum += weights(2 * h + 1, v[1], rf, m);
                 }
                 l += KV8 ? sum * exp2f(-vexp) : sum;
                 tc::wait_st();
@@ -958,13 +975,16 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             nfix += ntiles - max(min(full_hi, ntiles) - max(full_lo, 0), 0);
         // every product of the segment is done: O is at rest and Q's tile free
         if (alive)
-            alive = warp_wait_bounded(bar(C::B_O), (uint32_t)ns & 1u, p.dev_error, s_abort);
+            alive = wait_warp(bar(C::B_O), (uint32_t)ns & 1u, p.dev_error, s_abort);
         if (!alive) break;
         const Seg *next = segment(ns + 1);
-        // (assigned either way, so that the registers are free in the main loop)
-#pragma unroll
-        for (int k = 0; k < STEPS; ++k) qv[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (next) load_q(*next, 0);
+        if (next && r < next->nrows) {  // its Q rows, on their way to L2 meanwhile
+            const char *row =
+                static_cast<const char *>(p.q) + unit_of(*next) * Dh * 2;
+            for (int k = 0; k < Dh * 2; k += 128)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(row + k));
+        }
+        __syncwarp();
         // ---- the rows' results
         if (warp_on) {
             tc::fence_after_sync();
@@ -972,7 +992,6 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             const bool part = sg.cut() != 0;
             const int64_t prow =
                 ((int64_t)(2 * group + sg.cut() / 2) * Hkv + g) * (X * kTile) + warp * 32;
-            const int64_t unit = unit_of(sg);
             const int head = g * G + (sg.row0 + min(r, sg.nrows - 1)) % G;
             float mul, lse;
             if (part) {
@@ -1016,19 +1035,21 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                 }
                 __syncwarp();
                 const int cc = lane & 7, col = 32 * c + 4 * cc;
-#pragma unroll
+#pragma unroll 2
                 for (int k = 0; k < 8; ++k) {
                     const int rr = k * 4 + (lane >> 3);
                     const int64_t u = __shfl_sync(0xffffffffu, unit, rr);
                     const float4 o = *reinterpret_cast<const float4 *>(
                         stage + rr * 128 + ((cc ^ (rr & 7)) << 4));
-                    if (rr >= rows || col >= Dh) continue;
-                    if (part)
-                        *reinterpret_cast<float4 *>(p.part_o + (prow + rr) * Dh + col) = o;
-                    else
-                        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + u * Dh +
-                                                   col) =
-                            make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+                    const int64_t at = (part ? prow + rr : u) * Dh + col;
+                    if (rr < rows && col < Dh) {
+                        if (part)
+                            *reinterpret_cast<float4 *>(p.part_o + at) = o;
+                        else
+                            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at) =
+                                make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+                    }
+                    __syncwarp();
                 }
                 __syncwarp();
             }
@@ -1060,9 +1081,9 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             for (int isv = 0; isv < 2; ++isv) {
                 const int u = 2 * jt + isv, rs = u % C::RU;
                 const int nb = isv ? C::VB : C::KB, s = jt % nb;
-                alive = warp_wait_bounded(bar(C::B_RFULL + rs), (uint32_t)(u / C::RU) & 1u,
+                alive = wait_warp(bar(C::B_RFULL + rs), (uint32_t)(u / C::RU) & 1u,
                                           p.dev_error, s_abort) &&
-                        warp_wait_bounded(bar((isv ? C::B_VEMPTY : C::B_KEMPTY) + s),
+                        wait_warp(bar((isv ? C::B_VEMPTY : C::B_KEMPTY) + s),
                                           ((uint32_t)(jt / nb) & 1u) ^ 1u, p.dev_error, s_abort);
                 if (!alive) break;
                 if (!isv && !((s_bad[jt % kInfo] >> (lane * 4 >> bs_shift)) & 1u))
