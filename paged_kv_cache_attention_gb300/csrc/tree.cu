@@ -84,7 +84,7 @@ struct Cfg {
     static constexpr int RU = !KV8 ? 0 : T == 256 ? 1 : 4;
     static constexpr int RAW = T * kTile;
     static constexpr int ROWB = T < 128 ? T : 128;   // bytes of a raw box row
-    static constexpr int DW = !KV8 ? 0 : X == 2 ? 2 : 4;  // converting warps
+    static constexpr int DW = !KV8 ? 0 : X == 2 ? 4 : 8;  // converting warps
     static constexpr int W_TMA = 4 * X, W_MMA = 4 * X + 1, W_CVT = 4 * X + 2;
     static constexpr int THREADS = 32 * (4 * X + 2 + DW);
     static constexpr int TMEM = 512;                 // two S of 128 columns, X O of T
@@ -217,6 +217,21 @@ __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, int32_t 
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int32_t *dev_error,
                                           int32_t *abort = nullptr) {
     return __all_sync(0xffffffffu, wait_one(bar, parity, dev_error, abort));
+}
+
+// One lane of a converged warp, always the same.  The compiler knows that only one
+// thread goes on, and keeps descriptors and coordinates in uniform registers: a
+// group of 8 products takes 160 cycles to issue, against 460 under lane == 0.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t on;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(on)
+        :
+        : "memory");
+    return on != 0;
 }
 
 // Whether the phase has completed, without waiting.
@@ -372,6 +387,25 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         bool alive = true;
         int nk = 0, nv = 0, nfix = 0;  // tiles (8-bit: raw tiles) and repaired tiles so far
         uint32_t landed = 0;           // bit i: the last use of V buffer i was a repaired tile
+        // The boxes of a tile: page j's rows lie in lane j's `row`.
+        auto load_tile = [&](const CUtensorMap *tm, uint32_t dst, uint32_t full, int row) {
+            constexpr int B = KV8 ? C::ROWB : 128;           // bytes of a box row
+            constexpr int PARTS = KV8 ? T / C::ROWB : C::HALVES;
+            int rows[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) rows[j] = __shfl_sync(0xffffffffu, row, j);
+            if (elect_one()) {
+                mbar_arrive_expect_tx(full, KV8 ? C::RAW : C::TILE);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j < npg)
+#pragma unroll
+                        for (int h = 0; h < PARTS; ++h)
+                            tma_load_3d(dst + h * (kTile * B) + j * BS * B, tm, full,
+                                        h * (KV8 ? 128 : 64), cy, rows[j]);
+            }
+            __syncwarp();
+        };
         auto load_segment = [&](const Seg &sg) {
             const int tok_lo = sg.tok_lo, tok_hi = sg.tok_hi;
             // 32 page ids per warp-wide load, a load ahead: beside 150 streaming SMs
@@ -384,52 +418,53 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                 return pg >= first && pg <= last ? bt[pg] : -1;
             };
             int ids = -1, ids_next = page_ids(0);
-            for (int i = 0; i < sg.ntiles && alive; ++i) {
-                if (i % tpb == 0) {
-                    ids = ids_next;
-                    ids_next = page_ids(i + tpb);
-                }
-                int id = __shfl_sync(0xffffffffu, ids, ((i % tpb) * npg + lane) & 31);
-                const int pg = (sg.tile0 + i) * npg + lane;
-                const bool attended = lane < npg && pg >= first && pg <= last;
-                const bool bad = attended && (id < 0 || id >= p.num_blocks);
-                if (bad) flag_error(p.dev_error, PKV_DEVERR_BLOCK_ID);
-                if (!attended || bad) id = -1;
-                const int row = id < 0 ? oob : p.hnd ? id * Hkv + g : id * BS;
-                const int id_now = id, jn = KV8 ? nk / 2 : nk;
-                const uint32_t badpg = __ballot_sync(0xffffffffu, bad);
-                if (lane == 0) {
-                    s_bad[jn % kInfo] = (uint8_t)badpg;
-                    mbar_arrive(bar(C::B_INFO + jn % kInfo));
+            // bf16: V goes one tile behind K, so that the products of the next tile's
+            // K do not wait for the V slots
+            int row_v = oob;
+            for (int i = 0; i < sg.ntiles + (KV8 ? 0 : 1) && alive; ++i) {
+                int row = oob, id = -1;
+                if (KV8 || i < sg.ntiles) {
+                    if (i % tpb == 0) {
+                        ids = ids_next;
+                        ids_next = page_ids(i + tpb);
+                    }
+                    id = __shfl_sync(0xffffffffu, ids, ((i % tpb) * npg + lane) & 31);
+                    const int pg = (sg.tile0 + i) * npg + lane;
+                    const bool attended = lane < npg && pg >= first && pg <= last;
+                    const bool bad = attended && (id < 0 || id >= p.num_blocks);
+                    if (bad) flag_error(p.dev_error, PKV_DEVERR_BLOCK_ID);
+                    if (!attended || bad) id = -1;
+                    if (id >= 0) row = p.hnd ? id * Hkv + g : id * BS;
+                    const uint32_t badpg = __ballot_sync(0xffffffffu, bad);
+                    const int jn = KV8 ? nk / 2 : nk;
+                    if (lane == 0) {
+                        s_bad[jn % kInfo] = (uint8_t)badpg;
+                        mbar_arrive(bar(C::B_INFO + jn % kInfo));
+                    }
                 }
                 if constexpr (!KV8) {
-                    const int ks = nk % C::KB, vs = nv % C::VB;
-                    // lane -> (page, 64-dim half)
-                    const int lp = lane / C::HALVES, lh = lane % C::HALVES;
-                    const int brow = __shfl_sync(0xffffffffu, row, lp);
-                    alive = wait_warp(bar(C::B_KEMPTY + ks),
-                                              ((uint32_t)(nk / C::KB) & 1u) ^ 1u, p.dev_error,
-                                              s_abort);
-                    if (!alive) break;
-                    if (lane == 0) mbar_arrive_expect_tx(bar(C::B_KFULL + ks), C::TILE);
-                    __syncwarp();
-                    if (lp < npg)
-                        tma_load_3d(base + C::OFF_K + ks * C::TILE + lh * C::HALF + lp * BS * 128,
-                                    &tmk, bar(C::B_KFULL + ks), lh * 64, cy, brow);
-                    ++nk;
+                    if (i < sg.ntiles) {
+                        const int ks = nk % C::KB;
+                        alive = wait_warp(bar(C::B_KEMPTY + ks),
+                                          ((uint32_t)(nk / C::KB) & 1u) ^ 1u, p.dev_error,
+                                          s_abort);
+                        if (!alive) break;
+                        load_tile(&tmk, base + C::OFF_K + ks * C::TILE, bar(C::B_KFULL + ks), row);
+                        ++nk;
+                    }
+                    const int vrow = row_v;
+                    row_v = row;
+                    if (i == 0) continue;
+                    const int iv = i - 1, vs = nv % C::VB;
                     alive = wait_warp(bar(C::B_VEMPTY + vs),
                                               ((uint32_t)(nv / C::VB) & 1u) ^ 1u, p.dev_error,
                                               s_abort);
                     if (!alive) break;
-                    const bool fix = sg.partial(i);
+                    const bool fix = sg.partial(iv);
                     landed = fix ? landed | 1u << vs : landed & ~(1u << vs);
                     const uint32_t vbar = fix ? bar(C::B_LAND) : bar(C::B_VFULL + vs);
                     const uint32_t vb = base + C::OFF_V + vs * C::TILE;
-                    if (lane == 0) mbar_arrive_expect_tx(vbar, C::TILE);
-                    __syncwarp();
-                    if (lp < npg)
-                        tma_load_3d(vb + lh * C::HALF + lp * BS * 128, &tmv, vbar, lh * 64, cy,
-                                    brow);
+                    load_tile(&tmv, vb, vbar, vrow);
                     ++nv;
                     if (fix) {
                         alive = wait_warp(bar(C::B_LAND), (uint32_t)nfix & 1u, p.dev_error,
@@ -439,7 +474,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                         // lane owns rows lane, lane + 32, ..: rows outside the range
                         // are zeroed, and rows with an infinity or a NaN, noted
                         uint32_t *pois = s_poison + ((nfix - 1) & 1) * 4;
-                        const int k0 = (sg.tile0 + i) * kTile;
+                        const int k0 = (sg.tile0 + iv) * kTile;
 #pragma unroll 1
                         for (int w = 0; w < 4; ++w) {
                             const int r = w * 32 + lane, key = k0 + r;
@@ -471,11 +506,8 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                         }
                     }
                 } else {
-                    constexpr int PARTS = T / C::ROWB;  // boxes across the head size
-                    const int lp = lane / PARTS, lh = lane % PARTS;
-                    const int brow = __shfl_sync(0xffffffffu, row, lp);
                     // scale bytes: lane l < 8 copies bytes 16 l .. of the tile
-                    const int sid = __shfl_sync(0xffffffffu, id_now, (lane * 16 >> bs_shift) & 31);
+                    const int sid = __shfl_sync(0xffffffffu, id, (lane * 16 >> bs_shift) & 31);
                     for (int v = 0; v < 2 && alive; ++v) {
                         const int s = nk % C::RU;
                         const uint32_t full = bar(C::B_RFULL + s);
@@ -483,12 +515,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                                                   ((uint32_t)(nk / C::RU) & 1u) ^ 1u, p.dev_error,
                                                   s_abort);
                         if (!alive) break;
-                        if (lane == 0) mbar_arrive_expect_tx(full, C::RAW);
-                        __syncwarp();
-                        if (lp < npg)
-                            tma_load_3d(base + C::OFF_RAW + s * C::RAW +
-                                            lh * (kTile * C::ROWB) + lp * BS * C::ROWB,
-                                        v ? &tmv : &tmk, full, lh * 128, cy, brow);
+                        load_tile(v ? &tmv : &tmk, base + C::OFF_RAW + s * C::RAW, full, row);
                         if (lane < 8) {
                             if (sid >= 0)
                                 cp_async16(base + C::OFF_SCALE + s * kTile + lane * 16,
@@ -622,7 +649,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             if (!sg) break;
             const int nx = sg->nrows > kTile ? 2 : 1, total = sg->ntiles * nx;
             release(ns);
-            if (lane == 0) {
+            if (elect_one()) {
                 int sx = 0;             // row tile of the next S
                 bool k_ready = false;
                 // S of unit n; `must`: waits for its K tile, else gives up if that is
@@ -697,7 +724,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                 // a wait gave up: let the products in flight finish (bounded)
                 if (!alive) wait_one(bar(C::B_O), (uint32_t)ns & 1u, p.dev_error);
             }
-            alive = __shfl_sync(0xffffffffu, alive ? 1 : 0, 0) != 0;
+            alive = __all_sync(0xffffffffu, alive);
         }
         __syncwarp();
     } else if (warp < 4 * X) {
@@ -1138,7 +1165,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                                             : rq * 64u + ((cc ^ ((rq >> 1) & 3)) << 4));
                 }
                 const uint32_t do0 = sw128(rq, 2 * c4), do1 = sw128(rq, 2 * c4 + 1);
-                constexpr int BATCH = T == 256 ? 2 : 4;  // groups whose loads are in flight
+                constexpr int BATCH = T == 256 ? 1 : C::DW == 8 ? 2 : 4;  // groups in flight
 #pragma unroll 1
                 for (int g0 = 0; g0 < ROWS / 8; g0 += BATCH) {
                     uint4 code[BATCH][C::HALVES];
