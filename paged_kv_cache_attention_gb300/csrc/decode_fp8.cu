@@ -195,7 +195,7 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
         const int s = j % NST;
         const uint32_t bar = wbars + 8 * s;
         const int first = (st_lo + warp + j * kWarps) * TOK;  // the stage's first token
-        if (lane == 0) {
+        if (elect_one()) {
             int id[TOK / BR];
             uint32_t bytes = 0;
 #pragma unroll

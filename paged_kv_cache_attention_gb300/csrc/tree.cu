@@ -219,21 +219,6 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int32_t
     return __all_sync(0xffffffffu, wait_one(bar, parity, dev_error, abort));
 }
 
-// One lane of a converged warp, always the same.  The compiler knows that only one
-// thread goes on, and keeps descriptors and coordinates in uniform registers: a
-// group of 8 products takes 160 cycles to issue, against 460 under lane == 0.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t on;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(on)
-        :
-        : "memory");
-    return on != 0;
-}
-
 // Whether the phase has completed, without waiting.
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     uint32_t ok;
