@@ -85,6 +85,10 @@ struct Cfg {
     static constexpr int RAW = T * kTile;
     static constexpr int ROWB = T < 128 ? T : 128;   // bytes of a raw box row
     static constexpr int DW = !KV8 ? 0 : X == 2 ? 4 : 8;  // converting warps
+    // K and V are converted side by side, each by half of them, unless both pass
+    // through one raw tile
+    static constexpr bool SPLIT = KV8 && RU > 1;
+    static constexpr int FILL = !KV8 ? 1 : SPLIT ? DW / 2 : DW;  // warps that fill a tile
     static constexpr int W_TMA = 4 * X, W_MMA = 4 * X + 1, W_CVT = 4 * X + 2;
     static constexpr int THREADS = 32 * (4 * X + 2 + DW);
     static constexpr int TMEM = 512;                 // two S of 128 columns, X O of T
@@ -99,13 +103,14 @@ struct Cfg {
     static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + KB, B_VFULL = B_KEMPTY + KB,
                          B_VEMPTY = B_VFULL + VB, B_SFULL = B_VEMPTY + VB,
                          B_PFULL = B_SFULL + 2, B_O = B_PFULL + 2, B_LAND = B_O + 1,
-                         B_POISON = B_LAND + 1, B_FACT = B_POISON + 2, B_RFULL = B_FACT + 2,
+                         B_POISON = B_LAND + 1, B_KFACT = B_POISON + 2, B_VFACT = B_KFACT + 4,
+                         B_RFULL = B_VFACT + 2,
                          B_REMPTY = B_RFULL + RU, B_Q = B_REMPTY + RU, B_IFULL = B_Q + 1,
                          B_IEMPTY = B_IFULL + kRing, B_INFO = B_IEMPTY + kRing,
                          NBAR = B_INFO + kInfo;
-    // tmem, abort, bad pages[kInfo] (8 bits each), poison[2][4], scale bytes[2][K, V]
+    // tmem, abort, bad pages[kInfo] (8 bits each), poison[2][4], scale bytes: K[4], V[2]
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-    static constexpr int SMEM = 1024 + OFF_MISC + 64;
+    static constexpr int SMEM = 1024 + OFF_MISC + 80;
     static_assert(256 + X * T <= 512, "tensor memory");
     static_assert(SMEM <= 232448, "shared memory");
 };
@@ -263,7 +268,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
     int32_t *s_abort = reinterpret_cast<int32_t *>(misc + 1);
     volatile uint8_t *s_bad = reinterpret_cast<uint8_t *>(misc + 2);  // [kInfo]
     uint32_t *s_poison = misc + 4;   // [2][4]
-    uint32_t *s_byte = misc + 12;    // [2][K, V]: a tile's largest scale bytes
+    uint32_t *s_byte = misc + 12;    // K[4], V[2]: a tile's largest scale bytes
     Seg *ring = reinterpret_cast<Seg *>(smem + C::OFF_RING);
     auto bar = [&](int i) { return base + C::OFF_BAR + 8 * i; };
 
@@ -275,27 +280,27 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
 
     // ---- set-up: barriers and TMEM
     if (threadIdx.x == 32 * C::W_TMA) {
-        constexpr int kFill = KV8 ? C::DW : 1;  // arrivals that fill a tile
         for (int i = 0; i < C::KB; ++i) {
-            mbar_init(bar(C::B_KFULL + i), kFill);
+            mbar_init(bar(C::B_KFULL + i), C::FILL);
             mbar_init(bar(C::B_KEMPTY + i), 1);
         }
         for (int i = 0; i < C::VB; ++i) {
-            mbar_init(bar(C::B_VFULL + i), kFill);
+            mbar_init(bar(C::B_VFULL + i), C::FILL);
             mbar_init(bar(C::B_VEMPTY + i), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(C::B_SFULL + i), 1);
             mbar_init(bar(C::B_PFULL + i), 4);
-            mbar_init(bar(C::B_POISON + i), kFill);
-            mbar_init(bar(C::B_FACT + i), 1);
+            mbar_init(bar(C::B_POISON + i), C::FILL);
+            mbar_init(bar(C::B_VFACT + i), 1);
         }
+        for (int i = 0; i < 4; ++i) mbar_init(bar(C::B_KFACT + i), 1);
         mbar_init(bar(C::B_O), 1);
         mbar_init(bar(C::B_LAND), 1);
         mbar_init(bar(C::B_Q), 4 * X);
         for (int i = 0; i < C::RU; ++i) {
             mbar_init(bar(C::B_RFULL + i), 1 + 8);
-            mbar_init(bar(C::B_REMPTY + i), C::DW);
+            mbar_init(bar(C::B_REMPTY + i), C::FILL);
         }
         for (int i = 0; i < kInfo; ++i) mbar_init(bar(C::B_INFO + i), 1);
         for (int i = 0; i < kRing; ++i) {
@@ -379,6 +384,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             int rows[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) rows[j] = __shfl_sync(0xffffffffu, row, j);
+            __syncwarp();
             if (elect_one()) {
                 mbar_arrive_expect_tx(full, KV8 ? C::RAW : C::TILE);
 #pragma unroll
@@ -806,8 +812,10 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             alive = wait_warp(bar(C::B_SFULL + (n & 1)), (uint32_t)(n >> 1) & 1u,
                                       p.dev_error, s_abort);
             if (KV8 && alive)
-                alive = wait_warp(bar(C::B_FACT + (jn & 1)), (uint32_t)(jn >> 1) & 1u,
-                                          p.dev_error, s_abort);
+                alive = wait_warp(bar(C::B_KFACT + (jn & 3)), (uint32_t)(jn >> 2) & 1u,
+                                  p.dev_error, s_abort) &&
+                        wait_warp(bar(C::B_VFACT + (jn & 1)), (uint32_t)(jn >> 1) & 1u,
+                                  p.dev_error, s_abort);
             if (fix && alive) {
                 alive = wait_warp(bar(C::B_POISON + (nfix & 1)),
                                           (uint32_t)(nfix >> 1) & 1u, p.dev_error, s_abort);
@@ -818,9 +826,9 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                 tc::fence_after_sync();
                 float rf = rowf, vexp = 0.f, shift = 0.f;
                 if constexpr (KV8) {
-                    const volatile uint32_t *by = s_byte + (jn & 1) * 2;
-                    rf *= scale_value(by[0]);
-                    vexp = (float)((int)by[1] - 127);
+                    const volatile uint32_t *by = s_byte;
+                    rf *= scale_value(by[jn & 3]);
+                    vexp = (float)((int)by[4 + (jn & 1)] - 127);
                     shift = vexp - kWeightExp;
                 }
                 // Chunk c (32 keys) of S as complete scores in log2 units: with bias,
@@ -1075,8 +1083,8 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         // 128 / DW rows of every K and V tile per warp; a lane converts 16 codes at
         // a time.  Rows r and r ^ 5 go side by side: their 16-byte chunks, four of
         // each, meet no bank twice, neither where they are read nor written.
-        constexpr int ROWS = kTile / C::DW;
-        const int w = warp - C::W_CVT;
+        constexpr int ROWS = kTile / C::FILL;
+        const int w = (warp - C::W_CVT) % C::FILL, side = (warp - C::W_CVT) / C::FILL;
         bool alive = true;
         int jt = 0, nfix = 0;                // key tiles and repaired tiles so far
         for (int ns = 0; alive; ++ns) {
@@ -1088,9 +1096,8 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             const int k0 = (sg.tile0 + i) * kTile;
             uint32_t in4 = 0;  // lane: which of rows 4 lane .. 4 lane + 3 are attended
             const bool fix = sg.partial(i);
-            uint32_t kmax = 1;
 #pragma unroll 1
-            for (int isv = 0; isv < 2; ++isv) {
+            for (int isv = side; isv < (C::SPLIT ? side + 1 : 2); ++isv) {
                 const int u = 2 * jt + isv, rs = u % C::RU;
                 const int nb = isv ? C::VB : C::KB, s = jt % nb;
                 alive = wait_warp(bar(C::B_RFULL + rs), (uint32_t)(u / C::RU) & 1u,
@@ -1098,7 +1105,8 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                         wait_warp(bar((isv ? C::B_VEMPTY : C::B_KEMPTY) + s),
                                           ((uint32_t)(jt / nb) & 1u) ^ 1u, p.dev_error, s_abort);
                 if (!alive) break;
-                if (!isv && !((s_bad[jt % kInfo] >> (lane * 4 >> bs_shift)) & 1u))
+                in4 = 0;
+                if (!((s_bad[jt % kInfo] >> (lane * 4 >> bs_shift)) & 1u))
                     in4 = range_bits(tok_lo - k0 - 4 * lane, tok_hi - k0 - 4 * lane) & 15u;
                 const uint8_t *sc = smem + C::OFF_SCALE + rs * kTile;
                 // the largest scale byte of the attended rows, NaN rows aside; not
@@ -1111,13 +1119,12 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     if (((in4 >> e) & 1u) && by != kScaleNaN) top = max(top, by);
                 }
                 top = __reduce_max_sync(0xffffffffu, top);
-                if (!isv) {
-                    kmax = top;
-                } else if (w == 0 && lane == 0) {
-                    // V's buffer is free, so the softmax that last used this slot is done
-                    s_byte[(jt & 1) * 2] = kmax;
-                    s_byte[(jt & 1) * 2 + 1] = top;
-                    mbar_arrive(bar(C::B_FACT + (jt & 1)));
+                if (w == 0 && lane == 0) {
+                    // The softmax that last used the slot is done: V's that of two tiles
+                    // ago, as its buffer is free; K's that of four tiles ago, as S of
+                    // two tiles ago is done, which came behind that tile's O.
+                    s_byte[isv ? 4 + (jt & 1) : jt & 3] = top;
+                    mbar_arrive(bar(isv ? C::B_VFACT + (jt & 1) : C::B_KFACT + (jt & 3)));
                 }
                 // NaN rows of a V tile that some row does not see are zeroed and noted
                 uint32_t bad4 = 0;
@@ -1150,7 +1157,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                                             : rq * 64u + ((cc ^ ((rq >> 1) & 3)) << 4));
                 }
                 const uint32_t do0 = sw128(rq, 2 * c4), do1 = sw128(rq, 2 * c4 + 1);
-                constexpr int BATCH = T == 256 ? 1 : C::DW == 8 ? 2 : 4;  // groups in flight
+                constexpr int BATCH = T == 256 ? 2 : 4;  // groups whose loads are in flight
 #pragma unroll 1
                 for (int g0 = 0; g0 < ROWS / 8; g0 += BATCH) {
                     uint4 code[BATCH][C::HALVES];
