@@ -77,14 +77,14 @@ struct Cfg {
     static constexpr int TILE = HALVES * HALF;
     // K and V tiles: as many as fit, for the bytes in flight (over 8-bit pools the
     // raw tiles are what is in flight)
-    static constexpr int KB = KV8 ? (T <= 128 ? 2 : 1) : T == 64 ? 4 : T == 128 ? 3 : 1;
-    static constexpr int VB = KV8 ? (T == 64 || (T == 128 && X == 1) ? 2 : 1)
+    static constexpr int KB = KV8 ? (T == 64 || (T == 128 && X == 1) ? 2 : 1) : T == 64 ? 4 : T == 128 ? 3 : 1;
+    static constexpr int VB = KV8 ? (T <= 128 ? 2 : 1)
                                   : T == 64 ? 4 : T == 128 ? 4 - X : 1;
     // raw tiles of codes, K and V in turn
     static constexpr int RU = !KV8 ? 0 : T == 256 ? 1 : 4;
     static constexpr int RAW = T * kTile;
     static constexpr int ROWB = T < 128 ? T : 128;   // bytes of a raw box row
-    static constexpr int DW = !KV8 ? 0 : X == 2 ? 4 : 8;  // converting warps
+    static constexpr int DW = !KV8 ? 0 : 4;        // converting warps
     // K and V are converted side by side, each by half of them, unless both pass
     // through one raw tile
     static constexpr bool SPLIT = KV8 && RU > 1;
@@ -804,23 +804,29 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             const int n = un + j * nx + x, jn = jt + j;
             const uint32_t t_s = tmem + (n & 1) * 128 + lane_base;
             const bool fix = j < full_lo || j >= full_hi;
-            alive = wait_warp(bar(C::B_INFO + jn % kInfo), (uint32_t)(jn / kInfo) & 1u,
-                                      p.dev_error, s_abort);
-            if (!alive) break;
-            const uint32_t badpg = s_bad[jn % kInfo];
-            const bool general = fix || badpg != 0 || p.alibi != nullptr;
-            alive = wait_warp(bar(C::B_SFULL + (n & 1)), (uint32_t)(n >> 1) & 1u,
-                                      p.dev_error, s_abort);
-            if (KV8 && alive)
-                alive = wait_warp(bar(C::B_KFACT + (jn & 3)), (uint32_t)(jn >> 2) & 1u,
-                                  p.dev_error, s_abort) &&
-                        wait_warp(bar(C::B_VFACT + (jn & 1)), (uint32_t)(jn >> 1) & 1u,
-                                  p.dev_error, s_abort);
+            // All barriers are tried at once, and waited for in turn if one of them is
+            // not there yet: a wait costs 130 cycles even where there is nothing to
+            // wait for.
+            const uint32_t b_info = bar(C::B_INFO + jn % kInfo), b_s = bar(C::B_SFULL + (n & 1));
+            const uint32_t ph_info = (uint32_t)(jn / kInfo) & 1u, ph_s = (uint32_t)(n >> 1) & 1u;
+            const uint32_t b_k = bar(C::B_KFACT + (jn & 3)), ph_k = (uint32_t)(jn >> 2) & 1u;
+            const uint32_t b_v = bar(C::B_VFACT + (jn & 1)), ph_v = (uint32_t)(jn >> 1) & 1u;
+            bool ready = mbar_test(b_info, ph_info) & mbar_test(b_s, ph_s);
+            if (KV8) ready = ready & mbar_test(b_k, ph_k) & mbar_test(b_v, ph_v);
+            if (!__all_sync(0xffffffffu, ready)) {
+                alive = wait_warp(b_info, ph_info, p.dev_error, s_abort) &&
+                        wait_warp(b_s, ph_s, p.dev_error, s_abort);
+                if (KV8 && alive)
+                    alive = wait_warp(b_k, ph_k, p.dev_error, s_abort) &&
+                            wait_warp(b_v, ph_v, p.dev_error, s_abort);
+            }
             if (fix && alive) {
-                alive = wait_warp(bar(C::B_POISON + (nfix & 1)),
-                                          (uint32_t)(nfix >> 1) & 1u, p.dev_error, s_abort);
+                alive = wait_warp(bar(C::B_POISON + (nfix & 1)), (uint32_t)(nfix >> 1) & 1u,
+                                  p.dev_error, s_abort);
                 ++nfix;
             }
+            const uint32_t badpg = s_bad[jn % kInfo];
+            const bool general = fix || badpg != 0 || p.alibi != nullptr;
             if (!alive) break;
             if (warp_on) {
                 tc::fence_after_sync();
