@@ -29,7 +29,14 @@
  *                          rows cu_seq_lens_k[r] .. cu_seq_lens_k[r+1]-1 of
  *                          contiguous [total_k, num_kv_heads, head_dim] K and
  *                          V arrays (the docs' varlen path before the keys are
- *                          paged).
+ *                          paged);
+ *   pkv_reshape_and_cache_fp8, pkv_gather_cache_fp8, pkv_paged_decode_fp8
+ *                          the write, the read back and the decode of a cache
+ *                          of 8-bit codes with a scale per token and kv head;
+ *   pkv_qk_norm_rope_reshape_and_cache  RMS norm of the q and k heads, rotary
+ *                          embedding and cache write in one pass;
+ *   pkv_paged_tree_attention  attention of a tree of drafted tokens per request
+ *                          over its pages (bf16 or 8-bit).
  *
  * What the attention computes (FlashInfer sink_attention_reference.py,
  * sink_softmax and sink_attention_unified): for request r, query row i and
@@ -449,7 +456,9 @@ PKV_API pkv_status pkv_paged_decode_noalloc(void *out, const void *q, const void
  * head row x of D values and a = max_i |x_i|,
  *   e = ceil(log2(a / 448)) clamped to [-126, 119], byte = e + 127,
  *   code_i = the e4m3 value nearest x_i * 2^-e (ties to even), at most 448.
- * A row with a NaN or an infinity gets byte 255 and codes 0.
+ * A row with a NaN or an infinity gets byte 255 and codes 0.  A slot is given at
+ * most once: two tokens with the same one race, and may leave the codes of one
+ * with the scale of the other.
  *   key, value    rows of `dtype` (PKV_BF16 or PKV_F32): token t, kv head h at
  *                 element t * key_stride + h * D (value_stride alike); strides
  *                 are in elements, at least Hkv * D and multiples of 16 bytes,

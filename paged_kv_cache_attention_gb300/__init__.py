@@ -22,6 +22,13 @@ Operations (same names as the C ABI):
     ``cu_seq_lens_q`` / ``cu_seq_lens_k`` (transformers docs
     "paged_attention", varlen path), keys read from the pages, causal or not;
     ``varlen_prefill_contiguous`` reads them from [total_k, Hkv, D] arrays;
+  * ``reshape_and_cache_fp8``, ``gather_cache_fp8`` and ``paged_decode_fp8`` --
+    the write, the read back (as bf16) and the decode of an 8-bit cache: e4m3
+    codes with one power-of-two scale per token and kv head;
+  * ``qk_norm_rope_reshape_and_cache`` -- the RMS norm of the q and k heads, the
+    rotary embedding and the cache write (bf16, float32 or 8-bit pools) fused;
+  * ``paged_tree_attention`` -- attention of a tree of up to 256 drafted tokens
+    per request over its pages (bf16 or 8-bit), for speculative decoding;
   * ``minference_prefill`` -- MInference's vertical + slash sparse prefill of
     one sequence (nano-vllm minference.py): pattern estimate, top-k, then
     attention over the kept keys.
@@ -695,7 +702,7 @@ def _fp8_pools(k_cache, v_cache, k_scale, v_scale, layout: str, dev: int) -> Cac
         key = (shape, layout)
         d = _descs.get(key)
         if d is not None and v_cache.shape == shape and \
-                k_scale.shape == v_scale.shape == _scale_shapes[key]:
+                k_scale.shape == v_scale.shape == _scale_shapes.get(key):
             return d
     _require(k_scale is not None, "k_scale is needed for an 8-bit cache")
     _require(v_scale is not None, "v_scale is needed for an 8-bit cache")
@@ -776,6 +783,8 @@ def _on_stream(dev: int, stream, call):
         return call(_stream_handle(stream))
     t = _types()
     if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError("stream must be of the tensors' device")
         with t.torch.cuda.stream(stream):
             return call(stream.cuda_stream)
     if t.device() != dev:
@@ -817,7 +826,8 @@ def reshape_and_cache_fp8(key, value, k_cache, v_cache, k_scale, v_scale, slot_m
     Hkv, block_size] uint8): value = code * 2^(byte - 127), the exponent the
     smallest that keeps max|x| within 448.  A row with a NaN or an infinity is
     stored as byte 255 and reads as NaN.  slot_mapping: [T] int64, negative =
-    skip; dev_error receives PKV_DEVERR_SLOT for slots outside the pool."""
+    skip, each slot at most once (tokens that share one leave a mixture there);
+    dev_error receives PKV_DEVERR_SLOT for slots outside the pool."""
     dev = _cuda_index("key", key)
     desc = _fp8_pools(k_cache, v_cache, k_scale, v_scale, layout, dev)
     dtype, T = key.dtype, key.size(0)
@@ -943,7 +953,8 @@ def qk_norm_rope_reshape_and_cache(query, key, value, k_cache, v_cache, position
 
     Rows are bf16 or float32; a token's heads are contiguous and tokens may
     have any stride (slices of a fused projection).  The rotated rows go to
-    query_out / key_out, or back in place when these are None.  With k_scale and
+    query_out / key_out (which overlap no other argument), or back in place when
+    these are None.  With k_scale and
     v_scale the pools are the 8-bit cache of reshape_and_cache_fp8, else pools of
     the rows' dtype.  query (with query_out and q_weight) may be None."""
     ty = _types()
