@@ -733,30 +733,106 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         const bool positions = p.window_left >= 0 || p.alibi;
         int un = 0, jt = 0, nfix = 0;        // units, key tiles and repaired tiles so far
         bool alive = true;
-        const Seg *sp = segment(0);
-        for (int ns = 0; sp && alive; ++ns) {
-        const Seg &sg = *sp;                 // stays in the ring until it is released
-        const int ntiles = sg.ntiles, nx = sg.nrows > kTile ? 2 : 1;
-        const int full_lo = sg.full_lo, full_hi = sg.full_hi;
-        const bool warp_on = warp * 32 < sg.nrows, row_on = r < sg.nrows;
-        // ---- this warp's rows of Q into shared memory (rows past the last: zeros),
-        // LPR lanes per row
-        const int64_t unit = unit_of(sg);
-        float rowf = fabsf(p.scale_log2);  // score = S * rowf
-        {
+        // Segment by segment: Q on its way, the rows of the segment before stored
+        // meanwhile, Q's last touch, the key tiles.
+        const Seg *prev = nullptr;
+        float m_ref = kNegInf, l = 0.f;
+        int64_t unit = 0;
+#pragma unroll 1
+        for (int ns = 0;; ++ns) {
+        const Seg *sp = segment(ns);         // stays in the ring until it is released
+        const int64_t unit_prev = unit;
+        if (sp) {
+            // this warp's rows of Q into shared memory (rows past the last: zeros),
+            // LPR lanes per row
+            unit = unit_of(*sp);
             constexpr int LPR = T / 8 < 32 ? T / 8 : 32, RPS = 32 / LPR;
-            const int c = lane % LPR, r0 = lane / LPR;
+            const int c = lane % LPR, r0 = lane / LPR, nrows = sp->nrows;
             const __nv_bfloat16 *qc = static_cast<const __nv_bfloat16 *>(p.q) + c * 8;
             const bool col_on = c * 8 < Dh;
-#pragma unroll 4
+#pragma unroll 1
             for (int k = 0; k < 32 / RPS; ++k) {
                 const int rr = k * RPS + r0;
                 const int64_t u = __shfl_sync(0xffffffffu, unit, rr);
                 const int row = (warp & 3) * 32 + rr;
                 cp_async16_or_zero(sq + (c >> 3) * C::HALF + sw128(row, c & 7),
                                    col_on ? qc + u * Dh : qc,
-                                   col_on && warp * 32 + rr < sg.nrows);
+                                   col_on && warp * 32 + rr < nrows);
             }
+        }
+        if (prev && prev->nrows > warp * 32) {
+            // ---- the rows' results
+            const Seg &sg = *prev;
+            tc::fence_after_sync();
+            // partials: [CTA group][its first or last row group][kv head][row]
+            const bool part = sg.cut() != 0, row_on = r < sg.nrows;
+            const int64_t prow =
+                ((int64_t)(2 * group + sg.cut() / 2) * Hkv + g) * (X * kTile) + r;
+            const int head = g * G + (sg.row0 + min(r, sg.nrows - 1)) % G;
+            float mul, lse;
+            if (part) {
+                mul = l == 0.f ? 0.f : 1.f / l;
+                lse = l == 0.f ? kNegInf : m_ref + log2f(l);
+                if (row_on) p.part_lse[prow] = lse;
+            } else {
+                const float sink = p.sink ? p.sink[head] * kLog2e : kNegInf;
+                const float M = fmaxf(m_ref, sink);
+                const float Ms = M == kNegInf ? 0.f : M;
+                const float f = exp2f(m_ref - Ms);
+                const float lam = l * f + exp2f(sink - Ms);
+                mul = lam == 0.f ? 0.f : f / lam;
+                lse = lam == 0.f ? kNegInf : (Ms + log2f(lam)) * kLn2;
+                // a NaN weight leaves m_ref as it was: keep the NaN
+                if (l != l) mul = lse = l;
+                if (row_on && p.lse_out) p.lse_out[unit_prev] = lse;
+            }
+            // Each thread stores its row, 32 columns at a time: whole sectors, without
+            // a turn through shared memory, where the next segment's Q is landing.
+#pragma unroll 1
+            for (int c = 0; c < T / 32; ++c) {
+                uint32_t v[32];
+                if (sg.ntiles > 0) {
+                    tc::ld_32x32b_x32(t_o + 32 * c, v);
+                    tc::wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = 0u;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * mul);
+                if (row_on && part) {
+                    float4 *o = reinterpret_cast<float4 *>(p.part_o + prow * Dh + 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (32 * c + 4 * e < Dh)
+                            o[e] = make_float4(
+                                __uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
+                                __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
+                } else if (row_on) {
+                    uint4 *o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
+                                                         unit_prev * Dh + 32 * c);
+                    auto two = [&](int e) {
+                        return pack_bf16(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                    };
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (32 * c + 8 * e < Dh)
+                            o[e] = make_uint4(two(8 * e), two(8 * e + 2), two(8 * e + 4),
+                                              two(8 * e + 6));
+                }
+                __syncwarp();
+            }
+            tc::fence_before_sync();
+        }
+        if (prev) release(ns - 1);
+        if (!sp) break;
+        const Seg &sg = *sp;
+        prev = sp;
+        const int ntiles = sg.ntiles, nx = sg.nrows > kTile ? 2 : 1;
+        const int full_lo = sg.full_lo, full_hi = sg.full_hi;
+        const bool warp_on = warp * 32 < sg.nrows, row_on = r < sg.nrows;
+        float rowf = fabsf(p.scale_log2);    // score = S * rowf
+        {
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
             const uint32_t neg = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // its sign goes into q
@@ -799,7 +875,8 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         // Weights are 2^(s - m_ref), over 8-bit pools times the tile's largest V
         // scale.  m_ref follows the row's largest score (there plus that scale
         // over 2^10, so that f16 holds the product); O and l share it.
-        float m_ref = kNegInf, l = 0.f;
+        m_ref = kNegInf;
+        l = 0.f;
         for (int j = 0; j < ntiles && x < nx; ++j) {
             const int n = un + j * nx + x, jn = jt + j;
             const uint32_t t_s = tmem + (n & 1) * 128 + lane_base;
@@ -888,8 +965,12 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     }
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        if ((pois >> e) & 1u) v[e] = 0x7fffffffu;
                         if (!((vis >> e) & 1u)) v[e] = __float_as_uint(kNegInf);
+                    }
+                    if (pois) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if ((pois & vis) >> e & 1u) v[e] = 0x7fffffffu;
                     }
                 };
                 auto maximum = [&](float m, const uint32_t (&v)[32]) {
@@ -1003,86 +1084,6 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         if (alive)
             alive = wait_warp(bar(C::B_O), (uint32_t)ns & 1u, p.dev_error, s_abort);
         if (!alive) break;
-        const Seg *next = segment(ns + 1);
-        if (next && r < next->nrows) {  // its Q rows, on their way to L2 meanwhile
-            const char *row =
-                static_cast<const char *>(p.q) + unit_of(*next) * Dh * 2;
-            for (int k = 0; k < Dh * 2; k += 128)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(row + k));
-        }
-        __syncwarp();
-        // ---- the rows' results
-        if (warp_on) {
-            tc::fence_after_sync();
-            // partials: [CTA group][its first or last row group][kv head][row]
-            const bool part = sg.cut() != 0;
-            const int64_t prow =
-                ((int64_t)(2 * group + sg.cut() / 2) * Hkv + g) * (X * kTile) + warp * 32;
-            const int head = g * G + (sg.row0 + min(r, sg.nrows - 1)) % G;
-            float mul, lse;
-            if (part) {
-                mul = l == 0.f ? 0.f : 1.f / l;
-                lse = l == 0.f ? kNegInf : m_ref + log2f(l);
-                if (row_on) p.part_lse[prow + lane] = lse;
-            } else {
-                const float sink = p.sink ? p.sink[head] * kLog2e : kNegInf;
-                const float M = fmaxf(m_ref, sink);
-                const float Ms = M == kNegInf ? 0.f : M;
-                const float f = exp2f(m_ref - Ms);
-                const float lam = l * f + exp2f(sink - Ms);
-                mul = lam == 0.f ? 0.f : f / lam;
-                lse = lam == 0.f ? kNegInf : (Ms + log2f(lam)) * kLn2;
-                // a NaN weight leaves m_ref as it was: keep the NaN
-                if (l != l) mul = lse = l;
-                if (row_on && p.lse_out) p.lse_out[unit] = lse;
-            }
-            // O goes through this warp's part of the Q tile, 32 columns at a time, so
-            // that whole 128-byte pieces of rows are stored: 16-byte chunk c of row r
-            // lies at chunk c ^ (r % 8), where neither side meets a bank twice
-            const int rows = min(sg.nrows - warp * 32, 32);
-#pragma unroll 1
-            for (int c = 0; c < T / 32; ++c) {
-                uint8_t *stage = smem + C::OFF_Q + x * C::TILE + (c % C::HALVES) * C::HALF +
-                                 (warp & 3) * 4096;
-                uint32_t v[32];
-                if (ntiles > 0) {
-                    tc::ld_32x32b_x32(t_o + 32 * c, v);
-                    tc::wait_ld();
-                }
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (ntiles > 0)
-                        o = make_float4(
-                            __uint_as_float(v[e]) * mul, __uint_as_float(v[e + 1]) * mul,
-                            __uint_as_float(v[e + 2]) * mul, __uint_as_float(v[e + 3]) * mul);
-                    *reinterpret_cast<float4 *>(stage + lane * 128 +
-                                                (((e / 4) ^ (lane & 7)) << 4)) = o;
-                }
-                __syncwarp();
-                const int cc = lane & 7, col = 32 * c + 4 * cc;
-#pragma unroll 2
-                for (int k = 0; k < 8; ++k) {
-                    const int rr = k * 4 + (lane >> 3);
-                    const int64_t u = __shfl_sync(0xffffffffu, unit, rr);
-                    const float4 o = *reinterpret_cast<const float4 *>(
-                        stage + rr * 128 + ((cc ^ (rr & 7)) << 4));
-                    const int64_t at = (part ? prow + rr : u) * Dh + col;
-                    if (rr < rows && col < Dh) {
-                        if (part)
-                            *reinterpret_cast<float4 *>(p.part_o + at) = o;
-                        else
-                            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at) =
-                                make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
-                    }
-                    __syncwarp();
-                }
-                __syncwarp();
-            }
-            tc::fence_before_sync();
-        }
-        release(ns);
-        sp = next;
         }
     } else if constexpr (KV8) {
         // ------------------------------------------------------------ codes -> f16 tiles
