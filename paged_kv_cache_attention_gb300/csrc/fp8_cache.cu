@@ -77,7 +77,7 @@ struct Row16<float> {
 // CTA's groups); group r0 takes the head rows r0, r0 + gpt, .. of the 2 H rows
 // of k and v, for UNR tokens at a time.
 // Registers are capped for six CTAs per SM: on 66001 tokens of 8 heads of 128
-// (GB300) that takes 69 us, 88 % of a copy's rate; five CTAs 75, uncapped with
+// (GB300) that takes 66 us, 91 % of a copy's rate; five CTAs 75, uncapped with
 // four tokens in flight 98, one token 87.
 template <typename T, int LPR, int UNR>
 __global__ void __launch_bounds__(kThreads, 6)
@@ -175,7 +175,9 @@ cudaError_t launch_write(const QuantWriteParams &p, cudaStream_t stream) {
 // ---------------------------------------------------------------------------
 // A CTA takes `rows` consecutive output rows: its first threads find each
 // row's request (binary search in cu_k) and slot, then all threads stream the
-// (row, K or V, head, 16-code vector) space, several vectors in flight.
+// (row, K or V, head, 16-code vector) space, several vectors in flight.  66K rows
+// of 8 heads of 128 (GB300): 67 us, 92 % of a copy's rate; a call of 300 rows
+// takes 2.8 us, launch and one chain of loads.
 constexpr int kMaxGatherRows = 64;
 constexpr int kGatherUnroll = 4;
 

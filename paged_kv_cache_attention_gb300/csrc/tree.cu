@@ -35,7 +35,8 @@
 //
 // Warps: four softmax warps per row tile, one row per thread; a TMA warp, which
 // also works out the CTA's segments and hands them to the others through a
-// ring; an MMA warp; over 8-bit pools the warps that convert codes.
+// ring; an MMA warp; over 8-bit pools the warps that convert codes, K's beside V's
+// (one after the other: 173 us instead of 157 for 8 x 32 drafts over 24K).
 //   S = Q K^T -> TMEM; the softmax reads S twice (maximum, weights), writes P (16
 //   bits) over S; O += P V with P from TMEM.  O is rescaled only when a row's
 //   maximum has grown a lot.
@@ -43,11 +44,28 @@
 // buffers in turn: S(n + 2) is issued right behind O(n), so a unit's softmax
 // always has the other buffer's products beside it -- those of the other row
 // tile, or of the next key tile when there is one.  Two row tiles share every
-// K and V tile.  K and V tiles are double-buffered where shared memory allows.
+// K and V tile.
 // Tiles that hold anything a row does not see (the drafts, the window's edge,
 // the ends of the partition) take a general path with visibility bits; V rows
 // behind the end are zeroed, and a V row with a non-finite value is zeroed too
 // and reaches, as NaN, only the rows that see it.
+//
+// Measured (GB300, 32/8 heads of 128): 8 x 64 drafts over 16K..32K tokens of bf16
+// 195 us, 63 % of a copy's rate; 16 x 24 over 0.5K..8K of the 8-bit cache 78 us,
+// 25 %; 4 x 8 over 60..900 of bf16 17 us, mostly the latency of two kernels.
+// With one row tile and 32-token pages, 8 x 32 over 24K takes 136 us, 87 %.
+//   Two row tiles per CTA (X = 2, heads up to 128) when a request may have more
+// than 128 rows: 8 x 64 drafts over 24K 183 us (8-bit: 241) against 260 (282) with
+// one, which reads K and V twice; 8 x 40 drafts, whose second tile is a quarter
+// full, 164 (221) against 254 (276).
+//   Slower: K and V on their way to L2 two tiles before their loads (70 -> 77 us,
+// 8-bit), fewer converted and more raw tiles (173 -> 198 us), eight converting
+// warps (short cases 73 -> 76 us, long ones 153 -> 149).
+//   What bounds it: with two row tiles 4 x 527 cycles of tensor work in about 4200
+// per key tile, the rest handing S, P and O between the warps; over 8-bit pools
+// the same hand-overs, the conversion's among them, about 3300 cycles per key
+// tile; and some 7 us per row group that a CTA meets, for Q, the general tile and
+// code that is fetched for the first time.
 #include "pkv_fp8.cuh"
 #include "pkv_tcgen05.cuh"
 
@@ -64,7 +82,7 @@ constexpr float kNegInf = -INFINITY;
 // range and lose nothing by it; f16 weights start at 2^kWeightExp and stay
 // below 2^15, with 11 bits kept down to 2^-20 of the reference and an error of
 // 2^-31 of it below that.  With 4 for both, rows of real spread rescaled in half
-// of the tiles: 402 us instead of 230 on 8 x 64 drafts over 16K..32K tokens.
+// of the tiles: 402 us instead of 229 on 8 x 64 drafts over 16K..32K tokens.
 template <bool KV8>
 constexpr float kLazy = KV8 ? 9.f : 24.f;
 constexpr int kWeightExp = 6;
@@ -76,8 +94,11 @@ struct Cfg {
     static constexpr int HALF = kTile * 128;         // 128 rows of 64 dims
     static constexpr int TILE = HALVES * HALF;
     // K and V tiles: as many as fit, for the bytes in flight (over 8-bit pools the
-    // raw tiles are what is in flight)
-    static constexpr int KB = KV8 ? (T == 64 || (T == 128 && X == 1) ? 2 : 1) : T == 64 ? 4 : T == 128 ? 3 : 1;
+    // raw tiles are what is in flight, and an f16 tile each way hides the
+    // conversion; beside two row tiles one K and two V tiles take 241 us, two and
+    // one 251, for 8 x 64 drafts over 24K)
+    static constexpr int KB = KV8 ? (T == 64 || (T == 128 && X == 1) ? 2 : 1)
+                                  : T == 64 ? 4 : T == 128 ? 3 : 1;
     static constexpr int VB = KV8 ? (T <= 128 ? 2 : 1)
                                   : T == 64 ? 4 : T == 128 ? 4 - X : 1;
     // raw tiles of codes, K and V in turn
