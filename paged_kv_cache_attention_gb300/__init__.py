@@ -659,8 +659,7 @@ def _arg_shape(name, t, dtype, shape, dev: int):
 
 def _arg_vector(name, t, dtype, n: int, dev: int):
     """A contiguous vector of n entries."""
-    if (t.dtype is dtype and t.get_device() == dev and t.dim() == 1 and t.size(0) == n
-            and t.is_contiguous()):
+    if t.dtype is dtype and t.get_device() == dev and t.shape == (n,) and t.is_contiguous():
         return
     _arg_shape(name, t, dtype, (n,), dev)
 
@@ -745,8 +744,7 @@ def _pools(k_cache, v_cache, k_scale, v_scale, dtype, layout: str, dev: int) -> 
 def _token_rows(name, t, dtype, tokens: int, heads: int, head_dim: int, dev: int) -> int:
     """Checks [tokens, heads, head_dim] rows whose heads are contiguous; returns
     the elements between tokens (a slice of a fused projection keeps its own)."""
-    if (t.dtype is dtype and t.get_device() == dev and t.dim() == 3 and t.size(0) == tokens
-            and t.size(1) == heads and t.size(2) == head_dim):
+    if t.dtype is dtype and t.get_device() == dev and t.shape == (tokens, heads, head_dim):
         if t.is_contiguous():
             return heads * head_dim
         if t.stride(2) == 1 and (heads == 1 or t.stride(1) == head_dim):
@@ -760,6 +758,7 @@ def _token_rows(name, t, dtype, tokens: int, heads: int, head_dim: int, dev: int
 class _Types:
     """torch and the dtypes the checks compare with, looked up once."""
     torch = bf16 = f32 = i32 = i64 = u8 = e4m3 = None
+    codes = {}                  # pkv_dtype of the rows' dtypes
     device = raw_stream = None  # the current device, and a device's current stream handle
 
 
@@ -768,7 +767,8 @@ def _types():
         import torch
         _Types.bf16, _Types.f32, _Types.i32 = torch.bfloat16, torch.float32, torch.int32
         _Types.i64, _Types.u8, _Types.e4m3 = torch.int64, torch.uint8, torch.float8_e4m3fn
-        _Types.device = torch.cuda.current_device
+        _Types.codes = {torch.bfloat16: PKV_BF16, torch.float32: PKV_F32}
+        _Types.device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         _Types.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                                     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
         _Types.torch = torch
@@ -830,8 +830,10 @@ def reshape_and_cache_fp8(key, value, k_cache, v_cache, k_scale, v_scale, slot_m
     dev_error receives PKV_DEVERR_SLOT for slots outside the pool."""
     dev = _cuda_index("key", key)
     desc = _fp8_pools(k_cache, v_cache, k_scale, v_scale, layout, dev)
-    dtype, T = key.dtype, key.size(0)
-    dt = _dtype_code(dtype)
+    dtype, T = key.dtype, key.shape[0]
+    dt = _types().codes.get(dtype)
+    if dt is None:
+        dt = _dtype_code(dtype)  # which says what it is
     ks = _token_rows("key", key, dtype, T, desc.num_kv_heads, desc.head_dim, dev)
     vs = _token_rows("value", value, dtype, T, desc.num_kv_heads, desc.head_dim, dev)
     _arg_vector("slot_mapping", slot_mapping, _types().i64, T, dev)
@@ -861,8 +863,9 @@ def gather_cache_fp8(k_cache, v_cache, k_scale, v_scale, block_table, cu_seq_len
     desc = _fp8_pools(k_cache, v_cache, k_scale, v_scale, layout, dev)
     _arg("cu_seq_lens_k", cu_seq_lens_k, ty.i32, 1, dev)
     _arg("block_table", block_table, ty.i32, 2, dev)
-    B = cu_seq_lens_k.size(0) - 1
-    _require(B >= 0 and block_table.size(0) == B, "block_table must have one row per request")
+    B = cu_seq_lens_k.shape[0] - 1
+    rows, max_blocks = block_table.shape
+    _require(B >= 0 and rows == B, "block_table must have one row per request")
     total_k = int(total_k)
     _require(total_k >= 0, "total_k must not be negative")
     shape = (total_k, desc.num_kv_heads, desc.head_dim)
@@ -879,7 +882,7 @@ def gather_cache_fp8(k_cache, v_cache, k_scale, v_scale, block_table, cu_seq_len
         return k, v, lib.pkv_gather_cache_fp8(
             k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             k_scale.data_ptr(), v_scale.data_ptr(), desc, block_table.data_ptr(),
-            block_table.size(1), cu_seq_lens_k.data_ptr(), B, total_k, err, handle)
+            max_blocks, cu_seq_lens_k.data_ptr(), B, total_k, err, handle)
     key, value, st = _on_stream(dev, stream, call)
     if st:
         _check("pkv_gather_cache_fp8", st)
@@ -916,7 +919,8 @@ def paged_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_s
     _require(D == desc.head_dim, "head_dim of q and cache differ")
     _arg("block_table", block_table, ty.i32, 2, dev)
     _arg_vector("cache_seqlens", cache_seqlens, ty.i32, B, dev)
-    _require(block_table.size(0) == B, "block_table / cache_seqlens batch mismatch")
+    rows, max_blocks = block_table.shape
+    _require(rows == B, "block_table / cache_seqlens batch mismatch")
     _attention_extras(sink, alibi_slopes, out, lse, q, B, Hq, dev)
     err = _error_word(dev_error, dev)
     scale = float(sm_scale) if sm_scale is not None else D ** -0.5
@@ -932,7 +936,7 @@ def paged_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_s
         return o, lib.pkv_paged_decode_fp8(
             o.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             k_scale.data_ptr(), v_scale.data_ptr(), desc, block_table.data_ptr(),
-            block_table.size(1), cache_seqlens.data_ptr(), max_seqlen, _ptr(sink),
+            max_blocks, cache_seqlens.data_ptr(), max_seqlen, _ptr(sink),
             _ptr(alibi_slopes), B, Hq, window_left, scale, partition_size, _ptr(lse), ws,
             ws_bytes, err, handle)
     out, st = _on_stream(dev, stream, call)
@@ -960,12 +964,14 @@ def qk_norm_rope_reshape_and_cache(query, key, value, k_cache, v_cache, position
     ty = _types()
     dev = _cuda_index("key", key)
     dtype = key.dtype
-    dt = _dtype_code(dtype)
+    dt = ty.codes.get(dtype)
+    if dt is None:
+        dt = _dtype_code(dtype)
     if k_scale is None and v_scale is None:
         desc = _pools(k_cache, v_cache, None, None, dtype, layout, dev)
     else:
         desc = _fp8_pools(k_cache, v_cache, k_scale, v_scale, layout, dev)
-    D, Hkv, T = desc.head_dim, desc.num_kv_heads, key.size(0)
+    D, Hkv, T = desc.head_dim, desc.num_kv_heads, key.shape[0]
     ks = _token_rows("key", key, dtype, T, Hkv, D, dev)
     vs = _token_rows("value", value, dtype, T, Hkv, D, dev)
     kos = ks
@@ -1050,14 +1056,15 @@ def paged_tree_attention(q, k_cache, v_cache, block_table, cu_seq_lens_q, cache_
     _require(D == desc.head_dim, "head_dim of q and cache differ")
     _arg("block_table", block_table, ty.i32, 2, dev)
     _arg("cache_seqlens", cache_seqlens, ty.i32, 1, dev)
-    B = cache_seqlens.size(0)
+    B = cache_seqlens.shape[0]
     _arg_vector("cu_seq_lens_q", cu_seq_lens_q, ty.i32, B + 1, dev)
-    _require(block_table.size(0) == B, "block_table must have one row per request")
+    rows, max_blocks = block_table.shape
+    _require(rows == B, "block_table must have one row per request")
     _arg("tree_mask", tree_mask, ty.i64, 2, dev)
-    words = tree_mask.size(1)
+    rows, words = tree_mask.shape
     max_seqlen_q, max_seqlen = int(max_seqlen_q), int(max_seqlen)
     window_left, partition_size = int(window_left), int(partition_size)
-    _require(tree_mask.size(0) == total_q and 64 * words >= max_seqlen_q,
+    _require(rows == total_q and 64 * words >= max_seqlen_q,
              "tree_mask must be [total_q, words] with words * 64 >= max_seqlen_q")
     if tree_depth is not None:
         _arg_vector("tree_depth", tree_depth, ty.i32, total_q, dev)
@@ -1074,7 +1081,7 @@ def paged_tree_attention(q, k_cache, v_cache, block_table, cu_seq_lens_q, cache_
         ws, ws_bytes, held = _scratch(need, dev, q.device, workspace)
         return o, lib.pkv_paged_tree_attention(
             o.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale),
-            _ptr(v_scale), desc, block_table.data_ptr(), block_table.size(1),
+            _ptr(v_scale), desc, block_table.data_ptr(), max_blocks,
             cu_seq_lens_q.data_ptr(), cache_seqlens.data_ptr(), max_seqlen_q, max_seqlen,
             total_q, tree_mask.data_ptr(), words, _ptr(tree_depth), _ptr(sink),
             _ptr(alibi_slopes), B, Hq, window_left, scale, partition_size, _ptr(lse), ws,
