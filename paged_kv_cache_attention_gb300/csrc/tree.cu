@@ -757,7 +757,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         // Segment by segment: Q on its way, the rows of the segment before stored
         // meanwhile, Q's last touch, the key tiles.
         const Seg *prev = nullptr;
-        float m_ref = kNegInf, l = 0.f;
+        float m_ref = kNegInf, l = 0.f, sink = kNegInf;
         int64_t unit = 0;
 #pragma unroll 1
         for (int ns = 0;; ++ns) {
@@ -769,17 +769,31 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             unit = unit_of(*sp);
             constexpr int LPR = T / 8 < 32 ? T / 8 : 32, RPS = 32 / LPR;
             const int c = lane % LPR, r0 = lane / LPR, nrows = sp->nrows;
-            const __nv_bfloat16 *qc = static_cast<const __nv_bfloat16 *>(p.q) + c * 8;
             const bool col_on = c * 8 < Dh;
-#pragma unroll 1
+            // the lane's first row as (draft, head of the group); RPS rows on, the
+            // head moves by RPS % G, and the draft by RPS / G or one more
+            const int i0 = sp->row0 + warp * 32 + r0, tok0 = i0 / G;
+            int rem = i0 - tok0 * G;
+            const int dr = RPS % G;
+            const int64_t Hq = p.num_qo_heads, step = (RPS / G) * Hq + dr;
+            const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) + c * 8 +
+                                       ((sp->q_start + tok0) * Hq + g * G + rem) * Dh;
+#pragma unroll 2
             for (int k = 0; k < 32 / RPS; ++k) {
-                const int rr = k * RPS + r0;
-                const int64_t u = __shfl_sync(0xffffffffu, unit, rr);
-                const int row = (warp & 3) * 32 + rr;
-                cp_async16_or_zero(sq + (c >> 3) * C::HALF + sw128(row, c & 7),
-                                   col_on ? qc + u * Dh : qc,
-                                   col_on && warp * 32 + rr < nrows);
+                const int rr = k * RPS + r0, row = (warp & 3) * 32 + rr;
+                const bool on = col_on && warp * 32 + rr < nrows;
+                cp_async16_or_zero(sq + (c >> 3) * C::HALF + sw128(row, c & 7), on ? src : p.q, on);
+                src += step * Dh;
+                rem += dr;
+                if (rem >= G) {
+                    rem -= G;
+                    src += (Hq - G) * Dh;
+                }
             }
+            // the row's mask, read in the last key tiles
+            if (r < nrows)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                    p.mask + (int64_t)(sp->q_start + (sp->row0 + r) / G) * p.mask_words));
         }
         if (prev && prev->nrows > warp * 32) {
             // ---- the rows' results
@@ -789,14 +803,12 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             const bool part = sg.cut() != 0, row_on = r < sg.nrows;
             const int64_t prow =
                 ((int64_t)(2 * group + sg.cut() / 2) * Hkv + g) * (X * kTile) + r;
-            const int head = g * G + (sg.row0 + min(r, sg.nrows - 1)) % G;
             float mul, lse;
             if (part) {
                 mul = l == 0.f ? 0.f : 1.f / l;
                 lse = l == 0.f ? kNegInf : m_ref + log2f(l);
                 if (row_on) p.part_lse[prow] = lse;
             } else {
-                const float sink = p.sink ? p.sink[head] * kLog2e : kNegInf;
                 const float M = fmaxf(m_ref, sink);
                 const float Ms = M == kNegInf ? 0.f : M;
                 const float f = exp2f(m_ref - Ms);
@@ -807,39 +819,32 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                 if (l != l) mul = lse = l;
                 if (row_on && p.lse_out) p.lse_out[unit_prev] = lse;
             }
-            // Each thread stores its row, 32 columns at a time: whole sectors, without
+            // Each thread stores its row, 16 columns at a time: whole sectors, without
             // a turn through shared memory, where the next segment's Q is landing.
 #pragma unroll 1
-            for (int c = 0; c < T / 32; ++c) {
-                uint32_t v[32];
-                if (sg.ntiles > 0) {
-                    tc::ld_32x32b_x32(t_o + 32 * c, v);
-                    tc::wait_ld();
-                } else {
+            for (int c = 0; c < T / 16; ++c) {
+                uint32_t v[16];
+                tc::ld_32x32b_x16(t_o + 16 * c, v);
+                tc::wait_ld();
+                float o[16];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = 0u;
-                }
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * mul);
-                if (row_on && part) {
-                    float4 *o = reinterpret_cast<float4 *>(p.part_o + prow * Dh + 32 * c);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (32 * c + 4 * e < Dh)
-                            o[e] = make_float4(
-                                __uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
-                                __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
-                } else if (row_on) {
-                    uint4 *o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
-                                                         unit_prev * Dh + 32 * c);
-                    auto two = [&](int e) {
-                        return pack_bf16(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-                    };
+                for (int e = 0; e < 16; ++e)
+                    o[e] = sg.ntiles > 0 ? __uint_as_float(v[e]) * mul : 0.f;
+                const bool on = row_on && 16 * c < Dh;
+                if (on && part) {
+                    float4 *at = reinterpret_cast<float4 *>(p.part_o + prow * Dh + 16 * c);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (32 * c + 8 * e < Dh)
-                            o[e] = make_uint4(two(8 * e), two(8 * e + 2), two(8 * e + 4),
-                                              two(8 * e + 6));
+                        at[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                } else if (on) {
+                    uint4 *at = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
+                                                          unit_prev * Dh + 16 * c);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        at[e] = make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]),
+                                           pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                                           pack_bf16(o[8 * e + 4], o[8 * e + 5]),
+                                           pack_bf16(o[8 * e + 6], o[8 * e + 7]));
                 }
                 __syncwarp();
             }
@@ -935,10 +940,10 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     vexp = (float)((int)by[4 + (jn & 1)] - 127);
                     shift = vexp - kWeightExp;
                 }
-                // Chunk c (32 keys) of S as complete scores in log2 units: with bias,
+                // Chunk c (16 keys) of S as complete scores in log2 units: with bias,
                 // -inf for what the row does not see, NaN for a key whose V row is
-                // not finite.
-                auto complete = [&](int c, uint32_t (&v)[32]) {
+                // not finite.  Short, because it is mostly fetched for one tile.
+                auto complete = [&](int c, uint32_t (&v)[16]) {
                     const int i = sg.row0 + min(r, sg.nrows - 1), node = i / G;
                     const int ctx = sg.ctx, tok_lo = sg.tok_lo, tok_hi = sg.tok_hi;
                     auto depth_of = [&](int k) {  // a draft's depth
@@ -946,14 +951,14 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     };
                     const int depth = depth_of(node), qpos = ctx + depth;
                     const int wlo = p.window_left < 0 ? 0 : max(qpos - p.window_left, 0);
-                    const int kc = (sg.tile0 + j) * kTile + 32 * c;
+                    const int kc = (sg.tile0 + j) * kTile + 16 * c;
                     uint32_t vis = range_bits(max(wlo, tok_lo) - kc, min(ctx, tok_hi) - kc);
                     const int n0 = kc - ctx;  // draft node of the chunk's first key
-                    if (n0 > -32 && n0 < sg.q_len && row_on) {
+                    if (n0 > -16 && n0 < sg.q_len && row_on) {
                         uint32_t d =
                             mask_bits(p.mask + (int64_t)(sg.q_start + node) * p.mask_words,
                                       p.mask_words, n0);
-                        d &= range_bits(max(tok_lo, ctx) - kc, tok_hi - kc);
+                        d &= range_bits(max(tok_lo, ctx) - kc, tok_hi - kc) & 0xffffu;
                         if (p.window_left >= 0) {
                             for (uint32_t m = d; m; m &= m - 1) {
                                 const int e = __ffs(m) - 1;
@@ -962,15 +967,14 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                         }
                         vis |= d;
                     }
-                    for (int q = 0; q < 32 / BS; ++q)
-                        if ((badpg >> (c * 32 / BS + q)) & 1u)
-                            vis &= ~range_bits(q * BS, q * BS + BS);
+                    if ((badpg >> (c * 16 >> bs_shift)) & 1u) vis = 0u;
                     const uint32_t pois =
                         fix ? *reinterpret_cast<volatile uint32_t *>(
-                                  s_poison + ((nfix - 1) & 1) * 4 + c)
+                                  s_poison + ((nfix - 1) & 1) * 4 + (c >> 1)) >>
+                                  (c & 1) * 16
                             : 0u;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
+                    for (int e = 0; e < 16; ++e)
                         v[e] = __float_as_uint(__uint_as_float(v[e]) * rf);
                     if (p.alibi) {
                         // lane e holds the position of the chunk's key e
@@ -979,25 +983,24 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                         const int kpos =
                             k < ctx ? k : ctx + depth_of(min(k - ctx, sg.q_len - 1));
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
+                        for (int e = 0; e < 16; ++e)
                             v[e] = __float_as_uint(
                                 fmaf(slope, (float)(__shfl_sync(0xffffffffu, kpos, e) - qpos),
                                      __uint_as_float(v[e])));
                     }
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
+                    for (int e = 0; e < 16; ++e)
                         if (!((vis >> e) & 1u)) v[e] = __float_as_uint(kNegInf);
-                    }
-                    if (pois) {
+                    if (pois & vis & 0xffffu) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
+                        for (int e = 0; e < 16; ++e)
                             if ((pois & vis) >> e & 1u) v[e] = 0x7fffffffu;
                     }
                 };
-                auto maximum = [&](float m, const uint32_t (&v)[32]) {
+                auto maximum = [&](float m, const auto &v) {
                     float a0 = m, a1 = kNegInf;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
+                    for (int e = 0; e < (int)(sizeof v / 4); e += 4) {
                         a0 = fmax3(a0, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
                         a1 = fmax3(a1, __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
                     }
@@ -1065,14 +1068,14 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     }
                 } else {
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32];
-                        tc::ld_32x32b_x32(t_s + 32 * c, v);
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t v[16];
+                        tc::ld_32x32b_x16(t_s + 16 * c, v);
                         tc::wait_ld();
                         complete(c, v);
                         __syncwarp();
                         mt = maximum(mt, v);
-                        tc::st_32x32b_x32(t_s + 32 * c, v);
+                        tc::st_32x32b_x16(t_s + 16 * c, v);
                     }
                     tc::wait_st();
                     rf = 1.f;
@@ -1101,6 +1104,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         jt += ntiles;
         if (x >= nx)  // this row tile is empty: its repaired tiles count all the same
             nfix += ntiles - max(min(full_hi, ntiles) - max(full_lo, 0), 0);
+        sink = p.sink && row_on ? p.sink[g * G + (sg.row0 + r) % G] * kLog2e : kNegInf;
         // every product of the segment is done: O is at rest and Q's tile free
         if (alive)
             alive = wait_warp(bar(C::B_O), (uint32_t)ns & 1u, p.dev_error, s_abort);
