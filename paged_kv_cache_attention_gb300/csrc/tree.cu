@@ -132,6 +132,7 @@ struct Cfg {
     // tmem, abort, bad pages[kInfo] (8 bits each), poison[2][4], scale bytes: K[4], V[2]
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = 1024 + OFF_MISC + 80;
+    static_assert(!KV8 || (KB <= 2 && VB <= 2), "f16 tiles");
     static_assert(256 + X * T <= 512, "tensor memory");
     static_assert(SMEM <= 232448, "shared memory");
 };
@@ -752,7 +753,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             return (int64_t)(sg.q_start + tok) * p.num_qo_heads + g * G + (i - tok * G);
         };
         const bool positions = p.window_left >= 0 || p.alibi;
-        int un = 0, jt = 0, nfix = 0;        // units, key tiles and repaired tiles so far
+        uint32_t un = 0, jt = 0, nfix = 0;   // units, key tiles and repaired tiles so far
         bool alive = true;
         // Segment by segment: Q on its way, the rows of the segment before stored
         // meanwhile, Q's last touch, the key tiles.
@@ -799,15 +800,17 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             // ---- the rows' results
             const Seg &sg = *prev;
             tc::fence_after_sync();
-            // partials: [CTA group][its first or last row group][kv head][row]
+            // partials: [CTA group][its first or last row group][kv head], there lse
+            // [row] and O [D / 4][row][4], so that the rows' threads store whole lines
+            // (row by row, 3900 cycles of stores instead of 1000)
             const bool part = sg.cut() != 0, row_on = r < sg.nrows;
-            const int64_t prow =
-                ((int64_t)(2 * group + sg.cut() / 2) * Hkv + g) * (X * kTile) + r;
+            const int64_t pslot = (int64_t)(2 * group + sg.cut() / 2) * Hkv + g;
+            float4 *po = reinterpret_cast<float4 *>(p.part_o) + pslot * (Dh / 4) * (X * kTile) + r;
             float mul, lse;
             if (part) {
                 mul = l == 0.f ? 0.f : 1.f / l;
                 lse = l == 0.f ? kNegInf : m_ref + log2f(l);
-                if (row_on) p.part_lse[prow] = lse;
+                if (row_on) p.part_lse[pslot * (X * kTile) + r] = lse;
             } else {
                 const float M = fmaxf(m_ref, sink);
                 const float Ms = M == kNegInf ? 0.f : M;
@@ -832,10 +835,10 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     o[e] = sg.ntiles > 0 ? __uint_as_float(v[e]) * mul : 0.f;
                 const bool on = row_on && 16 * c < Dh;
                 if (on && part) {
-                    float4 *at = reinterpret_cast<float4 *>(p.part_o + prow * Dh + 16 * c);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        at[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        po[(4 * c + e) * (X * kTile)] =
+                            make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 } else if (on) {
                     uint4 *at = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
                                                           unit_prev * Dh + 16 * c);
@@ -904,7 +907,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         m_ref = kNegInf;
         l = 0.f;
         for (int j = 0; j < ntiles && x < nx; ++j) {
-            const int n = un + j * nx + x, jn = jt + j;
+            const uint32_t n = un + j * nx + x, jn = jt + j;
             const uint32_t t_s = tmem + (n & 1) * 128 + lane_base;
             const bool fix = j < full_lo || j >= full_hi;
             // All barriers are tried at once, and waited for in turn if one of them is
@@ -933,40 +936,45 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             if (!alive) break;
             if (warp_on) {
                 tc::fence_after_sync();
-                float rf = rowf, vexp = 0.f, shift = 0.f;
+                float rf = rowf, vexp = 0.f, vinv = 1.f, shift = 0.f;
                 if constexpr (KV8) {
                     const volatile uint32_t *by = s_byte;
                     rf *= scale_value(by[jn & 3]);
-                    vexp = (float)((int)by[4 + (jn & 1)] - 127);
+                    const uint32_t vb = by[4 + (jn & 1)];  // 2^-vexp, subnormal for 254
+                    vinv = __uint_as_float(vb == 254u ? 0x00400000u : (254u - vb) << 23);
+                    vexp = (float)((int)vb - 127);
                     shift = vexp - kWeightExp;
                 }
-                // Chunk c (16 keys) of S as complete scores in log2 units: with bias,
-                // -inf for what the row does not see, NaN for a key whose V row is
-                // not finite.  Short, because it is mostly fetched for one tile.
-                auto complete = [&](int c, uint32_t (&v)[16]) {
-                    const int i = sg.row0 + min(r, sg.nrows - 1), node = i / G;
+                // General tiles.  The keys among kc .. kc + 31 that draft `node` at position
+                // qpos sees.
+                auto depth_of = [&](int k) {  // a draft's depth
+                    return positions ? min(max(p.depth[sg.q_start + k], 0), 65535) : 0;
+                };
+                auto visible = [&](int kc, int node, int qpos) {
                     const int ctx = sg.ctx, tok_lo = sg.tok_lo, tok_hi = sg.tok_hi;
-                    auto depth_of = [&](int k) {  // a draft's depth
-                        return positions ? min(max(p.depth[sg.q_start + k], 0), 65535) : 0;
-                    };
-                    const int depth = depth_of(node), qpos = ctx + depth;
                     const int wlo = p.window_left < 0 ? 0 : max(qpos - p.window_left, 0);
-                    const int kc = (sg.tile0 + j) * kTile + 16 * c;
                     uint32_t vis = range_bits(max(wlo, tok_lo) - kc, min(ctx, tok_hi) - kc);
-                    const int n0 = kc - ctx;  // draft node of the chunk's first key
-                    if (n0 > -16 && n0 < sg.q_len && row_on) {
+                    const int n0 = kc - ctx;  // draft node of the first key
+                    if (n0 > -32 && n0 < sg.q_len && row_on) {
                         uint32_t d =
                             mask_bits(p.mask + (int64_t)(sg.q_start + node) * p.mask_words,
                                       p.mask_words, n0);
-                        d &= range_bits(max(tok_lo, ctx) - kc, tok_hi - kc) & 0xffffu;
+                        d &= range_bits(max(tok_lo, ctx) - kc, tok_hi - kc);
                         if (p.window_left >= 0) {
                             for (uint32_t m = d; m; m &= m - 1) {
                                 const int e = __ffs(m) - 1;
-                                if (depth_of(n0 + e) < depth - p.window_left) d &= ~(1u << e);
+                                if (ctx + depth_of(n0 + e) < qpos - p.window_left)
+                                    d &= ~(1u << e);
                             }
                         }
                         vis |= d;
                     }
+                    return vis;
+                };
+                // Chunk c (16 keys) of S as complete scores in log2 units: with bias,
+                // -inf for what the row does not see, NaN for a key whose V row is
+                // not finite.  Short, because it is mostly fetched for one tile.
+                auto complete = [&](int c, uint32_t vis, int head, int qpos, uint32_t (&v)[16]) {
                     if ((badpg >> (c * 16 >> bs_shift)) & 1u) vis = 0u;
                     const uint32_t pois =
                         fix ? *reinterpret_cast<volatile uint32_t *>(
@@ -978,8 +986,9 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                         v[e] = __float_as_uint(__uint_as_float(v[e]) * rf);
                     if (p.alibi) {
                         // lane e holds the position of the chunk's key e
-                        const float slope = p.alibi[g * G + i % G] * kLog2e;
-                        const int k = kc + lane;
+                        const float slope = p.alibi[g * G + head] * kLog2e;
+                        const int ctx = sg.ctx;
+                        const int k = (sg.tile0 + j) * kTile + 16 * c + lane;
                         const int kpos =
                             k < ctx ? k : ctx + depth_of(min(k - ctx, sg.q_len - 1));
 #pragma unroll
@@ -1067,12 +1076,18 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                         mt = maximum(maximum(mt, v[0]), v[1]);
                     }
                 } else {
+                    const int i = sg.row0 + min(r, sg.nrows - 1), node = i / G;
+                    const int qpos = sg.ctx + depth_of(node);
+                    uint32_t vis = 0u;
 #pragma unroll 1
                     for (int c = 0; c < 8; ++c) {
+                        vis = c & 1 ? vis >> 16
+                                    : visible((sg.tile0 + j) * kTile + 16 * c, node, qpos);
+                        __syncwarp();
                         uint32_t v[16];
                         tc::ld_32x32b_x16(t_s + 16 * c, v);
                         tc::wait_ld();
-                        complete(c, v);
+                        complete(c, vis, i - node * G, qpos, v);
                         __syncwarp();
                         mt = maximum(mt, v);
                         tc::st_32x32b_x16(t_s + 16 * c, v);
@@ -1093,7 +1108,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     sum += weights(2 * h, v[0], rf, m);
                     sum += weights(2 * h + 1, v[1], rf, m);
                 }
-                l += KV8 ? sum * exp2f(-vexp) : sum;
+                l += sum * vinv;
                 tc::wait_st();
                 tc::fence_before_sync();
             }
@@ -1118,7 +1133,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         constexpr int ROWS = kTile / C::FILL;
         const int w = (warp - C::W_CVT) % C::FILL, side = (warp - C::W_CVT) / C::FILL;
         bool alive = true;
-        int jt = 0, nfix = 0;                // key tiles and repaired tiles so far
+        uint32_t jt = 0, nfix = 0;           // key tiles and repaired tiles so far
         for (int ns = 0; alive; ++ns) {
         const Seg *sp = segment(ns);
         if (!sp) break;
@@ -1130,12 +1145,13 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             const bool fix = sg.partial(i);
 #pragma unroll 1
             for (int isv = side; isv < (C::SPLIT ? side + 1 : 2); ++isv) {
-                const int u = 2 * jt + isv, rs = u % C::RU;
-                const int nb = isv ? C::VB : C::KB, s = jt % nb;
+                const uint32_t u = 2 * jt + isv, rs = u % C::RU;
+                const uint32_t nb = isv ? C::VB : C::KB, s = nb == 1 ? 0u : jt % 2;
+                const uint32_t turn = nb == 1 ? jt : jt / 2;
                 alive = wait_warp(bar(C::B_RFULL + rs), (uint32_t)(u / C::RU) & 1u,
                                           p.dev_error, s_abort) &&
                         wait_warp(bar((isv ? C::B_VEMPTY : C::B_KEMPTY) + s),
-                                          ((uint32_t)(jt / nb) & 1u) ^ 1u, p.dev_error, s_abort);
+                                          (turn & 1u) ^ 1u, p.dev_error, s_abort);
                 if (!alive) break;
                 in4 = 0;
                 if (!((s_bad[jt % kInfo] >> (lane * 4 >> bs_shift)) & 1u))
@@ -1279,18 +1295,19 @@ tree_merge_kernel(const TreeParams p, int rows) {
     const int first = (int)(s / share), last = (int)((s + tiles - 1) / share);
     if (first == last) return;  // one CTA had all of it
     const int n = last - first + 1;
-    auto at = [&](int i) {
-        const int slot = i == 0 ? 2 * first + 1 : 2 * (first + i);
-        return ((int64_t)slot * p.num_kv_heads + g) * rows + (row - rg * rows);
+    const int r = row - rg * rows;
+    auto slot = [&](int i) {
+        return (int64_t)(i == 0 ? 2 * first + 1 : 2 * (first + i)) * p.num_kv_heads + g;
     };
+    auto lse_of = [&](int i) { return p.part_lse[slot(i) * rows + r]; };
     const float sink = p.sink ? p.sink[h] * kLog2e : kNegInf;
     float M = sink;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, p.part_lse[at(i)]);
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, lse_of(i));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     const float Ms = M == kNegInf ? 0.f : M;
     float sum = 0.f;
-    for (int i = lane; i < n; i += 32) sum += exp2f(p.part_lse[at(i)] - Ms);
+    for (int i = lane; i < n; i += 32) sum += exp2f(lse_of(i) - Ms);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     const float lam = sum + exp2f(sink - Ms);
@@ -1301,9 +1318,9 @@ tree_merge_kernel(const TreeParams p, int rows) {
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int i = 0; i < n; ++i) {
-            const int64_t k = at(i);
-            const float w = exp2f(p.part_lse[k] - Ms);
-            const float4 v = *reinterpret_cast<const float4 *>(p.part_o + k * D + c);
+            const float w = exp2f(lse_of(i) - Ms);
+            const float4 v = reinterpret_cast<const float4 *>(
+                p.part_o)[(slot(i) * (D / 4) + c / 4) * rows + r];
             acc.x = fmaf(w, v.x, acc.x);
             acc.y = fmaf(w, v.y, acc.y);
             acc.z = fmaf(w, v.z, acc.z);
