@@ -652,8 +652,11 @@ def _arg(name, t, dtype, ndim: int, dev: int):
 
 
 def _arg_shape(name, t, dtype, shape, dev: int):
+    """A contiguous tensor of that shape."""
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+        return
     _arg(name, t, dtype, len(shape), dev)
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
@@ -716,12 +719,19 @@ def _fp8_pools(k_cache, v_cache, k_scale, v_scale, layout: str, dev: int) -> Cac
 
 def _pools(k_cache, v_cache, k_scale, v_scale, dtype, layout: str, dev: int) -> CacheDesc:
     """Checks two pools: of ``dtype`` without scales, else of the 8-bit cache."""
-    torch = _torch()
     fp8 = k_scale is not None or v_scale is not None
+    shape = k_cache.shape
+    key = (shape, layout, dtype)
+    if (not fp8 and k_cache.dtype is dtype and v_cache.dtype is dtype and v_cache.shape == shape
+            and k_cache.get_device() == v_cache.get_device() == dev
+            and k_cache.is_contiguous() and v_cache.is_contiguous()):
+        d = _descs.get(key)
+        if d is not None:
+            return d
+    torch = _torch()
     dt = torch.float8_e4m3fn if fp8 else dtype
     _arg("k_cache", k_cache, dt, 4, dev)
     _arg("v_cache", v_cache, dt, 4, dev)
-    shape = k_cache.shape
     if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must have the same shape")
     if layout not in LAYOUTS:
@@ -730,7 +740,8 @@ def _pools(k_cache, v_cache, k_scale, v_scale, dtype, layout: str, dev: int) -> 
     if layout == "HND":
         bs, hkv = hkv, bs
     if not fp8:
-        return _desc(nb, bs, hkv, d, _dtype_code(dt), LAYOUTS[layout])
+        desc = _descs[key] = _desc(nb, bs, hkv, d, _dtype_code(dt), LAYOUTS[layout])
+        return desc
     want = (nb, hkv, bs)
     for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
         if s is None:
@@ -747,8 +758,9 @@ def _token_rows(name, t, dtype, tokens: int, heads: int, head_dim: int, dev: int
     if t.dtype is dtype and t.get_device() == dev and t.shape == (tokens, heads, head_dim):
         if t.is_contiguous():
             return heads * head_dim
-        if t.stride(2) == 1 and (heads == 1 or t.stride(1) == head_dim):
-            return t.stride(0) if tokens > 1 else heads * head_dim
+        token, head, one = t.stride()
+        if one == 1 and (heads == 1 or head == head_dim):
+            return token if tokens > 1 else heads * head_dim
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     _require(t.get_device() == dev, f"{name} must be on the same device as the other tensors")
     _require(t.dtype is dtype, f"{name} must be {dtype}, got {t.dtype}")
@@ -897,7 +909,7 @@ def _attention_extras(sink, alibi_slopes, out, lse, q, rows: int, Hq: int, dev: 
     if alibi_slopes is not None:
         _arg_vector("alibi_slopes", alibi_slopes, ty.f32, Hq, dev)
     if out is not None:
-        _arg_shape("out", out, ty.bf16, tuple(q.shape), dev)
+        _arg_shape("out", out, ty.bf16, q.shape, dev)
     if lse is not None:
         _arg_shape("lse", lse, ty.f32, (rows, Hq), dev)
 
