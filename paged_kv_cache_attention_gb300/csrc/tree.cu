@@ -51,21 +51,22 @@
 // and reaches, as NaN, only the rows that see it.
 //
 // Measured (GB300, 32/8 heads of 128): 8 x 64 drafts over 16K..32K tokens of bf16
-// 195 us, 63 % of a copy's rate; 16 x 24 over 0.5K..8K of the 8-bit cache 78 us,
-// 25 %; 4 x 8 over 60..900 of bf16 17 us, mostly the latency of two kernels.
+// 182 us, 68 % of a copy's rate; 16 x 24 over 0.5K..8K of the 8-bit cache 72 us,
+// 27 %; 4 x 8 over 60..900 of bf16 16 us, mostly the latency of two kernels.
 // With one row tile and 32-token pages, 8 x 32 over 24K takes 136 us, 87 %.
 //   Two row tiles per CTA (X = 2, heads up to 128) when a request may have more
-// than 128 rows: 8 x 64 drafts over 24K 183 us (8-bit: 241) against 260 (282) with
+// than 128 rows: 8 x 64 drafts over 24K 170 us (8-bit: 232) against 260 (273) with
 // one, which reads K and V twice; 8 x 40 drafts, whose second tile is a quarter
-// full, 164 (221) against 254 (276).
+// full, 163 (216) against 253 (267).
 //   Slower: K and V on their way to L2 two tiles before their loads (70 -> 77 us,
 // 8-bit), fewer converted and more raw tiles (173 -> 198 us), eight converting
 // warps (short cases 73 -> 76 us, long ones 153 -> 149).
-//   What bounds it: with two row tiles 4 x 527 cycles of tensor work in about 4200
+//   What bounds it: with two row tiles 4 x 527 cycles of tensor work in about 4000
 // per key tile, the rest handing S, P and O between the warps; over 8-bit pools
 // the same hand-overs, the conversion's among them, about 3300 cycles per key
-// tile; and some 7 us per row group that a CTA meets, for Q, the general tile and
-// code that is fetched for the first time.
+// tile (8 x 32 drafts over 24K: 147 us; 126 without the softmax's arithmetic, 124
+// without the conversion's, 102 without either); and some 5 us per row group that
+// a CTA meets, for Q, the general tile and code that is fetched for the first time.
 #include "pkv_fp8.cuh"
 #include "pkv_tcgen05.cuh"
 
