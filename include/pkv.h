@@ -497,7 +497,7 @@ PKV_API pkv_status pkv_gather_cache_fp8(void *key, void *value, const void *k_ca
  * for partition_size 0: the partition is chosen from the shapes (512 to 2048
  * tokens).  With max_seqlen within one partition the workspace may be NULL.
  * k_scale and v_scale are 16-byte aligned.  Head sizes 64/80/96/112/128/256, at
- * most 16 query heads per kv head.
+ * most 16 query heads per kv head, max_seqlen at most 2^30.
  */
 PKV_API pkv_status pkv_paged_decode_fp8(void *out, const void *q, const void *k_cache,
                                         const void *v_cache, const uint8_t *k_scale,

@@ -190,7 +190,8 @@ pkv_status pkv_paged_decode_fp8(void *out, const void *q, const void *k_cache,
         return PKV_ERR_INVALID_ARG;
     if (num_qo_heads % cache.num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
     const int G = num_qo_heads / cache.num_kv_heads;
-    if (G > 16) return PKV_ERR_UNSUPPORTED;
+    // (positions and partition bounds are 32-bit)
+    if (G > 16 || max_seqlen > (1 << 30)) return PKV_ERR_UNSUPPORTED;
     int P = partition_size;
     if (P == 0) {
         // twice the default while that leaves the SMs eight full rounds of CTAs

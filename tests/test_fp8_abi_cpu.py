@@ -123,6 +123,8 @@ def test_decode_pools(pool, expected):
     (dict(part=-16), INVALID), (dict(part=24), INVALID), (dict(part=1 << 15), INVALID),
     (dict(part=16, max_seqlen=1 << 21), UNSUPPORTED),          # partitions beyond the grid
     (dict(part=16, max_seqlen=1 << 21, window=100), LAUNCHED),  # a window leaves a few
+    (dict(max_seqlen=(1 << 30) + 1, window=100), UNSUPPORTED),  # 32-bit partition bounds
+    (dict(max_seqlen=1 << 30, window=100), LAUNCHED),
     (dict(ws=None), LAUNCHED),                                  # one partition needs none
     (dict(max_seqlen=4096, ws=None), WORKSPACE),
     (dict(max_seqlen=4096, ws=FAKE + 16), WORKSPACE),
