@@ -494,7 +494,7 @@ PKV_API pkv_status pkv_gather_cache_fp8(void *key, void *value, const void *k_ca
  * paged_decode_fp8: pkv_paged_decode over the 8-bit cache: q and out are bf16,
  * everything else (masks, sink, ALiBi, partitions, lse, workspace of
  * pkv_paged_decode_workspace_size bytes for the same arguments) as there, but
- * for partition_size 0: the partition is chosen from the shapes (512 to 2048
+ * for partition_size 0: the partition is chosen from the shapes (512 to 1536
  * tokens).  With max_seqlen within one partition the workspace may be NULL.
  * k_scale and v_scale are 16-byte aligned.  Head sizes 64/80/96/112/128/256, at
  * most 16 query heads per kv head, max_seqlen at most 2^30.

@@ -35,7 +35,7 @@
 //
 // Measured (GB300): 64 sequences of 512..4096 tokens, 32/8 heads of 128: 59 us,
 // 5.1 TB/s, 76 % of a copy's rate (the bf16 cache takes 108 us); 8 of
-// 32K..128K, 64/8 heads of 64: 117 us, 84 %.  Half as long stages (twice the
+// 32K..128K, 64/8 heads of 64: 119 us, 82 %.  Half as long stages (twice the
 // warps) take 69 and 138 us, three or four of them in the ring 71 and 143, twice
 // as long ones 72 and 152; partitions of 1024 tokens 65 and 120.  What is
 // left is latency between dependent instructions at 2.5 warps per scheduler
