@@ -72,7 +72,7 @@ struct TreeParams {
     long long *line;               // [B + 2] the requests' places on the line of work,
                                    // its length and a CTA group's share (tree.cu)
     float *part_lse;               // [2 * groups, Hkv, rows of a row group] (log2 units)
-    float *part_o;                 // the same with [D]
+    float *part_o;                 // the same with [D / 4, rows, 4]
     int32_t *dev_error;
     const uint8_t *k_scale, *v_scale;
     int64_t num_blocks;
