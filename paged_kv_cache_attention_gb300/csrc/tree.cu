@@ -77,6 +77,7 @@ namespace {
 constexpr int kTile = 128;      // rows and keys per tile
 constexpr int kRing = 4;        // segments handed over ahead
 constexpr int kInfo = 8;        // key tiles whose bad pages are: more than are ever under way
+constexpr int kPoison = 4;      // repaired tiles whose poison words are kept: as many as V tiles
 constexpr float kNegInf = -INFINITY;
 // A row's reference moves (and O is rescaled, which costs about a tile's time)
 // only when a score exceeds it by kLazy log2 units.  bf16 weights have fp32's
@@ -125,15 +126,17 @@ struct Cfg {
     static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + KB, B_VFULL = B_KEMPTY + KB,
                          B_VEMPTY = B_VFULL + VB, B_SFULL = B_VEMPTY + VB,
                          B_PFULL = B_SFULL + 2, B_O = B_PFULL + 2, B_LAND = B_O + 1,
-                         B_POISON = B_LAND + 1, B_KFACT = B_POISON + 2, B_VFACT = B_KFACT + 4,
+                         B_POISON = B_LAND + 1, B_KFACT = B_POISON + kPoison, B_VFACT = B_KFACT + 4,
                          B_RFULL = B_VFACT + 2,
                          B_REMPTY = B_RFULL + RU, B_Q = B_REMPTY + RU, B_IFULL = B_Q + 1,
                          B_IEMPTY = B_IFULL + kRing, B_INFO = B_IEMPTY + kRing,
                          NBAR = B_INFO + kInfo;
-    // tmem, abort, bad pages[kInfo] (8 bits each), poison[2][4], scale bytes: K[4], V[2]
+    // tmem, abort, bad pages[kInfo] (8 bits each), poison[kPoison][4], scale bytes: K[4],
+    // V[2]
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-    static constexpr int SMEM = 1024 + OFF_MISC + 80;
+    static constexpr int SMEM = 1024 + OFF_MISC + 112;
     static_assert(!KV8 || (KB <= 2 && VB <= 2), "f16 tiles");
+    static_assert(VB <= kPoison && (kPoison & (kPoison - 1)) == 0, "poison words");
     static_assert(256 + X * T <= 512, "tensor memory");
     static_assert(SMEM <= 232448, "shared memory");
 };
@@ -291,8 +294,8 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     int32_t *s_abort = reinterpret_cast<int32_t *>(misc + 1);
     volatile uint8_t *s_bad = reinterpret_cast<uint8_t *>(misc + 2);  // [kInfo]
-    uint32_t *s_poison = misc + 4;   // [2][4]
-    uint32_t *s_byte = misc + 12;    // K[4], V[2]: a tile's largest scale bytes
+    uint32_t *s_poison = misc + 4;   // [kPoison][4]
+    uint32_t *s_byte = misc + 4 + 4 * kPoison;  // K[4], V[2]: a tile's largest scale bytes
     Seg *ring = reinterpret_cast<Seg *>(smem + C::OFF_RING);
     auto bar = [&](int i) { return base + C::OFF_BAR + 8 * i; };
 
@@ -315,10 +318,10 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(C::B_SFULL + i), 1);
             mbar_init(bar(C::B_PFULL + i), 4);
-            mbar_init(bar(C::B_POISON + i), C::FILL);
             mbar_init(bar(C::B_VFACT + i), 1);
         }
         for (int i = 0; i < 4; ++i) mbar_init(bar(C::B_KFACT + i), 1);
+        for (int i = 0; i < kPoison; ++i) mbar_init(bar(C::B_POISON + i), C::FILL);
         mbar_init(bar(C::B_O), 1);
         mbar_init(bar(C::B_LAND), 1);
         mbar_init(bar(C::B_Q), 4 * X);
@@ -488,7 +491,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                         if (!alive) break;
                         // lane owns rows lane, lane + 32, ..: rows outside the range
                         // are zeroed, and rows with an infinity or a NaN, noted
-                        uint32_t *pois = s_poison + ((nfix - 1) & 1) * 4;
+                        uint32_t *pois = s_poison + ((nfix - 1) % kPoison) * 4;
                         const int k0 = (sg.tile0 + iv) * kTile;
 #pragma unroll 1
                         for (int w = 0; w < 4; ++w) {
@@ -516,7 +519,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            mbar_arrive(bar(C::B_POISON + ((nfix - 1) & 1)));
+                            mbar_arrive(bar(C::B_POISON + (nfix - 1) % kPoison));
                             mbar_arrive(bar(C::B_VFULL + vs));
                         }
                     }
@@ -921,7 +924,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                         wait_warp(bar(C::B_VFACT + (jn & 1)), (jn >> 1) & 1u, p.dev_error,
                                   s_abort);
             if (fix && alive) {
-                alive = wait_warp(bar(C::B_POISON + (nfix & 1)), (uint32_t)(nfix >> 1) & 1u,
+                alive = wait_warp(bar(C::B_POISON + nfix % kPoison), (nfix / kPoison) & 1u,
                                   p.dev_error, s_abort);
                 ++nfix;
             }
@@ -972,7 +975,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     if ((badpg >> (c * 16 >> bs_shift)) & 1u) vis = 0u;
                     const uint32_t pois =
                         fix ? *reinterpret_cast<volatile uint32_t *>(
-                                  s_poison + ((nfix - 1) & 1) * 4 + (c >> 1)) >>
+                                  s_poison + ((nfix - 1) % kPoison) * 4 + (c >> 1)) >>
                                   (c & 1) * 16
                             : 0u;
 #pragma unroll
@@ -1180,7 +1183,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     word |= __shfl_xor_sync(0xffffffffu, word, 1);
                     word |= __shfl_xor_sync(0xffffffffu, word, 2);
                     word |= __shfl_xor_sync(0xffffffffu, word, 4);
-                    if (w == 0 && (lane & 7) == 0) s_poison[(nfix & 1) * 4 + (lane >> 3)] = word;
+                    if (w == 0 && (lane & 7) == 0) s_poison[(nfix % kPoison) * 4 + (lane >> 3)] = word;
                 }
                 const uint32_t zero4 = isv ? (~in4 & 15u) | (fix ? bad4 : 0u) : 0u;
                 const bool zeros = __any_sync(0xffffffffu, zero4 != 0u);
@@ -1248,7 +1251,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    if (isv && fix) mbar_arrive(bar(C::B_POISON + (nfix & 1)));
+                    if (isv && fix) mbar_arrive(bar(C::B_POISON + nfix % kPoison));
                     mbar_arrive(bar((isv ? C::B_VFULL : C::B_KFULL) + s));
                     mbar_arrive(bar(C::B_REMPTY + rs));
                 }

@@ -141,6 +141,18 @@ def test_many_requests(fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("kw", [dict(alibi=True, sink=True), dict(window=3, nan_draft=True),
+                                dict(kind="random")], ids=["alibi", "window", "random"])
+def test_many_short_requests_per_cta(d, kw, fp8):
+    """A CTA that takes request after request, every key tile of them a general
+    one, its V rows repaired ahead of the softmax."""
+    rng = random.Random(10)
+    lens = [rng.randint(1, 140) for _ in range(60)]
+    run(lens, [min(n, rng.randint(1, 6)) for n in lens], 6, 2, d, fp8=fp8, partition=2048, **kw)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_more_kv_heads_than_sms(fp8):
     run([40, 300], [3, 5], 160, 160, 64, fp8=fp8)
 
