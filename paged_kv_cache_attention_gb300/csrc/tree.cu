@@ -51,7 +51,7 @@
 // and reaches, as NaN, only the rows that see it.
 //
 // Measured (GB300, 32/8 heads of 128): 8 x 64 drafts over 16K..32K tokens of bf16
-// 182 us, 68 % of a copy's rate; 16 x 24 over 0.5K..8K of the 8-bit cache 72 us,
+// 184 us, 67 % of a copy's rate; 16 x 24 over 0.5K..8K of the 8-bit cache 72 us,
 // 27 %; 4 x 8 over 60..900 of bf16 16 us, mostly the latency of two kernels.
 // With one row tile and 32-token pages, 8 x 32 over 24K takes 136 us, 87 %.
 //   Two row tiles per CTA (X = 2, heads up to 128) when a request may have more
