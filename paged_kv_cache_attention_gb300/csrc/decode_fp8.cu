@@ -11,13 +11,15 @@
 // stay out of the codes, and the softmax's bookkeeping is skipped while no
 // row's maximum grows:
 //   * K: the byte, as 2^ek, multiplies the fp32 score of its key;
-//   * V: the byte multiplies p_j before p rounds to f16.  Weights are kept
-//     relative to the largest byte E seen so far by the warp, p_j *
-//     2^(ev_j - E + 6); with p <= 2^9 (below) that is at most 2^15, and f16
-//     keeps 11 bits of every weight down to 2^-20 of the reference's (an error
-//     of 2^-31 of it below that).  The accumulators move by 2^(E_old - E_new)
-//     with the softmax's own rescale;
-//   * a row's reference moves only when a score exceeds it by 9 log2 units.
+//   * V: the weight that rounds to f16 is p_j 2^ev_j, as 2^(s_j + ev_j - r) with a
+//     reference r of the row's own: the largest s_j + ev_j, less 6.  What a key
+//     adds counts, not its scale: a huge V row of hardly any weight costs the others
+//     nothing.  f16 keeps 11 bits of every weighted scale down to 2^-20 of the
+//     row's largest (an error of 2^-31 of that one below it).  The sum of the p_j
+//     alone has the row's largest score as its reference, so each score takes two
+//     exponentials;
+//   * both references move only when they are exceeded by 9 log2 units (weights
+//     stay below 2^15).
 // q is scaled per head by a power of two to at most 2^15 and held in f16,
 // which is exact for every bf16 value within 2^-28 of the row's largest (and
 // off by less than 2^-39 of the largest below that).
@@ -33,9 +35,9 @@
 // TMA (one box per page and 128 dims), the scale bytes by 16-byte cp.async on
 // the same barrier.
 //
-// Measured (GB300): 64 sequences of 512..4096 tokens, 32/8 heads of 128: 59 us,
+// Measured (GB300): 64 sequences of 512..4096 tokens (uniform), 32/8 heads of 128: 59 us,
 // 5.1 TB/s, 76 % of a copy's rate (the bf16 cache takes 108 us); 8 of
-// 32K..128K, 64/8 heads of 64: 119 us, 82 %.  Half as long stages (twice the
+// 32K..128K, 64/8 heads of 64: 120 us, 82 %.  Half as long stages (twice the
 // warps) take 69 and 138 us, three or four of them in the ring 71 and 143, twice
 // as long ones 72 and 152; partitions of 1024 tokens 65 and 120.  What is
 // left is latency between dependent instructions at 2.5 warps per scheduler
@@ -49,7 +51,7 @@ namespace {
 constexpr int kWarps = 2;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxGroup = 16;
-constexpr int kWeightExp = 6;    // weights are at most 2^kWeightExp * 2^kLazy
+constexpr float kWeightExp = 6.f;  // weights are at most 2^kWeightExp * 2^kLazy
 constexpr float kLazy = 9.f;     // log2 units a score may exceed its row's reference
 constexpr float kNegInf = -INFINITY;
 
@@ -73,27 +75,33 @@ __device__ __forceinline__ uint32_t swz(uint32_t r, uint32_t c) {
     return W == 128 ? sw128(r, c) : r * 64u + ((c ^ ((r >> 1) & 3u)) << 4);
 }
 
-// Normalise and store one row slice: the output itself when there is one
-// partition, else the partition's partial.
-__device__ __forceinline__ void store_row4(const DecodeParams &p, int64_t unit, int hq, int d,
-                                           float4 o, float M, float l, bool first) {
+// What a row's slices are multiplied by, for the sum l of its weights relative to
+// 2^M; with it the row's lse is stored.  One partition: the output's factor, with
+// the sink; else the partial's.
+__device__ __forceinline__ float finish_row(const DecodeParams &p, int64_t unit, int hq, float M,
+                                            float l, bool first) {
     if (p.num_parts > 1) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays
-        const int64_t idx = unit * p.num_parts + blockIdx.y;
-        *reinterpret_cast<float4 *>(p.part_o + idx * p.head_dim + d) =
-            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-        if (first) p.part_lse[idx] = l == 0.f ? kNegInf : M + log2f(l);
-        return;
+        if (first)
+            p.part_lse[unit * p.num_parts + blockIdx.y] = l == 0.f ? kNegInf : M + log2f(l);
+        return l == 0.f ? 0.f : 1.f / l;  // NaN stays
     }
     const float sink = p.sink ? p.sink[hq] * kLog2e : kNegInf;
     const float T = fmaxf(M, sink), Ts = T == kNegInf ? 0.f : T;
     const float f = exp2f(M - Ts);
     const float lam = (l != l ? l : l * f) + exp2f(sink - Ts);
-    const float inv = lam == 0.f ? 0.f : f / lam;
-    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + unit * p.head_dim + d) =
-        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-    if (first && p.lse_out)
-        p.lse_out[unit] = lam == 0.f ? kNegInf : (Ts + log2f(lam)) * kLn2;
+    if (first && p.lse_out) p.lse_out[unit] = lam == 0.f ? kNegInf : (Ts + log2f(lam)) * kLn2;
+    return lam == 0.f ? 0.f : f / lam;
+}
+
+// Store four finished columns: of the output itself when there is one partition,
+// else of the partition's partial.
+__device__ __forceinline__ void store_row4(const DecodeParams &p, int64_t unit, int d, float4 o) {
+    if (p.num_parts > 1)
+        *reinterpret_cast<float4 *>(p.part_o + (unit * p.num_parts + blockIdx.y) * p.head_dim +
+                                    d) = o;
+    else
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + unit * p.head_dim + d) =
+            make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
 }
 
 template <int D>
@@ -110,7 +118,8 @@ struct Shape {
     static constexpr int BAR_OFF = FACT_OFF + kWarps * 2 * TOK * 4;
     static constexpr int M_OFF = BAR_OFF + kWarps * NST * 8;
     static constexpr int L_OFF = M_OFF + kWarps * kMaxGroup * 4;
-    static constexpr int BLK_OFF = L_OFF + kWarps * kMaxGroup * 4;
+    static constexpr int R_OFF = L_OFF + kWarps * kMaxGroup * 4;
+    static constexpr int BLK_OFF = R_OFF + kWarps * kMaxGroup * 4;
     static constexpr int SMEM_FIXED = 1024 + BLK_OFF;        // + the partition's block ids
     static_assert(kWarps * 8 * D * 4 <= RING, "merge scratch must fit in the ring");
 };
@@ -132,6 +141,7 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
     int *s_blk = reinterpret_cast<int *>(smem + C::BLK_OFF);
     float *s_m = reinterpret_cast<float *>(smem + C::M_OFF);
     float *s_l = reinterpret_cast<float *>(smem + C::L_OFF);
+    float *s_r = reinterpret_cast<float *>(smem + C::R_OFF);
 
     // no early trigger: merge CTAs that wait on the SMs cost more (2 %) than
     // their launch latency
@@ -149,8 +159,8 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
         if (p.num_parts == 1)
             for (int i = threadIdx.x; i < G * (Dh / 4); i += kThreads) {
                 const int h = i / (Dh / 4), d = (i - h * (Dh / 4)) * 4;
-                store_row4(p, unit0 + h, g * G + h, d, make_float4(0.f, 0.f, 0.f, 0.f), kNegInf,
-                           0.f, d == 0);
+                finish_row(p, unit0 + h, g * G + h, kNegInf, 0.f, d == 0);
+                store_row4(p, unit0 + h, d, make_float4(0.f, 0.f, 0.f, 0.f));
             }
         return;
     }
@@ -269,11 +279,11 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
     }
 
     float oacc[NHT][NC][4];
-    float m_ref[NHT], l_run[NHT], al2[NHT];
+    float m_ref[NHT], r_ref[NHT], l_run[NHT], al2[NHT];
     bool head_ok[NHT];
 #pragma unroll
     for (int ht = 0; ht < NHT; ++ht) {
-        m_ref[ht] = kNegInf;
+        m_ref[ht] = r_ref[ht] = kNegInf;
         l_run[ht] = 0.f;
         head_ok[ht] = ht * 8 + gq < G;
         al2[ht] = (p.alibi && head_ok[ht]) ? p.alibi[g * G + ht * 8 + gq] * kLog2e : 0.f;
@@ -282,7 +292,6 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
 #pragma unroll
             for (int e = 0; e < 4; ++e) oacc[ht][mt][e] = 0.f;
     }
-    int gauge = 0;  // the largest V scale byte so far
     const int qpos = L - 1;
 
     int consumed = 0;
@@ -298,7 +307,6 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
         constexpr int NW = (TOK + 31) / 32;
         uint32_t okm[NW];
         bool full = true;
-        int vmax = 0;
 #pragma unroll
         for (int h = 0; h < NW; ++h) {
             const int t = tok0 + h * 32 + lane;
@@ -306,28 +314,18 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
                             s_blk[t / BS - pg_lo] >= 0;
             okm[h] = __ballot_sync(0xffffffffu, ok);
             full = full && okm[h] == (TOK < 32 ? (1u << (TOK % 32)) - 1u : 0xffffffffu);
-            if (ok) vmax = max(vmax, (int)sc[TOK + h * 32 + lane]);
-        }
-        vmax = __reduce_max_sync(0xffffffffu, vmax);
-        const bool regauge = vmax > gauge;
-        float gcorr = 1.f;
-        if (regauge) {
-            gcorr = gauge - vmax < -126 ? 0.f
-                                        : __uint_as_float((uint32_t)(127 + gauge - vmax) << 23);
-            gauge = vmax;
         }
 #pragma unroll
         for (int h = 0; h < NW; ++h) {
             const int t = h * 32 + lane;
             if (TOK < 32 && t >= TOK) break;
-            const uint32_t kbyte = sc[t], vbyte = sc[TOK + t];
-            const int x = (int)vbyte - gauge + kWeightExp + 127;
-            wfact[t] = scale_value(kbyte);
-            // an unattended row's byte may be anything: its factor is 0
-            wfact[TOK + t] = !((okm[h] >> lane) & 1u) ? 0.f
-                             : vbyte == kScaleNaN     ? __uint_as_float(0x7fffffffu)
-                             : x > 0                  ? __uint_as_float((uint32_t)x << 23)
-                                                      : 0.f;
+            const uint32_t vbyte = sc[TOK + t];
+            wfact[t] = scale_value(sc[t]);
+            // an unattended row's byte may be anything, but finite here: it meets a
+            // score of -inf
+            wfact[TOK + t] = vbyte == kScaleNaN && ((okm[h] >> lane) & 1u)
+                                 ? __uint_as_float(0x7fffffffu)
+                                 : (float)((int)vbyte - 127);
         }
         if (!full) {
             // unattended V rows may hold any bits: zero them, so that a zero
@@ -366,10 +364,10 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
         }
         // online softmax (log2 units), one head row per lane quad
         float ao[NHT];
-        bool moved = regauge;
+        bool moved = false;
 #pragma unroll
         for (int ht = 0; ht < NHT; ++ht) {
-            float mx = kNegInf, rf = rowf[ht];
+            float rf = rowf[ht];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const float2 kf = *reinterpret_cast<const float2 *>(wfact + nt * 8 + 2 * tq);
@@ -390,40 +388,50 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
                     }
                 rf = 1.f;  // the scores are complete
             }
+            float mx = kNegInf, rx = kNegInf;  // the largest score, and score + V exponent
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+                const float2 ev = *reinterpret_cast<const float2 *>(wfact + TOK + nt * 8 + 2 * tq);
                 mx = fmax3(mx, sacc[nt][2 * ht], sacc[nt][2 * ht + 1]);
+                rx = fmax3(rx, fmaf(sacc[nt][2 * ht], rf, ev.x),
+                           fmaf(sacc[nt][2 * ht + 1], rf, ev.y));
+            }
             mx *= rf;
-            if (!head_ok[ht]) mx = kNegInf;
+            rx -= kWeightExp;
+            if (!head_ok[ht]) mx = rx = kNegInf;
             ao[ht] = 1.f;
-            if (__any_sync(0xffffffffu, mx > m_ref[ht] + kLazy)) {
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float m_new = fmaxf(m_ref[ht], mx);
-                ao[ht] = m_new == kNegInf ? 1.f : fast_exp2(m_ref[ht] - m_new);
-                l_run[ht] *= ao[ht];
+            if (__any_sync(0xffffffffu, mx > m_ref[ht] + kLazy || rx > r_ref[ht] + kLazy)) {
+#pragma unroll
+                for (int off = 1; off < 4; off <<= 1) {
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                    rx = fmaxf(rx, __shfl_xor_sync(0xffffffffu, rx, off));
+                }
+                const float m_new = fmaxf(m_ref[ht], mx), r_new = fmaxf(r_ref[ht], rx);
+                ao[ht] = r_new == kNegInf ? 1.f : fast_exp2(r_ref[ht] - r_new);
+                l_run[ht] *= m_new == kNegInf ? 1.f : fast_exp2(m_ref[ht] - m_new);
                 m_ref[ht] = m_new;
+                r_ref[ht] = r_new;
                 moved = true;
             }
             const float msub = m_ref[ht] == kNegInf ? 0.f : m_ref[ht];
+            const float rsub = r_ref[ht] == kNegInf ? 0.f : r_ref[ht];
             float p0 = 0.f, p1 = 0.f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float2 vf = *reinterpret_cast<const float2 *>(wfact + TOK + nt * 8 + 2 * tq);
-                const float x = fast_exp2(fmaf(sacc[nt][2 * ht], rf, -msub));
-                const float y = fast_exp2(fmaf(sacc[nt][2 * ht + 1], rf, -msub));
-                p0 += x;
-                p1 += y;
-                sacc[nt][2 * ht] = x * vf.x;
-                sacc[nt][2 * ht + 1] = y * vf.y;
+                const float2 ev = *reinterpret_cast<const float2 *>(wfact + TOK + nt * 8 + 2 * tq);
+                const float x = sacc[nt][2 * ht], y = sacc[nt][2 * ht + 1];
+                p0 += fast_exp2(fmaf(x, rf, -msub));
+                p1 += fast_exp2(fmaf(y, rf, -msub));
+                sacc[nt][2 * ht] = fast_exp2(fmaf(x, rf, ev.x) - rsub);
+                sacc[nt][2 * ht + 1] = fast_exp2(fmaf(y, rf, ev.y) - rsub);
             }
             l_run[ht] += p0 + p1;
         }
         if (moved) {  // O^T columns of this lane are heads ht*8 + 2tq and +1
 #pragma unroll
             for (int ht = 0; ht < NHT; ++ht) {
-                const float a0 = __shfl_sync(0xffffffffu, ao[ht], 8 * tq) * gcorr;
-                const float a1 = __shfl_sync(0xffffffffu, ao[ht], 8 * tq + 4) * gcorr;
+                const float a0 = __shfl_sync(0xffffffffu, ao[ht], 8 * tq);
+                const float a1 = __shfl_sync(0xffffffffu, ao[ht], 8 * tq + 4);
 #pragma unroll
                 for (int mt = 0; mt < NC; ++mt) {
                     oacc[ht][mt][0] *= a0;
@@ -480,11 +488,9 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
         if (tq == 0) {
             s_m[warp * kMaxGroup + ht * 8 + gq] = m_ref[ht];
             s_l[warp * kMaxGroup + ht * 8 + gq] = l_run[ht];
+            s_r[warp * kMaxGroup + ht * 8 + gq] = r_ref[ht];
         }
     }
-    // O in its own units: the weights carry 2^(kWeightExp - gauge)
-    const float unit =
-        gauge > 0 ? __uint_as_float((uint32_t)gauge << 23) * (1.f / (1 << kWeightExp)) : 0.f;
     float *s_o = reinterpret_cast<float *>(smem);  // [warp][8 heads][D]
 #pragma unroll
     for (int ht = 0; ht < NHT; ++ht) {
@@ -495,23 +501,30 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
             for (int c = 0; c < 2; ++c)
                 *reinterpret_cast<float2 *>(s_o + (warp * 8 + 2 * tq + c) * D + mt * 16 +
                                             2 * gq) =
-                    make_float2(oacc[ht][mt][c] * unit, oacc[ht][mt][2 + c] * unit);
+                    make_float2(oacc[ht][mt][c], oacc[ht][mt][2 + c]);
         __syncthreads();
         const int heads = min(8, G - ht * 8);
         for (int i = threadIdx.x; i < heads * (Dh / 4); i += kThreads) {
             const int h = i / (Dh / 4), d = (i - h * (Dh / 4)) * 4, hh = ht * 8 + h;
             const float m0 = s_m[hh], m1 = s_m[kMaxGroup + hh];
             const float M = fmaxf(m0, m1), Ms = M == kNegInf ? 0.f : M;
-            const float f0 = exp2f(m0 - Ms), f1 = exp2f(m1 - Ms);
             const float l0 = s_l[hh], l1 = s_l[kMaxGroup + hh];
-            // a NaN sum keeps its reference at -inf: do not lose it to f = 0
-            const float l = (l0 != l0 ? l0 : f0 * l0) + (l1 != l1 ? l1 : f1 * l1);
+            // a NaN sum keeps its reference at -inf: do not lose it to a factor 0
+            const float l = (l0 != l0 ? l0 : exp2f(m0 - Ms) * l0) +
+                            (l1 != l1 ? l1 : exp2f(m1 - Ms) * l1);
+            const float mul = finish_row(p, unit0 + hh, g * G + hh, M, l, d == 0);
+            // O is relative to 2^r: 2^(r - M) in two halves, because r holds V's
+            // exponent and the whole may leave fp32's range where the result does not
+            const float h0 = exp2f(0.5f * (s_r[hh] - Ms));
+            const float h1 = exp2f(0.5f * (s_r[kMaxGroup + hh] - Ms));
             const float4 a = *reinterpret_cast<const float4 *>(s_o + h * D + d);
             const float4 c = *reinterpret_cast<const float4 *>(s_o + (8 + h) * D + d);
-            store_row4(p, unit0 + hh, g * G + hh, d,
-                       make_float4(a.x * f0 + c.x * f1, a.y * f0 + c.y * f1, a.z * f0 + c.z * f1,
-                                   a.w * f0 + c.w * f1),
-                       M, l, d == 0);
+            auto join = [&](float x, float y) {
+                return x * mul * h0 * h0 + y * mul * h1 * h1;
+            };
+            store_row4(p, unit0 + hh, d,
+                       make_float4(join(a.x, c.x), join(a.y, c.y), join(a.z, c.z),
+                                   join(a.w, c.w)));
         }
     }
 }
@@ -552,13 +565,14 @@ merge_fp8_kernel(const DecodeParams p, int D, int block_size) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     const float lam = sum + exp2f(sink - Ms);
+    const float inv = lam > 0.f ? 1.f / lam : (lam == 0.f ? 0.f : lam);
     // lane l sums columns 4l .. 4l+3 (and 128 + 4l .. for D = 256)
     float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
     const int c0 = 4 * lane;
     const float *po = p.part_o + base * D;
 #pragma unroll 4
     for (int i = warp % SPLIT; i < n; i += SPLIT) {
-        const float w = exp2f(lp[i] - Ms);
+        const float w = exp2f(lp[i] - Ms) * inv;
         const float *row = po + (int64_t)i * D;
         if (c0 < D) {
             const float4 v = *reinterpret_cast<const float4 *>(row + c0);
@@ -592,14 +606,12 @@ merge_fp8_kernel(const DecodeParams p, int D, int block_size) {
                 acc[k].w += v.w;
             }
     }
-    const float inv = lam > 0.f ? 1.f / lam : (lam == 0.f ? 0.f : lam);
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + unit * D;
 #pragma unroll
     for (int k = 0; k < 2; ++k)
         if (c0 + k * 128 < D)
             *reinterpret_cast<uint2 *>(out + k * 128 + c0) =
-                make_uint2(pack_bf16(acc[k].x * inv, acc[k].y * inv),
-                           pack_bf16(acc[k].z * inv, acc[k].w * inv));
+                make_uint2(pack_bf16(acc[k].x, acc[k].y), pack_bf16(acc[k].z, acc[k].w));
     if (p.lse_out && lane == 0)
         p.lse_out[unit] = lam == 0.f ? kNegInf : (Ms + log2f(lam)) * kLn2;
 }
