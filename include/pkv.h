@@ -580,8 +580,8 @@ PKV_API size_t pkv_paged_tree_attention_workspace_size(int batch, int num_qo_hea
  *   workspace      device scratch of pkv_paged_tree_attention_workspace_size
  *                  bytes, 256-byte aligned; needs no initialisation
  * A NaN or an infinity in a V row reaches only drafts that keep that key (where
- * some drafts do not, the whole output row of one that does is NaN).  Requests
- * whose drafts do not fit their length (q_len > cache_seqlens[r]) attend
+ * some drafts do not, the whole output row of one that does is NaN), and no lse.
+ * Requests whose drafts do not fit their length (q_len > cache_seqlens[r]) attend
  * nothing and set PKV_DEVERR_SEQLEN, as do lengths beyond their maximum and
  * offsets outside the rows of q (clipped).
  * Supported: head sizes 64/80/96/112/128/256, block_size 16 or 32, at most 16

@@ -764,6 +764,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         // meanwhile, Q's last touch, the key tiles.
         const Seg *prev = nullptr;
         float m_ref = kNegInf, l = 0.f, sink = kNegInf;
+        bool poisoned = false;               // the row keeps a key whose V is not finite
         int64_t unit = 0;
 #pragma unroll 1
         for (int ns = 0;; ++ns) {
@@ -827,6 +828,8 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                 if (l != l) mul = lse = l;
                 if (row_on && p.lse_out) p.lse_out[unit_prev] = lse;
             }
+            // (its V row was zeroed; the lse is of the scores alone)
+            if (poisoned) mul = __uint_as_float(0x7fffffffu);
             // Each thread stores its row, 16 columns at a time: whole sectors, without
             // a turn through shared memory, where the next segment's Q is landing.
 #pragma unroll 1
@@ -911,6 +914,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         // over 2^10, so that f16 holds the product); O and l share it.
         m_ref = kNegInf;
         l = 0.f;
+        poisoned = false;
         for (int j = 0; j < ntiles && x < nx; ++j) {
             const uint32_t n = un + j * nx + x, jn = jt + j;
             const uint32_t t_s = tmem + (n & 1) * 128 + lane_base;
@@ -969,8 +973,9 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     return vis;
                 };
                 // Chunk c (16 keys) of S as complete scores in log2 units: with bias,
-                // -inf for what the row does not see, NaN for a key whose V row is
-                // not finite.  Short, because it is mostly fetched for one tile.
+                // -inf for what the row does not see.  A key that it sees and whose V row
+                // is not finite poisons the row.  Short, because it is mostly fetched for
+                // one tile.
                 auto complete = [&](int c, uint32_t vis, int head, int qpos, uint32_t (&v)[16]) {
                     if ((badpg >> (c * 16 >> bs_shift)) & 1u) vis = 0u;
                     const uint32_t pois =
@@ -997,11 +1002,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
                         if (!((vis >> e) & 1u)) v[e] = __float_as_uint(kNegInf);
-                    if (pois & vis & 0xffffu) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if ((pois & vis) >> e & 1u) v[e] = 0x7fffffffu;
-                    }
+                    poisoned |= (pois & vis & 0xffffu) != 0u;
                 };
                 auto maximum = [&](float m, const auto &v) {
                     float a0 = m, a1 = kNegInf;
