@@ -498,6 +498,9 @@ PKV_API pkv_status pkv_gather_cache_fp8(void *key, void *value, const void *k_ca
  * tokens).  With max_seqlen within one partition the workspace may be NULL.
  * k_scale and v_scale are 16-byte aligned.  Head sizes 64/80/96/112/128/256, at
  * most 16 query heads per kv head, max_seqlen at most 2^30.
+ * Precision: scores, maxima, sums and outputs are fp32; q is held to 2^-39 of its
+ * row's largest element; a key's weight rounds to 11 bits, and what the key adds is
+ * off by no more than 2^-30 of the row's largest p_j |v_j| besides.
  */
 PKV_API pkv_status pkv_paged_decode_fp8(void *out, const void *q, const void *k_cache,
                                         const void *v_cache, const uint8_t *k_scale,
@@ -581,6 +584,9 @@ PKV_API size_t pkv_paged_tree_attention_workspace_size(int batch, int num_qo_hea
  *                  bytes, 256-byte aligned; needs no initialisation
  * A NaN or an infinity in a V row reaches only drafts that keep that key (where
  * some drafts do not, the whole output row of one that does is NaN), and no lse.
+ * Precision: as pkv_paged_decode_fp8 over 8-bit pools, but 2^-22 of the row's
+ * largest p_j |v_j|; over bf16 pools a key's weight rounds to bf16 (8 bits) and is
+ * summed unrounded.  Keys that a draft does not see cost it nothing.
  * Requests whose drafts do not fit their length (q_len > cache_seqlens[r]) attend
  * nothing and set PKV_DEVERR_SEQLEN, as do lengths beyond their maximum and
  * offsets outside the rows of q (clipped).

@@ -17,11 +17,14 @@
 // the padding of small trees is free.
 //
 // Over 8-bit pools the codes become f16 tiles, each row times 2^(its scale's
-// exponent - the tile's largest), exact unless a row is more than 2^15 smaller
-// than another of its tile (then off by 2^-25 of the largest scale).  The
-// tile's two largest scales are scalars of the softmax: K's multiplies the
-// scores, V's moves the exponent of the weights.  q is scaled per row by a power
-// of two into f16 (decode_fp8.cu gives the error bound).
+// exponent - the tile's largest), which is exact while the tile's scales lie within
+// 2^15 of one another.  The tile's two largest scales are scalars of the softmax:
+// K's multiplies the scores, V's moves the exponent of the weights.  Where a tile's
+// scales are wider apart than kSpreadK or kSpreadV (a hidden draft may hold
+// anything), its rows stay as the codes are, and the softmax takes the scale
+// bytes key by key: exact too, and slower.  So a key that a draft does not see
+// never costs it bits, and one that it hardly weighs next to none (kSpreadV).  q is scaled per row by a power of two into f16 (decode_fp8.cu gives
+// the error bound).
 //
 // Persistent CTAs, one per SM, in groups of one CTA per kv head.  The work of a kv
 // head is one line of key tiles: request after request, and in a request row
@@ -88,6 +91,17 @@ constexpr float kNegInf = -INFINITY;
 template <bool KV8>
 constexpr float kLazy = KV8 ? 9.f : 24.f;
 constexpr int kWeightExp = 6;
+// Over 8-bit pools the sum of the weights has a reference of its own, the row's
+// largest score as of when it was last exceeded by this much (fp32 has the room).
+constexpr float kLazySum = 60.f;
+// How far apart (log2) a tile's scales may lie for its rows to share one.  K: a code's
+// smallest step, 2^-9, times 2^-15 is f16's smallest number.  V: the same would be
+// exact, but f16 weights count from the tile's largest scale, which the row's
+// weightiest keys may not have: they lose kSpreadV of the 31 bits above.  8 x 32
+// drafts over 24K take 151 us where no tile is wider (scales that vary by 2^N(0, 1)
+// from row to row), 250 where 95 % of V's tiles are (2^N(0, 2)), and 497 where V's all
+// are and half of K's (2^N(0, 3); K's take the general code).
+constexpr int kSpreadK = 15, kSpreadV = 8;
 
 // T: tile width (head size padded to 64, 128 or 256); X: row tiles per CTA.
 template <int T, bool KV8, int X>
@@ -120,7 +134,9 @@ struct Cfg {
     static constexpr int OFF_V = OFF_K + KB * TILE;
     static constexpr int OFF_RAW = OFF_V + VB * TILE;
     static constexpr int OFF_SCALE = OFF_RAW + RU * RAW;
-    static constexpr int OFF_RING = OFF_SCALE + RU * kTile;  // [kRing] Seg
+    // scale bytes of tiles whose rows do not share one: K[4], V[2]
+    static constexpr int OFF_BYTES = OFF_SCALE + RU * kTile;
+    static constexpr int OFF_RING = OFF_BYTES + (KV8 ? 6 * kTile : 0);  // [kRing] Seg
     static constexpr int OFF_BAR = OFF_RING + kRing * 48;
     // barriers
     static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + KB, B_VFULL = B_KEMPTY + KB,
@@ -131,8 +147,7 @@ struct Cfg {
                          B_REMPTY = B_RFULL + RU, B_Q = B_REMPTY + RU, B_IFULL = B_Q + 1,
                          B_IEMPTY = B_IFULL + kRing, B_INFO = B_IEMPTY + kRing,
                          NBAR = B_INFO + kInfo;
-    // tmem, abort, bad pages[kInfo] (8 bits each), poison[kPoison][4], scale bytes: K[4],
-    // V[2]
+    // tmem, abort, bad pages[kInfo] (8 bits each), poison[kPoison][4], scales: K[4], V[2]
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = 1024 + OFF_MISC + 112;
     static_assert(!KV8 || (KB <= 2 && VB <= 2), "f16 tiles");
@@ -283,6 +298,63 @@ __device__ __forceinline__ uint32_t range_bits(int lo, int hi) {
     return top & ~((1u << lo) - 1u);
 }
 
+// ---------------------------------------------------------------------------
+// Tiles over 8-bit pools whose rows do not share a scale: what the softmax does
+// for them, key by key, on a warp's 32 rows of S at t_s.  Functions of their own,
+// so that the usual tiles' code stays close together.
+// ---------------------------------------------------------------------------
+// Byte e of four words as a float less 127: 2^23 + byte has it in its last bits (a
+// conversion would take the slow unit).
+__device__ __forceinline__ float byte_exponent(const uint32_t (&b)[4], int e) {
+    return __uint_as_float(__byte_perm(b[e / 4], 0x4b000000u, 0x7650 + e % 4)) - 8388735.f;
+}
+
+// S times f times 2^(its key's K exponent): the scores.
+__device__ __noinline__ void scale_keys(uint32_t t_s, const uint8_t *bytes, float f) {
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+        uint32_t v[16];
+        tc::ld_32x32b_x16(t_s + 16 * c, v);
+        const uint4 b4 = *reinterpret_cast<const uint4 *>(bytes + 16 * c);
+        const uint32_t b[4] = {b4.x, b4.y, b4.z, b4.w};
+        tc::wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            v[e] = __float_as_uint(__uint_as_float(v[e]) * f *
+                                   scale_value((b[e / 4] >> (8 * (e % 4))) & 255u));
+        tc::st_32x32b_x16(t_s + 16 * c, v);
+    }
+    tc::wait_st();
+}
+
+// For weights by key: S becomes S * f + the exponent of its key's V scale (vexp for
+// all keys without bytes).  Returns its largest, and the sum of 2^(S * f - top).
+__device__ __noinline__ float2 add_exponents(uint32_t t_s, const uint8_t *bytes, float vexp,
+                                             float f, float top) {
+    float m = kNegInf, s0 = 0.f, s1 = 0.f;
+    if (top == kNegInf) top = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+        uint32_t v[16];
+        tc::ld_32x32b_x16(t_s + 16 * c, v);
+        uint4 b4 = make_uint4(0u, 0u, 0u, 0u);
+        if (bytes) b4 = *reinterpret_cast<const uint4 *>(bytes + 16 * c);
+        const uint32_t b[4] = {b4.x, b4.y, b4.z, b4.w};
+        tc::wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const float x = __uint_as_float(v[e]);
+            (e & 1 ? s1 : s0) += fast_exp2(fmaf(x, f, -top));
+            const float y = fmaf(x, f, bytes ? byte_exponent(b, e) : vexp);
+            m = fmaxf(m, y);
+            v[e] = __float_as_uint(y);
+        }
+        tc::st_32x32b_x16(t_s + 16 * c, v);
+    }
+    tc::wait_st();
+    return make_float2(m, s0 + s1);
+}
+
 template <int T, bool KV8, int X>
 __global__ void __launch_bounds__(Cfg<T, KV8, X>::THREADS, 1)
 tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
@@ -295,7 +367,8 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
     int32_t *s_abort = reinterpret_cast<int32_t *>(misc + 1);
     volatile uint8_t *s_bad = reinterpret_cast<uint8_t *>(misc + 2);  // [kInfo]
     uint32_t *s_poison = misc + 4;   // [kPoison][4]
-    uint32_t *s_byte = misc + 4 + 4 * kPoison;  // K[4], V[2]: a tile's largest scale bytes
+    // K[4], V[2]: a tile's largest scale byte; 256 or more: its rows do not share one
+    uint32_t *s_byte = misc + 4 + 4 * kPoison;
     Seg *ring = reinterpret_cast<Seg *>(smem + C::OFF_RING);
     auto bar = [&](int i) { return base + C::OFF_BAR + 8 * i; };
 
@@ -763,7 +836,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         // Segment by segment: Q on its way, the rows of the segment before stored
         // meanwhile, Q's last touch, the key tiles.
         const Seg *prev = nullptr;
-        float m_ref = kNegInf, l = 0.f, sink = kNegInf;
+        float m_ref = kNegInf, l_ref = kNegInf, l = 0.f, sink = kNegInf;
         bool poisoned = false;               // the row keeps a key whose V is not finite
         int64_t unit = 0;
 #pragma unroll 1
@@ -812,19 +885,23 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             const bool part = sg.cut() != 0, row_on = r < sg.nrows;
             const int64_t pslot = (int64_t)(2 * group + sg.cut() / 2) * Hkv + g;
             float4 *po = reinterpret_cast<float4 *>(p.part_o) + pslot * (Dh / 4) * (X * kTile) + r;
-            float mul, lse;
+            float mul, lse, h = 1.f;
+            if (!KV8)
+                l_ref = m_ref;
+            else  // O's units, 2^(m_ref - l_ref), in two halves: the whole may overflow
+                h = l_ref == kNegInf ? 0.f : exp2f(0.5f * (m_ref - l_ref));
             if (part) {
                 mul = l == 0.f ? 0.f : 1.f / l;
-                lse = l == 0.f ? kNegInf : m_ref + log2f(l);
+                lse = l == 0.f ? kNegInf : l_ref + log2f(l);
                 if (row_on) p.part_lse[pslot * (X * kTile) + r] = lse;
             } else {
-                const float M = fmaxf(m_ref, sink);
+                const float M = fmaxf(l_ref, sink);
                 const float Ms = M == kNegInf ? 0.f : M;
-                const float f = exp2f(m_ref - Ms);
+                const float f = exp2f(l_ref - Ms);
                 const float lam = l * f + exp2f(sink - Ms);
                 mul = lam == 0.f ? 0.f : f / lam;
                 lse = lam == 0.f ? kNegInf : (Ms + log2f(lam)) * kLn2;
-                // a NaN weight leaves m_ref as it was: keep the NaN
+                // a NaN weight leaves the reference as it was: keep the NaN
                 if (l != l) mul = lse = l;
                 if (row_on && p.lse_out) p.lse_out[unit_prev] = lse;
             }
@@ -840,7 +917,9 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                 float o[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    o[e] = sg.ntiles > 0 ? __uint_as_float(v[e]) * mul : 0.f;
+                    o[e] = sg.ntiles == 0 ? 0.f
+                           : KV8          ? __uint_as_float(v[e]) * mul * h * h
+                                          : __uint_as_float(v[e]) * mul;
                 const bool on = row_on && 16 * c < Dh;
                 if (on && part) {
 #pragma unroll
@@ -909,10 +988,11 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::B_Q));
         }
-        // Weights are 2^(s - m_ref), over 8-bit pools times the tile's largest V
-        // scale.  m_ref follows the row's largest score (there plus that scale
-        // over 2^10, so that f16 holds the product); O and l share it.
-        m_ref = kNegInf;
+        // Weights are 2^(s - m_ref), and m_ref follows the row's largest score.  Over
+        // 8-bit pools they are 2^(s + v - m_ref) with the exponent v of the tile's
+        // (or the key's) V scale, and m_ref follows the largest s + v, less kWeightExp,
+        // so that f16 holds them; the sum l is there of 2^(s - l_ref).
+        m_ref = l_ref = kNegInf;
         l = 0.f;
         poisoned = false;
         for (int j = 0; j < ntiles && x < nx; ++j) {
@@ -920,32 +1000,27 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             const uint32_t t_s = tmem + (n & 1) * 128 + lane_base;
             const bool fix = j < full_lo || j >= full_hi;
             alive = wait_warp(bar(C::B_INFO + jn % kInfo), (jn / kInfo) & 1u, p.dev_error,
-                              s_abort) &&
-                    wait_warp(bar(C::B_SFULL + (n & 1)), (n >> 1) & 1u, p.dev_error, s_abort);
-            if (KV8 && alive)
-                alive = wait_warp(bar(C::B_KFACT + (jn & 3)), (jn >> 2) & 1u, p.dev_error,
-                                  s_abort) &&
-                        wait_warp(bar(C::B_VFACT + (jn & 1)), (jn >> 1) & 1u, p.dev_error,
-                                  s_abort);
+                              s_abort);
+            uint32_t kb = 0;                 // K's scale: there before S is
+            if constexpr (KV8) {
+                alive = alive && wait_warp(bar(C::B_KFACT + (jn & 3)), (jn >> 2) & 1u,
+                                           p.dev_error, s_abort);
+                kb = *reinterpret_cast<volatile uint32_t *>(s_byte + (jn & 3));
+            }
+            alive = alive && wait_warp(bar(C::B_SFULL + (n & 1)), (n >> 1) & 1u, p.dev_error,
+                                       s_abort);
             if (fix && alive) {
                 alive = wait_warp(bar(C::B_POISON + nfix % kPoison), (nfix / kPoison) & 1u,
                                   p.dev_error, s_abort);
                 ++nfix;
             }
             const uint32_t badpg = s_bad[jn % kInfo];
-            const bool general = fix || badpg != 0 || p.alibi != nullptr;
             if (!alive) break;
             if (warp_on) {
                 tc::fence_after_sync();
-                float rf = rowf, vexp = 0.f, vinv = 1.f, shift = 0.f;
-                if constexpr (KV8) {
-                    const volatile uint32_t *by = s_byte;
-                    rf *= scale_value(by[jn & 3]);
-                    const uint32_t vb = by[4 + (jn & 1)];  // 2^-vexp, subnormal for 254
-                    vinv = __uint_as_float(vb == 254u ? 0x00400000u : (254u - vb) << 23);
-                    vexp = (float)((int)vb - 127);
-                    shift = vexp - kWeightExp;
-                }
+                float rf = rowf;
+                if constexpr (KV8) rf *= kb > 255u ? 1.f : scale_value(kb);
+                const bool general = fix || badpg != 0 || p.alibi != nullptr || kb > 255u;
                 // General tiles.  The keys among kc .. kc + 31 that draft `node` at position
                 // qpos sees.
                 auto depth_of = [&](int k) {  // a draft's depth
@@ -1029,14 +1104,15 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     tc::st_32x32b_x16(t_s + 16 * c, w);
                     return s0 + s1;
                 };
-                // The row's reference follows mt; returns false if a wait gave up.
-                auto refer = [&](float mt) {
-                    if (j == 0) {
-                        m_ref = mt;
-                        return true;
+                // The row's references move up to sm, its largest score, and to mt, its
+                // largest weight's exponent; returns false if a wait gave up.
+                auto refer = [&](float sm, float mt) {
+                    if (KV8 && sm > l_ref + kLazySum) {
+                        l *= fast_exp2(l_ref - sm);
+                        l_ref = sm;
                     }
-                    const bool grow = mt > m_ref + kLazy<KV8> || (m_ref == kNegInf && mt > kNegInf);
-                    if (!__any_sync(0xffffffffu, grow)) return true;
+                    const bool grow = mt > m_ref + kLazy<KV8>;  // (-inf: by anything)
+                    if (KV8 && !__any_sync(0xffffffffu, grow)) return true;
                     if (nx == 1) {  // O must be at rest: the last PV is done
                         // (with two row tiles, S(n) came behind this O's last PV)
                         if (!wait_warp(bar(C::B_VEMPTY + (jn - 1) % C::VB),
@@ -1047,7 +1123,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     }
                     const float f = grow ? fast_exp2(m_ref - mt) : 1.f;
                     if (grow) m_ref = mt;
-                    l *= f;
+                    if (!KV8) l *= f;
 #pragma unroll 1
                     for (int c = 0; c < T / 16; ++c) {
                         uint32_t o[16];
@@ -1061,8 +1137,10 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     return true;
                 };
                 // Twice over S, in loops: unrolled over the row, the code alone outgrows
-                // the schedulers' instruction caches.  The first pass takes the
-                // maximum, and in a general tile leaves the completed scores behind.
+                // the schedulers' instruction caches (the second pass by 64 keys at a time
+                // instead of 32: 151 -> 160 us for 8 x 32 drafts over 24K of 8-bit).  The
+                // first pass takes the maximum, and in a general tile leaves the completed
+                // scores behind.
                 float mt = kNegInf;
                 if (!general) {
 #pragma unroll 1
@@ -1077,6 +1155,10 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     const int i = sg.row0 + min(r, sg.nrows - 1), node = i / G;
                     const int qpos = sg.ctx + depth_of(node);
                     uint32_t vis = 0u;
+                    if (KV8 && kb > 255u) {
+                        scale_keys(t_s, smem + C::OFF_BYTES + (jn & 3) * kTile, rf);
+                        rf = 1.f;
+                    }
 #pragma unroll 1
                     for (int c = 0; c < 8; ++c) {
                         vis = c & 1 ? vis >> 16
@@ -1093,20 +1175,64 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     tc::wait_st();
                     rf = 1.f;
                 }
-                alive = refer(mt * rf + shift);
-                if (!alive) break;
+                mt *= rf;
+                float wt = mt, vexp = 0.f;  // the largest weight's exponent; V's scale in it
+                bool by_key = false;
+                if constexpr (KV8) {
+                    alive = wait_warp(bar(C::B_VFACT + (jn & 1)), (jn >> 1) & 1u, p.dev_error,
+                                      s_abort);
+                    if (!alive) break;
+                    const uint32_t vb = *reinterpret_cast<volatile uint32_t *>(s_byte + 4 + (jn & 1));
+                    vexp = (float)((int)(vb & 255u) - 127);
+                    wt = mt + vexp - kWeightExp;
+                    by_key = vb > 255u;
+                }
+                // The sum over 8-bit pools is that of the weights, moved by m_ref - vexp -
+                // l_ref, unless V's scales differ from key to key, or are so far below those
+                // that m_ref stands for that what counts in it would underflow as a weight.
+                auto far = [&] { return KV8 && m_ref - vexp - l_ref > kLazySum; };
+                if (j == 0 && !by_key) {
+                    m_ref = wt;
+                    l_ref = mt;
+                } else if (by_key ||
+                           __any_sync(0xffffffffu, wt > m_ref + kLazy<KV8> ||
+                                                       (KV8 && mt > l_ref + kLazySum) || far())) {
+                    float key_sum = 0.f;
+                    if constexpr (KV8) {
+                        const bool bytes = by_key;
+                        by_key = by_key || __any_sync(0xffffffffu, far());
+                        if (by_key) {
+                            const float2 of = add_exponents(
+                                t_s, bytes ? smem + C::OFF_BYTES + (4 + (jn & 1)) * kTile : nullptr,
+                                vexp, rf, mt);
+                            wt = of.x - kWeightExp;
+                            key_sum = of.y;
+                            rf = 1.f;
+                            vexp = 0.f;
+                        }
+                    }
+                    if (j == 0) {
+                        m_ref = wt;
+                        l_ref = mt;
+                    } else {
+                        alive = refer(mt, wt);
+                        if (!alive) break;
+                    }
+                    if (by_key && mt != kNegInf) l += key_sum * fast_exp2(mt - l_ref);
+                }
                 const float m = (m_ref == kNegInf ? 0.f : m_ref) - vexp;
                 float sum = 0.f;
 #pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t v[2][32];
-                    tc::ld_32x32b_x32(t_s + 64 * h, v[0]);
-                    tc::ld_32x32b_x32(t_s + 64 * h + 32, v[1]);
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t v[32];
+                    tc::ld_32x32b_x32(t_s + 32 * h, v);
                     tc::wait_ld();
-                    sum += weights(2 * h, v[0], rf, m);
-                    sum += weights(2 * h + 1, v[1], rf, m);
+                    sum += weights(h, v, rf, m);
                 }
-                l += sum * vinv;
+                if (KV8)
+                    sum *= by_key ? 0.f
+                                  : fast_exp2(fminf(m - (l_ref == kNegInf ? 0.f : l_ref), kLazySum));
+                l += sum;
                 tc::wait_st();
                 tc::fence_before_sync();
             }
@@ -1155,39 +1281,6 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                 if (!((s_bad[jt % kInfo] >> (lane * 4 >> bs_shift)) & 1u))
                     in4 = range_bits(tok_lo - k0 - 4 * lane, tok_hi - k0 - 4 * lane) & 15u;
                 const uint8_t *sc = smem + C::OFF_SCALE + rs * kTile;
-                // the largest scale byte of the attended rows, NaN rows aside; not
-                // below 2^-90, so that 1 / scale stays finite
-                const uint32_t b4 = *reinterpret_cast<const uint32_t *>(sc + 4 * lane);
-                uint32_t top = 37;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t by = (b4 >> (8 * e)) & 255u;
-                    if (((in4 >> e) & 1u) && by != kScaleNaN) top = max(top, by);
-                }
-                top = __reduce_max_sync(0xffffffffu, top);
-                if (w == 0 && lane == 0) {
-                    // The softmax that last used the slot is done: V's that of two tiles
-                    // ago, as its buffer is free; K's that of four tiles ago, as S of
-                    // two tiles ago is done, which came behind that tile's O.
-                    s_byte[isv ? 4 + (jt & 1) : jt & 3] = top;
-                    mbar_arrive(bar(isv ? C::B_VFACT + (jt & 1) : C::B_KFACT + (jt & 3)));
-                }
-                // NaN rows of a V tile that some row does not see are zeroed and noted
-                uint32_t bad4 = 0;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (((b4 >> (8 * e)) & 255u) == kScaleNaN) bad4 |= 1u << e;
-                bad4 &= in4;
-                if (isv && fix) {
-                    // lane l holds rows 4l..: word q of the tile is lanes 8q .. 8q + 7
-                    uint32_t word = bad4 << (4 * (lane & 7));
-                    word |= __shfl_xor_sync(0xffffffffu, word, 1);
-                    word |= __shfl_xor_sync(0xffffffffu, word, 2);
-                    word |= __shfl_xor_sync(0xffffffffu, word, 4);
-                    if (w == 0 && (lane & 7) == 0) s_poison[(nfix % kPoison) * 4 + (lane >> 3)] = word;
-                }
-                const uint32_t zero4 = isv ? (~in4 & 15u) | (fix ? bad4 : 0u) : 0u;
-                const bool zeros = __any_sync(0xffffffffu, zero4 != 0u);
                 // Row r = 8 * group + rq: its chunks' places in the raw tile and in the
                 // f16 tile depend on the group only through 8 rows' distance.
                 const int q = lane >> 3, c4 = lane & 3, rq = (lane & 4) ? q ^ 5 : q;
@@ -1203,6 +1296,50 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                                             : rq * 64u + ((cc ^ ((rq >> 1) & 3)) << 4));
                 }
                 const uint32_t do0 = sw128(rq, 2 * c4), do1 = sw128(rq, 2 * c4 + 1);
+                // This lane's four bytes at once.  attended: a byte of ones per row; nan:
+                // the top bit of a NaN row's
+                const uint32_t b4 = *reinterpret_cast<const uint32_t *>(sc + 4 * lane);
+                const uint32_t attended = (in4 * 0x00204081u & 0x01010101u) * 255u;
+                const uint32_t x4 = b4 & attended;
+                const uint32_t nan = x4 & ((x4 & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                // the largest and the smallest scale of the attended rows, NaN rows aside
+                const uint32_t hi4 = x4 & ~((nan >> 7) * 255u), lo4 = b4 | ~attended;
+                const uint32_t hi2 = __vmaxu2(hi4 & 0x00ff00ffu, (hi4 >> 8) & 0x00ff00ffu);
+                const uint32_t lo2 = __vminu2(lo4 & 0x00ff00ffu, (lo4 >> 8) & 0x00ff00ffu);
+                const uint32_t top = __reduce_max_sync(0xffffffffu, max(hi2 & 0xffffu, hi2 >> 16));
+                const bool wide = __any_sync(
+                    0xffffffffu, min(lo2 & 0xffffu, lo2 >> 16) + (isv ? kSpreadV : kSpreadK) < top);
+                if (w == 0) {
+                    // The softmax that last used the slot is done: V's that of two tiles
+                    // ago, as its buffer is free; K's that of four tiles ago, as S of
+                    // two tiles ago is done, which came behind that tile's O.
+                    const int slot = isv ? 4 + (jt & 1) : jt & 3;
+                    if (wide)  // (a NaN row's values are NaN whatever its scale: 0, which
+                               // counts for no maximum)
+                        *reinterpret_cast<uint32_t *>(smem + C::OFF_BYTES + slot * kTile +
+                                                      4 * lane) = b4 & ~((nan >> 7) * 255u);
+                    __syncwarp();
+                    if (lane == 0) {
+                        s_byte[slot] = top | (wide ? 256u : 0u);
+                        mbar_arrive(bar(isv ? C::B_VFACT + (jt & 1) : C::B_KFACT + (jt & 3)));
+                    }
+                }
+                // NaN rows of a V tile that some row does not see are zeroed and noted
+                const uint32_t bad4 = ((nan >> 7) * 0x01020408u) >> 24 & 15u;
+                if (isv && fix) {
+                    // lane l holds rows 4l..: word q of the tile is lanes 8q .. 8q + 7
+                    uint32_t word = bad4 << (4 * (lane & 7));
+                    word |= __shfl_xor_sync(0xffffffffu, word, 1);
+                    word |= __shfl_xor_sync(0xffffffffu, word, 2);
+                    word |= __shfl_xor_sync(0xffffffffu, word, 4);
+                    if (w == 0 && (lane & 7) == 0) s_poison[(nfix % kPoison) * 4 + (lane >> 3)] = word;
+                }
+                const uint32_t zero4 = isv ? (~in4 & 15u) | (fix ? bad4 : 0u) : 0u;
+                const bool zeros = __any_sync(0xffffffffu, zero4 != 0u);
+                // (opaque to the compiler, which would make two loops: 150 -> 158 us for 8 x
+                // 32 drafts over 24K)
+                int scaled = wide ? 0 : -1;
+                asm("" : "+r"(scaled));
                 constexpr int BATCH = T == 256 ? 2 : 4;  // groups whose loads are in flight
 #pragma unroll 1
                 for (int g0 = 0; g0 < ROWS / 8; g0 += BATCH) {
@@ -1218,10 +1355,11 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                     }
 #pragma unroll
                     for (int gi = 0; gi < BATCH; ++gi) {
-                        // 2^(byte - top) in f16, a NaN for a NaN row
-                        const int d = (int)by[gi] - (int)top;
+                        // 2^(byte - top) in f16 (at least 2^-15 for what is attended), or
+                        // 1 where each key has its own scale; a NaN for a NaN row
+                        const int d = ((int)by[gi] - (int)top) & scaled;
                         uint32_t f = d >= -14 ? (uint32_t)(15 + min(d, 0)) << 10
-                                     : d >= -24 ? 1u << (24 + d)
+                                     : d == -15 ? 1u << 9
                                                 : 0u;
                         if (by[gi] == kScaleNaN) f = 0x7fffu;
                         f |= f << 16;
@@ -1316,7 +1454,7 @@ tree_merge_kernel(const TreeParams p, int rows) {
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int i = 0; i < n; ++i) {
-            const float w = exp2f(lse_of(i) - Ms);
+            const float w = exp2f(lse_of(i) - Ms) * inv;
             const float4 v = reinterpret_cast<const float4 *>(
                 p.part_o)[(slot(i) * (D / 4) + c / 4) * rows + r];
             acc.x = fmaf(w, v.x, acc.x);
@@ -1325,7 +1463,7 @@ tree_merge_kernel(const TreeParams p, int rows) {
             acc.w = fmaf(w, v.w, acc.w);
         }
         *reinterpret_cast<uint2 *>(out + c) =
-            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+            make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
     }
     if (p.lse_out && lane == 0) p.lse_out[unit] = lam == 0.f ? kNegInf : (Ms + log2f(lam)) * kLn2;
 }

@@ -7,6 +7,7 @@ import torch
 
 import paged_kv_cache_attention_gb300 as pkv
 from tests import _fp8 as R
+from tests.test_gpu_fp8_ranges import check
 from tests.test_gpu_tree import pack, tree
 
 pytestmark = pytest.mark.gpu
@@ -75,3 +76,116 @@ def test_lse_is_of_the_scores_alone(kind, m, d, partition, fp8, value):
             R.out_bound(ref, absv, smax, d, 2.0 ** -8)
         R.assert_within(got[ok], ref[ok], bound[ok], f"out, value at {at}")
         pools.rows = rows
+
+
+# a key's weight is held to 2^-25 where the largest score beside its tile's largest V
+# scale stands at 2^6 or more; the row's weightiest key may have 2^-8 of that scale,
+# and a code is at most twice as large as another row's largest: 2^-31 * 2^8 * 2
+TREE_FLOOR = 2.0 ** -22
+
+
+@pytest.mark.parametrize("size", [9, 14, 16, 20, 24, 40, 100])
+@pytest.mark.parametrize("m,hq,hkv,d,partition", [(12, 8, 2, 128, 0), (40, 8, 2, 64, 1024),
+                                                  (5, 4, 1, 256, 1024), (80, 4, 1, 128, 0)])
+def test_a_hidden_draft_costs_nothing(m, hq, hkv, d, partition, size):
+    """K and V of one draft are 2^size times the others'; only it sees itself."""
+    n = 430
+    pools, q, table, slots, mask, keep = step(n, m, hq, hkv, d, True, "tree", size + m)
+    at = m // 2
+    keep[:, n - m + at] = False
+    keep[at, n - m + at] = True
+    mask = pack([sum(1 << j for j in range(m) if keep[i, n - m + j]) for i in range(m)], 2)
+    s = slots[n - m + at]
+    pools.rows = 0.7 * torch.randn(pools.rows.shape, generator=torch.Generator().manual_seed(3)).to(BF16)
+    pools.rows[:, s // 16, :, s % 16] *= 2.0 ** size
+    pools.codes, pools.byte = R.quantise(pools.rows)
+    out, lse = attend(pools, q, table, n, mask, partition)
+    others = [i for i in range(m) if i != at]
+    check(out[others], lse[others], q[others], *pools.at(slots), keep[others], d ** -0.5,
+          TREE_FLOOR, "others")
+
+
+@pytest.mark.parametrize("size", [7, 8, 12, 24, 30, 60, 118])
+@pytest.mark.parametrize("m,hq,hkv,d,partition", [(12, 8, 2, 128, 0), (40, 8, 2, 64, 1024),
+                                                  (5, 4, 1, 256, 1024), (80, 4, 1, 128, 0)])
+@pytest.mark.parametrize("where", ["context", "draft"])
+def test_a_large_value_of_little_weight(where, m, hq, hkv, d, partition, size):
+    """One key's V is 2^size times the others' and its weight 2^-(size + 40)."""
+    n = 430
+    pools, q, table, slots, mask, keep = step(n, m, hq, hkv, d, True, "chain", size + m)
+    g = torch.Generator().manual_seed(4)
+    scale = d ** -0.5
+    way = torch.randn(d, generator=g)
+    q = (way + 0.05 * torch.randn(m, hq, d, generator=g)).to(BF16)
+    s = slots[77 if where == "context" else n - m]
+    pools.rows[0] = 0.3 * torch.randn(pools.rows[0].shape, generator=g).to(BF16)
+    pools.rows[0][s // 16, :, s % 16] = \
+        (-way * ((size + 40) * 0.693 / (scale * float(way @ way)))).to(BF16)
+    pools.rows[1] = torch.randn(pools.rows[1].shape, generator=g).to(BF16)
+    pools.rows[1][s // 16, :, s % 16] *= 2.0 ** size
+    pools.codes, pools.byte = R.quantise(pools.rows)
+    out, lse = attend(pools, q, table, n, mask, partition)
+    check(out, lse, q, *pools.at(slots), keep, scale, TREE_FLOOR, where)
+
+
+@pytest.mark.parametrize("size", [15, 16, 20, 24, 60, 118])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_large_key_across_the_queries(d, size):
+    """A kept key 2^size times the others', in dims where every query is 0."""
+    m, n, hq, hkv = 9, 300, 6, 2
+    pools, q, table, slots, mask, keep = step(n, m, hq, hkv, d, True, "tree", size)
+    g = torch.Generator().manual_seed(5)
+    q[..., :16] = 0
+    pools.rows = torch.randn(pools.rows.shape, generator=g).to(BF16)
+    s = slots[40]
+    pools.rows[0][s // 16, :, s % 16, :16] *= 2.0 ** size
+    pools.rows[0][s // 16, :, s % 16, 16:] = 0
+    pools.codes, pools.byte = R.quantise(pools.rows)
+    for partition in (0, 1024):
+        out, lse = attend(pools, q, table, n, mask, partition)
+        check(out, lse, q, *pools.at(slots), keep, d ** -0.5, TREE_FLOOR, f"partition {partition}")
+
+
+@pytest.mark.parametrize("sizes", [(60, 0, -60, 30), (-60, -20, 30, 60), (118, -110, 0, 118),
+                                   (-118, 118, -118, 118), (-118, -118, -118, -118),
+                                   (118, 118, 118, 118)])
+@pytest.mark.parametrize("d,m", [(128, 10), (64, 70), (256, 3)])
+def test_tiles_of_very_different_values(d, m, sizes):
+    """V of every 128 keys at a size of its own: the weights' sum does not follow V."""
+    n, hq, hkv = 470, 4, 1
+    pools, q, table, slots, mask, keep = step(n, m, hq, hkv, d, True, "chain", m)
+    g = torch.Generator().manual_seed(6)
+    pools.rows = torch.randn(pools.rows.shape, generator=g).to(BF16)
+    for t, e in enumerate(sizes):
+        s = slots[128 * t:128 * t + 128]
+        pools.rows[1][s // 16, :, s % 16] *= 2.0 ** e
+    pools.codes, pools.byte = R.quantise(pools.rows)
+    k, v = pools.at(slots)
+    top = 2.0 ** -max(sizes)  # near the ends of the range the definition is computed beside 1
+    for partition in (0, 1024):
+        out, lse = attend(pools, q, table, n, mask, partition)
+        check(out.to(torch.float64).cpu() * top, lse, q, k, v * top, keep, d ** -0.5, TREE_FLOOR,
+              f"partition {partition}")
+
+
+@pytest.mark.parametrize("partition", [0, 1024])
+@pytest.mark.parametrize("d", [128, 64])
+def test_rows_of_every_size_and_shape(d, partition):
+    """Scales that vary by 2^N(0, 4) from row to row, zero rows and a NaN row that no draft
+    sees among them."""
+    for seed in range(4):
+        g = torch.Generator().manual_seed(seed)
+        m, n, hq, hkv = 20 + 30 * (seed % 2), 390 + 17 * seed, 8, 2
+        pools, q, table, slots, mask, keep = step(n, m, hq, hkv, d, True, "tree", seed)
+        size = torch.exp2(4 * torch.randn(pools.rows.shape[:-1] + (1,), generator=g))
+        size[0] = torch.exp2(torch.log2(size[0]).clamp(max=2))
+        pools.rows = (torch.randn(pools.rows.shape, generator=g) * size).to(BF16)
+        for at in (3, 200, n - m + 2):
+            pools.rows[:, slots[at] // 16, :, slots[at] % 16] = 0
+        blind = n - m + 5
+        keep[:, blind] = False
+        mask = pack([sum(1 << j for j in range(m) if keep[i, n - m + j]) for i in range(m)], 2)
+        pools.rows[:, slots[blind] // 16, :, slots[blind] % 16] = float("nan")
+        pools.codes, pools.byte = R.quantise(pools.rows)
+        out, lse = attend(pools, q, table, n, mask, partition)
+        check(out, lse, q, *pools.at(slots), keep, d ** -0.5, TREE_FLOOR, f"seed {seed}")
