@@ -14,7 +14,9 @@ namespace {
 constexpr int kDefaultPartition = 512;
 constexpr int kMaxPartition = 16384;
 constexpr int kMaxAutoPartition = 1536;
-constexpr int kDecodeSlots = 912;  // CTAs of the 8-bit decode that run at once: 6 per SM
+// CTAs of the 8-bit decode that run at once: 6 per SM with heads up to 128 and up to
+// 8 of them per kv head, which the rule below was measured with (else 3 to 5)
+constexpr int kDecodeSlots = 912;
 
 bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -195,14 +197,18 @@ pkv_status pkv_paged_decode_fp8(void *out, const void *q, const void *k_cache,
     int P = partition_size;
     if (P == 0) {
         // Longer ones while the SMs have more than eight full rounds of CTAs and the
-        // longest sequence keeps eight partitions.  Share of a copy's rate with 512,
-        // 1024 and 1536: 8 of 32K..128K tokens 83, 88 and 89 % (heads of 64: 68, 78
+        // longest sequence keeps eight partitions of the keys it attends (a window leaves
+        // the last ones).  Share of a copy's rate with 512, 1024 and 1536, over five
+        // draws: 8 of 32K..128K tokens 83, 88 and 89 % (heads of 64: 68, 78
         // and 80), 16 of 4K..32K 76, 79 and 70; fewer than eight, 128 of 0.5K..8K:
-        // 85, 86 and 83.
+        // 85, 86 and 83.  16 of 32K..128K with a window of 4K: 51, 58 and 45.
+        const int64_t span = window_left >= 0 && window_left < max_seqlen
+                                 ? (int64_t)window_left + 1
+                                 : max_seqlen;
         P = kDefaultPartition;
         while (P < kMaxAutoPartition &&
-               (int64_t)batch * cache.num_kv_heads * (max_seqlen / P) > 8 * kDecodeSlots &&
-               max_seqlen / (P + kDefaultPartition) >= 8)
+               (int64_t)batch * cache.num_kv_heads * (span / P) > 8 * kDecodeSlots &&
+               span / (P + kDefaultPartition) >= 8)
             P += kDefaultPartition;
     }
     if (P < 0 || P % cache.block_size != 0 || P > kMaxPartition) return PKV_ERR_INVALID_ARG;
