@@ -767,6 +767,30 @@ def _token_rows(name, t, dtype, tokens: int, heads: int, head_dim: int, dev: int
     raise ValueError(f"{name} must be [{tokens}, {heads}, {head_dim}], got {list(t.shape)}")
 
 
+def _rows_meet(tokens: int, a: int, step_a: int, len_a: int, b: int, step_b: int,
+               len_b: int) -> bool:
+    """Whether one of ``tokens`` rows of len_a bytes at a, a + step_a, .. shares a
+    byte with one of len_b at b, b + step_b, .."""
+    if a >= b + (tokens - 1) * step_b + len_b or b >= a + (tokens - 1) * step_a + len_a or \
+            not (len_a and len_b):
+        return False
+    if tokens <= 1 or step_a < len_a or step_b < len_b:
+        return tokens == 1  # (shorter steps: the library refuses them)
+    if step_a == step_b:    # slices of one projection: the rows lie alike in each step
+        d = (b - a) % step_a
+        return d < len_a or step_a - d < len_b
+    i = j = 0
+    while i < tokens and j < tokens:
+        at_a, at_b = a + i * step_a, b + j * step_b
+        if at_a + len_a <= at_b:
+            i += 1
+        elif at_b + len_b <= at_a:
+            j += 1
+        else:
+            return True
+    return False
+
+
 class _Types:
     """torch and the dtypes the checks compare with, looked up once."""
     torch = bf16 = f32 = i32 = i64 = u8 = e4m3 = None
@@ -969,10 +993,10 @@ def qk_norm_rope_reshape_and_cache(query, key, value, k_cache, v_cache, position
 
     Rows are bf16 or float32; a token's heads are contiguous and tokens may
     have any stride (slices of a fused projection).  The rotated rows go to
-    query_out / key_out (which overlap no other argument), or back in place when
-    these are None.  With k_scale and
-    v_scale the pools are the 8-bit cache of reshape_and_cache_fp8, else pools of
-    the rows' dtype.  query (with query_out and q_weight) may be None."""
+    query_out / key_out, or back in place when these are None; they may not
+    overlap one another or value, nor query or key but as these themselves.  With
+    k_scale and v_scale the pools are the 8-bit cache of reshape_and_cache_fp8, else
+    pools of the rows' dtype.  query (with query_out and q_weight) may be None."""
     ty = _types()
     dev = _cuda_index("key", key)
     dtype = key.dtype
@@ -1016,6 +1040,22 @@ def qk_norm_rope_reshape_and_cache(query, key, value, k_cache, v_cache, position
     if q_weight is not None:
         _arg_vector("q_weight", q_weight, wd, D, dev)
     err = _error_word(dev_error, dev)
+    # outputs are written while other heads and tokens are still read
+    es = key.element_size()
+    rows = [("key", key.data_ptr(), ks * es, Hkv * D * es),
+            ("value", value.data_ptr(), vs * es, Hkv * D * es)]
+    outs = [("key_out", key_out.data_ptr(), kos * es, Hkv * D * es)]
+    if query is not None:
+        rows.append(("query", query.data_ptr(), qs * es, Hq * D * es))
+        outs.append(("query_out", query_out.data_ptr(), qos * es, Hq * D * es))
+        if _rows_meet(T, *outs[0][1:], *outs[1][1:]):
+            raise ValueError("query_out must not overlap key_out")
+    for out in outs:
+        for row in rows:
+            if out[1:] == row[1:] and out[0].startswith(row[0]):
+                continue  # in place
+            if _rows_meet(T, *out[1:], *row[1:]):
+                raise ValueError(f"{out[0]} must not overlap {row[0]}")
     lib = load_library()
 
     def call(handle):
