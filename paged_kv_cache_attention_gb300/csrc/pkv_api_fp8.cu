@@ -153,9 +153,10 @@ pkv_status pkv_gather_cache_fp8(void *key, void *value, const void *k_cache, con
                                 int64_t total_k, int32_t *dev_error, void *stream) {
     const pkv_status st = check_pool(cache, true, false);
     if (st != PKV_OK) return st;
-    if (batch < 0 || total_k < 0 || max_blocks_per_seq <= 0) return PKV_ERR_INVALID_ARG;
+    if (batch < 0 || total_k < 0 || max_blocks_per_seq < 0) return PKV_ERR_INVALID_ARG;
     if (total_k > (int64_t(1) << 30)) return PKV_ERR_UNSUPPORTED;
-    if (batch == 0 || total_k == 0) return PKV_OK;
+    if (batch == 0 || total_k == 0) return PKV_OK;  // (a table without columns has no rows)
+    if (max_blocks_per_seq == 0) return PKV_ERR_INVALID_ARG;
     if (!key || !value || !k_cache || !v_cache || !k_scale || !v_scale || !block_table ||
         !cu_seq_lens_k)
         return PKV_ERR_INVALID_ARG;
