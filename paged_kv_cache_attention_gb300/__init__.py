@@ -667,6 +667,14 @@ def _arg_vector(name, t, dtype, n: int, dev: int):
     _arg_shape(name, t, dtype, (n,), dev)
 
 
+def _int32(name, value) -> int:
+    """A host integer that the library takes in 32 bits (ctypes would cut it off)."""
+    value = int(value)
+    if -2 ** 31 <= value < 2 ** 31:
+        return value
+    raise ValueError(f"{name} must be within 32 bits, got {value}")
+
+
 def _error_word(dev_error, dev: int):
     """The address of the caller's error word, or None."""
     if dev_error is None:
@@ -960,7 +968,9 @@ def paged_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_s
     _attention_extras(sink, alibi_slopes, out, lse, q, B, Hq, dev)
     err = _error_word(dev_error, dev)
     scale = float(sm_scale) if sm_scale is not None else D ** -0.5
-    max_seqlen, window_left, partition_size = int(max_seqlen), int(window_left), int(partition_size)
+    max_seqlen = _int32("max_seqlen", max_seqlen)
+    window_left = _int32("window_left", window_left)
+    partition_size = _int32("partition_size", partition_size)
     # one partition needs no workspace
     need = 0 if max_seqlen <= (partition_size or 512) else \
         _decode_ws(B, Hq, D, max_seqlen, partition_size, window_left)
@@ -1114,8 +1124,10 @@ def paged_tree_attention(q, k_cache, v_cache, block_table, cu_seq_lens_q, cache_
     _require(rows == B, "block_table must have one row per request")
     _arg("tree_mask", tree_mask, ty.i64, 2, dev)
     rows, words = tree_mask.shape
-    max_seqlen_q, max_seqlen = int(max_seqlen_q), int(max_seqlen)
-    window_left, partition_size = int(window_left), int(partition_size)
+    max_seqlen_q = _int32("max_seqlen_q", max_seqlen_q)
+    max_seqlen = _int32("max_seqlen", max_seqlen)
+    window_left = _int32("window_left", window_left)
+    partition_size = _int32("partition_size", partition_size)
     _require(rows == total_q and 64 * words >= max_seqlen_q,
              "tree_mask must be [total_q, words] with words * 64 >= max_seqlen_q")
     if tree_depth is not None:
