@@ -101,7 +101,7 @@ TreeSplit tree_split(int batch, int Hq, int Hkv, int D, int max_q) {
     // rows of a row group: two tiles where the CTA takes two
     const size_t grow = kTreeTile * (D <= 128 && s.row_tiles > 1 ? 2 : 1);
     const size_t units = (size_t)2 * s.groups * Hkv * grow;
-    s.line_bytes = (((size_t)batch + 2) * 8 + 255) / 256 * 256;
+    s.line_bytes = (((size_t)batch + 1) * 8 + 255) / 256 * 256;
     s.lse_bytes = (units * sizeof(float) + 255) / 256 * 256;
     s.total = s.line_bytes + s.lse_bytes + units * D * sizeof(float);
     return s;

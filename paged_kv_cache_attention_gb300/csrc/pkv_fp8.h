@@ -69,8 +69,8 @@ struct TreeParams {
     const int32_t *depth;          // [total_q] or nullptr
     const float *sink, *alibi;
     float *lse_out;                // [total_q, Hq] or nullptr
-    long long *line;               // [B + 2] the requests' places on the line of work,
-                                   // its length and a CTA group's share (tree.cu)
+    long long *line;               // [B + 1] the requests' places on the line of work,
+                                   // and a CTA group's share of it (tree.cu)
     float *part_lse;               // [2 * groups, Hkv, rows of a row group] (log2 units)
     float *part_o;                 // the same with [D / 4, rows, 4]
     int32_t *dev_error;

@@ -447,7 +447,8 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         // ------------------------------------------------------------ segments, loads
         constexpr int kRows = X * kTile;
         const int groups = gridDim.x / Hkv;
-        // the line's length; the requests' places on it go to the merge kernel
+        // the line's length; the requests' places on it, and the share, go to the merge
+        // kernel
         long long total = 0;
         for (int b0 = 0; b0 < p.batch; b0 += 32) {
             long long c = 0;
@@ -465,10 +466,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
         }
         const long long share =
             max((total + groups - 1) / groups, (long long)p.min_tiles);
-        if (blockIdx.x == 0 && lane == 0) {
-            p.line[p.batch] = total;
-            p.line[p.batch + 1] = share;
-        }
+        if (blockIdx.x == 0 && lane == 0) p.line[p.batch] = share;
         const long long lo = min(share * group, total), hi = min(lo + share, total);
 
         // box coordinates of (page, kv head); one past the pool reads zeros
@@ -1427,7 +1425,7 @@ tree_merge_kernel(const TreeParams p, int rows) {
     const int D = p.head_dim, G = p.group, g = h / G;
     const int row = t * G + (h - g * G), rg = row / rows;
     const int tiles = cost_of(p, rq, rows).tiles;
-    const long long s = p.line[b] + (long long)rg * tiles, share = p.line[p.batch + 1];
+    const long long s = p.line[b] + (long long)rg * tiles, share = p.line[p.batch];
     const int first = (int)(s / share), last = (int)((s + tiles - 1) / share);
     if (first == last) return;  // one CTA had all of it
     const int n = last - first + 1;
