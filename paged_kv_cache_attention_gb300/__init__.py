@@ -799,6 +799,19 @@ def _rows_meet(tokens: int, a: int, step_a: int, len_a: int, b: int, step_b: int
     return False
 
 
+def _refuse_overlap(tokens: int, outs, ins) -> None:
+    """Outputs (name, address, bytes between tokens, bytes of a row) overlap neither one
+    another nor an input, but that of their own name as that input itself."""
+    if _rows_meet(tokens, *outs[0][1:], *outs[1][1:]):
+        raise ValueError(f"{outs[1][0]} must not overlap {outs[0][0]}")
+    for out in outs:
+        for row in ins:
+            if out[1:] == row[1:] and out[0].startswith(row[0]):
+                continue  # in place
+            if _rows_meet(tokens, *out[1:], *row[1:]):
+                raise ValueError(f"{out[0]} must not overlap {row[0]}")
+
+
 class _Types:
     """torch and the dtypes the checks compare with, looked up once."""
     torch = bf16 = f32 = i32 = i64 = u8 = e4m3 = None
@@ -1050,30 +1063,30 @@ def qk_norm_rope_reshape_and_cache(query, key, value, k_cache, v_cache, position
     if q_weight is not None:
         _arg_vector("q_weight", q_weight, wd, D, dev)
     err = _error_word(dev_error, dev)
-    # outputs are written while other heads and tokens are still read
+    # outputs are written while other heads and tokens are still read: apart from the
+    # inputs and one another, or in place in rows that lie q, k, v, or looked at closely
     es = key.element_size()
-    rows = [("key", key.data_ptr(), ks * es, Hkv * D * es),
-            ("value", value.data_ptr(), vs * es, Hkv * D * es)]
-    outs = [("key_out", key_out.data_ptr(), kos * es, Hkv * D * es)]
-    if query is not None:
-        rows.append(("query", query.data_ptr(), qs * es, Hq * D * es))
-        outs.append(("query_out", query_out.data_ptr(), qos * es, Hq * D * es))
-        if _rows_meet(T, *outs[0][1:], *outs[1][1:]):
-            raise ValueError("query_out must not overlap key_out")
-    for out in outs:
-        for row in rows:
-            if out[1:] == row[1:] and out[0].startswith(row[0]):
-                continue  # in place
-            if _rows_meet(T, *out[1:], *row[1:]):
-                raise ValueError(f"{out[0]} must not overlap {row[0]}")
+    k0, v0, ko0 = key.data_ptr(), value.data_ptr(), key_out.data_ptr()
+    q0, qo0 = (k0, ko0) if query is None else (query.data_ptr(), query_out.data_ptr())
+    kn, qn, span = Hkv * D * es, Hq * D * es, (T - 1) * es
+    k1, v1, ko1 = k0 + span * ks + kn, v0 + span * vs + kn, ko0 + span * kos + kn
+    q1, qo1 = q0 + span * qs + qn, qo0 + span * qos + qn
+    lo, hi = min(q0, k0, v0), max(q1, k1, v1)
+    if not ((ko1 <= lo or ko0 >= hi) and (qo1 <= lo or qo0 >= hi)
+            and (ko1 <= qo0 or qo1 <= ko0)) and \
+            not (q0 == qo0 and k0 == ko0 and qs == qos == ks == kos == vs
+                 and q0 + qn <= k0 and k0 + kn <= v0 and v0 + kn <= q0 + qs * es):
+        _refuse_overlap(T, (("key_out", ko0, kos * es, kn), ("query_out", qo0, qos * es, qn)),
+                        (("key", k0, ks * es, kn), ("query", q0, qs * es, qn),
+                         ("value", v0, vs * es, kn)))
     lib = load_library()
 
     def call(handle):
         return lib.pkv_qk_norm_rope_reshape_and_cache(
-            _ptr(query), key.data_ptr(), value.data_ptr(), qs, ks, vs, dt, _ptr(query_out),
-            key_out.data_ptr(), qos, kos, k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale),
-            _ptr(v_scale), positions.data_ptr(), slot_mapping.data_ptr(), T, Hq, desc,
-            _ptr(q_weight), k_weight.data_ptr(), w32, float(eps), cos_sin.data_ptr(), maxpos, rd,
+            q0 if Hq else None, k0, v0, qs, ks, vs, dt, qo0 if Hq else None, ko0, qos, kos,
+            k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale),
+            positions.data_ptr(), slot_mapping.data_ptr(), T, Hq, desc, _ptr(q_weight),
+            k_weight.data_ptr(), w32, float(eps), cos_sin.data_ptr(), maxpos, rd,
             bool(is_neox_style), err, handle)
     st = _on_stream(dev, stream, call)
     if st:
