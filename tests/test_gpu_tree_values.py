@@ -8,7 +8,7 @@ import torch
 import paged_kv_cache_attention_gb300 as pkv
 from tests import _fp8 as R
 from tests.test_gpu_fp8_ranges import check
-from tests.test_gpu_tree import pack, tree
+from tests.test_gpu_tree import pack, run, tree
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -189,3 +189,67 @@ def test_rows_of_every_size_and_shape(d, partition):
         pools.codes, pools.byte = R.quantise(pools.rows)
         out, lse = attend(pools, q, table, n, mask, partition)
         check(out, lse, q, *pools.at(slots), keep, d ** -0.5, TREE_FLOOR, f"seed {seed}")
+
+
+@pytest.mark.parametrize("scale", [1.0, 8.0, -8.0])
+@pytest.mark.parametrize("d,hkv", [(128, 2), (64, 1)])
+def test_scores_that_grow_by_hundreds(d, hkv, scale):
+    """Maxima far above the first tile's: the sum's reference has to follow."""
+    run([900, 700], [9, 40], 4, hkv, d, fp8=True, scale=scale, partition=1024)
+    run([900, 700], [9, 40], 4, hkv, d, fp8=True, scale=scale, sink=True, spread=2.0)
+
+
+@pytest.mark.parametrize("partition", [0, 1024])
+@pytest.mark.parametrize("window,slopes,sink", [(70, False, False), (-1, True, True),
+                                                (260, True, True), (-1, False, True)])
+@pytest.mark.parametrize("d,m", [(128, 12), (64, 70), (256, 4)])
+def test_wide_tiles_under_every_mask(d, m, window, slopes, sink, partition):
+    """Scales by 2^N(0, 4) from key to key, with a window, ALiBi slopes, a sink, and a draft
+    of NaN values that some drafts see."""
+    n, hq, hkv = 420, 8, 2
+    pools, q, table, slots, mask, keep = step(n, m, hq, hkv, d, True, "tree", m)
+    g = torch.Generator().manual_seed(d)
+    ctx = n - m
+    depth = torch.tensor([bin(sum(int(keep[i, ctx + j]) << j for j in range(m))).count("1") - 1
+                          for i in range(m)], dtype=I32)
+    size = torch.exp2(4 * torch.randn(pools.rows.shape[:-1] + (1,), generator=g))
+    size[0] = torch.exp2(torch.log2(size[0]).clamp(max=2))
+    pools.rows = (torch.randn(pools.rows.shape, generator=g) * size).to(BF16)
+    bad = m // 3
+    pools.rows[1][slots[ctx + bad] // 16, :, slots[ctx + bad] % 16, 3] = float("nan")
+    pools.codes, pools.byte = R.quantise(pools.rows)
+    kpos = torch.cat([torch.arange(ctx), ctx + depth.long()])
+    qpos = ctx + depth.long()
+    if window >= 0:
+        keep = keep & (kpos[None] >= qpos[:, None] - window)
+    snk = 2 * torch.randn(hq, generator=g) if sink else None
+    alibi = torch.exp2(-8.0 * (torch.arange(hq) + 1) / hq) if slopes else None
+    bias = None
+    if slopes:
+        bias = alibi.to(torch.float64)[:, None, None] * \
+            (kpos[None] - qpos[:, None]).to(torch.float64)[None]
+    kc, vc, ks, vs = pools.device(DEV)
+    lse = torch.zeros(m, hq, device=DEV)
+    out = pkv.paged_tree_attention(
+        q.to(DEV), kc, vc, table.to(DEV), torch.tensor([0, m], dtype=I32, device=DEV),
+        torch.tensor([n], dtype=I32, device=DEV), m, n, mask.to(DEV), tree_depth=depth.to(DEV),
+        k_scale=ks, v_scale=vs, sink=None if snk is None else snk.to(DEV), window_left=window,
+        partition_size=partition, lse=lse, alibi_slopes=None if alibi is None else alibi.to(DEV))
+    k, v = pools.at(slots)
+    ref, rl, absv, smax = R.attend(q, k, v, keep, d ** -0.5, snk, bias)
+    if slopes:
+        smax = smax + bias.abs().max()
+    R.assert_within(lse, rl, R.lse_bound(rl, smax, d), "lse")
+    sees = keep[:, ctx + bad]
+    assert not bool(torch.isfinite(out.cpu()[sees]).any())
+    # the row's largest weighted value, in the weights' own terms
+    floor = torch.zeros(m, hq, 1, dtype=torch.float64)
+    for h in range(hq):
+        big = v[:, h // 4].abs().amax(-1)
+        for i in range(m):
+            sc = (k[:, h // 4][keep[i]] @ q[i, h].to(torch.float64)) * d ** -0.5
+            if bias is not None:
+                sc = sc + bias[h, i][keep[i]]
+            floor[i, h] = TREE_FLOOR * sc.numel() * (torch.exp(sc - rl[i, h]) * big[keep[i]]).max()
+    bound = R.out_bound(ref, absv, smax, d, 2.0 ** -11 + 2.0 ** -13) + floor
+    R.assert_within(out[(~sees).to(DEV)], ref[~sees], bound[~sees], "out")
