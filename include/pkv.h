@@ -529,7 +529,8 @@ PKV_API pkv_status pkv_paged_decode_fp8(void *out, const void *q, const void *k_
  *                 key themselves (in place) and otherwise must not overlap an
  *                 input
  *   q_weight, k_weight  [D], fp32 when weight_f32 != 0, else dtype
- * Sums and products are fp32.  positions, slots and their errors, and
+ * Sums and products are fp32 (a row whose sum of squares leaves its range, with
+ * elements of 2^60 and more, comes out as zeros).  positions, slots and their errors, and
  * query == NULL with num_qo_heads == 0, as in pkv_rope_reshape_and_cache: a
  * token whose position is out of range is skipped (nothing of it is written).
  * Requirements: rotary_dim a multiple of 16, at most D; head sizes

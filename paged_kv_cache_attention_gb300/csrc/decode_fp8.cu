@@ -36,12 +36,13 @@
 // the same barrier.
 //
 // Measured (GB300): 64 sequences of 512..4096 tokens (uniform), 32/8 heads of 128: 59 us,
-// 5.1 TB/s, 76 % of a copy's rate (the bf16 cache takes 108 us); 8 of
-// 32K..128K, 64/8 heads of 64: 120 us, 82 %.  Half as long stages (twice the
+// 5.1 TB/s, 76 % of a copy's rate (the bf16 cache takes 108 us), 68 % over five
+// log-uniform draws, whose partitions are less even; one draw of 8 of 32K..128K, 64/8
+// heads of 64: 120 us, 82 %.  Half as long stages (twice the
 // warps) take 69 and 138 us, three or four of them in the ring 71 and 143, twice
 // as long ones 72 and 152; partitions of 1024 tokens 65 and 120.  What is
 // left is latency between dependent instructions at 2.5 warps per scheduler
-// (issue slots 39 % used, tensor pipe 22 %).
+// (issue slots 41 % used, tensor pipe 22 %).
 #include "pkv_fp8.cuh"
 
 namespace pkv {

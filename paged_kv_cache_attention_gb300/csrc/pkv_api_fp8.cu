@@ -200,9 +200,9 @@ pkv_status pkv_paged_decode_fp8(void *out, const void *q, const void *k_cache,
         // Longer ones while the SMs have more than eight full rounds of CTAs and the
         // longest sequence keeps eight partitions of the keys it attends (a window leaves
         // the last ones).  Share of a copy's rate with 512, 1024 and 1536, over five
-        // draws: 8 of 32K..128K tokens 83, 88 and 89 % (heads of 64: 68, 78
-        // and 80), 16 of 4K..32K 76, 79 and 70; fewer than eight, 128 of 0.5K..8K:
-        // 85, 86 and 83.  16 of 32K..128K with a window of 4K: 51, 58 and 45.
+        // draws: 8 of 32K..128K tokens 82, 87 and 89 % (heads of 64: 66, 77
+        // and 80), 16 of 4K..32K 75, 79 and 70; fewer than eight, 128 of 0.5K..8K:
+        // 85, 87 and 84.  16 of 32K..128K with a window of 4K: 51, 58 and 45.
         const int64_t span = window_left >= 0 && window_left < max_seqlen
                                  ? (int64_t)window_left + 1
                                  : max_seqlen;

@@ -169,7 +169,8 @@ __device__ __forceinline__ void pool_store(const PoolArgs &p, const PoolSlot &s,
 // one trip to memory covers them, the position, the slot and the weights.
 // Measured on 8448 tokens of 32 + 2 * 8 heads of 128 into bf16 pools (GB300,
 // 225 MB): 42 us, 79 % of a copy's rate.  Seven CTAs per SM and two q rows ahead
-// (uncapped and four rows: 56 us; one row: 46 us); two groups per token (each
+// (uncapped and four rows: 56 us; one row: 46 us; the cap costs the neox variant
+// 20 bytes of spills at its 72 registers); two groups per token (each
 // cos/sin row is loaded by fewer groups) take 42 us, four 44, eight 48.
 template <typename T, int LPR, bool FP8, bool NEOX>
 __global__ void __launch_bounds__(kThreads, sizeof(T) != 2 ? 4 : FP8 ? kCtas - 1 : kCtas)

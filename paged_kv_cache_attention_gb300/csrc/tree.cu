@@ -39,7 +39,7 @@
 // Warps: four softmax warps per row tile, one row per thread; a TMA warp, which
 // also works out the CTA's segments and hands them to the others through a
 // ring; an MMA warp; over 8-bit pools the warps that convert codes, K's beside V's
-// (one after the other: 173 us instead of 157 for 8 x 32 drafts over 24K).
+// (one after the other: 10 % more for 8 x 32 drafts over 24K).
 //   S = Q K^T -> TMEM; the softmax reads S twice (maximum, weights), writes P (16
 //   bits) over S; O += P V with P from TMEM.  O is rescaled only when a row's
 //   maximum has grown a lot.
@@ -53,22 +53,28 @@
 // behind the end are zeroed, and a V row with a non-finite value is zeroed too
 // and reaches, as NaN, only the rows that see it.
 //
+// P rounds to the operands' type: f16 over 8-bit pools, bf16 (half a step 2^-8) over
+// bf16 ones, as in prefill.cu and decode.cu; the sum of the weights is of those not
+// rounded.  Of the error against 64 bits, which the output's own rounding makes 0.0016
+// of the outputs' size, that leaves 0.0017 on short contexts and 0.0023 on 16K..32K.
+//
 // Measured (GB300, 32/8 heads of 128): 8 x 64 drafts over 16K..32K tokens of bf16
-// 184 us, 67 % of a copy's rate; 16 x 24 over 0.5K..8K of the 8-bit cache 72 us,
-// 27 %; 4 x 8 over 60..900 of bf16 16 us, mostly the latency of two kernels.
-// With one row tile and 32-token pages, 8 x 32 over 24K takes 136 us, 87 %.
+// 184 us in a replayed graph and 194 as calls, 67 and 64 % of a copy's rate; 16 x 24
+// over 0.5K..8K of the 8-bit cache 73 us, 27 %; 4 x 8 over 60..900 of bf16 16 us, mostly
+// the latency of two kernels.  With one row tile and 32-token pages, 8 x 32 over 24K
+// takes 137 us, 87 %.
 //   Two row tiles per CTA (X = 2, heads up to 128) when a request may have more
-// than 128 rows: 8 x 64 drafts over 24K 170 us (8-bit: 232) against 260 (273) with
+// than 128 rows: 8 x 64 drafts over 24K 175 us (8-bit: 242) against 255 (280) with
 // one, which reads K and V twice; 8 x 40 drafts, whose second tile is a quarter
-// full, 163 (216) against 253 (267).
+// full, 168 (225) against 249 (275).
 //   Slower: K and V on their way to L2 two tiles before their loads (70 -> 77 us,
 // 8-bit), fewer converted and more raw tiles (173 -> 198 us), eight converting
 // warps (short cases 73 -> 76 us, long ones 153 -> 149).
 //   What bounds it: with two row tiles 4 x 527 cycles of tensor work in about 4000
 // per key tile, the rest handing S, P and O between the warps; over 8-bit pools
 // the same hand-overs, the conversion's among them, about 3300 cycles per key
-// tile (8 x 32 drafts over 24K: 147 us; 126 without the softmax's arithmetic, 124
-// without the conversion's, 102 without either); and some 5 us per row group that
+// tile (8 x 32 drafts over 24K: 151 us; by a probe some 20 less without the softmax's
+// arithmetic, as many without the conversion's, 45 without either); and some 5 us per row group that
 // a CTA meets, for Q, the general tile and code that is fetched for the first time.
 #include "pkv_fp8.cuh"
 #include "pkv_tcgen05.cuh"
