@@ -494,8 +494,8 @@ PKV_API pkv_status pkv_gather_cache_fp8(void *key, void *value, const void *k_ca
  * paged_decode_fp8: pkv_paged_decode over the 8-bit cache: q and out are bf16,
  * everything else (masks, sink, ALiBi, partitions, lse, workspace of
  * pkv_paged_decode_workspace_size bytes for the same arguments) as there, but
- * for partition_size 0: the partition is chosen from the shapes (512 to 1536
- * tokens).  With max_seqlen within one partition the workspace may be NULL.
+ * for partition_size 0: the partition is chosen from the shapes and the window
+ * (512 to 1536 tokens).  With max_seqlen within one partition the workspace may be NULL.
  * k_scale and v_scale are 16-byte aligned.  Head sizes 64/80/96/112/128/256, at
  * most 16 query heads per kv head, max_seqlen at most 2^30.
  * Precision: scores, maxima, sums and outputs are fp32; q is held to 2^-39 of its
@@ -525,9 +525,9 @@ PKV_API pkv_status pkv_paged_decode_fp8(void *out, const void *q, const void *k_
  *   (then k_scale and v_scale are needed; else they are ignored).
  *   dtype         PKV_BF16 or PKV_F32, of query, key, value and the outputs
  *   *_stride      elements between tokens (heads are contiguous), as in
- *                 pkv_reshape_and_cache_fp8; query_out / key_out may be query /
- *                 key themselves (in place) and otherwise must not overlap an
- *                 input
+ *                 pkv_reshape_and_cache_fp8; query_out may be query, and
+ *                 key_out key or value, themselves (in place); otherwise they must
+ *                 not overlap one another or an input
  *   q_weight, k_weight  [D], fp32 when weight_f32 != 0, else dtype
  * Sums and products are fp32 (a row whose sum of squares leaves its range, with
  * elements of 2^60 and more, comes out as zeros).  positions, slots and their errors, and

@@ -799,14 +799,18 @@ def _rows_meet(tokens: int, a: int, step_a: int, len_a: int, b: int, step_b: int
     return False
 
 
+_SAME_ROWS = (("query_out", "query"), ("key_out", "key"), ("key_out", "value"))
+
+
 def _refuse_overlap(tokens: int, outs, ins) -> None:
     """Outputs (name, address, bytes between tokens, bytes of a row) overlap neither one
-    another nor an input, but that of their own name as that input itself."""
+    another nor an input, but that of their own name as that input itself, and key_out
+    value's rows likewise (a head's k and v are read before either is written)."""
     if _rows_meet(tokens, *outs[0][1:], *outs[1][1:]):
         raise ValueError(f"{outs[1][0]} must not overlap {outs[0][0]}")
     for out in outs:
         for row in ins:
-            if out[1:] == row[1:] and out[0].startswith(row[0]):
+            if out[1:] == row[1:] and (out[0], row[0]) in _SAME_ROWS:
                 continue  # in place
             if _rows_meet(tokens, *out[1:], *row[1:]):
                 raise ValueError(f"{out[0]} must not overlap {row[0]}")
@@ -1017,8 +1021,8 @@ def qk_norm_rope_reshape_and_cache(query, key, value, k_cache, v_cache, position
     Rows are bf16 or float32; a token's heads are contiguous and tokens may
     have any stride (slices of a fused projection).  The rotated rows go to
     query_out / key_out, or back in place when these are None; they may not
-    overlap one another or value, nor query or key but as these themselves.  With
-    k_scale and v_scale the pools are the 8-bit cache of reshape_and_cache_fp8, else
+    overlap one another or an input, but may be it: query_out query, key_out key or
+    value.  With k_scale and v_scale the pools are the 8-bit cache of reshape_and_cache_fp8, else
     pools of the rows' dtype.  query (with query_out and q_weight) may be None."""
     ty = _types()
     dev = _cuda_index("key", key)

@@ -35,7 +35,8 @@ def overlapping():
     x = fused()
     q, ko = one_buffer((0, HQ, ROW), (HQ * D - 16, HKV, ROW))
     yield dict(query=q, query_out=torch.zeros(T, HQ, D, dtype=BF16), key_out=ko)
-    yield shared(torch.zeros(T, HKV, D, dtype=BF16))              # key in place, over value
+    kv = torch.zeros(T + 1, HKV, D, dtype=BF16)
+    yield dict(key=kv[:-1], value=kv[1:])                         # key in place, over value
     yield dict(slices(x), key=x[:, HQ - 1:HQ + HKV - 1])          # query and key in place
     yield dict(slices(x), value=x[:, HQ + 1:HQ + HKV + 1])
     yield dict(slices(x), query_out=x[:, HKV:HQ + HKV], key_out=torch.zeros(T, HKV, D, dtype=BF16))
@@ -53,6 +54,8 @@ def apart():
     yield dict(slices(x), query_out=x[:, :HQ], key_out=x[:, HQ:HQ + HKV])
     kv = torch.zeros(T, HKV, D, dtype=BF16)
     yield dict(shared(kv), key_out=torch.zeros(T, HKV, D, dtype=BF16))
+    yield shared(kv)                                              # value's own rows
+    yield dict(value=kv, key_out=kv)
     q = fused(2 * T + 1, HQ)
     yield dict(query=q[T:2 * T], query_out=q[:T])
     qo, ko = one_buffer((0, HQ, HQ * D), (T * HQ * D, HKV, HKV * D))
@@ -69,7 +72,7 @@ def test_overlapping_rows_are_refused(lib, kw):  # noqa: F811
     assert not lib.calls
 
 
-@pytest.mark.parametrize("kw", list(apart()), ids=range(9))
+@pytest.mark.parametrize("kw", list(apart()), ids=range(11))
 def test_rows_apart_or_in_place_go_through(lib, kw):  # noqa: F811
     pkv.qk_norm_rope_reshape_and_cache(**dict(_norm_args(), **kw))
     assert lib.calls
