@@ -667,6 +667,9 @@ def _arg_vector(name, t, dtype, n: int, dev: int):
     _arg_shape(name, t, dtype, (n,), dev)
 
 
+_WIDEST = 2 ** 31 - 1  # a window that holds every key (lengths are at most 2^30)
+
+
 def _int32(name, value) -> int:
     """A host integer that the library takes in 32 bits (ctypes would cut it off)."""
     value = int(value)
@@ -986,7 +989,7 @@ def paged_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_s
     err = _error_word(dev_error, dev)
     scale = float(sm_scale) if sm_scale is not None else D ** -0.5
     max_seqlen = _int32("max_seqlen", max_seqlen)
-    window_left = _int32("window_left", window_left)
+    window_left = _int32("window_left", min(window_left, _WIDEST))
     partition_size = _int32("partition_size", partition_size)
     # one partition needs no workspace
     need = 0 if max_seqlen <= (partition_size or 512) else \
@@ -1143,7 +1146,7 @@ def paged_tree_attention(q, k_cache, v_cache, block_table, cu_seq_lens_q, cache_
     rows, words = tree_mask.shape
     max_seqlen_q = _int32("max_seqlen_q", max_seqlen_q)
     max_seqlen = _int32("max_seqlen", max_seqlen)
-    window_left = _int32("window_left", window_left)
+    window_left = _int32("window_left", min(window_left, _WIDEST))
     partition_size = _int32("partition_size", partition_size)
     _require(rows == total_q and 64 * words >= max_seqlen_q,
              "tree_mask must be [total_q, words] with words * 64 >= max_seqlen_q")
