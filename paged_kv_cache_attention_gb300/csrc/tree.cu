@@ -59,12 +59,12 @@
 // of the outputs' size, that leaves 0.0017 on short contexts and 0.0023 on 16K..32K.
 //
 // Measured (GB300, 32/8 heads of 128): 8 x 64 drafts over 16K..32K tokens of bf16
-// 184 us in a replayed graph and 194 as calls, 67 and 64 % of a copy's rate; 16 x 24
-// over 0.5K..8K of the 8-bit cache 73 us, 27 %; 4 x 8 over 60..900 of bf16 16 us, mostly
+// 185 us in a replayed graph and 194 as calls, 67 and 64 % of a copy's rate; 16 x 24
+// over 0.5K..8K of the 8-bit cache 72 us, 27 %; 4 x 8 over 60..900 of bf16 16 us, mostly
 // the latency of two kernels.  With one row tile and 32-token pages, 8 x 32 over 24K
 // takes 137 us, 87 %.
 //   Two row tiles per CTA (X = 2, heads up to 128) when a request may have more
-// than 128 rows: 8 x 64 drafts over 24K 175 us (8-bit: 242) against 255 (280) with
+// than 128 rows: 8 x 64 drafts over 24K 175 us (8-bit: 239) against 255 (280) with
 // one, which reads K and V twice; 8 x 40 drafts, whose second tile is a quarter
 // full, 168 (225) against 249 (275).
 //   Slower: K and V on their way to L2 two tiles before their loads (70 -> 77 us,
@@ -105,7 +105,7 @@ constexpr float kLazySum = 60.f;
 // exact, but f16 weights count from the tile's largest scale, which the row's
 // weightiest keys may not have: they lose kSpreadV of the 31 bits above.  8 x 32
 // drafts over 24K take 151 us where no tile is wider (scales that vary by 2^N(0, 1)
-// from row to row), 250 where 95 % of V's tiles are (2^N(0, 2)), and 497 where V's all
+// from row to row), 252 where 95 % of V's tiles are (2^N(0, 2)), and 500 where V's all
 // are and half of K's (2^N(0, 3); K's take the general code).
 constexpr int kSpreadK = 15, kSpreadV = 8;
 
@@ -1005,11 +1005,17 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
             const bool fix = j < full_lo || j >= full_hi;
             alive = wait_warp(bar(C::B_INFO + jn % kInfo), (jn / kInfo) & 1u, p.dev_error,
                               s_abort);
-            uint32_t kb = 0;                 // K's scale: there before S is
+            // the scales, on their way before S is there (heads of 64: 121 us instead of 118
+            // for 8 x 32 drafts over 16K..24K when V's is waited for where it is used)
+            uint32_t kb = 0, vb = 0;
             if constexpr (KV8) {
-                alive = alive && wait_warp(bar(C::B_KFACT + (jn & 3)), (jn >> 2) & 1u,
-                                           p.dev_error, s_abort);
+                alive = alive &&
+                        wait_warp(bar(C::B_KFACT + (jn & 3)), (jn >> 2) & 1u, p.dev_error,
+                                  s_abort) &&
+                        wait_warp(bar(C::B_VFACT + (jn & 1)), (jn >> 1) & 1u, p.dev_error,
+                                  s_abort);
                 kb = *reinterpret_cast<volatile uint32_t *>(s_byte + (jn & 3));
+                vb = *reinterpret_cast<volatile uint32_t *>(s_byte + 4 + (jn & 1));
             }
             alive = alive && wait_warp(bar(C::B_SFULL + (n & 1)), (n >> 1) & 1u, p.dev_error,
                                        s_abort);
@@ -1183,10 +1189,6 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
                 float wt = mt, vexp = 0.f;  // the largest weight's exponent; V's scale in it
                 bool by_key = false;
                 if constexpr (KV8) {
-                    alive = wait_warp(bar(C::B_VFACT + (jn & 1)), (jn >> 1) & 1u, p.dev_error,
-                                      s_abort);
-                    if (!alive) break;
-                    const uint32_t vb = *reinterpret_cast<volatile uint32_t *>(s_byte + 4 + (jn & 1));
                     vexp = (float)((int)(vb & 255u) - 127);
                     wt = mt + vexp - kWeightExp;
                     by_key = vb > 255u;
