@@ -36,7 +36,13 @@
  *   pkv_qk_norm_rope_reshape_and_cache  RMS norm of the q and k heads, rotary
  *                          embedding and cache write in one pass;
  *   pkv_paged_tree_attention  attention of a tree of drafted tokens per request
- *                          over its pages (bf16 or 8-bit).
+ *                          over its pages (bf16 or 8-bit);
+ *   pkv_update_block_tables  pages taken and given back, slots, positions and
+ *                          offsets of a step's tokens from the requests' lengths;
+ *   pkv_update_page_bounds, pkv_select_pages, pkv_paged_sparse_attention
+ *                          a sparse step: the least and the largest key of every
+ *                          page, the pages with the largest possible scores for
+ *                          each query, and the attention over these pages alone.
  *
  * What the attention computes (FlashInfer sink_attention_reference.py,
  * sink_softmax and sink_attention_unified): for request r, query row i and
@@ -109,7 +115,7 @@ typedef enum pkv_status {
     PKV_ERR_CUDA = 4,        /* a CUDA call failed (launch, tensor-map encode, sync) */
     PKV_ERR_OUT_OF_RANGE = 5, /* pkv_get_device_error: the kernels found device
                                  metadata out of range (PKV_DEVERR_BLOCK_ID, _SLOT,
-                                 _SEQLEN or _POSITION) and skipped it */
+                                 _SEQLEN, _POSITION or _NO_BLOCKS) and skipped it */
     PKV_ERR_TIMEOUT = 6      /* pkv_get_device_error: a bounded pipeline wait gave up
                                 (PKV_DEVERR_TIMEOUT); the outputs of that call are
                                 not valid */
@@ -132,6 +138,7 @@ typedef enum pkv_layout { PKV_NHD = 0, PKV_HND = 1 } pkv_layout;
                                   cu_seq_lens offset outside the rows of q / k */
 #define PKV_DEVERR_TIMEOUT 8u  /* a bounded pipeline wait gave up */
 #define PKV_DEVERR_POSITION 16u /* a rotary position outside [0, max_position) */
+#define PKV_DEVERR_NO_BLOCKS 32u /* update_block_tables: fewer free pages than the lengths need */
 
 /* Description of the two paged pools (same shape and dtype). */
 typedef struct pkv_cache_desc {
@@ -160,9 +167,9 @@ PKV_API int pkv_version(void);
  *
  * Returns PKV_OK when no bit is set; PKV_ERR_TIMEOUT when PKV_DEVERR_TIMEOUT
  * is set; otherwise PKV_ERR_OUT_OF_RANGE when a metadata bit is set (a block
- * id, slot, length or position outside its range: the kernels skipped the
- * offending page, row or token, so the outputs that depend on it are not the
- * attention the caller meant); PKV_ERR_INVALID_ARG for a NULL dev_error;
+ * id, slot, length or position outside its range, or too few free pages: the
+ * kernels skipped the offending page, row, token or step, so the outputs that
+ * depend on it are not the attention the caller meant); PKV_ERR_INVALID_ARG for a NULL dev_error;
  * PKV_ERR_CUDA when the synchronisation or the copy fails.
  *
  * The pages put the cache write before the attention in one forward
@@ -602,6 +609,132 @@ PKV_API pkv_status pkv_paged_tree_attention(
     const int32_t *tree_depth, const float *sink, const float *alibi_slopes, int batch,
     int num_qo_heads, int window_left, float sm_scale, int partition_size, float *lse_out,
     void *workspace, size_t workspace_bytes, int32_t *dev_error, void *stream);
+
+/*
+ * update_block_tables: the bookkeeping of a step, on the device.  Request r goes
+ * from old_seqlens[r] cached tokens to new_seqlens[r] ([batch] int32):
+ *   longer   its table row gets the pages that positions old .. new - 1 need beyond
+ *            ceil(old / block_size); they are its new tokens of this step
+ *   shorter  (drafts that were not accepted; 0: a request that is done) the pages
+ *            beyond ceil(new / block_size) are given back, their entries become -1
+ *   free_blocks  [num_blocks] int32, a stack of the free pages of a pool of
+ *            num_blocks pages; num_free [1] int32 its height (free_blocks[num_free
+ *            - 1] is the top).  The pages given back are stacked first, the first
+ *            request's first page topmost; then pages are taken off the top in the
+ *            order of requests and positions.  So giving back what was just taken
+ *            restores the stack.  Entries above the height keep what they held
+ *   block_table  [batch, max_blocks_per_seq] int32, in place
+ * and the arrays that the other calls take:
+ *   cu_seq_lens_q  [batch + 1] int32: prefix sums of max(new - old, 0)
+ *   cu_seq_lens_k  [batch + 1] int32: prefix sums of new
+ *   slot_mapping, positions  [num_rows] int64: of token i of request r at row
+ *            cu_seq_lens_q[r] + i: position old + i, and its slot; rows behind the
+ *            last token (padding of a captured step) get slot -1 and position 0
+ * All or nothing: if the free pages do not suffice (PKV_DEVERR_NO_BLOCKS), a length
+ * is negative or beyond max_blocks_per_seq * block_size, the tokens do not fit
+ * num_rows or the new lengths' sum 32 bits (PKV_DEVERR_SEQLEN), or num_free or a
+ * page id that is moved or goes on being filled is out of range, or there are more
+ * pages than the pool has (PKV_DEVERR_BLOCK_ID), nothing is moved, all offsets are 0
+ * and all slots -1, so that the step's other calls do nothing.
+ * The lengths are not changed; tables, stack and outputs must not overlap.
+ * Requirements: block_size 16 or 32, batch at most 16384, max_blocks_per_seq *
+ * block_size and num_rows at most 2^30.
+ */
+PKV_API pkv_status pkv_update_block_tables(int32_t *block_table, int max_blocks_per_seq,
+                                           const int32_t *old_seqlens, const int32_t *new_seqlens,
+                                           int batch, int32_t *free_blocks, int64_t num_blocks,
+                                           int32_t *num_free, int block_size,
+                                           int64_t *slot_mapping, int64_t *positions,
+                                           int num_rows, int32_t *cu_seq_lens_q,
+                                           int32_t *cu_seq_lens_k, int32_t *dev_error,
+                                           void *stream);
+
+/*
+ * update_page_bounds: after a cache write, the bounds of every page it wrote to.
+ * For a page and kv head with keys k[0 .. n-1]: lo_d and hi_d, the least and the
+ * largest k[., d]; e the least exponent >= -126 with |lo_d|, |hi_d| <= 127 * 2^e;
+ *   page_bounds   [num_blocks, num_kv_heads, 2, head_dim] int8: floor(lo_d * 2^-e),
+ *                 then ceil(hi_d * 2^-e); times 2^e they bound every key
+ *   bounds_scale  [num_blocks, num_kv_heads] uint8: e + 127; 255 (and codes 0) for a
+ *                 page with a key that is not finite
+ *   slot_mapping  [num_tokens] int64, as given to the write (negative: skipped;
+ *                 beyond the pool: skipped, PKV_DEVERR_SLOT).  A page's n is the
+ *                 offset of its last token there plus one: rows before it are
+ *                 read from the pool whoever wrote them.  The tokens of one page
+ *                 come in ascending order with fewer than 32 others between two
+ *                 of them (as update_block_tables orders them); else two of them
+ *                 race for its bounds
+ *   k_scale       the scales of an 8-bit pool (cache.dtype PKV_E4M3); else ignored
+ * Pools bf16 or 8-bit, NHD or HND; head sizes 64/80/96/112/128/256; block_size 16 or
+ * 32; num_tokens at most 2^22; k_cache and page_bounds 16-byte aligned.
+ */
+PKV_API pkv_status pkv_update_page_bounds(const void *k_cache, const uint8_t *k_scale,
+                                          pkv_cache_desc cache, int8_t *page_bounds,
+                                          uint8_t *bounds_scale, const int64_t *slot_mapping,
+                                          int64_t num_tokens, int32_t *dev_error, void *stream);
+
+/*
+ * select_pages: for every query row and kv head, the top_k pages of its request on
+ * which a key could score highest.  Rows as in paged_sparse_attention: with
+ * cu_seq_lens_q NULL row b is the one query of request b, at position
+ * cache_seqlens[b] - 1; else request r's queries are rows cu_seq_lens_q[r] .. and
+ * the last q_len positions of cache_seqlens[r].  Row t then has n = ceil((its
+ * position + 1) / block_size) pages.  The score of page p (bounds lo, hi, byte):
+ *   for query head h of the group, 2^E <= max_d |q_d| < 2^(E+1), e_h = max(E, -112) - 7,
+ *   c_d = rint(q_d * 2^-e_h);  I_h = sum_d max(c_d, 0) hi_d + min(c_d, 0) lo_d
+ *   score = max over h of I_h * 2^(e_h + byte - 127), rounded to fp32
+ * which is exact up to that rounding, so a list depends on nothing but its row's inputs.
+ * byte 255: +inf.  A head whose q is not finite is left out (no head: all alike).  The
+ * first num_first and the last num_recent (>= 1: the query's own) pages are always
+ * taken; then the highest scores, equal ones from the lowest page.
+ *   pages         [total_q, num_kv_heads, top_k] int32: the chosen page numbers of
+ *                 the request (columns of its table row), ascending, then -1; all n
+ *                 if n <= top_k.  Rows of no request are not touched
+ *   q             [total_q, num_qo_heads, head_dim] bf16, contiguous
+ *   page_bounds, bounds_scale  of update_page_bounds (num_blocks pages)
+ *   block_table, cache_seqlens  of batch requests; max_seqlen a host int >= every
+ *                 length
+ * A page id out of range makes its page the last choice (PKV_DEVERR_BLOCK_ID); a
+ * length out of range is clipped (PKV_DEVERR_SEQLEN).
+ * Requirements: num_first + num_recent <= top_k <= 16384; at most 16 query heads per
+ * kv head; total_q at most 2^24; max_seqlen at most 2^30 and 393216 pages; head
+ * sizes and block sizes as update_page_bounds; q and page_bounds 16-byte aligned.
+ */
+PKV_API pkv_status pkv_select_pages(int32_t *pages, int top_k, const void *q,
+                                    const int8_t *page_bounds, const uint8_t *bounds_scale,
+                                    int64_t num_blocks, int block_size, int num_kv_heads,
+                                    int head_dim, const int32_t *block_table,
+                                    int max_blocks_per_seq, const int32_t *cache_seqlens,
+                                    int max_seqlen, const int32_t *cu_seq_lens_q, int batch,
+                                    int total_q, int num_qo_heads, int num_first, int num_recent,
+                                    int32_t *dev_error, void *stream);
+
+/*
+ * paged_sparse_attention: row t attends, for each kv head g, to the keys of the pages
+ * pages[t, g, :] of its request up to and with its own position; softmax, sink and
+ * lse as in pkv_paged_decode.
+ *   out, q        [total_q, num_qo_heads, head_dim] bf16, contiguous
+ *   pages         [total_q, num_kv_heads, top_k] int32, as select_pages writes it
+ *                 or from any other choice: page numbers of the row's request,
+ *                 strictly ascending.  The list ends at its first negative entry, and
+ *                 (PKV_DEVERR_BLOCK_ID) at an entry that is not above the one before
+ *                 it or not a page of the row
+ *   cu_seq_lens_q, cache_seqlens, batch, total_q  as in select_pages.  Rows of no
+ *                 request are not touched; a row whose position is negative, or with
+ *                 an empty list, keeps no key
+ *   cache.dtype   PKV_BF16 (k_scale, v_scale ignored) or PKV_E4M3 (the 8-bit cache,
+ *                 scales 16-byte aligned)
+ * Precision: scores, sums and outputs fp32; a key's weight rounds to bf16 over bf16
+ * pools, and as in pkv_paged_decode_fp8 over 8-bit pools.
+ * Requirements: head sizes 64/80/96/112/128/256, block_size 16 or 32, at most 16
+ * query heads per kv head, top_k at most 16384, total_q at most 2^24.
+ */
+PKV_API pkv_status pkv_paged_sparse_attention(
+    void *out, const void *q, const void *k_cache, const void *v_cache, const uint8_t *k_scale,
+    const uint8_t *v_scale, pkv_cache_desc cache, const int32_t *block_table,
+    int max_blocks_per_seq, const int32_t *cache_seqlens, const int32_t *cu_seq_lens_q, int batch,
+    int total_q, const int32_t *pages, int top_k, const float *sink, int num_qo_heads,
+    float sm_scale, float *lse_out, int32_t *dev_error, void *stream);
 
 #ifdef __cplusplus
 }

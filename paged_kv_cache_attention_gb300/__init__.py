@@ -29,6 +29,11 @@ Operations (same names as the C ABI):
     rotary embedding and the cache write (bf16, float32 or 8-bit pools) fused;
   * ``paged_tree_attention`` -- attention of a tree of up to 256 drafted tokens
     per request over its pages (bf16 or 8-bit), for speculative decoding;
+  * ``update_block_tables`` -- pages taken and given back, slots, positions and
+    offsets of a step's tokens from the requests' lengths, on the GPU;
+  * ``update_page_bounds``, ``select_pages`` and ``paged_sparse_attention`` -- a
+    sparse step: 8-bit bounds of every page's keys, for each query the pages on
+    which a key could score highest, and the attention over these pages alone;
   * ``minference_prefill`` -- MInference's vertical + slash sparse prefill of
     one sequence (nano-vllm minference.py): pattern estimate, top-k, then
     attention over the kept keys.
@@ -56,8 +61,9 @@ __all__ = [
     "reshape_and_cache_fp8", "gather_cache_fp8", "paged_decode_fp8",
     "qk_norm_rope_reshape_and_cache", "paged_tree_attention",
     "paged_tree_attention_workspace_size",
+    "update_block_tables", "update_page_bounds", "select_pages", "paged_sparse_attention",
     "DEVERR_BLOCK_ID", "DEVERR_SLOT", "DEVERR_SEQLEN", "DEVERR_TIMEOUT", "DEVERR_POSITION",
-    "EXPORTED_SYMBOLS",
+    "DEVERR_NO_BLOCKS", "EXPORTED_SYMBOLS",
 ]
 
 PKV_F32 = 0
@@ -68,6 +74,7 @@ DEVERR_SLOT = 2
 DEVERR_SEQLEN = 4
 DEVERR_TIMEOUT = 8
 DEVERR_POSITION = 16
+DEVERR_NO_BLOCKS = 32
 
 EXPORTED_SYMBOLS = (
     "pkv_status_string", "pkv_version", "pkv_reshape_and_cache",
@@ -79,6 +86,8 @@ EXPORTED_SYMBOLS = (
     "pkv_reshape_and_cache_fp8", "pkv_gather_cache_fp8", "pkv_paged_decode_fp8",
     "pkv_qk_norm_rope_reshape_and_cache", "pkv_paged_tree_attention_workspace_size",
     "pkv_paged_tree_attention",
+    "pkv_update_block_tables", "pkv_update_page_bounds", "pkv_select_pages",
+    "pkv_paged_sparse_attention",
 )
 
 
@@ -182,6 +191,17 @@ def load_library(path: Optional[str] = None):
             P, P, P, P, P, P, CacheDesc, P, i32, P, P, i32, i32, i32, P, i32, P, P, P, i32, i32,
             i32, f32, i32, P, P, sz, P, P]
         lib.pkv_paged_tree_attention.restype = i32
+        lib.pkv_update_block_tables.argtypes = [P, i32, P, P, i32, P, i64, P, i32, P, P, i32, P, P,
+                                                P, P]
+        lib.pkv_update_block_tables.restype = i32
+        lib.pkv_update_page_bounds.argtypes = [P, P, CacheDesc, P, P, P, i64, P, P]
+        lib.pkv_update_page_bounds.restype = i32
+        lib.pkv_select_pages.argtypes = [P, i32, P, P, P, i64, i32, i32, i32, P, i32, P, i32, P, i32,
+                                         i32, i32, i32, i32, P, P]
+        lib.pkv_select_pages.restype = i32
+        lib.pkv_paged_sparse_attention.argtypes = [
+            P, P, P, P, P, P, CacheDesc, P, i32, P, P, i32, i32, P, i32, P, i32, f32, P, P, P]
+        lib.pkv_paged_sparse_attention.restype = i32
         _lib = lib
         return lib
 
@@ -821,7 +841,7 @@ def _refuse_overlap(tokens: int, outs, ins) -> None:
 
 class _Types:
     """torch and the dtypes the checks compare with, looked up once."""
-    torch = bf16 = f32 = i32 = i64 = u8 = e4m3 = None
+    torch = bf16 = f32 = i32 = i64 = u8 = i8 = e4m3 = None
     codes = {}                  # pkv_dtype of the rows' dtypes
     device = raw_stream = None  # the current device, and a device's current stream handle
 
@@ -831,6 +851,7 @@ def _types():
         import torch
         _Types.bf16, _Types.f32, _Types.i32 = torch.bfloat16, torch.float32, torch.int32
         _Types.i64, _Types.u8, _Types.e4m3 = torch.int64, torch.uint8, torch.float8_e4m3fn
+        _Types.i8 = torch.int8
         _Types.codes = {torch.bfloat16: PKV_BF16, torch.float32: PKV_F32}
         _Types.device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         _Types.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
@@ -1173,4 +1194,214 @@ def paged_tree_attention(q, k_cache, v_cache, block_table, cu_seq_lens_q, cache_
     out, st = _on_stream(dev, stream, call)
     if st:
         _check("pkv_paged_tree_attention", st)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# a sparse decode step
+# ---------------------------------------------------------------------------
+
+def _disjoint(tensors) -> None:
+    """Refuses (name, tensor) pairs of which two share memory (all contiguous)."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name)
+                   for name, t in tensors if t.numel())
+    for (_, end, a), (start, _, b) in zip(spans, spans[1:]):
+        if start < end:
+            raise ValueError(f"{b} must not overlap {a}")
+
+
+def update_block_tables(block_table, old_seqlens, new_seqlens, free_blocks, num_free,
+                        block_size: int, num_rows: int, slot_mapping=None, positions=None,
+                        cu_seq_lens_q=None, cu_seq_lens_k=None, dev_error=None, stream=None):
+    """The bookkeeping of a step on the GPU: request r goes from old_seqlens[r] to
+    new_seqlens[r] cached tokens ([B] int32).  Returns (slot_mapping [num_rows] int64,
+    positions [num_rows] int64, cu_seq_lens_q [B+1] int32, cu_seq_lens_k [B+1] int32)
+    of the new tokens, those of request r at rows cu_seq_lens_q[r] ..; rows behind the
+    last one have slot -1 and position 0.
+
+    block_table [B, max_blocks] int32, free_blocks [num_blocks] int32 (a stack of the
+    pool's free pages) and num_free [1] int32 (its height) are changed in place:
+    requests that grow take pages off the stack, requests that shrink (0: done) give
+    theirs back, which are there to be taken in the same step.  All or nothing: with
+    too few free pages (DEVERR_NO_BLOCKS) or metadata out of range nothing is moved,
+    all slots are -1 and all offsets 0."""
+    ty = _types()
+    dev = _cuda_index("block_table", block_table)
+    _arg("block_table", block_table, ty.i32, 2, dev)
+    B, max_blocks = block_table.shape
+    _arg_vector("old_seqlens", old_seqlens, ty.i32, B, dev)
+    _arg_vector("new_seqlens", new_seqlens, ty.i32, B, dev)
+    _arg("free_blocks", free_blocks, ty.i32, 1, dev)
+    _arg_vector("num_free", num_free, ty.i32, 1, dev)
+    num_rows, block_size = _int32("num_rows", num_rows), _int32("block_size", block_size)
+    _require(num_rows >= 0, "num_rows must not be negative")
+    if slot_mapping is not None:
+        _arg_vector("slot_mapping", slot_mapping, ty.i64, num_rows, dev)
+    if positions is not None:
+        _arg_vector("positions", positions, ty.i64, num_rows, dev)
+    if cu_seq_lens_q is not None:
+        _arg_vector("cu_seq_lens_q", cu_seq_lens_q, ty.i32, B + 1, dev)
+    if cu_seq_lens_k is not None:
+        _arg_vector("cu_seq_lens_k", cu_seq_lens_k, ty.i32, B + 1, dev)
+    err = _error_word(dev_error, dev)
+    given = [(n, t) for n, t in (
+        ("block_table", block_table), ("free_blocks", free_blocks), ("num_free", num_free),
+        ("slot_mapping", slot_mapping), ("positions", positions),
+        ("cu_seq_lens_q", cu_seq_lens_q), ("cu_seq_lens_k", cu_seq_lens_k)) if t is not None]
+    _disjoint(given + [("old_seqlens", old_seqlens)])
+    _disjoint(given + [("new_seqlens", new_seqlens)])
+    lib = load_library()
+
+    def call(handle):
+        empty, device = ty.torch.empty, block_table.device
+        slots = empty(num_rows, dtype=ty.i64, device=device) if slot_mapping is None else slot_mapping
+        pos = empty(num_rows, dtype=ty.i64, device=device) if positions is None else positions
+        cuq = empty(B + 1, dtype=ty.i32, device=device) if cu_seq_lens_q is None else cu_seq_lens_q
+        cuk = empty(B + 1, dtype=ty.i32, device=device) if cu_seq_lens_k is None else cu_seq_lens_k
+        return (slots, pos, cuq, cuk), lib.pkv_update_block_tables(
+            block_table.data_ptr(), max_blocks, old_seqlens.data_ptr(), new_seqlens.data_ptr(), B,
+            free_blocks.data_ptr(), free_blocks.shape[0], num_free.data_ptr(), block_size,
+            slots.data_ptr(), pos.data_ptr(), num_rows, cuq.data_ptr(), cuk.data_ptr(), err, handle)
+    outs, st = _on_stream(dev, stream, call)
+    if st:
+        _check("pkv_update_block_tables", st)
+    return outs
+
+
+def _bounds(page_bounds, bounds_scale, dev: int):
+    """Checks the bounds of a pool's pages; returns (num_blocks, num_kv_heads, head_dim)."""
+    ty = _types()
+    _arg("page_bounds", page_bounds, ty.i8, 4, dev)
+    nb, hkv, two, d = page_bounds.shape
+    _require(two == 2, "page_bounds must be [num_blocks, num_kv_heads, 2, head_dim]")
+    _arg_shape("bounds_scale", bounds_scale, ty.u8, (nb, hkv), dev)
+    return nb, hkv, d
+
+
+def update_page_bounds(k_cache, page_bounds, bounds_scale, slot_mapping, k_scale=None,
+                       dev_error=None, stream=None, layout: str = "NHD") -> None:
+    """The bounds of every page that a cache write at slot_mapping [T] (int64, negative =
+    skipped) has written to, from the keys in k_cache (bf16, or the 8-bit cache with
+    k_scale): page_bounds [num_blocks, Hkv, 2, D] int8 (the least and the largest key of
+    each channel, rounded outward) and bounds_scale [num_blocks, Hkv] uint8 (E8M0 bytes;
+    255: a key that is not finite) are changed in place.  The tokens of a page come in
+    ascending order, as update_block_tables orders them; rows of the page before its last
+    token here count as written."""
+    ty = _types()
+    dev = _cuda_index("k_cache", k_cache)
+    if k_scale is None:
+        desc = _pools(k_cache, k_cache, None, None, ty.bf16, layout, dev)
+    else:
+        desc = _fp8_pools(k_cache, k_cache, k_scale, k_scale, layout, dev)
+    nb, hkv, d = _bounds(page_bounds, bounds_scale, dev)
+    _require((nb, hkv, d) == (desc.num_blocks, desc.num_kv_heads, desc.head_dim),
+             "page_bounds must be [num_blocks, num_kv_heads, 2, head_dim] of the cache")
+    _arg("slot_mapping", slot_mapping, ty.i64, 1, dev)
+    err = _error_word(dev_error, dev)
+    lib = load_library()
+
+    def call(handle):
+        return lib.pkv_update_page_bounds(
+            k_cache.data_ptr(), _ptr(k_scale), desc, page_bounds.data_ptr(),
+            bounds_scale.data_ptr(), slot_mapping.data_ptr(), slot_mapping.shape[0], err, handle)
+    st = _on_stream(dev, stream, call)
+    if st:
+        _check("pkv_update_page_bounds", st)
+
+
+def _rows(q, head_dim: int, block_table, cache_seqlens, cu_seq_lens_q, dev: int):
+    """Checks the queries and their requests; returns (total_q, Hq, batch, max_blocks)."""
+    ty = _types()
+    _arg("q", q, ty.bf16, 3, dev)
+    total_q, Hq, D = q.shape
+    _require(D == head_dim, "head_dim of q and cache differ")
+    _arg("cache_seqlens", cache_seqlens, ty.i32, 1, dev)
+    B = cache_seqlens.shape[0]
+    _arg("block_table", block_table, ty.i32, 2, dev)
+    rows, max_blocks = block_table.shape
+    _require(rows == B, "block_table must have one row per request")
+    if cu_seq_lens_q is not None:
+        _arg_vector("cu_seq_lens_q", cu_seq_lens_q, ty.i32, B + 1, dev)
+    else:
+        _require(total_q == B, "without cu_seq_lens_q there is one query per request")
+    return total_q, Hq, B, max_blocks
+
+
+def select_pages(q, page_bounds, bounds_scale, block_table, cache_seqlens, max_seqlen: int,
+                 top_k: int, block_size: int, num_first: int = 1, num_recent: int = 1,
+                 cu_seq_lens_q=None, pages=None, dev_error=None, stream=None):
+    """For every query and kv head the top_k pages of its request on which a key could
+    score highest by the bounds of update_page_bounds (the highest over the group's
+    heads); returns pages [total_q, Hkv, top_k] int32, ascending page numbers of the
+    request, -1 behind them.
+
+    q: [total_q, Hq, D] bf16, one query per request, or with cu_seq_lens_q ([B+1]
+    int32) the last queries of each; block_table [B, max_blocks] and cache_seqlens [B]
+    int32 (with the queries' own tokens); max_seqlen: host int >= every length.  The
+    first num_first and the last num_recent (at least 1: a query's own) pages are always
+    taken, equal scores from the lowest page."""
+    ty = _types()
+    dev = _cuda_index("q", q)
+    nb, hkv, d = _bounds(page_bounds, bounds_scale, dev)
+    total_q, Hq, B, max_blocks = _rows(q, d, block_table, cache_seqlens, cu_seq_lens_q, dev)
+    max_seqlen, top_k = _int32("max_seqlen", max_seqlen), _int32("top_k", top_k)
+    block_size = _int32("block_size", block_size)
+    num_first, num_recent = _int32("num_first", num_first), _int32("num_recent", num_recent)
+    _require(top_k > 0, "top_k must be positive")
+    shape = (total_q, hkv, top_k)
+    if pages is not None:
+        _arg_shape("pages", pages, ty.i32, shape, dev)
+    err = _error_word(dev_error, dev)
+    lib = load_library()
+
+    def call(handle):
+        out = ty.torch.empty(shape, dtype=ty.i32, device=q.device) if pages is None else pages
+        return out, lib.pkv_select_pages(
+            out.data_ptr(), top_k, q.data_ptr(), page_bounds.data_ptr(), bounds_scale.data_ptr(),
+            nb, block_size, hkv, d, block_table.data_ptr(), max_blocks, cache_seqlens.data_ptr(),
+            max_seqlen, _ptr(cu_seq_lens_q), B, total_q, Hq, num_first, num_recent, err, handle)
+    out, st = _on_stream(dev, stream, call)
+    if st:
+        _check("pkv_select_pages", st)
+    return out
+
+
+def paged_sparse_attention(q, k_cache, v_cache, block_table, cache_seqlens, pages,
+                           cu_seq_lens_q=None, k_scale=None, v_scale=None, sink=None,
+                           sm_scale: Optional[float] = None, out=None, lse=None, dev_error=None,
+                           stream=None, layout: str = "NHD"):
+    """Attention of every query over its list of pages; returns out [total_q, Hq, D].
+
+    q [total_q, Hq, D] bf16, block_table, cache_seqlens and cu_seq_lens_q as in
+    select_pages; pages [total_q, Hkv, top_k] int32, for each kv head strictly ascending
+    page numbers of the request, -1 behind them (of select_pages, or any other choice).
+    A query sees the keys of these pages up to its own position.  Pools are bf16, or the
+    8-bit cache when k_scale and v_scale are given; sink, lse ([total_q, Hq] float32) and
+    layout as paged_decode."""
+    ty = _types()
+    dev = _cuda_index("q", q)
+    if k_scale is None and v_scale is None:
+        desc = _pools(k_cache, v_cache, None, None, ty.bf16, layout, dev)
+    else:
+        desc = _fp8_pools(k_cache, v_cache, k_scale, v_scale, layout, dev)
+    total_q, Hq, B, max_blocks = _rows(q, desc.head_dim, block_table, cache_seqlens,
+                                       cu_seq_lens_q, dev)
+    _arg("pages", pages, ty.i32, 3, dev)
+    top_k = pages.shape[2]
+    _arg_shape("pages", pages, ty.i32, (total_q, desc.num_kv_heads, top_k), dev)
+    _attention_extras(sink, None, out, lse, q, total_q, Hq, dev)
+    err = _error_word(dev_error, dev)
+    scale = float(sm_scale) if sm_scale is not None else desc.head_dim ** -0.5
+    lib = load_library()
+
+    def call(handle):
+        o = ty.torch.empty_like(q) if out is None else out
+        return o, lib.pkv_paged_sparse_attention(
+            o.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale),
+            _ptr(v_scale), desc, block_table.data_ptr(), max_blocks, cache_seqlens.data_ptr(),
+            _ptr(cu_seq_lens_q), B, total_q, pages.data_ptr(), top_k, _ptr(sink), Hq, scale,
+            _ptr(lse), err, handle)
+    out, st = _on_stream(dev, stream, call)
+    if st:
+        _check("pkv_paged_sparse_attention", st)
     return out

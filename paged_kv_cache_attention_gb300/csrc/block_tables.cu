@@ -1,0 +1,237 @@
+// block_tables.cu -- block tables, slots, positions and offsets of a step's tokens
+// from the requests' lengths (the bookkeeping before a cache write: vLLM
+// attention.py, InputMetadata's slot_mapping and block_tables; the placement of
+// transformers docs "paged_attention", decode path).
+//
+// Request r goes from old to new tokens: have = ceil(old / bs), want = ceil(new /
+// bs).  Released pages (entries want .. have - 1 of shrinking requests) are R in
+// request order, taken ones (have .. want - 1) A.  The free pages are a stack of
+// height F, the released ones on top of it with the first of them topmost:
+//   page j that is taken = released[j]                 j < R
+//                          free[F - 1 - (j - R)]       else
+//   free[F + R - 1 - i]  = released[i]                 i >= A
+// so one index i over max(A, R) says both what is read and where it goes: an
+// entry has one reader, which also clears it, and reads and writes of the stack
+// never meet.  Giving back the pages just taken restores the stack.
+//
+// Nothing but the launch and a few dependent loads bounds it (12 bytes per page
+// moved, 16 per token): one cluster of eight CTAs, each with the prefix sums of
+// all requests in its own shared memory, and cluster barriers between check,
+// tables and rows, in place of a launch for each.  Rows beyond kRowsHere take a
+// second launch over all SMs.
+#include "pkv_sparse.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kCluster = 8;
+constexpr int kRowsHere = 16384;
+constexpr int kRowThreads = 256;
+constexpr int kRowsPerCta = 2048;
+
+// Largest r in [0, n) with cu[r] <= i (cu[0] = 0 <= i): the request of item i.
+__device__ __forceinline__ int find(const int32_t *cu, int n, int i) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cu[mid] <= i)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// Slot and position of row t (table entries from L2: another SM may have written them).
+__device__ __forceinline__ void write_row(const TableParams &p, const int32_t *cu, int t,
+                                          int total) {
+    int64_t slot = -1, pos = 0;
+    if (t < total) {
+        const int r = find(cu, p.batch, t);
+        const int x = p.old_len[r] + t - cu[r];
+        const int id = __ldcg(p.block_table + (int64_t)r * p.max_blocks_per_seq +
+                              (x >> p.bs_shift));
+        pos = x;
+        slot = ((int64_t)id << p.bs_shift) + (x & (p.block_size - 1));
+    }
+    p.slots[t] = slot;
+    p.positions[t] = pos;
+}
+
+struct Sums {
+    long long tok, keys, taken, gone;
+};
+
+__device__ __forceinline__ Sums add(const Sums &a, const Sums &b) {
+    return {a.tok + b.tok, a.keys + b.keys, a.taken + b.taken, a.gone + b.gone};
+}
+
+__device__ __forceinline__ Sums shift_up(const Sums &a, int d) {
+    return {__shfl_up_sync(0xffffffffu, a.tok, d), __shfl_up_sync(0xffffffffu, a.keys, d),
+            __shfl_up_sync(0xffffffffu, a.taken, d), __shfl_up_sync(0xffffffffu, a.gone, d)};
+}
+
+__global__ void __launch_bounds__(kThreads) block_tables_kernel(const TableParams p) {
+    extern __shared__ int32_t s_cu[];  // [3][batch + 1]: rows, taken and released before r
+    int32_t *s_tok = s_cu, *s_take = s_tok + p.batch + 1, *s_gone = s_take + p.batch + 1;
+    __shared__ Sums s_warp[kThreads / 32];
+    __shared__ uint32_t s_bad;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rank = (int)cluster_rank();
+    const int gtid = rank * kThreads + threadIdx.x;
+    constexpr int kAll = kCluster * kThreads;
+    const int B = p.batch, M = p.max_blocks_per_seq, shift = p.bs_shift;
+
+    pdl_wait();
+    if (threadIdx.x == 0) s_bad = 0;
+    uint32_t bad = 0;
+    const int F = *p.num_free;
+    const long long cap = (long long)M << shift;
+    Sums run = {0, 0, 0, 0};  // of the requests before this chunk
+    for (int r0 = 0; r0 < B; r0 += kThreads) {
+        const int r = r0 + threadIdx.x;
+        Sums v = {0, 0, 0, 0};
+        if (r < B) {
+            int a = p.old_len[r], b = p.new_len[r];
+            if (a < 0 || b < 0 || a > cap || b > cap) {
+                bad |= PKV_DEVERR_SEQLEN;
+                a = b = 0;
+            }
+            const int have = (a + p.block_size - 1) >> shift, want = (b + p.block_size - 1) >> shift;
+            v.tok = max(b - a, 0);
+            v.keys = b;
+            v.taken = max(want - have, 0);
+            v.gone = max(have - want, 0);
+        }
+        Sums in = v;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const Sums o = shift_up(in, d);
+            if (lane >= d) in = add(in, o);
+        }
+        if (lane == 31) s_warp[warp] = in;
+        __syncthreads();
+        Sums before = run;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            const Sums o = s_warp[w];
+            if (w < warp) before = add(before, o);
+            run = add(run, o);
+        }
+        before = add(before, in);  // up to and with r
+        if (r < B) {
+            s_tok[r + 1] = (int)before.tok;
+            s_take[r + 1] = (int)before.taken;
+            s_gone[r + 1] = (int)before.gone;
+            if (rank == 0) {
+                p.cu_q[r + 1] = (int)before.tok;
+                p.cu_k[r + 1] = (int)before.keys;
+            }
+        }
+        __syncthreads();  // s_warp is used again
+    }
+    if (threadIdx.x == 0) {
+        s_tok[0] = s_take[0] = s_gone[0] = 0;
+        if (rank == 0) p.cu_q[0] = p.cu_k[0] = 0;
+    }
+    if (run.tok > p.rows || run.keys > 0x7fffffffLL) bad |= PKV_DEVERR_SEQLEN;
+    // more pages than the pool has: an entry of the tables or the stack is there twice
+    if (F < 0 || F > p.num_blocks || run.gone > p.num_blocks || F + run.gone - run.taken > p.num_blocks)
+        bad |= PKV_DEVERR_BLOCK_ID;
+    if (F + run.gone < run.taken) bad |= PKV_DEVERR_NO_BLOCKS;
+    const int total = (int)run.tok, A = (int)run.taken, R = (int)run.gone;
+    const bool countable = __syncthreads_or((int)bad) == 0;
+
+    // Where page i comes from, and the entry of the table it leaves.
+    auto released = [&](int i) {
+        const int r = find(s_gone, B, i);
+        const int want = (p.new_len[r] + p.block_size - 1) >> shift;
+        return p.block_table + (int64_t)r * M + want + (i - s_gone[r]);
+    };
+    const int moves = max(A, R);
+    if (countable) {
+        // every id that will be moved, and the pages that new tokens go on filling
+        for (int i = gtid; i < moves; i += kAll) {
+            const int id = i < R ? *released(i) : p.free_blocks[F - 1 - (i - R)];
+            if (id < 0 || id >= p.num_blocks) bad |= PKV_DEVERR_BLOCK_ID;
+        }
+        for (int r = gtid; r < B; r += kAll) {
+            const int a = p.old_len[r];
+            if (p.new_len[r] > a && (a & (p.block_size - 1))) {
+                const int id = p.block_table[(int64_t)r * M + (a >> shift)];
+                if (id < 0 || id >= p.num_blocks) bad |= PKV_DEVERR_BLOCK_ID;
+            }
+        }
+    }
+    if (bad) atomicOr(&s_bad, bad);
+    cluster_sync();  // every CTA has read num_free and checked its part
+    bad = 0;
+#pragma unroll
+    for (int c = 0; c < kCluster; ++c) bad |= cluster_ld32(cluster_addr(smem_u32(&s_bad), c));
+    if (bad) {  // nothing is moved, no row has a slot, no request a query or a key
+        if (gtid == 0) flag_error(p.dev_error, bad);
+        if (rank == 0)
+            for (int r = threadIdx.x; r <= B; r += kThreads) p.cu_q[r] = p.cu_k[r] = 0;
+        if (p.rows_here)
+            for (int t = gtid; t < p.rows; t += kAll) {
+                p.slots[t] = -1;
+                p.positions[t] = 0;
+            }
+        cluster_sync();  // the others may still read s_bad
+        return;
+    }
+    for (int i = gtid; i < moves; i += kAll) {
+        int id;
+        if (i < R) {
+            int32_t *e = released(i);
+            id = *e;
+            *e = -1;
+        } else {
+            id = p.free_blocks[F - 1 - (i - R)];
+        }
+        if (i < A) {
+            const int r = find(s_take, B, i);
+            const int have = (p.old_len[r] + p.block_size - 1) >> shift;
+            p.block_table[(int64_t)r * M + have + (i - s_take[r])] = id;
+        } else {
+            p.free_blocks[F + R - 1 - i] = id;
+        }
+    }
+    if (gtid == 0) *p.num_free = F + R - A;
+    cluster_sync();  // the tables are written
+    if (p.rows_here)
+        for (int t = gtid; t < p.rows; t += kAll) write_row(p, s_tok, t, total);
+}
+
+__global__ void __launch_bounds__(kRowThreads) block_rows_kernel(const TableParams p) {
+    extern __shared__ int32_t s_cu[];
+    pdl_wait();
+    for (int r = threadIdx.x; r <= p.batch; r += kRowThreads) s_cu[r] = p.cu_q[r];
+    __syncthreads();
+    const int total = s_cu[p.batch];
+    const int64_t t0 = (int64_t)blockIdx.x * kRowsPerCta;
+    for (int i = threadIdx.x; i < kRowsPerCta && t0 + i < p.rows; i += kRowThreads)
+        write_row(p, s_cu, (int)t0 + i, total);
+}
+
+}  // namespace
+
+cudaError_t launch_block_tables(const TableParams &p0, cudaStream_t stream) {
+    TableParams p = p0;
+    p.rows_here = p.rows <= kRowsHere;
+    const int smem = 3 * (p.batch + 1) * 4;
+    cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(block_tables_kernel), smem);
+    if (e != cudaSuccess) return e;
+    e = launch_cluster(block_tables_kernel, kCluster, kCluster, kThreads, smem, stream, p);
+    if (e != cudaSuccess || p.rows_here) return e;
+    const int smem2 = (p.batch + 1) * 4;
+    e = ensure_dynamic_smem(reinterpret_cast<const void *>(block_rows_kernel), smem2);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(block_rows_kernel,
+                      dim3((unsigned)((p.rows + (int64_t)kRowsPerCta - 1) / kRowsPerCta)),
+                      dim3(kRowThreads), smem2, stream, p);
+}
+
+}  // namespace pkv

@@ -43,7 +43,10 @@
 // as long ones 72 and 152; partitions of 1024 tokens 65 and 120.  What is
 // left is latency between dependent instructions at 2.5 warps per scheduler
 // (issue slots 41 % used, tensor pipe 22 %).
-#include "pkv_fp8.cuh"
+#include <cstring>
+#include <type_traits>
+
+#include "pkv_sparse.cuh"
 
 namespace pkv {
 
@@ -123,18 +126,35 @@ struct Shape {
     static constexpr int BLK_OFF = R_OFF + kWarps * kMaxGroup * 4;
     static constexpr int SMEM_FIXED = 1024 + BLK_OFF;        // + the partition's block ids
     static_assert(kWarps * 8 * D * 4 <= RING, "merge scratch must fit in the ring");
+    static_assert((kWarps * 8 + kMaxGroup) * D * 4 <= RING, "and the outputs behind it");
 };
 
-template <int D, int BS, int NHT, bool HND>
+// The same attention over lists of pages (sparse_decode.cu): the keys are the rows
+// of the pages that a CTA of a cluster takes of a row's list, one after another.
+struct SparseFp8Params {
+    DecodeFp8Params dense;  // what both have: q, pools, tables, shapes (no window, no ALiBi)
+    SparseParams s;
+};
+
+__device__ __forceinline__ const DecodeFp8Params &dense_params(const DecodeFp8Params &p) {
+    return p;
+}
+__device__ __forceinline__ const DecodeFp8Params &dense_params(const SparseFp8Params &p) {
+    return p.dense;
+}
+
+template <int D, int BS, int NHT, bool HND, typename P>
 __global__ void __launch_bounds__(kThreads)
-decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap tmk,
+decode_fp8_kernel(const P params, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmv) {
+    constexpr bool SPARSE = std::is_same<P, SparseFp8Params>::value;
     using C = Shape<D>;
     constexpr int NST = C::NST, TOK = C::TOK;
     constexpr int BR = BS < TOK ? BS : TOK;  // tokens per box: a page, or a stage's part of one
     constexpr int NC = D / 16;      // 16-dim chunks
     constexpr int NT = TOK / 8;     // 8-token tiles
     constexpr int NCP = TOK / 16;   // 16-byte pieces of a stage's K (or V) scale bytes
+    const DecodeFp8Params &pp = dense_params(params);
     const DecodeParams &p = pp.d;
 
     extern __shared__ uint8_t smem_raw[];
@@ -147,16 +167,42 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
     // no early trigger: merge CTAs that wait on the SMs cost more (2 %) than
     // their launch latency
     pdl_wait();
-    const int g = blockIdx.x, b = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.group, Dh = p.head_dim;
+    int g = blockIdx.x, b = blockIdx.z;  // kv head; sequence, or row
+    int rank = 0, L = 0, tok_lo = 0, tok_hi = 0;
+    const int32_t *list = nullptr;       // SPARSE: this CTA's entries
+    const int32_t *bt = nullptr;
+    if constexpr (SPARSE) {
+        const SparseParams &sp = params.s;
+        rank = sp.cluster > 1 ? (int)cluster_rank() : 0;
+        const int64_t unit = blockIdx.x / (unsigned)sp.cluster;
+        b = (int)(unit / p.num_kv_heads);
+        g = (int)(unit % p.num_kv_heads);
+        int r, keys;
+        if (!row_request(sp.r, b, BS, g == 0 && rank == 0 && threadIdx.x == 0, r, keys)) return;
+        const int npages = (keys + BS - 1) / BS;
+        list = sp.pages + unit * sp.top_k;
+        const int n = list_length<kThreads>(list, sp.top_k, npages, p.dev_error, rank == 0,
+                                            reinterpret_cast<int *>(s_m));
+        // pages of whole stages, so that every CTA's first stage starts with one of its own
+        constexpr int U = TOK > BS ? TOK / BS : 1;
+        const int per = ((n + sp.cluster - 1) / sp.cluster + U - 1) / U * U;
+        const int lo = min(rank * per, n), mine = min(per, n - lo);
+        list += lo;
+        tok_hi = mine * BS;
+        if (mine > 0 && list[mine - 1] == npages - 1) tok_hi -= npages * BS - keys;
+        bt = p.block_table + (int64_t)r * p.max_blocks_per_seq;
+    } else {
+        L = clipped_len(p, b, BS, blockIdx.y == 0 && g == 0 && threadIdx.x == 0);
+        const int start = first_kept(L, p.window_left);
+        const int part = start / p.partition_size + blockIdx.y;
+        tok_lo = max(part * p.partition_size, start);
+        tok_hi = min((part + 1) * p.partition_size, L);
+        bt = p.block_table + (int64_t)b * p.max_blocks_per_seq;
+    }
     const int64_t unit0 = (int64_t)b * p.num_qo_heads + g * G;
-    const int L = clipped_len(p, b, BS, blockIdx.y == 0 && g == 0 && threadIdx.x == 0);
-    const int start = first_kept(L, p.window_left);
-    const int part = start / p.partition_size + blockIdx.y;
-    const int tok_lo = max(part * p.partition_size, start);
-    const int tok_hi = min((part + 1) * p.partition_size, L);
-    if (tok_lo >= tok_hi) {  // this slot holds no attended key
+    if (!SPARSE && tok_lo >= tok_hi) {  // this slot holds no attended key
         if (p.num_parts == 1)
             for (int i = threadIdx.x; i < G * (Dh / 4); i += kThreads) {
                 const int h = i / (Dh / 4), d = (i - h * (Dh / 4)) * 4;
@@ -167,8 +213,10 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
     }
 
     // stages start at multiples of TOK; pages of the range
-    const int st_lo = tok_lo / TOK, nst = (tok_hi - 1) / TOK - st_lo + 1;
-    const int pg_lo = st_lo * TOK / BS, pg_first = tok_lo / BS, pg_last = (tok_hi - 1) / BS;
+    const int st_lo = tok_lo / TOK;
+    const int nst = SPARSE ? (tok_hi + TOK - 1) / TOK : (tok_hi - 1) / TOK - st_lo + 1;
+    const int pg_lo = st_lo * TOK / BS, pg_first = tok_lo / BS;
+    const int pg_last = SPARSE && tok_hi == 0 ? -1 : (tok_hi - 1) / BS;
 
     const uint32_t ring = smem_u32(smem);
     const uint32_t bars = ring + C::BAR_OFF;
@@ -178,12 +226,11 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
         tma_prefetch_desc(&tmk);
         tma_prefetch_desc(&tmv);
     }
-    const int32_t *bt = p.block_table + (int64_t)b * p.max_blocks_per_seq;
     const int pg_end = ((st_lo + nst) * TOK - 1) / BS;  // the last stage's last page
     for (int page = pg_lo + threadIdx.x; page <= pg_end; page += kThreads) {
         int id = -1;
         if (page >= pg_first && page <= pg_last) {  // else: no attended key, not read
-            id = bt[page];
+            id = bt[SPARSE ? list[page] : page];
             if (id < 0 || id >= p.num_blocks) {
                 flag_error(p.dev_error, PKV_DEVERR_BLOCK_ID);
                 id = -1;
@@ -375,7 +422,7 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
                 sacc[nt][2 * ht] *= kf.x;
                 sacc[nt][2 * ht + 1] *= kf.y;
             }
-            if (!full || p.alibi) {
+            if (!full || (!SPARSE && p.alibi)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -493,6 +540,10 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
         }
     }
     float *s_o = reinterpret_cast<float *>(smem);  // [warp][8 heads][D]
+    // SPARSE: the CTA's outputs [16 heads][D] behind it, and its heads' lse (the stages'
+    // scale bytes are free)
+    float *s_out = s_o + kWarps * 8 * D;
+    float *s_lse = reinterpret_cast<float *>(smem + C::FACT_OFF);
 #pragma unroll
     for (int ht = 0; ht < NHT; ++ht) {
         __syncthreads();  // the ring is free (ht 0); the last heads are written (ht 1)
@@ -513,7 +564,13 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
             // a NaN sum keeps its reference at -inf: do not lose it to a factor 0
             const float l = (l0 != l0 ? l0 : exp2f(m0 - Ms) * l0) +
                             (l1 != l1 ? l1 : exp2f(m1 - Ms) * l1);
-            const float mul = finish_row(p, unit0 + hh, g * G + hh, M, l, d == 0);
+            float mul;
+            if constexpr (SPARSE) {
+                mul = l == 0.f ? 0.f : 1.f / l;  // NaN stays
+                if (d == 0) s_lse[hh] = l == 0.f ? kNegInf : M + log2f(l);
+            } else {
+                mul = finish_row(p, unit0 + hh, g * G + hh, M, l, d == 0);
+            }
             // O is relative to 2^r: 2^(r - M) in two halves, because r holds V's
             // exponent and the whole may leave fp32's range where the result does not
             const float h0 = exp2f(0.5f * (s_r[hh] - Ms));
@@ -523,11 +580,15 @@ decode_fp8_kernel(const DecodeFp8Params pp, const __grid_constant__ CUtensorMap 
             auto join = [&](float x, float y) {
                 return x * mul * h0 * h0 + y * mul * h1 * h1;
             };
-            store_row4(p, unit0 + hh, d,
-                       make_float4(join(a.x, c.x), join(a.y, c.y), join(a.z, c.z),
-                                   join(a.w, c.w)));
+            const float4 o = make_float4(join(a.x, c.x), join(a.y, c.y), join(a.z, c.z),
+                                         join(a.w, c.w));
+            if constexpr (SPARSE)
+                *reinterpret_cast<float4 *>(s_out + hh * D + d) = o;
+            else
+                store_row4(p, unit0 + hh, d, o);
         }
     }
+    if constexpr (SPARSE) join_and_store<kThreads>(params.s, b, g, rank, s_out, D, s_lse);
 }
 
 // ---------------------------------------------------------------------------
@@ -632,8 +693,8 @@ template <int D, int BS, int NHT>
 cudaError_t launch_one(const DecodeFp8Params &p, const CUtensorMap *tk, const CUtensorMap *tv,
                        cudaStream_t stream) {
     using C = Shape<D>;
-    auto kern = p.d.hnd ? decode_fp8_kernel<D, BS, NHT, true>
-                        : decode_fp8_kernel<D, BS, NHT, false>;
+    auto kern = p.d.hnd ? decode_fp8_kernel<D, BS, NHT, true, DecodeFp8Params>
+                        : decode_fp8_kernel<D, BS, NHT, false, DecodeFp8Params>;
     // the pages of a partition, and those beside it in its first and last stage
     const int smem = C::SMEM_FIXED + (p.d.partition_size / BS + 6) * 4;
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), smem);
@@ -642,14 +703,38 @@ cudaError_t launch_one(const DecodeFp8Params &p, const CUtensorMap *tk, const CU
                       (size_t)smem, stream, p, *tk, *tv);
 }
 
-template <int D>
-cudaError_t launch_d(const DecodeFp8Params &p, int BS, const CUtensorMap *tk,
-                     const CUtensorMap *tv, cudaStream_t stream) {
+template <int D, int BS, int NHT>
+cudaError_t launch_one(const SparseFp8Params &p, const CUtensorMap *tk, const CUtensorMap *tv,
+                       cudaStream_t stream) {
+    using C = Shape<D>;
+    auto kern = p.s.hnd ? decode_fp8_kernel<D, BS, NHT, true, SparseFp8Params>
+                        : decode_fp8_kernel<D, BS, NHT, false, SparseFp8Params>;
+    // the CTA's entries, rounded up to a stage
+    const int smem = C::SMEM_FIXED + (p.s.cap + 8) * 4;
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), smem);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = (int64_t)p.s.r.rows * p.s.r.num_kv_heads * p.s.cluster;
+    if (grid > 0x7fffffff) return cudaErrorNotSupported;
+    return launch_cluster(kern, (unsigned)grid, p.s.cluster, kThreads, (size_t)smem, stream, p,
+                          *tk, *tv);
+}
+
+template <int D, typename P>
+cudaError_t launch_d(const P &p, int group, int BS, const CUtensorMap *tk, const CUtensorMap *tv,
+                     cudaStream_t stream) {
     if (BS == 16)
-        return p.d.group <= 8 ? launch_one<D, 16, 1>(p, tk, tv, stream)
-                              : launch_one<D, 16, 2>(p, tk, tv, stream);
-    return p.d.group <= 8 ? launch_one<D, 32, 1>(p, tk, tv, stream)
-                          : launch_one<D, 32, 2>(p, tk, tv, stream);
+        return group <= 8 ? launch_one<D, 16, 1>(p, tk, tv, stream)
+                          : launch_one<D, 16, 2>(p, tk, tv, stream);
+    return group <= 8 ? launch_one<D, 32, 1>(p, tk, tv, stream)
+                      : launch_one<D, 32, 2>(p, tk, tv, stream);
+}
+
+template <typename P>
+cudaError_t launch_any(const P &p, int D, int group, int BS, const CUtensorMap *tk,
+                       const CUtensorMap *tv, cudaStream_t stream) {
+    if (D <= 64) return launch_d<64>(p, group, BS, tk, tv, stream);
+    if (D <= 128) return launch_d<128>(p, group, BS, tk, tv, stream);
+    return launch_d<256>(p, group, BS, tk, tv, stream);
 }
 
 }  // namespace
@@ -665,15 +750,32 @@ cudaError_t launch_decode_fp8(const DecodeFp8Params &p, const pkv_cache_desc &ca
                               const CUtensorMap *tmap_k, const CUtensorMap *tmap_v,
                               cudaStream_t stream) {
     const int D = cache.head_dim, BS = cache.block_size;
-    cudaError_t e;
-    if (D <= 64)
-        e = launch_d<64>(p, BS, tmap_k, tmap_v, stream);
-    else if (D <= 128)
-        e = launch_d<128>(p, BS, tmap_k, tmap_v, stream);
-    else
-        e = launch_d<256>(p, BS, tmap_k, tmap_v, stream);
+    const cudaError_t e = launch_any(p, D, p.d.group, BS, tmap_k, tmap_v, stream);
     if (e != cudaSuccess || p.d.num_parts == 1) return e;
     return launch_merge_fp8(p.d, D, BS, stream);
+}
+
+cudaError_t launch_sparse_fp8(const SparseParams &s, int block_size, const CUtensorMap *tmap_k,
+                              const CUtensorMap *tmap_v, cudaStream_t stream) {
+    SparseFp8Params p;
+    std::memset(&p, 0, sizeof p);
+    p.s = s;
+    DecodeParams &d = p.dense.d;
+    d.q = s.q;
+    d.block_table = s.r.block_table;
+    d.dev_error = s.r.dev_error;
+    d.num_blocks = s.r.num_blocks;
+    d.num_kv_heads = s.r.num_kv_heads;
+    d.group = s.r.group;
+    d.num_qo_heads = s.r.num_kv_heads * s.r.group;
+    d.max_blocks_per_seq = s.r.max_blocks_per_seq;
+    d.head_dim = s.r.head_dim;
+    d.window_left = -1;
+    d.num_parts = 1;
+    d.scale_log2 = s.scale_log2;
+    p.dense.k_scale = s.k_scale;
+    p.dense.v_scale = s.v_scale;
+    return launch_any(p, s.r.head_dim, s.r.group, block_size, tmap_k, tmap_v, stream);
 }
 
 }  // namespace pkv

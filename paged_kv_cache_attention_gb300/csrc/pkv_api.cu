@@ -210,7 +210,7 @@ const char *pkv_status_string(int status) {
     }
 }
 
-int pkv_version(void) { return 600; }
+int pkv_version(void) { return 700; }
 
 pkv_status pkv_get_device_error(const int32_t *dev_error, int32_t *bits, int clear,
                                 void *stream) {
@@ -224,8 +224,8 @@ pkv_status pkv_get_device_error(const int32_t *dev_error, int32_t *bits, int cle
     if (clear && cudaMemsetAsync(const_cast<int32_t *>(dev_error), 0, sizeof word, s) != cudaSuccess)
         return PKV_ERR_CUDA;
     if (word & (int32_t)PKV_DEVERR_TIMEOUT) return PKV_ERR_TIMEOUT;
-    const int32_t metadata =
-        (int32_t)(PKV_DEVERR_BLOCK_ID | PKV_DEVERR_SLOT | PKV_DEVERR_SEQLEN | PKV_DEVERR_POSITION);
+    const int32_t metadata = (int32_t)(PKV_DEVERR_BLOCK_ID | PKV_DEVERR_SLOT | PKV_DEVERR_SEQLEN |
+                                       PKV_DEVERR_POSITION | PKV_DEVERR_NO_BLOCKS);
     return (word & metadata) ? PKV_ERR_OUT_OF_RANGE : PKV_OK;
 }
 

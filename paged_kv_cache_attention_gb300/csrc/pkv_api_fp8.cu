@@ -9,6 +9,30 @@
 
 namespace pkv {
 
+bool head_dim_ok(int d) {
+    return d == 64 || d == 80 || d == 96 || d == 112 || d == 128 || d == 256;
+}
+
+// TMA view of one pool whose box is 128 bytes (64 for the codes of a 64-dim
+// head) of box_rows tokens of one (page, kv head): NHD {D, Hkv, num_blocks *
+// bs}, HND {D, bs, num_blocks * Hkv}.
+pkv_status pool_map(CUtensorMap *map, const void *base, const pkv_cache_desc &c, int box_rows) {
+    const bool fp8 = c.dtype == PKV_E4M3;
+    const cuuint64_t e = fp8 ? 1 : 2, D = (cuuint64_t)c.head_dim;
+    const cuuint32_t bs = (cuuint32_t)box_rows;
+    const bool nhd = c.layout == PKV_NHD;
+    const cuuint64_t mid = nhd ? c.num_kv_heads : c.block_size;
+    const cuuint64_t rows = (cuuint64_t)c.num_blocks * (nhd ? c.block_size : c.num_kv_heads);
+    const cuuint64_t dims[3] = {D, mid, rows};
+    const cuuint64_t strides[2] = {D * e, D * e * mid};
+    const cuuint32_t w = fp8 ? (D == 64 ? 64 : 128) : 64;
+    const cuuint32_t box[3] = {w, nhd ? 1u : bs, nhd ? bs : 1u};
+    return encode_map_3d(map,
+                         fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                         base, dims, strides, box,
+                         w * e == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 namespace {
 
 constexpr int kDefaultPartition = 512;
@@ -23,10 +47,6 @@ bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p)
 pkv_status from_cuda(cudaError_t e) {
     if (e == cudaSuccess) return PKV_OK;
     return e == cudaErrorNotSupported ? PKV_ERR_UNSUPPORTED : PKV_ERR_CUDA;
-}
-
-bool head_dim_ok(int d) {
-    return d == 64 || d == 80 || d == 96 || d == 112 || d == 128 || d == 256;
 }
 
 // The shape of a pool and its dtype (one of the two given).
@@ -60,26 +80,6 @@ PoolArgs pool_args(const pkv_cache_desc &c, const void *k, const void *v, const 
     a.bs_shift = c.block_size == 16 ? 4 : 5;
     a.hnd = c.layout == PKV_HND ? 1 : 0;
     return a;
-}
-
-// TMA view of one pool whose box is 128 bytes (64 for the codes of a 64-dim
-// head) of box_rows tokens of one (page, kv head): NHD {D, Hkv, num_blocks *
-// bs}, HND {D, bs, num_blocks * Hkv}.
-pkv_status pool_map(CUtensorMap *map, const void *base, const pkv_cache_desc &c, int box_rows) {
-    const bool fp8 = c.dtype == PKV_E4M3;
-    const cuuint64_t e = fp8 ? 1 : 2, D = (cuuint64_t)c.head_dim;
-    const cuuint32_t bs = (cuuint32_t)box_rows;
-    const bool nhd = c.layout == PKV_NHD;
-    const cuuint64_t mid = nhd ? c.num_kv_heads : c.block_size;
-    const cuuint64_t rows = (cuuint64_t)c.num_blocks * (nhd ? c.block_size : c.num_kv_heads);
-    const cuuint64_t dims[3] = {D, mid, rows};
-    const cuuint64_t strides[2] = {D * e, D * e * mid};
-    const cuuint32_t w = fp8 ? (D == 64 ? 64 : 128) : 64;
-    const cuuint32_t box[3] = {w, nhd ? 1u : bs, nhd ? bs : 1u};
-    return encode_map_3d(map,
-                         fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                         base, dims, strides, box,
-                         w * e == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Workspace of the tree attention: the line of work, and two partials per CTA.

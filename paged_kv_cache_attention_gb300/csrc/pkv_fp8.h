@@ -90,6 +90,13 @@ pkv_status encode_map_3d(CUtensorMap *map, CUtensorMapDataType type, const void 
                          const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
                          const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle);
 
+// The head sizes of the 8-bit cache and of the calls over both kinds of pools.
+bool head_dim_ok(int d);
+
+// Tensor map of a pool (bf16 or e4m3) with boxes of 128 bytes (64 for the codes of a
+// 64-dim head) of box_rows tokens of one (page, kv head) (pkv_api_fp8.cu).
+pkv_status pool_map(CUtensorMap *map, const void *base, const pkv_cache_desc &c, int box_rows);
+
 cudaError_t launch_quant_write(const QuantWriteParams &p, int dtype, cudaStream_t stream);
 cudaError_t launch_gather(const GatherParams &p, cudaStream_t stream);
 cudaError_t launch_norm_rope(const NormRopeParams &p, int dtype, cudaStream_t stream);

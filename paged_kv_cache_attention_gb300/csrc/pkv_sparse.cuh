@@ -1,0 +1,159 @@
+// pkv_sparse.cuh -- device helpers of the sparse decode step: clusters and their
+// shared memory, a row's request and length.
+#pragma once
+
+#include "pkv_fp8.cuh"
+#include "pkv_sparse.h"
+
+namespace pkv {
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// Every thread of every CTA of the cluster; writes before it (shared memory of
+// the cluster, global memory) are seen after it by the whole cluster.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                 "barrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+
+// The address of a shared-memory word of this CTA in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t cluster_ld32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 cluster_ld128(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// Row t's request r and the number L of keys up to and with its own (0: the row
+// attends nothing).  False: a row of no request.  Taken by a whole warp, which
+// looks at 32 offsets at a time.
+__device__ __forceinline__ bool row_request(const RowParams &p, int t, int block_size,
+                                            bool report, int &r, int &L) {
+    const int lane = threadIdx.x & 31;
+    int behind = 0;  // queries of the request behind this one
+    r = t;
+    if (p.cu_q) {
+        int lo = 0, hi = p.batch;
+        while (true) {
+            const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+            const uint32_t m = __ballot_sync(0xffffffffu, at < hi && p.cu_q[at] <= t);
+            const int c = __ffs(~m) - 1;  // leading offsets that are not above t
+            const int below = m == 0xffffffffu ? 32 : c;
+            if (below == 0) return false;
+            lo += (below - 1) * step;
+            hi = min(hi, lo + step);
+            if (step == 1) break;
+        }
+        r = lo;
+        const int end = p.cu_q[r + 1];
+        if (t >= end) return false;
+        behind = end - t - 1;
+    }
+    int n = p.seqlens[r];
+    const int64_t table = (int64_t)p.max_blocks_per_seq * block_size;
+    const int cap = table < p.max_seqlen ? (int)table : p.max_seqlen;
+    if (n < 0 || n > cap) {
+        if (report) flag_error(p.dev_error, PKV_DEVERR_SEQLEN);
+        n = min(max(n, 0), cap);
+    }
+    L = max(n - behind, 0);
+    return true;
+}
+
+// The list of a row: strictly ascending pages below npages.  It ends at the first
+// entry that is negative, not above the one before it or not a page of the row (the
+// last two are errors).  Returns the entries before that; all threads of the CTA.
+template <int THREADS>
+__device__ __forceinline__ int list_length(const int32_t *list, int top_k, int npages,
+                                           int32_t *dev_error, bool report, int *s_min) {
+    int end = top_k;
+    for (int i = threadIdx.x; i < top_k; i += THREADS) {
+        const int e = list[i], before = i > 0 ? list[i - 1] : -1;
+        if (e <= before || e >= npages) {
+            end = i;
+            break;
+        }
+    }
+    end = __reduce_min_sync(0xffffffffu, end);
+    if ((threadIdx.x & 31) == 0) s_min[threadIdx.x >> 5] = end;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) end = min(end, s_min[w]);
+    if (report && threadIdx.x == 0 && end < top_k && list[end] >= 0)
+        flag_error(dev_error, PKV_DEVERR_BLOCK_ID);
+    return end;
+}
+
+// Join the cluster's parts of a row's heads and store them.  s_out [group][stride]
+// holds this CTA's normalised outputs (zeros without keys), s_lse [group] their
+// log-sum-exp in log2 units (-inf without keys, NaN stays):
+//   o = sum_c 2^(lse_c - T) o_c / (sum_c 2^(lse_c - T) + 2^(sink - T))
+template <int THREADS>
+__device__ __forceinline__ void join_and_store(const SparseParams &p, int t, int g, int rank,
+                                               const float *s_out, int stride,
+                                               const float *s_lse) {
+    const int C = p.cluster, G = p.r.group, D = p.r.head_dim;
+    if (C > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    const uint32_t out = smem_u32(s_out), lse = smem_u32(s_lse);
+    const int vecs = D / 4;
+    for (int i = rank * THREADS + threadIdx.x; i < G * vecs; i += C * THREADS) {
+        const int h = i / vecs, d = (i - h * vecs) * 4;
+        const int hq = g * G + h;
+        const float sink = p.sink ? p.sink[hq] * kLog2e : -INFINITY;
+        float T = sink;
+        for (int c = 0; c < C; ++c)
+            T = fmaxf(T, C > 1 ? __uint_as_float(cluster_ld32(cluster_addr(lse + 4 * h, c)))
+                               : s_lse[h]);
+        const float Ts = T == -INFINITY ? 0.f : T;
+        float sum = exp2f(sink - Ts);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < C; ++c) {
+            float l;
+            float4 v;
+            if (C > 1) {
+                l = __uint_as_float(cluster_ld32(cluster_addr(lse + 4 * h, c)));
+                v = cluster_ld128(cluster_addr(out + 4 * (h * stride + d), c));
+            } else {
+                l = s_lse[h];
+                v = *reinterpret_cast<const float4 *>(s_out + h * stride + d);
+            }
+            const float w = exp2f(l - Ts);
+            sum += w;
+            acc.x = fmaf(w, v.x, acc.x);
+            acc.y = fmaf(w, v.y, acc.y);
+            acc.z = fmaf(w, v.z, acc.z);
+            acc.w = fmaf(w, v.w, acc.w);
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int64_t unit = (int64_t)t * p.r.num_kv_heads * G + hq;
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + unit * D + d) =
+            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+        if (p.lse_out && d == 0)
+            p.lse_out[unit] = sum == 0.f ? -INFINITY : (Ts + log2f(sum)) * kLn2;
+    }
+    if (C > 1) cluster_sync();  // the others may still read this CTA's part
+}
+
+}  // namespace pkv
