@@ -697,8 +697,8 @@ PKV_API pkv_status pkv_update_page_bounds(const void *k_cache, const uint8_t *k_
  * A page id out of range makes its page the last choice (PKV_DEVERR_BLOCK_ID); a
  * length out of range is clipped (PKV_DEVERR_SEQLEN).
  * Requirements: num_first + num_recent <= top_k <= 16384; at most 16 query heads per
- * kv head; total_q at most 2^24; max_seqlen at most 2^30 and 393216 pages; head
- * sizes and block sizes as update_page_bounds; q and page_bounds 16-byte aligned.
+ * kv head; total_q at most 2^24; max_seqlen at most 262144 pages; head sizes and
+ * block sizes as update_page_bounds; q and page_bounds 16-byte aligned.
  */
 PKV_API pkv_status pkv_select_pages(int32_t *pages, int top_k, const void *q,
                                     const int8_t *page_bounds, const uint8_t *bounds_scale,

@@ -179,8 +179,10 @@ decode_fp8_kernel(const P params, const __grid_constant__ CUtensorMap tmk,
         const int64_t unit = blockIdx.x / (unsigned)sp.cluster;
         b = (int)(unit / p.num_kv_heads);
         g = (int)(unit % p.num_kv_heads);
-        int r, keys;
-        if (!row_request(sp.r, b, BS, g == 0 && rank == 0 && threadIdx.x == 0, r, keys)) return;
+        int r, keys, count;
+        if (!row_request(sp.r, b, BS, g == 0 && rank == 0 && threadIdx.x == 0, r, keys, count))
+            return;
+        keys = max(keys, 0);
         const int npages = (keys + BS - 1) / BS;
         list = sp.pages + unit * sp.top_k;
         const int n = list_length<kThreads>(list, sp.top_k, npages, p.dev_error, rank == 0,

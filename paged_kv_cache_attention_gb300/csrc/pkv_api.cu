@@ -8,6 +8,7 @@
 #include <cmath>
 #include <cstring>
 #include <mutex>
+#include <utility>
 #include <vector>
 
 #include "pkv_fp8.h"
@@ -188,6 +189,20 @@ cudaError_t ensure_dynamic_smem(const void *kernel, int bytes) {
         if (x.kernel == kernel && x.device == dev && x.bytes >= bytes) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess) done.push_back({kernel, dev, bytes});
+    return e;
+}
+
+cudaError_t ensure_wide_clusters(const void *kernel) {
+    static std::mutex mu;
+    static std::vector<std::pair<const void *, int>> done;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    for (const auto &x : done)
+        if (x.first == kernel && x.second == dev) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) done.push_back({kernel, dev});
     return e;
 }
 

@@ -13,6 +13,7 @@ namespace {
 constexpr int kMaxBatch = 16384;      // prefix sums of all requests in shared memory
 constexpr int kMaxTopK = 16384;
 constexpr int64_t kMaxLen = 1 << 30;  // positions are 32-bit
+constexpr int64_t kMaxPages = 262144;  // scores of a row in a cluster's shared memory
 
 bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -166,7 +167,7 @@ pkv_status pkv_select_pages(int32_t *pages, int top_k, const void *q, const int8
     if (max_seqlen < 0 || num_first < 0 || num_recent < 1 ||
         (int64_t)num_first + num_recent > top_k)
         return PKV_ERR_INVALID_ARG;
-    if (max_seqlen > kMaxLen) return PKV_ERR_UNSUPPORTED;
+    if (max_seqlen > kMaxPages * (int64_t)block_size) return PKV_ERR_UNSUPPORTED;
     if (batch == 0 || total_q == 0) return PKV_OK;
     if (max_blocks_per_seq == 0) return PKV_ERR_INVALID_ARG;
     if (!pages || !q || !page_bounds || !bounds_scale || !block_table || !cache_seqlens)
@@ -186,6 +187,7 @@ pkv_status pkv_select_pages(int32_t *pages, int top_k, const void *q, const int8
     p.num_first = num_first;
     p.num_recent = num_recent;
     p.block_size = block_size;
+    p.bs_shift = block_size == 16 ? 4 : 5;
     p.cluster = p.cap = 0;
     return from_cuda(launch_select_pages(p, static_cast<cudaStream_t>(stream)));
 }

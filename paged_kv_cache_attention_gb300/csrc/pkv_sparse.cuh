@@ -43,13 +43,13 @@ __device__ __forceinline__ float4 cluster_ld128(uint32_t addr) {
     return v;
 }
 
-// Row t's request r and the number L of keys up to and with its own (0: the row
-// attends nothing).  False: a row of no request.  Taken by a whole warp, which
-// looks at 32 offsets at a time.
+// Row t's request r, the number L of keys up to and with its own (0 and less: the row
+// attends nothing) and the request's rows from t on.  False: a row of no request.
+// Taken by a whole warp, which looks at 32 offsets at a time.
 __device__ __forceinline__ bool row_request(const RowParams &p, int t, int block_size,
-                                            bool report, int &r, int &L) {
+                                            bool report, int &r, int &L, int &count) {
     const int lane = threadIdx.x & 31;
-    int behind = 0;  // queries of the request behind this one
+    count = 1;
     r = t;
     if (p.cu_q) {
         int lo = 0, hi = p.batch;
@@ -66,7 +66,7 @@ __device__ __forceinline__ bool row_request(const RowParams &p, int t, int block
         r = lo;
         const int end = p.cu_q[r + 1];
         if (t >= end) return false;
-        behind = end - t - 1;
+        count = end - t;
     }
     int n = p.seqlens[r];
     const int64_t table = (int64_t)p.max_blocks_per_seq * block_size;
@@ -75,7 +75,7 @@ __device__ __forceinline__ bool row_request(const RowParams &p, int t, int block
         if (report) flag_error(p.dev_error, PKV_DEVERR_SEQLEN);
         n = min(max(n, 0), cap);
     }
-    L = max(n - behind, 0);
+    L = n - (count - 1);
     return true;
 }
 

@@ -51,8 +51,8 @@ struct SelectParams {
     const int8_t *bounds;
     const uint8_t *bounds_scale;
     int32_t *pages;                // [rows, Hkv, top_k]
-    int top_k, num_first, num_recent, block_size;
-    int cluster;                   // CTAs per row and kv head
+    int top_k, num_first, num_recent, block_size, bs_shift;
+    int cluster;                   // CTAs per tile of queries and kv head
     int cap;                       // pages a CTA has room for
 };
 

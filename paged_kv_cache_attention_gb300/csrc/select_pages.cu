@@ -14,19 +14,23 @@
 // page first.
 //
 // I_h is a product [pages, 2 D] x [2 D, heads]: mma.sync m16n8k16 in f16 (integers
-// up to 2048 are exact there), 16 pages as rows and up to 8 heads as columns.  The
-// order of the summands is free, so a lane loads 16 codes in one go and uses them
-// as the fragments of four steps, and the columns are laid out to match.  A code
-// becomes an f16 by putting it into the mantissa of 1024 (a byte permutation) and
-// taking 1152 off: 2.5 instructions for a pair.
+// up to 2048 are exact there), 16 pages as rows and heads of one or more queries as
+// columns.  The order of the summands is free, so a lane loads 16 codes in one go
+// and uses them as the fragments of four steps, and the columns are laid out to
+// match.  A code becomes an f16 by putting it into the mantissa of 1024 (a byte
+// permutation) and taking 1152 off: 2.5 instructions for a pair.
 //
-// A cluster of CTAs shares the pages of a (query, kv head); each keeps its pages'
-// scores in its own shared memory, as integers that sort like the scores.  The
-// top_k-th largest is found digit by digit (8 bits at a time, histograms summed over the
-// cluster), then the pages above it, and as many of those equal to it as there is
-// room for, are written in ascending order.  One launch, no workspace.
+// A cluster of CTAs shares the pages of a tile of queries of one request and kv
+// head; each keeps its pages' scores in its own shared memory, as integers that sort
+// like the scores.  The top_k-th largest is found digit by digit (8 bits at a time,
+// histograms summed over the cluster, until few are left), then the pages above it,
+// and as many of those equal to it as there is room for, are written in ascending
+// order.  One launch, no workspace.
 //
-// HBM bound: (2 D + 1) bytes per page and kv head, each read once in a decode step.
+// In a decode step (one query per tile) HBM bound: (2 D + 1) bytes per page and kv
+// head, each read once; every lane copies the pieces it will use itself
+// (cp.async, three tiles ahead), so that nothing waits but on its own loads.  In a
+// chunk the queries of a tile share the pages' loads and conversions.
 #include <cuda_fp16.h>
 
 #include "pkv_sparse.cuh"
@@ -35,10 +39,9 @@ namespace pkv {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr uint32_t kForced = 0xffffffffu;  // above every score
-constexpr int kNoVote = -100000;           // exponent of a head that has no say
+constexpr int kNoVote = -100000;           // exponent of a column that has no say
+constexpr int kRank = 128;                 // scores ranked against one another
 
 // An unsigned integer that sorts like x (no NaN; -0 was made 0).
 __device__ __forceinline__ uint32_t sortable(float x) {
@@ -46,13 +49,37 @@ __device__ __forceinline__ uint32_t sortable(float x) {
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
-// Four int8 codes of a word as f16 pairs (bytes 0 and 1, bytes 2 and 3), exact.
+// Four int8 codes of a word as f16 pairs (bytes 0 and 1, bytes 2 and 3), exact; plus
+// 1152 each unless EXACT.
+template <bool EXACT>
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
     const uint32_t u = w ^ 0x80808080u;  // code + 128
-    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    const uint32_t off = 0x64806480u;    // 1152, twice
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(off));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(off));
+    lo = __byte_perm(u, 0x64646464u, 0x4140);  // 1024 + code + 128
+    hi = __byte_perm(u, 0x64646464u, 0x4342);
+    if (EXACT) {
+        const uint32_t off = 0x64806480u;  // 1152, twice
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(off));
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(off));
+    }
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ float pow2(int e) {  // -126 <= e <= 127
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// x * 2^e, rounded once: 0 or 2^-126 <= |x|, -252 <= e <= 254.  The first product is
+// exact, or overflows as the whole does, or is so small that the whole is 0.
+__device__ __forceinline__ float scaled(float x, int e) {
+    const int last = min(max(e, -126), 127);
+    return x * pow2(e - last) * pow2(last);
 }
 
 __device__ __forceinline__ void block_sync(bool cluster) {
@@ -62,276 +89,631 @@ __device__ __forceinline__ void block_sync(bool cluster) {
         __syncthreads();
 }
 
-// NCH: 64-byte pieces of a page's codes; NT: 8-head column tiles.
-template <int NCH, int NT>
-__global__ void __launch_bounds__(kThreads) select_pages_kernel(const SelectParams p) {
-    extern __shared__ uint32_t s_key[];          // [cap]
-    __shared__ uint4 s_q[NT][NCH][2][32];        // column fragments: [..][steps 0-1, 2-3][lane]
-    __shared__ int s_exp[16];
-    __shared__ uint32_t s_hist[4][256];
-    __shared__ uint32_t s_pick[2];               // digit, pages above it
-    __shared__ int s_cnt[kWarps][2], s_total[2]; // above, equal: per warp, of the CTA
+// NCH: 64-byte pieces of a page's codes; NT: 8-column tiles; GP: columns of a query
+// (its group's heads, rounded up to a power of two).
+template <int NCH, int NT, int GP>
+struct Shape {
+    static constexpr int QT = NT * 8 / GP;               // queries of a tile
+    static constexpr int WARPS = QT == 1 ? 4 : 8;
+    static constexpr int NST = 2;                        // 16-page tiles in flight per warp
+    // Few columns: 1152 is taken off the sums, not off each code.  Four sums for a
+    // quarter of the channels each stay below 2^24 (32 channels * 255 * 1279).
+    static constexpr bool OFFSET = NT <= 2 && NCH <= 4;
+    static constexpr int STAGE = NCH * 1024;
+    static constexpr int Q_OFF = WARPS * NST * STAGE;   // columns: [NT][NCH][2][32 lanes]
+    static constexpr int KEY_OFF = Q_OFF + NT * NCH * 1024;  // scores: [QT][cap]
+    static constexpr int GROUP = WARPS / QT;            // warps that select for a query
+};
+
+template <int NCH, int NT, int GP>
+__global__ void __launch_bounds__(Shape<NCH, NT, GP>::WARPS * 32) select_pages_kernel(const SelectParams p) {
+    using S = Shape<NCH, NT, GP>;
+    // sums that do not wait for one another
+    constexpr int NA = S::OFFSET || NT == 1 ? 4 : NT <= 4 ? 2 : 1;
+    constexpr int kWarps = S::WARPS, kThreads = kWarps * 32;
+    constexpr int QT = S::QT, NST = S::NST, GS = S::GROUP * 32, BPT = 256 / GS;
+    extern __shared__ uint4 s_dyn[];
+    uint4 *s_q = s_dyn + S::Q_OFF / 16;
+    uint32_t *s_key = reinterpret_cast<uint32_t *>(s_dyn + S::KEY_OFF / 16);
+    __shared__ int s_exp[NT * 8];
+    __shared__ alignas(16) int s_sum[NT * 8][4];             // OFFSET: a column's sums over d / 4 % 4
+    __shared__ alignas(16) uint32_t s_hist[2][QT][256];
+    __shared__ uint32_t s_pick[QT][3];           // digit, pages above it, pages with it
+    __shared__ int s_scale[S::WARPS][S::NST][16];  // scale bytes of the tiles in flight
+    __shared__ uint32_t s_range[S::WARPS][2];    // least and largest score
+    __shared__ int s_left[QT];                   // scores in the list to be ranked
+    __shared__ int s_cnt[kWarps][2];             // above, equal: per warp
+    __shared__ int s_total[QT][2];               // of the CTA
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int gq = lane >> 2, tq = lane & 3;
     const int C = p.cluster, rank = C > 1 ? (int)cluster_rank() : 0;
     const int64_t unit = blockIdx.x / (unsigned)C;
-    const int t = (int)(unit / p.r.num_kv_heads), g = (int)(unit % p.r.num_kv_heads);
-    const int D = p.r.head_dim, G = p.r.group;
+    const int t0 = (int)(unit / p.r.num_kv_heads) * QT, g = (int)(unit % p.r.num_kv_heads);
+    const int D = p.r.head_dim, G = p.r.group, shift = p.bs_shift;
+    const int t_end = min(t0 + QT, p.r.rows);
 
     pdl_wait();
-    int r, L;
-    if (!row_request(p.r, t, p.block_size, g == 0 && rank == 0 && threadIdx.x == 0, r, L)) return;
-    const int n = (L + p.block_size - 1) / p.block_size;
-    int32_t *out = p.pages + unit * p.top_k;
-    if (n <= p.top_k) {  // all of them
-        for (int i = rank * kThreads + threadIdx.x; i < p.top_k; i += C * kThreads)
-            out[i] = i < n ? i : -1;
-        return;
-    }
-    const int per = ((n + C - 1) / C + 15) / 16 * 16;
-    const int base = rank * per, nl = min(max(n - base, 0), per);
+    // the tile's rows, request by request (one, but where requests meet)
+    for (int t = t0; t < t_end;) {
+        int r, L, count;
+        if (!row_request(p.r, t, p.block_size, g == 0 && rank == 0 && threadIdx.x == 0, r, L,
+                         count)) {
+            ++t;
+            continue;
+        }
+        const int nq = min(count, t_end - t);
+        const int first = t;
+        t += nq;
+        auto pages_of = [&](int j) { return (max(L + j, 0) + p.block_size - 1) >> shift; };
+        auto out_of = [&](int j) {
+            return p.pages + ((int64_t)(first + j) * p.r.num_kv_heads + g) * p.top_k;
+        };
+#pragma unroll 1
+        for (int j = 0; j < nq; ++j) {  // rows that take all their pages
+            const int n = pages_of(j);
+            if (n <= p.top_k)
+#pragma unroll 1
+                for (int i = rank * kThreads + threadIdx.x; i < p.top_k; i += C * kThreads)
+                    out_of(j)[i] = i < n ? i : -1;
+        }
+        const int n = pages_of(nq - 1);
+        if (n <= p.top_k) continue;
+        const int per = ((n + C - 1) / C + 15) / 16 * 16;
+        const int base = rank * per, nl = min(max(n - base, 0), per);
 
-    // the group's queries as column fragments
-    for (int i = threadIdx.x; i < 4 * 256; i += kThreads) (&s_hist[0][0])[i] = 0;
-    for (int i = threadIdx.x; i < NT * NCH * 64; i += kThreads)
-        (&s_q[0][0][0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
-    __syncthreads();
-    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) +
-                             ((int64_t)t * p.r.num_kv_heads + g) * G * D;
-    for (int h = warp; h < G; h += kWarps) {
-        uint32_t amax = 0;
-        for (int d = lane; d < D; d += 32)
-            amax = max(amax, (uint32_t)__bfloat16_as_ushort(q[h * D + d]) & 0x7fffu);
-        amax = __reduce_max_sync(0xffffffffu, amax);
-        const bool ok = amax < 0x7f80u;
-        const int e = max((int)(amax >> 7) - 127, -112) - 7;
-        if (lane == 0) s_exp[h] = ok ? e : kNoVote;
-        const float f = ok ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
-        for (int d = lane; d < D; d += 32) {
-            const float c = ok ? rintf(__bfloat162float(q[h * D + d]) * f) : 0.f;
+        // the queries as column fragments
+        if (QT > 1) __syncthreads();  // (the tile's rows before are done)
+#pragma unroll 1
+        for (int i = threadIdx.x; i < 2 * QT * 64; i += kThreads)
+            reinterpret_cast<uint4 *>(&s_hist[0][0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (threadIdx.x < QT) s_left[threadIdx.x] = 0;
+#pragma unroll 1
+        for (int i = threadIdx.x; i < NT * NCH * 64; i += kThreads) s_q[i] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+        for (int i = threadIdx.x; i < NT * 8; i += kThreads) {
+            s_exp[i] = kNoVote;
+            *reinterpret_cast<int4 *>(s_sum[i]) = make_int4(0, 0, 0, 0);
+        }
+        __syncthreads();
+        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) +
+                                 ((int64_t)first * p.r.num_kv_heads + g) * G * D;
+#pragma unroll 1
+        for (int i = warp; i < nq * G; i += kWarps) {
+            const int j = i / G, h = i - j * G, col = j * GP + h;
+            const __nv_bfloat16 *x = q + ((int64_t)j * p.r.num_kv_heads * G + h) * D;
+            constexpr int VL = NCH > 4 ? 8 : NCH > 2 ? 4 : 2;  // values of a lane
+            float v[VL];
+            uint32_t amax = 0;
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {  // against the lower, the upper bounds
-                const int k = part * D + d;
-                const int piece = k >> 6, tq = (k >> 4) & 3, step = (k >> 2) & 3, w = k & 3;
-                // column h % 8, its lane's word 2 * (step % 2) + w / 2, half w % 2
-                __half *dst = reinterpret_cast<__half *>(
-                    &s_q[h >> 3][piece][step >> 1][(h & 7) * 4 + tq]);
-                dst[4 * (step & 1) + w] = __float2half(part ? fmaxf(c, 0.f) : fminf(c, 0.f));
+            for (int m = 0; m < VL; ++m) {
+                const int d = lane + 32 * m;
+                const uint32_t bits = d < D ? (uint32_t)__bfloat16_as_ushort(x[d]) : 0u;
+                amax = max(amax, bits & 0x7fffu);
+                v[m] = __uint_as_float(bits << 16);
+            }
+            amax = __reduce_max_sync(0xffffffffu, amax);
+            if (amax >= 0x7f80u) continue;  // not finite
+            const int e = max((int)(amax >> 7) - 127, -112) - 7;
+            if (lane == 0) s_exp[col] = e;
+            const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+            // channel d is code d against the lower bounds and D + d against the upper:
+            // code k: piece k / 64, lane (col % 8, k / 16 % 4), step k / 4 % 4, its value k % 4
+            const uint32_t at = ((col >> 3) * NCH * 64 + (col & 7) * 4) * 16;
+            int sum = 0;
+#pragma unroll
+            for (int m = 0; m < VL; ++m) {
+                const int d = lane + 32 * m;
+                if (d >= D) break;
+                const float c = rintf(v[m] * f);
+                sum += (int)c;
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    const int k = part * D + d;
+                    const uint32_t o = at + (k >> 6) * 1024 + (k >> 3 & 1) * 512 + (k >> 4 & 3) * 16 +
+                                       (k & 7) * 2;
+                    *reinterpret_cast<__half *>(reinterpret_cast<char *>(s_q) + o) =
+                        __float2half(part ? fmaxf(c, 0.f) : fminf(c, 0.f));
+                }
+            }
+            if (S::OFFSET) {  // of the lanes with the same lane / 4 % 4, and so d / 4 % 4
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                if ((lane & 19) == 0) s_sum[col][lane >> 2] = sum;
             }
         }
-    }
-    for (int h = G + threadIdx.x; h < 16; h += kThreads) s_exp[h] = kNoVote;
-    __syncthreads();
-    int top_e = kNoVote, low_e = 100000;
-    for (int h = 0; h < G; ++h)
-        if (s_exp[h] != kNoVote) {
-            top_e = max(top_e, s_exp[h]);
-            low_e = min(low_e, s_exp[h]);
-        }
-    // the heads' factors are exact relative to the largest, but for exponents further
-    // apart than a float's (then each score is scaled by itself)
-    const bool apart = top_e != kNoVote && top_e - low_e > 126;
-    const int gq = lane >> 2, tq = lane & 3;
-    int ex[NT][2];
-    float fac[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            ex[nt][i] = s_exp[nt * 8 + 2 * tq + i];
-            fac[nt][i] = ex[nt][i] == kNoVote ? 0.f
-                                              : __uint_as_float((uint32_t)(127 + max(ex[nt][i] - top_e, -126)) << 23);
-        }
-
-    // scores of 16 pages at a time
-    const int32_t *bt = p.r.block_table + (int64_t)r * p.r.max_blocks_per_seq;
-    for (int i0 = warp * 16; i0 < nl; i0 += kWarps * 16) {
-        uint4 w[2][NCH];
-        uint32_t byte[2];
-        bool live[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int i = i0 + gq + 8 * j, page = base + i;
-            int id = -1;
-            live[j] = false;
-            if (i < nl) {
-                id = __ldg(bt + page);
-                live[j] = id >= 0 && id < p.r.num_blocks;
-                if (!live[j] && tq == 0) flag_error(p.r.dev_error, PKV_DEVERR_BLOCK_ID);
-            }
-            const int64_t at = (int64_t)(live[j] ? id : 0) * p.r.num_kv_heads + g;
-            byte[j] = live[j] ? p.bounds_scale[at] : 0u;
-            const int8_t *b = p.bounds + at * 2 * D;
-#pragma unroll
-            for (int c = 0; c < NCH; ++c) {
-                const int o = c * 64 + tq * 16;
-                w[j][c] = live[j] && o < 2 * D ? *reinterpret_cast<const uint4 *>(b + o)
-                                               : make_uint4(0u, 0u, 0u, 0u);
-            }
-        }
-        float acc[NT][4];
+        __syncthreads();
+        // The factors of a query's heads are exact relative to the largest, but for
+        // exponents further apart than a float's (then each score is scaled by itself).
+        // Of this lane's columns: exponents, factors, their query's largest exponent.
+        int ex[NT][2], top_e[NT][GP == 1 ? 2 : 1];
+        float fac[NT][2];
+        bool apart = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
-#pragma unroll
-        for (int c = 0; c < NCH; ++c) {
-            const uint32_t w0[4] = {w[0][c].x, w[0][c].y, w[0][c].z, w[0][c].w};
-            const uint32_t w1[4] = {w[1][c].x, w[1][c].y, w[1][c].z, w[1][c].w};
-#pragma unroll
-            for (int s2 = 0; s2 < 2; ++s2) {
-                uint32_t a[2][4];
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    codes_to_f16(w0[2 * s2 + s], a[s][0], a[s][2]);
-                    codes_to_f16(w1[2 * s2 + s], a[s][1], a[s][3]);
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const uint4 b = s_q[nt][c][s2][lane];
-                    mma_f16_16816(acc[nt], a[0][0], a[0][1], a[0][2], a[0][3], b.x, b.y);
-                    mma_f16_16816(acc[nt], a[1][0], a[1][1], a[1][2], a[1][3], b.z, b.w);
-                }
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int be = (int)byte[j] - 127;
-            float m = -INFINITY;
-            if (!apart) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (ex[nt][i] != kNoVote) m = fmaxf(m, acc[nt][2 * j + i] * fac[nt][i]);
-            } else {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (ex[nt][i] != kNoVote)
-                            m = fmaxf(m, ldexpf(acc[nt][2 * j + i], ex[nt][i] + be));
-            }
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            const int i = i0 + gq + 8 * j, page = base + i;
-            if (tq == j && i < nl) {
-                if (!apart && top_e != kNoVote) m = ldexpf(m, top_e + be);
-                if (byte[j] == kScaleNaN) m = INFINITY;
-                uint32_t key = live[j] ? sortable(m + 0.f) : 0u;
-                if (page < p.num_first || page >= n - p.num_recent) key = kForced;
-                s_key[i] = key;
-            }
-        }
-    }
-    __syncthreads();
-
-    // the top_k-th largest, 8 bits at a time
-    uint32_t prefix = 0;
-    int need = p.top_k;
+            for (int i = 0; i < 2; ++i) {
+                const int col = nt * 8 + 2 * tq + i, c0 = col / GP * GP;
+                int top = kNoVote, low = 100000;
 #pragma unroll 1
-    for (int pass = 0; pass < 4; ++pass) {
-        const int shift = 24 - 8 * pass;
-        for (int i = threadIdx.x; i < nl; i += kThreads) {
-            const uint32_t key = s_key[i];
-            if (pass == 0 || (key >> (shift + 8)) == (prefix >> (shift + 8)))
-                atomicAdd(&s_hist[pass][(key >> shift) & 255u], 1u);
+                for (int h = 0; h < GP; ++h) {
+                    const int e = s_exp[c0 + h];
+                    if (e != kNoVote) {
+                        top = max(top, e);
+                        low = min(low, e);
+                    }
+                }
+                ex[nt][i] = s_exp[col];
+                top_e[nt][GP == 1 ? i : 0] = top;
+                apart = apart || (top != kNoVote && top - low > 126);
+                fac[nt][i] = ex[nt][i] == kNoVote
+                                 ? 0.f
+                                 : __uint_as_float((uint32_t)(127 + max(ex[nt][i] - top, -126)) << 23);
+            }
+        apart = __any_sync(0xffffffffu, apart);
+        if (apart)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) fac[nt][0] = fac[nt][1] = 1.f;
+        uint4 qf[NT == 1 ? NCH : 1][2];  // a single tile's columns stay in registers
+        if (NT == 1)
+#pragma unroll
+            for (int c = 0; c < NCH; ++c)
+#pragma unroll
+                for (int s2 = 0; s2 < 2; ++s2) qf[c][s2] = s_q[(c * 2 + s2) * 32 + lane];
+        float off[S::OFFSET ? NT : 1][2][4];  // 1152 times a column's sums, exact
+        if (S::OFFSET)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    off[nt][i / 4][i % 4] = 1152.f * (float)s_sum[nt * 8 + 2 * tq + i / 4][i % 4];
+
+        // scores of 16 pages at a time, this warp's tiles every kWarps-th
+        const int32_t *bt = p.r.block_table + (int64_t)r * p.r.max_blocks_per_seq;
+        const uint32_t ring = smem_u32(s_dyn) + warp * NST * S::STAGE + lane * 16;
+        const int tiles = (nl + 15) / 16, mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
+        auto load_id = [&](int k) {  // of page `lane` (< 16) of tile k
+            const int i = (warp + k * kWarps) * 16 + (lane & 15);
+            return k < mine && i < nl ? __ldg(bt + base + i) : -1;
+        };
+        // Tile k goes to slot k % NST of the ring.  Page ids and scale bytes arrive while the
+        // tile before is worked on: an id is loaded a tile before its page's codes, a byte
+        // with them and put into shared memory a tile later (-1: no page).
+        int *scale = &s_scale[warp][0][0];
+        int byte_ahead = -1;
+        auto issue = [&](int k, int id) {
+            const bool live = id >= 0 && id < p.r.num_blocks;
+            const uint32_t at = (uint32_t)(live ? id : 0) * p.r.num_kv_heads + g;  // < 2^31
+            byte_ahead = live ? (int)p.bounds_scale[at] : -1;
+            if (!live && lane < 16 && (warp + k * kWarps) * 16 + lane < nl)
+                flag_error(p.r.dev_error, PKV_DEVERR_BLOCK_ID);
+            const uint32_t dst = ring + (k % NST) * S::STAGE;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t row = __shfl_sync(0xffffffffu, at, gq + 8 * j);
+                const int8_t *src = p.bounds + (uint64_t)row * (uint32_t)(2 * D) + tq * 16;
+#pragma unroll
+                for (int c = 0; c < NCH; ++c) {  // (pages out of the pool: scores not used)
+                    if (c < NCH - 1)
+                        cp_async16(dst + (j * NCH + c) * 512, src + c * 64);
+                    else
+                        cp_async16_or_zero(dst + (j * NCH + c) * 512, src + c * 64,
+                                           c * 64 + tq * 16 < 2 * D);
+                }
+            }
+        };
+        auto keep_byte = [&](int k) {
+            if (lane < 16) scale[(k % NST) * 16 + lane] = byte_ahead;
+        };
+#pragma unroll 1
+        for (int k = 0; k < NST - 1; ++k) {
+            if (k < mine) {
+                issue(k, load_id(k));
+                if (k < NST - 2) keep_byte(k);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        int next_id = load_id(NST - 1);
+#pragma unroll 1
+        for (int k = 0; k < mine; ++k) {
+            keep_byte(k + NST - 2);
+            if (k + NST - 1 < mine) issue(k + NST - 1, next_id);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            next_id = load_id(k + NST);
+            asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");
+            __syncwarp();
+            const uint32_t tile = ring + (k % NST) * S::STAGE;
+            {
+                // (whole numbers: partial sums in any order give the same)
+                float part[NT][NA][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4 * NA; ++e) part[nt][e / 4][e % 4] = 0.f;
+#pragma unroll
+                for (int c = 0; c < NCH; ++c) {
+                    const uint4 x0 = lds128(tile + c * 512);
+                    const uint4 x1 = lds128(tile + (NCH + c) * 512);
+                    const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w};
+                    const uint32_t w1[4] = {x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+                    for (int s2 = 0; s2 < 2; ++s2) {
+                        uint32_t a[2][4];
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            codes_to_f16<!S::OFFSET>(w0[2 * s2 + s], a[s][0], a[s][2]);
+                            codes_to_f16<!S::OFFSET>(w1[2 * s2 + s], a[s][1], a[s][3]);
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint4 b = NT == 1 ? qf[c % (NT == 1 ? NCH : 1)][s2]
+                                                    : s_q[((nt * NCH + c) * 2 + s2) * 32 + lane];
+                            mma_f16_16816(part[nt][2 * s2 % NA], a[0][0], a[0][1], a[0][2],
+                                          a[0][3], b.x, b.y);
+                            mma_f16_16816(part[nt][(2 * s2 + 1) % NA], a[1][0], a[1][1], a[1][2],
+                                          a[1][3], b.z, b.w);
+                        }
+                    }
+                }
+                float acc[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        acc[nt][e] = 0.f;
+#pragma unroll
+                        for (int i = 0; i < NA; ++i)
+                            acc[nt][e] += S::OFFSET
+                                              ? part[nt][i][e] - off[S::OFFSET ? nt : 0][e & 1][i]
+                                              : part[nt][i][e];
+                    }
+                // The best of a query's heads: of this lane's columns, then of the lanes that
+                // hold the query's other columns.
+                const int i0 = (warp + k * kWarps) * 16 + gq;
+                auto vote = [&](int nt, int j, int c) {
+                    const float x = acc[nt][2 * j + c] * fac[nt][c];
+                    return ex[nt][c] == kNoVote ? -INFINITY : x;
+                };
+                auto best = [&](int nt, int j) { return fmaxf(vote(nt, j, 0), vote(nt, j, 1)); };
+                auto store = [&](int query, float m, int top, int i, int byte, bool here) {
+                    if (!apart && top != kNoVote) m = scaled(m, top + byte - 127);
+                    if (byte == (int)kScaleNaN) m = INFINITY;
+                    uint32_t key = byte >= 0 ? sortable(m + 0.f) : 0u;
+                    const int page = base + i;
+                    if (page < p.num_first || page >= pages_of(query) - p.num_recent) key = kForced;
+                    if (here && i < nl && query < nq) s_key[query * p.cap + i] = key;
+                };
+                const int *bytes = scale + (k % NST) * 16 + gq;
+                if (apart) {  // rare: every score by itself, scaled before the heads are compared
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (ex[nt][e & 1] != kNoVote)
+                                acc[nt][e] = scaled(acc[nt][e],
+                                                    ex[nt][e & 1] + bytes[8 * (e >> 1)] - 127);
+                }
+                if constexpr (GP >= 4) {
+                    // a query's lanes have its score for both rows: even ones store the first
+                    const int j = tq & 1, i = i0 + 8 * j, byte = bytes[8 * j];
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt += GP == 16 ? 2 : 1) {
+                        float m[2];
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            m[r] = best(nt, r);
+                            if (GP == 16) m[r] = fmaxf(m[r], best(nt + 1, r));
+                            m[r] = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], 1));
+                            if (GP >= 8) m[r] = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], 2));
+                        }
+                        store((nt * 8 + 2 * tq) / GP, j ? m[1] : m[0], top_e[nt][0], i, byte,
+                              GP == 4 || tq < 2);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int i = i0 + 8 * j, byte = bytes[8 * j];
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (GP == 2) {
+                                store(nt * 4 + tq, best(nt, j), top_e[nt][0], i, byte, true);
+                            } else {
+                                store(nt * 8 + 2 * tq, vote(nt, j, 0), top_e[nt][0], i, byte, true);
+                                store(nt * 8 + 2 * tq + 1, vote(nt, j, 1), top_e[nt][GP == 1], i,
+                                      byte, true);
+                            }
+                        }
+                    }
+                }
+            }
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+
+        // The top_k-th largest score; a group of warps for each query.  The digits begin
+        // below the leading bits that all scores share, and end when few enough are left
+        // to be ranked against one another.  (Tiles shared by a cluster take all 32 bits in
+        // the same steps: their barriers are the whole cluster's.)
+        const int mq = warp / S::GROUP, li = threadIdx.x - mq * GS;
+        const int nrow = mq < nq ? pages_of(mq) : 0;
+        const bool choose = nrow > p.top_k;
+        const int nlr = choose ? min(max(nrow - base, 0), per) : 0;
+        const uint32_t *key_row = s_key + mq * p.cap;
+        const bool fixed = QT > 1 && C > 1;
+        auto sync = [&] {
+            if (C > 1)
+                cluster_sync();
+            else if (S::GROUP == 1)
+                __syncwarp();
+            else
+                asm volatile("bar.sync %0, %1;" ::"r"(mq + 1), "n"(GS) : "memory");
+        };
+        uint32_t prefix = 0;  // of the scores that are left: the bits from `digit` up
+        int need = p.top_k, left = 0, digit = 32, pass = 0;
+        if (!fixed) {
+            need -= p.num_first + p.num_recent;  // forced ones are above all others
+            uint32_t lo = 0xffffffffu, hi = 0;
+#pragma unroll 1
+            for (int i = li; i < nlr; i += GS) {
+                const uint32_t key = key_row[i];
+                if (key != kForced) {
+                    lo = min(lo, key);
+                    hi = max(hi, key);
+                }
+            }
+            lo = __reduce_min_sync(0xffffffffu, lo);
+            hi = __reduce_max_sync(0xffffffffu, hi);
+            if (S::GROUP > 1 || C > 1) {
+                if (lane == 0) {
+                    s_range[warp][0] = lo;
+                    s_range[warp][1] = hi;
+                }
+                sync();
+#pragma unroll 1
+                for (int c = 0; c < C; ++c)
+#pragma unroll 1
+                    for (int w = mq * S::GROUP; w < (mq + 1) * S::GROUP; ++w) {
+                        const uint32_t at = smem_u32(&s_range[w][0]);
+                        lo = min(lo, C > 1 ? cluster_ld32(cluster_addr(at, c)) : s_range[w][0]);
+                        hi = max(hi, C > 1 ? cluster_ld32(cluster_addr(at + 4, c)) : s_range[w][1]);
+                    }
+            }
+            if (need == 0) lo = hi = kForced - 1;  // none but the forced ones
+            digit = lo < hi ? 32 - __clz(lo ^ hi) : 0;
+            prefix = digit == 32 ? 0u : lo >> digit << digit;
+        }
+        bool ranked = false;
+        while (choose || fixed) {
+            if (digit == 0) break;
+            const int next = fixed ? digit - 8 : max(digit - 8, 0);
+            const uint32_t mask = (1u << (digit - next)) - 1u;
+            uint32_t *hist = s_hist[pass & 1][mq], *other = s_hist[(pass + 1) & 1][mq];
+#pragma unroll 1
+            for (int i = li; i < nlr; i += GS) {
+                const uint32_t key = key_row[i];
+                if ((digit == 32 || ((key ^ prefix) >> digit) == 0) && (fixed || key != kForced))
+                    atomicAdd(&hist[(key >> next) & mask], 1u);
+            }
+            sync();
+            // thread li: bins 255 - li * BPT and below, so that a prefix sum counts from
+            // the largest down
+            uint32_t v[BPT], own = 0;
+#pragma unroll
+            for (int b = 0; b < BPT; ++b) {
+                const int bin = 255 - li * BPT - b;
+                v[b] = 0;
+                if (C > 1)  // (C: 2, 4, 8 or 16; pairs of loads in flight)
+#pragma unroll 1
+                    for (int c = 0; c < C; c += 2) {
+                        const uint32_t at = smem_u32(&hist[bin]);
+                        const uint32_t x = cluster_ld32(cluster_addr(at, c));
+                        const uint32_t y = cluster_ld32(cluster_addr(at, c + 1));
+                        v[b] += x + y;
+                    }
+                else
+                    v[b] = hist[bin];
+                own += v[b];
+            }
+            uint32_t sum = own;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const uint32_t o = __shfl_up_sync(0xffffffffu, sum, off);
+                if (lane >= off) sum += o;
+            }
+            auto group_sync = [&] {  // (the cluster's CTAs stay together by themselves)
+                if (S::GROUP == 1)
+                    __syncwarp();
+                else
+                    asm volatile("bar.sync %0, %1;" ::"r"(mq + 1), "n"(GS) : "memory");
+            };
+            if (S::GROUP > 1) {
+                if (lane == 31) s_cnt[warp][0] = (int)sum;
+                group_sync();
+#pragma unroll 1
+                for (int w = mq * S::GROUP; w < warp; ++w) sum += (uint32_t)s_cnt[w][0];
+            }
+            if (choose && sum >= (uint32_t)need && sum - own < (uint32_t)need) {
+                uint32_t before = sum - own;
+#pragma unroll
+                for (int b = 0; b < BPT; ++b) {
+                    if (before < (uint32_t)need && before + v[b] >= (uint32_t)need) {
+                        s_pick[mq][0] = (uint32_t)(255 - li * BPT - b);
+                        s_pick[mq][1] = before;
+                        s_pick[mq][2] = v[b];
+                    }
+                    before += v[b];
+                }
+            }
+            // the other buffer: read before this pass's barrier, counted in after the next
+            if (pass > 0)
+#pragma unroll 1
+                for (int i = li; i < 256; i += GS) other[i] = 0;
+            group_sync();
+            ++pass;
+            digit = next;
+            if (choose) {
+                prefix |= s_pick[mq][0] << digit;
+                need -= (int)s_pick[mq][1];
+                left = (int)s_pick[mq][2];
+            }
+            group_sync();
+            if (!fixed && digit > 0 && left <= kRank) {
+                ranked = true;
+                break;
+            }
+        }
+        if (ranked) {
+            // the scores left, with their pages: [kRank] keys, then [kRank] pages
+            uint32_t *list = s_hist[pass & 1][mq], *all = list;  // (all zeros, read by no one)
+#pragma unroll 1
+            for (int i = li; i < nlr; i += GS) {
+                const uint32_t key = key_row[i];
+                if (key != kForced && ((key ^ prefix) >> digit) == 0) {
+                    const int at = atomicAdd(&s_left[mq], 1);
+                    list[at] = key;
+                    list[kRank + at] = (uint32_t)(base + i);
+                }
+            }
+            sync();
+            if (C > 1) {  // of the whole cluster, in the buffer whose counts are read
+                all = s_hist[(pass + 1) & 1][mq];
+#pragma unroll 1
+                for (int i = li; i < left; i += GS) {
+                    int c = 0, at = i;
+                    for (; c < C - 1; ++c) {
+                        const int m = (int)cluster_ld32(cluster_addr(smem_u32(&s_left[mq]), c));
+                        if (at < m) break;
+                        at -= m;
+                    }
+                    all[i] = cluster_ld32(cluster_addr(smem_u32(&list[at]), c));
+                    all[kRank + i] = cluster_ld32(cluster_addr(smem_u32(&list[kRank + at]), c));
+                }
+                sync();
+            }
+#pragma unroll 1
+            for (int i = li; i < left; i += GS) {
+                const uint32_t key = all[i], page = all[kRank + i];
+                int above = 0, equal = 0;  // equal ones with lower pages
+#pragma unroll 1
+                for (int j = 0; j < left; ++j) {
+                    above += all[j] > key;
+                    equal += all[j] == key && all[kRank + j] < page;
+                }
+                if (above + equal == need - 1) {  // the last one that is taken
+                    s_pick[mq][0] = key;
+                    s_pick[mq][1] = (uint32_t)equal + 1;
+                }
+            }
+            sync();
+            prefix = s_pick[mq][0];
+            need = (int)s_pick[mq][1];
+        }
+        __syncthreads();  // s_cnt is used again
+
+        // pages above it, and the first `need` of those equal to it, in ascending order
+        const int seg = ((nlr + S::GROUP - 1) / S::GROUP + 31) / 32 * 32;
+        const int lo = min((warp - mq * S::GROUP) * seg, nlr), hi = min(lo + seg, nlr);
+        int above = 0, equal = 0;
+#pragma unroll 1
+        for (int i = lo; i < hi; i += 32) {
+            const bool in = i + lane < hi;
+            const uint32_t key = in ? key_row[i + lane] : 0u;
+            above += __popc(__ballot_sync(0xffffffffu, in && key > prefix));
+            equal += __popc(__ballot_sync(0xffffffffu, in && key == prefix));
+        }
+        if (lane == 0) {
+            s_cnt[warp][0] = above;
+            s_cnt[warp][1] = equal;
+        }
+        __syncthreads();
+        if (li < 2) {
+            int s = 0;
+#pragma unroll 1
+            for (int w = 0; w < S::GROUP; ++w) s += s_cnt[mq * S::GROUP + w][li];
+            s_total[mq][li] = s;
         }
         block_sync(C > 1);
-        // thread b: bin 255 - b, so that a prefix sum counts from the largest down
-        uint32_t v = 0;
-        const uint32_t at = smem_u32(&s_hist[pass][255 - threadIdx.x]);
-        if (C > 1)
-            for (int c = 0; c < C; ++c) v += cluster_ld32(cluster_addr(at, c));
-        else
-            v = s_hist[pass][255 - threadIdx.x];
-        uint32_t sum = v;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const uint32_t o = __shfl_up_sync(0xffffffffu, sum, off);
-            if (lane >= off) sum += o;
+        int n_above = 0, n_equal = 0;  // before this warp's pages
+#pragma unroll 1
+        for (int c = 0; c < rank; ++c) {
+            n_above += (int)cluster_ld32(cluster_addr(smem_u32(&s_total[mq][0]), c));
+            n_equal += (int)cluster_ld32(cluster_addr(smem_u32(&s_total[mq][1]), c));
         }
-        if (lane == 31) s_cnt[warp][0] = (int)sum;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) sum += (uint32_t)s_cnt[w][0];
-        if (sum >= (uint32_t)need && sum - v < (uint32_t)need) {
-            s_pick[0] = 255u - threadIdx.x;
-            s_pick[1] = sum - v;
+#pragma unroll 1
+        for (int w = mq * S::GROUP; w < warp; ++w) {
+            n_above += s_cnt[w][0];
+            n_equal += s_cnt[w][1];
         }
-        __syncthreads();
-        prefix |= s_pick[0] << shift;
-        need -= (int)s_pick[1];
-        __syncthreads();  // s_pick and s_cnt are used again
+        const uint32_t below = (1u << lane) - 1u;
+        int32_t *out = out_of(mq);
+#pragma unroll 1
+        for (int i = lo; i < hi; i += 32) {
+            const bool in = i + lane < hi;
+            const uint32_t key = in ? key_row[i + lane] : 0u;
+            const uint32_t ma = __ballot_sync(0xffffffffu, in && key > prefix);
+            const uint32_t me = __ballot_sync(0xffffffffu, in && key == prefix);
+            const int a = n_above + __popc(ma & below), e = n_equal + __popc(me & below);
+            if (in && (key > prefix || (key == prefix && e < need)))
+                out[a + min(e, need)] = base + i + lane;
+            n_above += __popc(ma);
+            n_equal += __popc(me);
+        }
+        if (C > 1) cluster_sync();  // the others may still read this CTA's counts
     }
+}
 
-    // pages above it, and the first `need` of those equal to it, in ascending order
-    const int seg = ((nl + kWarps - 1) / kWarps + 31) / 32 * 32;
-    const int lo = min(warp * seg, nl), hi = min(lo + seg, nl);
-    int above = 0, equal = 0;
-    for (int i = lo; i < hi; i += 32) {
-        const uint32_t key = i + lane < hi ? s_key[i + lane] : 0u;
-        const bool in = i + lane < hi;
-        above += __popc(__ballot_sync(0xffffffffu, in && key > prefix));
-        equal += __popc(__ballot_sync(0xffffffffu, in && key == prefix));
-    }
-    if (lane == 0) {
-        s_cnt[warp][0] = above;
-        s_cnt[warp][1] = equal;
-    }
-    __syncthreads();
-    if (threadIdx.x < 2) {
-        int s = 0;
-        for (int w = 0; w < kWarps; ++w) s += s_cnt[w][threadIdx.x];
-        s_total[threadIdx.x] = s;
-    }
-    block_sync(C > 1);
-    int n_above = 0, n_equal = 0;  // before this warp's pages
-    for (int c = 0; c < rank; ++c) {
-        n_above += (int)cluster_ld32(cluster_addr(smem_u32(&s_total[0]), c));
-        n_equal += (int)cluster_ld32(cluster_addr(smem_u32(&s_total[1]), c));
-    }
-    for (int w = 0; w < warp; ++w) {
-        n_above += s_cnt[w][0];
-        n_equal += s_cnt[w][1];
-    }
-    const uint32_t below = (1u << lane) - 1u;
-    for (int i = lo; i < hi; i += 32) {
-        const bool in = i + lane < hi;
-        const uint32_t key = in ? s_key[i + lane] : 0u;
-        const uint32_t ma = __ballot_sync(0xffffffffu, in && key > prefix);
-        const uint32_t me = __ballot_sync(0xffffffffu, in && key == prefix);
-        const int a = n_above + __popc(ma & below), e = n_equal + __popc(me & below);
-        if (in && (key > prefix || (key == prefix && e < need))) out[a + min(e, need)] = base + i + lane;
-        n_above += __popc(ma);
-        n_equal += __popc(me);
-    }
-    if (C > 1) cluster_sync();  // the others may still read this CTA's counts
+template <int NCH, int NT, int GP>
+int smem_bytes(int cap) {
+    return Shape<NCH, NT, GP>::KEY_OFF + Shape<NCH, NT, GP>::QT * cap * 4;
+}
+
+constexpr int kMaxSmem = 208 * 1024;  // beside at most 17 KB of the kernel's own
+
+template <int NCH, int NT, int GP>
+cudaError_t launch_as(SelectParams p, bool &fits, cudaStream_t stream) {
+    using S = Shape<NCH, NT, GP>;
+    auto kern = select_pages_kernel<NCH, NT, GP>;
+    const int64_t units = (p.r.rows + (int64_t)S::QT - 1) / S::QT * p.r.num_kv_heads;
+    const int n = (p.r.max_seqlen + p.block_size - 1) >> p.bs_shift;
+    // as many CTAs per tile as there is room for at once, of at least 256 pages, and
+    // more if the scores would not fit
+    int c = 1;
+    auto cap = [&] { return ((n + c - 1) / c + 15) / 16 * 16; };
+    while (c < 16 && ((units * c < 2LL * device_sm_count() && n / c >= 512) ||
+                      smem_bytes<NCH, NT, GP>(cap()) > kMaxSmem))
+        c *= 2;
+    fits = smem_bytes<NCH, NT, GP>(cap()) <= kMaxSmem && units * c <= 0x7fffffff;
+    if (!fits) return cudaErrorNotSupported;
+    p.cluster = c;
+    p.cap = cap();
+    const int smem = smem_bytes<NCH, NT, GP>(p.cap);
+    cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), smem);
+    if (e == cudaSuccess && c > 8) e = ensure_wide_clusters(reinterpret_cast<const void *>(kern));
+    if (e != cudaSuccess) return e;
+    return launch_cluster(kern, (unsigned)(units * c), c, S::WARPS * 32, (size_t)smem, stream, p);
 }
 
 template <int NCH>
 cudaError_t launch_n(const SelectParams &p, cudaStream_t stream) {
-    auto kern = p.r.group <= 8 ? select_pages_kernel<NCH, 1> : select_pages_kernel<NCH, 2>;
-    const int smem = p.cap * 4;
-    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), smem);
-    if (e != cudaSuccess) return e;
-    const int64_t grid = (int64_t)p.r.rows * p.r.num_kv_heads * p.cluster;
-    if (grid > 0x7fffffff) return cudaErrorNotSupported;
-    return launch_cluster(kern, (unsigned)grid, p.cluster, kThreads, (size_t)smem, stream, p);
+    bool fits = false;
+    const int G = p.r.group;
+    // Tiles of queries where requests have several (4 on average); long contexts whose
+    // scores do not fit go on with one query at a time.
+    if (p.r.cu_q && p.r.rows >= 4LL * p.r.batch) {
+        const cudaError_t e = G == 1   ? launch_as<NCH, 1, 1>(p, fits, stream)
+                              : G == 2 ? launch_as<NCH, 2, 2>(p, fits, stream)
+                              : G <= 4 ? launch_as<NCH, 4, 4>(p, fits, stream)
+                              : G <= 8 ? launch_as<NCH, 8, 8>(p, fits, stream)
+                                       : launch_as<NCH, 8, 16>(p, fits, stream);
+        if (fits) return e;
+    }
+    return G <= 8 ? launch_as<NCH, 1, 8>(p, fits, stream) : launch_as<NCH, 2, 16>(p, fits, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_select_pages(const SelectParams &p0, cudaStream_t stream) {
-    SelectParams p = p0;
-    const int64_t units = (int64_t)p.r.rows * p.r.num_kv_heads;
-    const int n = (p.r.max_seqlen + p.block_size - 1) / p.block_size;
-    // as many CTAs per row as there is room for at once, of at least 128 pages, and
-    // more if the scores would not fit
-    int c = 1;
-    while (c < 8 && ((units * c < 2LL * device_sm_count() && n / c >= 256) || n / c > 32768)) c *= 2;
-    p.cluster = c;
-    p.cap = ((n + c - 1) / c + 15) / 16 * 16;
-    if (p.cap > 49152) return cudaErrorNotSupported;
+cudaError_t launch_select_pages(const SelectParams &p, cudaStream_t stream) {
     switch ((2 * p.r.head_dim + 63) / 64) {
     case 2: return launch_n<2>(p, stream);
     case 3: return launch_n<3>(p, stream);

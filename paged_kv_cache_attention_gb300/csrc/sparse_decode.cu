@@ -85,8 +85,9 @@ sparse_decode_kernel(const SparseParams p, const __grid_constant__ CUtensorMap t
     }
     pdl_wait();
     const bool first = g == 0 && rank == 0;
-    int r, L;
-    if (!row_request(p.r, t, BS, first && threadIdx.x == 0, r, L)) return;
+    int r, L, count;
+    if (!row_request(p.r, t, BS, first && threadIdx.x == 0, r, L, count)) return;
+    L = max(L, 0);
     const int npages = (L + BS - 1) / BS;
     const int32_t *list = p.pages + unit * p.top_k;
     const int n = list_length<kThreads>(list, p.top_k, npages, p.r.dev_error, rank == 0,

@@ -84,6 +84,24 @@ def test_chunks(queries, lens):
     check(c, 12, recent=2, chunk=True, extra=5)
 
 
+@pytest.mark.parametrize("hq,hkv,d,bs", [(2, 2, 64, 16), (4, 2, 80, 32), (6, 2, 128, 16),
+                                         (8, 2, 256, 16), (5, 1, 96, 32), (8, 1, 128, 16),
+                                         (11, 1, 112, 16), (32, 2, 128, 32), (16, 1, 256, 16)])
+def test_tiles_of_queries(hq, hkv, d, bs):
+    """Every width of a group; tiles that hold the ends of requests, and rows of which
+    some take all their pages."""
+    c = make([37 * bs + 5, 3, 200 * bs, 21 * bs + 1], [11, 3, 19, 9], hq, hkv, d, bs)
+    check(c, 20, recent=2, extra=2)
+    check(c, 1, first=0)
+
+
+@pytest.mark.parametrize("n", [3000, 70000, 300000])
+def test_tiles_over_long_contexts(n):
+    """Clusters share a tile's pages; one query at a time where the scores do not fit."""
+    check(make([n], [5], 4, 1, 64, 16, spread=3), 64, recent=3)
+    check(make([n], [4], 1, 1, 64, 16, spread=3), 200)
+
+
 @pytest.mark.parametrize("queries,lens", [([6, 4], [3, 100]), ([5], [0])])
 def test_rows_before_the_first_position(queries, lens):
     """More queries than keys: rows without a key have empty lists."""

@@ -98,8 +98,9 @@ def test_select_shapes(shape, expected):
     (dict(first=7), LAUNCHED), (dict(first=8), INVALID), (dict(recent=9), INVALID),
     (dict(first=2 ** 31 - 1, recent=2 ** 31 - 1), INVALID),
     (dict(max_seqlen=-1), INVALID), (dict(max_seqlen=0), LAUNCHED),
-    (dict(max_seqlen=393216 * 16), LAUNCHED), (dict(max_seqlen=393216 * 16 + 1), UNSUPPORTED),
-    (dict(max_seqlen=(1 << 30) + 1), UNSUPPORTED), (dict(b=None), INVALID), (dict(s=None), INVALID),
+    (dict(max_seqlen=262144 * 16), LAUNCHED), (dict(max_seqlen=262144 * 16 + 1), UNSUPPORTED),
+    (dict(max_seqlen=262144 * 32, bs=32, d=256, hq=128), LAUNCHED),
+    (dict(max_seqlen=2 ** 31 - 1), UNSUPPORTED), (dict(b=None), INVALID), (dict(s=None), INVALID),
     (dict(b=FAKE + 8), INVALID),
 ])
 def test_select_arguments(kw, expected):
