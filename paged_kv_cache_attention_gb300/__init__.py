@@ -1227,41 +1227,66 @@ def update_block_tables(block_table, old_seqlens, new_seqlens, free_blocks, num_
     all slots are -1 and all offsets 0."""
     ty = _types()
     dev = _cuda_index("block_table", block_table)
-    _arg("block_table", block_table, ty.i32, 2, dev)
+    i32 = ty.i32
+    shape = old_seqlens.shape
+    if not (block_table.dtype is old_seqlens.dtype is new_seqlens.dtype is free_blocks.dtype
+            is num_free.dtype is i32 and block_table.dim() == 2 and block_table.is_contiguous()
+            and old_seqlens.is_contiguous() and new_seqlens.is_contiguous()
+            and free_blocks.is_contiguous() and free_blocks.dim() == 1
+            and shape == new_seqlens.shape == block_table.shape[:1] and num_free.numel() == 1
+            and num_free.dim() == 1 and dev == old_seqlens.get_device() == new_seqlens.get_device()
+            == free_blocks.get_device() == num_free.get_device()):
+        _arg("block_table", block_table, i32, 2, dev)
+        _arg_vector("old_seqlens", old_seqlens, i32, block_table.shape[0], dev)
+        _arg_vector("new_seqlens", new_seqlens, i32, block_table.shape[0], dev)
+        _arg("free_blocks", free_blocks, i32, 1, dev)
+        _arg_vector("num_free", num_free, i32, 1, dev)
     B, max_blocks = block_table.shape
-    _arg_vector("old_seqlens", old_seqlens, ty.i32, B, dev)
-    _arg_vector("new_seqlens", new_seqlens, ty.i32, B, dev)
-    _arg("free_blocks", free_blocks, ty.i32, 1, dev)
-    _arg_vector("num_free", num_free, ty.i32, 1, dev)
+    nb = free_blocks.shape[0]
     num_rows, block_size = _int32("num_rows", num_rows), _int32("block_size", block_size)
     _require(num_rows >= 0, "num_rows must not be negative")
-    if slot_mapping is not None:
-        _arg_vector("slot_mapping", slot_mapping, ty.i64, num_rows, dev)
-    if positions is not None:
-        _arg_vector("positions", positions, ty.i64, num_rows, dev)
-    if cu_seq_lens_q is not None:
-        _arg_vector("cu_seq_lens_q", cu_seq_lens_q, ty.i32, B + 1, dev)
-    if cu_seq_lens_k is not None:
-        _arg_vector("cu_seq_lens_k", cu_seq_lens_k, ty.i32, B + 1, dev)
     err = _error_word(dev_error, dev)
-    given = [(n, t) for n, t in (
-        ("block_table", block_table), ("free_blocks", free_blocks), ("num_free", num_free),
-        ("slot_mapping", slot_mapping), ("positions", positions),
-        ("cu_seq_lens_q", cu_seq_lens_q), ("cu_seq_lens_k", cu_seq_lens_k)) if t is not None]
-    _disjoint(given + [("old_seqlens", old_seqlens)])
-    _disjoint(given + [("new_seqlens", new_seqlens)])
+    # what is changed in place lies apart from the rest
+    t0, f0, n0 = block_table.data_ptr(), free_blocks.data_ptr(), num_free.data_ptr()
+    o0, w0 = old_seqlens.data_ptr(), new_seqlens.data_ptr()
+    t1, f1, lb = t0 + 4 * B * max_blocks, f0 + 4 * nb, 4 * B
+    fresh = (slot_mapping is None and positions is None and cu_seq_lens_q is None
+             and cu_seq_lens_k is None)
+    if not (fresh and (t1 <= f0 or f1 <= t0) and not (t0 <= n0 < t1 or f0 <= n0 < f1)
+            and (o0 + lb <= t0 or t1 <= o0) and (w0 + lb <= t0 or t1 <= w0)
+            and (o0 + lb <= f0 or f1 <= o0) and (w0 + lb <= f0 or f1 <= w0)
+            and not (o0 <= n0 < o0 + lb or w0 <= n0 < w0 + lb)):
+        if slot_mapping is not None:
+            _arg_vector("slot_mapping", slot_mapping, ty.i64, num_rows, dev)
+        if positions is not None:
+            _arg_vector("positions", positions, ty.i64, num_rows, dev)
+        if cu_seq_lens_q is not None:
+            _arg_vector("cu_seq_lens_q", cu_seq_lens_q, i32, B + 1, dev)
+        if cu_seq_lens_k is not None:
+            _arg_vector("cu_seq_lens_k", cu_seq_lens_k, i32, B + 1, dev)
+        given = [(n, t) for n, t in (
+            ("block_table", block_table), ("free_blocks", free_blocks), ("num_free", num_free),
+            ("slot_mapping", slot_mapping), ("positions", positions),
+            ("cu_seq_lens_q", cu_seq_lens_q), ("cu_seq_lens_k", cu_seq_lens_k)) if t is not None]
+        _disjoint(given + [("old_seqlens", old_seqlens)])
+        _disjoint(given + [("new_seqlens", new_seqlens)])
     lib = load_library()
 
     def call(handle):
         empty, device = ty.torch.empty, block_table.device
-        slots = empty(num_rows, dtype=ty.i64, device=device) if slot_mapping is None else slot_mapping
-        pos = empty(num_rows, dtype=ty.i64, device=device) if positions is None else positions
-        cuq = empty(B + 1, dtype=ty.i32, device=device) if cu_seq_lens_q is None else cu_seq_lens_q
-        cuk = empty(B + 1, dtype=ty.i32, device=device) if cu_seq_lens_k is None else cu_seq_lens_k
+        if fresh:
+            slots, pos = empty((2, num_rows), dtype=ty.i64, device=device).unbind(0)
+            cuq, cuk = empty((2, B + 1), dtype=i32, device=device).unbind(0)
+        else:
+            slots = empty(num_rows, dtype=ty.i64, device=device) if slot_mapping is None else slot_mapping
+            pos = empty(num_rows, dtype=ty.i64, device=device) if positions is None else positions
+            cuq = empty(B + 1, dtype=i32, device=device) if cu_seq_lens_q is None else cu_seq_lens_q
+            cuk = empty(B + 1, dtype=i32, device=device) if cu_seq_lens_k is None else cu_seq_lens_k
+        sp, cp = slots.data_ptr(), cuq.data_ptr()
         return (slots, pos, cuq, cuk), lib.pkv_update_block_tables(
-            block_table.data_ptr(), max_blocks, old_seqlens.data_ptr(), new_seqlens.data_ptr(), B,
-            free_blocks.data_ptr(), free_blocks.shape[0], num_free.data_ptr(), block_size,
-            slots.data_ptr(), pos.data_ptr(), num_rows, cuq.data_ptr(), cuk.data_ptr(), err, handle)
+            t0, max_blocks, o0, w0, B, f0, nb, n0, block_size, sp,
+            sp + 8 * num_rows if fresh else pos.data_ptr(), num_rows, cp,
+            cp + 4 * B + 4 if fresh else cuk.data_ptr(), err, handle)
     outs, st = _on_stream(dev, stream, call)
     if st:
         _check("pkv_update_block_tables", st)
@@ -1271,10 +1296,14 @@ def update_block_tables(block_table, old_seqlens, new_seqlens, free_blocks, num_
 def _bounds(page_bounds, bounds_scale, dev: int):
     """Checks the bounds of a pool's pages; returns (num_blocks, num_kv_heads, head_dim)."""
     ty = _types()
-    _arg("page_bounds", page_bounds, ty.i8, 4, dev)
+    if not (page_bounds.dtype is ty.i8 and bounds_scale.dtype is ty.u8 and page_bounds.dim() == 4
+            and page_bounds.is_contiguous() and bounds_scale.is_contiguous()
+            and page_bounds.get_device() == bounds_scale.get_device() == dev
+            and bounds_scale.shape == page_bounds.shape[:2]):
+        _arg("page_bounds", page_bounds, ty.i8, 4, dev)
+        _arg_shape("bounds_scale", bounds_scale, ty.u8, page_bounds.shape[:2], dev)
     nb, hkv, two, d = page_bounds.shape
     _require(two == 2, "page_bounds must be [num_blocks, num_kv_heads, 2, head_dim]")
-    _arg_shape("bounds_scale", bounds_scale, ty.u8, (nb, hkv), dev)
     return nb, hkv, d
 
 
@@ -1296,7 +1325,9 @@ def update_page_bounds(k_cache, page_bounds, bounds_scale, slot_mapping, k_scale
     nb, hkv, d = _bounds(page_bounds, bounds_scale, dev)
     _require((nb, hkv, d) == (desc.num_blocks, desc.num_kv_heads, desc.head_dim),
              "page_bounds must be [num_blocks, num_kv_heads, 2, head_dim] of the cache")
-    _arg("slot_mapping", slot_mapping, ty.i64, 1, dev)
+    if not (slot_mapping.dtype is ty.i64 and slot_mapping.dim() == 1
+            and slot_mapping.get_device() == dev and slot_mapping.is_contiguous()):
+        _arg("slot_mapping", slot_mapping, ty.i64, 1, dev)
     err = _error_word(dev_error, dev)
     lib = load_library()
 
@@ -1312,14 +1343,19 @@ def update_page_bounds(k_cache, page_bounds, bounds_scale, slot_mapping, k_scale
 def _rows(q, head_dim: int, block_table, cache_seqlens, cu_seq_lens_q, dev: int):
     """Checks the queries and their requests; returns (total_q, Hq, batch, max_blocks)."""
     ty = _types()
-    _arg("q", q, ty.bf16, 3, dev)
+    if not (q.dtype is ty.bf16 and block_table.dtype is cache_seqlens.dtype is ty.i32
+            and q.dim() == 3 and block_table.dim() == 2 and q.is_contiguous()
+            and block_table.is_contiguous() and cache_seqlens.is_contiguous()
+            and dev == q.get_device() == block_table.get_device() == cache_seqlens.get_device()
+            and cache_seqlens.shape == block_table.shape[:1]):
+        _arg("q", q, ty.bf16, 3, dev)
+        _arg("cache_seqlens", cache_seqlens, ty.i32, 1, dev)
+        _arg("block_table", block_table, ty.i32, 2, dev)
+        _require(block_table.shape[0] == cache_seqlens.shape[0],
+                 "block_table must have one row per request")
     total_q, Hq, D = q.shape
+    B, max_blocks = block_table.shape
     _require(D == head_dim, "head_dim of q and cache differ")
-    _arg("cache_seqlens", cache_seqlens, ty.i32, 1, dev)
-    B = cache_seqlens.shape[0]
-    _arg("block_table", block_table, ty.i32, 2, dev)
-    rows, max_blocks = block_table.shape
-    _require(rows == B, "block_table must have one row per request")
     if cu_seq_lens_q is not None:
         _arg_vector("cu_seq_lens_q", cu_seq_lens_q, ty.i32, B + 1, dev)
     else:
@@ -1386,9 +1422,12 @@ def paged_sparse_attention(q, k_cache, v_cache, block_table, cache_seqlens, page
         desc = _fp8_pools(k_cache, v_cache, k_scale, v_scale, layout, dev)
     total_q, Hq, B, max_blocks = _rows(q, desc.head_dim, block_table, cache_seqlens,
                                        cu_seq_lens_q, dev)
-    _arg("pages", pages, ty.i32, 3, dev)
-    top_k = pages.shape[2]
-    _arg_shape("pages", pages, ty.i32, (total_q, desc.num_kv_heads, top_k), dev)
+    shape = pages.shape
+    top_k = shape[-1]
+    if not (pages.dtype is ty.i32 and shape == (total_q, desc.num_kv_heads, top_k)
+            and pages.get_device() == dev and pages.is_contiguous()):
+        _arg("pages", pages, ty.i32, 3, dev)
+        _arg_shape("pages", pages, ty.i32, (total_q, desc.num_kv_heads, top_k), dev)
     _attention_extras(sink, None, out, lse, q, total_q, Hq, dev)
     err = _error_word(dev_error, dev)
     scale = float(sm_scale) if sm_scale is not None else desc.head_dim ** -0.5

@@ -29,43 +29,63 @@ constexpr int kThreads = 512;
 constexpr int kCluster = 8;
 constexpr int kRowsHere = 16384;
 constexpr int kRowThreads = 256;
-constexpr int kRowsPerCta = 2048;
+constexpr int kAtOnce = 4;  // searches and loads that a thread has in flight
+constexpr int kRowsPerCta = kRowThreads * kAtOnce;
 
-// Largest r in [0, n) with cu[r] <= i (cu[0] = 0 <= i): the request of item i.
-__device__ __forceinline__ int find(const int32_t *cu, int n, int i) {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cu[mid] <= i)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return lo;
+
+// For each of i: the largest r in [0, n) with cu[r] <= i (cu[0] = 0 <= i), the request
+// of item i.  step: the largest power of two below n (0 for n <= 1).
+__device__ __forceinline__ void find(const int32_t *cu, int n, int step, const int (&i)[kAtOnce],
+                                     int (&r)[kAtOnce]) {
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) r[k] = 0;
+    for (; step > 0; step >>= 1)
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+            if (r[k] + step < n && cu[r[k] + step] <= i[k]) r[k] += step;
 }
 
-// Slot and position of row t (table entries from L2: another SM may have written them).
-__device__ __forceinline__ void write_row(const TableParams &p, const int32_t *cu, int t,
-                                          int total) {
-    int64_t slot = -1, pos = 0;
-    if (t < total) {
-        const int r = find(cu, p.batch, t);
-        const int x = p.old_len[r] + t - cu[r];
-        const int id = __ldcg(p.block_table + (int64_t)r * p.max_blocks_per_seq +
-                              (x >> p.bs_shift));
-        pos = x;
-        slot = ((int64_t)id << p.bs_shift) + (x & (p.block_size - 1));
+__device__ __forceinline__ int first_step(int n) { return n <= 1 ? 0 : 1 << (31 - __clz(n - 1)); }
+
+// Slots and positions of rows t, t + stride, .. (kAtOnce of them); FRESH: table entries
+// from L2, where another SM may just have written them.
+template <bool FRESH>
+__device__ __forceinline__ void write_rows(const TableParams &p, const int32_t *cu, int64_t t0,
+                                           int stride, int total) {
+    int t[kAtOnce], r[kAtOnce], x[kAtOnce], id[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) t[k] = (int)min(t0 + (int64_t)k * stride, (int64_t)p.rows);
+    find(cu, p.batch, first_step(p.batch), t, r);
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k)
+        x[k] = t[k] < total ? __ldg(p.old_len + r[k]) + t[k] - cu[r[k]] : 0;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+        const int32_t *e = p.block_table + (int64_t)r[k] * p.max_blocks_per_seq + (x[k] >> p.bs_shift);
+        id[k] = t[k] < total ? (FRESH ? __ldcg(e) : *e) : 0;
     }
-    p.slots[t] = slot;
-    p.positions[t] = pos;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k)
+        if (t[k] < p.rows) {
+            p.slots[t[k]] = t[k] < total ? ((int64_t)id[k] << p.bs_shift) + (x[k] & (p.block_size - 1))
+                                         : -1;
+            p.positions[t[k]] = x[k];
+        }
 }
 
+// Sums that stay at 2^32 - 1 (each is compared with a limit below that).
 struct Sums {
-    long long tok, keys, taken, gone;
+    uint32_t tok, keys, taken, gone;
 };
 
+__device__ __forceinline__ uint32_t add_up(uint32_t a, uint32_t b) {
+    const uint32_t s = a + b;
+    return s < a ? 0xffffffffu : s;
+}
+
 __device__ __forceinline__ Sums add(const Sums &a, const Sums &b) {
-    return {a.tok + b.tok, a.keys + b.keys, a.taken + b.taken, a.gone + b.gone};
+    return {add_up(a.tok, b.tok), add_up(a.keys, b.keys), add_up(a.taken, b.taken),
+            add_up(a.gone, b.gone)};
 }
 
 __device__ __forceinline__ Sums shift_up(const Sums &a, int d) {
@@ -100,10 +120,10 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(const TableParam
                 a = b = 0;
             }
             const int have = (a + p.block_size - 1) >> shift, want = (b + p.block_size - 1) >> shift;
-            v.tok = max(b - a, 0);
-            v.keys = b;
-            v.taken = max(want - have, 0);
-            v.gone = max(have - want, 0);
+            v.tok = (uint32_t)max(b - a, 0);
+            v.keys = (uint32_t)b;
+            v.taken = (uint32_t)max(want - have, 0);
+            v.gone = (uint32_t)max(have - want, 0);
         }
         Sums in = v;
 #pragma unroll
@@ -136,32 +156,50 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(const TableParam
         s_tok[0] = s_take[0] = s_gone[0] = 0;
         if (rank == 0) p.cu_q[0] = p.cu_k[0] = 0;
     }
-    if (run.tok > p.rows || run.keys > 0x7fffffffLL) bad |= PKV_DEVERR_SEQLEN;
+    if (run.tok > (uint32_t)p.rows || run.keys > 0x7fffffffu) bad |= PKV_DEVERR_SEQLEN;
     // more pages than the pool has: an entry of the tables or the stack is there twice
-    if (F < 0 || F > p.num_blocks || run.gone > p.num_blocks || F + run.gone - run.taken > p.num_blocks)
+    const int64_t height = F + (int64_t)run.gone - run.taken;
+    if (F < 0 || F > p.num_blocks || run.gone > p.num_blocks || height > p.num_blocks)
         bad |= PKV_DEVERR_BLOCK_ID;
-    if (F + run.gone < run.taken) bad |= PKV_DEVERR_NO_BLOCKS;
+    if (height < 0) bad |= PKV_DEVERR_NO_BLOCKS;
     const int total = (int)run.tok, A = (int)run.taken, R = (int)run.gone;
     const bool countable = __syncthreads_or((int)bad) == 0;
 
-    // Where page i comes from, and the entry of the table it leaves.
-    auto released = [&](int i) {
-        const int r = find(s_gone, B, i);
-        const int want = (p.new_len[r] + p.block_size - 1) >> shift;
-        return p.block_table + (int64_t)r * M + want + (i - s_gone[r]);
+    const int moves = max(A, R), step = first_step(B);
+    // The pages kAll apart from i on: ids, and the entries of the table that they leave
+    // (nullptr: of the stack).
+    auto pages_from = [&](int i, int (&id)[kAtOnce], int32_t *(&from)[kAtOnce]) {
+        int at[kAtOnce], r[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) at[k] = min(i + k * kAll, moves);
+        find(s_gone, B, step, at, r);
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            from[k] = nullptr;
+            if (at[k] < R) {
+                const int want = (__ldg(p.new_len + r[k]) + p.block_size - 1) >> shift;
+                from[k] = p.block_table + (int64_t)r[k] * M + want + (at[k] - s_gone[r[k]]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+            id[k] = at[k] < R ? *from[k] : at[k] < moves ? p.free_blocks[F - 1 - (at[k] - R)] : 0;
     };
-    const int moves = max(A, R);
+    int id[kAtOnce];
+    int32_t *from[kAtOnce];
     if (countable) {
         // every id that will be moved, and the pages that new tokens go on filling
-        for (int i = gtid; i < moves; i += kAll) {
-            const int id = i < R ? *released(i) : p.free_blocks[F - 1 - (i - R)];
-            if (id < 0 || id >= p.num_blocks) bad |= PKV_DEVERR_BLOCK_ID;
+        for (int i = gtid; i < moves; i += kAtOnce * kAll) {
+            pages_from(i, id, from);
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k)
+                if (id[k] < 0 || id[k] >= p.num_blocks) bad |= PKV_DEVERR_BLOCK_ID;
         }
         for (int r = gtid; r < B; r += kAll) {
             const int a = p.old_len[r];
             if (p.new_len[r] > a && (a & (p.block_size - 1))) {
-                const int id = p.block_table[(int64_t)r * M + (a >> shift)];
-                if (id < 0 || id >= p.num_blocks) bad |= PKV_DEVERR_BLOCK_ID;
+                const int e = p.block_table[(int64_t)r * M + (a >> shift)];
+                if (e < 0 || e >= p.num_blocks) bad |= PKV_DEVERR_BLOCK_ID;
             }
         }
     }
@@ -182,27 +220,28 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(const TableParam
         cluster_sync();  // the others may still read s_bad
         return;
     }
-    for (int i = gtid; i < moves; i += kAll) {
-        int id;
-        if (i < R) {
-            int32_t *e = released(i);
-            id = *e;
-            *e = -1;
-        } else {
-            id = p.free_blocks[F - 1 - (i - R)];
-        }
-        if (i < A) {
-            const int r = find(s_take, B, i);
-            const int have = (p.old_len[r] + p.block_size - 1) >> shift;
-            p.block_table[(int64_t)r * M + have + (i - s_take[r])] = id;
-        } else {
-            p.free_blocks[F + R - 1 - i] = id;
+    for (int i = gtid; i < moves; i += kAtOnce * kAll) {
+        if (moves > kAtOnce * kAll) pages_from(i, id, from);  // (else: as they were checked)
+        int at[kAtOnce], r[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) at[k] = min(i + k * kAll, moves);
+        find(s_take, B, step, at, r);
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            if (from[k]) *from[k] = -1;
+            if (at[k] < A) {
+                const int have = (__ldg(p.old_len + r[k]) + p.block_size - 1) >> shift;
+                p.block_table[(int64_t)r[k] * M + have + (at[k] - s_take[r[k]])] = id[k];
+            } else if (at[k] < moves) {
+                p.free_blocks[F + R - 1 - at[k]] = id[k];
+            }
         }
     }
     if (gtid == 0) *p.num_free = F + R - A;
     cluster_sync();  // the tables are written
     if (p.rows_here)
-        for (int t = gtid; t < p.rows; t += kAll) write_row(p, s_tok, t, total);
+        for (int t = gtid; t < p.rows; t += kAtOnce * kAll)
+            write_rows<true>(p, s_tok, t, kAll, total);
 }
 
 __global__ void __launch_bounds__(kRowThreads) block_rows_kernel(const TableParams p) {
@@ -210,10 +249,8 @@ __global__ void __launch_bounds__(kRowThreads) block_rows_kernel(const TablePara
     pdl_wait();
     for (int r = threadIdx.x; r <= p.batch; r += kRowThreads) s_cu[r] = p.cu_q[r];
     __syncthreads();
-    const int total = s_cu[p.batch];
-    const int64_t t0 = (int64_t)blockIdx.x * kRowsPerCta;
-    for (int i = threadIdx.x; i < kRowsPerCta && t0 + i < p.rows; i += kRowThreads)
-        write_row(p, s_cu, (int)t0 + i, total);
+    write_rows<false>(p, s_cu, (int64_t)blockIdx.x * kRowsPerCta + threadIdx.x, kRowThreads,
+                      s_cu[p.batch]);
 }
 
 }  // namespace

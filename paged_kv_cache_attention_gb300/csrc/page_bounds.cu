@@ -14,8 +14,12 @@
 // and merged: codes would depend on the steps, and errors would add up).
 //
 // HBM bound: n * D keys read, 2 D + 1 bytes written per page and kv head.  A warp
-// takes a page of a kv head: its lanes hold 16 bytes of a row each, all rows of a
-// page are in flight at once, the rows' lanes meet in shuffles at the end.
+// works by itself: it looks through a window of up to 32 tokens and takes the pages
+// that end there, for some or all kv heads.  Its lanes hold 16 bytes of a row each,
+// all rows of a page are in flight at once, and the rows' lanes meet in shuffles.
+// Least and largest are kept in the 16-bit type that is exact: bf16, or for 8-bit
+// pools f16 relative to the page's largest row scale (codes times 2^0 .. 2^-15 are
+// f16 values; pages whose scales lie further apart go by fp32).
 #include <cuda_fp16.h>
 
 #include "pkv_sparse.cuh"
@@ -26,164 +30,263 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxTokens = 128;  // of a CTA
-constexpr int kAhead = 32;       // tokens looked at beyond one for its page
 
-// bytes 0..3 of w: clamped codes of four floats times inv (rounded down, or up)
-template <bool UP>
-__device__ __forceinline__ uint32_t codes4(const float *x, float inv) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float y = x[i] * inv;  // exact, or less than the smallest float
-        int c = UP ? (int)ceilf(y) : (int)floorf(y);
-        if (UP && x[i] > 0.f) c = max(c, 1);
-        if (!UP && x[i] < 0.f) c = min(c, -1);
-        w |= ((uint32_t)c & 0xffu) << (8 * i);
-    }
-    return w;
+template <bool FP8>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {  // a NaN stays
+    uint32_t r;
+    if (FP8)
+        asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
-// The 16 bytes of a row that a lane holds: 8 bf16 values, or 16 codes times f.
 template <bool FP8>
-__device__ __forceinline__ void load_row(const uint4 &w, float f, float (&x)[FP8 ? 16 : 8]) {
-    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if (FP8)
+        asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        r = bf16x2_max_nan(a, b);
+    return r;
+}
+
+// The two values of a pair as floats; FP8: times f.
+template <bool FP8>
+__device__ __forceinline__ void unpack2(uint32_t w, float f, float &x, float &y) {
+    if (FP8) {
+        const float2 v = __half22float2(*reinterpret_cast<__half2 *>(&w));
+        x = v.x * f;
+        y = v.y * f;
+    } else {
+        x = __uint_as_float(w << 16);
+        y = __uint_as_float(w & 0xffff0000u);
+    }
+}
+
+// The code of x * inv, rounded up or down.  The product is exact, or below the
+// smallest float: still not 0.
+__device__ __forceinline__ uint32_t code_of(float x, float inv, bool up) {
+    const float y = x * inv;
+    const int c = up ? max(__float2int_ru(y), x > 0.f ? 1 : -128)
+                     : min(__float2int_rd(y), x < 0.f ? -1 : 127);
+    return (uint32_t)c & 0xffu;
+}
+
+// Least and largest of a page whose row scales lie far apart, in fp32; the channels
+// 16 c .. of row r0, r0 + step, ..
+__device__ __noinline__ void fp32_bounds(const char *rows, int64_t row_bytes, const uint8_t *scale,
+                                         int n, int r0, int step, float (&lo)[16], float (&hi)[16]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (FP8) {
-            uint32_t lo, hi;
-            e4m3_to_f16(v[i], lo, hi);
-            const float2 a = __half22float2(*reinterpret_cast<__half2 *>(&lo));
-            const float2 b = __half22float2(*reinterpret_cast<__half2 *>(&hi));
-            x[4 * i] = a.x * f;
-            x[4 * i + 1] = a.y * f;
-            x[4 * i + 2] = b.x * f;
-            x[4 * i + 3] = b.y * f;
-        } else {
-            x[2 * i] = __uint_as_float(v[i] << 16);
-            x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+    for (int i = 0; i < 16; ++i) {
+        lo[i] = INFINITY;
+        hi[i] = -INFINITY;
+    }
+    for (int r = r0; r < n; r += step) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(rows + r * row_bytes);
+        const float f = scale_value(scale[r]);
+        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t p[2];
+            e4m3_to_f16(v[i], p[0], p[1]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float x, y;
+                unpack2<true>(p[k], f, x, y);
+                lo[4 * i + 2 * k] = fminf(lo[4 * i + 2 * k], x);
+                hi[4 * i + 2 * k] = fmaxf(hi[4 * i + 2 * k], x);
+                lo[4 * i + 2 * k + 1] = fminf(lo[4 * i + 2 * k + 1], y);
+                hi[4 * i + 2 * k + 1] = fmaxf(hi[4 * i + 2 * k + 1], y);
+            }
+        }
+    }
+}
+
+// SPAN: lanes of a row (16 bytes each), a power of two; the last ones may be idle.
+template <bool FP8, int BS, int SPAN>
+__global__ void __launch_bounds__(kThreads) page_bounds_kernel(const BoundsParams p) {
+    constexpr int V = FP8 ? 16 : 8;     // channels of a lane
+    constexpr int P = V / 2;            // pairs
+    constexpr int STEP = 32 / SPAN;     // rows side by side
+    constexpr int ROWS = BS / STEP;     // rows of a lane
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t id = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int groups = (p.num_kv_heads + p.heads_per_warp - 1) / p.heads_per_warp;
+    const int64_t window = id / groups;
+    const int g0 = (int)(id - window * groups) * p.heads_per_warp;
+    const int64_t t0 = window * p.tokens_per_warp;
+    if (t0 >= p.num_tokens) return;
+
+    // the tokens of the window that are the last of their page among the next 32
+    auto slot_of = [&](int64_t t) {
+        int64_t s = t < p.num_tokens ? p.slots[t] : -1;
+        if (s >= p.capacity) {
+            if (g0 == 0 && t < t0 + p.tokens_per_warp) flag_error(p.dev_error, PKV_DEVERR_SLOT);
+            s = -1;
+        }
+        return s < 0 ? -1 : (int)s;  // (slots are below 2^31)
+    };
+    const int slot = slot_of(t0 + lane), next = slot_of(t0 + 32 + lane);
+    const int page = slot < 0 ? -1 - lane : slot >> p.bs_shift;
+    const int next_page = next < 0 ? -1 : next >> p.bs_shift;
+    const uint32_t alike = __match_any_sync(0xffffffffu, page);
+    const uint32_t upto = (2u << lane) - 1u;  // this lane and those before it
+    uint32_t work = __ballot_sync(0xffffffffu,
+                                  slot >= 0 && lane < p.tokens_per_warp && !(alike & ~upto));
+    for (uint32_t rest = work; rest; rest &= rest - 1) {
+        const int c = __ffs(rest) - 1;
+        const int pc = __shfl_sync(0xffffffffu, page, c);
+        if (__ballot_sync(0xffffffffu, next_page == pc) & ((2u << c) - 1u)) work &= ~(1u << c);
+    }
+
+    const int D = p.head_dim, E = FP8 ? 1 : 2;
+    const int c = lane & (SPAN - 1), r0 = lane / SPAN;
+    const bool in = c * V < D;
+    const int64_t row_bytes = (int64_t)(p.hnd ? 1 : p.num_kv_heads) * D * E;
+    const int heads = min(p.heads_per_warp, p.num_kv_heads - g0);
+    for (; work; work &= work - 1) {
+        const int s = __shfl_sync(0xffffffffu, slot, __ffs(work) - 1);
+        const int64_t blk = s >> p.bs_shift;
+        const int n = (s & (BS - 1)) + 1;
+#pragma unroll 1
+        for (int h = 0; h < heads; ++h) {
+            const int g = g0 + h;
+            const int64_t unit = blk * p.num_kv_heads + g;
+            const char *rows = static_cast<const char *>(p.k) +
+                               (p.hnd ? unit * BS * D * E
+                                      : (blk * BS * p.num_kv_heads + g) * (int64_t)D * E) +
+                               (in ? c * 16 : 0);
+            uint4 x[ROWS];  // (rows past the last: the last again)
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i)
+                x[i] = *reinterpret_cast<const uint4 *>(rows + min(r0 + i * STEP, n - 1) * row_bytes);
+            int byte = 0, top = 0;
+            bool ok = true, near = true;
+            if (FP8) {
+                byte = p.k_scale[unit * BS + min(lane, n - 1)];  // lane = row
+                ok = __all_sync(0xffffffffu, byte != (int)kScaleNaN);
+                top = __reduce_max_sync(0xffffffffu, byte);
+                near = __all_sync(0xffffffffu, byte >= top - 15);
+            }
+            uint32_t lo[P], hi[P];
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                uint32_t v[P];
+                if (FP8) {
+                    // the row's scale relative to the largest, 2^0 .. 2^-15, as an f16 pair
+                    const int d = __shfl_sync(0xffffffffu, byte, min(r0 + i * STEP, n - 1)) - top;
+                    const uint32_t f1 = d >= -14 ? (uint32_t)(15 + d) << 10 : 0x200u;
+                    const uint32_t f = f1 | (f1 << 16);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        e4m3_to_f16(w[k], v[2 * k % P], v[(2 * k + 1) % P]);
+                        v[2 * k % P] = f16x2_mul(v[2 * k % P], f);
+                        v[(2 * k + 1) % P] = f16x2_mul(v[(2 * k + 1) % P], f);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] = w[k];
+                }
+#pragma unroll
+                for (int k = 0; k < P; ++k) {
+                    lo[k] = i == 0 ? v[k] : min2<FP8>(lo[k], v[k]);
+                    hi[k] = i == 0 ? v[k] : max2<FP8>(hi[k], v[k]);
+                }
+            }
+#pragma unroll
+            for (int off = SPAN; off < 32; off <<= 1)
+#pragma unroll
+                for (int k = 0; k < P; ++k) {
+                    lo[k] = min2<FP8>(lo[k], __shfl_xor_sync(0xffffffffu, lo[k], off));
+                    hi[k] = max2<FP8>(hi[k], __shfl_xor_sync(0xffffffffu, hi[k], off));
+                }
+            const float f = FP8 ? scale_value((uint32_t)top) : 1.f;
+            float a[V], b[V];
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+                unpack2<FP8>(lo[k], f, a[2 * k], a[2 * k + 1]);
+                unpack2<FP8>(hi[k], f, b[2 * k], b[2 * k + 1]);
+            }
+            if constexpr (FP8) {
+                if (ok && !near) {  // rare
+                    fp32_bounds(rows, row_bytes, p.k_scale + unit * BS, n, r0, STEP, a, b);
+                    for (int off = SPAN; off < 32; off <<= 1)
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            a[i] = fminf(a[i], __shfl_xor_sync(0xffffffffu, a[i], off));
+                            b[i] = fmaxf(b[i], __shfl_xor_sync(0xffffffffu, b[i], off));
+                        }
+                }
+            }
+            uint32_t amax = 0;  // (the bits of a NaN are above an infinity's)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                amax = max(amax, max(__float_as_uint(fabsf(a[i])), __float_as_uint(fabsf(b[i]))));
+            amax = __reduce_max_sync(0xffffffffu, in ? amax : 0u);
+            ok = ok && amax < 0x7f800000u;
+            // amax = m * 2^x with 1 <= m < 2 and 127 = 1.984375 * 2^6: e = x - 6, one more
+            // above 1.984375 (a carry out of the mantissa)
+            const int e = max((int)((amax + 0x1ffffu) >> 23) - 127 - 6, -126);
+            const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+            int8_t *out = p.bounds + unit * 2 * D + c * V;
+            // all rows' lanes have the bounds: the first store the lower, the next the upper
+            const bool split = STEP > 1;
+            if (in && r0 < 2) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if (split && u == 1) break;
+                    const bool up = split ? r0 == 1 : u == 1;
+#pragma unroll
+                    for (int i = 0; i < V; i += 8) {
+                        uint32_t w[2] = {0u, 0u};
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            w[k / 4] |= code_of(up ? b[i + k] : a[i + k], inv, up) << (8 * (k % 4));
+                        *reinterpret_cast<uint2 *>(out + (up ? D : 0) + i) =
+                            ok ? make_uint2(w[0], w[1]) : make_uint2(0u, 0u);
+                    }
+                }
+            }
+            if (lane == 0) p.bounds_scale[unit] = ok ? (uint8_t)(e + 127) : (uint8_t)kScaleNaN;
         }
     }
 }
 
 template <bool FP8, int BS>
-__global__ void __launch_bounds__(kThreads) page_bounds_kernel(const BoundsParams p) {
-    constexpr int V = FP8 ? 16 : 8;
-    __shared__ int64_t s_slot[kMaxTokens + kAhead];
-    __shared__ int s_work[kMaxTokens];  // tokens that are the last of their page
-    __shared__ int s_count;
-    pdl_wait();
-    const int g = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t0 = (int64_t)blockIdx.y * p.tokens_per_cta;
-    const int nt = (int)min((int64_t)p.tokens_per_cta, p.num_tokens - t0);
-    if (threadIdx.x == 0) s_count = 0;
-    for (int i = threadIdx.x; i < nt + kAhead; i += kThreads) {
-        int64_t s = t0 + i < p.num_tokens ? p.slots[t0 + i] : -1;
-        if (s >= p.capacity) {
-            if (i < nt) flag_error(p.dev_error, PKV_DEVERR_SLOT);
-            s = -1;
-        }
-        s_slot[i] = s < 0 ? -1 : s;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < nt; i += kThreads) {
-        const int64_t s = s_slot[i];
-        if (s < 0) continue;
-        bool last = true;
-        for (int j = 1; j <= kAhead && last; ++j) {
-            const int64_t o = s_slot[i + j];
-            last = o < 0 || (o >> p.bs_shift) != (s >> p.bs_shift);
-        }
-        if (last) s_work[atomicAdd(&s_count, 1)] = i;
-    }
-    __syncthreads();
-    const int work = s_count, D = p.head_dim;
-    const int lanes = D / V;             // lanes of a row: 4 .. 32
-    const int span = lanes <= 4 ? 4 : lanes <= 8 ? 8 : lanes <= 16 ? 16 : 32;
-    const int step = 32 / span;          // rows side by side
-    const int c = lane & (span - 1), r0 = lane / span;
-    const bool in = c < lanes;
-    for (int w = warp; w < work; w += kWarps) {
-        const int64_t slot = s_slot[s_work[w]];
-        const int64_t blk = slot >> p.bs_shift;
-        const int n = (int)(slot & (BS - 1)) + 1;
-        const int64_t unit = blk * p.num_kv_heads + g;
-        const int64_t row0 = p.hnd ? unit * BS : blk * BS * p.num_kv_heads + g;
-        const int64_t rstep = p.hnd ? 1 : p.num_kv_heads;
-        float lo[V], hi[V];
-        bool ok = true;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            lo[i] = INFINITY;
-            hi[i] = -INFINITY;
-        }
-#pragma unroll 8
-        for (int r = r0; r < n; r += step) {
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            float f = 1.f;
-            if (in)
-                x = *reinterpret_cast<const uint4 *>(static_cast<const char *>(p.k) +
-                                                     (row0 + r * rstep) * D * (FP8 ? 1 : 2) +
-                                                     c * 16);
-            if (FP8) {
-                const uint32_t byte = p.k_scale[unit * BS + r];
-                ok = ok && byte != kScaleNaN;
-                f = scale_value(byte == kScaleNaN ? 127u : byte);
-            }
-            float y[V];
-            load_row<FP8>(x, f, y);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                ok = ok && fabsf(y[i]) < INFINITY;  // false for a NaN too
-                lo[i] = fminf(lo[i], y[i]);
-                hi[i] = fmaxf(hi[i], y[i]);
-            }
-        }
-        for (int off = span; off < 32; off <<= 1)
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], off));
-                hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], off));
-            }
-        ok = __all_sync(0xffffffffu, ok);
-        uint32_t amax = 0;
-        if (in && ok)
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                amax = max(amax, max(__float_as_uint(fabsf(lo[i])), __float_as_uint(fabsf(hi[i]))));
-        amax = __reduce_max_sync(0xffffffffu, amax);
-        // amax = m * 2^x with 1 <= m < 2 and 127 = 1.984375 * 2^6: e = x - 6, one more
-        // above 1.984375 (a carry out of the mantissa)
-        const int e = max((int)((amax + 0x1ffffu) >> 23) - 127 - 6, -126);
-        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-        if (r0 == 0 && in) {
-            int8_t *out = p.bounds + unit * 2 * D + c * V;
-#pragma unroll
-            for (int i = 0; i < V / 4; ++i) {
-                *reinterpret_cast<uint32_t *>(out + 4 * i) = ok ? codes4<false>(lo + 4 * i, inv) : 0u;
-                *reinterpret_cast<uint32_t *>(out + D + 4 * i) = ok ? codes4<true>(hi + 4 * i, inv) : 0u;
-            }
-            if (c == 0) p.bounds_scale[unit] = ok ? (uint8_t)(e + 127) : (uint8_t)kScaleNaN;
-        }
-    }
+cudaError_t launch_span(const BoundsParams &p, unsigned grid, cudaStream_t stream) {
+    constexpr int L = FP8 ? 4 : 8;  // lanes of a row of 64 channels
+    auto kern = p.head_dim <= 64    ? page_bounds_kernel<FP8, BS, L>
+                : p.head_dim <= 128 ? page_bounds_kernel<FP8, BS, 2 * L>
+                                    : page_bounds_kernel<FP8, BS, 4 * L>;
+    return launch_pdl(kern, dim3(grid), dim3(kThreads), 0, stream, p);
 }
 
 }  // namespace
 
 cudaError_t launch_page_bounds(const BoundsParams &p0, cudaStream_t stream) {
     BoundsParams p = p0;
-    // few tokens: a CTA each; prompts: as many as fill a CTA's warps with pages
-    const int64_t fill = 4LL * device_sm_count();
-    int per = 8;
-    while (per < kMaxTokens && (p.num_tokens + per - 1) / per * p.num_kv_heads > fill) per *= 2;
-    p.tokens_per_cta = per;
-    const int64_t y = (p.num_tokens + per - 1) / per;
-    if (y > 65535) return cudaErrorNotSupported;
-    auto kern = p.k_scale ? (p.block_size == 16 ? page_bounds_kernel<true, 16>
-                                                : page_bounds_kernel<true, 32>)
-                          : (p.block_size == 16 ? page_bounds_kernel<false, 16>
-                                                : page_bounds_kernel<false, 32>);
-    return launch_pdl(kern, dim3(p.num_kv_heads, (unsigned)y), dim3(kThreads), 0, stream, p);
+    // A warp per token and kv head while they all run at once (a decode step); then
+    // windows of more tokens, then more kv heads per warp.
+    const int64_t warps = 16LL * device_sm_count();
+    p.tokens_per_warp = 1;
+    p.heads_per_warp = 1;
+    while (p.tokens_per_warp < 32 &&
+           (p.num_tokens + p.tokens_per_warp - 1) / p.tokens_per_warp * p.num_kv_heads > warps)
+        p.tokens_per_warp *= 2;
+    const int64_t windows = (p.num_tokens + p.tokens_per_warp - 1) / p.tokens_per_warp;
+    while (p.heads_per_warp < p.num_kv_heads &&
+           windows * (p.num_kv_heads / p.heads_per_warp) > 2 * warps)
+        p.heads_per_warp *= 2;
+    const int groups = (p.num_kv_heads + p.heads_per_warp - 1) / p.heads_per_warp;
+    const unsigned grid = (unsigned)((windows * groups + kWarps - 1) / kWarps);
+    if (p.k_scale)
+        return p.block_size == 16 ? launch_span<true, 16>(p, grid, stream)
+                                  : launch_span<true, 32>(p, grid, stream);
+    return p.block_size == 16 ? launch_span<false, 16>(p, grid, stream)
+                              : launch_span<false, 32>(p, grid, stream);
 }
 
 }  // namespace pkv

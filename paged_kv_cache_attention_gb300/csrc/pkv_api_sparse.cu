@@ -148,7 +148,7 @@ pkv_status pkv_update_page_bounds(const void *k_cache, const uint8_t *k_scale,
     p.block_size = cache.block_size;
     p.bs_shift = cache.block_size == 16 ? 4 : 5;
     p.hnd = cache.layout == PKV_HND ? 1 : 0;
-    p.tokens_per_cta = 0;
+    p.tokens_per_warp = p.heads_per_warp = 0;
     return from_cuda(launch_page_bounds(p, static_cast<cudaStream_t>(stream)));
 }
 

@@ -30,7 +30,7 @@ struct BoundsParams {
     int64_t num_tokens, capacity;
     int32_t *dev_error;
     int num_kv_heads, head_dim, block_size, bs_shift, hnd;
-    int tokens_per_cta;
+    int tokens_per_warp, heads_per_warp;
 };
 
 // What the calls with a row per query share: which request and how many keys a

@@ -41,7 +41,7 @@ namespace {
 
 constexpr uint32_t kForced = 0xffffffffu;  // above every score
 constexpr int kNoVote = -100000;           // exponent of a column that has no say
-constexpr int kRank = 128;                 // scores ranked against one another
+constexpr int kRank = 32;                  // scores ranked against one another
 
 // An unsigned integer that sorts like x (no NaN; -0 was made 0).
 __device__ __forceinline__ uint32_t sortable(float x) {
@@ -80,6 +80,14 @@ __device__ __forceinline__ float pow2(int e) {  // -126 <= e <= 127
 __device__ __forceinline__ float scaled(float x, int e) {
     const int last = min(max(e, -126), 127);
     return x * pow2(e - last) * pow2(last);
+}
+
+// Count one more in a word of shared memory, if on (no branch).
+__device__ __forceinline__ void count_if(uint32_t addr, bool on) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                 "@p red.shared::cta.add.u32 [%0], 1;\n\t}" ::"r"(addr),
+                 "r"((uint32_t)on)
+                 : "memory");
 }
 
 __device__ __forceinline__ void block_sync(bool cluster) {
@@ -121,6 +129,7 @@ __global__ void __launch_bounds__(Shape<NCH, NT, GP>::WARPS * 32) select_pages_k
     __shared__ uint32_t s_pick[QT][3];           // digit, pages above it, pages with it
     __shared__ int s_scale[S::WARPS][S::NST][16];  // scale bytes of the tiles in flight
     __shared__ uint32_t s_range[S::WARPS][2];    // least and largest score
+    __shared__ uint32_t s_both[2];               // the same of the CTA
     __shared__ int s_left[QT];                   // scores in the list to be ranked
     __shared__ int s_cnt[kWarps][2];             // above, equal: per warp
     __shared__ int s_total[QT][2];               // of the CTA
@@ -167,6 +176,8 @@ __global__ void __launch_bounds__(Shape<NCH, NT, GP>::WARPS * 32) select_pages_k
 #pragma unroll 1
         for (int i = threadIdx.x; i < 2 * QT * 64; i += kThreads)
             reinterpret_cast<uint4 *>(&s_hist[0][0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
+        const int32_t *bt = p.r.block_table + (int64_t)r * p.r.max_blocks_per_seq + base;
+        for (int i = threadIdx.x; i < nl; i += kThreads) s_key[i] = (uint32_t)__ldg(bt + i);
         if (threadIdx.x < QT) s_left[threadIdx.x] = 0;
 #pragma unroll 1
         for (int i = threadIdx.x; i < NT * NCH * 64; i += kThreads) s_q[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -176,6 +187,46 @@ __global__ void __launch_bounds__(Shape<NCH, NT, GP>::WARPS * 32) select_pages_k
             *reinterpret_cast<int4 *>(s_sum[i]) = make_int4(0, 0, 0, 0);
         }
         __syncthreads();
+        const uint32_t ring = smem_u32(s_dyn) + warp * NST * S::STAGE + lane * 16;
+        const int tiles = (nl + 15) / 16, mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
+        // Tile k goes to slot k % NST of the ring.  A scale byte is loaded with its page's
+        // codes and put into shared memory a tile later (-1: no page).  The page ids wait in
+        // the first row of scores, where a tile's are read before its scores are written.
+        int *scale = &s_scale[warp][0][0];
+        int byte_ahead = -1;
+        auto issue = [&](int k) {
+            const int i = (warp + k * kWarps) * 16 + (lane & 15);
+            const int id = i < nl ? (int)s_key[i] : -1;
+            const bool live = id >= 0 && id < p.r.num_blocks;
+            const uint32_t at = (uint32_t)(live ? id : 0) * p.r.num_kv_heads + g;  // < 2^31
+            byte_ahead = live ? (int)p.bounds_scale[at] : -1;
+            if (!live && i < nl) flag_error(p.r.dev_error, PKV_DEVERR_BLOCK_ID);
+            const uint32_t dst = ring + (k % NST) * S::STAGE;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t row = __shfl_sync(0xffffffffu, at, gq + 8 * j);
+                const int8_t *src = p.bounds + (uint64_t)row * (uint32_t)(2 * D) + tq * 16;
+#pragma unroll
+                for (int c = 0; c < NCH; ++c) {  // (pages out of the pool: scores not used)
+                    if (c < NCH - 1)
+                        cp_async16(dst + (j * NCH + c) * 512, src + c * 64);
+                    else
+                        cp_async16_or_zero(dst + (j * NCH + c) * 512, src + c * 64,
+                                           c * 64 + tq * 16 < 2 * D);
+                }
+            }
+        };
+        auto keep_byte = [&](int k) {
+            if (lane < 16) scale[(k % NST) * 16 + lane] = byte_ahead;
+        };
+#pragma unroll 1
+        for (int k = 0; k < NST - 1; ++k) {
+            if (k < mine) {
+                issue(k);
+                if (k < NST - 2) keep_byte(k);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
         const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) +
                                  ((int64_t)first * p.r.num_kv_heads + g) * G * D;
 #pragma unroll 1
@@ -270,57 +321,11 @@ __global__ void __launch_bounds__(Shape<NCH, NT, GP>::WARPS * 32) select_pages_k
                     off[nt][i / 4][i % 4] = 1152.f * (float)s_sum[nt * 8 + 2 * tq + i / 4][i % 4];
 
         // scores of 16 pages at a time, this warp's tiles every kWarps-th
-        const int32_t *bt = p.r.block_table + (int64_t)r * p.r.max_blocks_per_seq;
-        const uint32_t ring = smem_u32(s_dyn) + warp * NST * S::STAGE + lane * 16;
-        const int tiles = (nl + 15) / 16, mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
-        auto load_id = [&](int k) {  // of page `lane` (< 16) of tile k
-            const int i = (warp + k * kWarps) * 16 + (lane & 15);
-            return k < mine && i < nl ? __ldg(bt + base + i) : -1;
-        };
-        // Tile k goes to slot k % NST of the ring.  Page ids and scale bytes arrive while the
-        // tile before is worked on: an id is loaded a tile before its page's codes, a byte
-        // with them and put into shared memory a tile later (-1: no page).
-        int *scale = &s_scale[warp][0][0];
-        int byte_ahead = -1;
-        auto issue = [&](int k, int id) {
-            const bool live = id >= 0 && id < p.r.num_blocks;
-            const uint32_t at = (uint32_t)(live ? id : 0) * p.r.num_kv_heads + g;  // < 2^31
-            byte_ahead = live ? (int)p.bounds_scale[at] : -1;
-            if (!live && lane < 16 && (warp + k * kWarps) * 16 + lane < nl)
-                flag_error(p.r.dev_error, PKV_DEVERR_BLOCK_ID);
-            const uint32_t dst = ring + (k % NST) * S::STAGE;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint32_t row = __shfl_sync(0xffffffffu, at, gq + 8 * j);
-                const int8_t *src = p.bounds + (uint64_t)row * (uint32_t)(2 * D) + tq * 16;
-#pragma unroll
-                for (int c = 0; c < NCH; ++c) {  // (pages out of the pool: scores not used)
-                    if (c < NCH - 1)
-                        cp_async16(dst + (j * NCH + c) * 512, src + c * 64);
-                    else
-                        cp_async16_or_zero(dst + (j * NCH + c) * 512, src + c * 64,
-                                           c * 64 + tq * 16 < 2 * D);
-                }
-            }
-        };
-        auto keep_byte = [&](int k) {
-            if (lane < 16) scale[(k % NST) * 16 + lane] = byte_ahead;
-        };
-#pragma unroll 1
-        for (int k = 0; k < NST - 1; ++k) {
-            if (k < mine) {
-                issue(k, load_id(k));
-                if (k < NST - 2) keep_byte(k);
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        }
-        int next_id = load_id(NST - 1);
 #pragma unroll 1
         for (int k = 0; k < mine; ++k) {
             keep_byte(k + NST - 2);
-            if (k + NST - 1 < mine) issue(k + NST - 1, next_id);
+            if (k + NST - 1 < mine) issue(k + NST - 1);
             asm volatile("cp.async.commit_group;" ::: "memory");
-            next_id = load_id(k + NST);
             asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");
             __syncwarp();
             const uint32_t tile = ring + (k % NST) * S::STAGE;
@@ -441,13 +446,17 @@ __global__ void __launch_bounds__(Shape<NCH, NT, GP>::WARPS * 32) select_pages_k
         const int nlr = choose ? min(max(nrow - base, 0), per) : 0;
         const uint32_t *key_row = s_key + mq * p.cap;
         const bool fixed = QT > 1 && C > 1;
-        auto sync = [&] {
-            if (C > 1)
-                cluster_sync();
-            else if (S::GROUP == 1)
+        auto group_sync = [&] {
+            if (S::GROUP == 1)
                 __syncwarp();
             else
                 asm volatile("bar.sync %0, %1;" ::"r"(mq + 1), "n"(GS) : "memory");
+        };
+        auto sync = [&] {
+            if (C > 1)
+                cluster_sync();
+            else
+                group_sync();
         };
         uint32_t prefix = 0;  // of the scores that are left: the bits from `digit` up
         int need = p.top_k, left = 0, digit = 32, pass = 0;
@@ -455,29 +464,43 @@ __global__ void __launch_bounds__(Shape<NCH, NT, GP>::WARPS * 32) select_pages_k
             need -= p.num_first + p.num_recent;  // forced ones are above all others
             uint32_t lo = 0xffffffffu, hi = 0;
 #pragma unroll 1
-            for (int i = li; i < nlr; i += GS) {
-                const uint32_t key = key_row[i];
-                if (key != kForced) {
-                    lo = min(lo, key);
-                    hi = max(hi, key);
-                }
+            for (int i = li * 4; i < nlr; i += GS * 4) {
+                const uint4 k4 = *reinterpret_cast<const uint4 *>(key_row + i);
+                const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    if (i + b < nlr && key[b] != kForced) {
+                        lo = min(lo, key[b]);
+                        hi = max(hi, key[b]);
+                    }
             }
             lo = __reduce_min_sync(0xffffffffu, lo);
             hi = __reduce_max_sync(0xffffffffu, hi);
-            if (S::GROUP > 1 || C > 1) {
+            if (S::GROUP > 1) {
                 if (lane == 0) {
                     s_range[warp][0] = lo;
                     s_range[warp][1] = hi;
                 }
-                sync();
-#pragma unroll 1
-                for (int c = 0; c < C; ++c)
-#pragma unroll 1
-                    for (int w = mq * S::GROUP; w < (mq + 1) * S::GROUP; ++w) {
-                        const uint32_t at = smem_u32(&s_range[w][0]);
-                        lo = min(lo, C > 1 ? cluster_ld32(cluster_addr(at, c)) : s_range[w][0]);
-                        hi = max(hi, C > 1 ? cluster_ld32(cluster_addr(at + 4, c)) : s_range[w][1]);
-                    }
+                group_sync();
+#pragma unroll
+                for (int w = 0; w < S::GROUP; ++w) {
+                    lo = min(lo, s_range[mq * S::GROUP + w][0]);
+                    hi = max(hi, s_range[mq * S::GROUP + w][1]);
+                }
+            }
+            if (C > 1) {  // (one query: all warps have the same) lane c looks at CTA c
+                if (threadIdx.x == 0) {
+                    s_both[0] = lo;
+                    s_both[1] = hi;
+                }
+                cluster_sync();
+                if (lane < C) {
+                    const uint32_t at = cluster_addr(smem_u32(s_both), lane);
+                    lo = cluster_ld32(at);
+                    hi = cluster_ld32(at + 4);
+                }
+                lo = __reduce_min_sync(0xffffffffu, lo);
+                hi = __reduce_max_sync(0xffffffffu, hi);
             }
             if (need == 0) lo = hi = kForced - 1;  // none but the forced ones
             digit = lo < hi ? 32 - __clz(lo ^ hi) : 0;
@@ -489,11 +512,18 @@ __global__ void __launch_bounds__(Shape<NCH, NT, GP>::WARPS * 32) select_pages_k
             const int next = fixed ? digit - 8 : max(digit - 8, 0);
             const uint32_t mask = (1u << (digit - next)) - 1u;
             uint32_t *hist = s_hist[pass & 1][mq], *other = s_hist[(pass + 1) & 1][mq];
+            const uint32_t bins = smem_u32(hist);
 #pragma unroll 1
-            for (int i = li; i < nlr; i += GS) {
-                const uint32_t key = key_row[i];
-                if ((digit == 32 || ((key ^ prefix) >> digit) == 0) && (fixed || key != kForced))
-                    atomicAdd(&hist[(key >> next) & mask], 1u);
+            for (int i = li * 4; i < nlr; i += GS * 4) {
+                const uint4 k4 = *reinterpret_cast<const uint4 *>(key_row + i);
+                const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    // (64-bit: a shift by 32 leaves nothing)
+                    const bool in = (uint32_t)((uint64_t)(key[b] ^ prefix) >> digit) == 0;
+                    count_if(bins + ((key[b] >> next) & mask) * 4,
+                             i + b < nlr && in && (fixed || key[b] != kForced));
+                }
             }
             sync();
             // thread li: bins 255 - li * BPT and below, so that a prefix sum counts from
@@ -503,13 +533,15 @@ __global__ void __launch_bounds__(Shape<NCH, NT, GP>::WARPS * 32) select_pages_k
             for (int b = 0; b < BPT; ++b) {
                 const int bin = 255 - li * BPT - b;
                 v[b] = 0;
-                if (C > 1)  // (C: 2, 4, 8 or 16; pairs of loads in flight)
+                if (C > 1)  // (C: 2, 4, 8 or 16)
 #pragma unroll 1
-                    for (int c = 0; c < C; c += 2) {
-                        const uint32_t at = smem_u32(&hist[bin]);
-                        const uint32_t x = cluster_ld32(cluster_addr(at, c));
-                        const uint32_t y = cluster_ld32(cluster_addr(at, c + 1));
-                        v[b] += x + y;
+                    for (int c = 0; c < C; c += 4) {
+                        const uint32_t at = bins + 4 * bin;
+                        uint32_t x[4];  // four loads in flight
+#pragma unroll
+                        for (int d = 0; d < 4; ++d)
+                            x[d] = c + d < C ? cluster_ld32(cluster_addr(at, c + d)) : 0u;
+                        v[b] += x[0] + x[1] + x[2] + x[3];
                     }
                 else
                     v[b] = hist[bin];
@@ -521,12 +553,6 @@ __global__ void __launch_bounds__(Shape<NCH, NT, GP>::WARPS * 32) select_pages_k
                 const uint32_t o = __shfl_up_sync(0xffffffffu, sum, off);
                 if (lane >= off) sum += o;
             }
-            auto group_sync = [&] {  // (the cluster's CTAs stay together by themselves)
-                if (S::GROUP == 1)
-                    __syncwarp();
-                else
-                    asm volatile("bar.sync %0, %1;" ::"r"(mq + 1), "n"(GS) : "memory");
-            };
             if (S::GROUP > 1) {
                 if (lane == 31) s_cnt[warp][0] = (int)sum;
                 group_sync();
@@ -567,27 +593,42 @@ __global__ void __launch_bounds__(Shape<NCH, NT, GP>::WARPS * 32) select_pages_k
             // the scores left, with their pages: [kRank] keys, then [kRank] pages
             uint32_t *list = s_hist[pass & 1][mq], *all = list;  // (all zeros, read by no one)
 #pragma unroll 1
-            for (int i = li; i < nlr; i += GS) {
-                const uint32_t key = key_row[i];
-                if (key != kForced && ((key ^ prefix) >> digit) == 0) {
-                    const int at = atomicAdd(&s_left[mq], 1);
-                    list[at] = key;
-                    list[kRank + at] = (uint32_t)(base + i);
-                }
+            for (int i = li * 4; i < nlr; i += GS * 4) {
+                const uint4 k4 = *reinterpret_cast<const uint4 *>(key_row + i);
+                const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
+                // (kForced has other leading bits than the scores that are left, or they
+                // have all bits in common and are not ranked)
+                const bool some = ((key[0] ^ prefix) >> digit) == 0 ||
+                                  ((key[1] ^ prefix) >> digit) == 0 ||
+                                  ((key[2] ^ prefix) >> digit) == 0 ||
+                                  ((key[3] ^ prefix) >> digit) == 0;
+                if (some)
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b)
+                    if (i + b < nlr && key[b] != kForced && ((key[b] ^ prefix) >> digit) == 0) {
+                        const int at = atomicAdd(&s_left[mq], 1);
+                        list[at] = key[b];
+                        list[kRank + at] = (uint32_t)(base + i + b);
+                    }
             }
             sync();
             if (C > 1) {  // of the whole cluster, in the buffer whose counts are read
                 all = s_hist[(pass + 1) & 1][mq];
+                if (warp == 0) {  // (one query, left <= 32) lane c: CTA c's count
+                    const int m = lane < C ? (int)cluster_ld32(cluster_addr(smem_u32(s_left), lane)) : 0;
+                    int c = 0, at = lane;
 #pragma unroll 1
-                for (int i = li; i < left; i += GS) {
-                    int c = 0, at = i;
-                    for (; c < C - 1; ++c) {
-                        const int m = (int)cluster_ld32(cluster_addr(smem_u32(&s_left[mq]), c));
-                        if (at < m) break;
-                        at -= m;
+                    for (int d = 0; d < C - 1; ++d) {
+                        const int md = __shfl_sync(0xffffffffu, m, d);
+                        if (c == d && at >= md) {
+                            at -= md;
+                            ++c;
+                        }
                     }
-                    all[i] = cluster_ld32(cluster_addr(smem_u32(&list[at]), c));
-                    all[kRank + i] = cluster_ld32(cluster_addr(smem_u32(&list[kRank + at]), c));
+                    if (lane < left) {
+                        all[lane] = cluster_ld32(cluster_addr(smem_u32(&list[at]), c));
+                        all[kRank + lane] = cluster_ld32(cluster_addr(smem_u32(&list[kRank + at]), c));
+                    }
                 }
                 sync();
             }
@@ -595,7 +636,7 @@ __global__ void __launch_bounds__(Shape<NCH, NT, GP>::WARPS * 32) select_pages_k
             for (int i = li; i < left; i += GS) {
                 const uint32_t key = all[i], page = all[kRank + i];
                 int above = 0, equal = 0;  // equal ones with lower pages
-#pragma unroll 1
+#pragma unroll 4
                 for (int j = 0; j < left; ++j) {
                     above += all[j] > key;
                     equal += all[j] == key && all[kRank + j] < page;
@@ -612,15 +653,23 @@ __global__ void __launch_bounds__(Shape<NCH, NT, GP>::WARPS * 32) select_pages_k
         __syncthreads();  // s_cnt is used again
 
         // pages above it, and the first `need` of those equal to it, in ascending order
-        const int seg = ((nlr + S::GROUP - 1) / S::GROUP + 31) / 32 * 32;
+        // (each warp a run of pages, four consecutive ones a lane)
+        const int seg = ((nlr + S::GROUP - 1) / S::GROUP + 127) / 128 * 128;
         const int lo = min((warp - mq * S::GROUP) * seg, nlr), hi = min(lo + seg, nlr);
         int above = 0, equal = 0;
+        if (S::GROUP > 1 || C > 1) {  // how many before this warp's?
 #pragma unroll 1
-        for (int i = lo; i < hi; i += 32) {
-            const bool in = i + lane < hi;
-            const uint32_t key = in ? key_row[i + lane] : 0u;
-            above += __popc(__ballot_sync(0xffffffffu, in && key > prefix));
-            equal += __popc(__ballot_sync(0xffffffffu, in && key == prefix));
+            for (int i = lo + 4 * lane; i < hi; i += 128) {
+                const uint4 k4 = *reinterpret_cast<const uint4 *>(key_row + i);
+                const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    above += i + b < hi && key[b] > prefix;
+                    equal += i + b < hi && key[b] == prefix;
+                }
+            }
+            above = __reduce_add_sync(0xffffffffu, above);
+            equal = __reduce_add_sync(0xffffffffu, equal);
         }
         if (lane == 0) {
             s_cnt[warp][0] = above;
@@ -635,10 +684,11 @@ __global__ void __launch_bounds__(Shape<NCH, NT, GP>::WARPS * 32) select_pages_k
         }
         block_sync(C > 1);
         int n_above = 0, n_equal = 0;  // before this warp's pages
-#pragma unroll 1
-        for (int c = 0; c < rank; ++c) {
-            n_above += (int)cluster_ld32(cluster_addr(smem_u32(&s_total[mq][0]), c));
-            n_equal += (int)cluster_ld32(cluster_addr(smem_u32(&s_total[mq][1]), c));
+        if (C > 1) {  // lane c looks at CTA c
+            n_above = lane < rank ? (int)cluster_ld32(cluster_addr(smem_u32(&s_total[mq][0]), lane)) : 0;
+            n_equal = lane < rank ? (int)cluster_ld32(cluster_addr(smem_u32(&s_total[mq][1]), lane)) : 0;
+            n_above = __reduce_add_sync(0xffffffffu, n_above);
+            n_equal = __reduce_add_sync(0xffffffffu, n_equal);
         }
 #pragma unroll 1
         for (int w = mq * S::GROUP; w < warp; ++w) {
@@ -648,16 +698,39 @@ __global__ void __launch_bounds__(Shape<NCH, NT, GP>::WARPS * 32) select_pages_k
         const uint32_t below = (1u << lane) - 1u;
         int32_t *out = out_of(mq);
 #pragma unroll 1
-        for (int i = lo; i < hi; i += 32) {
-            const bool in = i + lane < hi;
-            const uint32_t key = in ? key_row[i + lane] : 0u;
-            const uint32_t ma = __ballot_sync(0xffffffffu, in && key > prefix);
-            const uint32_t me = __ballot_sync(0xffffffffu, in && key == prefix);
-            const int a = n_above + __popc(ma & below), e = n_equal + __popc(me & below);
-            if (in && (key > prefix || (key == prefix && e < need)))
-                out[a + min(e, need)] = base + i + lane;
-            n_above += __popc(ma);
-            n_equal += __popc(me);
+        for (int i0 = lo; i0 < hi; i0 += 128) {
+            const int i = i0 + 4 * lane;
+            uint4 k4 = make_uint4(0u, 0u, 0u, 0u);
+            if (i < hi) k4 = *reinterpret_cast<const uint4 *>(key_row + i);
+            const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
+            bool up[4], same[4], some = false;
+            int before = 0, mine_up = 0, all_up = 0;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                up[b] = i + b < hi && key[b] > prefix;
+                same[b] = i + b < hi && key[b] == prefix;
+                some = some || same[b];
+                const uint32_t m = __ballot_sync(0xffffffffu, up[b]);
+                before += __popc(m & below);
+                all_up += __popc(m);
+            }
+            int same_before = 0, all_same = 0, mine_same = 0;
+            if (__any_sync(0xffffffffu, some))
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const uint32_t m = __ballot_sync(0xffffffffu, same[b]);
+                    same_before += __popc(m & below);
+                    all_same += __popc(m);
+                }
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const int a = n_above + before + mine_up, e = n_equal + same_before + mine_same;
+                if (up[b] || (same[b] && e < need)) out[a + min(e, need)] = base + i + b;
+                mine_up += up[b];
+                mine_same += same[b];
+            }
+            n_above += all_up;
+            n_equal += all_same;
         }
         if (C > 1) cluster_sync();  // the others may still read this CTA's counts
     }
