@@ -1243,8 +1243,11 @@ def update_block_tables(block_table, old_seqlens, new_seqlens, free_blocks, num_
         _arg_vector("num_free", num_free, i32, 1, dev)
     B, max_blocks = block_table.shape
     nb = free_blocks.shape[0]
-    num_rows, block_size = _int32("num_rows", num_rows), _int32("block_size", block_size)
-    _require(num_rows >= 0, "num_rows must not be negative")
+    num_rows, block_size = int(num_rows), int(block_size)
+    if not (0 <= num_rows <= _WIDEST and 0 < block_size <= _WIDEST):
+        _int32("num_rows", num_rows)
+        _int32("block_size", block_size)
+        _require(num_rows >= 0, "num_rows must not be negative")
     err = _error_word(dev_error, dev)
     # what is changed in place lies apart from the rest
     t0, f0, n0 = block_table.data_ptr(), free_blocks.data_ptr(), num_free.data_ptr()
@@ -1274,19 +1277,13 @@ def update_block_tables(block_table, old_seqlens, new_seqlens, free_blocks, num_
 
     def call(handle):
         empty, device = ty.torch.empty, block_table.device
-        if fresh:
-            slots, pos = empty((2, num_rows), dtype=ty.i64, device=device).unbind(0)
-            cuq, cuk = empty((2, B + 1), dtype=i32, device=device).unbind(0)
-        else:
-            slots = empty(num_rows, dtype=ty.i64, device=device) if slot_mapping is None else slot_mapping
-            pos = empty(num_rows, dtype=ty.i64, device=device) if positions is None else positions
-            cuq = empty(B + 1, dtype=i32, device=device) if cu_seq_lens_q is None else cu_seq_lens_q
-            cuk = empty(B + 1, dtype=i32, device=device) if cu_seq_lens_k is None else cu_seq_lens_k
-        sp, cp = slots.data_ptr(), cuq.data_ptr()
+        slots = empty(num_rows, dtype=ty.i64, device=device) if slot_mapping is None else slot_mapping
+        pos = empty(num_rows, dtype=ty.i64, device=device) if positions is None else positions
+        cuq = empty(B + 1, dtype=i32, device=device) if cu_seq_lens_q is None else cu_seq_lens_q
+        cuk = empty(B + 1, dtype=i32, device=device) if cu_seq_lens_k is None else cu_seq_lens_k
         return (slots, pos, cuq, cuk), lib.pkv_update_block_tables(
-            t0, max_blocks, o0, w0, B, f0, nb, n0, block_size, sp,
-            sp + 8 * num_rows if fresh else pos.data_ptr(), num_rows, cp,
-            cp + 4 * B + 4 if fresh else cuk.data_ptr(), err, handle)
+            t0, max_blocks, o0, w0, B, f0, nb, n0, block_size, slots.data_ptr(), pos.data_ptr(),
+            num_rows, cuq.data_ptr(), cuk.data_ptr(), err, handle)
     outs, st = _on_stream(dev, stream, call)
     if st:
         _check("pkv_update_block_tables", st)
@@ -1380,10 +1377,15 @@ def select_pages(q, page_bounds, bounds_scale, block_table, cache_seqlens, max_s
     dev = _cuda_index("q", q)
     nb, hkv, d = _bounds(page_bounds, bounds_scale, dev)
     total_q, Hq, B, max_blocks = _rows(q, d, block_table, cache_seqlens, cu_seq_lens_q, dev)
-    max_seqlen, top_k = _int32("max_seqlen", max_seqlen), _int32("top_k", top_k)
-    block_size = _int32("block_size", block_size)
-    num_first, num_recent = _int32("num_first", num_first), _int32("num_recent", num_recent)
-    _require(top_k > 0, "top_k must be positive")
+    max_seqlen, top_k, block_size = int(max_seqlen), int(top_k), int(block_size)
+    num_first, num_recent = int(num_first), int(num_recent)
+    if not (0 <= max_seqlen <= _WIDEST and 0 < top_k <= _WIDEST and 0 < block_size <= _WIDEST
+            and 0 <= num_first <= _WIDEST and 0 < num_recent <= _WIDEST):
+        for name, value in (("max_seqlen", max_seqlen), ("top_k", top_k),
+                            ("block_size", block_size), ("num_first", num_first),
+                            ("num_recent", num_recent)):
+            _int32(name, value)
+        _require(top_k > 0, "top_k must be positive")
     shape = (total_q, hkv, top_k)
     if pages is not None:
         _arg_shape("pages", pages, ty.i32, shape, dev)

@@ -100,8 +100,6 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(const TableParam
     __shared__ uint32_t s_bad;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = (int)cluster_rank();
-    const int gtid = rank * kThreads + threadIdx.x;
-    constexpr int kAll = kCluster * kThreads;
     const int B = p.batch, M = p.max_blocks_per_seq, shift = p.bs_shift;
 
     pdl_wait();
@@ -163,15 +161,27 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(const TableParam
         bad |= PKV_DEVERR_BLOCK_ID;
     if (height < 0) bad |= PKV_DEVERR_NO_BLOCKS;
     const int total = (int)run.tok, A = (int)run.taken, R = (int)run.gone;
+    // A small step (all CTAs see the same sums) is done by the first CTA alone, without
+    // the cluster's barriers.
+    constexpr int kFew = kAtOnce * kThreads;
+    const bool alone = max(run.taken, run.gone) <= (uint32_t)kFew && p.rows <= kFew && B <= kFew;
+    if (alone && rank > 0) return;
+    const int gtid = rank * kThreads + threadIdx.x, all = alone ? kThreads : kCluster * kThreads;
+    auto sync = [&] {
+        if (alone)
+            __syncthreads();
+        else
+            cluster_sync();
+    };
     const bool countable = __syncthreads_or((int)bad) == 0;
 
     const int moves = max(A, R), step = first_step(B);
-    // The pages kAll apart from i on: ids, and the entries of the table that they leave
+    // The pages `all` apart from i on: ids, and the entries of the table that they leave
     // (nullptr: of the stack).
     auto pages_from = [&](int i, int (&id)[kAtOnce], int32_t *(&from)[kAtOnce]) {
         int at[kAtOnce], r[kAtOnce];
 #pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) at[k] = min(i + k * kAll, moves);
+        for (int k = 0; k < kAtOnce; ++k) at[k] = min(i + k * all, moves);
         find(s_gone, B, step, at, r);
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
@@ -189,13 +199,13 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(const TableParam
     int32_t *from[kAtOnce];
     if (countable) {
         // every id that will be moved, and the pages that new tokens go on filling
-        for (int i = gtid; i < moves; i += kAtOnce * kAll) {
+        for (int i = gtid; i < moves; i += kAtOnce * all) {
             pages_from(i, id, from);
 #pragma unroll
             for (int k = 0; k < kAtOnce; ++k)
                 if (id[k] < 0 || id[k] >= p.num_blocks) bad |= PKV_DEVERR_BLOCK_ID;
         }
-        for (int r = gtid; r < B; r += kAll) {
+        for (int r = gtid; r < B; r += all) {
             const int a = p.old_len[r];
             if (p.new_len[r] > a && (a & (p.block_size - 1))) {
                 const int e = p.block_table[(int64_t)r * M + (a >> shift)];
@@ -204,27 +214,28 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(const TableParam
         }
     }
     if (bad) atomicOr(&s_bad, bad);
-    cluster_sync();  // every CTA has read num_free and checked its part
-    bad = 0;
+    sync();  // every CTA has read num_free and checked its part
+    bad = s_bad;
+    if (!alone)
 #pragma unroll
-    for (int c = 0; c < kCluster; ++c) bad |= cluster_ld32(cluster_addr(smem_u32(&s_bad), c));
+        for (int c = 0; c < kCluster; ++c) bad |= cluster_ld32(cluster_addr(smem_u32(&s_bad), c));
     if (bad) {  // nothing is moved, no row has a slot, no request a query or a key
         if (gtid == 0) flag_error(p.dev_error, bad);
         if (rank == 0)
             for (int r = threadIdx.x; r <= B; r += kThreads) p.cu_q[r] = p.cu_k[r] = 0;
         if (p.rows_here)
-            for (int t = gtid; t < p.rows; t += kAll) {
+            for (int t = gtid; t < p.rows; t += all) {
                 p.slots[t] = -1;
                 p.positions[t] = 0;
             }
-        cluster_sync();  // the others may still read s_bad
+        sync();  // the others may still read s_bad
         return;
     }
-    for (int i = gtid; i < moves; i += kAtOnce * kAll) {
-        if (moves > kAtOnce * kAll) pages_from(i, id, from);  // (else: as they were checked)
+    for (int i = gtid; i < moves; i += kAtOnce * all) {
+        if (moves > kAtOnce * all) pages_from(i, id, from);  // (else: as they were checked)
         int at[kAtOnce], r[kAtOnce];
 #pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) at[k] = min(i + k * kAll, moves);
+        for (int k = 0; k < kAtOnce; ++k) at[k] = min(i + k * all, moves);
         find(s_take, B, step, at, r);
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
@@ -238,10 +249,10 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(const TableParam
         }
     }
     if (gtid == 0) *p.num_free = F + R - A;
-    cluster_sync();  // the tables are written
+    sync();  // the tables are written
     if (p.rows_here)
-        for (int t = gtid; t < p.rows; t += kAtOnce * kAll)
-            write_rows<true>(p, s_tok, t, kAll, total);
+        for (int t = gtid; t < p.rows; t += kAtOnce * all)
+            write_rows<true>(p, s_tok, t, all, total);
 }
 
 __global__ void __launch_bounds__(kRowThreads) block_rows_kernel(const TableParams p) {
