@@ -249,6 +249,12 @@ pkv_status pkv_paged_sparse_attention(void *out, const void *q, const void *k_ca
     if ((st = pool_map(&tk, k_cache, cache, rows)) != PKV_OK) return st;
     if ((st = pool_map(&tv, v_cache, cache, rows)) != PKV_OK) return st;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!fp8 && cu_seq_lens_q && total_q >= 4LL * batch) {  // chunks: 4 queries on average
+        bool fits = false;
+        const cudaError_t e =
+            launch_sparse_tile(p, fits, cache.block_size, k_cache, v_cache, &tk, &tv, s);
+        if (fits) return from_cuda(e);
+    }
     return from_cuda(fp8 ? launch_sparse_fp8(p, cache.block_size, &tk, &tv, s)
                          : launch_sparse(p, cache.block_size, &tk, &tv, s));
 }

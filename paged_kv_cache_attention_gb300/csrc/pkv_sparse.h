@@ -67,6 +67,7 @@ struct SparseParams {
     int top_k, hnd;
     int cluster;                   // CTAs per row and kv head
     int cap;                       // list entries a CTA has room for
+    int words, group_shift;        // tiles of queries: see sparse_tile.cu
     float scale_log2;
 };
 
@@ -75,6 +76,10 @@ cudaError_t launch_page_bounds(const BoundsParams &p, cudaStream_t stream);
 cudaError_t launch_select_pages(const SelectParams &p, cudaStream_t stream);
 cudaError_t launch_sparse(const SparseParams &p, int block_size, const CUtensorMap *tmap_k,
                           const CUtensorMap *tmap_v, cudaStream_t stream);
+// Tiles of queries; fits: whether there is a kernel for the shape (else nothing is done).
+cudaError_t launch_sparse_tile(const SparseParams &p, bool &fits, int block_size,
+                               const void *k_cache, const void *v_cache, const CUtensorMap *tmap_k,
+                               const CUtensorMap *tmap_v, cudaStream_t stream);
 cudaError_t launch_sparse_fp8(const SparseParams &p, int block_size, const CUtensorMap *tmap_k,
                               const CUtensorMap *tmap_v, cudaStream_t stream);
 

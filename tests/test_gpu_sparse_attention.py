@@ -112,6 +112,91 @@ def test_chunks(layout, fp8, queries, lens):
     run(lens, queries, 8, 2, 64, 16, layout, fp8, top_k=9, sink=True, extra=4, chunk=True)
 
 
+@pytest.mark.parametrize("kind", ["last", "random"])
+@pytest.mark.parametrize("hq,hkv,d,bs", [(2, 2, 64, 16), (4, 2, 80, 32), (6, 2, 128, 16),
+                                         (5, 1, 96, 16), (8, 1, 128, 32), (11, 1, 112, 16),
+                                         (32, 2, 64, 32), (6, 2, 256, 16)])
+def test_tiles_of_queries(hq, hkv, d, bs, kind):
+    """Every width of a group; tiles that hold the ends of requests."""
+    run([17 * bs + 5, 3, 60 * bs, 11 * bs + 1], [21, 3, 37, 9], hq, hkv, d, bs, top_k=8, kind=kind,
+        sink=True, extra=3, layout="HND")
+
+
+def test_wide_lists_and_tables():
+    """Unions of hundreds of pages; a table too wide for them to be numbered."""
+    run([16 * 700 + 3], [9], 4, 1, 64, top_k=150)
+    g = torch.Generator().manual_seed(9)
+    pools = R.Pools(40, 16, 2, 64, "NHD", False, g)
+    narrow, slots = R.paged([300, 200], 16, 40, g)
+    kc, vc, _, _ = pools.device(DEV)
+    q = torch.randn(10, 4, 64, generator=g).to(BF16).to(DEV)
+    lens = torch.tensor([300, 200], dtype=I32, device=DEV)
+    cu = torch.tensor([0, 6, 10], dtype=I32, device=DEV)
+    rows = S.rows_of([6, 4], [300, 200])
+    pages = lists(rows, 2, 5, 16, random.Random(9), "last").to(DEV)
+    wide = torch.full((2, 700000), -1, dtype=I32)
+    wide[:, :narrow.shape[1]] = narrow
+    outs = [pkv.paged_sparse_attention(q, kc, vc, t.to(DEV), lens, pages, cu_seq_lens_q=cu)
+            for t in (narrow, wide)]
+    ref, _, absv, smax, _ = S.attend_lists(q.cpu(), pools, slots, rows, pages.cpu(), 16, 0.125, None)
+    for o in outs:
+        R.assert_within(o, ref, R.out_bound(ref, absv, smax, 64, 2.0 ** -8), "out")
+
+
+@pytest.mark.parametrize("pool", [0, 1])
+@pytest.mark.parametrize("value", ["nan", "inf", "-inf"])
+def test_chunk_with_a_key_that_is_not_finite(pool, value):
+    """It reaches the queries that keep it, and not those that share its page's loads:
+    a page of some, a page of all of which some see only a part, a page of all."""
+    def edit(pools, slots):
+        for at in (slots[0][37], slots[0][295], slots[1][3]):
+            pools.rows[pool][at // 16, 0, at % 16, 5] = float(value)
+
+    out, lse, ref, rl, bound, lb = run([300, 40], [16, 8], 4, 1, 64, top_k=9, edit=edit, seed=7)
+    fin = torch.isfinite(ref)
+    assert 0 < int(fin.sum()) < fin.numel()
+    assert torch.equal(torch.isnan(out), torch.isnan(ref))
+    bad = ~fin & ~torch.isnan(ref)
+    assert torch.equal(out.double()[bad], ref[bad])
+    off = torch.where(fin, (out.double() - ref).abs() - bound, torch.zeros_like(ref))
+    assert float(off.max()) <= 0
+    # (a row with a score of +inf: its sum is infinite, and taken relative to its largest
+    # score it is inf - inf, so that such an lse is either)
+    fin = torch.isfinite(rl)
+    assert torch.equal(torch.isfinite(lse), fin)
+    off = torch.where(fin, (lse.double() - rl).abs() - lb, torch.zeros_like(rl))
+    assert float(off.max()) <= 0
+
+
+def test_chunk_lists_that_end_early():
+    """Lists of a chunk with errors and entries behind their end; pages out of the pool."""
+    pools, table, slots, _ = small()
+    g = torch.Generator().manual_seed(11)
+    q = torch.randn(6, 2, 64, generator=g).to(BF16)
+    given = [[1, 3, 5, -1], [1, -1, 3, 5], [1, 3, 3, 5], [3, 1, 4, 5], [1, 3, 7, 8], [0, 2, 4, 6]]
+    held = [[1, 3, 5, -1], [1, -1, -1, -1], [1, 3, -1, -1], [3, -1, -1, -1], [1, 3, -1, -1],
+            [0, 2, -1, -1]]
+    kc, vc, _, _ = pools.device(DEV)
+    err = torch.zeros(1, dtype=I32, device=DEV)
+    cu, lens = (torch.tensor(x, dtype=I32, device=DEV) for x in ([0, 6], [100]))
+    for broken, bits in ((False, pkv.DEVERR_BLOCK_ID), (True, pkv.DEVERR_BLOCK_ID)):
+        t = table.clone()
+        want = [list(x) for x in held]
+        if broken:
+            t[0, 4] = -1
+            want[5] = [0, 2, 6, -1]
+        else:
+            want[5] = [0, 2, 4, 6]
+        out = pkv.paged_sparse_attention(q.to(DEV), kc, vc, t.to(DEV), lens,
+                                         torch.tensor(given, dtype=I32, device=DEV).view(6, 1, 4),
+                                         cu_seq_lens_q=cu, dev_error=err)
+        assert pkv.get_device_error(err, clear=True) == bits
+        pages = torch.tensor(want, dtype=I32).view(6, 1, 4)
+        ref, _, absv, smax, _ = S.attend_lists(q, pools, slots, S.rows_of([6], [100]), pages, 16, 0.125,
+                                               None)
+        R.assert_within(out, ref, R.out_bound(ref, absv, smax, 64, 2.0 ** -8), "out")
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_empty_lists(fp8):
     """Rows without keys: zeros, and the sink (or -inf) as lse."""
