@@ -79,6 +79,46 @@ __device__ __forceinline__ bool row_request(const RowParams &p, int t, int block
     return true;
 }
 
+// The rows [t0, t_end) of a tile of `queries` rows.  With few requests a tile holds rows
+// of one request only, and the tiles are numbered request by request (one that holds
+// the end of one request and the beginning of the next would take twice as long);
+// else every `queries` rows.  Taken by a whole warp.
+__device__ __forceinline__ void tile_rows(const RowParams &p, int tile, int queries, int &t0,
+                                          int &t_end) {
+    t0 = t_end = 0;
+    if (p.batch > kTiledRequests) {
+        const int64_t t = (int64_t)tile * queries;
+        t0 = (int)min(t, (int64_t)p.rows);
+        t_end = (int)min(t + queries, (int64_t)p.rows);
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    for (int r0 = 0; r0 < p.batch; r0 += 32) {
+        const int r = r0 + lane;
+        int a = 0, b = 0;
+        if (r < p.batch) {
+            a = min(max(p.cu_q[r], 0), p.rows);
+            b = min(max(p.cu_q[r + 1], a), p.rows);
+        }
+        const int own = (b - a + queries - 1) / queries;
+        int sum = own;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, sum, off);
+            if (lane >= off) sum += o;
+        }
+        const uint32_t over = __ballot_sync(0xffffffffu, sum > tile);
+        if (over) {
+            const int w = __ffs(over) - 1;
+            const int k = tile - __shfl_sync(0xffffffffu, sum - own, w);
+            t0 = __shfl_sync(0xffffffffu, a, w) + k * queries;
+            t_end = min(t0 + queries, __shfl_sync(0xffffffffu, b, w));
+            return;
+        }
+        tile -= __shfl_sync(0xffffffffu, sum, 31);
+    }
+}
+
 // The list of a row: strictly ascending pages below npages.  It ends at the first
 // entry that is negative, not above the one before it or not a page of the row (the
 // last two are errors).  Returns the entries before that; all threads of the CTA.

@@ -45,6 +45,13 @@ struct RowParams {
     int num_kv_heads, group, head_dim;
 };
 
+// Tiles of `queries` rows that cover all rows (tile_rows).
+constexpr int kTiledRequests = 256;
+inline int64_t row_tiles(const RowParams &r, int queries) {
+    const int64_t tiles = ((int64_t)r.rows + queries - 1) / queries;
+    return r.batch > kTiledRequests ? tiles : tiles + (r.batch < r.rows ? r.batch : r.rows);
+}
+
 struct SelectParams {
     RowParams r;
     const void *q;                 // [rows, Hq, D] bf16

@@ -138,11 +138,12 @@ __global__ void __launch_bounds__(Shape<NCH, NT, GP>::WARPS * 32) select_pages_k
     const int gq = lane >> 2, tq = lane & 3;
     const int C = p.cluster, rank = C > 1 ? (int)cluster_rank() : 0;
     const int64_t unit = blockIdx.x / (unsigned)C;
-    const int t0 = (int)(unit / p.r.num_kv_heads) * QT, g = (int)(unit % p.r.num_kv_heads);
+    const int tile = (int)(unit / p.r.num_kv_heads), g = (int)(unit % p.r.num_kv_heads);
     const int D = p.r.head_dim, G = p.r.group, shift = p.bs_shift;
-    const int t_end = min(t0 + QT, p.r.rows);
 
     pdl_wait();
+    int t0 = tile, t_end = tile + 1;
+    if (QT > 1) tile_rows(p.r, tile, QT, t0, t_end);
     // the tile's rows, request by request (one, but where requests meet)
     for (int t = t0; t < t_end;) {
         int r, L, count;
@@ -747,7 +748,7 @@ template <int NCH, int NT, int GP>
 cudaError_t launch_as(SelectParams p, bool &fits, cudaStream_t stream) {
     using S = Shape<NCH, NT, GP>;
     auto kern = select_pages_kernel<NCH, NT, GP>;
-    const int64_t units = (p.r.rows + (int64_t)S::QT - 1) / S::QT * p.r.num_kv_heads;
+    const int64_t units = (S::QT > 1 ? row_tiles(p.r, S::QT) : p.r.rows) * p.r.num_kv_heads;
     const int n = (p.r.max_seqlen + p.block_size - 1) >> p.bs_shift;
     // as many CTAs per tile as there is room for at once, of at least 256 pages, and
     // more if the scores would not fit

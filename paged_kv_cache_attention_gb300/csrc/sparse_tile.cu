@@ -123,7 +123,8 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
     uint8_t *smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // 1024-aligned
     const uint32_t base = smem_u32(smem), bars = base + kOffBar;
     uint16_t *s_page = reinterpret_cast<uint16_t *>(smem + kOffList);
-    uint32_t *s_own = reinterpret_cast<uint32_t *>(s_page + (p.cap + 1) / 2 * 2);
+    uint32_t *s_own = reinterpret_cast<uint32_t *>(s_page + (p.cap + PP + 1) / 2 * 2);
+    __shared__ int s_end[kRows];       // where the queries' lists end
     __shared__ float s_max[2][kRows];  // the rows' largest scores (in the end: sums) by halves
     __shared__ int s_dead;  // a wait gave up: all others do
     __shared__ int s_bad;   // a value that is not finite
@@ -135,8 +136,7 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.r.group, Dh = p.r.head_dim, Hkv = p.r.num_kv_heads;
     const int queries = kRows >> p.group_shift;
-    const int g = blockIdx.x % Hkv, t0 = (int)(blockIdx.x / Hkv) * queries;
-    const int t_end = min(t0 + queries, p.r.rows);
+    const int g = blockIdx.x % Hkv;
     uint32_t *s_bits = s_own + queries * p.words;            // the union's
     int *s_before = reinterpret_cast<int *>(s_bits + p.words);
 
@@ -145,14 +145,14 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
             mbar_init(bar(i), i == kPFull ? kSoft : 1);
         fence_barrier_init();
         s_dead = s_bad = 0;
-        tma_prefetch_desc(&tmk);
-        tma_prefetch_desc(&tmv);
     }
     if (warp == kIssue) {
         tc::tmem_alloc(base + kOffTmem, kCols);
         tc::tmem_relinquish();
     }
     pdl_wait();
+    int t0, t_end;
+    tile_rows(p.r, (int)(blockIdx.x / Hkv), queries, t0, t_end);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -178,34 +178,11 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
             const int j = i / words, w = i - j * words;
             (j < nq ? s_own + j * p.words : s_bits)[w] = 0;
         }
-        __syncthreads();
-#pragma unroll 1
-        for (int j = warp; j < nq; j += kThreads / 32) {
-            const int npages = (max(L + j, 0) + BS - 1) >> SHIFT;
-            const int32_t *list = p.pages + ((int64_t)(first + j) * Hkv + g) * p.top_k;
-            int last = -1;  // the entry before these 32
-#pragma unroll 1
-            for (int e0 = 0; e0 < p.top_k; e0 += 32) {
-                const int e = e0 + lane < p.top_k ? list[e0 + lane] : -1;
-                int before = __shfl_up_sync(0xffffffffu, e, 1);
-                if (lane == 0) before = last;
-                const uint32_t end = __ballot_sync(0xffffffffu, e <= before || e >= npages);
-                const int good = end ? __ffs(end) - 1 : 32;
-                if (lane == good && e >= 0) flag_error(p.r.dev_error, PKV_DEVERR_BLOCK_ID);
-                if (lane < good) {
-                    const int id = bt[e];
-                    if (id >= 0 && id < p.r.num_blocks) {
-                        atomicOr(&s_own[j * p.words + (e >> 5)], 1u << (e & 31));
-                        atomicOr(&s_bits[e >> 5], 1u << (e & 31));
-                    } else {
-                        flag_error(p.r.dev_error, PKV_DEVERR_BLOCK_ID);
-                    }
-                }
-                if (end) break;
-                last = __shfl_sync(0xffffffffu, e, 31);
-            }
-        }
-        // Q: row = query << group_shift | head, 128-byte swizzle; zeros in rows that are none
+        if (threadIdx.x < nq) s_end[threadIdx.x] = p.top_k;
+        // Q: row = query << group_shift | head, 128-byte swizzle; zeros in rows that are none.
+        // A negative scale goes into Q, so that scores grow with the products, and one of 0 too.
+        const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+#pragma unroll 4
         for (int i = threadIdx.x; i < kRows * 16; i += kThreads) {
             const int row = i >> 4, c = i & 15;
             const int j = row >> p.group_shift, h = row & ((1 << p.group_shift) - 1);
@@ -214,7 +191,38 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
                 v = *reinterpret_cast<const uint4 *>(
                     static_cast<const __nv_bfloat16 *>(p.q) +
                     (((int64_t)(first + j) * Hkv + g) * G + h) * Dh + c * 8);
-            *reinterpret_cast<uint4 *>(smem + kOffQ + (c >> 3) * kHalf + sw128(row, c & 7)) = v;
+            *reinterpret_cast<uint4 *>(smem + kOffQ + (c >> 3) * kHalf + sw128(row, c & 7)) =
+                p.scale_log2 == 0.f ? make_uint4(0u, 0u, 0u, 0u)
+                                    : make_uint4(v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign);
+        }
+        __syncthreads();
+        // where each list ends, then its bits
+        const int64_t list_step = (int64_t)Hkv * p.top_k;
+        const int32_t *lists = p.pages + ((int64_t)first * Hkv + g) * p.top_k;
+        const int entries = nq * p.top_k;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < entries; i += kThreads) {
+            const int j = i / p.top_k, x = i - j * p.top_k;
+            const int32_t *list = lists + j * list_step;
+            const int e = list[x], before = x > 0 ? list[x - 1] : -1;
+            if (e <= before || e >= (max(L + j, 0) + BS - 1) >> SHIFT) atomicMin(&s_end[j], x);
+        }
+        __syncthreads();
+#pragma unroll 4
+        for (int i = threadIdx.x; i < entries; i += kThreads) {
+            const int j = i / p.top_k, x = i - j * p.top_k;
+            const int e = lists[j * list_step + x];
+            if (x < s_end[j]) {
+                const int id = bt[e];
+                if (id >= 0 && id < p.r.num_blocks) {
+                    atomicOr(&s_own[j * p.words + (e >> 5)], 1u << (e & 31));
+                    atomicOr(&s_bits[e >> 5], 1u << (e & 31));
+                } else {
+                    flag_error(p.r.dev_error, PKV_DEVERR_BLOCK_ID);
+                }
+            } else if (x == s_end[j] && e >= 0) {
+                flag_error(p.r.dev_error, PKV_DEVERR_BLOCK_ID);
+            }
         }
         fence_proxy_async_smem();
         __syncthreads();
@@ -240,6 +248,7 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
             int at = s_before[w];
             for (uint32_t b = s_bits[w]; b; b &= b - 1) s_page[at++] = (uint16_t)(w * 32 + __ffs(b) - 1);
         }
+        if (threadIdx.x < PP) s_page[n + threadIdx.x] = 0;  // up to the last step's end
         __syncthreads();
 
         if (warp == kLoad) {
@@ -358,59 +367,58 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
             const bool live = j0 < nq && h < G;
             const int limit = live ? L + j0 : 0;
             const uint32_t *own = s_own + (live ? j0 : 0) * p.words;
+            const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
             float ref = kNegInf, l = 0.f;
             bool ok = true;
 #pragma unroll 1
             for (int j = 0; j < steps; ++j) {
                 const int k = done + j;
                 // keys of each page that the row keeps; pages that some row of the warp does
-                int held[HP];
-                uint32_t any = 0;
-                bool part = false;
+                uint32_t held = 0, any = 0;  // 8 bits a page
+                const int i0 = j * PP + half * HP;
+                const uint32_t *two = reinterpret_cast<const uint32_t *>(s_page + i0);
 #pragma unroll
-                for (int g2 = 0; g2 < HP; ++g2) {
-                    const int i = j * PP + half * HP + g2;
-                    held[g2] = 0;
-                    if (i < n) {
-                        const int page = s_page[i];
-                        if (live && (own[page >> 5] >> (page & 31)) & 1)
-                            held[g2] = min(max(limit - page * BS, 0), BS);
-                    }
-                    if (__any_sync(0xffffffffu, held[g2] > 0)) any |= 1u << g2;
-                    part = part || (held[g2] > 0 && held[g2] < BS);
+                for (int g2 = 0; g2 < HP; ++g2) {  // (entries past the last: page 0)
+                    const int page = (two[g2 / 2] >> (g2 % 2 * 16)) & 0xffff;
+                    const bool mine = live && i0 + g2 < n && (own[page >> 5] >> (page & 31)) & 1;
+                    const int keep = mine ? min(max(limit - page * BS, 0), BS) : 0;
+                    held |= (uint32_t)keep << (8 * g2);
+                    any |= (keep > 0 ? 1u << g2 : 0u) | (keep > 0 && keep < BS ? 256u : 0u);
                 }
-                part = __any_sync(0xffffffffu, part);
+                any = __reduce_or_sync(0xffffffffu, any);
+                const bool part = any & 256u;
                 if (!__all_sync(0xffffffffu, wait(kSFull, k & 1))) {
                     ok = false;
                     break;
                 }
                 tc::fence_after_sync();
-                constexpr int CP = 32 / BS;  // pages of 32 keys
-                float mx = kNegInf;
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    if (!((any >> (c * CP)) & ((1u << CP) - 1u))) continue;
-                    uint32_t s[32];
-                    tc::ld_32x32b_x32(colS + lanes + half * 64 + c * 32, s);
+                // 16 keys at a time, those of pages that some row of the warp keeps.  (Rolled
+                // loops: code that is not in the instruction cache costs more than they do.)
+                constexpr int KP = BS / 16;
+                const uint32_t colH = colS + lanes + half * 64;
+                auto load_scores = [&](int c, uint32_t (&s)[16]) {
+                    tc::ld_32x32b_x16(colH + c * 16, s);
+                    const int keep = (int)((held >> (8 * (c / KP))) & 255u) - c % KP * 16;
                     tc::wait_ld();
+                    if (part)
 #pragma unroll
-                    for (int g2 = 0; g2 < CP; ++g2) {
-                        const int keep = held[c * CP + g2];
-                        float top = kNegInf;
-                        if (!part) {
+                        for (int e = 0; e < 16; ++e)
+                            if (e >= keep) s[e] = 0xff800000u;
+                    return keep > 0;
+                };
+                float mx = kNegInf;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    if (!((any >> (c / KP)) & 1u)) continue;
+                    uint32_t s[16];
+                    const bool mine = load_scores(c, s);
+                    float top = kNegInf;
 #pragma unroll
-                            for (int e = 0; e < BS; e += 2)
-                                top = fmax3(top, __uint_as_float(s[g2 * BS + e]) * p.scale_log2,
-                                            __uint_as_float(s[g2 * BS + e + 1]) * p.scale_log2);
-                            if (keep) mx = fmaxf(mx, top);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < BS; ++e)
-                                if (e < keep)
-                                    mx = fmaxf(mx, __uint_as_float(s[g2 * BS + e]) * p.scale_log2);
-                        }
-                    }
+                    for (int e = 0; e < 16; e += 2)
+                        top = fmax3(top, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                    if (mine) mx = fmaxf(mx, top);
                 }
+                mx *= scale;
                 s_max[half][row] = mx;
                 pair_sync();
                 mx = fmaxf(mx, s_max[half ^ 1][row]);
@@ -439,32 +447,28 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
                     ref = next;
                 }
                 const float sub = ref == kNegInf ? 0.f : ref;
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t w[16];
-                    if ((any >> (c * CP)) & ((1u << CP) - 1u)) {
-                        uint32_t s[32];
-                        tc::ld_32x32b_x32(colS + lanes + half * 64 + c * 32, s);
-                        tc::wait_ld();
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t w[8];
+                    if ((any >> (c / KP)) & 1u) {
+                        uint32_t s[16];
+                        const bool mine = load_scores(c, s);
                         float sum[2] = {0.f, 0.f};
+                        const uint32_t all = mine ? 0xffffffffu : 0u;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const int keep = held[c * CP + e / BS];
-                            float x[2];
-#pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                x[u] = fast_exp2(fmaf(__uint_as_float(s[e + u]), p.scale_log2, -sub));
-                                x[u] = (part ? (e + u) % BS < keep : keep > 0) ? x[u] : 0.f;
-                                sum[u] += x[u];
-                            }
-                            w[e / 2] = pack_bf16(x[0], x[1]);
+                        for (int e = 0; e < 16; e += 2) {
+                            const float x = fast_exp2(fmaf(__uint_as_float(s[e]), scale, -sub));
+                            const float y = fast_exp2(fmaf(__uint_as_float(s[e + 1]), scale, -sub));
+                            sum[0] += x;
+                            sum[1] += y;
+                            w[e / 2] = pack_bf16(x, y) & all;
                         }
-                        l += sum[0] + sum[1];
+                        if (mine) l += sum[0] + sum[1];
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) w[e] = 0u;
+                        for (int e = 0; e < 8; ++e) w[e] = 0u;
                     }
-                    tc::st_32x32b_x16(colS + lanes + half * 64 + c * 16, w);
+                    tc::st_32x32b_x8(colH + c * 8, w);
                 }
                 tc::wait_st();
                 tc::fence_before_sync();
@@ -525,8 +529,9 @@ cudaError_t launch_bs(SparseParams p, bool &fits, const void *k, const void *v,
     const int64_t queries = kRows >> p.group_shift, lists = queries * p.top_k;
     p.cap = (int)(lists < p.r.max_blocks_per_seq ? lists : p.r.max_blocks_per_seq);
     p.words = p.r.max_blocks_per_seq / 32 + 1;
-    const int64_t smem = 1024 + kOffList + (p.cap + 2) * 2LL + ((queries + 2) * p.words + 1) * 4LL;
-    const int64_t grid = (p.r.rows + queries - 1) / queries * p.r.num_kv_heads;
+    const int64_t smem = 1024 + kOffList + (p.cap + kKeys / BS + 2) * 2LL +
+                         ((queries + 2) * p.words + 1) * 4LL;
+    const int64_t grid = row_tiles(p.r, (int)queries) * p.r.num_kv_heads;
     fits = smem <= 224 * 1024 && grid <= 0x7fffffff && p.r.max_blocks_per_seq <= 65536;
     if (!fits) return cudaErrorNotSupported;
     auto kern = sparse_tile_kernel<BS>;

@@ -122,6 +122,11 @@ def test_tiles_of_queries(hq, hkv, d, bs, kind):
         sink=True, extra=3, layout="HND")
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
+def test_chunk_scales(scale):
+    run([300, 33], [9, 7], 4, 2, 64, top_k=9, scale=scale, sink=True)
+
+
 def test_wide_lists_and_tables():
     """Unions of hundreds of pages; a table too wide for them to be numbered."""
     run([16 * 700 + 3], [9], 4, 1, 64, top_k=150)
