@@ -102,8 +102,8 @@ __device__ __forceinline__ void block_sync(bool cluster) {
 template <int NCH, int NT, int GP>
 struct Shape {
     static constexpr int QT = NT * 8 / GP;               // queries of a tile
-    static constexpr int WARPS = QT == 1 ? 4 : 8;
-    static constexpr int NST = 2;                        // 16-page tiles in flight per warp
+    static constexpr int WARPS = QT == 1 ? 4 : 16;
+    static constexpr int NST = QT == 1 ? 2 : 1;          // 16-page tiles in the ring per warp
     // Few columns: 1152 is taken off the sums, not off each code.  Four sums for a
     // quarter of the channels each stay below 2^24 (32 channels * 255 * 1279).
     static constexpr bool OFFSET = NT <= 2 && NCH <= 4;
@@ -324,10 +324,11 @@ __global__ void __launch_bounds__(Shape<NCH, NT, GP>::WARPS * 32) select_pages_k
         // scores of 16 pages at a time, this warp's tiles every kWarps-th
 #pragma unroll 1
         for (int k = 0; k < mine; ++k) {
-            keep_byte(k + NST - 2);
+            if (NST > 1) keep_byte(k + NST - 2);
             if (k + NST - 1 < mine) issue(k + NST - 1);
             asm volatile("cp.async.commit_group;" ::: "memory");
             asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");
+            if (NST == 1) keep_byte(k);
             __syncwarp();
             const uint32_t tile = ring + (k % NST) * S::STAGE;
             {
