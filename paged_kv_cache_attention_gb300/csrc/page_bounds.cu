@@ -30,6 +30,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
+constexpr int kRounds = 8;
 
 template <bool FP8>
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {  // a NaN stays
@@ -64,13 +65,11 @@ __device__ __forceinline__ void unpack2(uint32_t w, float f, float &x, float &y)
     }
 }
 
-// The code of x * inv, rounded up or down.  The product is exact, or below the
-// smallest float: still not 0.
-__device__ __forceinline__ uint32_t code_of(float x, float inv, bool up) {
-    const float y = x * inv;
-    const int c = up ? max(__float2int_ru(y), x > 0.f ? 1 : -128)
-                     : min(__float2int_rd(y), x < 0.f ? -1 : 127);
-    return (uint32_t)c & 0xffu;
+// The code of x * inv rounded up, for a lower bound (x has its sign turned) with the sign
+// turned back.  The product is exact, or below the smallest float: still not 0.
+__device__ __forceinline__ uint32_t code_of(float x, float inv, bool upper) {
+    const int c = max(__float2int_ru(x * inv), x > 0.f ? 1 : -127);
+    return (uint32_t)(upper ? c : -c) & 0xffu;
 }
 
 // Least and largest of a page whose row scales lie far apart, in fp32; the channels
@@ -158,10 +157,10 @@ __global__ void __launch_bounds__(kThreads) page_bounds_kernel(const BoundsParam
                                (p.hnd ? unit * BS * D * E
                                       : (blk * BS * p.num_kv_heads + g) * (int64_t)D * E) +
                                (in ? c * 16 : 0);
-            uint4 x[ROWS];  // (rows past the last: the last again)
+            uint4 raw[ROWS];  // (rows past the last: the last again)
 #pragma unroll
             for (int i = 0; i < ROWS; ++i)
-                x[i] = *reinterpret_cast<const uint4 *>(rows + min(r0 + i * STEP, n - 1) * row_bytes);
+                raw[i] = *reinterpret_cast<const uint4 *>(rows + min(r0 + i * STEP, n - 1) * row_bytes);
             int byte = 0, top = 0;
             bool ok = true, near = true;
             if (FP8) {
@@ -173,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) page_bounds_kernel(const BoundsParam
             uint32_t lo[P], hi[P];
 #pragma unroll
             for (int i = 0; i < ROWS; ++i) {
-                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
                 uint32_t v[P];
                 if (FP8) {
                     // the row's scale relative to the largest, 2^0 .. 2^-15, as an f16 pair
@@ -196,22 +195,45 @@ __global__ void __launch_bounds__(kThreads) page_bounds_kernel(const BoundsParam
                     hi[k] = i == 0 ? v[k] : max2<FP8>(hi[k], v[k]);
                 }
             }
-#pragma unroll
-            for (int off = SPAN; off < 32; off <<= 1)
+            // The rows' lanes meet and share the channels out: lanes 16 apart keep the upper
+            // bounds, or the lower ones with their signs turned (so that all are largest
+            // values); lanes 8 and 4 apart keep half of their channels each.
+            const bool up = STEP == 1 || (lane & 16);
+            const float f = FP8 ? scale_value((uint32_t)top) : 1.f;
+            constexpr int LEVELS = STEP == 8 ? 3 : STEP == 4 ? 2 : STEP == 2 ? 1 : 0;
+            constexpr int N = LEVELS == 0 ? V : V >> (LEVELS - 1);  // values a lane keeps
+            float x[N], y[LEVELS == 0 ? V : 1];  // y: the lower bounds of a row of 32 lanes
+            int at = 0;                          // the first one's channel, of the lane's V
+            if constexpr (LEVELS == 0) {
 #pragma unroll
                 for (int k = 0; k < P; ++k) {
-                    lo[k] = min2<FP8>(lo[k], __shfl_xor_sync(0xffffffffu, lo[k], off));
-                    hi[k] = max2<FP8>(hi[k], __shfl_xor_sync(0xffffffffu, hi[k], off));
+                    unpack2<FP8>(hi[k], f, x[2 * k], x[2 * k + 1]);
+                    unpack2<FP8>(lo[k] ^ 0x80008000u, f, y[2 * k], y[2 * k + 1]);
                 }
-            const float f = FP8 ? scale_value((uint32_t)top) : 1.f;
-            float a[V], b[V];
+            } else {
+                uint32_t v[P];
 #pragma unroll
-            for (int k = 0; k < P; ++k) {
-                unpack2<FP8>(lo[k], f, a[2 * k], a[2 * k + 1]);
-                unpack2<FP8>(hi[k], f, b[2 * k], b[2 * k + 1]);
+                for (int k = 0; k < P; ++k) {
+                    const uint32_t low = lo[k] ^ 0x80008000u;
+                    v[k] = max2<FP8>(up ? hi[k] : low,
+                                     __shfl_xor_sync(0xffffffffu, up ? low : hi[k], 16));
+                }
+#pragma unroll
+                for (int level = 1; level < LEVELS; ++level) {
+                    const int m = P >> level, off = 16 >> level;
+                    const bool second = lane & off;
+                    if (second) at += 2 * m;
+#pragma unroll
+                    for (int k = 0; k < m; ++k)
+                        v[k] = max2<FP8>(second ? v[k + m] : v[k],
+                                         __shfl_xor_sync(0xffffffffu, second ? v[k] : v[k + m], off));
+                }
+#pragma unroll
+                for (int k = 0; k < N / 2; ++k) unpack2<FP8>(v[k], f, x[2 * k], x[2 * k + 1]);
             }
             if constexpr (FP8) {
                 if (ok && !near) {  // rare
+                    float a[V], b[V];
                     fp32_bounds(rows, row_bytes, p.k_scale + unit * BS, n, r0, STEP, a, b);
                     for (int off = SPAN; off < 32; off <<= 1)
 #pragma unroll
@@ -219,36 +241,38 @@ __global__ void __launch_bounds__(kThreads) page_bounds_kernel(const BoundsParam
                             a[i] = fminf(a[i], __shfl_xor_sync(0xffffffffu, a[i], off));
                             b[i] = fmaxf(b[i], __shfl_xor_sync(0xffffffffu, b[i], off));
                         }
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+#pragma unroll
+                        for (int k = 0; k < N; ++k)
+                            if (i == at + k) x[k] = up ? b[i] : -a[i];
                 }
             }
             uint32_t amax = 0;  // (the bits of a NaN are above an infinity's)
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                amax = max(amax, max(__float_as_uint(fabsf(a[i])), __float_as_uint(fabsf(b[i]))));
+            for (int k = 0; k < N; ++k) amax = max(amax, __float_as_uint(fabsf(x[k])));
+            if (LEVELS == 0)
+#pragma unroll
+                for (int k = 0; k < N; ++k) amax = max(amax, __float_as_uint(fabsf(y[k])));
             amax = __reduce_max_sync(0xffffffffu, in ? amax : 0u);
             ok = ok && amax < 0x7f800000u;
             // amax = m * 2^x with 1 <= m < 2 and 127 = 1.984375 * 2^6: e = x - 6, one more
             // above 1.984375 (a carry out of the mantissa)
             const int e = max((int)((amax + 0x1ffffu) >> 23) - 127 - 6, -126);
             const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-            int8_t *out = p.bounds + unit * 2 * D + c * V;
-            // all rows' lanes have the bounds: the first store the lower, the next the upper
-            const bool split = STEP > 1;
-            if (in && r0 < 2) {
+            int8_t *out = p.bounds + unit * 2 * D + c * V + at;
+            auto store = [&](const float *z, bool upper) {
+                uint32_t w[(N + 3) / 4] = {};
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    if (split && u == 1) break;
-                    const bool up = split ? r0 == 1 : u == 1;
+                for (int k = 0; k < N; ++k)
+                    w[k / 4] |= code_of(z[k], inv, upper) << (8 * (k % 4));
 #pragma unroll
-                    for (int i = 0; i < V; i += 8) {
-                        uint32_t w[2] = {0u, 0u};
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            w[k / 4] |= code_of(up ? b[i + k] : a[i + k], inv, up) << (8 * (k % 4));
-                        *reinterpret_cast<uint2 *>(out + (up ? D : 0) + i) =
-                            ok ? make_uint2(w[0], w[1]) : make_uint2(0u, 0u);
-                    }
-                }
+                for (int k = 0; k < N / 4; ++k)
+                    reinterpret_cast<uint32_t *>(out + (upper ? D : 0))[k] = ok ? w[k] : 0u;
+            };
+            if (in) {
+                store(x, up);
+                if (LEVELS == 0) store(y, false);
             }
             if (lane == 0) p.bounds_scale[unit] = ok ? (uint8_t)(e + 127) : (uint8_t)kScaleNaN;
         }
@@ -278,7 +302,7 @@ cudaError_t launch_page_bounds(const BoundsParams &p0, cudaStream_t stream) {
         p.tokens_per_warp *= 2;
     const int64_t windows = (p.num_tokens + p.tokens_per_warp - 1) / p.tokens_per_warp;
     while (p.heads_per_warp < p.num_kv_heads &&
-           windows * (p.num_kv_heads / p.heads_per_warp) > 2 * warps)
+           windows * (p.num_kv_heads / p.heads_per_warp) > kRounds * warps)
         p.heads_per_warp *= 2;
     const int groups = (p.num_kv_heads + p.heads_per_warp - 1) / p.heads_per_warp;
     const unsigned grid = (unsigned)((windows * groups + kWarps - 1) / kWarps);
