@@ -713,7 +713,8 @@ PKV_API pkv_status pkv_select_pages(int32_t *pages, int top_k, const void *q,
  * paged_sparse_attention: row t attends, for each kv head g, to the keys of the pages
  * pages[t, g, :] of its request up to and with its own position; softmax, sink and
  * lse as in pkv_paged_decode.
- *   out, q        [total_q, num_qo_heads, head_dim] bf16, contiguous
+ *   out, q        [total_q, num_qo_heads, head_dim] bf16, contiguous; they must not
+ *                 overlap
  *   pages         [total_q, num_kv_heads, top_k] int32, as select_pages writes it
  *                 or from any other choice: page numbers of the row's request,
  *                 strictly ascending.  The list ends at its first negative entry, and

@@ -1386,14 +1386,15 @@ def select_pages(q, page_bounds, bounds_scale, block_table, cache_seqlens, max_s
                             ("num_recent", num_recent)):
             _int32(name, value)
         _require(top_k > 0, "top_k must be positive")
-    shape = (total_q, hkv, top_k)
     if pages is not None:
-        _arg_shape("pages", pages, ty.i32, shape, dev)
+        _arg_shape("pages", pages, ty.i32, (total_q, hkv, top_k), dev)
     err = _error_word(dev_error, dev)
     lib = load_library()
 
     def call(handle):
-        out = ty.torch.empty(shape, dtype=ty.i32, device=q.device) if pages is None else pages
+        out = pages
+        if out is None:
+            out = ty.torch.empty(total_q, hkv, top_k, dtype=ty.i32, device=q.device)
         return out, lib.pkv_select_pages(
             out.data_ptr(), top_k, q.data_ptr(), page_bounds.data_ptr(), bounds_scale.data_ptr(),
             nb, block_size, hkv, d, block_table.data_ptr(), max_blocks, cache_seqlens.data_ptr(),
@@ -1415,7 +1416,7 @@ def paged_sparse_attention(q, k_cache, v_cache, block_table, cache_seqlens, page
     page numbers of the request, -1 behind them (of select_pages, or any other choice).
     A query sees the keys of these pages up to its own position.  Pools are bf16, or the
     8-bit cache when k_scale and v_scale are given; sink, lse ([total_q, Hq] float32) and
-    layout as paged_decode."""
+    layout as paged_decode; out must not overlap q."""
     ty = _types()
     dev = _cuda_index("q", q)
     if k_scale is None and v_scale is None:
@@ -1431,6 +1432,8 @@ def paged_sparse_attention(q, k_cache, v_cache, block_table, cache_seqlens, page
         _arg("pages", pages, ty.i32, 3, dev)
         _arg_shape("pages", pages, ty.i32, (total_q, desc.num_kv_heads, top_k), dev)
     _attention_extras(sink, None, out, lse, q, total_q, Hq, dev)
+    if out is not None:
+        _disjoint((("q", q), ("out", out)))
     err = _error_word(dev_error, dev)
     scale = float(sm_scale) if sm_scale is not None else desc.head_dim ** -0.5
     lib = load_library()

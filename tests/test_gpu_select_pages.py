@@ -95,6 +95,16 @@ def test_tiles_of_queries(hq, hkv, d, bs):
     check(c, 1, first=0)
 
 
+@pytest.mark.parametrize("batch", [256, 257])
+def test_chunks_of_many_requests(batch):
+    """Tiles request by request, and beyond that count every so many rows."""
+    g = torch.Generator().manual_seed(batch)
+    lens = torch.randint(0, 400, (batch,), generator=g).tolist()
+    queries = [min(n, 5) if i % 9 else 0 for i, n in enumerate(lens)]
+    queries[7] = lens[7] = 300
+    check(make(lens, queries, 4, 2, 64, 16), 6, chunk=True, extra=3)
+
+
 @pytest.mark.parametrize("n", [3000, 70000, 300000])
 def test_tiles_over_long_contexts(n):
     """Clusters share a tile's pages; one query at a time where the scores do not fit."""

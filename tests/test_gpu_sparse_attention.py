@@ -122,6 +122,32 @@ def test_tiles_of_queries(hq, hkv, d, bs, kind):
         sink=True, extra=3, layout="HND")
 
 
+@pytest.mark.parametrize("batch", [256, 257])
+def test_chunks_of_many_requests(batch):
+    """Tiles request by request, and beyond that count every so many rows."""
+    g = torch.Generator().manual_seed(batch)
+    lens = torch.randint(0, 60, (batch,), generator=g).tolist()
+    queries = [min(n, 5) if i % 9 else 0 for i, n in enumerate(lens)]
+    queries[7] = lens[7] = 200
+    run(lens, queries, 4, 2, 64, top_k=3, chunk=True, extra=3)
+
+
+def test_offsets_that_are_none():
+    """Offsets that decrease or leave the rows: nothing outside is read or written."""
+    pools, table, slots, _ = small()
+    kc, vc, _, _ = pools.device(DEV)
+    q = torch.randn(8, 2, 64, generator=torch.Generator().manual_seed(1)).to(BF16).to(DEV)
+    pages = torch.arange(4, dtype=I32, device=DEV).expand(8, 1, 4).contiguous()
+    two = torch.cat([table, table]).to(DEV)
+    lens = torch.tensor([100, 100], dtype=I32, device=DEV)
+    for cu in ([2, 1, 8], [0, 19, 3], [3, 3, 3], [-5, 0, 90], [8, 2, 0], [0, 4, 8]):
+        out = torch.full((8, 2, 64), 7.0, dtype=BF16, device=DEV)
+        pkv.paged_sparse_attention(q, kc, vc, two, lens, pages, out=out,
+                                   cu_seq_lens_q=torch.tensor(cu, dtype=I32, device=DEV))
+        assert bool(torch.isfinite(out.float()).all())
+    assert not bool((out == 7.0).any())
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
 def test_chunk_scales(scale):
     run([300, 33], [9, 7], 4, 2, 64, top_k=9, scale=scale, sink=True)

@@ -229,6 +229,13 @@ def test_tables_that_overlap(lib, a, b):
     assert not lib.calls
 
 
+def test_out_over_q(lib):
+    args = _sparse_args()
+    with pytest.raises(ValueError, match="overlap"):
+        pkv.paged_sparse_attention(**args, out=args["q"])
+    assert not lib.calls
+
+
 @pytest.mark.parametrize("call", ALL)
 def test_cpu_tensors_are_refused(call):
     f, make = CALLS[call]
