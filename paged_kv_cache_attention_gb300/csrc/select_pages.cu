@@ -75,8 +75,8 @@ __device__ __forceinline__ float pow2(int e) {  // -126 <= e <= 127
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// x * 2^e, rounded once: 0 or 2^-126 <= |x|, -252 <= e <= 254.  The first product is
-// exact, or overflows as the whole does, or is so small that the whole is 0.
+// x * 2^e, rounded once: x whole, -252 <= e <= 254.  The first product is exact, or
+// overflows as the whole does, or is so small that the whole is 0.
 __device__ __forceinline__ float scaled(float x, int e) {
     const int last = min(max(e, -126), 127);
     return x * pow2(e - last) * pow2(last);
@@ -117,7 +117,7 @@ template <int NCH, int NT, int GP, int W>
 __global__ void __launch_bounds__(W * 32) select_pages_kernel(const SelectParams p) {
     using S = Shape<NCH, NT, GP, W>;
     // sums that do not wait for one another
-    constexpr int NA = S::OFFSET || NT == 1 ? 4 : NT <= 4 ? 2 : 1;
+    constexpr int NA = S::OFFSET || NT == 1 ? 4 : NT == 2 ? 2 : 1;
     constexpr int kWarps = S::WARPS, kThreads = kWarps * 32;
     constexpr int QT = S::QT, NST = S::NST, GS = S::GROUP * 32, BPT = 256 / GS;
     extern __shared__ uint4 s_dyn[];
@@ -276,37 +276,25 @@ __global__ void __launch_bounds__(W * 32) select_pages_kernel(const SelectParams
             }
         }
         __syncthreads();
-        // The factors of a query's heads are exact relative to the largest, but for
-        // exponents further apart than a float's (then each score is scaled by itself).
-        // Of this lane's columns: exponents, factors, their query's largest exponent.
-        int ex[NT][2], top_e[NT][GP == 1 ? 2 : 1];
-        float fac[NT][2];
-        bool apart = false;
+        // Of this lane's columns: exponents, as factors, and -inf for those that have no say;
+        // the first of their query's recent pages.  With exponents within +-60 (and scale
+        // bytes near 127) all products are exact, and a score is one of a few; else each
+        // score is scaled by itself.
+        int ex[NT][2], recent[NT][GP == 1 ? 2 : 1];
+        float fac[NT][2], bias[NT][2];
+        bool plain = true;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int col = nt * 8 + 2 * tq + i, c0 = col / GP * GP;
-                int top = kNoVote, low = 100000;
-#pragma unroll 1
-                for (int h = 0; h < GP; ++h) {
-                    const int e = s_exp[c0 + h];
-                    if (e != kNoVote) {
-                        top = max(top, e);
-                        low = min(low, e);
-                    }
-                }
-                ex[nt][i] = s_exp[col];
-                top_e[nt][GP == 1 ? i : 0] = top;
-                apart = apart || (top != kNoVote && top - low > 126);
-                fac[nt][i] = ex[nt][i] == kNoVote
-                                 ? 0.f
-                                 : __uint_as_float((uint32_t)(127 + max(ex[nt][i] - top, -126)) << 23);
+                const int col = nt * 8 + 2 * tq + i;
+                const int e = ex[nt][i] = s_exp[col];
+                recent[nt][GP == 1 ? i : 0] = pages_of(col / GP) - p.num_recent;
+                plain = plain && (e == kNoVote || (e >= -60 && e <= 60));
+                fac[nt][i] = e == kNoVote ? 0.f : pow2(max(min(e, 60), -60));
+                bias[nt][i] = e == kNoVote ? -INFINITY : 0.f;
             }
-        apart = __any_sync(0xffffffffu, apart);
-        if (apart)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) fac[nt][0] = fac[nt][1] = 1.f;
+        plain = __all_sync(0xffffffffu, plain);
         uint4 qf[NT == 1 ? NCH : 1][2];  // a single tile's columns stay in registers
         if (NT == 1)
 #pragma unroll
@@ -375,35 +363,43 @@ __global__ void __launch_bounds__(W * 32) select_pages_kernel(const SelectParams
                                               ? part[nt][i][e] - off[S::OFFSET ? nt : 0][e & 1][i]
                                               : part[nt][i][e];
                     }
-                // The best of a query's heads: of this lane's columns, then of the lanes that
-                // hold the query's other columns.
+                // Scores: of this lane's columns, then the best of the lanes that hold the
+                // query's other columns.
                 const int i0 = (warp + k * kWarps) * 16 + gq;
-                auto vote = [&](int nt, int j, int c) {
-                    const float x = acc[nt][2 * j + c] * fac[nt][c];
-                    return ex[nt][c] == kNoVote ? -INFINITY : x;
-                };
-                auto best = [&](int nt, int j) { return fmaxf(vote(nt, j, 0), vote(nt, j, 1)); };
-                auto store = [&](int query, float m, int top, int i, int byte, bool here) {
-                    if (!apart && top != kNoVote) m = scaled(m, top + byte - 127);
-                    if (byte == (int)kScaleNaN) m = INFINITY;
-                    uint32_t key = byte >= 0 ? sortable(m + 0.f) : 0u;
-                    const int page = base + i;
-                    if (page < p.num_first || page >= pages_of(query) - p.num_recent) key = kForced;
-                    if (here && i < nl && query < nq) s_key[query * p.cap + i] = key;
-                };
                 const int *bytes = scale + (k % NST) * 16 + gq;
-                if (apart) {  // rare: every score by itself, scaled before the heads are compared
+                const int byte2[2] = {bytes[0], bytes[8]};
+                const bool near = plain && (uint32_t)(byte2[0] - 67) <= 103u &&
+                                  (uint32_t)(byte2[1] - 67) <= 103u;
+                const bool fast = __all_sync(0xffffffffu, near);
+                if (fast) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (ex[nt][e & 1] != kNoVote)
-                                acc[nt][e] = scaled(acc[nt][e],
-                                                    ex[nt][e & 1] + bytes[8 * (e >> 1)] - 127);
+                            acc[nt][e] = fmaf(acc[nt][e], fac[nt][e & 1], bias[nt][e & 1]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            acc[nt][e] = ex[nt][e & 1] == kNoVote
+                                             ? -INFINITY
+                                             : scaled(acc[nt][e], ex[nt][e & 1] + byte2[e >> 1] - 127);
                 }
+                auto store = [&](int query, float m, int i, int byte, int first_recent, bool here) {
+                    if (fast)
+                        m *= pow2(byte - 127);
+                    else if (byte == (int)kScaleNaN)
+                        m = INFINITY;
+                    uint32_t key = byte >= 0 ? sortable(m + 0.f) : 0u;
+                    const int page = base + i;
+                    if (page < p.num_first || page >= first_recent) key = kForced;
+                    if (here && i < nl && query < nq) s_key[query * p.cap + i] = key;
+                };
+                auto best = [&](int nt, int j) { return fmaxf(acc[nt][2 * j], acc[nt][2 * j + 1]); };
                 if constexpr (GP >= 4) {
                     // a query's lanes have its score for both rows: even ones store the first
-                    const int j = tq & 1, i = i0 + 8 * j, byte = bytes[8 * j];
+                    const int j = tq & 1, i = i0 + 8 * j, byte = j ? byte2[1] : byte2[0];
 #pragma unroll
                     for (int nt = 0; nt < NT; nt += GP == 16 ? 2 : 1) {
                         float m[2];
@@ -414,21 +410,21 @@ __global__ void __launch_bounds__(W * 32) select_pages_kernel(const SelectParams
                             m[r] = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], 1));
                             if (GP >= 8) m[r] = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], 2));
                         }
-                        store((nt * 8 + 2 * tq) / GP, j ? m[1] : m[0], top_e[nt][0], i, byte,
+                        store((nt * 8 + 2 * tq) / GP, j ? m[1] : m[0], i, byte, recent[nt][0],
                               GP == 4 || tq < 2);
                     }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const int i = i0 + 8 * j, byte = bytes[8 * j];
+                        const int i = i0 + 8 * j, byte = byte2[j];
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             if (GP == 2) {
-                                store(nt * 4 + tq, best(nt, j), top_e[nt][0], i, byte, true);
+                                store(nt * 4 + tq, best(nt, j), i, byte, recent[nt][0], true);
                             } else {
-                                store(nt * 8 + 2 * tq, vote(nt, j, 0), top_e[nt][0], i, byte, true);
-                                store(nt * 8 + 2 * tq + 1, vote(nt, j, 1), top_e[nt][GP == 1], i,
-                                      byte, true);
+                                store(nt * 8 + 2 * tq, acc[nt][2 * j], i, byte, recent[nt][0], true);
+                                store(nt * 8 + 2 * tq + 1, acc[nt][2 * j + 1], i, byte,
+                                      recent[nt][GP == 1], true);
                             }
                         }
                     }
@@ -604,7 +600,7 @@ __global__ void __launch_bounds__(W * 32) select_pages_kernel(const SelectParams
                                   ((key[2] ^ prefix) >> digit) == 0 ||
                                   ((key[3] ^ prefix) >> digit) == 0;
                 if (some)
-#pragma unroll 1
+#pragma unroll
                 for (int b = 0; b < 4; ++b)
                     if (i + b < nlr && key[b] != kForced && ((key[b] ^ prefix) >> digit) == 0) {
                         const int at = atomicAdd(&s_left[mq], 1);
