@@ -259,20 +259,23 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
                 const int k = done + j, m = min(PP, n - j * PP);
                 const int next = lane < min(PP, n - (j + 1) * PP) ? bt[s_page[(j + 1) * PP + lane]] : 0;
                 const int cy = p.hnd ? 0 : g, cz = p.hnd ? id * Hkv + g : id * BS;
-                const uint32_t dst = base + lane * BS * 128;
                 bool ok = true;
 #pragma unroll 1
                 for (int v = 0; v < 2 && ok; ++v) {  // K, then V
                     if (k > 0) ok = __all_sync(0xffffffffu, wait(v ? kVEmpty : kKEmpty, (k - 1) & 1));
                     if (!ok) break;
                     const uint32_t full = bar(v ? kVFull : kKFull);
-                    if (lane == 0) mbar_arrive_expect_tx(full, m * BS * 256);
-                    __syncwarp();
-                    if (lane < m)
+                    const bool one = elect_one();
+                    if (one) mbar_arrive_expect_tx(full, m * BS * 256);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            tma_load_3d(dst + (v ? kOffV : kOffK) + h * kHalf, v ? &tmv : &tmk, full,
-                                        h * 64, cy, cz);
+                    for (int i = 0; i < PP; ++i) {
+                        const int z = __shfl_sync(0xffffffffu, cz, i);
+                        if (i < m && one)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                tma_load_3d(base + (v ? kOffV : kOffK) + h * kHalf + i * BS * 128,
+                                            v ? &tmv : &tmk, full, h * 64, cy, z);
+                    }
                 }
                 if (!ok) break;
                 id = next;
