@@ -25,7 +25,7 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kCluster = 8;
 constexpr int kRowsHere = 16384;
 constexpr int kRowThreads = 256;
@@ -93,6 +93,11 @@ __device__ __forceinline__ Sums shift_up(const Sums &a, int d) {
             __shfl_up_sync(0xffffffffu, a.taken, d), __shfl_up_sync(0xffffffffu, a.gone, d)};
 }
 
+__device__ __forceinline__ Sums of_lane(const Sums &a, int l) {
+    return {__shfl_sync(0xffffffffu, a.tok, l), __shfl_sync(0xffffffffu, a.keys, l),
+            __shfl_sync(0xffffffffu, a.taken, l), __shfl_sync(0xffffffffu, a.gone, l)};
+}
+
 __global__ void __launch_bounds__(kThreads) block_tables_kernel(const TableParams p) {
     extern __shared__ int32_t s_cu[];  // [3][batch + 1]: rows, taken and released before r
     int32_t *s_tok = s_cu, *s_take = s_tok + p.batch + 1, *s_gone = s_take + p.batch + 1;
@@ -131,14 +136,16 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(const TableParam
         }
         if (lane == 31) s_warp[warp] = in;
         __syncthreads();
-        Sums before = run;
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-            const Sums o = s_warp[w];
-            if (w < warp) before = add(before, o);
-            run = add(run, o);
+        static_assert(kThreads == 32 * 32, "a lane for each warp");
+        const int used = min((B - r0 + 31) / 32, 32);  // warps that have a request
+        Sums warps = s_warp[lane];  // up to and with warp `lane`
+        for (int d = 1; d < used; d <<= 1) {
+            const Sums o = shift_up(warps, d);
+            if (lane >= d) warps = add(warps, o);
         }
-        before = add(before, in);  // up to and with r
+        Sums before = add(run, in);  // up to and with r
+        if (warp > 0) before = add(before, of_lane(warps, warp - 1));
+        run = add(run, of_lane(warps, used - 1));
         if (r < B) {
             s_tok[r + 1] = (int)before.tok;
             s_take[r + 1] = (int)before.taken;
