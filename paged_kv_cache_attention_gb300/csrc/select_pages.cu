@@ -108,13 +108,18 @@ struct Shape {
     // quarter of the channels each stay below 2^24 (32 channels * 255 * 1279).
     static constexpr bool OFFSET = NT <= 2 && NCH <= 4;
     static constexpr int STAGE = NCH * 1024;
-    static constexpr int Q_OFF = WARPS * NST * STAGE;   // columns: [NT][NCH][2][32 lanes]
+    // Histograms, [2][QT][256]: of several queries in place of the ring, once the scores
+    // are there; of one behind it, so that they are cleared beside the first loads.
+    static constexpr int RING = WARPS * NST * STAGE;
+    static constexpr int HIST = QT * 2048, HIST_OFF = QT > 1 ? 0 : RING;
+    static constexpr int Q_OFF = RING > HIST_OFF + HIST ? RING : HIST_OFF + HIST;  // columns: [NT][NCH][2][32 lanes]
     static constexpr int KEY_OFF = Q_OFF + NT * NCH * 1024;  // scores: [QT][cap]
     static constexpr int GROUP = WARPS / QT;            // warps that select for a query
 };
 
 template <int NCH, int NT, int GP, int W>
-__global__ void __launch_bounds__(W * 32) select_pages_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(W * 32, 16 / W)
+select_pages_kernel(const SelectParams p) {
     using S = Shape<NCH, NT, GP, W>;
     // sums that do not wait for one another
     constexpr int NA = S::OFFSET || NT == 1 ? 4 : NT == 2 ? 2 : 1;
@@ -123,9 +128,9 @@ __global__ void __launch_bounds__(W * 32) select_pages_kernel(const SelectParams
     extern __shared__ uint4 s_dyn[];
     uint4 *s_q = s_dyn + S::Q_OFF / 16;
     uint32_t *s_key = reinterpret_cast<uint32_t *>(s_dyn + S::KEY_OFF / 16);
+    auto s_hist = reinterpret_cast<uint32_t (*)[QT][256]>(s_dyn + S::HIST_OFF / 16);
     __shared__ int s_exp[NT * 8];
     __shared__ alignas(16) int s_sum[NT * 8][4];             // OFFSET: a column's sums over d / 4 % 4
-    __shared__ alignas(16) uint32_t s_hist[2][QT][256];
     __shared__ uint32_t s_pick[QT][3];           // digit, pages above it, pages with it
     __shared__ int s_scale[S::WARPS][S::NST][16];  // scale bytes of the tiles in flight
     __shared__ uint32_t s_range[S::WARPS][2];    // least and largest score
@@ -174,9 +179,10 @@ __global__ void __launch_bounds__(W * 32) select_pages_kernel(const SelectParams
 
         // the queries as column fragments
         if (QT > 1) __syncthreads();  // (the tile's rows before are done)
+        if (QT == 1)
 #pragma unroll 1
-        for (int i = threadIdx.x; i < 2 * QT * 64; i += kThreads)
-            reinterpret_cast<uint4 *>(&s_hist[0][0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
+            for (int i = threadIdx.x; i < 128; i += kThreads)
+                reinterpret_cast<uint4 *>(&s_hist[0][0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
         const int32_t *bt = p.r.block_table + (int64_t)r * p.r.max_blocks_per_seq + base;
         for (int i = threadIdx.x; i < nl; i += kThreads) s_key[i] = (uint32_t)__ldg(bt + i);
         if (threadIdx.x < QT) s_left[threadIdx.x] = 0;
@@ -456,6 +462,12 @@ __global__ void __launch_bounds__(W * 32) select_pages_kernel(const SelectParams
             else
                 group_sync();
         };
+        if (QT > 1) {
+#pragma unroll
+            for (int i = li; i < 128; i += GS)
+                *reinterpret_cast<uint4 *>(&s_hist[i >> 6][mq][(i & 63) * 4]) = make_uint4(0u, 0u, 0u, 0u);
+            group_sync();
+        }
         uint32_t prefix = 0;  // of the scores that are left: the bits from `digit` up
         int need = p.top_k, left = 0, digit = 32, pass = 0;
         if (!fixed) {
@@ -738,7 +750,8 @@ int smem_bytes(int cap) {
     return S::KEY_OFF + S::QT * cap * 4;
 }
 
-constexpr int kMaxSmem = 208 * 1024;  // beside at most 17 KB of the kernel's own
+constexpr int kMaxSmem = 224 * 1024;  // beside at most 3 KB of the kernel's own
+constexpr int kHalfSmem = 111 * 1024;  // the same of two CTAs per SM
 
 template <int NCH, int NT, int GP, int W>
 cudaError_t launch_as(SelectParams p, bool &fits, cudaStream_t stream) {
@@ -764,6 +777,14 @@ cudaError_t launch_as(SelectParams p, bool &fits, cudaStream_t stream) {
     return launch_cluster(kern, (unsigned)(units * c), c, S::WARPS * 32, (size_t)smem, stream, p);
 }
 
+template <int NCH, int NT, int GP>
+cudaError_t launch_tiles(const SelectParams &p, bool &fits, cudaStream_t stream) {
+    const int n = (p.r.max_seqlen + p.block_size - 1) >> p.bs_shift;
+    if (smem_bytes<Shape<NCH, NT, GP, 8>>((n + 15) / 16 * 16) <= kHalfSmem)
+        return launch_as<NCH, NT, GP, 8>(p, fits, stream);
+    return launch_as<NCH, NT, GP, 16>(p, fits, stream);
+}
+
 template <int NCH>
 cudaError_t launch_n(const SelectParams &p, cudaStream_t stream) {
     bool fits = false;
@@ -771,11 +792,11 @@ cudaError_t launch_n(const SelectParams &p, cudaStream_t stream) {
     // Tiles of queries where requests have several (4 on average); long contexts whose
     // scores do not fit go on with one query at a time.
     if (p.r.cu_q && p.r.rows >= 4LL * p.r.batch) {
-        const cudaError_t e = G == 1   ? launch_as<NCH, 1, 1, 16>(p, fits, stream)
-                              : G == 2 ? launch_as<NCH, 2, 2, 16>(p, fits, stream)
-                              : G <= 4 ? launch_as<NCH, 4, 4, 16>(p, fits, stream)
-                              : G <= 8 ? launch_as<NCH, 8, 8, 16>(p, fits, stream)
-                                       : launch_as<NCH, 8, 16, 16>(p, fits, stream);
+        const cudaError_t e = G == 1   ? launch_tiles<NCH, 1, 1>(p, fits, stream)
+                              : G == 2 ? launch_tiles<NCH, 2, 2>(p, fits, stream)
+                              : G <= 4 ? launch_tiles<NCH, 4, 4>(p, fits, stream)
+                              : G <= 8 ? launch_tiles<NCH, 8, 8>(p, fits, stream)
+                                       : launch_tiles<NCH, 8, 16>(p, fits, stream);
         if (fits) return e;
     }
     // Small CTAs, of which all queries of a decode step have theirs at once; larger ones
