@@ -400,7 +400,7 @@ select_pages_kernel(const SelectParams p) {
                     uint32_t key = byte >= 0 ? sortable(m + 0.f) : 0u;
                     const int page = base + i;
                     if (page < p.num_first || page >= first_recent) key = kForced;
-                    if (here && i < nl && query < nq) s_key[query * p.cap + i] = key;
+                    if (here) s_key[query * p.cap + i] = key;
                 };
                 auto best = [&](int nt, int j) { return fmaxf(acc[nt][2 * j], acc[nt][2 * j + 1]); };
                 if constexpr (GP >= 4) {
@@ -447,7 +447,8 @@ select_pages_kernel(const SelectParams p) {
         const int mq = warp / S::GROUP, li = threadIdx.x - mq * GS;
         const int nrow = mq < nq ? pages_of(mq) : 0;
         const bool choose = nrow > p.top_k;
-        const int nlr = choose ? min(max(nrow - base, 0), per) : 0;
+        // Whole tiles are looked through: what lies behind a row counts as forced.
+        const int scan = choose ? tiles * 16 : 0;
         const uint32_t *key_row = s_key + mq * p.cap;
         const bool fixed = QT > 1 && C > 1;
         auto group_sync = [&] {
@@ -469,23 +470,23 @@ select_pages_kernel(const SelectParams p) {
             group_sync();
         }
         uint32_t prefix = 0;  // of the scores that are left: the bits from `digit` up
-        int need = p.top_k, left = 0, digit = 32, pass = 0;
+        int need = p.top_k + (n + 15) / 16 * 16 - nrow, left = 0, digit = 32, pass = 0;
         if (!fixed) {
-            need -= p.num_first + p.num_recent;  // forced ones are above all others
+            need = p.top_k - p.num_first - p.num_recent;  // forced ones are above all others
             uint32_t lo = 0xffffffffu, hi = 0;
 #pragma unroll 1
-            for (int i = li * 4; i < nlr; i += GS * 4) {
+            for (int i = li * 4; i < scan; i += GS * 4) {
                 const uint4 k4 = *reinterpret_cast<const uint4 *>(key_row + i);
                 const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    if (i + b < nlr && key[b] != kForced) {
-                        lo = min(lo, key[b]);
-                        hi = max(hi, key[b]);
-                    }
+                for (int b = 0; b < 4; ++b) {
+                    lo = min(lo, key[b]);
+                    hi = max(hi, key[b] + 1u);  // (0 for forced ones)
+                }
             }
             lo = __reduce_min_sync(0xffffffffu, lo);
             hi = __reduce_max_sync(0xffffffffu, hi);
+            if (hi > 0) --hi;
             if (S::GROUP > 1) {
                 if (lane == 0) {
                     s_range[warp][0] = lo;
@@ -516,23 +517,27 @@ select_pages_kernel(const SelectParams p) {
             digit = lo < hi ? 32 - __clz(lo ^ hi) : 0;
             prefix = digit == 32 ? 0u : lo >> digit << digit;
         }
+        // Of what is left: all keys less than this far above prefix (not forced ones, unless
+        // all 32 bits are taken).
+        auto limit_of = [&] {
+            const uint32_t all = digit == 32 ? 0xffffffffu : (1u << digit) - 1u;
+            return fixed ? all : min(all, kForced - 1 - prefix);
+        };
         bool ranked = false;
         while (choose || fixed) {
             if (digit == 0) break;
             const int next = fixed ? digit - 8 : max(digit - 8, 0);
-            const uint32_t mask = (1u << (digit - next)) - 1u;
+            const uint32_t limit = limit_of();
             uint32_t *hist = s_hist[pass & 1][mq], *other = s_hist[(pass + 1) & 1][mq];
             const uint32_t bins = smem_u32(hist);
 #pragma unroll 1
-            for (int i = li * 4; i < nlr; i += GS * 4) {
+            for (int i = li * 4; i < scan; i += GS * 4) {
                 const uint4 k4 = *reinterpret_cast<const uint4 *>(key_row + i);
                 const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                    // (64-bit: a shift by 32 leaves nothing)
-                    const bool in = (uint32_t)((uint64_t)(key[b] ^ prefix) >> digit) == 0;
-                    count_if(bins + ((key[b] >> next) & mask) * 4,
-                             i + b < nlr && in && (fixed || key[b] != kForced));
+                    const uint32_t d = key[b] - prefix;
+                    count_if(bins + (d >> next) * 4, d <= limit);
                 }
             }
             sync();
@@ -601,20 +606,17 @@ select_pages_kernel(const SelectParams p) {
         if (ranked) {
             // the scores left, with their pages: [kRank] keys, then [kRank] pages
             uint32_t *list = s_hist[pass & 1][mq], *all = list;  // (all zeros, read by no one)
+            const uint32_t limit = limit_of();
 #pragma unroll 1
-            for (int i = li * 4; i < nlr; i += GS * 4) {
+            for (int i = li * 4; i < scan; i += GS * 4) {
                 const uint4 k4 = *reinterpret_cast<const uint4 *>(key_row + i);
                 const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
-                // (kForced has other leading bits than the scores that are left, or they
-                // have all bits in common and are not ranked)
-                const bool some = ((key[0] ^ prefix) >> digit) == 0 ||
-                                  ((key[1] ^ prefix) >> digit) == 0 ||
-                                  ((key[2] ^ prefix) >> digit) == 0 ||
-                                  ((key[3] ^ prefix) >> digit) == 0;
+                const bool some = key[0] - prefix <= limit || key[1] - prefix <= limit ||
+                                  key[2] - prefix <= limit || key[3] - prefix <= limit;
                 if (some)
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
-                    if (i + b < nlr && key[b] != kForced && ((key[b] ^ prefix) >> digit) == 0) {
+                    if (key[b] - prefix <= limit) {
                         const int at = atomicAdd(&s_left[mq], 1);
                         list[at] = key[b];
                         list[kRank + at] = (uint32_t)(base + i + b);
@@ -662,7 +664,8 @@ select_pages_kernel(const SelectParams p) {
         __syncthreads();  // s_cnt is used again
 
         // pages above it, and the first `need` of those equal to it, in ascending order
-        // (each warp a run of pages, four consecutive ones a lane)
+        // (each warp a run of pages)
+        const int nlr = choose ? min(max(nrow - base, 0), per) : 0;
         const int seg = ((nlr + S::GROUP - 1) / S::GROUP + 127) / 128 * 128;
         const int lo = min((warp - mq * S::GROUP) * seg, nlr), hi = min(lo + seg, nlr);
         int above = 0, equal = 0;
@@ -704,42 +707,40 @@ select_pages_kernel(const SelectParams p) {
             n_above += s_cnt[w][0];
             n_equal += s_cnt[w][1];
         }
-        const uint32_t below = (1u << lane) - 1u;
         int32_t *out = out_of(mq);
 #pragma unroll 1
-        for (int i0 = lo; i0 < hi; i0 += 128) {
-            const int i = i0 + 4 * lane;
-            uint4 k4 = make_uint4(0u, 0u, 0u, 0u);
-            if (i < hi) k4 = *reinterpret_cast<const uint4 *>(key_row + i);
-            const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
-            bool up[4], same[4], some = false;
-            int before = 0, mine_up = 0, all_up = 0;
+        for (int i0 = lo; i0 < hi; i0 += 1024) {
+            uint32_t up = 0, same = 0;  // lane w: of the 32 pages from i0 + 32 w on
+#pragma unroll 1
+            for (int w0 = 0; w0 < 32 && i0 + w0 * 32 < hi; w0 += 4)
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                up[b] = i + b < hi && key[b] > prefix;
-                same[b] = i + b < hi && key[b] == prefix;
-                some = some || same[b];
-                const uint32_t m = __ballot_sync(0xffffffffu, up[b]);
-                before += __popc(m & below);
-                all_up += __popc(m);
-            }
-            int same_before = 0, all_same = 0, mine_same = 0;
-            if (__any_sync(0xffffffffu, some))
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const uint32_t m = __ballot_sync(0xffffffffu, same[b]);
-                    same_before += __popc(m & below);
-                    all_same += __popc(m);
+                for (int w = w0; w < w0 + 4; ++w) {
+                    const int i = i0 + w * 32 + lane;
+                    const uint32_t key = i < hi ? key_row[i] : 0u;
+                    const uint32_t u = __ballot_sync(0xffffffffu, i < hi && key > prefix);
+                    const uint32_t e = __ballot_sync(0xffffffffu, i < hi && key == prefix);
+                    if (lane == w) {
+                        up = u;
+                        same = e;
+                    }
                 }
+            int sum = __popc(up) + (__popc(same) << 16);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const int a = n_above + before + mine_up, e = n_equal + same_before + mine_same;
-                if (up[b] || (same[b] && e < need)) out[a + min(e, need)] = base + i + b;
-                mine_up += up[b];
-                mine_same += same[b];
+            for (int off = 1; off < 32; off <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, sum, off);
+                if (lane >= off) sum += o;
             }
-            n_above += all_up;
-            n_equal += all_same;
+            const int a = n_above + (sum & 0xffff) - __popc(up);
+            const int e = n_equal + (sum >> 16) - __popc(same);
+            const int room = max(need - e, 0);
+            while (__popc(same) > room) same ^= 0x80000000u >> __clz(same);
+            int32_t *o = out + a + min(e, need);
+#pragma unroll 1
+            for (uint32_t take = up | same; take; take &= take - 1)
+                *o++ = base + i0 + lane * 32 + __ffs(take) - 1;
+            sum = __shfl_sync(0xffffffffu, sum, 31);
+            n_above += sum & 0xffff;
+            n_equal += sum >> 16;
         }
         if (C > 1) cluster_sync();  // the others may still read this CTA's counts
     }
