@@ -103,17 +103,20 @@ template <int NCH, int NT, int GP, int W>
 struct Shape {
     static constexpr int QT = NT * 8 / GP;               // queries of a tile
     static constexpr int WARPS = W;
-    static constexpr int NST = QT == 1 ? 2 : 1;          // 16-page tiles in the ring per warp
+    // 16-page tiles of a step: two share what is read of the columns, where registers allow
+    static constexpr int PT = QT > 1 && NT <= 4 ? 2 : 1;
+    static constexpr int STEP = 16 * PT;                 // pages of a step
+    static constexpr int NST = 2;                        // steps in the ring per warp
     // Few columns: 1152 is taken off the sums, not off each code.  Four sums for a
     // quarter of the channels each stay below 2^24 (32 channels * 255 * 1279).
-    static constexpr bool OFFSET = NT <= 2 && NCH <= 4;
+    static constexpr bool OFFSET = QT == 1 && NCH <= 4;
     static constexpr int STAGE = NCH * 1024;
-    // Histograms, [2][QT][256]: of several queries in place of the ring, once the scores
-    // are there; of one behind it, so that they are cleared beside the first loads.
-    static constexpr int RING = WARPS * NST * STAGE;
-    static constexpr int HIST = QT * 2048, HIST_OFF = QT > 1 ? 0 : RING;
-    static constexpr int Q_OFF = RING > HIST_OFF + HIST ? RING : HIST_OFF + HIST;  // columns: [NT][NCH][2][32 lanes]
-    static constexpr int KEY_OFF = Q_OFF + NT * NCH * 1024;  // scores: [QT][cap]
+    // One query: the ring, histograms [2][256], columns [NT][NCH][2][32 lanes].  Several:
+    // columns, and in their place histograms [2][QT][256] once the scores are there.
+    static constexpr int HIST = QT * 2048, COLS = NT * NCH * 1024;
+    static constexpr int HIST_OFF = QT > 1 ? 0 : WARPS * NST * STAGE;
+    static constexpr int Q_OFF = QT > 1 ? 0 : HIST_OFF + HIST;
+    static constexpr int KEY_OFF = QT > 1 && HIST > COLS ? HIST : Q_OFF + COLS;  // scores: [QT][cap]
     static constexpr int GROUP = WARPS / QT;            // warps that select for a query
 };
 
@@ -122,17 +125,18 @@ __global__ void __launch_bounds__(W * 32, 16 / W)
 select_pages_kernel(const SelectParams p) {
     using S = Shape<NCH, NT, GP, W>;
     // sums that do not wait for one another
-    constexpr int NA = S::OFFSET || NT == 1 ? 4 : NT == 2 ? 2 : 1;
+    constexpr int NA = S::OFFSET ? 4 : NT * S::PT <= 2 ? 2 : 1;
     constexpr int kWarps = S::WARPS, kThreads = kWarps * 32;
-    constexpr int QT = S::QT, NST = S::NST, GS = S::GROUP * 32, BPT = 256 / GS;
+    constexpr int QT = S::QT, NST = S::NST, PT = S::PT, STEP = S::STEP, GS = S::GROUP * 32, BPT = 256 / GS;
     extern __shared__ uint4 s_dyn[];
     uint4 *s_q = s_dyn + S::Q_OFF / 16;
     uint32_t *s_key = reinterpret_cast<uint32_t *>(s_dyn + S::KEY_OFF / 16);
     auto s_hist = reinterpret_cast<uint32_t (*)[QT][256]>(s_dyn + S::HIST_OFF / 16);
     __shared__ int s_exp[NT * 8];
+    __shared__ alignas(16) float2 s_col[NT * 8];  // the exponent as a factor; -inf if no say
     __shared__ alignas(16) int s_sum[NT * 8][4];             // OFFSET: a column's sums over d / 4 % 4
     __shared__ uint32_t s_pick[QT][3];           // digit, pages above it, pages with it
-    __shared__ int s_scale[S::WARPS][S::NST][16];  // scale bytes of the tiles in flight
+    __shared__ int s_scale[QT == 1 ? W : 1][S::NST][16];  // scale bytes of the steps in flight
     __shared__ uint32_t s_range[S::WARPS][2];    // least and largest score
     __shared__ uint32_t s_both[2];               // the same of the CTA
     __shared__ int s_left[QT];                   // scores in the list to be ranked
@@ -174,7 +178,7 @@ select_pages_kernel(const SelectParams p) {
         }
         const int n = pages_of(nq - 1);
         if (n <= p.top_k) continue;
-        const int per = ((n + C - 1) / C + 15) / 16 * 16;
+        const int per = ((n + C - 1) / C + STEP - 1) / STEP * STEP;
         const int base = rank * per, nl = min(max(n - base, 0), per);
 
         // the queries as column fragments
@@ -191,48 +195,69 @@ select_pages_kernel(const SelectParams p) {
 #pragma unroll 1
         for (int i = threadIdx.x; i < NT * 8; i += kThreads) {
             s_exp[i] = kNoVote;
+            s_col[i] = make_float2(0.f, -INFINITY);
             *reinterpret_cast<int4 *>(s_sum[i]) = make_int4(0, 0, 0, 0);
         }
         __syncthreads();
-        const uint32_t ring = smem_u32(s_dyn) + warp * NST * S::STAGE + lane * 16;
-        const int tiles = (nl + 15) / 16, mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
-        // Tile k goes to slot k % NST of the ring.  A scale byte is loaded with its page's
-        // codes and put into shared memory a tile later (-1: no page).  The page ids wait in
-        // the first row of scores, where a tile's are read before its scores are written.
-        int *scale = &s_scale[warp][0][0];
-        int byte_ahead = -1;
-        auto issue = [&](int k) {
-            const int i = (warp + k * kWarps) * 16 + (lane & 15);
+        const int tiles = (nl + STEP - 1) / STEP;
+        const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
+        // Rows of the bounds in step k, for the tiles' pages gq and gq + 8, and the scale
+        // byte (-1: no page) of page `lane` of the step.  The page ids wait in the first
+        // row of scores, where a step's are read before its scores are written.
+        auto rows_of = [&](int k, uint32_t (&row)[2 * PT], int &byte) {
+            const int i = (warp + k * kWarps) * STEP + (PT == 2 ? lane : lane & 15);
             const int id = i < nl ? (int)s_key[i] : -1;
             const bool live = id >= 0 && id < p.r.num_blocks;
             const uint32_t at = (uint32_t)(live ? id : 0) * p.r.num_kv_heads + g;  // < 2^31
-            byte_ahead = live ? (int)p.bounds_scale[at] : -1;
+            byte = live ? (int)p.bounds_scale[at] : -1;
             if (!live && i < nl) flag_error(p.r.dev_error, PKV_DEVERR_BLOCK_ID);
-            const uint32_t dst = ring + (k % NST) * S::STAGE;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint32_t row = __shfl_sync(0xffffffffu, at, gq + 8 * j);
-                const int8_t *src = p.bounds + (uint64_t)row * (uint32_t)(2 * D) + tq * 16;
+            for (int j = 0; j < 2 * PT; ++j) row[j] = __shfl_sync(0xffffffffu, at, gq + 8 * j);
+        };
+        auto source = [&](uint32_t row, int c) {  // this lane's 16 codes of piece c
+            return p.bounds + (uint64_t)row * (uint32_t)(2 * D) + tq * 16 + c * 64;
+        };
+        // One query: step k goes to slot k % NST of a ring; its scale bytes follow a step
+        // later.
+        const uint32_t ring = smem_u32(s_dyn) + warp * NST * S::STAGE + lane * 16;
+        int *scale = &s_scale[QT == 1 ? warp : 0][0][0];
+        int byte_ahead = -1;
+        auto issue = [&](int k) {
+            const uint32_t dst = ring + (k % NST) * S::STAGE;
+            uint32_t row[2 * PT];
+            rows_of(k, row, byte_ahead);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int c = 0; c < NCH; ++c) {  // (pages out of the pool: scores not used)
                     if (c < NCH - 1)
-                        cp_async16(dst + (j * NCH + c) * 512, src + c * 64);
+                        cp_async16(dst + (j * NCH + c) * 512, source(row[j], c));
                     else
-                        cp_async16_or_zero(dst + (j * NCH + c) * 512, src + c * 64,
+                        cp_async16_or_zero(dst + (j * NCH + c) * 512, source(row[j], c),
                                            c * 64 + tq * 16 < 2 * D);
                 }
-            }
         };
         auto keep_byte = [&](int k) {
             if (lane < 16) scale[(k % NST) * 16 + lane] = byte_ahead;
         };
-#pragma unroll 1
-        for (int k = 0; k < NST - 1; ++k) {
-            if (k < mine) {
-                issue(k);
-                if (k < NST - 2) keep_byte(k);
+        // Several queries: into registers, a piece ahead.
+        auto load = [&](uint4 (&x)[2 * PT], const uint32_t (&row)[2 * PT], int c) {
+#pragma unroll
+            for (int j = 0; j < 2 * PT; ++j) {
+                x[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (c < NCH - 1 || c * 64 + tq * 16 < 2 * D)
+                    x[j] = __ldg(reinterpret_cast<const uint4 *>(source(row[j], c)));
             }
+        };
+        uint32_t row[2 * PT];
+        int byte = -1;
+        uint4 x[2 * PT];
+        if (QT == 1) {
+            if (mine > 0) issue(0);
             asm volatile("cp.async.commit_group;" ::: "memory");
+        } else if (mine > 0) {
+            rows_of(0, row, byte);
+            load(x, row, 0);
         }
         const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) +
                                  ((int64_t)first * p.r.num_kv_heads + g) * G * D;
@@ -253,7 +278,10 @@ select_pages_kernel(const SelectParams p) {
             amax = __reduce_max_sync(0xffffffffu, amax);
             if (amax >= 0x7f80u) continue;  // not finite
             const int e = max((int)(amax >> 7) - 127, -112) - 7;
-            if (lane == 0) s_exp[col] = e;
+            if (lane == 0) {
+                s_exp[col] = e;
+                s_col[col] = make_float2(pow2(max(min(e, 60), -60)), 0.f);
+            }
             const float f = __uint_as_float((uint32_t)(127 - e) << 23);
             // channel d is code d against the lower bounds and D + d against the upper:
             // code k: piece k / 64, lane (col % 8, k / 16 % 4), step k / 4 % 4, its value k % 4
@@ -282,29 +310,17 @@ select_pages_kernel(const SelectParams p) {
             }
         }
         __syncthreads();
-        // Of this lane's columns: exponents, as factors, and -inf for those that have no say;
-        // the first of their query's recent pages.  With exponents within +-60 (and scale
-        // bytes near 127) all products are exact, and a score is one of a few; else each
-        // score is scaled by itself.
-        int ex[NT][2], recent[NT][GP == 1 ? 2 : 1];
-        float fac[NT][2], bias[NT][2];
+        // With exponents within +-60 (and scale bytes near 127) all products are exact, and a
+        // score is one of a few; else each score is scaled by itself.
         bool plain = true;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int col = nt * 8 + 2 * tq + i;
-                const int e = ex[nt][i] = s_exp[col];
-                recent[nt][GP == 1 ? i : 0] = pages_of(col / GP) - p.num_recent;
-                plain = plain && (e == kNoVote || (e >= -60 && e <= 60));
-                fac[nt][i] = e == kNoVote ? 0.f : pow2(max(min(e, 60), -60));
-                bias[nt][i] = e == kNoVote ? -INFINITY : 0.f;
-            }
+        for (int i = lane; i < NT * 8; i += 32)
+            plain = plain && (s_exp[i] == kNoVote || (s_exp[i] >= -60 && s_exp[i] <= 60));
         plain = __all_sync(0xffffffffu, plain);
-        uint4 qf[NT == 1 ? NCH : 1][2];  // a single tile's columns stay in registers
-        if (NT == 1)
+        constexpr bool HELD = NT == 1 && NCH <= 4;
+        uint4 qf[HELD ? NCH : 1][2];  // a single tile's columns stay in registers
+        if (HELD)
 #pragma unroll
-            for (int c = 0; c < NCH; ++c)
+            for (int c = 0; c < (HELD ? NCH : 1); ++c)
 #pragma unroll
                 for (int s2 = 0; s2 < 2; ++s2) qf[c][s2] = s_q[(c * 2 + s2) * 32 + lane];
         float off[S::OFFSET ? NT : 1][2][4];  // 1152 times a column's sums, exact
@@ -315,48 +331,81 @@ select_pages_kernel(const SelectParams p) {
                 for (int i = 0; i < 8; ++i)
                     off[nt][i / 4][i % 4] = 1152.f * (float)s_sum[nt * 8 + 2 * tq + i / 4][i % 4];
 
-        // scores of 16 pages at a time, this warp's tiles every kWarps-th
-#pragma unroll 1
-        for (int k = 0; k < mine; ++k) {
-            if (NST > 1) keep_byte(k + NST - 2);
-            if (k + NST - 1 < mine) issue(k + NST - 1);
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");
-            if (NST == 1) keep_byte(k);
-            __syncwarp();
-            const uint32_t tile = ring + (k % NST) * S::STAGE;
-            {
-                // (whole numbers: partial sums in any order give the same)
-                float part[NT][NA][4];
+        // (whole numbers: partial sums in any order give the same)
+        float part[PT][NT][NA][4];
+        auto multiply = [&](int c, const uint4 (&x)[2 * PT]) {  // piece c of a step's pages
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+            for (int s2 = 0; s2 < 2; ++s2) {
+                uint32_t a[PT][2][4];
 #pragma unroll
-                    for (int e = 0; e < 4 * NA; ++e) part[nt][e / 4][e % 4] = 0.f;
-#pragma unroll
-                for (int c = 0; c < NCH; ++c) {
-                    const uint4 x0 = lds128(tile + c * 512);
-                    const uint4 x1 = lds128(tile + (NCH + c) * 512);
+                for (int u = 0; u < PT; ++u) {
+                    const uint4 x0 = x[2 * u], x1 = x[2 * u + 1];
                     const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w};
                     const uint32_t w1[4] = {x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
-                    for (int s2 = 0; s2 < 2; ++s2) {
-                        uint32_t a[2][4];
-#pragma unroll
-                        for (int s = 0; s < 2; ++s) {
-                            codes_to_f16<!S::OFFSET>(w0[2 * s2 + s], a[s][0], a[s][2]);
-                            codes_to_f16<!S::OFFSET>(w1[2 * s2 + s], a[s][1], a[s][3]);
-                        }
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const uint4 b = NT == 1 ? qf[c % (NT == 1 ? NCH : 1)][s2]
-                                                    : s_q[((nt * NCH + c) * 2 + s2) * 32 + lane];
-                            mma_f16_16816(part[nt][2 * s2 % NA], a[0][0], a[0][1], a[0][2],
-                                          a[0][3], b.x, b.y);
-                            mma_f16_16816(part[nt][(2 * s2 + 1) % NA], a[1][0], a[1][1], a[1][2],
-                                          a[1][3], b.z, b.w);
-                        }
+                    for (int s = 0; s < 2; ++s) {
+                        codes_to_f16<!S::OFFSET>(w0[2 * s2 + s], a[u][s][0], a[u][s][2]);
+                        codes_to_f16<!S::OFFSET>(w1[2 * s2 + s], a[u][s][1], a[u][s][3]);
                     }
                 }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint4 b = HELD ? qf[HELD ? c : 0][s2]
+                                            : s_q[((nt * NCH + c) * 2 + s2) * 32 + lane];
+#pragma unroll
+                    for (int u = 0; u < PT; ++u) {
+                        mma_f16_16816(part[u][nt][2 * s2 % NA], a[u][0][0], a[u][0][1], a[u][0][2],
+                                      a[u][0][3], b.x, b.y);
+                        mma_f16_16816(part[u][nt][(2 * s2 + 1) % NA], a[u][1][0], a[u][1][1],
+                                      a[u][1][2], a[u][1][3], b.z, b.w);
+                    }
+                }
+            }
+        };
+        // the scores of a step, this warp's steps every kWarps-th
+#pragma unroll 1
+        for (int k = 0; k < mine; ++k) {
+#pragma unroll
+            for (int u = 0; u < PT; ++u)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4 * NA; ++e) part[u][nt][e / 4][e % 4] = 0.f;
+            uint32_t row_next[2 * PT];
+            int byte_next = -1;
+            if constexpr (QT == 1) {
+                keep_byte(k);
+                if (k + 1 < mine) issue(k + 1);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+                __syncwarp();
+                const uint32_t slot = ring + (k % NST) * S::STAGE;
+#pragma unroll
+                for (int c = 0; c < NCH; ++c) {
+                    const uint4 y[2] = {lds128(slot + c * 512), lds128(slot + (NCH + c) * 512)};
+                    multiply(c, y);
+                }
+            } else {
+                if (k + 1 < mine) {
+                    rows_of(k + 1, row_next, byte_next);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 2 * PT; ++j) row_next[j] = row[j];
+                }
+#pragma unroll
+                for (int c = 0; c < NCH; ++c) {
+                    uint4 y[2 * PT];
+                    if (c + 1 < NCH)
+                        load(y, row, c + 1);
+                    else
+                        load(y, row_next, 0);
+                    multiply(c, x);
+#pragma unroll
+                    for (int j = 0; j < 2 * PT; ++j) x[j] = y[j];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < PT; ++u) {
                 float acc[NT][4];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -365,41 +414,47 @@ select_pages_kernel(const SelectParams p) {
                         acc[nt][e] = 0.f;
 #pragma unroll
                         for (int i = 0; i < NA; ++i)
-                            acc[nt][e] += S::OFFSET
-                                              ? part[nt][i][e] - off[S::OFFSET ? nt : 0][e & 1][i]
-                                              : part[nt][i][e];
+                            acc[nt][e] += S::OFFSET ? part[u][nt][i][e] -
+                                                          off[S::OFFSET ? nt : 0][e & 1][i]
+                                                    : part[u][nt][i][e];
                     }
                 // Scores: of this lane's columns, then the best of the lanes that hold the
                 // query's other columns.
-                const int i0 = (warp + k * kWarps) * 16 + gq;
-                const int *bytes = scale + (k % NST) * 16 + gq;
-                const int byte2[2] = {bytes[0], bytes[8]};
+                const int i0 = (warp + k * kWarps) * STEP + u * 16 + gq;
+                int byte2[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    byte2[j] = QT == 1 ? scale[(k % NST) * 16 + gq + 8 * j]
+                                       : __shfl_sync(0xffffffffu, byte, u * 16 + gq + 8 * j);
                 const bool near = plain && (uint32_t)(byte2[0] - 67) <= 103u &&
                                   (uint32_t)(byte2[1] - 67) <= 103u;
                 const bool fast = __all_sync(0xffffffffu, near);
                 if (fast) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float4 f = *reinterpret_cast<const float4 *>(&s_col[nt * 8 + 2 * tq]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            acc[nt][e] = fmaf(acc[nt][e], fac[nt][e & 1], bias[nt][e & 1]);
+                            acc[nt][e] = e & 1 ? fmaf(acc[nt][e], f.z, f.w) : fmaf(acc[nt][e], f.x, f.y);
+                    }
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            acc[nt][e] = ex[nt][e & 1] == kNoVote
-                                             ? -INFINITY
-                                             : scaled(acc[nt][e], ex[nt][e & 1] + byte2[e >> 1] - 127);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const int ex = s_exp[nt * 8 + 2 * tq + (e & 1)];
+                            acc[nt][e] = ex == kNoVote ? -INFINITY
+                                                       : scaled(acc[nt][e], ex + byte2[e >> 1] - 127);
+                        }
                 }
-                auto store = [&](int query, float m, int i, int byte, int first_recent, bool here) {
+                auto store = [&](int query, float m, int i, int byte, bool here) {
                     if (fast)
                         m *= pow2(byte - 127);
                     else if (byte == (int)kScaleNaN)
                         m = INFINITY;
                     uint32_t key = byte >= 0 ? sortable(m + 0.f) : 0u;
                     const int page = base + i;
-                    if (page < p.num_first || page >= first_recent) key = kForced;
+                    if (page < p.num_first || page >= pages_of(query) - p.num_recent) key = kForced;
                     if (here) s_key[query * p.cap + i] = key;
                 };
                 auto best = [&](int nt, int j) { return fmaxf(acc[nt][2 * j], acc[nt][2 * j + 1]); };
@@ -416,7 +471,7 @@ select_pages_kernel(const SelectParams p) {
                             m[r] = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], 1));
                             if (GP >= 8) m[r] = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], 2));
                         }
-                        store((nt * 8 + 2 * tq) / GP, j ? m[1] : m[0], i, byte, recent[nt][0],
+                        store((nt * 8 + 2 * tq) / GP, j ? m[1] : m[0], i, byte,
                               GP == 4 || tq < 2);
                     }
                 } else {
@@ -426,18 +481,22 @@ select_pages_kernel(const SelectParams p) {
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             if (GP == 2) {
-                                store(nt * 4 + tq, best(nt, j), i, byte, recent[nt][0], true);
+                                store(nt * 4 + tq, best(nt, j), i, byte, true);
                             } else {
-                                store(nt * 8 + 2 * tq, acc[nt][2 * j], i, byte, recent[nt][0], true);
-                                store(nt * 8 + 2 * tq + 1, acc[nt][2 * j + 1], i, byte,
-                                      recent[nt][GP == 1], true);
+                                store(nt * 8 + 2 * tq, acc[nt][2 * j], i, byte, true);
+                                store(nt * 8 + 2 * tq + 1, acc[nt][2 * j + 1], i, byte, true);
                             }
                         }
                     }
                 }
             }
+            if (QT > 1) {
+                byte = byte_next;
+#pragma unroll
+                for (int j = 0; j < 2 * PT; ++j) row[j] = row_next[j];
+            }
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (QT == 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
 
         // The top_k-th largest score; a group of warps for each query.  The digits begin
@@ -448,7 +507,7 @@ select_pages_kernel(const SelectParams p) {
         const int nrow = mq < nq ? pages_of(mq) : 0;
         const bool choose = nrow > p.top_k;
         // Whole tiles are looked through: what lies behind a row counts as forced.
-        const int scan = choose ? tiles * 16 : 0;
+        const int scan = choose ? tiles * STEP : 0;
         const uint32_t *key_row = s_key + mq * p.cap;
         const bool fixed = QT > 1 && C > 1;
         auto group_sync = [&] {
@@ -470,7 +529,7 @@ select_pages_kernel(const SelectParams p) {
             group_sync();
         }
         uint32_t prefix = 0;  // of the scores that are left: the bits from `digit` up
-        int need = p.top_k + (n + 15) / 16 * 16 - nrow, left = 0, digit = 32, pass = 0;
+        int need = p.top_k + (n + STEP - 1) / STEP * STEP - nrow, left = 0, digit = 32, pass = 0;
         if (!fixed) {
             need = p.top_k - p.num_first - p.num_recent;  // forced ones are above all others
             uint32_t lo = 0xffffffffu, hi = 0;
@@ -763,7 +822,7 @@ cudaError_t launch_as(SelectParams p, bool &fits, cudaStream_t stream) {
     // as many CTAs per tile as there is room for at once, of at least 256 pages, and
     // more if the scores would not fit
     int c = 1;
-    auto cap = [&] { return ((n + c - 1) / c + 15) / 16 * 16; };
+    auto cap = [&] { return ((n + c - 1) / c + S::STEP - 1) / S::STEP * S::STEP; };
     while (c < 16 && ((units * c < 2LL * device_sm_count() && n / c >= 512) ||
                       smem_bytes<S>(cap()) > kMaxSmem))
         c *= 2;
@@ -781,7 +840,7 @@ cudaError_t launch_as(SelectParams p, bool &fits, cudaStream_t stream) {
 template <int NCH, int NT, int GP>
 cudaError_t launch_tiles(const SelectParams &p, bool &fits, cudaStream_t stream) {
     const int n = (p.r.max_seqlen + p.block_size - 1) >> p.bs_shift;
-    if (smem_bytes<Shape<NCH, NT, GP, 8>>((n + 15) / 16 * 16) <= kHalfSmem)
+    if (smem_bytes<Shape<NCH, NT, GP, 8>>((n + 31) / 32 * 32) <= kHalfSmem)
         return launch_as<NCH, NT, GP, 8>(p, fits, stream);
     return launch_as<NCH, NT, GP, 16>(p, fits, stream);
 }
