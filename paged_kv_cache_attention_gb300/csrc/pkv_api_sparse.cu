@@ -236,7 +236,9 @@ pkv_status pkv_paged_sparse_attention(void *out, const void *q, const void *k_ca
     p.top_k = top_k;
     p.hnd = cache.layout == PKV_HND ? 1 : 0;
     p.scale_log2 = sm_scale * 1.4426950408889634f;
-    // as many CTAs per row and kv head as run at once, of at least 128 keys
+    // As many CTAs per row and kv head as run at once, of at least 128 keys (8 kv heads,
+    // 1024 keys: 8 rows 27.7 us in one CTA each, 9.7 in eight; 16 rows 28 and 14.5 in
+    // four; 64 rows 46 and 61 in eight).
     const int64_t units = (int64_t)total_q * cache.num_kv_heads;
     int c = 1;
     while (c < 8 && units * c < 3LL * device_sm_count() &&
@@ -249,7 +251,11 @@ pkv_status pkv_paged_sparse_attention(void *out, const void *q, const void *k_ca
     if ((st = pool_map(&tk, k_cache, cache, rows)) != PKV_OK) return st;
     if ((st = pool_map(&tv, v_cache, cache, rows)) != PKV_OK) return st;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (!fp8 && cu_seq_lens_q && total_q >= 4LL * batch) {  // chunks: 4 queries on average
+    // Chunks: tiles of 128 rows, where a request's queries fill a quarter of one on average
+    // (16 requests, 8 kv heads of 4, 1024 keys a query and no two lists alike: 4 queries
+    // 52 us, 32 row by row; 8 queries 69 and 62; 16 84 and 94; 64 117 and 289).
+    if (!fp8 && cu_seq_lens_q && total_q >= 4LL * batch &&
+        (int64_t)total_q * p.r.group >= 32LL * batch) {
         bool fits = false;
         const cudaError_t e =
             launch_sparse_tile(p, fits, cache.block_size, k_cache, v_cache, &tk, &tv, s);

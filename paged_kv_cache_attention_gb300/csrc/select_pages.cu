@@ -819,11 +819,11 @@ cudaError_t launch_as(SelectParams p, bool &fits, cudaStream_t stream) {
     auto kern = select_pages_kernel<NCH, NT, GP, W>;
     const int64_t units = (S::QT > 1 ? row_tiles(p.r, S::QT) : p.r.rows) * p.r.num_kv_heads;
     const int n = (p.r.max_seqlen + p.block_size - 1) >> p.bs_shift;
-    // as many CTAs per tile as there is room for at once, of at least 256 pages, and
-    // more if the scores would not fit
+    // CTAs per tile: more while they have an SM each (8 kv heads of 8 contexts of 100K
+    // tokens: 4 CTAs 26 us, 1 43, 8 39) and 512 pages to share out, or the scores do not fit
     int c = 1;
     auto cap = [&] { return ((n + c - 1) / c + S::STEP - 1) / S::STEP * S::STEP; };
-    while (c < 16 && ((units * c < 2LL * device_sm_count() && n / c >= 512) ||
+    while (c < 16 && ((units * c <= device_sm_count() && n / c >= 512) ||
                       smem_bytes<S>(cap()) > kMaxSmem))
         c *= 2;
     fits = smem_bytes<S>(cap()) <= kMaxSmem && units * c <= 0x7fffffff;
@@ -849,8 +849,9 @@ template <int NCH>
 cudaError_t launch_n(const SelectParams &p, cudaStream_t stream) {
     bool fits = false;
     const int G = p.r.group;
-    // Tiles of queries where requests have several (4 on average); long contexts whose
-    // scores do not fit go on with one query at a time.
+    // Tiles of queries where requests have several, 4 on average (16 requests of 24K tokens,
+    // 8 kv heads of 4: 4 queries 41 us, 40 one at a time; 8 queries 44 and 65; 64 140 and
+    // 411); long contexts whose scores do not fit go on with one query at a time.
     if (p.r.cu_q && p.r.rows >= 4LL * p.r.batch) {
         const cudaError_t e = G == 1   ? launch_tiles<NCH, 1, 1>(p, fits, stream)
                               : G == 2 ? launch_tiles<NCH, 2, 2>(p, fits, stream)
@@ -859,9 +860,10 @@ cudaError_t launch_n(const SelectParams &p, cudaStream_t stream) {
                                        : launch_tiles<NCH, 8, 16>(p, fits, stream);
         if (fits) return e;
     }
-    // Small CTAs, of which all queries of a decode step have theirs at once; larger ones
-    // where a query's pages are shared by a cluster (8 kv heads, 1M tokens: 66 -> 55 us).
-    if ((int64_t)p.r.rows * p.r.num_kv_heads < 2LL * device_sm_count())
+    // Small CTAs, of which all queries of a decode step have theirs at once (64 queries of
+    // 8K tokens, 8 kv heads: 15 us, 20 in CTAs of eight warps); larger ones where a CTA has
+    // an SM to itself (one of 400K tokens: 29 us, 33 in CTAs of four).
+    if ((int64_t)p.r.rows * p.r.num_kv_heads <= device_sm_count())
         return G <= 8 ? launch_as<NCH, 1, 8, 8>(p, fits, stream)
                       : launch_as<NCH, 2, 16, 8>(p, fits, stream);
     return G <= 8 ? launch_as<NCH, 1, 8, 4>(p, fits, stream)

@@ -103,13 +103,15 @@ def test_many_rows(fp8):
     run(lens, [1] * 130, 8, 4, 64, fp8=fp8, top_k=20, sink=True)
 
 
+@pytest.mark.parametrize("hq", [8, 32])
 @pytest.mark.parametrize("layout,fp8", KINDS)
 @pytest.mark.parametrize("queries,lens", [([3, 1, 8, 5], [3, 300, 500, 9]), ([33], [500]),
                                           ([0, 2, 0, 17, 1], [30, 90, 0, 17, 200]),
                                           ([6, 4], [3, 100])])
-def test_chunks(layout, fp8, queries, lens):
-    """Rows of a chunk, each up to its own position; rows of no request stay."""
-    run(lens, queries, 8, 2, 64, 16, layout, fp8, top_k=9, sink=True, extra=4, chunk=True)
+def test_chunks(layout, fp8, queries, lens, hq):
+    """Rows of a chunk, each up to its own position; rows of no request stay.  Few heads
+    are taken row by row, many in tiles."""
+    run(lens, queries, hq, 2, 64, 16, layout, fp8, top_k=9, sink=True, extra=4, chunk=True)
 
 
 @pytest.mark.parametrize("kind", ["last", "random"])
@@ -122,45 +124,49 @@ def test_tiles_of_queries(hq, hkv, d, bs, kind):
         sink=True, extra=3, layout="HND")
 
 
+@pytest.mark.parametrize("hq", [4, 32])
 @pytest.mark.parametrize("batch", [256, 257])
-def test_chunks_of_many_requests(batch):
+def test_chunks_of_many_requests(batch, hq):
     """Tiles request by request, and beyond that count every so many rows."""
     g = torch.Generator().manual_seed(batch)
     lens = torch.randint(0, 60, (batch,), generator=g).tolist()
     queries = [min(n, 5) if i % 9 else 0 for i, n in enumerate(lens)]
     queries[7] = lens[7] = 200
-    run(lens, queries, 4, 2, 64, top_k=3, chunk=True, extra=3)
+    run(lens, queries, hq, 2, 64, top_k=3, chunk=True, extra=3)
 
 
-def test_offsets_that_are_none():
+@pytest.mark.parametrize("hq", [2, 16])
+def test_offsets_that_are_none(hq):
     """Offsets that decrease or leave the rows: nothing outside is read or written."""
     pools, table, slots, _ = small()
     kc, vc, _, _ = pools.device(DEV)
-    q = torch.randn(8, 2, 64, generator=torch.Generator().manual_seed(1)).to(BF16).to(DEV)
+    q = torch.randn(8, hq, 64, generator=torch.Generator().manual_seed(1)).to(BF16).to(DEV)
     pages = torch.arange(4, dtype=I32, device=DEV).expand(8, 1, 4).contiguous()
     two = torch.cat([table, table]).to(DEV)
     lens = torch.tensor([100, 100], dtype=I32, device=DEV)
     for cu in ([2, 1, 8], [0, 19, 3], [3, 3, 3], [-5, 0, 90], [8, 2, 0], [0, 4, 8]):
-        out = torch.full((8, 2, 64), 7.0, dtype=BF16, device=DEV)
+        out = torch.full((8, hq, 64), 7.0, dtype=BF16, device=DEV)
         pkv.paged_sparse_attention(q, kc, vc, two, lens, pages, out=out,
                                    cu_seq_lens_q=torch.tensor(cu, dtype=I32, device=DEV))
         assert bool(torch.isfinite(out.float()).all())
     assert not bool((out == 7.0).any())
 
 
+@pytest.mark.parametrize("hq", [4, 16])
 @pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
-def test_chunk_scales(scale):
-    run([300, 33], [9, 7], 4, 2, 64, top_k=9, scale=scale, sink=True)
+def test_chunk_scales(scale, hq):
+    run([300, 33], [9, 7], hq, 2, 64, top_k=9, scale=scale, sink=True)
 
 
-def test_wide_lists_and_tables():
+@pytest.mark.parametrize("hq", [4, 32])
+def test_wide_lists_and_tables(hq):
     """Unions of hundreds of pages; a table too wide for them to be numbered."""
     run([16 * 700 + 3], [9], 4, 1, 64, top_k=150)
     g = torch.Generator().manual_seed(9)
     pools = R.Pools(40, 16, 2, 64, "NHD", False, g)
     narrow, slots = R.paged([300, 200], 16, 40, g)
     kc, vc, _, _ = pools.device(DEV)
-    q = torch.randn(10, 4, 64, generator=g).to(BF16).to(DEV)
+    q = torch.randn(10, hq, 64, generator=g).to(BF16).to(DEV)
     lens = torch.tensor([300, 200], dtype=I32, device=DEV)
     cu = torch.tensor([0, 6, 10], dtype=I32, device=DEV)
     rows = S.rows_of([6, 4], [300, 200])
@@ -199,11 +205,12 @@ def test_chunk_with_a_key_that_is_not_finite(pool, value):
     assert float(off.max()) <= 0
 
 
-def test_chunk_lists_that_end_early():
+@pytest.mark.parametrize("hq", [2, 8])
+def test_chunk_lists_that_end_early(hq):
     """Lists of a chunk with errors and entries behind their end; pages out of the pool."""
     pools, table, slots, _ = small()
     g = torch.Generator().manual_seed(11)
-    q = torch.randn(6, 2, 64, generator=g).to(BF16)
+    q = torch.randn(6, hq, 64, generator=g).to(BF16)
     given = [[1, 3, 5, -1], [1, -1, 3, 5], [1, 3, 3, 5], [3, 1, 4, 5], [1, 3, 7, 8], [0, 2, 4, 6]]
     held = [[1, 3, 5, -1], [1, -1, -1, -1], [1, 3, -1, -1], [3, -1, -1, -1], [1, 3, -1, -1],
             [0, 2, -1, -1]]
