@@ -107,10 +107,11 @@ def test_many_rows(fp8):
 @pytest.mark.parametrize("layout,fp8", KINDS)
 @pytest.mark.parametrize("queries,lens", [([3, 1, 8, 5], [3, 300, 500, 9]), ([33], [500]),
                                           ([0, 2, 0, 17, 1], [30, 90, 0, 17, 200]),
-                                          ([6, 4], [3, 100])])
+                                          ([6, 4], [3, 100]), ([30, 1, 8, 13], [30, 300, 500, 50]),
+                                          ([0, 20, 0, 47, 1], [30, 90, 0, 47, 200])])
 def test_chunks(layout, fp8, queries, lens, hq):
-    """Rows of a chunk, each up to its own position; rows of no request stay.  Few heads
-    are taken row by row, many in tiles."""
+    """Rows of a chunk, each up to its own position; rows of no request stay.  Few
+    queries are taken row by row, many in tiles."""
     run(lens, queries, hq, 2, 64, 16, layout, fp8, top_k=9, sink=True, extra=4, chunk=True)
 
 
@@ -124,28 +125,28 @@ def test_tiles_of_queries(hq, hkv, d, bs, kind):
         sink=True, extra=3, layout="HND")
 
 
-@pytest.mark.parametrize("hq", [4, 32])
+@pytest.mark.parametrize("most,hq", [(5, 4), (12, 8)])
 @pytest.mark.parametrize("batch", [256, 257])
-def test_chunks_of_many_requests(batch, hq):
+def test_chunks_of_many_requests(batch, most, hq):
     """Tiles request by request, and beyond that count every so many rows."""
     g = torch.Generator().manual_seed(batch)
     lens = torch.randint(0, 60, (batch,), generator=g).tolist()
-    queries = [min(n, 5) if i % 9 else 0 for i, n in enumerate(lens)]
+    queries = [min(n, most) if i % 9 else 0 for i, n in enumerate(lens)]
     queries[7] = lens[7] = 200
     run(lens, queries, hq, 2, 64, top_k=3, chunk=True, extra=3)
 
 
-@pytest.mark.parametrize("hq", [2, 16])
-def test_offsets_that_are_none(hq):
+@pytest.mark.parametrize("n,hq", [(8, 2), (16, 8)])
+def test_offsets_that_are_none(n, hq):
     """Offsets that decrease or leave the rows: nothing outside is read or written."""
     pools, table, slots, _ = small()
     kc, vc, _, _ = pools.device(DEV)
-    q = torch.randn(8, hq, 64, generator=torch.Generator().manual_seed(1)).to(BF16).to(DEV)
-    pages = torch.arange(4, dtype=I32, device=DEV).expand(8, 1, 4).contiguous()
+    q = torch.randn(n, hq, 64, generator=torch.Generator().manual_seed(1)).to(BF16).to(DEV)
+    pages = torch.arange(4, dtype=I32, device=DEV).expand(n, 1, 4).contiguous()
     two = torch.cat([table, table]).to(DEV)
     lens = torch.tensor([100, 100], dtype=I32, device=DEV)
-    for cu in ([2, 1, 8], [0, 19, 3], [3, 3, 3], [-5, 0, 90], [8, 2, 0], [0, 4, 8]):
-        out = torch.full((8, hq, 64), 7.0, dtype=BF16, device=DEV)
+    for cu in ([2, 1, n], [0, 19, 3], [3, 3, 3], [-5, 0, 90], [n, 2, 0], [0, n // 2, n]):
+        out = torch.full((n, hq, 64), 7.0, dtype=BF16, device=DEV)
         pkv.paged_sparse_attention(q, kc, vc, two, lens, pages, out=out,
                                    cu_seq_lens_q=torch.tensor(cu, dtype=I32, device=DEV))
         assert bool(torch.isfinite(out.float()).all())
@@ -158,18 +159,18 @@ def test_chunk_scales(scale, hq):
     run([300, 33], [9, 7], hq, 2, 64, top_k=9, scale=scale, sink=True)
 
 
-@pytest.mark.parametrize("hq", [4, 32])
-def test_wide_lists_and_tables(hq):
+@pytest.mark.parametrize("queries,hq", [([6, 4], 4), ([12, 8], 32)])
+def test_wide_lists_and_tables(queries, hq):
     """Unions of hundreds of pages; a table too wide for them to be numbered."""
     run([16 * 700 + 3], [9], 4, 1, 64, top_k=150)
     g = torch.Generator().manual_seed(9)
     pools = R.Pools(40, 16, 2, 64, "NHD", False, g)
     narrow, slots = R.paged([300, 200], 16, 40, g)
     kc, vc, _, _ = pools.device(DEV)
-    q = torch.randn(10, hq, 64, generator=g).to(BF16).to(DEV)
+    q = torch.randn(sum(queries), hq, 64, generator=g).to(BF16).to(DEV)
     lens = torch.tensor([300, 200], dtype=I32, device=DEV)
-    cu = torch.tensor([0, 6, 10], dtype=I32, device=DEV)
-    rows = S.rows_of([6, 4], [300, 200])
+    cu = torch.tensor([0, queries[0], sum(queries)], dtype=I32, device=DEV)
+    rows = S.rows_of(queries, [300, 200])
     pages = lists(rows, 2, 5, 16, random.Random(9), "last").to(DEV)
     wide = torch.full((2, 700000), -1, dtype=I32)
     wide[:, :narrow.shape[1]] = narrow
@@ -205,32 +206,34 @@ def test_chunk_with_a_key_that_is_not_finite(pool, value):
     assert float(off.max()) <= 0
 
 
-@pytest.mark.parametrize("hq", [2, 8])
-def test_chunk_lists_that_end_early(hq):
+@pytest.mark.parametrize("n,hq", [(6, 2), (12, 8)])
+def test_chunk_lists_that_end_early(n, hq):
     """Lists of a chunk with errors and entries behind their end; pages out of the pool."""
     pools, table, slots, _ = small()
     g = torch.Generator().manual_seed(11)
-    q = torch.randn(6, hq, 64, generator=g).to(BF16)
+    q = torch.randn(n, hq, 64, generator=g).to(BF16)
     given = [[1, 3, 5, -1], [1, -1, 3, 5], [1, 3, 3, 5], [3, 1, 4, 5], [1, 3, 7, 8], [0, 2, 4, 6]]
     held = [[1, 3, 5, -1], [1, -1, -1, -1], [1, 3, -1, -1], [3, -1, -1, -1], [1, 3, -1, -1],
             [0, 2, -1, -1]]
+    if n == 12:
+        given, held = ([*x[:5], *x[:5], x[0], x[5]] for x in (given, held))
     kc, vc, _, _ = pools.device(DEV)
     err = torch.zeros(1, dtype=I32, device=DEV)
-    cu, lens = (torch.tensor(x, dtype=I32, device=DEV) for x in ([0, 6], [100]))
+    cu, lens = (torch.tensor(x, dtype=I32, device=DEV) for x in ([0, n], [100]))
     for broken, bits in ((False, pkv.DEVERR_BLOCK_ID), (True, pkv.DEVERR_BLOCK_ID)):
         t = table.clone()
         want = [list(x) for x in held]
         if broken:
             t[0, 4] = -1
-            want[5] = [0, 2, 6, -1]
+            want[-1] = [0, 2, 6, -1]
         else:
-            want[5] = [0, 2, 4, 6]
+            want[-1] = [0, 2, 4, 6]
         out = pkv.paged_sparse_attention(q.to(DEV), kc, vc, t.to(DEV), lens,
-                                         torch.tensor(given, dtype=I32, device=DEV).view(6, 1, 4),
+                                         torch.tensor(given, dtype=I32, device=DEV).view(n, 1, 4),
                                          cu_seq_lens_q=cu, dev_error=err)
         assert pkv.get_device_error(err, clear=True) == bits
-        pages = torch.tensor(want, dtype=I32).view(6, 1, 4)
-        ref, _, absv, smax, _ = S.attend_lists(q, pools, slots, S.rows_of([6], [100]), pages, 16, 0.125,
+        pages = torch.tensor(want, dtype=I32).view(n, 1, 4)
+        ref, _, absv, smax, _ = S.attend_lists(q, pools, slots, S.rows_of([n], [100]), pages, 16, 0.125,
                                                None)
         R.assert_within(out, ref, R.out_bound(ref, absv, smax, 64, 2.0 ** -8), "out")
 
