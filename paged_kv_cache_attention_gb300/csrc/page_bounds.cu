@@ -20,6 +20,10 @@
 // Least and largest are kept in the 16-bit type that is exact: bf16, or for 8-bit
 // pools f16 relative to the page's largest row scale (codes times 2^0 .. 2^-15 are
 // f16 values; pages whose scales lie further apart go by fp32).
+//
+// Measured (8 kv heads of 128): 64 tokens 2.9 us; 16K bf16 tokens in 8 prompts 7.0 us;
+// 88K tokens of 8-bit pages in 13 prompts 24 us with their 97 MB in L2 (14.4 at HBM's
+// rate), 36 us without: then its loads wait for one another page by page, issue at 50%.
 #include <cuda_fp16.h>
 
 #include "pkv_sparse.cuh"
@@ -293,7 +297,8 @@ cudaError_t launch_span(const BoundsParams &p, unsigned grid, cudaStream_t strea
 cudaError_t launch_page_bounds(const BoundsParams &p0, cudaStream_t stream) {
     BoundsParams p = p0;
     // A warp per token and kv head while they all run at once (a decode step); then
-    // windows of more tokens, then more kv heads per warp.
+    // windows of more tokens, then more kv heads per warp.  (64 tokens: windows of 1
+    // token 2.9 us, 4 5.2, 32 26; 1000 tokens 8.0, 6.6, 27; 16K tokens 12.6, 8.3, 7.1.)
     const int64_t warps = 16LL * device_sm_count();
     p.tokens_per_warp = 1;
     p.heads_per_warp = 1;

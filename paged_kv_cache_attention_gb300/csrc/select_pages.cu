@@ -28,9 +28,18 @@
 // order.  One launch, no workspace.
 //
 // In a decode step (one query per tile) HBM bound: (2 D + 1) bytes per page and kv
-// head, each read once; every lane copies the pieces it will use itself
-// (cp.async, three tiles ahead), so that nothing waits but on its own loads.  In a
-// chunk the queries of a tile share the pages' loads and conversions.
+// head, each read once; every lane copies the pieces it will use itself (cp.async, a
+// tile ahead; three ahead leave room for fewer CTAs: 62 us for 48), so that nothing
+// waits but on its own loads.  64 queries of 20K tokens, 8 kv heads of 128: 42 us, 59% of
+// HBM's rate; all CTAs read first and choose then.  One query of 1M tokens: 52 us, 36%: a
+// cluster of 16 CTAs on 128 of 152 SMs, and barriers for each digit.
+//
+// In a chunk the queries of a tile share the pages' loads and conversions: 934 queries of
+// 26K tokens, 8 kv heads of 4: 132 us (600 row by row).  There two CTAs of eight warps
+// an SM run one's choice beside the other's scores (163 us in one of 16), and two page
+// tiles share what is read of the columns (138 us with one).  The scores
+// take half of the time; the 25 GFLOP alone are 44 us at the rate of mma.sync (a product
+// every 8.6 clocks of a scheduler), 13 us at cuBLAS's.
 #include <cuda_fp16.h>
 
 #include "pkv_sparse.cuh"

@@ -18,8 +18,12 @@
 // another has such a value the tile of queries is taken again, row by row.
 //
 // Two CTAs share an SM, so that one's softmax runs beside the other's products and loads.
-// Bound by the softmax's exponentials, 16 a clock: 128 keys of 128 rows take 1024 clocks,
-// less the pages that are no row's of a warp.
+// Eight softmax warps, of two halves of the keys: 181 us where four took 318 (890 queries
+// of 1024 keys each, 8 kv heads of 4, D = 128).  Now 117 us, row by row 255.  A step takes
+// 5000 clocks, 2950 with two CTAs: 2600 of softmax (every score is looked at, an eighth
+// is a row's own: 15 GFLOP of products that count, 8 us, in eight times as many), the
+// rest the way from products to softmax and back.  Tiles are of one request each (rows
+// counted on over requests, beyond kTiledRequests: 165 us).
 #include "pkv_sparse.cuh"
 #include "pkv_tcgen05.cuh"
 
