@@ -5,8 +5,10 @@
 // on once for each of them, and a product of 16 rows has the heads of one query.  Here a
 // CTA takes 128 rows, (query, head) pairs of consecutive queries of one request and kv
 // head (32 queries of 4 heads), and the union of their lists:
-//   * every query's list becomes a bitmap of the request's pages; the union's pages
-//     are numbered in ascending order and taken 128 keys at a time;
+//   * every query's list becomes a bitmap of the request's pages, a window of a few
+//     thousand pages at a time (what two CTAs have room for, however wide the tables
+//     are); the union's pages are numbered in ascending order and taken 128 keys at a
+//     time;
 //   * S = Q K^T and O += P V are tcgen05 products of 128 x 128 x 128 with S, O and P
 //     (bf16, in place of S) in tensor memory, K and V by TMA, page by page;
 //   * thread = row in the softmax: a page that is not the row's weighs nothing, one that
@@ -50,8 +52,9 @@ enum { kKFull, kKEmpty, kVFull, kVReady, kVEmpty, kSFull, kPFull, kODone, kDrain
 constexpr int kOffQ = 0, kOffK = kTile, kOffV = 2 * kTile, kOffBar = 3 * kTile;
 constexpr int kOffTmem = kOffBar + kBars * 8;
 constexpr int kOffList = kOffTmem + 8;
-// then pages [cap] u16, bitmaps of the queries [queries][words], of the union [words] and its
-// prefix counts [words + 1]
+// then of a window: pages [32 words + PP] u16, bitmaps of the queries [queries][words], of the
+// union [words] and its prefix counts [words + 1]
+constexpr int kListBytes = 14000;
 
 // 0 * x + sum of bf16 pairs.
 __device__ __forceinline__ uint32_t zero_times(uint32_t x, uint32_t sum) {
@@ -127,7 +130,7 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
     uint8_t *smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // 1024-aligned
     const uint32_t base = smem_u32(smem), bars = base + kOffBar;
     uint16_t *s_page = reinterpret_cast<uint16_t *>(smem + kOffList);
-    uint32_t *s_own = reinterpret_cast<uint32_t *>(s_page + (p.cap + PP + 1) / 2 * 2);
+    uint32_t *s_own = reinterpret_cast<uint32_t *>(s_page + p.words * 32 + PP);
     __shared__ int s_end[kRows];       // where the queries' lists end
     __shared__ float s_max[2][kRows];  // the rows' largest scores (in the end: sums) by halves
     __shared__ int s_dead;  // a wait gave up: all others do
@@ -173,15 +176,10 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
         }
         const int first = t, nq = min(count, t_end - t);
         t += nq;
-        const int total = L + count - 1;  // the request's keys
-        const int words = ((max(L + nq - 1, 0) + BS - 1) >> SHIFT) / 32 + 1;
-        const int32_t *bt = p.r.block_table + (int64_t)r * p.r.max_blocks_per_seq;
+        const int keys = L + count - 1;  // of the request
+        const int all_words = ((max(L + nq - 1, 0) + BS - 1) >> SHIFT) / 32 + 1;
+        const int32_t *table = p.r.block_table + (int64_t)r * p.r.max_blocks_per_seq;
 
-        // ------------------------------------------------ the lists as bitmaps
-        for (int i = threadIdx.x; i < (nq + 1) * words; i += kThreads) {
-            const int j = i / words, w = i - j * words;
-            (j < nq ? s_own + j * p.words : s_bits)[w] = 0;
-        }
         if (threadIdx.x < nq) s_end[threadIdx.x] = p.top_k;
         // Q: row = query << group_shift | head, 128-byte swizzle; zeros in rows that are none.
         // A negative scale goes into Q, so that scores grow with the products, and one of 0 too.
@@ -200,7 +198,7 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
                                     : make_uint4(v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign);
         }
         __syncthreads();
-        // where each list ends, then its bits
+        // where each list ends
         const int64_t list_step = (int64_t)Hkv * p.top_k;
         const int32_t *lists = p.pages + ((int64_t)first * Hkv + g) * p.top_k;
         const int entries = nq * p.top_k;
@@ -211,279 +209,297 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
             const int e = list[x], before = x > 0 ? list[x - 1] : -1;
             if (e <= before || e >= (max(L + j, 0) + BS - 1) >> SHIFT) atomicMin(&s_end[j], x);
         }
-        __syncthreads();
+        // Two softmax warps have the same rows (a warp reaches its quarter of the TMEM lanes
+        // only): each takes half of a step's keys and of O's columns.
+        const int quarter = warp & 3, half = warp >> 2;
+        const int row = quarter * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(quarter + 1) : "memory"); };
+        const int j0 = row >> p.group_shift, h = row & ((1 << p.group_shift) - 1);
+        const bool live = j0 < nq && h < G;
+        float ref = kNegInf, l = 0.f;
+        bool ok = true;
+
+        int before = 0;  // steps of the windows before
+        // the pages in windows of p.words * 32
+        for (int w0 = 0; w0 < all_words && !*static_cast<volatile int *>(&s_dead); w0 += p.words) {
+            const int words = min(p.words, all_words - w0), page0 = w0 * 32;
+            const int32_t *bt = table + page0;
+            const int total = keys - page0 * BS;
+            // ------------------------------------------------ the lists as bitmaps
+            for (int i = threadIdx.x; i < (nq + 1) * words; i += kThreads) {
+                const int j = i / words, w = i - j * words;
+                (j < nq ? s_own + j * p.words : s_bits)[w] = 0;
+            }
+            __syncthreads();
 #pragma unroll 4
-        for (int i = threadIdx.x; i < entries; i += kThreads) {
-            const int j = i / p.top_k, x = i - j * p.top_k;
-            const int e = lists[j * list_step + x];
-            if (x < s_end[j]) {
-                const int id = bt[e];
-                if (id >= 0 && id < p.r.num_blocks) {
-                    atomicOr(&s_own[j * p.words + (e >> 5)], 1u << (e & 31));
-                    atomicOr(&s_bits[e >> 5], 1u << (e & 31));
-                } else {
+            for (int i = threadIdx.x; i < entries; i += kThreads) {
+                const int j = i / p.top_k, x = i - j * p.top_k;
+                const int e = lists[j * list_step + x] - page0;
+                if (x < s_end[j] && (uint32_t)e < (uint32_t)words * 32u) {
+                    const int id = bt[e];
+                    if (id >= 0 && id < p.r.num_blocks) {
+                        atomicOr(&s_own[j * p.words + (e >> 5)], 1u << (e & 31));
+                        atomicOr(&s_bits[e >> 5], 1u << (e & 31));
+                    } else {
+                        flag_error(p.r.dev_error, PKV_DEVERR_BLOCK_ID);
+                    }
+                } else if (x == s_end[j] && e >= 0 && page0 == 0) {
                     flag_error(p.r.dev_error, PKV_DEVERR_BLOCK_ID);
                 }
-            } else if (x == s_end[j] && e >= 0) {
-                flag_error(p.r.dev_error, PKV_DEVERR_BLOCK_ID);
             }
-        }
-        fence_proxy_async_smem();
-        __syncthreads();
-        if (warp == 0) {
-            int sum = 0;
+            fence_proxy_async_smem();
+            __syncthreads();
+            if (warp == 0) {
+                int sum = 0;
 #pragma unroll 1
-            for (int w0 = 0; w0 < words; w0 += 32) {
-                const int own = w0 + lane < words ? __popc(s_bits[w0 + lane]) : 0;
-                int in = own;
+                for (int w0 = 0; w0 < words; w0 += 32) {
+                    const int own = w0 + lane < words ? __popc(s_bits[w0 + lane]) : 0;
+                    int in = own;
 #pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const int o = __shfl_up_sync(0xffffffffu, in, off);
-                    if (lane >= off) in += o;
-                }
-                if (w0 + lane < words) s_before[w0 + lane] = sum + in - own;
-                sum += __shfl_sync(0xffffffffu, in, 31);
-            }
-            if (lane == 0) s_before[words] = sum;
-        }
-        __syncthreads();
-        const int n = s_before[words], steps = (n + PP - 1) / PP;
-        for (int w = threadIdx.x; w < words; w += kThreads) {
-            int at = s_before[w];
-            for (uint32_t b = s_bits[w]; b; b &= b - 1) s_page[at++] = (uint16_t)(w * 32 + __ffs(b) - 1);
-        }
-        if (threadIdx.x < PP) s_page[n + threadIdx.x] = 0;  // up to the last step's end
-        __syncthreads();
-
-        if (warp == kLoad) {
-            // ------------------------------------------------ pages by TMA
-            int id = lane < min(PP, n) ? bt[s_page[lane]] : 0;
-            int j = 0;
-            for (; j < steps; ++j) {
-                const int k = done + j, m = min(PP, n - j * PP);
-                const int next = lane < min(PP, n - (j + 1) * PP) ? bt[s_page[(j + 1) * PP + lane]] : 0;
-                const int cy = p.hnd ? 0 : g, cz = p.hnd ? id * Hkv + g : id * BS;
-                bool ok = true;
-#pragma unroll 1
-                for (int v = 0; v < 2 && ok; ++v) {  // K, then V
-                    if (k > 0) ok = __all_sync(0xffffffffu, wait(v ? kVEmpty : kKEmpty, (k - 1) & 1));
-                    if (!ok) break;
-                    const uint32_t full = bar(v ? kVFull : kKFull);
-                    const bool one = elect_one();
-                    if (one) mbar_arrive_expect_tx(full, m * BS * 256);
-#pragma unroll
-                    for (int i = 0; i < PP; ++i) {
-                        const int z = __shfl_sync(0xffffffffu, cz, i);
-                        if (i < m && one)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                tma_load_3d(base + (v ? kOffV : kOffK) + h * kHalf + i * BS * 128,
-                                            v ? &tmv : &tmk, full, h * 64, cy, z);
+                    for (int off = 1; off < 32; off <<= 1) {
+                        const int o = __shfl_up_sync(0xffffffffu, in, off);
+                        if (lane >= off) in += o;
                     }
+                    if (w0 + lane < words) s_before[w0 + lane] = sum + in - own;
+                    sum += __shfl_sync(0xffffffffu, in, 31);
                 }
-                if (!ok) break;
-                id = next;
+                if (lane == 0) s_before[words] = sum;
             }
-            if (j < steps) {  // a wait gave up: let the copies in flight land
-                for (int b = 0; b < 2; ++b)
-                    for (int par = 0; par < 2; ++par)
-                        mbar_wait_bounded(bar(b ? kVFull : kKFull), par, p.r.dev_error);
+            __syncthreads();
+            const int n = s_before[words], steps = (n + PP - 1) / PP;
+            for (int w = threadIdx.x; w < words; w += kThreads) {
+                int at = s_before[w];
+                for (uint32_t b = s_bits[w]; b; b &= b - 1) s_page[at++] = (uint16_t)(w * 32 + __ffs(b) - 1);
             }
-        } else if (warp == kIssue) {
-            // ------------------------------------------------ products
-            bool ok = true;
-            if (elect_one()) {
-                constexpr uint32_t idS = tc::idesc_bf16_f32(kRows, kKeys, 0, 0);
-                constexpr uint32_t idO = tc::idesc_bf16_f32(kRows, kD, 0, 1);
-                const uint64_t dq = tc::smem_desc_sw128(base + kOffQ, 16, 1024);
-                const uint64_t dk = tc::smem_desc_sw128(base + kOffK, 16, 1024);
-                const uint64_t dv = tc::smem_desc_sw128(base + kOffV, kHalf, 1024);
+            if (threadIdx.x < PP) s_page[n + threadIdx.x] = 0;  // up to the last step's end
+            __syncthreads();
+
+            if (warp == kLoad) {
+                // ------------------------------------------------ pages by TMA
+                int id = lane < min(PP, n) ? bt[s_page[lane]] : 0;
+                int j = 0;
+                for (; j < steps; ++j) {
+                    const int k = done + j, m = min(PP, n - j * PP);
+                    const int next = lane < min(PP, n - (j + 1) * PP) ? bt[s_page[(j + 1) * PP + lane]] : 0;
+                    const int cy = p.hnd ? 0 : g, cz = p.hnd ? id * Hkv + g : id * BS;
+                    bool ok = true;
 #pragma unroll 1
-                for (int j = 0; j < steps && ok; ++j) {
-                    const int k = done + j;
-                    // S goes where P was: the product with it must be done
-                    ok = wait(kKFull, k & 1) && (k == 0 || wait(kODone, (k - 1) & 1));
+                    for (int v = 0; v < 2 && ok; ++v) {  // K, then V
+                        if (k > 0) ok = __all_sync(0xffffffffu, wait(v ? kVEmpty : kKEmpty, (k - 1) & 1));
+                        if (!ok) break;
+                        const uint32_t full = bar(v ? kVFull : kKFull);
+                        const bool one = elect_one();
+                        if (one) mbar_arrive_expect_tx(full, m * BS * 256);
+#pragma unroll
+                        for (int i = 0; i < PP; ++i) {
+                            const int z = __shfl_sync(0xffffffffu, cz, i);
+                            if (i < m && one)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    tma_load_3d(base + (v ? kOffV : kOffK) + h * kHalf + i * BS * 128,
+                                                v ? &tmv : &tmk, full, h * 64, cy, z);
+                        }
+                    }
                     if (!ok) break;
-                    tc::fence_after_sync();
-                    tc::mma_ss8<kHalf>(colS, dq, dk, idS, 0u);
-                    tc::commit(bar(kSFull));
-                    tc::commit(bar(kKEmpty));
-                    ok = wait(kPFull, k & 1) && wait(kVReady, k & 1);
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    // P: 16 keys in 8 columns, the second half's where its S was
-#pragma unroll
-                    for (int i = 0; i < kKeys / 16; ++i)
-                        tc::mma_ts(colO, colS + (i / 4) * 64 + (i % 4) * 8, dv + i * 128, idO,
-                                   j > 0 || i > 0 ? 1u : 0u);
-                    tc::commit(bar(kODone));
-                    tc::commit(bar(kVEmpty));
+                    id = next;
                 }
-                if (!ok) {  // the products in flight
-                    tc::commit(bar(kDrain));
-                    mbar_wait_bounded(bar(kDrain), 0, p.r.dev_error);
+                if (j < steps) {  // a wait gave up: let the copies in flight land
+                    for (int b = 0; b < 2; ++b)
+                        for (int par = 0; par < 2; ++par)
+                            mbar_wait_bounded(bar(b ? kVFull : kKFull), par, p.r.dev_error);
                 }
-            }
-            __syncwarp();
-        } else if (warp == kCheck) {
-            // ------------------------------------------------ V: tails zeroed, all finite?
-            uint32_t sum[4] = {0u, 0u, 0u, 0u};  // of 0 * v: NaN if v is not finite
+            } else if (warp == kIssue) {
+                // ------------------------------------------------ products
+                bool ok = true;
+                if (elect_one()) {
+                    constexpr uint32_t idS = tc::idesc_bf16_f32(kRows, kKeys, 0, 0);
+                    constexpr uint32_t idO = tc::idesc_bf16_f32(kRows, kD, 0, 1);
+                    const uint64_t dq = tc::smem_desc_sw128(base + kOffQ, 16, 1024);
+                    const uint64_t dk = tc::smem_desc_sw128(base + kOffK, 16, 1024);
+                    const uint64_t dv = tc::smem_desc_sw128(base + kOffV, kHalf, 1024);
 #pragma unroll 1
-            for (int j = 0; j < steps; ++j) {
-                const int k = done + j, m = min(PP, n - j * PP);
-                if (!__all_sync(0xffffffffu, wait(kVFull, k & 1))) break;
-                // keys of the step that the request has (only its last page can end inside)
-                const int end = (m - 1) * BS + min(BS, total - (int)s_page[j * PP + m - 1] * BS);
-                uint4 *v = reinterpret_cast<uint4 *>(smem + kOffV) + lane;
-                if (end < kKeys) {
-#pragma unroll 1
-                    for (int i = lane; i < kKeys * 16; i += 32)  // (8 chunks a row, two halves)
-                        if (((i >> 3) & (kKeys - 1)) >= end) v[i - lane] = make_uint4(0u, 0u, 0u, 0u);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-#pragma unroll 1
-                for (int i0 = 0; i0 < kKeys * 16; i0 += 8 * 32) {
-                    uint4 x[8];
+                    for (int j = 0; j < steps && ok; ++j) {
+                        const int k = done + j;
+                        // S goes where P was: the product with it must be done
+                        ok = wait(kKFull, k & 1) && (k == 0 || wait(kODone, (k - 1) & 1));
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        tc::mma_ss8<kHalf>(colS, dq, dk, idS, 0u);
+                        tc::commit(bar(kSFull));
+                        tc::commit(bar(kKEmpty));
+                        ok = wait(kPFull, k & 1) && wait(kVReady, k & 1);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        // P: 16 keys in 8 columns, the second half's where its S was
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = v[i0 + 32 * i];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        sum[0] = zero_times(x[i].x, sum[0]);
-                        sum[1] = zero_times(x[i].y, sum[1]);
-                        sum[2] = zero_times(x[i].z, sum[2]);
-                        sum[3] = zero_times(x[i].w, sum[3]);
+                        for (int i = 0; i < kKeys / 16; ++i)
+                            tc::mma_ts(colO, colS + (i / 4) * 64 + (i % 4) * 8, dv + i * 128, idO,
+                                       before + j > 0 || i > 0 ? 1u : 0u);
+                        tc::commit(bar(kODone));
+                        tc::commit(bar(kVEmpty));
+                    }
+                    if (!ok) {  // the products in flight
+                        tc::commit(bar(kDrain));
+                        mbar_wait_bounded(bar(kDrain), 0, p.r.dev_error);
                     }
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kVReady));
-            }
-            if ((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7fff7fffu) s_bad = 1;
-        } else {
-            // ------------------------------------------------ softmax, thread = row
-            // Two warps have the same rows (a warp reaches its quarter of the TMEM lanes
-            // only): each takes half of a step's keys and of O's columns.
-            const int quarter = warp & 3, half = warp >> 2;
-            const int row = quarter * 32 + lane;
-            const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-            constexpr int HP = PP / 2;  // pages of a half
-            auto pair_sync = [&] {
-                asm volatile("bar.sync %0, 64;" ::"r"(quarter + 1) : "memory");
-            };
-            const int j0 = row >> p.group_shift, h = row & ((1 << p.group_shift) - 1);
-            const bool live = j0 < nq && h < G;
-            const int limit = live ? L + j0 : 0;
-            const uint32_t *own = s_own + (live ? j0 : 0) * p.words;
-            const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
-            float ref = kNegInf, l = 0.f;
-            bool ok = true;
+            } else if (warp == kCheck) {
+                // ------------------------------------------------ V: tails zeroed, all finite?
+                uint32_t sum[4] = {0u, 0u, 0u, 0u};  // of 0 * v: NaN if v is not finite
 #pragma unroll 1
-            for (int j = 0; j < steps; ++j) {
-                const int k = done + j;
-                // keys of each page that the row keeps; pages that some row of the warp does
-                uint32_t held = 0, any = 0;  // 8 bits a page
-                const int i0 = j * PP + half * HP;
-                const uint32_t *two = reinterpret_cast<const uint32_t *>(s_page + i0);
-#pragma unroll
-                for (int g2 = 0; g2 < HP; ++g2) {  // (entries past the last: page 0)
-                    const int page = (two[g2 / 2] >> (g2 % 2 * 16)) & 0xffff;
-                    const bool mine = live && i0 + g2 < n && (own[page >> 5] >> (page & 31)) & 1;
-                    const int keep = mine ? min(max(limit - page * BS, 0), BS) : 0;
-                    held |= (uint32_t)keep << (8 * g2);
-                    any |= (keep > 0 ? 1u << g2 : 0u) | (keep > 0 && keep < BS ? 256u : 0u);
-                }
-                any = __reduce_or_sync(0xffffffffu, any);
-                const bool part = any & 256u;
-                if (!__all_sync(0xffffffffu, wait(kSFull, k & 1))) {
-                    ok = false;
-                    break;
-                }
-                tc::fence_after_sync();
-                // 16 keys at a time, those of pages that some row of the warp keeps.  (Rolled
-                // loops: code that is not in the instruction cache costs more than they do.)
-                constexpr int KP = BS / 16;
-                const uint32_t colH = colS + lanes + half * 64;
-                auto load_scores = [&](int c, uint32_t (&s)[16]) {
-                    tc::ld_32x32b_x16(colH + c * 16, s);
-                    const int keep = (int)((held >> (8 * (c / KP))) & 255u) - c % KP * 16;
-                    tc::wait_ld();
-                    if (part)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (e >= keep) s[e] = 0xff800000u;
-                    return keep > 0;
-                };
-                float mx = kNegInf;
+                for (int j = 0; j < steps; ++j) {
+                    const int k = done + j, m = min(PP, n - j * PP);
+                    if (!__all_sync(0xffffffffu, wait(kVFull, k & 1))) break;
+                    // keys of the step that the request has (only its last page can end inside)
+                    const int end = (m - 1) * BS + min(BS, total - (int)s_page[j * PP + m - 1] * BS);
+                    uint4 *v = reinterpret_cast<uint4 *>(smem + kOffV) + lane;
+                    if (end < kKeys) {
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    if (!((any >> (c / KP)) & 1u)) continue;
-                    uint32_t s[16];
-                    const bool mine = load_scores(c, s);
-                    float top = kNegInf;
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2)
-                        top = fmax3(top, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-                    if (mine) mx = fmaxf(mx, top);
-                }
-                mx *= scale;
-                s_max[half][row] = mx;
-                pair_sync();
-                mx = fmaxf(mx, s_max[half ^ 1][row]);
-                if (__any_sync(0xffffffffu, mx > ref + kGrow || (ref == kNegInf && mx > kNegInf))) {
-                    const float next = fmaxf(ref, mx);
-                    const float a = next == kNegInf ? 1.f : fast_exp2(ref - next);
-                    l *= a;
-                    if (j > 0) {  // (ok: the next product is issued after this warp's P)
-                        if (!__all_sync(0xffffffffu, wait(kODone, (k - 1) & 1))) {
-                            ok = false;
-                            break;
-                        }
-                        tc::fence_after_sync();
-#pragma unroll 1
-                        for (int c = half * 64; c < half * 64 + 64; c += 32) {
-                            uint32_t o[32];
-                            tc::ld_32x32b_x32(colO + lanes + c, o);
-                            tc::wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-                            tc::st_32x32b_x32(colO + lanes + c, o);
-                        }
-                        tc::wait_st();
+                        for (int i = lane; i < kKeys * 16; i += 32)  // (8 chunks a row, two halves)
+                            if (((i >> 3) & (kKeys - 1)) >= end) v[i - lane] = make_uint4(0u, 0u, 0u, 0u);
+                        fence_proxy_async_smem();
+                        __syncwarp();
                     }
-                    ref = next;
-                }
-                const float sub = ref == kNegInf ? 0.f : ref;
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t w[8];
-                    if ((any >> (c / KP)) & 1u) {
+                    for (int i0 = 0; i0 < kKeys * 16; i0 += 8 * 32) {
+                        uint4 x[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = v[i0 + 32 * i];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            sum[0] = zero_times(x[i].x, sum[0]);
+                            sum[1] = zero_times(x[i].y, sum[1]);
+                            sum[2] = zero_times(x[i].z, sum[2]);
+                            sum[3] = zero_times(x[i].w, sum[3]);
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kVReady));
+                }
+                if ((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7fff7fffu) s_bad = 1;
+            } else {
+                // ------------------------------------------------ softmax, thread = row
+                constexpr int HP = PP / 2;  // pages of a half
+                const int limit = live ? L + j0 - page0 * BS : 0;
+                const uint32_t *own = s_own + (live ? j0 : 0) * p.words;
+                const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
+#pragma unroll 1
+                for (int j = 0; j < steps; ++j) {
+                    const int k = done + j;
+                    // keys of each page that the row keeps; pages that some row of the warp does
+                    uint32_t held = 0, any = 0;  // 8 bits a page
+                    const int i0 = j * PP + half * HP;
+                    const uint32_t *two = reinterpret_cast<const uint32_t *>(s_page + i0);
+#pragma unroll
+                    for (int g2 = 0; g2 < HP; ++g2) {  // (entries past the last: page 0)
+                        const int page = (two[g2 / 2] >> (g2 % 2 * 16)) & 0xffff;
+                        const bool mine = live && i0 + g2 < n && (own[page >> 5] >> (page & 31)) & 1;
+                        const int keep = mine ? min(max(limit - page * BS, 0), BS) : 0;
+                        held |= (uint32_t)keep << (8 * g2);
+                        any |= (keep > 0 ? 1u << g2 : 0u) | (keep > 0 && keep < BS ? 256u : 0u);
+                    }
+                    any = __reduce_or_sync(0xffffffffu, any);
+                    const bool part = any & 256u;
+                    if (!__all_sync(0xffffffffu, wait(kSFull, k & 1))) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after_sync();
+                    // 16 keys at a time, those of pages that some row of the warp keeps.  (Rolled
+                    // loops: code that is not in the instruction cache costs more than they do.)
+                    constexpr int KP = BS / 16;
+                    const uint32_t colH = colS + lanes + half * 64;
+                    auto load_scores = [&](int c, uint32_t (&s)[16]) {
+                        tc::ld_32x32b_x16(colH + c * 16, s);
+                        const int keep = (int)((held >> (8 * (c / KP))) & 255u) - c % KP * 16;
+                        tc::wait_ld();
+                        if (part)
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (e >= keep) s[e] = 0xff800000u;
+                        return keep > 0;
+                    };
+                    float mx = kNegInf;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        if (!((any >> (c / KP)) & 1u)) continue;
                         uint32_t s[16];
                         const bool mine = load_scores(c, s);
-                        float sum[2] = {0.f, 0.f};
-                        const uint32_t all = mine ? 0xffffffffu : 0u;
+                        float top = kNegInf;
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const float x = fast_exp2(fmaf(__uint_as_float(s[e]), scale, -sub));
-                            const float y = fast_exp2(fmaf(__uint_as_float(s[e + 1]), scale, -sub));
-                            sum[0] += x;
-                            sum[1] += y;
-                            w[e / 2] = pack_bf16(x, y) & all;
-                        }
-                        if (mine) l += sum[0] + sum[1];
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) w[e] = 0u;
+                        for (int e = 0; e < 16; e += 2)
+                            top = fmax3(top, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                        if (mine) mx = fmaxf(mx, top);
                     }
-                    tc::st_32x32b_x8(colH + c * 8, w);
+                    mx *= scale;
+                    s_max[half][row] = mx;
+                    pair_sync();
+                    mx = fmaxf(mx, s_max[half ^ 1][row]);
+                    if (__any_sync(0xffffffffu, mx > ref + kGrow || (ref == kNegInf && mx > kNegInf))) {
+                        const float next = fmaxf(ref, mx);
+                        const float a = next == kNegInf ? 1.f : fast_exp2(ref - next);
+                        l *= a;
+                        if (before + j > 0) {  // (ok: the next product is issued after this warp's P)
+                            if (!__all_sync(0xffffffffu, wait(kODone, (k - 1) & 1))) {
+                                ok = false;
+                                break;
+                            }
+                            tc::fence_after_sync();
+#pragma unroll 1
+                            for (int c = half * 64; c < half * 64 + 64; c += 32) {
+                                uint32_t o[32];
+                                tc::ld_32x32b_x32(colO + lanes + c, o);
+                                tc::wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                                tc::st_32x32b_x32(colO + lanes + c, o);
+                            }
+                            tc::wait_st();
+                        }
+                        ref = next;
+                    }
+                    const float sub = ref == kNegInf ? 0.f : ref;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t w[8];
+                        if ((any >> (c / KP)) & 1u) {
+                            uint32_t s[16];
+                            const bool mine = load_scores(c, s);
+                            float sum[2] = {0.f, 0.f};
+                            const uint32_t all = mine ? 0xffffffffu : 0u;
+#pragma unroll
+                            for (int e = 0; e < 16; e += 2) {
+                                const float x = fast_exp2(fmaf(__uint_as_float(s[e]), scale, -sub));
+                                const float y = fast_exp2(fmaf(__uint_as_float(s[e + 1]), scale, -sub));
+                                sum[0] += x;
+                                sum[1] += y;
+                                w[e / 2] = pack_bf16(x, y) & all;
+                            }
+                            if (mine) l += sum[0] + sum[1];
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) w[e] = 0u;
+                        }
+                        tc::st_32x32b_x8(colH + c * 8, w);
+                    }
+                    tc::wait_st();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kPFull));
                 }
-                tc::wait_st();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kPFull));
             }
+            before += steps;
+            done += steps;
+            tc::fence_before_sync();
+            __syncthreads();
+            tc::fence_after_sync();
+        }
+        if (warp < kSoft) {
             // ------------------------------------------------ the row's output
-            if (steps > 0 && ok) ok = __all_sync(0xffffffffu, wait(kODone, (done + steps - 1) & 1));
+            if (before > 0 && ok) ok = __all_sync(0xffffffffu, wait(kODone, (done - 1) & 1));
             tc::fence_after_sync();
             s_max[half][row] = l;
             pair_sync();
@@ -498,14 +514,14 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
 #pragma unroll 1
             for (int c = half * 64; c < min(Dh, half * 64 + 64); c += 16) {
                 uint32_t o[16];
-                if (steps > 0) {
+                if (before > 0) {
                     tc::ld_32x32b_x16(colO + lanes + c, o);
                     tc::wait_ld();
                 }
                 uint32_t w[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    w[e] = steps > 0 ? pack_bf16(__uint_as_float(o[2 * e]) * mul,
+                    w[e] = before > 0 ? pack_bf16(__uint_as_float(o[2 * e]) * mul,
                                                  __uint_as_float(o[2 * e + 1]) * mul)
                                      : 0u;
                 if (live) {
@@ -515,7 +531,6 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
             }
             tc::fence_before_sync();
         }
-        done += steps;
         __syncthreads();
         tc::fence_after_sync();
         if (s_bad && !s_dead) {  // all rows again, by themselves
@@ -533,13 +548,15 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
 template <int BS>
 cudaError_t launch_bs(SparseParams p, bool &fits, const void *k, const void *v,
                       const CUtensorMap *tk, const CUtensorMap *tv, cudaStream_t stream) {
-    const int64_t queries = kRows >> p.group_shift, lists = queries * p.top_k;
-    p.cap = (int)(lists < p.r.max_blocks_per_seq ? lists : p.r.max_blocks_per_seq);
-    p.words = p.r.max_blocks_per_seq / 32 + 1;
-    const int64_t smem = 1024 + kOffList + (p.cap + kKeys / BS + 2) * 2LL +
-                         ((queries + 2) * p.words + 1) * 4LL;
+    const int queries = kRows >> p.group_shift;
+    // Words of the bitmaps, 32 pages each, of a window that leaves room for two CTAs: for
+    // 32 queries 70 words, 2240 pages (of a table of 4096: 185 us in one CTA per SM and
+    // one window, 117 so).
+    const int a_word = (queries + 2) * 4 + 32 * 2;
+    p.words = min(p.r.max_blocks_per_seq / 32 + 1, kListBytes / a_word);
+    const int64_t smem = 1024 + kOffList + (kKeys / BS + 2) * 2 + 4 + (int64_t)p.words * a_word;
     const int64_t grid = row_tiles(p.r, (int)queries) * p.r.num_kv_heads;
-    fits = smem <= 224 * 1024 && grid <= 0x7fffffff && p.r.max_blocks_per_seq <= 65536;
+    fits = grid <= 0x7fffffff;
     if (!fits) return cudaErrorNotSupported;
     auto kern = sparse_tile_kernel<BS>;
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), (int)smem);

@@ -181,6 +181,14 @@ def test_wide_lists_and_tables(queries, hq):
         R.assert_within(o, ref, R.out_bound(ref, absv, smax, 64, 2.0 ** -8), "out")
 
 
+@pytest.mark.parametrize("top_k", [2, 40])
+@pytest.mark.parametrize("kind", ["last", "random"])
+@pytest.mark.parametrize("hq,hkv,bs,n", [(2, 2, 16, 1700), (1, 1, 32, 1500), (4, 1, 16, 4600)])
+def test_chunks_of_long_contexts(hq, hkv, bs, n, kind, top_k):
+    """More pages than a tile's bitmaps hold at a time, windows without a page."""
+    run([bs * n + 3, 700], [33, 35], hq, hkv, 64, bs, kind=kind, top_k=top_k, sink=True, extra=2)
+
+
 @pytest.mark.parametrize("pool", [0, 1])
 @pytest.mark.parametrize("value", ["nan", "inf", "-inf"])
 def test_chunk_with_a_key_that_is_not_finite(pool, value):
