@@ -22,8 +22,9 @@
 // f16 values; pages whose scales lie further apart go by fp32).
 //
 // Measured (8 kv heads of 128): 64 tokens 2.9 us; 16K bf16 tokens in 8 prompts 7.0 us;
-// 88K tokens of 8-bit pages in 13 prompts 24 us with their 97 MB in L2 (14.4 at HBM's
-// rate), 36 us without: then its loads wait for one another page by page, issue at 50%.
+// 88K tokens of 8-bit pages in 13 prompts 21.6 us (97 MB, 14.4 at HBM's rate; 24.4 with
+// the two CTAs per SM that unbounded registers leave room for).  Issue at 50%, DRAM at 45%:
+// a warp loads a page, then works on it.
 #include <cuda_fp16.h>
 
 #include "pkv_sparse.cuh"
@@ -34,6 +35,8 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
+// Rounds of warps before a warp takes more kv heads (88K 8-bit tokens: 5 and 8 21.6 us, 12
+// 25; 2, with two CTAs per SM, 33 where 8 took 24.4).
 constexpr int kRounds = 8;
 
 template <bool FP8>
@@ -108,7 +111,7 @@ __device__ __noinline__ void fp32_bounds(const char *rows, int64_t row_bytes, co
 
 // SPAN: lanes of a row (16 bytes each), a power of two; the last ones may be idle.
 template <bool FP8, int BS, int SPAN>
-__global__ void __launch_bounds__(kThreads) page_bounds_kernel(const BoundsParams p) {
+__global__ void __launch_bounds__(kThreads, 3) page_bounds_kernel(const BoundsParams p) {
     constexpr int V = FP8 ? 16 : 8;     // channels of a lane
     constexpr int P = V / 2;            // pairs
     constexpr int STEP = 32 / SPAN;     // rows side by side
