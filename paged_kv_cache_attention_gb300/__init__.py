@@ -1426,7 +1426,7 @@ def paged_sparse_attention(q, k_cache, v_cache, block_table, cache_seqlens, page
     total_q, Hq, B, max_blocks = _rows(q, desc.head_dim, block_table, cache_seqlens,
                                        cu_seq_lens_q, dev)
     shape = pages.shape
-    top_k = shape[-1]
+    top_k = shape[-1] if shape else 0
     if not (pages.dtype is ty.i32 and shape == (total_q, desc.num_kv_heads, top_k)
             and pages.get_device() == dev and pages.is_contiguous()):
         _arg("pages", pages, ty.i32, 3, dev)

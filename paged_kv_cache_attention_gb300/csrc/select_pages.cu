@@ -828,11 +828,13 @@ cudaError_t launch_as(SelectParams p, bool &fits, cudaStream_t stream) {
     auto kern = select_pages_kernel<NCH, NT, GP, W>;
     const int64_t units = (S::QT > 1 ? row_tiles(p.r, S::QT) : p.r.rows) * p.r.num_kv_heads;
     const int n = (p.r.max_seqlen + p.block_size - 1) >> p.bs_shift;
-    // CTAs per tile: more while they have an SM each (8 kv heads of 8 contexts of 100K
-    // tokens: 4 CTAs 26 us, 1 43, 8 39) and 512 pages to share out, or the scores do not fit
+    // CTAs per tile: several if the scores do not fit; of one query while they have an SM
+    // each (8 kv heads of 8 contexts of 100K tokens: 4 CTAs 26 us, 1 43, 8 39) and 512 pages
+    // to share out.  (Of several queries the choice in a cluster costs more than it saves:
+    // 64 queries of 32K tokens, 8 kv heads: 1 CTA 32 us, 2 33, 4 115.)
     int c = 1;
     auto cap = [&] { return ((n + c - 1) / c + S::STEP - 1) / S::STEP * S::STEP; };
-    while (c < 16 && ((units * c <= device_sm_count() && n / c >= 512) ||
+    while (c < 16 && ((S::QT == 1 && units * c <= device_sm_count() && n / c >= 512) ||
                       smem_bytes<S>(cap()) > kMaxSmem))
         c *= 2;
     fits = smem_bytes<S>(cap()) <= kMaxSmem && units * c <= 0x7fffffff;
@@ -858,10 +860,13 @@ template <int NCH>
 cudaError_t launch_n(const SelectParams &p, cudaStream_t stream) {
     bool fits = false;
     const int G = p.r.group;
-    // Tiles of queries where requests have several, 4 on average (16 requests of 24K tokens,
-    // 8 kv heads of 4: 4 queries 41 us, 40 one at a time; 8 queries 44 and 65; 64 140 and
-    // 411); long contexts whose scores do not fit go on with one query at a time.
-    if (p.r.cu_q && p.r.rows >= 4LL * p.r.batch) {
+    // Tiles of queries where requests have several, 4 on average, and one at a time would
+    // take all SMs a few rounds (24K tokens, 8 kv heads of 4, 16 requests of 4 queries: 41 us,
+    // 40 one at a time; of 8 44 and 65, of 64 140 and 411; 32K tokens, 1 request of 8 queries:
+    // 32 and 16, of 32 32 and 29, of 64 32 and 43); long contexts whose scores do not fit go
+    // on with one query at a time.
+    if (p.r.cu_q && p.r.rows >= 4LL * p.r.batch &&
+        (int64_t)p.r.rows * p.r.num_kv_heads > 3LL * device_sm_count()) {
         const cudaError_t e = G == 1   ? launch_tiles<NCH, 1, 1>(p, fits, stream)
                               : G == 2 ? launch_tiles<NCH, 2, 2>(p, fits, stream)
                               : G <= 4 ? launch_tiles<NCH, 4, 4>(p, fits, stream)

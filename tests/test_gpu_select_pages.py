@@ -76,12 +76,18 @@ def test_sizes_of_lists(top_k):
     check(c, top_k, first=0)
 
 
+# Rows of no request: enough of them that the queries before them are taken in tiles
+# (few rows are taken one at a time).
+MANY = 500
+
+
+@pytest.mark.parametrize("extra", [5, MANY])
 @pytest.mark.parametrize("queries,lens", [([3, 1, 8, 5], [3, 700, 1200, 9]), ([40], [2500]),
                                           ([0, 2, 0, 17, 1], [30, 900, 0, 17, 2000])])
-def test_chunks(queries, lens):
+def test_chunks(queries, lens, extra):
     """Rows of a chunk, each up to its own position; rows of no request stay."""
     c = make(lens, queries, 8, 2, 64, 16)
-    check(c, 12, recent=2, chunk=True, extra=5)
+    check(c, 12, recent=2, chunk=True, extra=extra)
 
 
 @pytest.mark.parametrize("hq,hkv,d,bs", [(2, 2, 64, 16), (4, 2, 80, 32), (6, 2, 128, 16),
@@ -91,8 +97,9 @@ def test_tiles_of_queries(hq, hkv, d, bs):
     """Every width of a group; tiles that hold the ends of requests, and rows of which
     some take all their pages."""
     c = make([37 * bs + 5, 3, 200 * bs, 21 * bs + 1], [11, 3, 19, 9], hq, hkv, d, bs)
+    check(c, 20, recent=2, extra=MANY)
+    check(c, 1, first=0, extra=MANY)
     check(c, 20, recent=2, extra=2)
-    check(c, 1, first=0)
 
 
 @pytest.mark.parametrize("batch", [256, 257])
@@ -105,17 +112,24 @@ def test_chunks_of_many_requests(batch):
     check(make(lens, queries, 4, 2, 64, 16), 6, chunk=True, extra=3)
 
 
+@pytest.mark.parametrize("extra", [0, MANY])
+@pytest.mark.parametrize("hq", [1, 2, 4, 8, 16])
 @pytest.mark.parametrize("n", [3000, 70000, 300000])
-def test_tiles_over_long_contexts(n):
+def test_tiles_over_long_contexts(n, hq, extra):
     """Clusters share a tile's pages; one query at a time where the scores do not fit."""
-    check(make([n], [5], 4, 1, 64, 16, spread=3), 64, recent=3)
-    check(make([n], [4], 1, 1, 64, 16, spread=3), 200)
+    check(make([n], [5], hq, 1, 64, 16, spread=3), 64, recent=3, extra=extra)
+    check(make([n], [4], hq, 1, 64, 16, spread=3), 200, extra=extra)
 
 
+def test_tiles_over_the_longest_contexts():
+    check(make([16 * 65536 + 3, 40], [5, 11], 4, 1, 64, 16, spread=3), 64, recent=3, extra=MANY)
+
+
+@pytest.mark.parametrize("extra", [0, MANY])
 @pytest.mark.parametrize("queries,lens", [([6, 4], [3, 100]), ([5], [0])])
-def test_rows_before_the_first_position(queries, lens):
+def test_rows_before_the_first_position(queries, lens, extra):
     """More queries than keys: rows without a key have empty lists."""
-    check(make(lens, queries, 4, 2, 64, 16), 3, chunk=True)
+    check(make(lens, queries, 4, 2, 64, 16), 3, chunk=True, extra=extra)
 
 
 @pytest.mark.parametrize("n", [65536 * 16 + 9, 300000])
