@@ -193,6 +193,54 @@ def test_scales_far_apart():
         c["q"] = keep
 
 
+@pytest.mark.parametrize("hq", [1, 2, 8, 16])
+def test_values_in_tiles(hq):
+    """Scales far apart, ties, scores of 0 and values that are not finite, for several
+    queries at a time."""
+    c = make([16 * 300, 16 * 50 + 3], [11, 5], hq, 1, 64, 16)
+    kept = c["q"], c["codes"], c["byte"]
+    g = torch.Generator().manual_seed(6)
+    size = torch.randint(-130, 127, (16, hq, 1), generator=g).float()
+    c["q"] = (kept[0].float().clamp(-1, 1) * torch.exp2(size)).to(BF16)
+    for lo, hi in ((1, 250), (1, 30), (200, 250), (120, 124)):
+        c["byte"] = torch.randint(lo, hi, c["byte"].shape, generator=g).to(U8)
+        check(c, 40, extra=MANY)
+    c["q"], c["byte"] = kept[0].clone(), kept[2].clone()
+    bad = torch.rand(c["byte"].shape, generator=g) < 0.05
+    c["byte"][bad] = 255
+    check(c, 30, extra=MANY)
+    check(c, 3, extra=MANY)
+    c["q"][3, 0, 7] = float("nan")
+    c["q"][5] = float("inf")
+    c["q"][6, :, 1] = float("-inf")
+    check(c, 30, extra=MANY)
+    c["q"], c["byte"] = kept[0], torch.full_like(c["byte"], 120)
+    c["codes"] = kept[1].clone()
+    c["codes"][:] = c["codes"][:1]
+    check(c, 40, extra=MANY)                  # all alike
+    c["byte"] = torch.where(torch.rand(c["byte"].shape, generator=g) < 0.05, 121, 120).to(U8)
+    check(c, 40, extra=MANY)                  # two values
+    c["codes"].zero_()
+    check(c, 40, first=0, extra=MANY)
+
+
+def test_page_ids_out_of_range_in_tiles():
+    c = make([16 * 90], [9], 4, 1, 64, 16)
+    w = want(c, 20, 1, 1)
+    lost = [p for p in range(1, 85) if p in w[4, 0].tolist()][3]
+    table = c["table"].clone()
+    table[0, lost] = c["codes"].shape[0]
+    err = torch.zeros(1, dtype=I32, device=DEV)
+    q = torch.cat([c["q"], torch.zeros(MANY, 4, 64, dtype=BF16)])
+    cu, lens = (torch.tensor(x, dtype=I32, device=DEV) for x in ([0, 9], [16 * 90]))
+    got = pkv.select_pages(q.to(DEV), c["codes"].to(DEV), c["byte"].to(DEV), table.to(DEV), lens, 16 * 90,
+                           20, 16, cu_seq_lens_q=cu, dev_error=err)
+    assert pkv.get_device_error(err) == pkv.DEVERR_BLOCK_ID
+    for t in range(9):
+        pages = got[t, 0].tolist()
+        assert lost not in pages and set(w[t, 0].tolist()) - {lost} <= set(pages)
+
+
 def test_zero_queries():
     c = make([16 * 100], [1], 4, 2, 64, 16)
     c["q"].zero_()
@@ -238,14 +286,15 @@ def test_page_ids_and_lengths_out_of_range():
     assert bool((got == -1).all())
 
 
-def test_offsets_that_are_none():
+@pytest.mark.parametrize("rows", [4, 4 + MANY])
+def test_offsets_that_are_none(rows):
     """Offsets that decrease or leave the rows: no row is written twice or read beyond."""
-    c = make([160, 160], [2, 2], 2, 1, 64, 16)
+    c = make([160, 160], [rows // 2, rows // 2], 2, 1, 64, 16)
     args = (c["q"].to(DEV), c["codes"].to(DEV), c["byte"].to(DEV), c["table"].to(DEV),
             torch.tensor(c["lens"], dtype=I32, device=DEV), 160, 4, 16)
-    for cu in ([2, 1, 4], [0, 9, 3], [3, 3, 3], [-5, 0, 90], [4, 2, 0]):
+    for cu in ([2, 1, rows], [0, rows + 5, 3], [3, 3, 3], [-5, 0, 900], [rows, 2, 0]):
         got = pkv.select_pages(*args, cu_seq_lens_q=torch.tensor(cu, dtype=I32, device=DEV),
-                               pages=torch.full((4, 1, 4), -9, dtype=I32, device=DEV))
+                               pages=torch.full((rows, 1, 4), -9, dtype=I32, device=DEV))
         assert bool(((got >= -1) & (got < 10) | (got == -9)).all())
 
 
