@@ -251,13 +251,14 @@ pkv_status pkv_paged_sparse_attention(void *out, const void *q, const void *k_ca
     if ((st = pool_map(&tk, k_cache, cache, rows)) != PKV_OK) return st;
     if ((st = pool_map(&tv, v_cache, cache, rows)) != PKV_OK) return st;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // Chunks: tiles of 128 rows, where requests have 8 queries and fill a quarter of a tile
-    // on average.  Of 16 requests, 8 kv heads, 1024 keys a query and no two lists alike (the
-    // less they differ, the better tiles do), in tiles and row by row: groups of 4 heads, 4
-    // queries 52 and 32 us, 8 69 and 62, 16 84 and 94, 64 117 and 289; of one, 32 queries
-    // 101 and 154; of 16, 4 queries 53 and 34.
+    // Chunks: tiles of 128 rows, where requests have 8 queries and fill a quarter of a tile on
+    // average and rows would take all SMs a few rounds.  In tiles and row by row, 8 kv heads,
+    // 1024 keys a query and no two lists alike (the less they differ, the better tiles
+    // do): 16 requests, groups of 4 heads, 4 queries 52 and 32 us, 8 69 and 62, 16 84 and
+    // 94, 64 117 and 289; groups of one, 32 queries 101 and 154; 1 request, 64 queries 67
+    // and 30, 128 68 and 61, 256 68 and 92.
     if (!fp8 && cu_seq_lens_q && total_q >= 8LL * batch &&
-        (int64_t)total_q * p.r.group >= 32LL * batch) {
+        (int64_t)total_q * p.r.group >= 32LL * batch && units > 12LL * device_sm_count()) {
         bool fits = false;
         const cudaError_t e =
             launch_sparse_tile(p, fits, cache.block_size, k_cache, v_cache, &tk, &tv, s);

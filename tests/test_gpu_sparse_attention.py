@@ -14,6 +14,11 @@ DEV = "cuda"
 BF16, I32 = torch.bfloat16, torch.int32
 
 
+# Rows of no request: enough of them that the queries before them are taken in tiles
+# (few rows are taken one at a time).
+MANY = 2000
+
+
 def lists(rows, hkv, top_k, bs, rng, kind):
     """Pages of every row and kv head: strictly ascending, then -1."""
     out = torch.full((len(rows), hkv, top_k), -1, dtype=I32)
@@ -103,16 +108,15 @@ def test_many_rows(fp8):
     run(lens, [1] * 130, 8, 4, 64, fp8=fp8, top_k=20, sink=True)
 
 
-@pytest.mark.parametrize("hq", [8, 32])
+@pytest.mark.parametrize("extra", [4, MANY])
 @pytest.mark.parametrize("layout,fp8", KINDS)
 @pytest.mark.parametrize("queries,lens", [([3, 1, 8, 5], [3, 300, 500, 9]), ([33], [500]),
                                           ([0, 2, 0, 17, 1], [30, 90, 0, 17, 200]),
                                           ([6, 4], [3, 100]), ([30, 1, 8, 13], [30, 300, 500, 50]),
                                           ([0, 20, 0, 47, 1], [30, 90, 0, 47, 200])])
-def test_chunks(layout, fp8, queries, lens, hq):
-    """Rows of a chunk, each up to its own position; rows of no request stay.  Few
-    queries are taken row by row, many in tiles."""
-    run(lens, queries, hq, 2, 64, 16, layout, fp8, top_k=9, sink=True, extra=4, chunk=True)
+def test_chunks(layout, fp8, queries, lens, extra):
+    """Rows of a chunk, each up to its own position; rows of no request stay."""
+    run(lens, queries, 8, 2, 64, 16, layout, fp8, top_k=9, sink=True, extra=extra, chunk=True)
 
 
 @pytest.mark.parametrize("kind", ["last", "random"])
@@ -122,7 +126,7 @@ def test_chunks(layout, fp8, queries, lens, hq):
 def test_tiles_of_queries(hq, hkv, d, bs, kind):
     """Every width of a group; tiles that hold the ends of requests."""
     run([17 * bs + 5, 3, 60 * bs, 11 * bs + 1], [21, 3, 37, 9], hq, hkv, d, bs, top_k=8, kind=kind,
-        sink=True, extra=3, layout="HND")
+        sink=True, extra=MANY, layout="HND")
 
 
 @pytest.mark.parametrize("most,hq", [(5, 4), (12, 8)])
@@ -133,10 +137,10 @@ def test_chunks_of_many_requests(batch, most, hq):
     lens = torch.randint(0, 60, (batch,), generator=g).tolist()
     queries = [min(n, most) if i % 9 else 0 for i, n in enumerate(lens)]
     queries[7] = lens[7] = 200
-    run(lens, queries, hq, 2, 64, top_k=3, chunk=True, extra=3)
+    run(lens, queries, hq, 2, 64, top_k=3, chunk=True, extra=MANY if most > 5 else 3)
 
 
-@pytest.mark.parametrize("n,hq", [(8, 2), (16, 8)])
+@pytest.mark.parametrize("n,hq", [(8, 2), (MANY, 4)])
 def test_offsets_that_are_none(n, hq):
     """Offsets that decrease or leave the rows: nothing outside is read or written."""
     pools, table, slots, _ = small()
@@ -145,7 +149,7 @@ def test_offsets_that_are_none(n, hq):
     pages = torch.arange(4, dtype=I32, device=DEV).expand(n, 1, 4).contiguous()
     two = torch.cat([table, table]).to(DEV)
     lens = torch.tensor([100, 100], dtype=I32, device=DEV)
-    for cu in ([2, 1, n], [0, 19, 3], [3, 3, 3], [-5, 0, 90], [n, 2, 0], [0, n // 2, n]):
+    for cu in ([2, 1, n], [0, n + 11, 3], [3, 3, 3], [-5, 0, 9000], [n, 2, 0], [0, n // 2, n]):
         out = torch.full((n, hq, 64), 7.0, dtype=BF16, device=DEV)
         pkv.paged_sparse_attention(q, kc, vc, two, lens, pages, out=out,
                                    cu_seq_lens_q=torch.tensor(cu, dtype=I32, device=DEV))
@@ -153,32 +157,33 @@ def test_offsets_that_are_none(n, hq):
     assert not bool((out == 7.0).any())
 
 
-@pytest.mark.parametrize("hq", [4, 16])
+@pytest.mark.parametrize("extra", [0, MANY])
 @pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
-def test_chunk_scales(scale, hq):
-    run([300, 33], [9, 7], hq, 2, 64, top_k=9, scale=scale, sink=True)
+def test_chunk_scales(scale, extra):
+    run([300, 33], [9, 7], 4, 2, 64, top_k=9, scale=scale, sink=True, extra=extra)
 
 
-@pytest.mark.parametrize("queries,hq", [([6, 4], 4), ([12, 8], 32)])
-def test_wide_lists_and_tables(queries, hq):
-    """Unions of hundreds of pages; a table too wide for them to be numbered."""
-    run([16 * 700 + 3], [9], 4, 1, 64, top_k=150)
+@pytest.mark.parametrize("extra", [0, MANY])
+def test_wide_lists_and_tables(extra):
+    """Unions of hundreds of pages; tables much wider than their requests."""
+    run([16 * 700 + 3], [9], 4, 1, 64, top_k=150, extra=extra)
     g = torch.Generator().manual_seed(9)
     pools = R.Pools(40, 16, 2, 64, "NHD", False, g)
     narrow, slots = R.paged([300, 200], 16, 40, g)
     kc, vc, _, _ = pools.device(DEV)
-    q = torch.randn(sum(queries), hq, 64, generator=g).to(BF16).to(DEV)
+    q = torch.randn(10 + extra, 4, 64, generator=g).to(BF16).to(DEV)
     lens = torch.tensor([300, 200], dtype=I32, device=DEV)
-    cu = torch.tensor([0, queries[0], sum(queries)], dtype=I32, device=DEV)
-    rows = S.rows_of(queries, [300, 200])
-    pages = lists(rows, 2, 5, 16, random.Random(9), "last").to(DEV)
+    cu = torch.tensor([0, 6, 10], dtype=I32, device=DEV)
+    rows = S.rows_of([6, 4], [300, 200])
+    pages = lists(rows, 2, 5, 16, random.Random(9), "last")
+    padded = torch.cat([pages, torch.zeros(extra, 2, 5, dtype=I32)]).to(DEV)
     wide = torch.full((2, 700000), -1, dtype=I32)
     wide[:, :narrow.shape[1]] = narrow
-    outs = [pkv.paged_sparse_attention(q, kc, vc, t.to(DEV), lens, pages, cu_seq_lens_q=cu)
+    outs = [pkv.paged_sparse_attention(q, kc, vc, t.to(DEV), lens, padded, cu_seq_lens_q=cu)
             for t in (narrow, wide)]
-    ref, _, absv, smax, _ = S.attend_lists(q.cpu(), pools, slots, rows, pages.cpu(), 16, 0.125, None)
+    ref, _, absv, smax, _ = S.attend_lists(q[:10].cpu(), pools, slots, rows, pages, 16, 0.125, None)
     for o in outs:
-        R.assert_within(o, ref, R.out_bound(ref, absv, smax, 64, 2.0 ** -8), "out")
+        R.assert_within(o[:10], ref, R.out_bound(ref, absv, smax, 64, 2.0 ** -8), "out")
 
 
 @pytest.mark.parametrize("top_k", [2, 40])
@@ -186,19 +191,21 @@ def test_wide_lists_and_tables(queries, hq):
 @pytest.mark.parametrize("hq,hkv,bs,n", [(2, 2, 16, 1700), (1, 1, 32, 1500), (4, 1, 16, 4600)])
 def test_chunks_of_long_contexts(hq, hkv, bs, n, kind, top_k):
     """More pages than a tile's bitmaps hold at a time, windows without a page."""
-    run([bs * n + 3, 700], [33, 35], hq, hkv, 64, bs, kind=kind, top_k=top_k, sink=True, extra=2)
+    run([bs * n + 3, 700], [33, 35], hq, hkv, 64, bs, kind=kind, top_k=top_k, sink=True, extra=MANY)
 
 
+@pytest.mark.parametrize("extra", [0, MANY])
 @pytest.mark.parametrize("pool", [0, 1])
 @pytest.mark.parametrize("value", ["nan", "inf", "-inf"])
-def test_chunk_with_a_key_that_is_not_finite(pool, value):
+def test_chunk_with_a_key_that_is_not_finite(pool, value, extra):
     """It reaches the queries that keep it, and not those that share its page's loads:
     a page of some, a page of all of which some see only a part, a page of all."""
     def edit(pools, slots):
         for at in (slots[0][37], slots[0][295], slots[1][3]):
             pools.rows[pool][at // 16, 0, at % 16, 5] = float(value)
 
-    out, lse, ref, rl, bound, lb = run([300, 40], [16, 8], 4, 1, 64, top_k=9, edit=edit, seed=7)
+    out, lse, ref, rl, bound, lb = run([300, 40], [16, 8], 4, 1, 64, top_k=9, edit=edit, seed=7,
+                                       extra=extra)
     fin = torch.isfinite(ref)
     assert 0 < int(fin.sum()) < fin.numel()
     assert torch.equal(torch.isnan(out), torch.isnan(ref))
@@ -214,20 +221,20 @@ def test_chunk_with_a_key_that_is_not_finite(pool, value):
     assert float(off.max()) <= 0
 
 
-@pytest.mark.parametrize("n,hq", [(6, 2), (12, 8)])
-def test_chunk_lists_that_end_early(n, hq):
+@pytest.mark.parametrize("extra", [0, MANY])
+def test_chunk_lists_that_end_early(extra):
     """Lists of a chunk with errors and entries behind their end; pages out of the pool."""
     pools, table, slots, _ = small()
     g = torch.Generator().manual_seed(11)
-    q = torch.randn(n, hq, 64, generator=g).to(BF16)
+    q = torch.randn(6 + extra, 2, 64, generator=g).to(BF16)
     given = [[1, 3, 5, -1], [1, -1, 3, 5], [1, 3, 3, 5], [3, 1, 4, 5], [1, 3, 7, 8], [0, 2, 4, 6]]
     held = [[1, 3, 5, -1], [1, -1, -1, -1], [1, 3, -1, -1], [3, -1, -1, -1], [1, 3, -1, -1],
             [0, 2, -1, -1]]
-    if n == 12:
-        given, held = ([*x[:5], *x[:5], x[0], x[5]] for x in (given, held))
+    padded = torch.zeros(6 + extra, 1, 4, dtype=I32)
+    padded[:6, 0] = torch.tensor(given)
     kc, vc, _, _ = pools.device(DEV)
     err = torch.zeros(1, dtype=I32, device=DEV)
-    cu, lens = (torch.tensor(x, dtype=I32, device=DEV) for x in ([0, n], [100]))
+    cu, lens = (torch.tensor(x, dtype=I32, device=DEV) for x in ([0, 6], [100]))
     for broken, bits in ((False, pkv.DEVERR_BLOCK_ID), (True, pkv.DEVERR_BLOCK_ID)):
         t = table.clone()
         want = [list(x) for x in held]
@@ -237,13 +244,12 @@ def test_chunk_lists_that_end_early(n, hq):
         else:
             want[-1] = [0, 2, 4, 6]
         out = pkv.paged_sparse_attention(q.to(DEV), kc, vc, t.to(DEV), lens,
-                                         torch.tensor(given, dtype=I32, device=DEV).view(n, 1, 4),
-                                         cu_seq_lens_q=cu, dev_error=err)
+                                         padded.to(DEV), cu_seq_lens_q=cu, dev_error=err)
         assert pkv.get_device_error(err, clear=True) == bits
-        pages = torch.tensor(want, dtype=I32).view(n, 1, 4)
-        ref, _, absv, smax, _ = S.attend_lists(q, pools, slots, S.rows_of([n], [100]), pages, 16, 0.125,
-                                               None)
-        R.assert_within(out, ref, R.out_bound(ref, absv, smax, 64, 2.0 ** -8), "out")
+        pages = torch.tensor(want, dtype=I32).view(6, 1, 4)
+        ref, _, absv, smax, _ = S.attend_lists(q[:6], pools, slots, S.rows_of([6], [100]), pages, 16,
+                                               0.125, None)
+        R.assert_within(out[:6], ref, R.out_bound(ref, absv, smax, 64, 2.0 ** -8), "out")
 
 
 @pytest.mark.parametrize("fp8", [False, True])
