@@ -13,6 +13,7 @@
 
 #include "pkv_fp8.h"
 #include "pkv_internal.h"
+#include "pkv_sparse.h"
 
 namespace pkv {
 

@@ -172,8 +172,4 @@ int device_sm_count();
 // current device, done once per (kernel, device, size) and remembered.
 cudaError_t ensure_dynamic_smem(const void *kernel, int bytes);
 
-// Lets `kernel` be launched with clusters of up to 16 CTAs on the current device,
-// once per (kernel, device).
-cudaError_t ensure_wide_clusters(const void *kernel);
-
 }  // namespace pkv

@@ -90,6 +90,10 @@ cudaError_t launch_sparse_tile(const SparseParams &p, bool &fits, int block_size
 cudaError_t launch_sparse_fp8(const SparseParams &p, int block_size, const CUtensorMap *tmap_k,
                               const CUtensorMap *tmap_v, cudaStream_t stream);
 
+// Lets `kernel` be launched with clusters of up to 16 CTAs on the current device,
+// once per (kernel, device).
+cudaError_t ensure_wide_clusters(const void *kernel);
+
 // Launch with clusters of `cluster` CTAs along x (and launch_pdl's attribute).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned grid, int cluster, unsigned block,

@@ -848,6 +848,8 @@ cudaError_t launch_as(SelectParams p, bool &fits, cudaStream_t stream) {
     return launch_cluster(kern, (unsigned)(units * c), c, S::WARPS * 32, (size_t)smem, stream, p);
 }
 
+// Eight warps while two CTAs fit an SM, else 16 in one (934 queries of 26K tokens: 132 us
+// and 163).
 template <int NCH, int NT, int GP>
 cudaError_t launch_tiles(const SelectParams &p, bool &fits, cudaStream_t stream) {
     const int n = (p.r.max_seqlen + p.block_size - 1) >> p.bs_shift;

@@ -21,7 +21,7 @@
 //
 // Two CTAs share an SM, so that one's softmax runs beside the other's products and loads.
 // Eight softmax warps, of two halves of the keys: 181 us where four took 318 (890 queries
-// of 1024 keys each, 8 kv heads of 4, D = 128).  Now 117 us, row by row 255.  A step takes
+// of 1024 keys each, 8 kv heads of 4, D = 128).  Now 114 us, row by row 255.  A step takes
 // 5000 clocks, 2950 with two CTAs: 2600 of softmax (every score is looked at, an eighth
 // is a row's own: 15 GFLOP of products that count, 8 us, in eight times as many), the
 // rest the way from products to softmax and back.  Tiles are of one request each (rows
@@ -214,7 +214,17 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
         const int quarter = warp & 3, half = warp >> 2;
         const int row = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(quarter + 1) : "memory"); };
+        // (whether x holds in either: a warp that gave up leaves together with its partner)
+        auto pair_any = [&](bool x) {
+            uint32_t r;
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+                "bar.red.or.pred p, %2, 64, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(r)
+                : "r"((uint32_t)x), "r"(quarter + 1)
+                : "memory");
+            return r != 0;
+        };
         const int j0 = row >> p.group_shift, h = row & ((1 << p.group_shift) - 1);
         const bool live = j0 < nq && h < G;
         float ref = kNegInf, l = 0.f;
@@ -402,10 +412,7 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
                     }
                     any = __reduce_or_sync(0xffffffffu, any);
                     const bool part = any & 256u;
-                    if (!__all_sync(0xffffffffu, wait(kSFull, k & 1))) {
-                        ok = false;
-                        break;
-                    }
+                    ok = ok && __all_sync(0xffffffffu, wait(kSFull, k & 1));
                     tc::fence_after_sync();
                     // 16 keys at a time, those of pages that some row of the warp keeps.  (Rolled
                     // loops: code that is not in the instruction cache costs more than they do.)
@@ -424,7 +431,7 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
                     float mx = kNegInf;
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
-                        if (!((any >> (c / KP)) & 1u)) continue;
+                        if (!ok || !((any >> (c / KP)) & 1u)) continue;
                         uint32_t s[16];
                         const bool mine = load_scores(c, s);
                         float top = kNegInf;
@@ -435,20 +442,20 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
                     }
                     mx *= scale;
                     s_max[half][row] = mx;
-                    pair_sync();
+                    if (pair_any(!ok)) {
+                        ok = false;
+                        break;
+                    }
                     mx = fmaxf(mx, s_max[half ^ 1][row]);
                     if (__any_sync(0xffffffffu, mx > ref + kGrow || (ref == kNegInf && mx > kNegInf))) {
                         const float next = fmaxf(ref, mx);
                         const float a = next == kNegInf ? 1.f : fast_exp2(ref - next);
                         l *= a;
                         if (before + j > 0) {  // (ok: the next product is issued after this warp's P)
-                            if (!__all_sync(0xffffffffu, wait(kODone, (k - 1) & 1))) {
-                                ok = false;
-                                break;
-                            }
+                            ok = __all_sync(0xffffffffu, wait(kODone, (k - 1) & 1));
                             tc::fence_after_sync();
 #pragma unroll 1
-                            for (int c = half * 64; c < half * 64 + 64; c += 32) {
+                            for (int c = half * 64; ok && c < half * 64 + 64; c += 32) {
                                 uint32_t o[32];
                                 tc::ld_32x32b_x32(colO + lanes + c, o);
                                 tc::wait_ld();
@@ -502,7 +509,7 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
             if (before > 0 && ok) ok = __all_sync(0xffffffffu, wait(kODone, (done - 1) & 1));
             tc::fence_after_sync();
             s_max[half][row] = l;
-            pair_sync();
+            pair_any(false);
             l += s_max[half ^ 1][row];
             const float sink = p.sink && live ? p.sink[g * G + h] * kLog2e : kNegInf;
             const float T = fmaxf(ref, sink), Ts = T == kNegInf ? 0.f : T;
