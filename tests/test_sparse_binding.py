@@ -186,6 +186,7 @@ REFUSALS = [
     (("sparse",), "pages", lambda: z(2, HKV, 5, dtype=I32)),
     (("sparse",), "pages", lambda: z(3, HKV, 5, dtype=I64)),
     (("sparse",), "pages", lambda: z(3, HKV, 10, dtype=I32)[:, :, ::2]),
+    (("sparse",), "pages", lambda: z(3, dtype=I32)[0]),
     (("sparse",), "v_cache", lambda: z(NB, BS, HKV, 2 * D)),
     (("sparse",), "k_cache", lambda: _pool(dtype=E4M3)),
     (("sparse",), "k_scale", lambda: z(NB, HKV, BS, dtype=U8)),
