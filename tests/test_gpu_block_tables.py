@@ -165,6 +165,27 @@ def test_lengths_beyond_32_bits_in_sum():
     book.same()
 
 
+@pytest.mark.parametrize("batch,old,new,bits", [
+    (3, 1 << 29, 1 << 29, 0), (4, 1 << 29, 1 << 29, pkv.DEVERR_SEQLEN),      # 2^31
+    (9, 1 << 29, 1 << 29, pkv.DEVERR_SEQLEN),                               # 2^32 + 2^29
+    (8, 0, 1 << 29, pkv.DEVERR_SEQLEN | pkv.DEVERR_NO_BLOCKS),              # 2^32 tokens
+    (8, 1 << 29, 0, pkv.DEVERR_BLOCK_ID),                                   # 2^28 pages back
+])
+def test_sums_that_pass_32_bits(batch, old, new, bits):
+    """Lengths of which each is in range and the sum of all is not: of the keys alone
+    (nothing grows, no page moves), of the tokens, of the pages."""
+    table = torch.full((batch, 1 << 25), -1, dtype=I32, device=DEV)
+    free = torch.arange(40, dtype=I32, device=DEV)
+    num, err = torch.tensor([40], dtype=I32, device=DEV), torch.zeros(1, dtype=I32, device=DEV)
+    lens = [torch.full((batch,), x, dtype=I32, device=DEV) for x in (old, new)]
+    got = pkv.update_block_tables(table, *lens, free, num, 16, 8, dev_error=err)
+    assert pkv.get_device_error(err) == bits
+    assert got[0].tolist() == [-1] * 8 and got[1].tolist() == [0] * 8
+    assert got[2].tolist() == [0] * (batch + 1)
+    assert got[3].tolist() == [0 if bits else (new * r) for r in range(batch + 1)]
+    assert num.item() == 40 and free.tolist() == list(range(40)) and bool((table == -1).all())
+
+
 def test_outputs_given_and_streams():
     book = Book(4, 8, 20, 16)
     outs = dict(slot_mapping=torch.full((9,), 5, dtype=I64, device=DEV),
