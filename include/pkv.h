@@ -679,7 +679,11 @@ PKV_API pkv_status pkv_update_page_bounds(const void *k_cache, const uint8_t *k_
  * cu_seq_lens_q NULL row b is the one query of request b, at position
  * cache_seqlens[b] - 1; else request r's queries are rows cu_seq_lens_q[r] .. and
  * the last q_len positions of cache_seqlens[r].  Row t then has n = ceil((its
- * position + 1) / block_size) pages.  The score of page p (bounds lo, hi, byte):
+ * position + 1) / block_size) pages.  A request may have more queries than tokens: the
+ * first ones' positions are negative, and they have no page.  Offsets that decrease or
+ * leave [0, total_q] set PKV_DEVERR_SEQLEN; a request that they end beyond total_q has
+ * the rows that exist, the last of them at its last position.  The score of page p
+ * (bounds lo, hi, byte):
  *   for query head h of the group, 2^E <= max_d |q_d| < 2^(E+1), e_h = max(E, -112) - 7,
  *   c_d = rint(q_d * 2^-e_h);  I_h = sum_d max(c_d, 0) hi_d + min(c_d, 0) lo_d
  *   score = max over h of I_h * 2^(e_h + byte - 127), rounded to fp32
@@ -720,7 +724,8 @@ PKV_API pkv_status pkv_select_pages(int32_t *pages, int top_k, const void *q,
  *                 strictly ascending.  The list ends at its first negative entry, and
  *                 (PKV_DEVERR_BLOCK_ID) at an entry that is not above the one before
  *                 it or not a page of the row
- *   cu_seq_lens_q, cache_seqlens, batch, total_q  as in select_pages.  Rows of no
+ *   cu_seq_lens_q, cache_seqlens, batch, total_q  as in select_pages (offsets out of
+ *                 range: PKV_DEVERR_SEQLEN).  Rows of no
  *                 request are not touched; a row whose position is negative, or with
  *                 an empty list, keeps no key
  *   cache.dtype   PKV_BF16 (k_scale, v_scale ignored) or PKV_E4M3 (the 8-bit cache,

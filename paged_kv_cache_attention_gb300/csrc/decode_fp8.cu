@@ -176,6 +176,13 @@ decode_fp8_kernel(const P params, const __grid_constant__ CUtensorMap tmk,
     int rank = 0, L = 0, tok_lo = 0, tok_hi = 0;
     const int32_t *list = nullptr;       // SPARSE: this CTA's entries
     const int32_t *bt = nullptr;
+    auto check = [&] {
+        if constexpr (SPARSE) {
+            const RowParams &r = params.s.r;
+            if (g == 0 && rank == 0)
+                check_offsets(r, b + (int64_t)threadIdx.x * r.rows, (int64_t)kThreads * r.rows);
+        }
+    };
     if constexpr (SPARSE) {
         const SparseParams &sp = params.s;
         rank = sp.cluster > 1 ? (int)cluster_rank() : 0;
@@ -184,7 +191,7 @@ decode_fp8_kernel(const P params, const __grid_constant__ CUtensorMap tmk,
         g = (int)(unit % p.num_kv_heads);
         int r, keys, count;
         if (!row_request(sp.r, b, BS, g == 0 && rank == 0 && threadIdx.x == 0, r, keys, count))
-            return;
+            return check();
         keys = max(keys, 0);
         const int npages = (keys + BS - 1) / BS;
         list = sp.pages + unit * sp.top_k;
@@ -293,6 +300,7 @@ decode_fp8_kernel(const P params, const __grid_constant__ CUtensorMap tmk,
         }
     };
     for (int j = 0; j < NST && j < nmine; ++j) issue(j);
+    check();
 
     // q as the A operand: row = head, 16 dims per k-step in the byte order.  A
     // negative sm_scale goes into q, so that scores grow with the products.

@@ -44,8 +44,9 @@ __device__ __forceinline__ float4 cluster_ld128(uint32_t addr) {
 }
 
 // Row t's request r, the number L of keys up to and with its own (0 and less: the row
-// attends nothing) and the request's rows from t on.  False: a row of no request.
-// Taken by a whole warp, which looks at 32 offsets at a time.
+// attends nothing) and the request's rows from t on, of those that exist: its last one is
+// at its last position.  False: a row of no request.  Taken by a whole warp, which looks
+// at 32 offsets at a time.
 __device__ __forceinline__ bool row_request(const RowParams &p, int t, int block_size,
                                             bool report, int &r, int &L, int &count) {
     const int lane = threadIdx.x & 31;
@@ -64,7 +65,7 @@ __device__ __forceinline__ bool row_request(const RowParams &p, int t, int block
             if (step == 1) break;
         }
         r = lo;
-        const int end = p.cu_q[r + 1];
+        const int end = min(p.cu_q[r + 1], p.rows);  // (more: check_offsets)
         if (t >= end) return false;
         count = end - t;
     }
@@ -77,6 +78,18 @@ __device__ __forceinline__ bool row_request(const RowParams &p, int t, int block
     }
     L = n - (count - 1);
     return true;
+}
+
+// Offsets that decrease or leave the rows are flagged: each is looked at by one of the
+// `step` threads of a launch that call this with `first` from 0 on, also those of requests
+// that no row belongs to.  (Off the path to a CTA's first load.)
+__device__ __forceinline__ void check_offsets(const RowParams &p, int64_t first, int64_t step) {
+    if (!p.cu_q) return;
+    for (int64_t i = first; i <= p.batch; i += step) {
+        const int a = p.cu_q[i];
+        if (a > p.rows || a < (i > 0 ? p.cu_q[i - 1] : 0))
+            flag_error(p.dev_error, PKV_DEVERR_SEQLEN);
+    }
 }
 
 // The rows [t0, t_end) of a tile of `queries` rows.  With few requests a tile holds rows

@@ -812,6 +812,10 @@ select_pages_kernel(const SelectParams p) {
         }
         if (C > 1) cluster_sync();  // the others may still read this CTA's counts
     }
+    if (g == 0 && rank == 0) {
+        const int64_t all = gridDim.x / (unsigned)C / (unsigned)p.r.num_kv_heads;  // tiles
+        check_offsets(p.r, tile + threadIdx.x * all, kThreads * all);
+    }
 }
 
 template <typename S>

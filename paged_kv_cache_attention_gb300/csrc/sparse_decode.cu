@@ -87,7 +87,12 @@ sparse_decode_kernel(const SparseParams p, const __grid_constant__ CUtensorMap t
     pdl_wait();
     const bool first = g == 0 && rank == 0;
     int r, L, count;
-    if (!row_request(p.r, t, BS, first && threadIdx.x == 0, r, L, count)) return;
+    const bool live = row_request(p.r, t, BS, first && threadIdx.x == 0, r, L, count);
+    auto check = [&] {
+        if (first)
+            check_offsets(p.r, t + (int64_t)threadIdx.x * p.r.rows, (int64_t)kThreads * p.r.rows);
+    };
+    if (!live) return check();
     L = max(L, 0);
     const int npages = (L + BS - 1) / BS;
     const int32_t *list = p.pages + unit * p.top_k;
@@ -134,6 +139,7 @@ sparse_decode_kernel(const SparseParams p, const __grid_constant__ CUtensorMap t
     };
     if (elect_one())
         for (int j = 0; j < NST && j < nmine; ++j) issue(j);
+    check();
 
     // Q as the A operand (rows = query heads, zero-padded to 16; dims past the head
     // size are zeros, as the boxes' columns past it)

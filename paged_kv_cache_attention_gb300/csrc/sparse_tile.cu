@@ -550,6 +550,10 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
         __syncthreads();
     }
     if (warp == kIssue) tc::tmem_dealloc(tmem, kCols);
+    if (g == 0) {
+        const int64_t all = gridDim.x / (unsigned)Hkv;  // tiles
+        check_offsets(p.r, blockIdx.x / Hkv + threadIdx.x * all, kThreads * all);
+    }
 }
 
 template <int BS>

@@ -298,6 +298,51 @@ def test_offsets_that_are_none(rows):
         assert bool(((got >= -1) & (got < 10) | (got == -9)).all())
 
 
+@pytest.mark.parametrize("n", [4, 4 + MANY])
+@pytest.mark.parametrize("cu", ["0 n+2", "0 n-1 n+7", "0 2 n+9 n+9", "-3 2 n", "-9 -4 n", "2 n+1 n+1",
+                                "0 n n+5 n+9", "n n+1 n+2", "0 2 2**31-1 2**31-1"])
+def test_offsets_outside_the_rows(cu, n):
+    """They are flagged; a request has the rows that exist, its last one at its last
+    position, and nothing else is written."""
+    cu = [eval(x, {"n": n}) for x in cu.split()]
+    lens = [1000, 777, 1300][:len(cu) - 1]
+    c = make(lens, [0] * (len(lens) - 1) + [n], 4, 2, 64, 16)
+    whole = torch.full((n + 6, 2, 9), -9, dtype=I32, device=DEV)
+    err = torch.zeros(1, dtype=I32, device=DEV)
+    pkv.select_pages(c["q"].to(DEV), c["codes"].to(DEV), c["byte"].to(DEV), c["table"].to(DEV),
+                     torch.tensor(lens, dtype=I32, device=DEV), 1300, 9, 16, dev_error=err,
+                     cu_seq_lens_q=torch.tensor(cu, dtype=I32, device=DEV), pages=whole[3:3 + n])
+    assert pkv.get_device_error(err) == pkv.DEVERR_SEQLEN
+    w = torch.full((n + 6, 2, 9), -9, dtype=I32)
+    for r, (a, b) in enumerate(zip(cu, cu[1:])):
+        b = min(b, n)
+        for t in range(max(a, 0), b):
+            m = max(0, lens[r] - (b - t) + 1)
+            ids = c["table"][r, :S.pages_of(m, 16)].long()
+            w[3 + t] = S.choose(S.scores(c["q"][t], c["codes"][ids], c["byte"][ids]), 9, 1, 1)
+    assert torch.equal(whole.cpu(), w)
+
+
+@pytest.mark.parametrize("n", [1, 8, 4 + MANY])
+def test_offsets_that_decrease(n):
+    """Flagged wherever they stand, also in requests that no row belongs to; nothing outside
+    the rows is written."""
+    c = make([160], [n], 2, 1, 64, 16)
+    args = [c[x].to(DEV) for x in ("q", "codes", "byte")]
+    for batch in (3, 300, 1000):
+        table = c["table"].expand(batch, -1).contiguous().to(DEV)
+        lens = torch.full((batch,), 160, dtype=I32, device=DEV)
+        for at in {1, batch // 2, batch - 1, batch}:
+            cu = [0] + [n] * batch
+            cu[at] = n - 1 if at > 1 else n + 1   # (in the second place: above the third)
+            err = torch.zeros(1, dtype=I32, device=DEV)
+            whole = torch.full((n + 6, 1, 4), -9, dtype=I32, device=DEV)
+            pkv.select_pages(*args, table, lens, 160, 4, 16, dev_error=err, pages=whole[3:3 + n],
+                             cu_seq_lens_q=torch.tensor(cu, dtype=I32, device=DEV))
+            assert pkv.get_device_error(err) == pkv.DEVERR_SEQLEN, (batch, at)
+            assert bool((whole[:3] == -9).all()) and bool((whole[-3:] == -9).all())
+
+
 def test_in_a_graph_and_on_two_streams():
     c = make([16 * 700, 16 * 30 + 4], [1, 1], 8, 2, 128, 16)
     a = [x.to(DEV) for x in (c["q"], c["codes"], c["byte"], c["table"])]

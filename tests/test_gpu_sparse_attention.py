@@ -157,6 +157,87 @@ def test_offsets_that_are_none(n, hq):
     assert not bool((out == 7.0).any())
 
 
+def guarded(n, *shape, dtype=BF16):
+    """A tensor of 3 + n + 3 rows of sevens, and the n rows in its middle."""
+    whole = torch.full((n + 6, *shape), 7.0, dtype=dtype, device=DEV)
+    return whole, whole[3:3 + n]
+
+
+def untouched(whole):
+    return bool((whole[:3] == 7.0).all()) and bool((whole[-3:] == 7.0).all())
+
+
+def by_offsets(cu, lens, n):
+    """(request, keys up to and with its own) of the rows that offsets which do not decrease
+    leave a request, by row: the rows that exist, the last of them at the last position."""
+    rows = {}
+    for r, (a, b) in enumerate(zip(cu, cu[1:])):
+        b = min(b, n)
+        for t in range(max(a, 0), b):
+            rows[t] = (r, max(0, lens[r] - (b - t) + 1))
+    return rows
+
+
+@pytest.mark.parametrize("n,hq,fp8", [(4, 2, False), (4, 2, True), (MANY, 4, False)])
+@pytest.mark.parametrize("cu", ["0 n+2", "0 n-1 n+7", "0 2 n+9 n+9", "-3 2 n", "-9 -4 n", "2 n+1 n+1",
+                                "0 n n+5 n+9", "n n+1 n+2", "0 2 2**31-1 2**31-1"])
+def test_offsets_outside_the_rows(cu, n, hq, fp8):
+    """They are flagged; a request has the rows that exist, its last one at its last
+    position, and nothing else is written."""
+    cu = [eval(x, {"n": n}) for x in cu.split()]
+    g = torch.Generator().manual_seed(6)
+    lens = [100, 77, 130][:len(cu) - 1]
+    pools = R.Pools(24, 16, 1, 64, "NHD", fp8, g)
+    table, slots = R.paged(lens, 16, 24, g)
+    kc, vc, ks, vs = pools.device(DEV)
+    q = torch.randn(n, hq, 64, generator=g).to(BF16)
+    rows = by_offsets(cu, lens, n)
+    at = sorted(rows)
+    held = lists([rows[t] for t in at], 1, 4, 16, random.Random(6), "last")
+    pages = torch.full((n, 1, 4), -1, dtype=I32)
+    pages[at] = held
+    (whole, out), (whole_lse, lse) = guarded(n, hq, 64), guarded(n, hq, dtype=torch.float32)
+    err = torch.zeros(1, dtype=I32, device=DEV)
+    pkv.paged_sparse_attention(q.to(DEV), kc, vc, table.to(DEV),
+                               torch.tensor(lens, dtype=I32, device=DEV), pages.to(DEV), k_scale=ks,
+                               v_scale=vs, out=out, lse=lse, dev_error=err,
+                               cu_seq_lens_q=torch.tensor(cu, dtype=I32, device=DEV))
+    assert pkv.get_device_error(err) == pkv.DEVERR_SEQLEN
+    assert untouched(whole) and untouched(whole_lse)
+    none = [t for t in range(n) if t not in rows]
+    assert bool((out[none] == 7.0).all()) and bool((lse[none] == 7.0).all())
+    if at:
+        ref, rl, absv, smax, floor = S.attend_lists(q[at], pools, slots, [rows[t] for t in at], held,
+                                                    16, 0.125, None)
+        bound = R.out_bound(ref, absv, smax, 64, 2.0 ** -11, floor) if fp8 else \
+            R.out_bound(ref, absv, smax, 64, 2.0 ** -8)
+        R.assert_within(out[at], ref, bound, "out")
+        R.assert_within(lse[at], rl, R.lse_bound(rl, smax, 64), "lse")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n", [1, 8, MANY])
+def test_offsets_that_decrease(n, fp8):
+    """Flagged wherever they stand, also in requests that no row belongs to; nothing outside
+    the rows is written."""
+    pools, table, slots, _ = small(fp8)
+    kc, vc, ks, vs = pools.device(DEV)
+    q = torch.randn(n, 4, 64, generator=torch.Generator().manual_seed(1)).to(BF16).to(DEV)
+    pages = torch.full((n, 1, 4), -1, dtype=I32, device=DEV)
+    for batch in (3, 300, 1000):
+        for at in {1, batch // 2, batch - 1, batch}:
+            cu = [0] + [n] * batch
+            cu[at] = n - 1 if at > 1 else n + 1   # (in the second place: above the third)
+            err = torch.zeros(1, dtype=I32, device=DEV)
+            whole, out = guarded(n, 4, 64)
+            pkv.paged_sparse_attention(
+                q, kc, vc, table.expand(batch, -1).contiguous().to(DEV),
+                torch.full((batch,), 100, dtype=I32, device=DEV), pages, k_scale=ks, v_scale=vs,
+                out=out, dev_error=err, cu_seq_lens_q=torch.tensor(cu, dtype=I32, device=DEV))
+            assert pkv.get_device_error(err) == pkv.DEVERR_SEQLEN, (batch, at)
+            assert untouched(whole)
+
+
 @pytest.mark.parametrize("extra", [0, MANY])
 @pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
 def test_chunk_scales(scale, extra):
