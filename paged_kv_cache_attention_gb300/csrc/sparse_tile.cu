@@ -182,7 +182,8 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
 
         if (threadIdx.x < nq) s_end[threadIdx.x] = p.top_k;
         // Q: row = query << group_shift | head, 128-byte swizzle; zeros in rows that are none.
-        // A negative scale goes into Q, so that scores grow with the products, and one of 0 too.
+        // A negative scale goes into Q, so that scores grow with the products, and one of 0 too
+        // (0 times a value that is not finite: NaN).
         const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;
 #pragma unroll 4
         for (int i = threadIdx.x; i < kRows * 16; i += kThreads) {
@@ -194,7 +195,8 @@ sparse_tile_kernel(const SparseParams p, const void *k_cache, const void *v_cach
                     static_cast<const __nv_bfloat16 *>(p.q) +
                     (((int64_t)(first + j) * Hkv + g) * G + h) * Dh + c * 8);
             *reinterpret_cast<uint4 *>(smem + kOffQ + (c >> 3) * kHalf + sw128(row, c & 7)) =
-                p.scale_log2 == 0.f ? make_uint4(0u, 0u, 0u, 0u)
+                p.scale_log2 == 0.f ? make_uint4(zero_times(v.x, 0u), zero_times(v.y, 0u),
+                                                 zero_times(v.z, 0u), zero_times(v.w, 0u))
                                     : make_uint4(v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign);
         }
         __syncthreads();

@@ -245,6 +245,32 @@ def test_chunk_scales(scale, extra):
 
 
 @pytest.mark.parametrize("extra", [0, MANY])
+@pytest.mark.parametrize("value", ["nan", "inf", "-inf"])
+def test_a_scale_of_zero_times_a_query_that_is_not_finite(value, extra):
+    """0 times it is NaN, in tiles as row by row; other heads and rows are not touched."""
+    pools, table, slots, _ = small()
+    kc, vc, _, _ = pools.device(DEV)
+    q = torch.randn(9 + extra, 4, 64, generator=torch.Generator().manual_seed(8)).to(BF16)
+    q[2, 1, 40], q[7, 3, 0] = float(value), float(value)
+    rows = S.rows_of([9], [100])
+    pages = lists(rows, 1, 4, 16, random.Random(8), "last")
+    padded = torch.cat([pages, torch.zeros(extra, 1, 4, dtype=I32)]).to(DEV)
+    lse = torch.zeros(9 + extra, 4, device=DEV)
+    cu, lens = (torch.tensor(x, dtype=I32, device=DEV) for x in ([0, 9], [100]))
+    out = pkv.paged_sparse_attention(q.to(DEV), kc, vc, table.to(DEV), lens, padded, cu_seq_lens_q=cu,
+                                     sm_scale=0.0, lse=lse)[:9].cpu()
+    bad = torch.zeros(9, 4, dtype=torch.bool)
+    bad[2, 1] = bad[7, 3] = True
+    assert torch.equal(torch.isnan(out).all(-1), bad) and torch.equal(torch.isnan(out).any(-1), bad)
+    assert torch.equal(torch.isnan(lse[:9]).cpu(), bad)
+    ref, rl, absv, smax, _ = S.attend_lists(q[:9].nan_to_num(0.0, 0.0, 0.0), pools, slots, rows, pages,
+                                            16, 0.0, None)
+    fine = ~bad
+    R.assert_within(out[fine], ref[fine], R.out_bound(ref, absv, smax, 64, 2.0 ** -8)[fine], "out")
+    R.assert_within(lse[:9].cpu()[fine], rl[fine], R.lse_bound(rl, smax, 64)[fine], "lse")
+
+
+@pytest.mark.parametrize("extra", [0, MANY])
 def test_wide_lists_and_tables(extra):
     """Unions of hundreds of pages; tables much wider than their requests."""
     run([16 * 700 + 3], [9], 4, 1, 64, top_k=150, extra=extra)
