@@ -112,6 +112,16 @@ def test_chunks_of_many_requests(batch):
     check(make(lens, queries, 4, 2, 64, 16), 6, chunk=True, extra=3)
 
 
+@pytest.mark.parametrize("decodes,chunks", [(40, 1), (120, 3), (262, 4)])
+def test_decodes_beside_chunks(decodes, chunks):
+    """Requests of one query beside chunks, in tiles request by request, in tiles of
+    whatever rows come, and one at a time."""
+    g = torch.Generator().manual_seed(decodes)
+    lens = torch.randint(1, 900, (decodes,), generator=g).tolist() + [930 + 40 * i for i in range(chunks)]
+    check(make(lens, [1] * decodes + [100 + 13 * i for i in range(chunks)], 8, 2, 64, 16), 9, recent=2,
+          extra=MANY if decodes > 250 else 0)
+
+
 @pytest.mark.parametrize("extra", [0, MANY])
 @pytest.mark.parametrize("hq", [1, 2, 4, 8, 16])
 @pytest.mark.parametrize("n", [3000, 70000, 300000])

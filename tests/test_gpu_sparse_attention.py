@@ -140,6 +140,17 @@ def test_chunks_of_many_requests(batch, most, hq):
     run(lens, queries, hq, 2, 64, top_k=3, chunk=True, extra=MANY if most > 5 else 3)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("decodes,chunks", [(40, 1), (120, 3), (262, 4)])
+def test_decodes_beside_chunks(decodes, chunks, fp8):
+    """Requests of one query beside chunks, in tiles request by request, in tiles of
+    whatever rows come, and row by row."""
+    g = torch.Generator().manual_seed(decodes)
+    lens = torch.randint(1, 200, (decodes,), generator=g).tolist() + [230 + 40 * i for i in range(chunks)]
+    queries = [1] * decodes + [200 + 13 * i for i in range(chunks)]
+    run(lens, queries, 8, 2, 64, fp8=fp8, top_k=5, sink=True, extra=MANY if decodes > 250 else 0)
+
+
 @pytest.mark.parametrize("n,hq", [(8, 2), (MANY, 4)])
 def test_offsets_that_are_none(n, hq):
     """Offsets that decrease or leave the rows: nothing outside is read or written."""
