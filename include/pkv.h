@@ -622,7 +622,9 @@ PKV_API pkv_status pkv_paged_tree_attention(
  *            - 1] is the top).  The pages given back are stacked first, the first
  *            request's first page topmost; then pages are taken off the top in the
  *            order of requests and positions.  So giving back what was just taken
- *            restores the stack.  Entries above the height keep what they held
+ *            restores the stack.  Entries above the height keep what they held.  A page
+ *            is on the stack or in one place of one table row: pages that requests share
+ *            would be given back by each of them
  *   block_table  [batch, max_blocks_per_seq] int32, in place
  * and the arrays that the other calls take:
  *   cu_seq_lens_q  [batch + 1] int32: prefix sums of max(new - old, 0)
@@ -716,7 +718,7 @@ PKV_API pkv_status pkv_select_pages(int32_t *pages, int top_k, const void *q,
 /*
  * paged_sparse_attention: row t attends, for each kv head g, to the keys of the pages
  * pages[t, g, :] of its request up to and with its own position; softmax, sink and
- * lse as in pkv_paged_decode.
+ * lse as in pkv_paged_decode (without window and ALiBi).
  *   out, q        [total_q, num_qo_heads, head_dim] bf16, contiguous; they must not
  *                 overlap
  *   pages         [total_q, num_kv_heads, top_k] int32, as select_pages writes it
@@ -725,9 +727,8 @@ PKV_API pkv_status pkv_select_pages(int32_t *pages, int top_k, const void *q,
  *                 (PKV_DEVERR_BLOCK_ID) at an entry that is not above the one before
  *                 it or not a page of the row
  *   cu_seq_lens_q, cache_seqlens, batch, total_q  as in select_pages (offsets out of
- *                 range: PKV_DEVERR_SEQLEN).  Rows of no
- *                 request are not touched; a row whose position is negative, or with
- *                 an empty list, keeps no key
+ *                 range: PKV_DEVERR_SEQLEN).  Rows of no request are not touched; a
+ *                 row whose position is negative, or with an empty list, keeps no key
  *   cache.dtype   PKV_BF16 (k_scale, v_scale ignored) or PKV_E4M3 (the 8-bit cache,
  *                 scales 16-byte aligned)
  * Precision: scores, sums and outputs fp32; a key's weight rounds to bf16 over bf16

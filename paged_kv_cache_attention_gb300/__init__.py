@@ -1311,8 +1311,9 @@ def update_page_bounds(k_cache, page_bounds, bounds_scale, slot_mapping, k_scale
     k_scale): page_bounds [num_blocks, Hkv, 2, D] int8 (the least and the largest key of
     each channel, rounded outward) and bounds_scale [num_blocks, Hkv] uint8 (E8M0 bytes;
     255: a key that is not finite) are changed in place.  The tokens of a page come in
-    ascending order, as update_block_tables orders them; rows of the page before its last
-    token here count as written."""
+    ascending order with fewer than 32 others between two of them, as update_block_tables
+    orders them (a request's tokens side by side; else two of them race for the bounds, and
+    nothing tells); rows of the page before its last token here count as written."""
     ty = _types()
     dev = _cuda_index("k_cache", k_cache)
     if k_scale is None:

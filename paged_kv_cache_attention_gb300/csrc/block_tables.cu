@@ -14,10 +14,12 @@
 // entry has one reader, which also clears it, and reads and writes of the stack
 // never meet.  Giving back the pages just taken restores the stack.
 //
-// Nothing but the launch and a chain of dependent loads bounds it (12 bytes per page
-// moved, 16 per token): one cluster of eight CTAs, each with the prefix sums of
-// all requests in its own shared memory, and cluster barriers between check,
-// tables and rows, in place of a launch for each.  A step of at most kFew requests,
+// A small step is bound by the launch and a chain of dependent loads (12 bytes per page
+// moved, 16 per token), a large one by the eight SMs that do it: their issue slots are 52 %
+// busy, with two binary searches for a page moved and one for a row, between barriers.  One
+// cluster of eight CTAs, each with the prefix sums of all requests in its own shared
+// memory, and cluster barriers between check, tables and rows, in place of a launch for
+// each.  A step of at most kFew requests,
 // pages and rows is the first CTA's alone (64 requests of a token each: 6.1 us, 7.4 with
 // the cluster's barriers).  Rows beyond kRowsHere take a second launch over all SMs (near
 // it both measure the same: 12K rows 8.4 us here, 8.2 there).

@@ -132,8 +132,8 @@ struct Shape {
 // The same attention over lists of pages (sparse_decode.cu): the keys are the rows
 // of the pages that a CTA of a cluster takes of a row's list, one after another.
 // Measured: 8 rows of 256 pages of 16, 8 kv heads of 64: 14.3 us (clusters of 8; 70 us in
-// one CTA per row and kv head), 35 % of a copy's rate; 8 pages a warp are too few to hide
-// the list, the first loads and the join.
+// one CTA per row and kv head), 35 % of a copy's rate; 16 pages a warp, four stages, are
+// too few to hide the list, the first loads and the join.
 struct SparseFp8Params {
     DecodeFp8Params dense;  // what both have: q, pools, tables, shapes (no window, no ALiBi)
     SparseParams s;

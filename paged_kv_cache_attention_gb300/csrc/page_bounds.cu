@@ -22,9 +22,9 @@
 // f16 values; pages whose scales lie further apart go by fp32).
 //
 // Measured (8 kv heads of 128): 64 tokens 2.9 us; 16K bf16 tokens in 8 prompts 7.0 us;
-// 88K tokens of 8-bit pages in 13 prompts 21.6 us (97 MB, 14.4 at HBM's rate; 24.4 with
-// the two CTAs per SM that unbounded registers leave room for).  Issue at 50%, DRAM at 45%:
-// a warp loads a page, then works on it.
+// 88K tokens of 8-bit pages in 13 prompts 23.9 us from HBM (97 MB, 14.4 at its rate), 21.6
+// where L2 still holds some of them (24.4 with the two CTAs per SM that unbounded registers
+// leave room for).  Issue at 50%, DRAM at 45%: a warp loads a page, then works on it.
 #include <cuda_fp16.h>
 
 #include "pkv_sparse.cuh"

@@ -21,11 +21,17 @@
 //
 // Two CTAs share an SM, so that one's softmax runs beside the other's products and loads.
 // Eight softmax warps, of two halves of the keys: 181 us where four took 318 (890 queries
-// of 1024 keys each, 8 kv heads of 4, D = 128).  Now 114 us, row by row 255.  A step takes
-// 5000 clocks, 2950 with two CTAs: 2600 of softmax (every score is looked at, an eighth
-// is a row's own: 15 GFLOP of products that count, 8 us, in eight times as many), the
-// rest the way from products to softmax and back.  Tiles are of one request each (rows
-// counted on over requests, beyond kTiledRequests: 165 us).
+// of 1024 keys each, 8 kv heads of 4, D = 128).  Now 116 us, row by row 255.  A step takes
+// 5000 clocks, 2950 with two CTAs: 2600 of softmax, the rest the way from products to
+// softmax and back.  A tile's union has 275 pages where a list has 64 (neighbours share 31
+// on average): 4.7 times the products that count, 37 us of the tensor pipe's time at
+// cuBLAS's rate for 7.9.  So most of the time is hand-overs, and SMs that run one tile where
+// others run two (240 tiles of 35 steps on 152 SMs; spread evenly they would take some
+// 81 us).  Tiles are of one request each (rows counted on over requests, beyond
+// kTiledRequests: 165 us).
+//
+// A weight rounds to bf16 for its product with V (at most 2^-8 of it, as in the dense
+// calls: the products are of bf16 pairs); the sum of the weights takes it unrounded.
 #include "pkv_sparse.cuh"
 #include "pkv_tcgen05.cuh"
 
