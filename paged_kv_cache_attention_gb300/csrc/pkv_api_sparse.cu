@@ -256,7 +256,10 @@ pkv_status pkv_paged_sparse_attention(void *out, const void *q, const void *k_ca
     // 1024 keys a query and no two lists alike (the less they differ, the better tiles
     // do): 16 requests, groups of 4 heads, 4 queries 52 and 32 us, 8 69 and 62, 16 84 and
     // 94, 64 117 and 289; groups of one, 32 queries 101 and 154; 1 request, 64 queries 67
-    // and 30, 128 68 and 61, 256 68 and 92.
+    // and 30, 128 68 and 61, 256 68 and 92.  That was over 32K tokens and less: beyond, the
+    // lists differ more and their windows are more, which the rule does not know (256 queries
+    // of one request, 8 kv heads, 64 pages a query, groups of 4 and of one: 32K tokens 97 and
+    // 170 us in tiles, 256K 196 and 539, 1M 363 and 1441; 115 to 118 row by row in all).
     if (!fp8 && cu_seq_lens_q && total_q >= 8LL * batch &&
         (int64_t)total_q * p.r.group >= 32LL * batch && units > 12LL * device_sm_count()) {
         bool fits = false;
